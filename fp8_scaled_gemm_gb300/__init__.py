@@ -43,11 +43,21 @@ _BIAS = {torch.bfloat16: torch.bfloat16, torch.float16: torch.float16, torch.flo
          torch.float8_e4m3fn: torch.bfloat16}
 
 
+# activations of the products' epilogues and of the gradients
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
+
+
 class Options(ctypes.Structure):
     """fp8mm_options of include/fp8mm.h."""
     _fields_ = [("a_type", ctypes.c_int), ("b_type", ctypes.c_int), ("out_type", ctypes.c_int),
                 ("variant", ctypes.c_int), ("tile_n", ctypes.c_int), ("split_k", ctypes.c_int),
                 ("ldo", ctypes.c_int64)]
+
+
+class Epilogue(ctypes.Structure):
+    """fp8mm_epilogue of include/fp8mm.h."""
+    _fields_ = [("activation", ctypes.c_int), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("preact", ctypes.c_void_p), ("ldp", ctypes.c_int64)]
 
 
 STATUS = {
@@ -59,7 +69,7 @@ STATUS = {
 EXPORTS = (
     "fp8_scaled_mm", "fp8_scaled_mm_config", "fp8_scaled_mm_ex", "fp8_scaled_mm_host",
     "fp8_scaled_mm_noalloc", "fp8_quantize", "fp8_scaled_mm_bf16", "fp8_scaled_bmm",
-    "fp8_scaled_mm_layout",
+    "fp8_scaled_mm_layout", "fp8_scaled_mm_epilogue", "fp8_scaled_mm_act_grad",
     "fp8mm_reserve_workspace", "fp8mm_device_status", "fp8mm_status_string",
     "fp8mm_last_cuda_error", "fp8mm_last_error", "fp8mm_describe_choice", "fp8mm_describe_bmm_choice", "fp8mm_debug_inject", "fp8mm_debug_quant", "fp8mm_describe_model_choice",
     "fp8mm_describe_quant_plan",
@@ -114,6 +124,11 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.fp8_scaled_bmm.argtypes = [vp, vp, vp, vp, i32, vp, vp, i64, i64, i64, i64, vp,
                                        ctypes.POINTER(Options)]
         lib.fp8_scaled_bmm.restype = i32
+        lib.fp8_scaled_mm_epilogue.argtypes = common + [ctypes.POINTER(Options), ctypes.POINTER(Epilogue)]
+        lib.fp8_scaled_mm_epilogue.restype = i32
+        lib.fp8_scaled_mm_act_grad.argtypes = [vp, vp, vp, vp, i32, i32, vp, i64, vp, i64, i64, i64, vp,
+                                               ctypes.POINTER(Options)]
+        lib.fp8_scaled_mm_act_grad.restype = i32
         lib.fp8_quantize.argtypes = [vp, i64, i64, i32, i32, vp, vp, vp]
         lib.fp8_quantize.restype = i32
         lib.fp8_scaled_mm_bf16.argtypes = [vp, vp, i32, vp, vp, i64, i64, i64, vp, vp, vp, vp, vp,
@@ -250,6 +265,61 @@ def fp8_scaled_mm_ex(A, B, scale_a, scale_b, scale_mode: int, bias=None, out=Non
     _check(load().fp8_scaled_mm_ex(_ptr(A), _ptr(B), _ptr(scale_a), _ptr(scale_b), scale_mode,
                                    _ptr(bias), _ptr(out), M, N, K, _stream_handle(stream),
                                    ctypes.byref(opt)))
+    return out
+
+
+def _aux_matrix(name, t, M, N, dtype) -> int:
+    """Leading dimension of a [M, N] matrix beside out (residual, preact, z)."""
+    if t.dtype != dtype or tuple(t.shape) != (M, N) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA [M, N] tensor of out's dtype (bfloat16 for a float8_e4m3fn output)")
+    if t.is_contiguous():
+        return N
+    if (t.stride(1) != 1 and N > 1) or (t.stride(0) < N and M > 1):
+        raise ValueError(f"{name}'s rows must be contiguous, their stride at least N")
+    return max(N, t.stride(0))
+
+
+def fp8_scaled_mm_epilogue(A, B, scale_a, scale_b, scale_mode: int, bias=None, activation: int = ACT_NONE,
+                           residual=None, preact=None, out=None, stream=None, out_dtype=torch.bfloat16,
+                           return_preact: bool = False, variant: int = VARIANT_AUTO, tile_n: int = 0,
+                           split_k: int = 0):
+    """out = act(z) + residual with z = A.B * scale + bias, in one kernel.
+
+    ``residual`` [M, N] (or None) has out's dtype (bf16 for a float8_e4m3fn
+    output) and may be ``out``; ``preact`` receives z. Returns out, or
+    (out, preact) with ``return_preact`` (preact is then made if not given).
+    """
+    if out is None:
+        out = torch.empty((A.shape[0], B.shape[1]), dtype=out_dtype, device=A.device)
+    M, N, K = _validate(A, B, scale_a, scale_b, scale_mode, bias, out, True, typed=True)
+    if return_preact and preact is None:
+        preact = torch.empty((M, N), dtype=_BIAS[out.dtype], device=out.device)
+    ldr = 0 if residual is None else _aux_matrix("residual", residual, M, N, _BIAS[out.dtype])
+    ldp = 0 if preact is None else _aux_matrix("preact", preact, M, N, _BIAS[out.dtype])
+    ldo = 0 if out.is_contiguous() else int(out.stride(0))
+    opt = Options(_FP8[A.dtype], _FP8[B.dtype], _OUT[out.dtype], int(variant), int(tile_n), int(split_k), ldo)
+    epi = Epilogue(int(activation), None if residual is None else residual.data_ptr(), ldr,
+                   None if preact is None else preact.data_ptr(), ldp)
+    _check(load().fp8_scaled_mm_epilogue(_ptr(A), _ptr(B), _ptr(scale_a), _ptr(scale_b), scale_mode, _ptr(bias),
+                                         _ptr(out), M, N, K, _stream_handle(stream), ctypes.byref(opt),
+                                         ctypes.byref(epi)))
+    return (out, preact) if return_preact else out
+
+
+def fp8_scaled_mm_act_grad(A, B, scale_a, scale_b, scale_mode: int, z, activation: int, out=None, stream=None,
+                           out_dtype=None, variant: int = VARIANT_AUTO, tile_n: int = 0, split_k: int = 0):
+    """dz = (A.B * scale) * act'(z): a backward product with the gradient of
+    the activation before it. ``z`` [M, N] is what fp8_scaled_mm_epilogue
+    returned as preact; out has z's dtype unless given otherwise."""
+    if out is None:
+        out = torch.empty((A.shape[0], B.shape[1]), dtype=out_dtype or z.dtype, device=A.device)
+    M, N, K = _validate(A, B, scale_a, scale_b, scale_mode, None, out, True, typed=True)
+    ldz = _aux_matrix("z", z, M, N, _BIAS[out.dtype])
+    ldo = 0 if out.is_contiguous() else int(out.stride(0))
+    opt = Options(_FP8[A.dtype], _FP8[B.dtype], _OUT[out.dtype], int(variant), int(tile_n), int(split_k), ldo)
+    _check(load().fp8_scaled_mm_act_grad(_ptr(A), _ptr(B), _ptr(scale_a), _ptr(scale_b), scale_mode,
+                                         int(activation), _ptr(z), ldz, _ptr(out), M, N, K, _stream_handle(stream),
+                                         ctypes.byref(opt)))
     return out
 
 

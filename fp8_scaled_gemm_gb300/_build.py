@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libfp8mm.so")
 
-SOURCES = ["fp8mm_api.cu"]
+SOURCES = ["fp8mm_api.cu", "fp8mm_epilogue.cu"]
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 
@@ -49,17 +50,23 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [
-        nvcc_path(), "-gencode", GENCODE, "-O3", "-lineinfo", "-std=c++17",
-        "-Xcompiler", "-fPIC", "-shared", "-cudart", "static",
-        "-I", INCLUDE, "-I", CSRC,
-        *[os.path.join(CSRC, s) for s in SOURCES],
-        "-o", tmp,
-    ]
+    flags = ["-gencode", GENCODE, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-cudart", "static",
+             "-I", INCLUDE, "-I", CSRC]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
+        flags.insert(0, "-Xptxas=-v")
+    with tempfile.TemporaryDirectory(dir=BUILD_DIR) as work:
+        # one nvcc per translation unit, all at once, then the link
+        jobs = []
+        for src in SOURCES:
+            obj = os.path.join(work, src + ".o")
+            cmd = [nvcc_path(), *flags, "-c", os.path.join(CSRC, src), "-o", obj]
+            if verbose:
+                print(" ".join(cmd), file=sys.stderr)
+            jobs.append((obj, cmd, subprocess.Popen(cmd)))
+        failed = [(p.returncode, cmd) for _, cmd, p in jobs if p.wait() != 0]
+        if failed:
+            raise subprocess.CalledProcessError(*failed[0])
+        subprocess.run([nvcc_path(), *flags, "-shared", *[obj for obj, _, _ in jobs], "-o", tmp], check=True)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

@@ -19,15 +19,15 @@
 #include <vector>
 
 #include "fp8mm.h"
-#include "fp8mm_kernel.cuh"
-#include "fp8mm_kernel_pair.cuh"
-#include "fp8mm_kernel_ck.cuh"
+#include "fp8mm_host.h"
+#include "fp8mm_launch.cuh"
 #include "fp8mm_quant.cuh"
 #include "fp8mm_transpose.cuh"
 
 namespace {
 
-constexpr int kMaxDevices = 64;
+using namespace fp8mm_host;
+
 constexpr unsigned long long kDefaultTimeoutCycles = 4000000000ull;  // ~2 s at 2 GHz
 
 thread_local std::string t_last_error;
@@ -93,11 +93,21 @@ bool tuned_lookup(const TuneKey &k, TuneVal *v)
     return true;
 }
 
+}  // namespace
+
+namespace fp8mm_host {
+
+void set_error(const char *text) { t_last_error = text; }
+
 int cuda_fail(cudaError_t e, const char *what)
 {
     t_last_error = std::string(what) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")";
     return FP8MM_ERR_CUDA;
 }
+
+}  // namespace fp8mm_host
+
+namespace {
 
 // Per-device initialisation; returns FP8MM_OK and the state, or an error.
 int device_state(DeviceState **out)
@@ -367,16 +377,6 @@ int cached_col_out_map(CUtensorMap *map, void *out, int64_t M, int64_t N, int ou
     return rc;
 }
 
-struct Choice {
-    int variant;   // FP8MM_VARIANT_TILE, _SWAP, _PAIR, _SWAPK or _SWAPPAIR
-    int tile_n;
-    int split;
-    int tiles_p, tiles_q, kblocks, units, grid;
-    int sk_tiles;  // PAIR: tiles whose K blocks are spread over all pairs (stream-K), 0: none
-};
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 // Tile rows per group of the tile order (columns run inside a group): a
 // group's A strips stay in L2 while Bt is swept once per group, so Bt's
 // DRAM reads fall as the group grows until the strips no longer fit. Pair
@@ -523,46 +523,6 @@ int pick_split(int64_t tiles, int kblocks, int sms, int tile_n)
     return best;
 }
 
-// Launch with programmatic stream serialization: the kernel may start its
-// set-up while the previous kernel in the stream finishes; it calls
-// griddepcontrol.wait before touching global memory.
-template <typename Kern, typename... Args>
-int launch_pdl(Kern kern, int grid, int threads, int smem, cudaStream_t stream, const char *what, Args... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-    if (e != cudaSuccess)
-        return cuda_fail(e, what);
-    return FP8MM_OK;
-}
-
-template <int BN, int CS>
-int launch_swapk(const CUtensorMap &mp, const CUtensorMap &mq, const fp8mm::KernelParams &kp, int grid,
-                 cudaStream_t stream)
-{
-    using C = fp8mm::ClusterKCfg<BN, CS>;
-    auto kern = fp8mm::fp8mm_swap_ck_kernel<BN, CS>;
-    static bool attr_set[kMaxDevices] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (!attr_set[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-        if (e != cudaSuccess)
-            return cuda_fail(e, "cudaFuncSetAttribute");
-        attr_set[dev] = true;
-    }
-    return launch_pdl(kern, grid, fp8mm::kThreads, C::kSmemBytes, stream, "cluster-K kernel launch", mp, mq, kp);
-}
-
 // Cluster-K CTAs resident per SM: tiles up to 64 wide keep the CTA under
 // half of the SM's shared memory (fp8mm::ClusterKCfg), so two fit.
 // (cudaOccupancyMaxActiveClusters reports one CTA per SM for these clusters,
@@ -572,13 +532,6 @@ int launch_swapk(const CUtensorMap &mp, const CUtensorMap &mq, const fp8mm::Kern
 int ck_ctas_per_sm(int tile_n) { return tile_n <= 64 ? 2 : 1; }
 
 int swap_tile_for(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
-
-// The 256-wide 1-SM kernel runs 16 epilogue warps up to this K. Measured on
-// GB300 (CUDA-graph replays, row-wise + bias) against 8 warps: 8191 x 8193 x
-// 32 87.0 -> 71.3 us, 8192 x 8192 x 32 52.6 -> 44.8, 8192 x 8192 x 512
-// 54.8 -> 46.1; at K = 1024 16 warps lost (16384 x 8192 x 1024 127.7 ->
-// 141.1, 4096 x 4096 x 1024 21.3 -> 23.2).
-constexpr int64_t kTileWideMaxK = 512;
 
 Choice choose(int64_t M, int64_t N, int64_t K, int sms, int variant, int tile_n, int split, int64_t batch = 1)
 {
@@ -790,102 +743,11 @@ void log_choice(int dev, int64_t batch, int64_t M, int64_t N, int64_t K, int mod
             req_variant != FP8MM_VARIANT_AUTO ? "requested" : tuned ? "tuned" : "model");
 }
 
-template <int BN, bool SWAP, bool WIDE = false>
-int launch_kernel(const CUtensorMap &mp, const CUtensorMap &mq, const CUtensorMap &mo,
-                  const fp8mm::KernelParams &kp, int grid, cudaStream_t stream)
-{
-    using C = fp8mm::TileCfg<BN, SWAP, WIDE>;
-    auto kern = fp8mm::fp8mm_tc_kernel<BN, SWAP, WIDE>;
-    static bool attr_set[kMaxDevices] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (!attr_set[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-        if (e != cudaSuccess)
-            return cuda_fail(e, "cudaFuncSetAttribute");
-        attr_set[dev] = true;
-    }
-    return launch_pdl(kern, grid, C::kThreads, C::kSmemBytes, stream, "kernel launch", mp, mq,
-                      mo, kp);
-}
-
-template <int BN, bool SWAP>
-int launch_pair(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo,
-                const fp8mm::KernelParams &kp, int grid, cudaStream_t stream)
-{
-    using C = fp8mm::PairCfg<BN, SWAP>;
-    auto kern = fp8mm::fp8mm_pair_kernel<BN, SWAP>;
-    static bool attr_set[kMaxDevices] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (!attr_set[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-        if (e != cudaSuccess)
-            return cuda_fail(e, "cudaFuncSetAttribute");
-        attr_set[dev] = true;
-    }
-    return launch_pdl(kern, grid, fp8mm::EpiShape<SWAP>::kThreads, C::kSmemBytes, stream, "pair kernel launch",
-                      ma, mb, mo, kp);
-}
-
-int dispatch(const Choice &c, const CUtensorMap &mp, const CUtensorMap &mq, const CUtensorMap &mo,
-             const fp8mm::KernelParams &kp, cudaStream_t stream)
-{
-    if (c.variant == FP8MM_VARIANT_SWAPK) {
-        switch (c.tile_n * 10 + c.split) {
-        case 162: return launch_swapk<16, 2>(mp, mq, kp, c.grid, stream);
-        case 164: return launch_swapk<16, 4>(mp, mq, kp, c.grid, stream);
-        case 168: return launch_swapk<16, 8>(mp, mq, kp, c.grid, stream);
-        case 322: return launch_swapk<32, 2>(mp, mq, kp, c.grid, stream);
-        case 324: return launch_swapk<32, 4>(mp, mq, kp, c.grid, stream);
-        case 328: return launch_swapk<32, 8>(mp, mq, kp, c.grid, stream);
-        case 642: return launch_swapk<64, 2>(mp, mq, kp, c.grid, stream);
-        case 644: return launch_swapk<64, 4>(mp, mq, kp, c.grid, stream);
-        case 648: return launch_swapk<64, 8>(mp, mq, kp, c.grid, stream);
-        case 1282: return launch_swapk<128, 2>(mp, mq, kp, c.grid, stream);
-        case 1284: return launch_swapk<128, 4>(mp, mq, kp, c.grid, stream);
-        case 1288: return launch_swapk<128, 8>(mp, mq, kp, c.grid, stream);
-        }
-        return FP8MM_ERR_MODE;
-    }
-    if (c.variant == FP8MM_VARIANT_PAIR) {
-        switch (c.tile_n) {
-        case 128: return launch_pair<128, false>(mp, mq, mo, kp, c.grid, stream);
-        case 256: return launch_pair<256, false>(mp, mq, mo, kp, c.grid, stream);
-        }
-    } else if (c.variant == FP8MM_VARIANT_SWAPPAIR) {
-        switch (c.tile_n) {
-        case 16: return launch_pair<16, true>(mp, mq, mo, kp, c.grid, stream);
-        case 32: return launch_pair<32, true>(mp, mq, mo, kp, c.grid, stream);
-        case 64: return launch_pair<64, true>(mp, mq, mo, kp, c.grid, stream);
-        case 128: return launch_pair<128, true>(mp, mq, mo, kp, c.grid, stream);
-        }
-    } else if (c.variant == FP8MM_VARIANT_TILE) {
-        switch (c.tile_n) {
-        case 128: return launch_kernel<128, false>(mp, mq, mo, kp, c.grid, stream);
-        case 256:
-            // shallow K: 16 epilogue warps (the epilogue sets the time per
-            // tile); deeper K keeps 8 and two stage buffers per warp
-            if (kp.K <= kTileWideMaxK)
-                return launch_kernel<256, false, true>(mp, mq, mo, kp, c.grid, stream);
-            return launch_kernel<256, false>(mp, mq, mo, kp, c.grid, stream);
-        }
-    } else {
-        switch (c.tile_n) {
-        case 16: return launch_kernel<16, true>(mp, mq, mo, kp, c.grid, stream);
-        case 32: return launch_kernel<32, true>(mp, mq, mo, kp, c.grid, stream);
-        case 64: return launch_kernel<64, true>(mp, mq, mo, kp, c.grid, stream);
-        case 128: return launch_kernel<128, true>(mp, mq, mo, kp, c.grid, stream);
-        }
-    }
-    return FP8MM_ERR_MODE;
-}
-
 // Tensor maps for the chosen kernel, then the launch. P is the operand whose
 // 128-row boxes feed the MMA's A side (A, or Bt for SWAP); Q's boxes are
 // tile_n rows (half of that per CTA for PAIR).
 int encode_and_dispatch(const Choice &c, const void *A, const void *B, void *out, int64_t M, int64_t N,
-                        int64_t K, fp8mm::KernelParams kp, cudaStream_t stream, int64_t batch = 1)
+                        int64_t K, fp8mm::KernelParams kp, cudaStream_t stream, int64_t batch = 1, bool epi = false)
 {
     CUtensorMap mp, mq, mo;
     std::memset(&mo, 0, sizeof mo);
@@ -928,7 +790,7 @@ int encode_and_dispatch(const Choice &c, const void *A, const void *B, void *out
     rc = cached_operand_map(&mq, swap ? A : B, swap ? M : N, K, q_box, batch);
     if (rc != FP8MM_OK)
         return rc;
-    return dispatch(c, mp, mq, mo, kp, stream);
+    return epi ? dispatch_epilogue(c, mp, mq, mo, kp, stream) : dispatch<false>(c, mp, mq, mo, kp, stream);
 }
 
 int check_args(const void *A, const void *B, const float *sa, const float *sb, int scale_mode,
@@ -958,7 +820,7 @@ uint32_t fmt_code(int t) { return t == FP8MM_TYPE_E5M2 ? 1u : 0u; }
 int run(const void *A, const void *B, const float *sa, const float *sb, int scale_mode, const void *bias,
         void *out, int64_t M, int64_t N, int64_t K, cudaStream_t stream, int variant, int tile_n, int split,
         int a_type = FP8MM_TYPE_E4M3, int b_type = FP8MM_TYPE_E4M3, int out_type = FP8MM_OUT_BF16,
-        int64_t batch = 1, int64_t ldo = 0)
+        int64_t batch = 1, int64_t ldo = 0, const fp8mm::EpiParams *epi = nullptr)
 {
     int rc = check_args(A, B, sa, sb, scale_mode, bias, out, M, N, K);
     if (rc != FP8MM_OK)
@@ -1085,7 +947,9 @@ int run(const void *A, const void *B, const float *sa, const float *sb, int scal
         kp.counters = d->counters;
     }
 
-    return encode_and_dispatch(c, A, B, out, M, N, K, kp, stream, batch);
+    if (epi)
+        kp.e = *epi;
+    return encode_and_dispatch(c, A, B, out, M, N, K, kp, stream, batch, epi != nullptr);
 }
 
 // ------------------------------------------------------ quantisation ---
@@ -1460,9 +1324,102 @@ int grow_stage(DeviceState &d, int i, size_t bytes)
     return FP8MM_OK;
 }
 
+// ---------------------------------------------------- extended epilogue ---
+
+// The bias's type: the output's, bf16 for an e4m3fn output. Bytes of it.
+int64_t aux_bytes(int out_type) { return out_type == FP8MM_OUT_F32 ? 4 : 2; }
+
+bool out_type_known(int t) { return t >= FP8MM_OUT_BF16 && t <= FP8MM_OUT_E4M3; }
+
+// An auxiliary [M, N] matrix of the epilogue: its leading dimension and base.
+int check_aux(const void *ptr, int64_t ld, int64_t N, int out_type)
+{
+    if (ld < 0 || (ld > 0 && ld < N) || ld >= (int64_t(1) << 36))
+        return FP8MM_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(ptr) & (aux_bytes(out_type) - 1))
+        return FP8MM_ERR_ALIGN;
+    return FP8MM_OK;
+}
+
+int aux_vec(const void *ptr, int64_t ld, int out_type)
+{
+    return (reinterpret_cast<uintptr_t>(ptr) & 15) == 0 && (ld * aux_bytes(out_type)) % 16 == 0 ? 1 : 0;
+}
+
 }  // namespace
 
+namespace fp8mm_host {
+
+int device_sms(int *sms)
+{
+    DeviceState *d = nullptr;
+    const int rc = device_state(&d);
+    if (rc == FP8MM_OK)
+        *sms = d->sms;
+    return rc;
+}
+
+}  // namespace fp8mm_host
+
 extern "C" {
+
+int fp8_scaled_mm_epilogue(const void *A, const void *B, const float *scale_a, const float *scale_b, int scale_mode,
+                           const void *bias, void *out, int64_t M, int64_t N, int64_t K, void *stream,
+                           const fp8mm_options *options, const fp8mm_epilogue *epilogue)
+{
+    fp8mm_options o = {FP8MM_TYPE_E4M3, FP8MM_TYPE_E4M3, FP8MM_OUT_BF16, FP8MM_VARIANT_AUTO, 0, 0, 0};
+    if (options)
+        o = *options;
+    if (!epilogue)
+        return FP8MM_ERR_NULL;
+    if (epilogue->activation < FP8MM_ACT_NONE || epilogue->activation > FP8MM_ACT_SILU || !out_type_known(o.out_type))
+        return FP8MM_ERR_MODE;
+    int rc = check_aux(epilogue->residual, epilogue->ldr, N, o.out_type);
+    if (rc == FP8MM_OK)
+        rc = check_aux(epilogue->preact, epilogue->ldp, N, o.out_type);
+    if (rc != FP8MM_OK)
+        return rc;
+    if (epilogue->preact && (epilogue->preact == out || epilogue->preact == epilogue->residual))
+        return FP8MM_ERR_MODE;   // z may not land on the output or on the residual
+    fp8mm::EpiParams e{};
+    e.act = epilogue->activation;
+    e.in = epilogue->residual;
+    e.ld_in = epilogue->ldr > 0 ? epilogue->ldr : N;
+    e.pre = epilogue->preact;
+    e.ld_pre = epilogue->ldp > 0 ? epilogue->ldp : N;
+    if (e.in == out && e.in && (o.out_type == FP8MM_OUT_E4M3 || e.ld_in != (o.ldo > 0 ? o.ldo : N)))
+        return FP8MM_ERR_MODE;   // in place: every element over itself
+    e.vec_in = aux_vec(e.in, e.ld_in, o.out_type);
+    e.vec_pre = aux_vec(e.pre, e.ld_pre, o.out_type);
+    return run(A, B, scale_a, scale_b, scale_mode, bias, out, M, N, K, static_cast<cudaStream_t>(stream), o.variant,
+               o.tile_n, o.split_k, o.a_type, o.b_type, o.out_type, 1, o.ldo, &e);
+}
+
+int fp8_scaled_mm_act_grad(const void *A, const void *B, const float *scale_a, const float *scale_b, int scale_mode,
+                           int activation, const void *z, int64_t ldz, void *out, int64_t M, int64_t N, int64_t K,
+                           void *stream, const fp8mm_options *options)
+{
+    fp8mm_options o = {FP8MM_TYPE_E4M3, FP8MM_TYPE_E4M3, FP8MM_OUT_BF16, FP8MM_VARIANT_AUTO, 0, 0, 0};
+    if (options)
+        o = *options;
+    if (activation < FP8MM_ACT_RELU || activation > FP8MM_ACT_SILU || !out_type_known(o.out_type))
+        return FP8MM_ERR_MODE;
+    int rc = check_aux(z, ldz, N, o.out_type);
+    if (rc != FP8MM_OK)
+        return rc;
+    if (!z && M > 0 && N > 0)
+        return FP8MM_ERR_NULL;
+    fp8mm::EpiParams e{};
+    e.act = activation;
+    e.grad = 1;
+    e.in = z;
+    e.ld_in = ldz > 0 ? ldz : N;
+    if (z == out && z && (o.out_type == FP8MM_OUT_E4M3 || e.ld_in != (o.ldo > 0 ? o.ldo : N)))
+        return FP8MM_ERR_MODE;
+    e.vec_in = aux_vec(e.in, e.ld_in, o.out_type);
+    return run(A, B, scale_a, scale_b, scale_mode, nullptr, out, M, N, K, static_cast<cudaStream_t>(stream), o.variant,
+               o.tile_n, o.split_k, o.a_type, o.b_type, o.out_type, 1, o.ldo, &e);
+}
 
 int fp8_scaled_mm(const void *A, const void *B, const float *scale_a, const float *scale_b, int scale_mode,
                   const void *bias, void *out, int64_t M, int64_t N, int64_t K, void *stream)

@@ -1,0 +1,13 @@
+// fp8mm_epilogue.cu -- the matmul kernels with the extended epilogue
+// (activation, residual, stored pre-activation; activation gradient).
+#include "fp8mm_launch.cuh"
+
+namespace fp8mm_host {
+
+int dispatch_epilogue(const Choice &c, const CUtensorMap &mp, const CUtensorMap &mq, const CUtensorMap &mo,
+                      const fp8mm::KernelParams &kp, cudaStream_t stream)
+{
+    return dispatch<true>(c, mp, mq, mo, kp, stream);
+}
+
+}  // namespace fp8mm_host

@@ -49,6 +49,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "fp8mm_act.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fp8mm {
@@ -78,6 +79,24 @@ constexpr int kStatusTimeoutBase = 0x100;
 // e4m3fn (round to nearest even, saturating at +-448) are stored from
 // registers.
 constexpr int kOutBF16 = 0, kOutF16 = 1, kOutF32 = 2, kOutE4M3 = 3;
+
+// The extended epilogue (kernels with EPI = true), applied to
+// z = acc * scale + bias in fp32, before the output's rounding:
+//   forward   pre = z (when asked for);  out = act(z) + in  (in: the residual)
+//   gradient  out = z * act'(in)         (in: the forward pass's z; no bias)
+// `in` and `pre` are row-major [M, N] with leading dimensions of their own.
+// Their type is the bias's: the output type, bf16 for an e4m3fn output. `in`
+// may be the output itself: an element is read by the warp that writes it,
+// before it writes.
+struct EpiParams {
+    int act;                        // kAct*
+    int grad;                       // 0 forward, 1 gradient
+    const void *in;                 // residual or z; nullptr: none (forward only)
+    long long ld_in;
+    void *pre;                      // forward: where z goes; nullptr: nowhere
+    long long ld_pre;
+    int vec_in, vec_pre;            // 16-byte accesses allowed: base and row pitch aligned
+};
 
 // A batch of `batch` independent problems of one shape: operand tensor maps
 // are 3-D ({K, rows, batch}); item b has its own scales (scale_a + b, or
@@ -112,6 +131,7 @@ struct KernelParams {
     float *sk_ws;                   // per pair: one fp32 partial tile, [CTA half][BN/4][128][4]
     unsigned int *sk_flags;         // per pair: 16 "partial written" flags (one per epilogue warp)
     unsigned long long timeout_cycles;
+    EpiParams e;                    // read by kernels with EPI = true only
 };
 
 // WIDE: the 256-wide row-major kernel with 16 epilogue warps (four per TMEM
@@ -373,6 +393,209 @@ __device__ __forceinline__ float bias_value(const KernelParams &p, int n)
     return p.out_type == kOutF16 ? __half2float(__ushort_as_half(b)) : __bfloat162float(__ushort_as_bfloat16(b));
 }
 
+// ------------------------------------------------- extended epilogue ---
+
+// One element of an array of the bias's type (the epilogue's in and pre).
+__device__ __forceinline__ float aux_load1(const KernelParams &p, const void *base, size_t idx)
+{
+    if (p.out_type == kOutF32)
+        return static_cast<const float *>(base)[idx];
+    const unsigned short b = static_cast<const unsigned short *>(base)[idx];
+    return p.out_type == kOutF16 ? __half2float(__ushort_as_half(b)) : __bfloat162float(__ushort_as_bfloat16(b));
+}
+
+__device__ __forceinline__ void aux_store1(const KernelParams &p, void *base, size_t idx, float y)
+{
+    if (p.out_type == kOutF32)
+        static_cast<float *>(base)[idx] = y;
+    else
+        static_cast<unsigned short *>(base)[idx] =
+            p.out_type == kOutF16 ? __half_as_ushort(__float2half_rn(y)) : __bfloat16_as_ushort(__float2bfloat16_rn(y));
+}
+
+// The two 16-bit values of a word in the epilogue's type (bf16 or fp16).
+__device__ __forceinline__ void aux_unpack2(uint32_t w, bool f16, float &lo, float &hi)
+{
+    if (f16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        lo = f.x;
+        hi = f.y;
+    } else {
+        lo = __uint_as_float(w << 16);
+        hi = __uint_as_float(w & 0xFFFF0000u);
+    }
+}
+
+// CH consecutive elements of row m from column n0 of p.e.in; 0 outside [M, N].
+template <int CH>
+__device__ __forceinline__ void epi_load_row(const KernelParams &p, int m, int n0, float (&r)[CH])
+{
+    const size_t base = static_cast<size_t>(m) * p.e.ld_in + n0;
+    if (m < p.M && p.e.vec_in && n0 + CH <= p.N) {
+        if (p.out_type == kOutF32) {
+#pragma unroll
+            for (int j = 0; j < CH; j += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.e.in) + base + j);
+                r[j] = x.x;
+                r[j + 1] = x.y;
+                r[j + 2] = x.z;
+                r[j + 3] = x.w;
+            }
+        } else {
+            const bool f16 = p.out_type == kOutF16;
+            uint4 w[CH / 8];
+#pragma unroll
+            for (int j = 0; j < CH / 8; ++j)
+                w[j] = *reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(p.e.in) + base + 8 * j);
+#pragma unroll
+            for (int j = 0; j < CH / 8; ++j) {
+                aux_unpack2(w[j].x, f16, r[8 * j], r[8 * j + 1]);
+                aux_unpack2(w[j].y, f16, r[8 * j + 2], r[8 * j + 3]);
+                aux_unpack2(w[j].z, f16, r[8 * j + 4], r[8 * j + 5]);
+                aux_unpack2(w[j].w, f16, r[8 * j + 6], r[8 * j + 7]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+            r[j] = (m < p.M && n0 + j < p.N) ? aux_load1(p, p.e.in, base + j) : 0.0f;
+    }
+}
+
+// CH consecutive elements of row m from column n0 to p.e.pre.
+template <int CH>
+__device__ __forceinline__ void epi_store_row(const KernelParams &p, int m, int n0, const float (&y)[CH])
+{
+    if (m >= p.M)
+        return;
+    const size_t base = static_cast<size_t>(m) * p.e.ld_pre + n0;
+    if (p.e.vec_pre && n0 + CH <= p.N) {
+        if (p.out_type == kOutF32) {
+#pragma unroll
+            for (int j = 0; j < CH; j += 4)
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.e.pre) + base + j) =
+                    make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < CH; j += 8) {
+                uint4 w;
+                w.x = pack_out2(y[j + 0], y[j + 1], p.out_type);
+                w.y = pack_out2(y[j + 2], y[j + 3], p.out_type);
+                w.z = pack_out2(y[j + 4], y[j + 5], p.out_type);
+                w.w = pack_out2(y[j + 6], y[j + 7], p.out_type);
+                *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(p.e.pre) + base + j) = w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+            if (n0 + j < p.N)
+                aux_store1(p, p.e.pre, base + j, y[j]);
+    }
+}
+
+// z values of row m, columns n0 .. n0 + CH - 1, to output values.
+template <int CH>
+__device__ __forceinline__ void epi_row(const KernelParams &p, float (&y)[CH], int m, int n0)
+{
+    if (p.e.grad) {
+        float z[CH];
+        epi_load_row<CH>(p, m, n0, z);
+        apply_slope<CH>(p.e.act, y, z);
+        return;
+    }
+    if (p.e.pre != nullptr)
+        epi_store_row<CH>(p, m, n0, y);
+    apply_act<CH>(p.e.act, y);
+    if (p.e.in != nullptr) {
+        float r[CH];
+        epi_load_row<CH>(p, m, n0, r);
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+            y[j] += r[j];
+    }
+}
+
+// The same for a thread that holds one column n, rows m0 .. m0 + CH - 1
+// (neighbouring lanes hold neighbouring columns).
+template <int CH>
+__device__ __forceinline__ void epi_col(const KernelParams &p, float (&y)[CH], int n, int m0)
+{
+    const bool n_in = n < p.N;
+    float r[CH];
+    if (p.e.in != nullptr) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+            r[j] = (n_in && m0 + j < p.M) ? aux_load1(p, p.e.in, static_cast<size_t>(m0 + j) * p.e.ld_in + n) : 0.0f;
+    }
+    if (p.e.grad) {
+        apply_slope<CH>(p.e.act, y, r);
+        return;
+    }
+    if (p.e.pre != nullptr) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+            if (n_in && m0 + j < p.M)
+                aux_store1(p, p.e.pre, static_cast<size_t>(m0 + j) * p.e.ld_pre + n, y[j]);
+    }
+    apply_act<CH>(p.e.act, y);
+    if (p.e.in != nullptr) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+            y[j] += r[j];
+    }
+}
+
+// The same for four consecutive columns n .. n + 3 of row m < M.
+__device__ __forceinline__ void epi_quad(const KernelParams &p, float (&y)[4], int m, int n)
+{
+    float r[4] = {};
+    if (p.e.in != nullptr) {
+        const size_t at = static_cast<size_t>(m) * p.e.ld_in + n;
+        if (p.e.vec_in && n + 3 < p.N) {   // n % 4 == 0
+            if (p.out_type == kOutF32) {
+                const float4 x = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.e.in) + at);
+                r[0] = x.x;
+                r[1] = x.y;
+                r[2] = x.z;
+                r[3] = x.w;
+            } else {
+                const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const unsigned short *>(p.e.in) + at);
+                aux_unpack2(w.x, p.out_type == kOutF16, r[0], r[1]);
+                aux_unpack2(w.y, p.out_type == kOutF16, r[2], r[3]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                r[i] = n + i < p.N ? aux_load1(p, p.e.in, at + i) : 0.0f;
+        }
+    }
+    if (p.e.grad) {
+        apply_slope<4>(p.e.act, y, r);
+        return;
+    }
+    if (p.e.pre != nullptr) {
+        const size_t at = static_cast<size_t>(m) * p.e.ld_pre + n;
+        if (p.e.vec_pre && n + 3 < p.N) {
+            if (p.out_type == kOutF32) {
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.e.pre) + at) = make_float4(y[0], y[1], y[2], y[3]);
+            } else {
+                *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(p.e.pre) + at) =
+                    make_uint2(pack_out2(y[0], y[1], p.out_type), pack_out2(y[2], y[3], p.out_type));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (n + i < p.N)
+                    aux_store1(p, p.e.pre, at + i, y[i]);
+        }
+    }
+    apply_act<4>(p.e.act, y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        y[i] += r[i];
+}
+
 // CH consecutive values of output row m from column n0, for the fp32 and
 // e4m3 outputs: 16-byte stores when the row segment is aligned and whole
 // (p.vec_store), element stores otherwise. Rows m >= M are skipped.
@@ -412,7 +635,7 @@ __device__ __forceinline__ void store_row_wide(const KernelParams &p, const floa
 // operands already loaded: the thread owns output column n, rows
 // m = qbase + j; lane l holds the row scale of row qbase + (l % CH) in sal
 // (broadcast with shuffles), and sb, b are column n's scale and bias.
-template <int CH>
+template <int CH, bool EPI>
 __device__ __forceinline__ void store_swap_chunk(const KernelParams &p, const float (&v)[CH], int n, int qbase,
                                                  float s_tensor, float sal, float sb, float b)
 {
@@ -423,6 +646,8 @@ __device__ __forceinline__ void store_swap_chunk(const KernelParams &p, const fl
         const float s = p.rowwise ? __shfl_sync(kAll, sal, j) * sb : s_tensor;
         y[j] = fmaf(v[j], s, b);
     }
+    if constexpr (EPI)
+        epi_col<CH>(p, y, n, qbase);
     if (n >= p.N)
         return;
     if (p.out_type == kOutBF16 || p.out_type == kOutF16) {
@@ -447,10 +672,12 @@ __device__ __forceinline__ void store_swap_chunk(const KernelParams &p, const fl
 
 // SWAP epilogue of a chunk of the CTA's last tile: the CH values of tile row
 // `row` (output column n) go to the staging array [BN][128] of output
-// elements in the drained operand ring, at [qloc + j][row].
-template <int CH>
+// elements in the drained operand ring, at [qloc + j][row]; qbase is the
+// output row of the chunk's first value.
+template <int CH, bool EPI>
 __device__ __forceinline__ void stage_swap_chunk(const KernelParams &p, const float (&v)[CH], uint8_t *stage, int row,
-                                                 int qloc, float s_tensor, float sal, float sb, float b)
+                                                 int qloc, float s_tensor, float sal, float sb, float b, int n,
+                                                 int qbase)
 {
     constexpr unsigned kAll = 0xffffffffu;
     float y[CH];
@@ -459,6 +686,8 @@ __device__ __forceinline__ void stage_swap_chunk(const KernelParams &p, const fl
         const float s = p.rowwise ? __shfl_sync(kAll, sal, j) * sb : s_tensor;
         y[j] = fmaf(v[j], s, b);
     }
+    if constexpr (EPI)
+        epi_col<CH>(p, y, n, qbase);
     // one type test per chunk, not per element (a per-element test in this
     // unrolled loop measured 28 % slower at 128 x 14336 x 4096)
     if (p.out_type == kOutBF16) {
@@ -478,7 +707,7 @@ __device__ __forceinline__ void stage_swap_chunk(const KernelParams &p, const fl
 // and broadcast with shuffles).
 // TILE: the thread owns output row m = pidx, columns n = qbase + j.
 // SWAP: the thread owns output column n = pidx, rows m = qbase + j.
-template <int CH, bool SWAP>
+template <int CH, bool SWAP, bool EPI>
 __device__ __forceinline__ void store_chunk(const KernelParams &p, const float (&v)[CH], int pidx,
                                             int qbase, float s_tensor, int lane)
 {
@@ -496,6 +725,8 @@ __device__ __forceinline__ void store_chunk(const KernelParams &p, const float (
             const float s = p.rowwise ? sa * __shfl_sync(kAll, sbl, j) : s_tensor;
             y[j] = fmaf(v[j], s, __shfl_sync(kAll, bl, j));
         }
+        if constexpr (EPI)
+            epi_row<CH>(p, y, m, qbase);
         if (m >= p.M)
             return;
         if (p.out_type == kOutF32 || p.out_type == kOutE4M3) {
@@ -525,7 +756,7 @@ __device__ __forceinline__ void store_chunk(const KernelParams &p, const float (
         const float sal = (p.rowwise && ql < p.M) ? __ldg(p.scale_a + ql) : 0.0f;
         const float sb = (p.rowwise && n_in) ? __ldg(p.scale_b + n) : 0.0f;
         const float b = (p.bias != nullptr && n_in) ? bias_value(p, n) : 0.0f;
-        store_swap_chunk<CH>(p, v, n, qbase, s_tensor, sal, sb, b);
+        store_swap_chunk<CH, EPI>(p, v, n, qbase, s_tensor, sal, sb, b);
     }
 }
 
@@ -592,7 +823,7 @@ __device__ __forceinline__ void store_out4(const KernelParams &p, int m, int n, 
 // thread stores its row's 32 values from registers (16-byte stores when the
 // rows are aligned). Stream-K partials in `add` are added first, as in the
 // staged epilogue below.
-template <int BN>
+template <int BN, bool EPI>
 __device__ __forceinline__ void epilogue_rows_wide(const KernelParams &p, uint32_t trow, int m_row0, int n0, int lane,
                                                 float s_tensor, const PartialSrc add)
 {
@@ -623,6 +854,8 @@ __device__ __forceinline__ void epilogue_rows_wide(const KernelParams &p, uint32
             const float s = p.rowwise ? sa * __shfl_sync(kAll, sbl, j) : s_tensor;
             v[j] = fmaf(v[j], s, __shfl_sync(kAll, bl, j));
         }
+        if constexpr (EPI)
+            epi_row<32>(p, v, m, n0 + c * 32);
         store_row_wide<32>(p, v, m, n0 + c * 32);
     }
 }
@@ -717,7 +950,7 @@ __device__ __forceinline__ ColPre<BN> load_col_pre(const KernelParams &p, int n0
     return c;
 }
 
-template <int BN, int NBUF, bool PRE = false, bool FAST_PLAIN = false>
+template <int BN, int NBUF, bool EPI, bool PRE = false, bool FAST_PLAIN = false>
 __device__ __forceinline__ void epilogue_rows_staged(const KernelParams &p, const CUtensorMap *tmap_out,
                                                      uint32_t trow, int m_row0, int n0, int lane,
                                                      uint8_t *stage, uint32_t stage_smem, uint32_t &chunks,
@@ -725,7 +958,7 @@ __device__ __forceinline__ void epilogue_rows_staged(const KernelParams &p, cons
                                                      ColPre<BN> pre = ColPre<BN>{}, float *colv = nullptr)
 {
     if (p.out_type == kOutF32 || p.out_type == kOutE4M3) {
-        epilogue_rows_wide<BN>(p, trow, m_row0, n0, lane, s_tensor, add);
+        epilogue_rows_wide<BN, EPI>(p, trow, m_row0, n0, lane, s_tensor, add);
         return;
     }
     constexpr unsigned kAll = 0xffffffffu;
@@ -801,7 +1034,19 @@ __device__ __forceinline__ void epilogue_rows_staged(const KernelParams &p, cons
                 }
             }
             uint32_t w[16];
-            if (colv != nullptr) {
+            if constexpr (EPI) {
+                // z of the half block, then the extended epilogue on it
+                float y[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float s = p.rowwise ? sa * __shfl_sync(kAll, sbl2[h], j) : s_tensor;
+                    y[j] = fmaf(v[j], s, __shfl_sync(kAll, bl2[h], j));
+                }
+                epi_row<32>(p, y, m, nb + h * 32);
+#pragma unroll
+                for (int j = 0; j < 32; j += 2)
+                    w[j / 2] = pack_out2(y[j], y[j + 1], p.out_type);
+            } else if (colv != nullptr) {
                 convert_row32_any(p, v, w, p.rowwise ? sa : s_tensor, colv + h * 32, colv + 64 + h * 32);
             } else {
             const float sbl = sbl2[h];
@@ -912,7 +1157,7 @@ __device__ __forceinline__ void tmem_load_chunk(uint32_t taddr, float (&v)[CH])
         ptx::tmem_ld_16cols(taddr, v);
 }
 
-template <int BN, bool SWAP, bool WIDE = false>
+template <int BN, bool SWAP, bool WIDE, bool EPI>
 __global__ void __launch_bounds__(TileCfg<BN, SWAP, WIDE>::kThreads, 1)
     fp8mm_tc_kernel(const __grid_constant__ CUtensorMap tmap_p,
                     const __grid_constant__ CUtensorMap tmap_q,
@@ -1117,7 +1362,7 @@ __global__ void __launch_bounds__(TileCfg<BN, SWAP, WIDE>::kThreads, 1)
                 if constexpr (!SWAP) {
                     // the grouped plain-store loop: the 256-wide kernels, which
                     // take the output-bound shallow-K launches
-                    epilogue_rows_staged<kWarpCols, C::kStageBufs, true, (BN >= 256)>(
+                    epilogue_rows_staged<kWarpCols, C::kStageBufs, EPI, true, (BN >= 256)>(
                         pb, &tmap_out, trow + col0, w.tp * kTileP + q * 32, w.tq * BN + col0, lane, stage,
                         stage_smem, chunks, s_tensor, w.b, PartialSrc{}, pre,
                         reinterpret_cast<float *>(smem + (colv0 - sbase)) + ew * 128);
@@ -1135,9 +1380,10 @@ __global__ void __launch_bounds__(TileCfg<BN, SWAP, WIDE>::kThreads, 1)
                         float v[CH];
                         tmem_load_chunk<CH>(trow + c * CH, v);
                         if (last)
-                            stage_swap_chunk<CH>(pb, v, smem, row, c * CH, s_tensor, sal, sw_sb, sw_b);
+                            stage_swap_chunk<CH, EPI>(pb, v, smem, row, c * CH, s_tensor, sal, sw_sb, sw_b, pidx,
+                                                      w.tq * BN + c * CH);
                         else
-                            store_swap_chunk<CH>(pb, v, pidx, w.tq * BN + c * CH, s_tensor, sal, sw_sb, sw_b);
+                            store_swap_chunk<CH, EPI>(pb, v, pidx, w.tq * BN + c * CH, s_tensor, sal, sw_sb, sw_b);
                     }
                     if (last) {
                         staged = true;
@@ -1221,7 +1467,7 @@ __global__ void __launch_bounds__(TileCfg<BN, SWAP, WIDE>::kThreads, 1)
                             v[4 * g + 2] = acc4[g].z;
                             v[4 * g + 3] = acc4[g].w;
                         }
-                        store_chunk<CH, SWAP>(pb, v, pidx, w.tq * BN + c * CH, s_tensor, lane);
+                        store_chunk<CH, SWAP, EPI>(pb, v, pidx, w.tq * BN + c * CH, s_tensor, lane);
                     }
                 }
             }

@@ -58,7 +58,7 @@ struct ClusterKCfg {
     static_assert(kSmemBytes <= 232448, "exceeds 227 KB of shared memory");
 };
 
-template <int BN, int CS>
+template <int BN, int CS, bool EPI>
 __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(kThreads, 1)
     fp8mm_swap_ck_kernel(const __grid_constant__ CUtensorMap tmap_p,
                          const __grid_constant__ CUtensorMap tmap_q, const KernelParams p)
@@ -293,6 +293,8 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     y[i] = fmaf(y[i], pb.rowwise ? sa * red_sb[i] : red_stensor, red_bias[i]);
+                if constexpr (EPI)
+                    epi_quad(pb, y, m, n);
                 // (Staging these rows for one TMA store instead measured 3-5 %
                 // slower here: 16 and 128 x 4096 x 4096.)
                 store_out4(pb, m, n, y);

@@ -137,7 +137,7 @@ __device__ __forceinline__ int sk_partials(const KernelParams &p, int c, int pai
 // 256-row tiles. With p.splits > 1 (row-major form only) each slice writes its
 // fp32 partial to the workspace and the last slice to arrive, per epilogue
 // warp of each CTA, sums the slices in slice order and stores the result.
-template <int BN, bool SWAP>
+template <int BN, bool SWAP, bool EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThreads, 1)
     fp8mm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                       const __grid_constant__ CUtensorMap tmap_b,
@@ -422,7 +422,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThr
                         }
                         add.count = ok_all ? n_add : 0;
                     }
-                    epilogue_rows_staged<kWarpCols, 1>(pb, &tmap_out, trow + col0,
+                    epilogue_rows_staged<kWarpCols, 1, EPI>(pb, &tmap_out, trow + col0,
                                                     w.tp * 256 + static_cast<int>(rank) * 128 + q * 32,
                                                     w.tq * BN + col0, lane, stage, stage_smem, chunks, s_tensor,
                                                     w.b, add);
@@ -438,7 +438,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThr
                     for (int c = 0; c < BN / CH; ++c) {
                         float v[CH];
                         tmem_load_chunk<CH>(trow + c * CH, v);
-                        store_chunk<CH, true>(pb, v, pidx, w.tq * BN + c * CH, s_tensor, lane);
+                        store_chunk<CH, true, EPI>(pb, v, pidx, w.tq * BN + c * CH, s_tensor, lane);
                     }
                 }
                 ptx::tc_fence_before();
@@ -521,7 +521,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThr
                             v[4 * g + 2] = acc4[g].z;
                             v[4 * g + 3] = acc4[g].w;
                         }
-                        store_chunk<CH, false>(pb, v, m, w.tq * BN + c * CH, s_tensor, lane);
+                        store_chunk<CH, false, EPI>(pb, v, m, w.tq * BN + c * CH, s_tensor, lane);
                     }
                 }
             }

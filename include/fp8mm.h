@@ -329,6 +329,75 @@ int fp8_scaled_mm_bf16(const void *A, const void *B, int scale_mode,
                        void *A_q, void *B_q, float *scale_a, float *scale_b,
                        void *stream, const fp8mm_options *options);
 
+/* Activations of the calls below, in fp32:
+ *   RELU       max(z, 0)
+ *   GELU       z Phi(z), Phi the normal distribution function
+ *   GELU_TANH  z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2
+ *   SILU       z / (1 + exp(-z))
+ * A NaN stays NaN; +inf gives +inf and -inf gives 0. Slopes are 1 and 0
+ * there; RELU's slope at 0 is 0. */
+typedef enum fp8mm_activation {
+    FP8MM_ACT_NONE = 0,
+    FP8MM_ACT_RELU = 1,
+    FP8MM_ACT_GELU = 2,
+    FP8MM_ACT_GELU_TANH = 3,
+    FP8MM_ACT_SILU = 4
+} fp8mm_activation;
+
+typedef struct fp8mm_epilogue {
+    int activation;           /* fp8mm_activation                               */
+    const void *residual;     /* [M, N] added after the activation, or NULL     */
+    int64_t ldr;              /* elements between its rows: 0 = N, else >= N    */
+    void *preact;             /* [M, N] receives z, or NULL                     */
+    int64_t ldp;              /* elements between its rows: 0 = N, else >= N    */
+} fp8mm_epilogue;
+
+/*
+ * The product with the rest of a linear layer in its epilogue:
+ *
+ *   z   = acc * (scale_a (x) scale_b) + bias          fp32
+ *   out = cast( act(z) + residual )                   one rounding
+ *
+ * and, when epilogue->preact is given, preact = cast(z): what the backward
+ * pass needs (fp8_act_grad, fp8_scaled_mm_act_grad). The activation takes
+ * the unrounded z. residual and preact have the bias's element type: the
+ * output's, bf16 for an e4m3fn output; rows contiguous, leading dimensions
+ * of their own, aligned to their element. Rows that are 16-byte aligned are
+ * read and written fastest.
+ *
+ * residual may be out itself (same address, same leading dimension, not for
+ * an e4m3fn output): the sum then replaces it. Otherwise out, preact and
+ * every input must not overlap.
+ *
+ * Other arguments, kernels, choice, workspace and errors as
+ * fp8_scaled_mm_ex; options may be NULL. FP8MM_ERR_NULL without epilogue,
+ * FP8MM_ERR_MODE for an unknown activation or a forbidden aliasing,
+ * FP8MM_ERR_SHAPE / _ALIGN for ldr, ldp and the two pointers.
+ */
+int fp8_scaled_mm_epilogue(const void *A, const void *B,
+                           const float *scale_a, const float *scale_b, int scale_mode,
+                           const void *bias, void *out,
+                           int64_t M, int64_t N, int64_t K,
+                           void *stream, const fp8mm_options *options, const fp8mm_epilogue *epilogue);
+
+/*
+ * The product of a backward pass with the gradient of the activation before
+ * it in its epilogue:
+ *
+ *   out = cast( acc * (scale_a (x) scale_b) * act'(z) )
+ *
+ * For y = W2 act(z): A holds dy, B holds W2, z is what fp8_scaled_mm_epilogue
+ * stored as preact, and out is dz. z is [M, N] with leading dimension ldz
+ * (0 = N) and the element type residual has above; it may be out itself
+ * under the same conditions. Where RELU's slope is 0 the result is 0 even
+ * for an infinite product. activation: RELU .. SILU.
+ */
+int fp8_scaled_mm_act_grad(const void *A, const void *B,
+                           const float *scale_a, const float *scale_b, int scale_mode,
+                           int activation, const void *z, int64_t ldz, void *out,
+                           int64_t M, int64_t N, int64_t K,
+                           void *stream, const fp8mm_options *options);
+
 /*
  * Allocation-free variant of fp8_scaled_mm. The pages have no counterpart:
  * this is an addition for callers that cannot allocate device memory while
