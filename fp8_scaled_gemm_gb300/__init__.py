@@ -70,6 +70,8 @@ EXPORTS = (
     "fp8_scaled_mm", "fp8_scaled_mm_config", "fp8_scaled_mm_ex", "fp8_scaled_mm_host",
     "fp8_scaled_mm_noalloc", "fp8_quantize", "fp8_scaled_mm_bf16", "fp8_scaled_bmm",
     "fp8_scaled_mm_layout", "fp8_scaled_mm_epilogue", "fp8_scaled_mm_act_grad",
+    "fp8_act_grad", "fp8_act_grad_workspace", "fp8_layer_norm", "fp8_layer_norm_grad",
+    "fp8_layer_norm_grad_workspace",
     "fp8mm_reserve_workspace", "fp8mm_device_status", "fp8mm_status_string",
     "fp8mm_last_cuda_error", "fp8mm_last_error", "fp8mm_describe_choice", "fp8mm_describe_bmm_choice", "fp8mm_debug_inject", "fp8mm_debug_quant", "fp8mm_describe_model_choice",
     "fp8mm_describe_quant_plan",
@@ -129,6 +131,18 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.fp8_scaled_mm_act_grad.argtypes = [vp, vp, vp, vp, i32, i32, vp, i64, vp, i64, i64, i64, vp,
                                                ctypes.POINTER(Options)]
         lib.fp8_scaled_mm_act_grad.restype = i32
+        f32 = ctypes.c_float
+        lib.fp8_act_grad.argtypes = [vp, i64, vp, i64, i32, i32, vp, i64, vp, i64, i64, vp, i64, vp]
+        lib.fp8_act_grad.restype = i32
+        lib.fp8_act_grad_workspace.argtypes = [i64, i64]
+        lib.fp8_act_grad_workspace.restype = i64
+        lib.fp8_layer_norm.argtypes = [vp, i32, i64, vp, vp, i32, f32, vp, i32, i64, vp, vp, vp, i32, vp, i64, i64, vp]
+        lib.fp8_layer_norm.restype = i32
+        lib.fp8_layer_norm_grad.argtypes = [vp, i32, i64, vp, i32, i64, vp, i32, vp, vp, vp, i64, vp, i64, vp, vp, i64,
+                                            i64, vp, i64, vp]
+        lib.fp8_layer_norm_grad.restype = i32
+        lib.fp8_layer_norm_grad_workspace.argtypes = [i64, i64]
+        lib.fp8_layer_norm_grad_workspace.restype = i64
         lib.fp8_quantize.argtypes = [vp, i64, i64, i32, i32, vp, vp, vp]
         lib.fp8_quantize.restype = i32
         lib.fp8_scaled_mm_bf16.argtypes = [vp, vp, i32, vp, vp, i64, i64, i64, vp, vp, vp, vp, vp,
@@ -504,6 +518,138 @@ def fp8_scaled_mm_bf16(A, B, scale_mode: int, bias=None, out=None, stream=None,
     if return_quantized:
         return out, a_q, bt_q.t(), scale_a, scale_b
     return out
+
+
+_ROW = {torch.bfloat16: OUT_BF16, torch.float16: OUT_F16, torch.float32: OUT_F32}
+
+
+def _rows(name, t, shape=None, dtype=None) -> int:
+    """Row stride of a 2-D bf16 / fp16 / fp32 CUDA matrix with contiguous rows."""
+    if t.dim() != 2 or t.dtype not in _ROW or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor of bfloat16, float16 or float32")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    R, C = t.shape
+    if (C > 1 and t.stride(1) != 1) or (R > 1 and t.stride(0) < C):
+        raise ValueError(f"{name}'s rows must be contiguous, their stride at least {C}")
+    return t.stride(0) if R > 1 else C
+
+
+def _vector(name, t, n, dtypes):
+    if t is not None and (t.dtype not in dtypes or t.numel() != n or not t.is_contiguous() or not t.is_cuda):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} values of " +
+                         " or ".join(str(d) for d in dtypes))
+
+
+def _new(shape, dtype, device, stream):
+    """An output or workspace made on the stream the call runs on, so that its
+    memory is not handed out again before the call is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def fp8_act_grad(dy, z, activation: int, dz=None, dbias=None, stream=None, return_dz: bool = True,
+                 return_dbias: bool = True):
+    """(dz, dbias) with dz = dy * act'(z) and dbias = its fp32 sum over rows.
+
+    ``dy`` and ``z`` are [M, N] of one dtype (bf16, fp16 or fp32); ``z`` may
+    be None with ACT_NONE. dz has their dtype. A result that is not asked for
+    (``return_dz``, ``return_dbias``) is None.
+    """
+    lddy = _rows("dy", dy)
+    M, N = dy.shape
+    ldz = 0 if z is None else _rows("z", z, dy.shape, dy.dtype)
+    if dz is None and return_dz:
+        dz = _new((M, N), dy.dtype, dy.device, stream)
+    lddz = 0 if dz is None else _rows("dz", dz, dy.shape, dy.dtype)
+    ws = None
+    if dbias is None and return_dbias:
+        dbias = _new((N,), torch.float32, dy.device, stream)
+    _vector("dbias", dbias, N, (torch.float32,))
+    lib = load()
+    ws_bytes = 0
+    if dbias is not None:
+        ws_bytes = lib.fp8_act_grad_workspace(M, N)
+        if ws_bytes < 0:
+            _check(int(ws_bytes))
+        ws = _new((ws_bytes,), torch.uint8, dy.device, stream)
+    _check(lib.fp8_act_grad(_ptr(dy), lddy, _ptr(z), ldz, _ROW[dy.dtype], int(activation), _ptr(dz), lddz, _ptr(dbias),
+                            M, N, _ptr(ws), ws_bytes, _stream_handle(stream)))
+    return dz, dbias
+
+
+def fp8_layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, y=None, y_dtype=None, q_dtype=None, stream=None,
+                   return_y: bool = True):
+    """Layer norm of the rows of x [R, C]: (y, mean, rstd), and with
+    ``q_dtype`` also (q, q_scale), the rows' fp8 codes and fp32 scales (the A
+    operand of a row-wise product), made from the unrounded y in the same pass.
+
+    x is bf16, fp16 or fp32 with contiguous rows; gamma and beta are [C] of
+    one of these dtypes (both the same) or None; y has x's dtype unless
+    ``y_dtype`` says otherwise, and is None with ``return_y`` false.
+    """
+    ldx = _rows("x", x)
+    R, C = x.shape
+    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+        raise ValueError("gamma and beta must have one dtype")
+    _vector("gamma", gamma, C, tuple(_ROW))
+    _vector("beta", beta, C, tuple(_ROW))
+    params = gamma if gamma is not None else beta
+    if y is None and return_y:
+        y = _new((R, C), y_dtype or x.dtype, x.device, stream)
+    ldy = 0 if y is None else _rows("y", y, (R, C), y_dtype)
+    stats = _new((2, R), torch.float32, x.device, stream)
+    q = q_scale = None
+    if q_dtype is not None:
+        if q_dtype not in _FP8:
+            raise ValueError("q_dtype must be torch.float8_e4m3fn or torch.float8_e5m2")
+        q = _new((R, C), q_dtype, x.device, stream)
+        q_scale = _new((R,), torch.float32, x.device, stream)
+    _check(load().fp8_layer_norm(_ptr(x), _ROW[x.dtype], ldx, _ptr(gamma), _ptr(beta),
+                                 OUT_F32 if params is None else _ROW[params.dtype], float(eps), _ptr(y),
+                                 OUT_F32 if y is None else _ROW[y.dtype], ldy, _ptr(stats[0]), _ptr(stats[1]),
+                                 _ptr(q), _FP8.get(q_dtype, 0), _ptr(q_scale), R, C, _stream_handle(stream)))
+    return (y, stats[0], stats[1]) if q is None else (y, stats[0], stats[1], q, q_scale)
+
+
+def fp8_layer_norm_grad(dy, x, gamma, mean, rstd, residual_grad=None, dx=None, stream=None,
+                        return_params: bool = True):
+    """Backward pass of fp8_layer_norm: (dx, dgamma, dbeta).
+
+    ``mean`` and ``rstd`` are what the forward pass returned; ``gamma`` may be
+    None. ``residual_grad`` [R, C] of x's dtype is added to dx (and may be
+    ``dx``). dx has x's dtype, dgamma and dbeta are fp32 (None without
+    ``return_params``).
+    """
+    lddy = _rows("dy", dy)
+    ldx = _rows("x", x, dy.shape)
+    R, C = x.shape
+    _vector("gamma", gamma, C, tuple(_ROW))
+    _vector("mean", mean, R, (torch.float32,))
+    _vector("rstd", rstd, R, (torch.float32,))
+    lddres = 0 if residual_grad is None else _rows("residual_grad", residual_grad, x.shape, x.dtype)
+    if dx is None:
+        dx = _new((R, C), x.dtype, x.device, stream)
+    lddx = _rows("dx", dx, x.shape, x.dtype)
+    lib = load()
+    dgamma = dbeta = ws = None
+    ws_bytes = 0
+    if return_params:
+        ws_bytes = lib.fp8_layer_norm_grad_workspace(R, C)
+        if ws_bytes < 0:
+            _check(int(ws_bytes))
+        dgamma = _new((C,), torch.float32, x.device, stream)
+        dbeta = _new((C,), torch.float32, x.device, stream)
+        ws = _new((ws_bytes,), torch.uint8, x.device, stream)
+    _check(lib.fp8_layer_norm_grad(_ptr(dy), _ROW[dy.dtype], lddy, _ptr(x), _ROW[x.dtype], ldx, _ptr(gamma),
+                                   OUT_F32 if gamma is None else _ROW[gamma.dtype], _ptr(mean), _ptr(rstd),
+                                   _ptr(residual_grad), lddres, _ptr(dx), lddx, _ptr(dgamma), _ptr(dbeta), R, C,
+                                   _ptr(ws), ws_bytes, _stream_handle(stream)))
+    return dx, dgamma, dbeta
 
 
 def fp8mm_reserve_workspace(nbytes: int) -> None:

@@ -1,0 +1,103 @@
+// fp8mm_norm.cu -- C entry of layer norm's forward pass.
+#include "fp8mm_norm.cuh"
+#include "fp8mm_rows_host.h"
+
+namespace {
+
+using namespace fp8mm_host;
+using fp8norm::NormParams;
+
+template <int ES, int G, int LANES, int WARPS, int CH>
+int launch_rows(const NormParams &p, int sms, cudaStream_t stream)
+{
+    constexpr int threads = fp8norm::kCtaThreads<LANES, WARPS>;
+    constexpr int teams = threads / (LANES * WARPS);
+    const int grid = static_cast<int>(std::min<int64_t>(cdiv(p.R, teams), static_cast<int64_t>(sms) * 64));
+    return launch_pdl(fp8norm::norm_rows_kernel<ES, G, LANES, WARPS, CH>, grid, threads, 0, stream,
+                      "layer norm launch", p);
+}
+
+// The smallest team that holds a row of g groups in registers.
+template <int ES>
+int launch(const NormParams &p, bool vec, int sms, cudaStream_t stream)
+{
+    const int64_t g = p.groups;
+    if (vec) {
+        if (g <= 4) return launch_rows<ES, 8, 4, 1, 1>(p, sms, stream);
+        if (g <= 8) return launch_rows<ES, 8, 8, 1, 1>(p, sms, stream);
+        if (g <= 16) return launch_rows<ES, 8, 16, 1, 1>(p, sms, stream);
+        if (g <= 32) return launch_rows<ES, 8, 32, 1, 1>(p, sms, stream);
+        if (g <= 64) return launch_rows<ES, 8, 32, 1, 2>(p, sms, stream);
+        if (g <= 128) return launch_rows<ES, 8, 32, 1, 4>(p, sms, stream);
+        if (g <= 256) return launch_rows<ES, 8, 32, 2, 4>(p, sms, stream);
+        if (g <= 512) return launch_rows<ES, 8, 32, 4, 4>(p, sms, stream);
+        if (g <= 1024) return launch_rows<ES, 8, 32, 8, 4>(p, sms, stream);
+        if (g <= 2048) return launch_rows<ES, 8, 32, 16, 4>(p, sms, stream);
+        if (g <= 4096) return launch_rows<ES, 8, 32, 32, 4>(p, sms, stream);
+    } else {
+        if (g <= 256) return launch_rows<ES, 1, 32, 1, 8>(p, sms, stream);
+        if (g <= 1024) return launch_rows<ES, 1, 32, 4, 8>(p, sms, stream);
+        if (g <= 4096) return launch_rows<ES, 1, 32, 8, 16>(p, sms, stream);
+        if (g <= 8192) return launch_rows<ES, 1, 32, 16, 16>(p, sms, stream);
+        if (g <= 16384) return launch_rows<ES, 1, 32, 32, 16>(p, sms, stream);
+    }
+    const int grid = static_cast<int>(std::min<int64_t>(p.R, static_cast<int64_t>(sms) * 8));
+    if (vec)
+        return launch_pdl(fp8norm::norm_long_kernel<ES, 8>, grid, fp8norm::kLongThreads, 0, stream,
+                          "layer norm launch", p);
+    return launch_pdl(fp8norm::norm_long_kernel<ES, 1>, grid, fp8norm::kLongThreads, 0, stream, "layer norm launch", p);
+}
+
+}  // namespace
+
+extern "C" int fp8_layer_norm(const void *x, int x_type, int64_t ldx, const void *gamma, const void *beta,
+                              int param_type, float eps, void *y, int y_type, int64_t ldy, float *mean, float *rstd,
+                              void *q, int q_type, float *q_scale, int64_t R, int64_t C, void *stream)
+{
+    if (!row_type_known(x_type) || !row_type_known(y_type) || !row_type_known(param_type) ||
+        (q && q_type != FP8MM_TYPE_E4M3 && q_type != FP8MM_TYPE_E5M2))
+        return FP8MM_ERR_MODE;
+    if (R < 0 || C < 0 || R > (int64_t(1) << 40) / std::max<int64_t>(C, 1) || !(eps >= 0.0f) || eps > 3e38f)
+        return FP8MM_ERR_SHAPE;
+    int rc;
+    if ((rc = check_rows(x, ldx, C, x_type)) != FP8MM_OK || (rc = check_rows(y, ldy, C, y_type)) != FP8MM_OK ||
+        (rc = check_rows(gamma, 0, C, param_type)) != FP8MM_OK ||
+        (rc = check_rows(beta, 0, C, param_type)) != FP8MM_OK ||
+        (rc = check_rows(mean, 0, C, FP8MM_OUT_F32)) != FP8MM_OK ||
+        (rc = check_rows(rstd, 0, C, FP8MM_OUT_F32)) != FP8MM_OK ||
+        (rc = check_rows(q_scale, 0, C, FP8MM_OUT_F32)) != FP8MM_OK)
+        return rc;
+    if (R == 0 || C == 0)
+        return FP8MM_OK;
+    if (!x || (q && !q_scale))
+        return FP8MM_ERR_NULL;
+    if (y == x || q == x || (q && q == y))
+        return FP8MM_ERR_MODE;   // a long row is read more than once
+    int sms = 0;
+    if ((rc = device_sms(&sms)) != FP8MM_OK)
+        return rc;
+    NormParams p{};
+    p.x = x;
+    p.ldx = ldx > 0 ? ldx : C;
+    p.x_f16 = x_type == FP8MM_OUT_F16;
+    p.gamma = gamma;
+    p.beta = beta;
+    p.param_type = param_type;
+    p.eps = eps;
+    p.y = y;
+    p.y_type = y_type;
+    p.ldy = ldy > 0 ? ldy : C;
+    p.mean = mean;
+    p.rstd = rstd;
+    p.q = static_cast<uint8_t *>(q);
+    p.q_type = q_type;
+    p.q_scale = q_scale;
+    p.R = R;
+    p.C = C;
+    const bool vec = C % 8 == 0 && rows_vec(x, p.ldx, x_type) && (!y || rows_vec(y, p.ldy, y_type)) &&
+                     rows_vec(gamma, 0, param_type) && rows_vec(beta, 0, param_type) &&
+                     (reinterpret_cast<uintptr_t>(q) & 7) == 0;
+    p.groups = vec ? C / 8 : C;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return x_type == FP8MM_OUT_F32 ? launch<4>(p, vec, sms, s) : launch<2>(p, vec, sms, s);
+}

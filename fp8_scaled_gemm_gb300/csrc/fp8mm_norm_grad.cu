@@ -1,0 +1,183 @@
+// fp8mm_norm_grad.cu -- C entry of layer norm's backward pass.
+#include "fp8mm_norm.cuh"
+#include "fp8mm_rows_host.h"
+
+namespace {
+
+using namespace fp8mm_host;
+using fp8norm::NormGradParams;
+
+// CTAs per SM of the row kernels, and so of the partial sums.
+constexpr int kCtasPerSm = 2;
+
+// Partial sums of dgamma and dbeta a call on R rows may write.
+int64_t max_partials(int64_t R, int sms) { return std::min<int64_t>(R, static_cast<int64_t>(sms) * kCtasPerSm); }
+
+int sum_partials(const NormGradParams &p, int P, float *dgamma, float *dbeta, cudaStream_t stream)
+{
+    fp8rows::PartialSumParams s{};
+    s.partial = p.partial;
+    s.out0 = dgamma;
+    s.out1 = dbeta;
+    s.C = p.C;
+    s.P = P;
+    s.K = 2;
+    return launch_pdl(fp8rows::partial_sum_kernel, static_cast<int>(cdiv(p.C, 32)), fp8rows::kSumThreads, 0, stream,
+                      "parameter sum launch", s);
+}
+
+template <int ES, int DES, int G, int LANES, int WARPS, int CH>
+int launch_rows(const NormGradParams &p, int sms, cudaStream_t stream, int *partials)
+{
+    constexpr int threads = fp8norm::kCtaThreads<LANES, WARPS>;
+    constexpr int teams = threads / (LANES * WARPS);
+    const int grid = static_cast<int>(std::min<int64_t>(cdiv(p.R, teams),
+                                                        static_cast<int64_t>(sms) * (threads > 512 ? 1 : kCtasPerSm)));
+    *partials = grid;
+    return launch_pdl(fp8norm::norm_grad_rows_kernel<ES, DES, G, LANES, WARPS, CH>, grid, threads, 0, stream,
+                      "layer norm gradient launch", p);
+}
+
+template <int ES, int DES, int G>
+int launch_long(const NormGradParams &p, int sms, cudaStream_t stream, int *partials)
+{
+    int rc = FP8MM_OK;
+    if (p.dx)
+        rc = launch_pdl(fp8norm::norm_grad_long_kernel<ES, DES, G>,
+                        static_cast<int>(std::min<int64_t>(p.R, static_cast<int64_t>(sms) * 8)),
+                        fp8norm::kLongThreads, 0, stream, "layer norm gradient launch", p);
+    if (rc != FP8MM_OK || !p.partial)
+        return rc;
+    const int64_t strips = cdiv(p.groups, 256);
+    const int64_t slabs = std::max<int64_t>(
+        1, std::min<int64_t>(max_partials(p.R, sms), static_cast<int64_t>(sms) * 8 / strips));
+    *partials = static_cast<int>(slabs);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(strips), static_cast<unsigned>(slabs), 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = stream;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8norm::norm_grad_cols_kernel<ES, DES, G>, p);
+    return e == cudaSuccess ? FP8MM_OK : cuda_fail(e, "layer norm parameter launch");
+}
+
+// The smallest team that holds a row of g groups, and its column sums, in registers.
+template <int ES, int DES>
+int launch(const NormGradParams &p, bool vec, int sms, cudaStream_t stream, int *P)
+{
+    const int64_t g = p.groups;
+    if (vec) {
+        if (g <= 4) return launch_rows<ES, DES, 8, 4, 1, 1>(p, sms, stream, P);
+        if (g <= 8) return launch_rows<ES, DES, 8, 8, 1, 1>(p, sms, stream, P);
+        if (g <= 16) return launch_rows<ES, DES, 8, 16, 1, 1>(p, sms, stream, P);
+        if (g <= 32) return launch_rows<ES, DES, 8, 32, 1, 1>(p, sms, stream, P);
+        if (g <= 64) return launch_rows<ES, DES, 8, 32, 1, 2>(p, sms, stream, P);
+        if (g <= 128) return launch_rows<ES, DES, 8, 32, 2, 2>(p, sms, stream, P);
+        if (g <= 256) return launch_rows<ES, DES, 8, 32, 4, 2>(p, sms, stream, P);
+        if (g <= 512) return launch_rows<ES, DES, 8, 32, 8, 2>(p, sms, stream, P);
+        if (g <= 1024) return launch_rows<ES, DES, 8, 32, 16, 2>(p, sms, stream, P);
+        return launch_long<ES, DES, 8>(p, sms, stream, P);
+    }
+    if (g <= 256) return launch_rows<ES, DES, 1, 32, 1, 8>(p, sms, stream, P);
+    if (g <= 1024) return launch_rows<ES, DES, 1, 32, 4, 8>(p, sms, stream, P);
+    if (g <= 2048) return launch_rows<ES, DES, 1, 32, 8, 8>(p, sms, stream, P);
+    if (g <= 4096) return launch_rows<ES, DES, 1, 32, 16, 8>(p, sms, stream, P);
+    if (g <= 8192) return launch_rows<ES, DES, 1, 32, 32, 8>(p, sms, stream, P);
+    return launch_long<ES, DES, 1>(p, sms, stream, P);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t fp8_layer_norm_grad_workspace(int64_t R, int64_t C)
+{
+    if (R < 0 || C < 0 || R > (int64_t(1) << 40) / std::max<int64_t>(C, 1))
+        return FP8MM_ERR_SHAPE;
+    int sms = 0;
+    const int rc = device_sms(&sms);
+    if (rc != FP8MM_OK)
+        return rc;
+    return max_partials(R, sms) * 2 * C * static_cast<int64_t>(sizeof(float));
+}
+
+int fp8_layer_norm_grad(const void *dy, int dy_type, int64_t lddy, const void *x, int x_type, int64_t ldx,
+                        const void *gamma, int param_type, const float *mean, const float *rstd, const void *dres,
+                        int64_t lddres, void *dx, int64_t lddx, float *dgamma, float *dbeta, int64_t R, int64_t C,
+                        void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (!row_type_known(x_type) || !row_type_known(dy_type) || !row_type_known(param_type))
+        return FP8MM_ERR_MODE;
+    if (R < 0 || C < 0 || R > (int64_t(1) << 40) / std::max<int64_t>(C, 1))
+        return FP8MM_ERR_SHAPE;
+    int rc;
+    if ((rc = check_rows(x, ldx, C, x_type)) != FP8MM_OK || (rc = check_rows(dy, lddy, C, dy_type)) != FP8MM_OK ||
+        (rc = check_rows(dres, lddres, C, x_type)) != FP8MM_OK || (rc = check_rows(dx, lddx, C, x_type)) != FP8MM_OK ||
+        (rc = check_rows(gamma, 0, C, param_type)) != FP8MM_OK)
+        return rc;
+    for (const void *f : {static_cast<const void *>(mean), static_cast<const void *>(rstd),
+                          static_cast<const void *>(dgamma), static_cast<const void *>(dbeta),
+                          static_cast<const void *>(workspace)})
+        if ((rc = check_rows(f, 0, C, FP8MM_OUT_F32)) != FP8MM_OK)
+            return rc;
+    if (!dgamma != !dbeta)
+        return FP8MM_ERR_NULL;
+    if (C == 0 || (R == 0 && !dgamma))
+        return FP8MM_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int sms = 0;
+    if (R == 0) {
+        // sums over no rows
+        if ((rc = device_sms(&sms)) != FP8MM_OK)
+            return rc;
+        cudaError_t e = cudaMemsetAsync(dgamma, 0, static_cast<size_t>(C) * 4, s);
+        if (e == cudaSuccess)
+            e = cudaMemsetAsync(dbeta, 0, static_cast<size_t>(C) * 4, s);
+        return e == cudaSuccess ? FP8MM_OK : cuda_fail(e, "cudaMemsetAsync(parameter gradients)");
+    }
+    if (!dy || !x || !mean || !rstd)
+        return FP8MM_ERR_NULL;
+    const int64_t ldr = lddres > 0 ? lddres : C, ldd = lddx > 0 ? lddx : C;
+    if (dx && (dx == dy || dx == x || (dx == dres && ldr != ldd)))
+        return FP8MM_ERR_MODE;   // dx may replace dres only, every element over itself
+    if ((rc = device_sms(&sms)) != FP8MM_OK)
+        return rc;
+    if (dgamma) {
+        const int64_t need = max_partials(R, sms) * 2 * C * static_cast<int64_t>(sizeof(float));
+        if (!workspace)
+            return FP8MM_ERR_NULL;
+        if (workspace_bytes < need)
+            return FP8MM_ERR_SHAPE;
+    }
+    NormGradParams p{};
+    p.dy = dy;
+    p.x = x;
+    p.lddy = lddy > 0 ? lddy : C;
+    p.ldx = ldx > 0 ? ldx : C;
+    p.dy_f16 = dy_type == FP8MM_OUT_F16;
+    p.x_f16 = x_type == FP8MM_OUT_F16;
+    p.gamma = gamma;
+    p.param_type = param_type;
+    p.mean = mean;
+    p.rstd = rstd;
+    p.dres = dx ? dres : nullptr;
+    p.lddres = ldr;
+    p.dx = dx;
+    p.lddx = ldd;
+    p.x_type = x_type;
+    p.partial = dgamma ? static_cast<float *>(workspace) : nullptr;
+    p.R = R;
+    p.C = C;
+    const bool vec = C % 8 == 0 && rows_vec(x, p.ldx, x_type) && rows_vec(dy, p.lddy, dy_type) &&
+                     (!p.dres || rows_vec(dres, ldr, x_type)) && (!dx || rows_vec(dx, ldd, x_type)) &&
+                     rows_vec(gamma, 0, param_type);
+    p.groups = vec ? C / 8 : C;
+    int P = 0;
+    const bool x4 = x_type == FP8MM_OUT_F32, d4 = dy_type == FP8MM_OUT_F32;
+    rc = x4 ? (d4 ? launch<4, 4>(p, vec, sms, s, &P) : launch<4, 2>(p, vec, sms, s, &P))
+            : (d4 ? launch<2, 4>(p, vec, sms, s, &P) : launch<2, 2>(p, vec, sms, s, &P));
+    if (rc != FP8MM_OK || !dgamma)
+        return rc;
+    return sum_partials(p, P, dgamma, dbeta, s);
+}
+
+}  // extern "C"

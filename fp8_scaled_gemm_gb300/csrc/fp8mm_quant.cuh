@@ -26,24 +26,14 @@
 // above +inf, so a packed 16-bit unsigned max (two elements per instruction)
 // gives amax, and a NaN anywhere makes the scale NaN as a float max would.
 //
-// Division: x / scale must be the correctly rounded fp32 quotient, because
-// the quotient decides an fp8 code. For scales in [2^-80, 2^100) the kernels
-// use r = RN(1/scale), q0 = RN(x r), e = RN(q0 scale - x) (one FMA, exact)
-// and q1 = RN(q0 - e r) (one FMA): Markstein's correction of a quotient by
-// its residual (P. Markstein, "Computation of elementary functions on the
-// IBM RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990), which gives
-// RN(x / scale) for every bf16 x and every scale this recipe produces while
-// the residual stays a normal number, i.e. for |x| >= 2^-100. Smaller |x|
-// have |x / scale| < 2^-20, below half the smallest fp8 subnormal, and q1
-// is then within a few fp32 ulps of the quotient: the code is +-0 either
-// way. The signs of the FMA operands are chosen so that x = -0 gives -0.
-// Scales outside that range, zero, inf or NaN take the IEEE division
-// __fdiv_rn.
+// The division x / scale and the conversion to codes are in
+// fp8mm_quant_convert.cuh.
 #pragma once
 
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "fp8mm_quant_convert.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fp8q {
@@ -74,8 +64,6 @@ struct QuantParams {
     unsigned long long timeout_cycles;   // its bound on each wait
 };
 
-__device__ __forceinline__ float qmax_of(int q_type) { return q_type == 0 ? 448.0f : 57344.0f; }
-
 // Two |bf16| patterns per word, unsigned max per half.
 __device__ __forceinline__ uint32_t amax_acc(uint32_t acc, uint32_t w) { return __vmaxu2(acc, w & 0x7FFF7FFFu); }
 __device__ __forceinline__ uint32_t amax_acc(uint32_t acc, const uint4 &v)
@@ -86,56 +74,6 @@ __device__ __forceinline__ uint32_t amax_acc(uint32_t acc, const uint4 &v)
     return amax_acc(acc, v.w);
 }
 __device__ __forceinline__ uint32_t fold_halves(uint32_t acc) { return max(acc & 0xFFFFu, acc >> 16); }
-
-struct Divider {
-    float s, r;
-    int mode;   // 0: zero scale, 1: reciprocal + one correction, 2: IEEE division
-};
-
-__device__ __forceinline__ Divider make_divider(float s)
-{
-    Divider d;
-    d.s = s;
-    d.r = 0.0f;
-    if (s == 0.0f) {
-        d.mode = 0;
-    } else if (s >= 0x1p-80f && s < 0x1p100f) {
-        d.r = __frcp_rn(s);
-        d.mode = 1;
-    } else {
-        d.mode = 2;
-    }
-    return d;
-}
-
-// x / scale for the reciprocal path (mode 1); x is finite there.
-__device__ __forceinline__ float div_fast(const Divider &d, float x)
-{
-    const float q0 = __fmul_rn(x, d.r);
-    const float e = __fmaf_rn(q0, d.s, -x);
-    return __fmaf_rn(-e, d.r, q0);
-}
-
-// x / scale for the other modes.
-__device__ __forceinline__ float div_slow(const Divider &d, float x)
-{
-    if (d.mode == 0)
-        return x;                                           // +-0 stays +-0
-    const float v = __fdiv_rn(x, d.s);
-    return v != v ? __uint_as_float(0x7FFFFFFFu) : v;       // one NaN code
-}
-
-// Two fp32 values to two fp8 codes (lo in the low byte), round to nearest even,
-// saturating at +-qmax: the same as clamping to [-qmax, qmax] and rounding.
-__device__ __forceinline__ uint32_t cvt_pair(float lo, float hi, int q_type)
-{
-    uint16_t r;
-    if (q_type == 0)
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    else
-        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }

@@ -399,6 +399,96 @@ int fp8_scaled_mm_act_grad(const void *A, const void *B,
                            void *stream, const fp8mm_options *options);
 
 /*
+ * Gradient of an activation and of the bias before it (the backward pass of
+ * fp8_scaled_mm_epilogue, when the product that makes dy does not apply the
+ * slope itself):
+ *
+ *   dz       = cast( dy * act'(z) )
+ *   dbias[n] = sum over m of dy[m, n] act'(z[m, n])     fp32, from the unrounded products
+ *
+ *   dy, z, dz  [M, N], rows contiguous, row strides lddy, ldz, lddz (0 = N),
+ *              all of `type`: FP8MM_OUT_BF16, _F16 or _F32. z may be NULL
+ *              with FP8MM_ACT_NONE (slope 1: the bias gradient alone). dz may
+ *              be NULL (not wanted), or dy or z itself with the same stride.
+ *   dbias      fp32 [N], or NULL (not wanted).
+ *   workspace  device memory of at least fp8_act_grad_workspace(M, N) bytes,
+ *              4-byte aligned, when dbias is wanted; its contents are
+ *              scratch of this call. Calls on different streams with
+ *              workspaces of their own do not interfere.
+ *
+ * M == 0 gives a dbias of zeros. The sums are added in an order that depends
+ * on the sizes and the SM count only, so results repeat. M * N <= 2^40.
+ * Asynchronous on `stream`; errors as above.
+ */
+int fp8_act_grad(const void *dy, int64_t lddy, const void *z, int64_t ldz, int type, int activation,
+                 void *dz, int64_t lddz, float *dbias, int64_t M, int64_t N,
+                 void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace fp8_act_grad needs for dbias on the current device, or
+ * a negative fp8mm_status. */
+int64_t fp8_act_grad_workspace(int64_t M, int64_t N);
+
+/*
+ * Layer norm of each row, with the row's fp8 codes on request: the step
+ * before a row-wise product.
+ *
+ *   mean = sum x / C,  var = sum (x - mean)^2 / C,  rstd = 1 / sqrt(var + eps)
+ *   y    = (x - mean) rstd gamma + beta
+ *   q_scale = max |y| / qmax,  q = fp8( y / q_scale )      as fp8_quantize, row-wise
+ *
+ * in fp32; q is made from the unrounded y. q [R, C] with q_scale [R] is the A
+ * operand of fp8_scaled_mm with FP8MM_SCALE_ROWWISE.
+ *
+ *   x          [R, C] of x_type, row stride ldx (0 = C); types
+ *              FP8MM_OUT_BF16, _F16 or _F32.
+ *   gamma, beta  [C] of param_type, or NULL for 1 and 0.
+ *   eps        finite, >= 0.
+ *   y          [R, C] of y_type, row stride ldy, or NULL (not wanted); not x.
+ *   mean, rstd fp32 [R], or NULL (not wanted): what the backward pass takes.
+ *   q, q_scale fp8 [R, C] contiguous of q_type (FP8MM_TYPE_*) and fp32 [R],
+ *              or q NULL (not wanted).
+ *
+ * A NaN or infinity makes its whole row NaN. Rows of zeros in y give the
+ * codes of zeros and a zero scale. Any C >= 1; rows whose x, y, gamma and
+ * beta start on 16 bytes (q on 8) with C % 8 == 0 run fastest.
+ * R * C <= 2^40. Asynchronous on `stream`, one launch, no workspace.
+ */
+int fp8_layer_norm(const void *x, int x_type, int64_t ldx,
+                   const void *gamma, const void *beta, int param_type, float eps,
+                   void *y, int y_type, int64_t ldy, float *mean, float *rstd,
+                   void *q, int q_type, float *q_scale, int64_t R, int64_t C, void *stream);
+
+/*
+ * Layer norm's backward pass: with xhat = (x - mean) rstd and w = dy gamma,
+ *
+ *   dx     = cast( rstd (w - sum w / C - xhat sum(w xhat) / C) + dres )
+ *   dgamma = sum over rows of dy xhat,   dbeta = sum over rows of dy      fp32 [C]
+ *
+ *   dy         [R, C] of dy_type, row stride lddy; x as in fp8_layer_norm.
+ *   gamma      as in fp8_layer_norm (NULL: 1); mean, rstd fp32 [R].
+ *   dres       [R, C] of x_type with row stride lddres, added to dx (the
+ *              gradient of a residual stream that x also feeds), or NULL.
+ *   dx         [R, C] of x_type, or NULL (not wanted); may be dres itself
+ *              with the same stride, but not x or dy.
+ *   dgamma, dbeta  both or neither.
+ *   workspace  device memory of at least fp8_layer_norm_grad_workspace(R, C)
+ *              bytes, 4-byte aligned, when dgamma and dbeta are wanted;
+ *              scratch of this call.
+ *
+ * R == 0 gives parameter gradients of zeros. The sums are added in an order
+ * that depends on the sizes, alignment and SM count only, so results repeat.
+ */
+int fp8_layer_norm_grad(const void *dy, int dy_type, int64_t lddy, const void *x, int x_type, int64_t ldx,
+                        const void *gamma, int param_type, const float *mean, const float *rstd,
+                        const void *dres, int64_t lddres, void *dx, int64_t lddx,
+                        float *dgamma, float *dbeta, int64_t R, int64_t C,
+                        void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace fp8_layer_norm_grad needs for dgamma and dbeta on the
+ * current device, or a negative fp8mm_status. */
+int64_t fp8_layer_norm_grad_workspace(int64_t R, int64_t C);
+
+/*
  * Allocation-free variant of fp8_scaled_mm. The pages have no counterpart:
  * this is an addition for callers that cannot allocate device memory while
  * they run (for example code running inside a memory pool it does not own,

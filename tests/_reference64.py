@@ -102,3 +102,49 @@ def assert_close(got: torch.Tensor, want: np.ndarray, tol: np.ndarray, what=""):
         i = int(np.argmax(np.where(bad, err / np.maximum(lim, 1e-300), 0)))
         raise AssertionError(f"{what}: {int(bad.sum())} of {bad.size} off; worst {g[fin][i]} for {want[fin][i]} "
                              f"(error {err[i]:.3g}, allowed {lim[i]:.3g})")
+
+
+# ------------------------------------------------------------ layer norm ---
+
+def layer_norm(x, gamma, beta, eps):
+    """(y, mean, rstd) of rows x in 64 bits."""
+    x = np.asarray(x, dtype=np.float64)
+    mean = x.mean(axis=1)
+    rstd = 1.0 / np.sqrt(((x - mean[:, None]) ** 2).mean(axis=1) + eps)
+    return (x - mean[:, None]) * rstd[:, None] * gamma + beta, mean, rstd
+
+
+def layer_norm_grad(dy, x, gamma, mean, rstd):
+    """(dx, dgamma, dbeta) for given statistics."""
+    h = (x - mean[:, None]) * rstd[:, None]
+    w = dy * gamma
+    dx = rstd[:, None] * (w - w.mean(axis=1, keepdims=True) - h * (w * h).mean(axis=1, keepdims=True))
+    return dx, (dy * h).sum(axis=0), dy.sum(axis=0)
+
+
+# A fp32 sum of n terms made of chains of at most 128 additions (per thread,
+# then over lanes, warps and CTAs) is off by at most 128 x 2^-24 of the sum of
+# the terms' magnitudes.
+SUM_ERR = 2.0 ** -17
+
+
+def layer_norm_tol(x, gamma, beta, eps):
+    """Bounds of the fp32 kernels' error in (y, mean, rstd)."""
+    y, mean, rstd = layer_norm(x, gamma, beta, eps)
+    mean_tol = SUM_ERR * np.abs(x).mean(axis=1) + 2.0 ** -23 * np.abs(mean)
+    h = (x - mean[:, None]) * rstd[:, None]
+    # the variance: its own sum, the squared error of the mean (second order),
+    # and 8 roundings; rstd takes half of its relative error
+    rstd_rel = SUM_ERR + 2.0 ** -20 + (mean_tol * rstd) ** 2
+    y_tol = np.abs(gamma) * (rstd[:, None] * mean_tol[:, None] + np.abs(h) * (rstd_rel[:, None] + 2.0 ** -21)) + \
+        2.0 ** -22 * (np.abs(y) + np.abs(beta))
+    return y_tol, mean_tol, rstd * rstd_rel
+
+
+def layer_norm_grad_tol(dy, x, gamma, mean, rstd):
+    """Bounds of the fp32 kernels' error in (dx, dgamma, dbeta)."""
+    h = np.abs((x - mean[:, None]) * rstd[:, None])
+    w = np.abs(dy * gamma)
+    m1, m2 = w.mean(axis=1, keepdims=True), (w * h).mean(axis=1, keepdims=True)
+    dx = rstd[:, None] * ((SUM_ERR + 2.0 ** -20) * (m1 + h * m2) + 2.0 ** -20 * w)
+    return dx, (SUM_ERR + 2.0 ** -21) * (np.abs(dy) * h).sum(axis=0), SUM_ERR * np.abs(dy).sum(axis=0)
