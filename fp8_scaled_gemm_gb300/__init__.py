@@ -15,6 +15,7 @@ Summary (bias).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -97,6 +98,8 @@ def lib_path() -> str:
 def load(build_if_missing: bool = False) -> ctypes.CDLL:
     """Load ``libfp8mm.so`` (built by ``__graft_entry__.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -191,13 +194,15 @@ def _check(rc: int):
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream_handle(stream) -> ctypes.c_void_p:
+def _stream_handle(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(int(stream.cuda_stream))
+        # the current stream of the current device, without the Stream object
+        # torch.cuda.current_stream() makes (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return int(stream.cuda_stream)
 
 
 def _validate(A, B, scale_a, scale_b, scale_mode, bias, out, device_side: bool, typed: bool = False):
@@ -304,10 +309,10 @@ def fp8_scaled_mm_epilogue(A, B, scale_a, scale_b, scale_mode: int, bias=None, a
     (out, preact) with ``return_preact`` (preact is then made if not given).
     """
     if out is None:
-        out = torch.empty((A.shape[0], B.shape[1]), dtype=out_dtype, device=A.device)
+        out = _new(A, (A.shape[0], B.shape[1]), out_dtype, stream)
     M, N, K = _validate(A, B, scale_a, scale_b, scale_mode, bias, out, True, typed=True)
     if return_preact and preact is None:
-        preact = torch.empty((M, N), dtype=_BIAS[out.dtype], device=out.device)
+        preact = _new(A, (M, N), _BIAS[out.dtype], stream)
     ldr = 0 if residual is None else _aux_matrix("residual", residual, M, N, _BIAS[out.dtype])
     ldp = 0 if preact is None else _aux_matrix("preact", preact, M, N, _BIAS[out.dtype])
     ldo = 0 if out.is_contiguous() else int(out.stride(0))
@@ -326,7 +331,7 @@ def fp8_scaled_mm_act_grad(A, B, scale_a, scale_b, scale_mode: int, z, activatio
     the activation before it. ``z`` [M, N] is what fp8_scaled_mm_epilogue
     returned as preact; out has z's dtype unless given otherwise."""
     if out is None:
-        out = torch.empty((A.shape[0], B.shape[1]), dtype=out_dtype or z.dtype, device=A.device)
+        out = _new(A, (A.shape[0], B.shape[1]), out_dtype or z.dtype, stream)
     M, N, K = _validate(A, B, scale_a, scale_b, scale_mode, None, out, True, typed=True)
     ldz = _aux_matrix("z", z, M, N, _BIAS[out.dtype])
     ldo = 0 if out.is_contiguous() else int(out.stride(0))
@@ -527,10 +532,12 @@ def _rows(name, t, shape=None, dtype=None) -> int:
     """Row stride of a 2-D bf16 / fp16 / fp32 CUDA matrix with contiguous rows."""
     if t.dim() != 2 or t.dtype not in _ROW or not t.is_cuda:
         raise ValueError(f"{name} must be a 2-D CUDA tensor of bfloat16, float16 or float32")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}")
+    if t.is_contiguous():
+        return t.shape[1]
     R, C = t.shape
     if (C > 1 and t.stride(1) != 1) or (R > 1 and t.stride(0) < C):
         raise ValueError(f"{name}'s rows must be contiguous, their stride at least {C}")
@@ -543,13 +550,23 @@ def _vector(name, t, n, dtypes):
                          " or ".join(str(d) for d in dtypes))
 
 
-def _new(shape, dtype, device, stream):
-    """An output or workspace made on the stream the call runs on, so that its
-    memory is not handed out again before the call is done with it."""
+def _new(like, shape, dtype, stream):
+    """An output or workspace on ``like``'s device, made on the stream the
+    call runs on, so that its memory is not handed out again before the call
+    is done with it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(entry: str, device: int, rows: int, cols: int) -> int:
+    """A workspace query's answer: it depends on the sizes and the device only."""
+    n = int(getattr(load(), entry)(rows, cols))
+    if n < 0:
+        _check(n)
+    return n
 
 
 def fp8_act_grad(dy, z, activation: int, dz=None, dbias=None, stream=None, return_dz: bool = True,
@@ -564,21 +581,17 @@ def fp8_act_grad(dy, z, activation: int, dz=None, dbias=None, stream=None, retur
     M, N = dy.shape
     ldz = 0 if z is None else _rows("z", z, dy.shape, dy.dtype)
     if dz is None and return_dz:
-        dz = _new((M, N), dy.dtype, dy.device, stream)
+        dz = _new(dy, (M, N), dy.dtype, stream)
     lddz = 0 if dz is None else _rows("dz", dz, dy.shape, dy.dtype)
-    ws = None
     if dbias is None and return_dbias:
-        dbias = _new((N,), torch.float32, dy.device, stream)
-    _vector("dbias", dbias, N, (torch.float32,))
-    lib = load()
-    ws_bytes = 0
+        dbias = _new(dy, N, torch.float32, stream)
+    ws, ws_bytes = None, 0
     if dbias is not None:
-        ws_bytes = lib.fp8_act_grad_workspace(M, N)
-        if ws_bytes < 0:
-            _check(int(ws_bytes))
-        ws = _new((ws_bytes,), torch.uint8, dy.device, stream)
-    _check(lib.fp8_act_grad(_ptr(dy), lddy, _ptr(z), ldz, _ROW[dy.dtype], int(activation), _ptr(dz), lddz, _ptr(dbias),
-                            M, N, _ptr(ws), ws_bytes, _stream_handle(stream)))
+        _vector("dbias", dbias, N, (torch.float32,))
+        ws_bytes = _workspace_bytes("fp8_act_grad_workspace", dy.get_device(), M, N)
+        ws = _new(dy, ws_bytes, torch.uint8, stream)
+    _check(load().fp8_act_grad(_ptr(dy), lddy, _ptr(z), ldz, _ROW[dy.dtype], int(activation), _ptr(dz), lddz,
+                               _ptr(dbias), M, N, _ptr(ws), ws_bytes, _stream_handle(stream)))
     return dz, dbias
 
 
@@ -596,24 +609,28 @@ def fp8_layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, y=None, y_dtype=
     R, C = x.shape
     if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
         raise ValueError("gamma and beta must have one dtype")
-    _vector("gamma", gamma, C, tuple(_ROW))
-    _vector("beta", beta, C, tuple(_ROW))
+    _vector("gamma", gamma, C, _ROW)
+    _vector("beta", beta, C, _ROW)
     params = gamma if gamma is not None else beta
-    if y is None and return_y:
-        y = _new((R, C), y_dtype or x.dtype, x.device, stream)
-    ldy = 0 if y is None else _rows("y", y, (R, C), y_dtype)
-    stats = _new((2, R), torch.float32, x.device, stream)
+    if y is None:
+        y_ld = C
+        if return_y:
+            y = _new(x, (R, C), y_dtype or x.dtype, stream)
+    else:
+        y_ld = _rows("y", y, x.shape, y_dtype)
+    mean = _new(x, R, torch.float32, stream)
+    rstd = _new(x, R, torch.float32, stream)
     q = q_scale = None
     if q_dtype is not None:
         if q_dtype not in _FP8:
             raise ValueError("q_dtype must be torch.float8_e4m3fn or torch.float8_e5m2")
-        q = _new((R, C), q_dtype, x.device, stream)
-        q_scale = _new((R,), torch.float32, x.device, stream)
+        q = _new(x, (R, C), q_dtype, stream)
+        q_scale = _new(x, R, torch.float32, stream)
     _check(load().fp8_layer_norm(_ptr(x), _ROW[x.dtype], ldx, _ptr(gamma), _ptr(beta),
-                                 OUT_F32 if params is None else _ROW[params.dtype], float(eps), _ptr(y),
-                                 OUT_F32 if y is None else _ROW[y.dtype], ldy, _ptr(stats[0]), _ptr(stats[1]),
-                                 _ptr(q), _FP8.get(q_dtype, 0), _ptr(q_scale), R, C, _stream_handle(stream)))
-    return (y, stats[0], stats[1]) if q is None else (y, stats[0], stats[1], q, q_scale)
+                                 OUT_F32 if params is None else _ROW[params.dtype], eps, _ptr(y),
+                                 OUT_F32 if y is None else _ROW[y.dtype], y_ld, _ptr(mean), _ptr(rstd), _ptr(q),
+                                 _FP8.get(q_dtype, 0), _ptr(q_scale), R, C, _stream_handle(stream)))
+    return (y, mean, rstd) if q is None else (y, mean, rstd, q, q_scale)
 
 
 def fp8_layer_norm_grad(dy, x, gamma, mean, rstd, residual_grad=None, dx=None, stream=None,
@@ -628,27 +645,25 @@ def fp8_layer_norm_grad(dy, x, gamma, mean, rstd, residual_grad=None, dx=None, s
     lddy = _rows("dy", dy)
     ldx = _rows("x", x, dy.shape)
     R, C = x.shape
-    _vector("gamma", gamma, C, tuple(_ROW))
+    _vector("gamma", gamma, C, _ROW)
     _vector("mean", mean, R, (torch.float32,))
     _vector("rstd", rstd, R, (torch.float32,))
     lddres = 0 if residual_grad is None else _rows("residual_grad", residual_grad, x.shape, x.dtype)
     if dx is None:
-        dx = _new((R, C), x.dtype, x.device, stream)
-    lddx = _rows("dx", dx, x.shape, x.dtype)
-    lib = load()
+        dx, lddx = _new(x, (R, C), x.dtype, stream), C
+    else:
+        lddx = _rows("dx", dx, x.shape, x.dtype)
     dgamma = dbeta = ws = None
     ws_bytes = 0
     if return_params:
-        ws_bytes = lib.fp8_layer_norm_grad_workspace(R, C)
-        if ws_bytes < 0:
-            _check(int(ws_bytes))
-        dgamma = _new((C,), torch.float32, x.device, stream)
-        dbeta = _new((C,), torch.float32, x.device, stream)
-        ws = _new((ws_bytes,), torch.uint8, x.device, stream)
-    _check(lib.fp8_layer_norm_grad(_ptr(dy), _ROW[dy.dtype], lddy, _ptr(x), _ROW[x.dtype], ldx, _ptr(gamma),
-                                   OUT_F32 if gamma is None else _ROW[gamma.dtype], _ptr(mean), _ptr(rstd),
-                                   _ptr(residual_grad), lddres, _ptr(dx), lddx, _ptr(dgamma), _ptr(dbeta), R, C,
-                                   _ptr(ws), ws_bytes, _stream_handle(stream)))
+        ws_bytes = _workspace_bytes("fp8_layer_norm_grad_workspace", x.get_device(), R, C)
+        dgamma = _new(x, C, torch.float32, stream)
+        dbeta = _new(x, C, torch.float32, stream)
+        ws = _new(x, ws_bytes, torch.uint8, stream)
+    _check(load().fp8_layer_norm_grad(_ptr(dy), _ROW[dy.dtype], lddy, _ptr(x), _ROW[x.dtype], ldx, _ptr(gamma),
+                                      OUT_F32 if gamma is None else _ROW[gamma.dtype], _ptr(mean), _ptr(rstd),
+                                      _ptr(residual_grad), lddres, _ptr(dx), lddx, _ptr(dgamma), _ptr(dbeta), R, C,
+                                      _ptr(ws), ws_bytes, _stream_handle(stream)))
     return dx, dgamma, dbeta
 
 
