@@ -63,4 +63,27 @@ int launch_pdl(Kern kern, int grid, int threads, int smem, cudaStream_t stream, 
     return FP8MM_OK;
 }
 
+// The same with the grid in clusters of `cluster` CTAs.
+template <typename Kern, typename... Args>
+int launch_clusters(Kern kern, int grid, int cluster, int threads, cudaStream_t stream, const char *what, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e != cudaSuccess)
+        return cuda_fail(e, what);
+    return FP8MM_OK;
+}
+
 }  // namespace fp8mm_host

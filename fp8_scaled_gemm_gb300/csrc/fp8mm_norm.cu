@@ -7,39 +7,60 @@ namespace {
 using namespace fp8mm_host;
 using fp8norm::NormParams;
 
-template <int ES, int G, int LANES, int WARPS, int CH>
-int launch_rows(const NormParams &p, int sms, cudaStream_t stream)
+template <int ES, int G, int KIND, int CH, bool MANY>
+int launch_norm(const NormParams &p, int64_t grid, int threads, cudaStream_t stream)
 {
-    constexpr int threads = fp8norm::kCtaThreads<LANES, WARPS>;
-    constexpr int teams = threads / (LANES * WARPS);
-    const int grid = static_cast<int>(std::min<int64_t>(cdiv(p.R, teams), static_cast<int64_t>(sms) * 64));
-    return launch_pdl(fp8norm::norm_rows_kernel<ES, G, LANES, WARPS, CH>, grid, threads, 0, stream,
-                      "layer norm launch", p);
+    auto kern = fp8norm::norm_kernel<ES, G, KIND, CH, MANY>;
+    constexpr int per_thread = 2 * 2 * CH * 16;             // gamma's and beta's float4s
+    static bool attr_set[kMaxDevices] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!attr_set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (MANY ? 1024 : 256) * per_thread);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "cudaFuncSetAttribute");
+        attr_set[dev] = true;
+    }
+    return launch_pdl(kern, static_cast<int>(grid), threads, threads * per_thread, stream, "layer norm launch", p);
 }
 
-// The smallest team that holds a row of g groups in registers.
+// Teams of LANES lanes of a warp.
+template <int ES, int G, int LANES, int CH>
+int launch_lanes(const NormParams &p, int sms, cudaStream_t stream)
+{
+    return launch_norm<ES, G, LANES, CH, false>(
+        p, std::min<int64_t>(cdiv(p.R, 256 / LANES), static_cast<int64_t>(sms) * (CH == 4 ? 3 : 4)), 256, stream);
+}
+
+// A CTA per row, as many of them on an SM as threads fit: 768 or 1024.
+template <int ES, int G, int CH, bool MANY>
+int launch_cta(const NormParams &p, int sms, cudaStream_t stream)
+{
+    const int threads = static_cast<int>(cdiv(p.C, 32 * 8 * CH)) * 32;
+    return launch_norm<ES, G, fp8norm::kCta, CH, MANY>(
+        p, std::min<int64_t>(p.R, static_cast<int64_t>(sms) * ((MANY ? 1024 : 768) / threads)), threads, stream);
+}
+
 template <int ES>
 int launch(const NormParams &p, bool vec, int sms, cudaStream_t stream)
 {
-    const int64_t g = p.groups;
+    const int64_t C = p.C;
     if (vec) {
-        if (g <= 4) return launch_rows<ES, 8, 4, 1, 1>(p, sms, stream);
-        if (g <= 8) return launch_rows<ES, 8, 8, 1, 1>(p, sms, stream);
-        if (g <= 16) return launch_rows<ES, 8, 16, 1, 1>(p, sms, stream);
-        if (g <= 32) return launch_rows<ES, 8, 32, 1, 1>(p, sms, stream);
-        if (g <= 64) return launch_rows<ES, 8, 32, 1, 2>(p, sms, stream);
-        if (g <= 128) return launch_rows<ES, 8, 32, 1, 4>(p, sms, stream);
-        if (g <= 256) return launch_rows<ES, 8, 32, 2, 4>(p, sms, stream);
-        if (g <= 512) return launch_rows<ES, 8, 32, 4, 4>(p, sms, stream);
-        if (g <= 1024) return launch_rows<ES, 8, 32, 8, 4>(p, sms, stream);
-        if (g <= 2048) return launch_rows<ES, 8, 32, 16, 4>(p, sms, stream);
-        if (g <= 4096) return launch_rows<ES, 8, 32, 32, 4>(p, sms, stream);
+        if (C <= 32) return launch_lanes<ES, 8, 4, 1>(p, sms, stream);
+        if (C <= 64) return launch_lanes<ES, 8, 8, 1>(p, sms, stream);
+        if (C <= 128) return launch_lanes<ES, 8, 16, 1>(p, sms, stream);
+        if (C <= 256) return launch_lanes<ES, 8, 32, 1>(p, sms, stream);
+        if (C <= 512) return launch_lanes<ES, 8, 32, 2>(p, sms, stream);
+        if constexpr (ES == 2) {
+            if (C <= 1024) return launch_lanes<2, 8, 32, 4>(p, sms, stream);
+            if (C <= 8192) return launch_cta<2, 8, 4, false>(p, sms, stream);
+        }
+        if (C <= 16384) return launch_cta<ES, 8, 2, true>(p, sms, stream);
     } else {
-        if (g <= 256) return launch_rows<ES, 1, 32, 1, 8>(p, sms, stream);
-        if (g <= 1024) return launch_rows<ES, 1, 32, 4, 8>(p, sms, stream);
-        if (g <= 4096) return launch_rows<ES, 1, 32, 8, 16>(p, sms, stream);
-        if (g <= 8192) return launch_rows<ES, 1, 32, 16, 16>(p, sms, stream);
-        if (g <= 16384) return launch_rows<ES, 1, 32, 32, 16>(p, sms, stream);
+        if (C <= 256) return launch_lanes<ES, 1, 32, 1>(p, sms, stream);
+        if (C <= 512) return launch_lanes<ES, 1, 32, 2>(p, sms, stream);
+        if (C <= 16384) return launch_cta<ES, 1, 2, true>(p, sms, stream);
     }
     const int grid = static_cast<int>(std::min<int64_t>(p.R, static_cast<int64_t>(sms) * 8));
     if (vec)

@@ -12,11 +12,24 @@
 //   dx = rstd (w - sum w / C - xhat sum(w xhat) / C) [+ dres]
 //   dgamma = sum over rows of dy xhat,  dbeta = sum over rows of dy
 //
-// Both are bound by HBM. A team of LANES x WARPS threads holds a row: thread
-// t the element groups t, t + T, ... (T threads), so that every element is
-// read once. Rows whose starts are 16-byte aligned take groups of 8
-// elements, others single elements. Rows too long for a team go through
-// the long kernels, which read the row again from L2 for each pass.
+// Both are bound by HBM, if the instructions and the waits between a row's
+// reductions are kept out of the way:
+//  - A team of threads takes a row and goes on to other rows with the same
+//    columns, E = 8 CH per thread, so that backward's column sums stay in
+//    registers and the next row's loads are issued before the present row's
+//    reductions. A team is 4 to 32 lanes of a warp, some warps of a CTA, or
+//    (backward, wide rows) the CTAs of a cluster, each with a slice of the
+//    columns, that exchange their sums through distributed shared memory.
+//  - E is as large as the registers allow: a reduction costs a warp about 30
+//    instructions whatever E is (with E = 8, 43 instructions per element ran
+//    the forward pass at 47 % of HBM; with 32 it is about 12).
+//  - Arithmetic goes two columns at a time (f32x2).
+//  - Every warp covers 32 E neighbouring columns, so a thread's addresses
+//    differ by constants. Rows that start on 16 bytes take 16-byte loads of
+//    8 elements; other rows take single elements, neighbouring lanes
+//    neighbouring ones.
+// Rows too long for a team go through the long kernels, which read the row
+// again from L2 for each pass.
 #pragma once
 
 #include "fp8mm_act.cuh"
@@ -26,6 +39,400 @@
 namespace fp8norm {
 
 using namespace fp8rows;
+
+// ------------------------------------------------------------------ teams ---
+
+constexpr int kMaxCluster = 8;       // CTAs that share a row (backward)
+
+// Kinds of team: LANES 4 .. 32 lanes of a warp; kCta some warps of a CTA with
+// a named barrier of their own; kCluster all threads of a cluster's CTAs.
+constexpr int kCta = 0, kCluster = -1;
+
+// A thread's columns: E = 8 CH of them from c0 on. G = 8: groups of 8
+// neighbours, 8 x (lanes) apart; G = 1: single columns 32 apart. `left`
+// columns lie between c0 and the end of the row (of the CTA's slice).
+template <int G, int KIND, int CH>
+struct Place {
+    static constexpr int E = 8 * CH;
+    static constexpr int kLanes = KIND > 0 ? KIND : 32;
+    static constexpr int kStep = G == 8 ? 8 * kLanes : kLanes;   // between a thread's groups
+    long long c0;
+    int left;
+
+    __device__ __forceinline__ Place(long long begin, long long end, int t)
+    {
+        c0 = begin + static_cast<long long>(t / kLanes) * (kLanes * E) + (t % kLanes) * G;
+        left = static_cast<int>(max(0ll, min(end - c0, 1ll << 30)));
+    }
+    // whether the thread's group k (of E / G) lies inside
+    __device__ __forceinline__ bool in(int k) const { return k * kStep < left; }
+};
+
+template <int ES, int G, int CH>
+struct RawE {
+    Raw<ES, G> r[8 * CH / G];
+};
+
+// The thread's elements of the row at `p` (its first element).
+template <int ES, int G, int KIND, int CH>
+__device__ __forceinline__ void load_e(RawE<ES, G, CH> &r, const uint8_t *p, const Place<G, KIND, CH> &pl)
+{
+    constexpr int N = 8 * CH / G;
+    constexpr int step = Place<G, KIND, CH>::kStep;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        if (pl.in(k))
+            load_raw<ES, G>(r.r[k], p, k * step);
+        else
+            clear_raw<ES, G>(r.r[k]);
+    }
+}
+
+template <int ES, int G, int CH>
+__device__ __forceinline__ void clear_e(RawE<ES, G, CH> &r)
+{
+#pragma unroll
+    for (int k = 0; k < 8 * CH / G; ++k)
+        clear_raw<ES, G>(r.r[k]);
+}
+
+// As fp32 pairs.
+template <int ES, int G, int CH>
+__device__ __forceinline__ void to_pairs(const RawE<ES, G, CH> &r, bool f16, uint64_t (&v)[4 * CH])
+{
+    if constexpr (ES == 2) {
+        // one branch for all elements
+        if (f16) {
+#pragma unroll
+            for (int i = 0; i < 4 * CH; ++i) {
+                float lo, hi;
+                if constexpr (G == 8) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r.r[i / 4].w[i % 4]));
+                    lo = f.x;
+                    hi = f.y;
+                } else {
+                    lo = half_bits(r.r[2 * i].w[0], true);
+                    hi = half_bits(r.r[2 * i + 1].w[0], true);
+                }
+                v[i] = ptx::f32x2(lo, hi);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4 * CH; ++i) {
+                if constexpr (G == 8)
+                    v[i] = ptx::f32x2(__uint_as_float(r.r[i / 4].w[i % 4] << 16),
+                                      __uint_as_float(r.r[i / 4].w[i % 4] & 0xFFFF0000u));
+                else
+                    v[i] = ptx::f32x2(__uint_as_float(r.r[2 * i].w[0] << 16), __uint_as_float(r.r[2 * i + 1].w[0] << 16));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4 * CH; ++i) {
+            if constexpr (G == 8)
+                v[i] = ptx::f32x2(__uint_as_float(r.r[i / 4].w[2 * (i % 4)]), __uint_as_float(r.r[i / 4].w[2 * (i % 4) + 1]));
+            else
+                v[i] = ptx::f32x2(__uint_as_float(r.r[2 * i].w[0]), __uint_as_float(r.r[2 * i + 1].w[0]));
+        }
+    }
+}
+
+// Pairs to memory in `type`, one rounding; p: the thread's first element.
+template <int G, int KIND, int CH>
+__device__ __forceinline__ void store_e(uint8_t *p, int type, const Place<G, KIND, CH> &pl, const uint64_t (&v)[4 * CH])
+{
+    constexpr int step = Place<G, KIND, CH>::kStep;
+    if (type == kF32) {
+        float *o = reinterpret_cast<float *>(p);
+#pragma unroll
+        for (int i = 0; i < 4 * CH; ++i) {
+            if constexpr (G == 8) {
+                if (i % 2 == 0 && pl.in(i / 4)) {
+                    float a, b, c, d;
+                    ptx::unpack_f32x2(v[i], a, b);
+                    ptx::unpack_f32x2(v[i + 1], c, d);
+                    *reinterpret_cast<float4 *>(o + (i / 4) * step + 2 * (i % 4)) = make_float4(a, b, c, d);
+                }
+            } else {
+                float a, b;
+                ptx::unpack_f32x2(v[i], a, b);
+                if (pl.in(2 * i))
+                    o[2 * i * step] = a;
+                if (pl.in(2 * i + 1))
+                    o[(2 * i + 1) * step] = b;
+            }
+        }
+        return;
+    }
+    uint32_t w[4 * CH];
+    if (type == kF16) {
+#pragma unroll
+        for (int i = 0; i < 4 * CH; ++i)
+            w[i] = ptx::cvt_16x2<true>(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4 * CH; ++i)
+            w[i] = ptx::cvt_16x2<false>(v[i]);
+    }
+    unsigned short *o = reinterpret_cast<unsigned short *>(p);
+    if constexpr (G == 8) {
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+            if (pl.in(k))
+                *reinterpret_cast<uint4 *>(o + k * step) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4 * CH; ++i) {
+            if (pl.in(2 * i))
+                o[2 * i * step] = static_cast<unsigned short>(w[i] & 0xFFFFu);
+            if (pl.in(2 * i + 1))
+                o[(2 * i + 1) * step] = static_cast<unsigned short>(w[i] >> 16);
+        }
+    }
+}
+
+// The thread's parameters; `fill` without a vector, 0 outside the row.
+template <int G, int KIND, int CH>
+__device__ __forceinline__ void param_e(const void *base, int type, const Place<G, KIND, CH> &pl, float fill,
+                                        uint64_t (&v)[4 * CH])
+{
+    constexpr int step = Place<G, KIND, CH>::kStep;
+    if (base == nullptr) {
+#pragma unroll
+        for (int i = 0; i < 4 * CH; ++i)
+            v[i] = ptx::f32x2(fill, fill);
+    } else if (type == kF32) {
+        const float *p = static_cast<const float *>(base) + pl.c0;
+#pragma unroll
+        for (int i = 0; i < 4 * CH; ++i) {
+            if constexpr (G == 8) {
+                if (i % 2 == 0) {
+                    const float4 f = pl.in(i / 4) ? __ldg(reinterpret_cast<const float4 *>(p + (i / 4) * step + 2 * (i % 4)))
+                                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    v[i] = ptx::f32x2(f.x, f.y);
+                    v[i + 1] = ptx::f32x2(f.z, f.w);
+                }
+            } else {
+                v[i] = ptx::f32x2(pl.in(2 * i) ? __ldg(p + 2 * i * step) : 0.0f,
+                                  pl.in(2 * i + 1) ? __ldg(p + (2 * i + 1) * step) : 0.0f);
+            }
+        }
+    } else {
+        RawE<2, G, CH> r;
+        load_e<2, G, KIND, CH>(r, static_cast<const uint8_t *>(base) + pl.c0 * 2, pl);
+        to_pairs<2, G, CH>(r, type == kF16, v);
+    }
+}
+
+// A thread's own copy of its parameters in shared memory, fp32: float4 j of
+// it at slots[j * threads of the CTA], so that a warp's accesses are free of
+// bank conflicts. Only the thread that wrote it reads it: no barrier.
+template <int CH>
+__device__ __forceinline__ void keep_params(float4 *slots, int threads, const uint64_t (&v)[4 * CH])
+{
+#pragma unroll
+    for (int j = 0; j < 2 * CH; ++j) {
+        float4 f;
+        ptx::unpack_f32x2(v[2 * j], f.x, f.y);
+        ptx::unpack_f32x2(v[2 * j + 1], f.z, f.w);
+        slots[j * threads] = f;
+    }
+}
+
+// v with the columns outside the row set to 0.
+template <int G, int KIND, int CH>
+__device__ __forceinline__ void mask_e(uint64_t (&v)[4 * CH], const Place<G, KIND, CH> &pl)
+{
+#pragma unroll
+    for (int i = 0; i < 4 * CH; ++i) {
+        if constexpr (G == 8) {
+            v[i] = pl.in(i / 4) ? v[i] : 0ull;
+        } else {
+            float a, b;
+            ptx::unpack_f32x2(v[i], a, b);
+            v[i] = ptx::f32x2(pl.in(2 * i) ? a : 0.0f, pl.in(2 * i + 1) ? b : 0.0f);
+        }
+    }
+}
+
+template <int N>
+__device__ __forceinline__ float sum_pairs(const uint64_t (&v)[N])
+{
+    uint64_t s0 = v[0], s1 = v[1];
+#pragma unroll
+    for (int i = 2; i < N; i += 2) {
+        s0 = ptx::add_f32x2(s0, v[i]);
+        s1 = ptx::add_f32x2(s1, v[i + 1]);
+    }
+    s0 = ptx::add_f32x2(s0, s1);
+    float lo, hi;
+    ptx::unpack_f32x2(s0, lo, hi);
+    return lo + hi;
+}
+
+struct Team {
+    int T, warps;        // threads and warps of the team in this CTA
+    int id;              // team within the CTA: barrier id + 1 of it
+    int warp0;           // its first warp
+    uint32_t rank, ctas; // place in the cluster
+};
+
+template <int KIND>
+__device__ __forceinline__ void team_barrier(const Team &tm)
+{
+    if constexpr (KIND == kCluster)
+        ptx::cluster_sync();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(tm.id + 1), "r"(tm.T) : "memory");
+}
+
+// Words of one reduction's exchange buffer for NV values.
+template <int KIND, int NV>
+constexpr int kRedWords = KIND == kCluster ? kMaxCluster * 32 * NV : 32 * NV;
+
+// Sums of NV values over the team, the same bits in every thread. The caller
+// alternates between buffers so that two barriers lie between uses of one.
+template <int KIND, int NV>
+__device__ __forceinline__ void team_sum8(float (&v)[NV], const Team &tm, float *red)
+{
+    constexpr int L = KIND > 0 ? KIND : 32;
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o, L);
+    if constexpr (KIND <= 0) {
+        const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
+        int n = tm.warps;
+        const float *mine = red;
+        if constexpr (KIND == kCluster) {
+            // lane r hands the warp's sums to CTA r
+            if (lane < static_cast<int>(tm.ctas)) {
+                const uint32_t at = ptx::mapa_shared(
+                    ptx::smem_addr(red + (tm.rank * tm.warps + warp) * NV), static_cast<uint32_t>(lane));
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    ptx::st_shared_cluster_f32(at + 4 * i, v[i]);
+            }
+            n *= static_cast<int>(tm.ctas);
+        } else {
+            mine = red + tm.warp0 * NV;
+            if (lane == 0) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    red[warp * NV + i] = v[i];
+            }
+        }
+        team_barrier<KIND>(tm);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            v[i] = 0.0f;
+        for (int e = lane; e < n; e += 32)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                v[i] += mine[e * NV + i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+    }
+}
+
+// Largest of NV magnitudes over the team, on their bit patterns: unsigned
+// order is the order of |v| with NaN above infinity.
+template <int KIND, int NV>
+__device__ __forceinline__ void team_amax8(float (&v)[NV], const Team &tm, float *red)
+{
+    uint32_t u[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        u[i] = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+    if constexpr (KIND > 0 && KIND < 32) {
+#pragma unroll
+        for (int o = KIND / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                u[i] = max(u[i], __shfl_xor_sync(0xFFFFFFFFu, u[i], o, KIND));
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            u[i] = __reduce_max_sync(0xFFFFFFFFu, u[i]);
+    }
+    if constexpr (KIND <= 0) {
+        const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
+        int n = tm.warps;
+        const float *mine = red;
+        if constexpr (KIND == kCluster) {
+            if (lane < static_cast<int>(tm.ctas)) {
+                const uint32_t at = ptx::mapa_shared(
+                    ptx::smem_addr(red + (tm.rank * tm.warps + warp) * NV), static_cast<uint32_t>(lane));
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    ptx::st_shared_cluster_f32(at + 4 * i, __uint_as_float(u[i]));
+            }
+            n *= static_cast<int>(tm.ctas);
+        } else {
+            mine = red + tm.warp0 * NV;
+            if (lane == 0) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    red[warp * NV + i] = __uint_as_float(u[i]);
+            }
+        }
+        team_barrier<KIND>(tm);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            u[i] = 0;
+        for (int e = lane; e < n; e += 32)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                u[i] = max(u[i], __float_as_uint(mine[e * NV + i]));
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            u[i] = __reduce_max_sync(0xFFFFFFFFu, u[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        v[i] = __uint_as_float(u[i]);
+}
+
+// The team this thread belongs to, and which of all teams it is.
+template <int KIND>
+__device__ __forceinline__ Team this_team(int team_threads, int &t, long long &first, long long &stride)
+{
+    Team tm{};
+    if constexpr (KIND > 0) {
+        tm.T = KIND;
+        tm.warps = 1;
+        const int per_cta = static_cast<int>(blockDim.x) / KIND;
+        tm.id = static_cast<int>(threadIdx.x) / KIND;
+        t = static_cast<int>(threadIdx.x) % KIND;
+        first = static_cast<long long>(blockIdx.x) * per_cta + tm.id;
+        stride = static_cast<long long>(gridDim.x) * per_cta;
+    } else if constexpr (KIND == kCta) {
+        tm.T = team_threads;
+        tm.warps = team_threads >> 5;
+        const int per_cta = static_cast<int>(blockDim.x) / team_threads;
+        tm.id = static_cast<int>(threadIdx.x) / team_threads;
+        tm.warp0 = tm.id * tm.warps;
+        t = static_cast<int>(threadIdx.x) % team_threads;
+        first = static_cast<long long>(blockIdx.x) * per_cta + tm.id;
+        stride = static_cast<long long>(gridDim.x) * per_cta;
+    } else {
+        tm.T = static_cast<int>(blockDim.x);
+        tm.warps = tm.T >> 5;
+        tm.rank = ptx::cluster_ctarank();
+        asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(tm.ctas));
+        t = static_cast<int>(threadIdx.x);
+        first = blockIdx.x / tm.ctas;
+        stride = gridDim.x / tm.ctas;
+        ptx::cluster_sync();             // no remote store before every CTA runs
+    }
+    return tm;
+}
+
+// ---------------------------------------------------------------- forward ---
 
 struct NormParams {
     const void *x;
@@ -41,7 +448,8 @@ struct NormParams {
     uint8_t *q;                // fp8 codes [R, C], or nullptr
     int q_type;
     float *q_scale;
-    long long R, C, groups;
+    long long R, C;
+    long long groups;          // long kernel: element groups per row
 };
 
 // The fp8 codes of G values of a row, C ABI semantics of fp8_quantize.
@@ -62,92 +470,154 @@ __device__ __forceinline__ void store_codes(uint8_t *dst, const fp8q::Divider &d
     }
 }
 
-// Threads of a CTA of such teams.
-template <int LANES, int WARPS>
-constexpr int kCtaThreads = LANES * WARPS > 256 ? LANES * WARPS : 256;
-
-template <int ES, int G, int LANES, int WARPS, int CH>
-__global__ void __launch_bounds__(kCtaThreads<LANES, WARPS>) norm_rows_kernel(const NormParams p)
+// The codes of the thread's values: with a scale in the normal range by its
+// reciprocal (the unrounded y is off by more than that product's rounding),
+// else by division, as fp8_quantize does.
+template <int G, int KIND, int CH>
+__device__ __forceinline__ void store_codes_e(uint8_t *p, const Place<G, KIND, CH> &pl, float scale,
+                                              const uint64_t (&v)[4 * CH], int q_type)
 {
-    constexpr int T = LANES * WARPS;
-    constexpr int kTeams = kCtaThreads<LANES, WARPS> / T;
-    __shared__ float red[3][32];
+    constexpr int step = Place<G, KIND, CH>::kStep;
+    uint32_t c[4 * CH];                  // two codes each
+    if (scale >= 0x1p-80f && scale < 0x1p100f) {
+        const float r = fp8mm::rcp_approx(scale);
+        const uint64_t r2 = ptx::f32x2(r, r);
+        if (q_type == 0) {
+#pragma unroll
+            for (int i = 0; i < 4 * CH; ++i) {
+                float a, b;
+                ptx::unpack_f32x2(ptx::mul_f32x2(v[i], r2), a, b);
+                c[i] = fp8q::cvt_pair(a, b, 0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4 * CH; ++i) {
+                float a, b;
+                ptx::unpack_f32x2(ptx::mul_f32x2(v[i], r2), a, b);
+                c[i] = fp8q::cvt_pair(a, b, 1);
+            }
+        }
+    } else {
+        const fp8q::Divider d = fp8q::make_divider(scale);
+#pragma unroll
+        for (int i = 0; i < 4 * CH; ++i) {
+            float a, b;
+            ptx::unpack_f32x2(v[i], a, b);
+            c[i] = fp8q::cvt_pair(fp8q::div_slow(d, a), fp8q::div_slow(d, b), q_type);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * CH; ++i) {
+        if constexpr (G == 8) {
+            if (i % 4 == 0 && pl.in(i / 4))
+                *reinterpret_cast<uint2 *>(p + (i / 4) * step) =
+                    make_uint2(c[i] | (c[i + 1] << 16), c[i + 2] | (c[i + 3] << 16));
+        } else {
+            if (pl.in(2 * i))
+                p[2 * i * step] = static_cast<uint8_t>(c[i] & 0xFFu);
+            if (pl.in(2 * i + 1))
+                p[(2 * i + 1) * step] = static_cast<uint8_t>(c[i] >> 8);
+        }
+    }
+}
+
+// 16-bit rows in 16-byte groups take CTAs of up to 256 threads of 32 columns,
+// three per SM, which hide each other's barriers. The others (fp32, single
+// elements: more registers per column as loaded) and wider rows take 16
+// columns and up to 1024 threads (MANY). The CTA's dynamic shared memory holds
+// gamma and beta (keep_params).
+template <int ES, int G, int KIND, int CH, bool MANY>
+__global__ void __launch_bounds__(MANY ? 1024 : 256, MANY ? 1 : 3) norm_kernel(const NormParams p)
+{
+    __shared__ float red[3][kRedWords<KIND, 1>];
+    extern __shared__ float4 params[];
     ptx::grid_launch_dependents();
+    int t;
+    long long first, stride;
+    const Team tm = this_team<KIND>(static_cast<int>(blockDim.x), t, first, stride);
+    const Place<G, KIND, CH> pl(0, p.C, t);
+    const int threads = static_cast<int>(blockDim.x);
+    float4 *const my_gamma = params + threadIdx.x, *const my_beta = my_gamma + 2 * CH * threads;
     ptx::grid_dependency_wait();
 
-    const int team = static_cast<int>(threadIdx.x) / T;
-    const int t = static_cast<int>(threadIdx.x) % T;
-    const float c_f = static_cast<float>(p.C);
-    for (long long base = static_cast<long long>(blockIdx.x) * kTeams; base < p.R;
-         base += static_cast<long long>(gridDim.x) * kTeams) {
-        const long long row = base + team;
+    const float inv_c = 1.0f / static_cast<float>(p.C);
+    const uint8_t *x = static_cast<const uint8_t *>(p.x) + (first * p.ldx + pl.c0) * ES;
+    const long long x_step = stride * p.ldx * ES;
+    RawE<ES, G, CH> raw;
+    clear_e<ES, G, CH>(raw);
+    if (first < p.R)
+        load_e<ES, G, KIND, CH>(raw, x, pl);
+    {
+        uint64_t v[4 * CH];
+        param_e<G, KIND, CH>(p.gamma, p.param_type, pl, 1.0f, v);
+        keep_params<CH>(my_gamma, threads, v);
+        param_e<G, KIND, CH>(p.beta, p.param_type, pl, 0.0f, v);
+        keep_params<CH>(my_beta, threads, v);
+    }
+
+    // every thread of a CTA makes the same number of turns
+    const long long first0 = KIND > 0 ? first - tm.id : first;
+    for (long long turn = 0; first0 + turn * stride < p.R; ++turn) {
+        const long long row = first + turn * stride;
+        uint64_t v[4 * CH];
+        to_pairs<ES, G, CH>(raw, p.x_f16, v);
+        x += x_step;
+        if (row + stride < p.R)
+            load_e<ES, G, KIND, CH>(raw, x, pl);
+        float s[1] = {sum_pairs(v)};
+        team_sum8<KIND, 1>(s, tm, red[0]);
+        const float mean = s[0] * inv_c;
+        const uint64_t m2 = ptx::f32x2(-mean, -mean);
+#pragma unroll
+        for (int i = 0; i < 4 * CH; ++i)
+            v[i] = ptx::add_f32x2(v[i], m2);
+        if (!pl.in(8 * CH / G - 1))
+            mask_e<G, KIND, CH>(v, pl);
+        uint64_t q0 = 0, q1 = 0;
+#pragma unroll
+        for (int i = 0; i < 4 * CH; i += 2) {
+            q0 = ptx::fma_f32x2(v[i], v[i], q0);
+            q1 = ptx::fma_f32x2(v[i + 1], v[i + 1], q1);
+        }
+        const uint64_t q2[2] = {q0, q1};
+        s[0] = sum_pairs(q2);
+        team_sum8<KIND, 1>(s, tm, red[1]);
+        const float rstd = rsqrtf(fmaf(s[0], inv_c, p.eps));
+        const uint64_t r2 = ptx::f32x2(rstd, rstd);
+#pragma unroll
+        for (int j = 0; j < 2 * CH; ++j) {
+            const float4 ga = my_gamma[j * threads], be = my_beta[j * threads];
+            v[2 * j] = ptx::fma_f32x2(ptx::mul_f32x2(v[2 * j], r2), ptx::f32x2(ga.x, ga.y), ptx::f32x2(be.x, be.y));
+            v[2 * j + 1] =
+                ptx::fma_f32x2(ptx::mul_f32x2(v[2 * j + 1], r2), ptx::f32x2(ga.z, ga.w), ptx::f32x2(be.z, be.w));
+        }
         const bool valid = row < p.R;
-        Raw<ES, G> raw[CH];
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const long long g = t + c * T;
-            if (valid && g < p.groups)
-                load_raw<ES, G>(raw[c], p.x, row * p.ldx + g * G);
-            else
-                clear_raw<ES, G>(raw[c]);
-        }
-        float v[CH][G];
-        float s[1] = {0.0f};
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            to_float<ES, G>(raw[c], p.x_f16, v[c]);
-#pragma unroll
-            for (int i = 0; i < G; ++i)
-                s[0] += v[c][i];
-        }
-        team_sum<LANES, WARPS, 1>(s, red[0]);
-        const float mean = s[0] / c_f;
-        s[0] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const bool in = t + c * T < p.groups;
-#pragma unroll
-            for (int i = 0; i < G; ++i) {
-                v[c][i] = in ? v[c][i] - mean : 0.0f;
-                s[0] = fmaf(v[c][i], v[c][i], s[0]);
+        if (valid) {
+            if (t == 0) {
+                if (p.mean)
+                    p.mean[row] = mean;
+                if (p.rstd)
+                    p.rstd[row] = rstd;
             }
-        }
-        team_sum<LANES, WARPS, 1>(s, red[1]);
-        const float rstd = 1.0f / sqrtf(s[0] / c_f + p.eps);
-        if (valid && t == 0) {
-            if (p.mean)
-                p.mean[row] = mean;
-            if (p.rstd)
-                p.rstd[row] = rstd;
-        }
-        float amax = 0.0f;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const long long g = t + c * T;
-            if (g < p.groups) {
-                float ga[G], be[G];
-                load_param<G>(p.gamma, p.param_type, g * G, 1.0f, ga);
-                load_param<G>(p.beta, p.param_type, g * G, 0.0f, be);
-#pragma unroll
-                for (int i = 0; i < G; ++i) {
-                    v[c][i] = fmaf(v[c][i] * rstd, ga[i], be[i]);
-                    amax = fp8mm::max_nan(amax, fabsf(v[c][i]));
-                }
-                if (p.y && valid)
-                    store_group<G>(p.y, p.y_type, row * p.ldy + g * G, v[c]);
-            }
+            if (p.y)
+                store_e<G, KIND, CH>(static_cast<uint8_t *>(p.y) + (row * p.ldy + pl.c0) * (p.y_type == kF32 ? 4 : 2),
+                                     p.y_type, pl, v);
         }
         if (p.q) {
-            amax = team_max<LANES, WARPS>(amax, red[2]);
-            const float scale = __fdiv_rn(amax, fp8q::qmax_of(p.q_type));
-            if (valid && t == 0)
-                p.q_scale[row] = scale;
-            const fp8q::Divider d = fp8q::make_divider(scale);
+            float amax[1] = {0.0f};
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const long long g = t + c * T;
-                if (valid && g < p.groups)
-                    store_codes<G>(p.q + row * p.C + g * G, d, v[c], p.q_type);
+            for (int i = 0; i < 4 * CH; ++i) {
+                float a, b;
+                ptx::unpack_f32x2(v[i], a, b);
+                amax[0] = fp8mm::max_nan(amax[0], fabsf(a));
+                amax[0] = fp8mm::max_nan(amax[0], fabsf(b));
+            }
+            team_amax8<KIND, 1>(amax, tm, red[2]);
+            const float scale = amax[0] * (p.q_type == 0 ? 1.0f / 448.0f : 1.0f / 57344.0f);
+            if (valid) {
+                if (t == 0)
+                    p.q_scale[row] = scale;
+                store_codes_e<G, KIND, CH>(p.q + row * p.C + pl.c0, pl, scale, v, p.q_type);
             }
         }
     }
@@ -240,132 +710,187 @@ struct NormGradParams {
     void *dx;                  // nullptr: not wanted
     long long lddx;
     int x_type;
-    float *partial;            // [grid][2][C]: dgamma and dbeta sums of each CTA's rows, or nullptr
-    long long R, C, groups;
+    float *partial;            // [CTAs or clusters][2][C]: dgamma and dbeta sums of their rows, or nullptr
+    long long R, C;
+    long long groups;          // long kernels: element groups per row
+    int team_threads;          // kCta: threads of a team
+    long long slice_cols;      // kCluster: columns of each CTA
 };
 
-// Rows base + team, base + teams x grid + team, ... : each thread keeps the
-// dgamma and dbeta sums of its columns in registers over all its rows; the
-// CTA's teams then add theirs in order through shared memory.
-template <int ES, int DES, int G, int LANES, int WARPS, int CH>
-__global__ void __launch_bounds__(kCtaThreads<LANES, WARPS>) norm_grad_rows_kernel(const NormGradParams p)
+// Columns per thread over 8 (CH) and threads of a CTA: two 16-bit operands in
+// 16-byte groups leave room for 16 columns; rows of up to 256 columns take
+// one group per thread.
+constexpr int kGradThreads = 512;
+template <int ES, int DES, int G, int KIND>
+constexpr int kGradCh = (ES == 2 && DES == 2 && G == 8 && (KIND <= 0 || KIND == 32)) ? 2 : 1;
+
+// Each thread keeps the dgamma and dbeta sums of its columns in registers over
+// all its rows; a CTA's teams then add theirs in order through shared memory.
+template <int ES, int DES, int G, int KIND, int CH>
+__global__ void __launch_bounds__(kGradThreads, 1) norm_grad_kernel(const NormGradParams p)
 {
-    constexpr int T = LANES * WARPS;
-    constexpr int kThreads = kCtaThreads<LANES, WARPS>;
-    constexpr int kTeams = kThreads / T;
-    __shared__ float red[2][64];
-    __shared__ float cols[kTeams > 1 ? kThreads * CH * G : 1];
+    constexpr int P = 4 * CH;
+    __shared__ float red[2][kRedWords<KIND, 2>];
+    // gamma (keep_params); after the rows, the teams' sums meet here
+    __shared__ float4 params[kGradThreads * 2 * CH];
+    float *const cols = reinterpret_cast<float *>(params);
     ptx::grid_launch_dependents();
+    int t;
+    long long first, stride, begin = 0, end = p.C;
+    const Team tm = this_team<KIND>(p.team_threads, t, first, stride);
+    if constexpr (KIND == kCluster) {
+        begin = min(p.C, tm.rank * p.slice_cols);
+        end = min(p.C, begin + p.slice_cols);
+    }
+    const Place<G, KIND, CH> pl(begin, end, t);
     ptx::grid_dependency_wait();
 
-    const int team = static_cast<int>(threadIdx.x) / T;
-    const int t = static_cast<int>(threadIdx.x) % T;
     const float inv_c = 1.0f / static_cast<float>(p.C);
-    float dga[CH][G] = {}, dbe[CH][G] = {};
+    const uint8_t *px = static_cast<const uint8_t *>(p.x) + (first * p.ldx + pl.c0) * ES;
+    const uint8_t *pd = static_cast<const uint8_t *>(p.dy) + (first * p.lddy + pl.c0) * DES;
+    const uint8_t *pr = static_cast<const uint8_t *>(p.dres) + (first * p.lddres + pl.c0) * ES;
+    uint8_t *po = static_cast<uint8_t *>(p.dx) + (first * p.lddx + pl.c0) * ES;
+    const long long x_step = stride * p.ldx * ES, d_step = stride * p.lddy * DES, r_step = stride * p.lddres * ES,
+                    o_step = stride * p.lddx * ES;
+    RawE<ES, G, CH> nx;
+    RawE<DES, G, CH> nd;
+    clear_e<ES, G, CH>(nx);
+    clear_e<DES, G, CH>(nd);
+    float nmean = 0.0f, nrstd = 0.0f;
+    if (first < p.R) {
+        load_e<ES, G, KIND, CH>(nx, px, pl);
+        load_e<DES, G, KIND, CH>(nd, pd, pl);
+        nmean = __ldg(p.mean + first);
+        nrstd = __ldg(p.rstd + first);
+    }
+    uint64_t dga[P] = {}, dbe[P] = {};
+    const int threads = static_cast<int>(blockDim.x);
+    float4 *const my_gamma = params + threadIdx.x;
+    {
+        uint64_t ga[P];
+        param_e<G, KIND, CH>(p.gamma, p.param_type, pl, 1.0f, ga);
+        keep_params<CH>(my_gamma, threads, ga);
+    }
+
     int flip = 0;
-    for (long long base = static_cast<long long>(blockIdx.x) * kTeams; base < p.R;
-         base += static_cast<long long>(gridDim.x) * kTeams) {
-        const long long row = base + team;
+    const long long first0 = KIND > 0 ? first - tm.id : first;
+    for (long long turn = 0; first0 + turn * stride < p.R; ++turn) {
+        const long long row = first + turn * stride;
         const bool valid = row < p.R;
-        Raw<ES, G> rx[CH];
-        Raw<DES, G> rd[CH];
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const long long g = t + c * T;
-            if (valid && g < p.groups) {
-                load_raw<ES, G>(rx[c], p.x, row * p.ldx + g * G);
-                load_raw<DES, G>(rd[c], p.dy, row * p.lddy + g * G);
-            } else {
-                clear_raw<ES, G>(rx[c]);
-                clear_raw<DES, G>(rd[c]);
-            }
+        RawE<ES, G, CH> rr;
+        if (valid && p.dres)
+            load_e<ES, G, KIND, CH>(rr, pr, pl);
+        else
+            clear_e<ES, G, CH>(rr);
+        const float mean = nmean, rstd = nrstd;
+        const uint64_t m2 = ptx::f32x2(-mean, -mean), r2 = ptx::f32x2(rstd, rstd);
+        uint64_t h[P], w[P];
+        to_pairs<ES, G, CH>(nx, p.x_f16, h);
+        to_pairs<DES, G, CH>(nd, p.dy_f16, w);
+        px += x_step;
+        pd += d_step;
+        if (row + stride < p.R) {
+            load_e<ES, G, KIND, CH>(nx, px, pl);
+            load_e<DES, G, KIND, CH>(nd, pd, pl);
+            nmean = __ldg(p.mean + row + stride);
+            nrstd = __ldg(p.rstd + row + stride);
         }
-        const float mean = valid ? __ldg(p.mean + row) : 0.0f;
-        const float rstd = valid ? __ldg(p.rstd + row) : 0.0f;
         float s[2] = {0.0f, 0.0f};
+        if (valid) {
+            uint64_t s1 = 0, s2 = 0;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const long long g = t + c * T;
-            if (g < p.groups) {
-                float x[G], d[G], ga[G];
-                to_float<ES, G>(rx[c], p.x_f16, x);
-                to_float<DES, G>(rd[c], p.dy_f16, d);
-                load_param<G>(p.gamma, p.param_type, g * G, 1.0f, ga);
+            for (int j = 0; j < P / 2; ++j) {
+                const float4 g4 = my_gamma[j * threads];
 #pragma unroll
-                for (int i = 0; i < G; ++i) {
-                    const float h = (x[i] - mean) * rstd;
-                    const float w = d[i] * ga[i];
-                    s[0] += w;
-                    s[1] = fmaf(w, h, s[1]);
-                    dga[c][i] = fmaf(d[i], h, dga[c][i]);
-                    dbe[c][i] += d[i];
+                for (int i = 2 * j; i < 2 * j + 2; ++i) {
+                    h[i] = ptx::mul_f32x2(ptx::add_f32x2(h[i], m2), r2);
+                    dga[i] = ptx::fma_f32x2(w[i], h[i], dga[i]);
+                    dbe[i] = ptx::add_f32x2(dbe[i], w[i]);
+                    w[i] = ptx::mul_f32x2(w[i], i == 2 * j ? ptx::f32x2(g4.x, g4.y) : ptx::f32x2(g4.z, g4.w));
+                    s1 = ptx::add_f32x2(s1, w[i]);
+                    s2 = ptx::fma_f32x2(w[i], h[i], s2);
                 }
             }
+            float lo, hi;
+            ptx::unpack_f32x2(s1, lo, hi);
+            s[0] = lo + hi;
+            ptx::unpack_f32x2(s2, lo, hi);
+            s[1] = lo + hi;
         }
         if (p.dx == nullptr)
-            continue;                   // uniform: parameter sums only
-        team_sum<LANES, WARPS, 2>(s, red[flip]);
+            continue;                    // parameter sums only
+        team_sum8<KIND, 2>(s, tm, red[flip]);
         flip ^= 1;
-        const float m1 = s[0] * inv_c, m2 = s[1] * inv_c;
+        const float a = -s[0] * inv_c, b = -s[1] * inv_c;
+        const uint64_t a2 = ptx::f32x2(a, a), b2 = ptx::f32x2(b, b);
+        if (valid) {
+            uint64_t r[P];
+            to_pairs<ES, G, CH>(rr, p.x_f16, r);
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const long long g = t + c * T;
-            if (valid && g < p.groups) {
-                float x[G], d[G], ga[G], o[G];
-                to_float<ES, G>(rx[c], p.x_f16, x);
-                to_float<DES, G>(rd[c], p.dy_f16, d);
-                load_param<G>(p.gamma, p.param_type, g * G, 1.0f, ga);
+            for (int i = 0; i < P; ++i)
+                w[i] = ptx::fma_f32x2(ptx::fma_f32x2(h[i], b2, ptx::add_f32x2(w[i], a2)), r2, r[i]);
+            store_e<G, KIND, CH>(po, p.x_type, pl, w);
+        }
+        pr += r_step;
+        po += o_step;
+    }
+    if (p.partial != nullptr) {
+        const long long slot = KIND == kCluster ? blockIdx.x / tm.ctas : blockIdx.x;
 #pragma unroll
-                for (int i = 0; i < G; ++i) {
-                    const float h = (x[i] - mean) * rstd;
-                    o[i] = rstd * (fmaf(-h, m2, d[i] * ga[i]) - m1);
-                }
-                if (p.dres) {
-                    Raw<ES, G> rr;
-                    load_raw<ES, G>(rr, p.dres, row * p.lddres + g * G);
-                    float r[G];
-                    to_float<ES, G>(rr, p.x_f16, r);
+        for (int k = 0; k < 2; ++k) {
+            float f[2 * P];
 #pragma unroll
-                    for (int i = 0; i < G; ++i)
-                        o[i] += r[i];
-                }
-                store_group<G>(p.dx, p.x_type, row * p.lddx + g * G, o);
+            for (int i = 0; i < P; ++i)
+                ptx::unpack_f32x2(k == 0 ? dga[i] : dbe[i], f[2 * i], f[2 * i + 1]);
+            if constexpr (KIND > 0 && KIND < 32) {
+                // teams of one warp first
+#pragma unroll
+                for (int o = KIND; o < 32; o <<= 1)
+#pragma unroll
+                    for (int i = 0; i < 2 * P; ++i)
+                        f[i] += __shfl_xor_sync(0xFFFFFFFFu, f[i], o);
             }
+            // then the teams (or warps of teams) in order
+            int teams = 1, mine = 0;
+            bool speaks = true;
+            if constexpr (KIND > 0) {
+                teams = static_cast<int>(blockDim.x) / 32;
+                mine = static_cast<int>(threadIdx.x) >> 5;
+                speaks = static_cast<int>(threadIdx.x & 31) < KIND;
+            } else if constexpr (KIND == kCta) {
+                teams = static_cast<int>(blockDim.x) / tm.T;
+                mine = tm.id;
+            }
+            if constexpr (KIND != kCluster) {
+                for (int m = 0; m + 1 < teams; ++m) {
+                    __syncthreads();
+                    if (mine == m && speaks) {
+#pragma unroll
+                        for (int i = 0; i < 2 * P; ++i) {
+                            const int at = i * tm.T + t;
+                            cols[at] = m == 0 ? f[i] : cols[at] + f[i];
+                        }
+                    }
+                }
+                __syncthreads();
+                if (teams > 1 && mine == teams - 1 && speaks) {
+#pragma unroll
+                    for (int i = 0; i < 2 * P; ++i)
+                        f[i] += cols[i * tm.T + t];
+                }
+            }
+            if (mine == teams - 1 && speaks) {
+                uint64_t v[P];
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                    v[i] = ptx::f32x2(f[2 * i], f[2 * i + 1]);
+                store_e<G, KIND, CH>(reinterpret_cast<uint8_t *>(p.partial + (slot * 2 + k) * p.C + pl.c0), kF32, pl, v);
+            }
+            __syncthreads();
         }
     }
-    if (p.partial == nullptr)
-        return;
-    // this CTA's column sums, the teams' in order
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        float *dst = p.partial + (static_cast<long long>(blockIdx.x) * 2 + k) * p.C;
-        float(*v)[G] = k == 0 ? dga : dbe;
-        if constexpr (kTeams > 1) {
-            __syncthreads();
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-#pragma unroll
-                for (int i = 0; i < G; ++i)
-                    cols[team * (T * CH * G) + (t + c * T) * G + i] = v[c][i];
-            __syncthreads();
-            for (long long c = threadIdx.x; c < p.C; c += kThreads) {
-                float a = cols[c];
-                for (int m = 1; m < kTeams; ++m)
-                    a += cols[m * (T * CH * G) + c];
-                dst[c] = a;
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const long long g = t + c * T;
-                if (g < p.groups) {
-#pragma unroll
-                    for (int i = 0; i < G; ++i)
-                        dst[g * G + i] = v[c][i];
-                }
-            }
-        }
-    }
+    if constexpr (KIND == kCluster)
+        ptx::cluster_sync();             // no CTA leaves while a peer's stores may reach it
 }
 
 // Rows of any length: dx by one CTA per row. The parameter sums come from

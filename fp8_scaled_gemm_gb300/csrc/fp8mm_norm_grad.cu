@@ -26,16 +26,31 @@ int sum_partials(const NormGradParams &p, int P, float *dgamma, float *dbeta, cu
                       "parameter sum launch", s);
 }
 
-template <int ES, int DES, int G, int LANES, int WARPS, int CH>
-int launch_rows(const NormGradParams &p, int sms, cudaStream_t stream, int *partials)
+// Teams of LANES lanes of a warp, or of some warps of a CTA: one CTA per SM,
+// so that few column sums are left to add.
+template <int ES, int DES, int G, int KIND>
+int launch_cta(NormGradParams p, int team, int sms, cudaStream_t stream, int *partials)
 {
-    constexpr int threads = fp8norm::kCtaThreads<LANES, WARPS>;
-    constexpr int teams = threads / (LANES * WARPS);
-    const int grid = static_cast<int>(std::min<int64_t>(cdiv(p.R, teams),
-                                                        static_cast<int64_t>(sms) * (threads > 512 ? 1 : kCtasPerSm)));
-    *partials = grid;
-    return launch_pdl(fp8norm::norm_grad_rows_kernel<ES, DES, G, LANES, WARPS, CH>, grid, threads, 0, stream,
-                      "layer norm gradient launch", p);
+    constexpr int most = fp8norm::kGradThreads;
+    p.team_threads = team;
+    const int teams = KIND > 0 ? most / team : std::min(most / team, 15);   // named barriers 1 .. 15
+    const int64_t grid = std::min<int64_t>(cdiv(p.R, teams), sms);
+    *partials = static_cast<int>(grid);
+    return launch_pdl(fp8norm::norm_grad_kernel<ES, DES, G, KIND, fp8norm::kGradCh<ES, DES, G, KIND>>,
+                      static_cast<int>(grid), teams * team, 0, stream, "layer norm gradient launch", p);
+}
+
+// A cluster of `ctas` CTAs per row.
+template <int ES, int DES, int G>
+int launch_cluster(NormGradParams p, int ctas, int64_t slice_cols, int threads, int sms, cudaStream_t stream,
+                   int *partials)
+{
+    p.slice_cols = slice_cols;
+    const int64_t clusters = std::min<int64_t>(p.R, std::max(1, sms / ctas));
+    *partials = static_cast<int>(clusters);
+    constexpr int CH = fp8norm::kGradCh<ES, DES, G, fp8norm::kCluster>;
+    return launch_clusters(fp8norm::norm_grad_kernel<ES, DES, G, fp8norm::kCluster, CH>,
+                           static_cast<int>(clusters) * ctas, ctas, threads, stream, "layer norm gradient launch", p);
 }
 
 template <int ES, int DES, int G>
@@ -60,29 +75,36 @@ int launch_long(const NormGradParams &p, int sms, cudaStream_t stream, int *part
     return e == cudaSuccess ? FP8MM_OK : cuda_fail(e, "layer norm parameter launch");
 }
 
-// The smallest team that holds a row of g groups, and its column sums, in registers.
+template <int ES, int DES, int G>
+int launch_wide(const NormGradParams &p, int sms, cudaStream_t stream, int *P)
+{
+    constexpr int warp_cols = 32 * 8 * fp8norm::kGradCh<ES, DES, G, fp8norm::kCta>;
+    constexpr int most = fp8norm::kGradThreads / 32;
+    const int64_t warps = cdiv(p.C, warp_cols);
+    if (warps <= most)
+        return launch_cta<ES, DES, G, fp8norm::kCta>(p, static_cast<int>(warps) * 32, sms, stream, P);
+    for (int ctas = 2; ctas <= fp8norm::kMaxCluster; ctas *= 2)
+        if (warps <= most * ctas) {
+            const int64_t each = cdiv(warps, ctas);
+            return launch_cluster<ES, DES, G>(p, ctas, each * warp_cols, static_cast<int>(each) * 32, sms, stream, P);
+        }
+    return launch_long<ES, DES, G>(p, sms, stream, P);
+}
+
 template <int ES, int DES>
 int launch(const NormGradParams &p, bool vec, int sms, cudaStream_t stream, int *P)
 {
-    const int64_t g = p.groups;
+    const int64_t C = p.C;
     if (vec) {
-        if (g <= 4) return launch_rows<ES, DES, 8, 4, 1, 1>(p, sms, stream, P);
-        if (g <= 8) return launch_rows<ES, DES, 8, 8, 1, 1>(p, sms, stream, P);
-        if (g <= 16) return launch_rows<ES, DES, 8, 16, 1, 1>(p, sms, stream, P);
-        if (g <= 32) return launch_rows<ES, DES, 8, 32, 1, 1>(p, sms, stream, P);
-        if (g <= 64) return launch_rows<ES, DES, 8, 32, 1, 2>(p, sms, stream, P);
-        if (g <= 128) return launch_rows<ES, DES, 8, 32, 2, 2>(p, sms, stream, P);
-        if (g <= 256) return launch_rows<ES, DES, 8, 32, 4, 2>(p, sms, stream, P);
-        if (g <= 512) return launch_rows<ES, DES, 8, 32, 8, 2>(p, sms, stream, P);
-        if (g <= 1024) return launch_rows<ES, DES, 8, 32, 16, 2>(p, sms, stream, P);
-        return launch_long<ES, DES, 8>(p, sms, stream, P);
+        if (C <= 32) return launch_cta<ES, DES, 8, 4>(p, 4, sms, stream, P);
+        if (C <= 64) return launch_cta<ES, DES, 8, 8>(p, 8, sms, stream, P);
+        if (C <= 128) return launch_cta<ES, DES, 8, 16>(p, 16, sms, stream, P);
+        if (C <= 256 * fp8norm::kGradCh<ES, DES, 8, 32>) return launch_cta<ES, DES, 8, 32>(p, 32, sms, stream, P);
+        return launch_wide<ES, DES, 8>(p, sms, stream, P);
     }
-    if (g <= 256) return launch_rows<ES, DES, 1, 32, 1, 8>(p, sms, stream, P);
-    if (g <= 1024) return launch_rows<ES, DES, 1, 32, 4, 8>(p, sms, stream, P);
-    if (g <= 2048) return launch_rows<ES, DES, 1, 32, 8, 8>(p, sms, stream, P);
-    if (g <= 4096) return launch_rows<ES, DES, 1, 32, 16, 8>(p, sms, stream, P);
-    if (g <= 8192) return launch_rows<ES, DES, 1, 32, 32, 8>(p, sms, stream, P);
-    return launch_long<ES, DES, 1>(p, sms, stream, P);
+    if (C <= 256)
+        return launch_cta<ES, DES, 1, 32>(p, 32, sms, stream, P);
+    return launch_wide<ES, DES, 1>(p, sms, stream, P);
 }
 
 }  // namespace

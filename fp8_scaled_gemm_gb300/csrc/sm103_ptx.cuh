@@ -371,6 +371,12 @@ __device__ __forceinline__ void bulk_wait_group_all()
 }
 
 
+// Store a float to the shared memory of a CTA in the cluster (address from mapa).
+__device__ __forceinline__ void st_shared_cluster_f32(uint32_t cluster_addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+
 // Load a float from the shared memory of a CTA in the cluster (address from mapa).
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr)
 {
@@ -482,6 +488,18 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
+}
+
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
 
 // Both lanes to bf16 (F16: fp16), round to nearest even, lo in the low half.

@@ -77,7 +77,7 @@ def forward(R, C, *, x_dtype=BF16, y_dtype=None, p_dtype=F32, q_dtype=torch.floa
 
 
 WIDTHS = [1, 2, 7, 8, 24, 33, 64, 120, 255, 256, 264, 512, 520, 1000, 1024, 1032, 2048, 2056, 4095, 4096, 4104, 8192,
-          8200, 8193, 16384, 16385, 16392, 32768, 32776, 40000]
+          8200, 8193, 16384, 16385, 16392, 32768, 32776, 40000, 65544, 70001]
 
 
 @pytest.mark.parametrize("C", WIDTHS)
