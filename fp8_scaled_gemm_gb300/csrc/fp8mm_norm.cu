@@ -7,39 +7,38 @@ namespace {
 using namespace fp8mm_host;
 using fp8norm::NormParams;
 
-template <int ES, int G, int KIND, int CH, bool MANY>
+template <int ES, int G, int KIND, int CH>
 int launch_norm(const NormParams &p, int64_t grid, int threads, cudaStream_t stream)
 {
-    auto kern = fp8norm::norm_kernel<ES, G, KIND, CH, MANY>;
-    constexpr int per_thread = 2 * 2 * CH * 16;             // gamma's and beta's float4s
+    auto kern = fp8norm::norm_kernel<ES, G, KIND, CH>;
+    const int smem = (KIND > 0 ? KIND : threads) * 4 * CH * 16;   // one team's gamma and beta
     static bool attr_set[kMaxDevices] = {};
     int dev = 0;
     cudaGetDevice(&dev);
-    if (!attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (MANY ? 1024 : 256) * per_thread);
+    if (KIND <= 0 && !attr_set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 * 4 * CH * 16);
         if (e != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute");
         attr_set[dev] = true;
     }
-    return launch_pdl(kern, static_cast<int>(grid), threads, threads * per_thread, stream, "layer norm launch", p);
+    return launch_pdl(kern, static_cast<int>(grid), threads, smem, stream, "layer norm launch", p);
 }
 
-// Teams of LANES lanes of a warp.
+// Teams of LANES lanes of a warp, 256 threads to a CTA.
 template <int ES, int G, int LANES, int CH>
 int launch_lanes(const NormParams &p, int sms, cudaStream_t stream)
 {
-    return launch_norm<ES, G, LANES, CH, false>(
+    return launch_norm<ES, G, LANES, CH>(
         p, std::min<int64_t>(cdiv(p.R, 256 / LANES), static_cast<int64_t>(sms) * (CH == 4 ? 3 : 4)), 256, stream);
 }
 
-// A CTA per row, as many of them on an SM as threads fit: 768 or 1024.
-template <int ES, int G, int CH, bool MANY>
+// A CTA per row, as many of them on an SM as make 1024 threads.
+template <int ES, int G, int CH>
 int launch_cta(const NormParams &p, int sms, cudaStream_t stream)
 {
     const int threads = static_cast<int>(cdiv(p.C, 32 * 8 * CH)) * 32;
-    return launch_norm<ES, G, fp8norm::kCta, CH, MANY>(
-        p, std::min<int64_t>(p.R, static_cast<int64_t>(sms) * ((MANY ? 1024 : 768) / threads)), threads, stream);
+    return launch_norm<ES, G, fp8norm::kCta, CH>(
+        p, std::min<int64_t>(p.R, static_cast<int64_t>(sms) * (1024 / threads)), threads, stream);
 }
 
 template <int ES>
@@ -52,15 +51,13 @@ int launch(const NormParams &p, bool vec, int sms, cudaStream_t stream)
         if (C <= 128) return launch_lanes<ES, 8, 16, 1>(p, sms, stream);
         if (C <= 256) return launch_lanes<ES, 8, 32, 1>(p, sms, stream);
         if (C <= 512) return launch_lanes<ES, 8, 32, 2>(p, sms, stream);
-        if constexpr (ES == 2) {
-            if (C <= 1024) return launch_lanes<2, 8, 32, 4>(p, sms, stream);
-            if (C <= 8192) return launch_cta<2, 8, 4, false>(p, sms, stream);
-        }
-        if (C <= 16384) return launch_cta<ES, 8, 2, true>(p, sms, stream);
+        if (C <= 1024) return launch_lanes<ES, 8, 32, 4>(p, sms, stream);
+        if (C <= 16384) return launch_cta<ES, 8, 2>(p, sms, stream);
     } else {
         if (C <= 256) return launch_lanes<ES, 1, 32, 1>(p, sms, stream);
         if (C <= 512) return launch_lanes<ES, 1, 32, 2>(p, sms, stream);
-        if (C <= 16384) return launch_cta<ES, 1, 2, true>(p, sms, stream);
+        if (C <= 1024) return launch_lanes<ES, 1, 32, 4>(p, sms, stream);
+        if (C <= 16384) return launch_cta<ES, 1, 2>(p, sms, stream);
     }
     const int grid = static_cast<int>(std::min<int64_t>(p.R, static_cast<int64_t>(sms) * 8));
     if (vec)

@@ -44,9 +44,12 @@ using namespace fp8rows;
 
 constexpr int kMaxCluster = 8;       // CTAs that share a row (backward)
 
-// Kinds of team: LANES 4 .. 32 lanes of a warp; kCta some warps of a CTA with
-// a named barrier of their own; kCluster all threads of a cluster's CTAs.
-constexpr int kCta = 0, kCluster = -1;
+// Kinds of team: LANES 4 .. 32 lanes of a warp; kCta all threads of a CTA;
+// kTeams some warps of a CTA, with a named barrier of their own; kCluster all
+// threads of a cluster's CTAs. (A barrier number that is not a constant makes
+// a CTA hold all 16 of its barriers, and 4 such CTAs are all that fit an SM:
+// small CTAs use kCta.)
+constexpr int kCta = 0, kCluster = -1, kTeams = -2;
 
 // A thread's columns: E = 8 CH of them from c0 on. G = 8: groups of 8
 // neighbours, 8 x (lanes) apart; G = 1: single columns 32 apart. `left`
@@ -224,9 +227,8 @@ __device__ __forceinline__ void param_e(const void *base, int type, const Place<
     }
 }
 
-// A thread's own copy of its parameters in shared memory, fp32: float4 j of
-// it at slots[j * threads of the CTA], so that a warp's accesses are free of
-// bank conflicts. Only the thread that wrote it reads it: no barrier.
+// A thread's parameters in shared memory, fp32: float4 j of them at
+// slots[j * threads], so that a warp's accesses are free of bank conflicts.
 template <int CH>
 __device__ __forceinline__ void keep_params(float4 *slots, int threads, const uint64_t (&v)[4 * CH])
 {
@@ -282,6 +284,8 @@ __device__ __forceinline__ void team_barrier(const Team &tm)
 {
     if constexpr (KIND == kCluster)
         ptx::cluster_sync();
+    else if constexpr (KIND == kCta)
+        __syncthreads();
     else
         asm volatile("bar.sync %0, %1;" ::"r"(tm.id + 1), "r"(tm.T) : "memory");
 }
@@ -410,7 +414,7 @@ __device__ __forceinline__ Team this_team(int team_threads, int &t, long long &f
         t = static_cast<int>(threadIdx.x) % KIND;
         first = static_cast<long long>(blockIdx.x) * per_cta + tm.id;
         stride = static_cast<long long>(gridDim.x) * per_cta;
-    } else if constexpr (KIND == kCta) {
+    } else if constexpr (KIND == kCta || KIND == kTeams) {
         tm.T = team_threads;
         tm.warps = team_threads >> 5;
         const int per_cta = static_cast<int>(blockDim.x) / team_threads;
@@ -521,13 +525,16 @@ __device__ __forceinline__ void store_codes_e(uint8_t *p, const Place<G, KIND, C
     }
 }
 
-// 16-bit rows in 16-byte groups take CTAs of up to 256 threads of 32 columns,
-// three per SM, which hide each other's barriers. The others (fp32, single
-// elements: more registers per column as loaded) and wider rows take 16
-// columns and up to 1024 threads (MANY). The CTA's dynamic shared memory holds
-// gamma and beta (keep_params).
-template <int ES, int G, int KIND, int CH, bool MANY>
-__global__ void __launch_bounds__(MANY ? 1024 : 256, MANY ? 1 : 3) norm_kernel(const NormParams p)
+// One row per CTA at a time (KIND > 0: per team of lanes), 64 registers, and
+// as many CTAs on an SM as make 1024 threads: they hide each other's barriers.
+// 16 columns per thread; measured at 16384 x 8192 bf16 with codes, 121 us:
+// 8 columns 177; 32 columns and 768 threads 150; the next two rows in shared
+// memory (cp.async) instead of the next one in registers 119 to 121; several
+// rows' teams in one CTA 155; gamma and beta from global memory (L1) for every
+// row 174. They are kept in shared memory (keep_params).
+template <int ES, int G, int KIND, int CH>
+__global__ void __launch_bounds__(KIND > 0 ? 256 : 1024, KIND > 0 ? (CH == 4 ? 3 : 4) : 1)
+    norm_kernel(const NormParams p)
 {
     __shared__ float red[3][kRedWords<KIND, 1>];
     extern __shared__ float4 params[];
@@ -536,8 +543,7 @@ __global__ void __launch_bounds__(MANY ? 1024 : 256, MANY ? 1 : 3) norm_kernel(c
     long long first, stride;
     const Team tm = this_team<KIND>(static_cast<int>(blockDim.x), t, first, stride);
     const Place<G, KIND, CH> pl(0, p.C, t);
-    const int threads = static_cast<int>(blockDim.x);
-    float4 *const my_gamma = params + threadIdx.x, *const my_beta = my_gamma + 2 * CH * threads;
+    float4 *const my_gamma = params + t, *const my_beta = my_gamma + 2 * CH * tm.T;
     ptx::grid_dependency_wait();
 
     const float inv_c = 1.0f / static_cast<float>(p.C);
@@ -547,13 +553,15 @@ __global__ void __launch_bounds__(MANY ? 1024 : 256, MANY ? 1 : 3) norm_kernel(c
     clear_e<ES, G, CH>(raw);
     if (first < p.R)
         load_e<ES, G, KIND, CH>(raw, x, pl);
-    {
+    if (tm.id == 0) {
         uint64_t v[4 * CH];
         param_e<G, KIND, CH>(p.gamma, p.param_type, pl, 1.0f, v);
-        keep_params<CH>(my_gamma, threads, v);
+        keep_params<CH>(my_gamma, tm.T, v);
         param_e<G, KIND, CH>(p.beta, p.param_type, pl, 0.0f, v);
-        keep_params<CH>(my_beta, threads, v);
+        keep_params<CH>(my_beta, tm.T, v);
     }
+    if constexpr (KIND > 0)
+        __syncthreads();                 // several teams read the first one's copy
 
     // every thread of a CTA makes the same number of turns
     const long long first0 = KIND > 0 ? first - tm.id : first;
@@ -586,7 +594,7 @@ __global__ void __launch_bounds__(MANY ? 1024 : 256, MANY ? 1 : 3) norm_kernel(c
         const uint64_t r2 = ptx::f32x2(rstd, rstd);
 #pragma unroll
         for (int j = 0; j < 2 * CH; ++j) {
-            const float4 ga = my_gamma[j * threads], be = my_beta[j * threads];
+            const float4 ga = my_gamma[j * tm.T], be = my_beta[j * tm.T];
             v[2 * j] = ptx::fma_f32x2(ptx::mul_f32x2(v[2 * j], r2), ptx::f32x2(ga.x, ga.y), ptx::f32x2(be.x, be.y));
             v[2 * j + 1] =
                 ptx::fma_f32x2(ptx::mul_f32x2(v[2 * j + 1], r2), ptx::f32x2(ga.z, ga.w), ptx::f32x2(be.z, be.w));
@@ -713,7 +721,7 @@ struct NormGradParams {
     float *partial;            // [CTAs or clusters][2][C]: dgamma and dbeta sums of their rows, or nullptr
     long long R, C;
     long long groups;          // long kernels: element groups per row
-    int team_threads;          // kCta: threads of a team
+    int team_threads;          // kTeams: threads of a team
     long long slice_cols;      // kCluster: columns of each CTA
 };
 
@@ -857,7 +865,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) norm_grad_kernel(const NormGr
                 teams = static_cast<int>(blockDim.x) / 32;
                 mine = static_cast<int>(threadIdx.x) >> 5;
                 speaks = static_cast<int>(threadIdx.x & 31) < KIND;
-            } else if constexpr (KIND == kCta) {
+            } else if constexpr (KIND == kTeams) {
                 teams = static_cast<int>(blockDim.x) / tm.T;
                 mine = tm.id;
             }

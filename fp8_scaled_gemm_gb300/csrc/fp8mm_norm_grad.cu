@@ -78,11 +78,11 @@ int launch_long(const NormGradParams &p, int sms, cudaStream_t stream, int *part
 template <int ES, int DES, int G>
 int launch_wide(const NormGradParams &p, int sms, cudaStream_t stream, int *P)
 {
-    constexpr int warp_cols = 32 * 8 * fp8norm::kGradCh<ES, DES, G, fp8norm::kCta>;
+    constexpr int warp_cols = 32 * 8 * fp8norm::kGradCh<ES, DES, G, fp8norm::kTeams>;
     constexpr int most = fp8norm::kGradThreads / 32;
     const int64_t warps = cdiv(p.C, warp_cols);
     if (warps <= most)
-        return launch_cta<ES, DES, G, fp8norm::kCta>(p, static_cast<int>(warps) * 32, sms, stream, P);
+        return launch_cta<ES, DES, G, fp8norm::kTeams>(p, static_cast<int>(warps) * 32, sms, stream, P);
     for (int ctas = 2; ctas <= fp8norm::kMaxCluster; ctas *= 2)
         if (warps <= most * ctas) {
             const int64_t each = cdiv(warps, ctas);
