@@ -7,16 +7,18 @@
 //   silu       x s(x)
 //
 // All go through one exponential and one reciprocal (ex2.approx and
-// rcp.approx, relative errors of about 2^-22 and 2^-23), which the products'
-// epilogues can afford: 10 to 16 instructions per element.
+// rcp.approx, relative errors of about 2^-22 and 2^-23), two elements at a
+// time (f32x2): 5 to 14 instructions per element, so that the products'
+// epilogues stay hidden behind the matrix instructions of the next tile.
 //
 // Phi: for a = |x|, Phi(-a) = exp(-a^2/2) h(a), where h is half the scaled
 // complementary error function of a/sqrt(2). h falls like 1/a, so it is a
 // polynomial in t = 1/(1 + p a) without constant term (the form of
 // C. Hastings, "Approximations for Digital Computers", 1955). The seven
 // coefficients and p are a least-maximum fit of the relative error over
-// 0 <= a <= 20 against scipy's erfcx: at most 1.3e-6 of h, so Phi keeps that
-// relative accuracy in its tail, where 1 + erf(x) has none left.
+// 0 <= a <= 20 against scipy's erfcx: at most 1.3e-6 of h, so Phi keeps its
+// relative accuracy in the tail (with the rounding of the exponent's argument
+// 8e-6 at x = -13), where 1 + erf(x) has none left.
 //
 // Limits: NaN gives NaN; -inf gives -0 or +0 (relu: 0), +inf gives +inf;
 // slopes are 0 and 1 there. The arguments are clamped where the function has
@@ -24,6 +26,9 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "sm103_ptx.cuh"
 
 namespace fp8mm {
 
@@ -59,137 +64,163 @@ __device__ __forceinline__ float clamp_nan(float x, float lim) { return min_nan(
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// 1 / (1 + exp(-x)); 0 where exp(-x) overflows.
-__device__ __forceinline__ float logistic(float x) { return rcp_approx(1.0f + ex2_approx(-kLog2e * x)); }
+// ------------------------------------------------------ pairs of values ---
 
-// Phi(-a) and exp(-a^2/2) for 0 <= a <= 20.
-__device__ __forceinline__ float normal_tail(float a, float &e)
+struct Pair {
+    float lo, hi;
+};
+
+__device__ __forceinline__ uint64_t pack(Pair p) { return ptx::f32x2(p.lo, p.hi); }
+__device__ __forceinline__ uint64_t both(float c) { return ptx::f32x2(c, c); }
+__device__ __forceinline__ Pair unpack(uint64_t v)
 {
-    const float t = rcp_approx(fmaf(0.36864640577302416f, a, 1.0f));
-    e = ex2_approx((a * a) * (-0.5f * kLog2e));
-    float h = 0.04837304787388369f;
-    h = fmaf(h, t, -0.17252712897935096f);
-    h = fmaf(h, t, 0.15209262775945798f);
-    h = fmaf(h, t, 0.0424434924047982f);
-    h = fmaf(h, t, 0.13644234400211985f);
-    h = fmaf(h, t, 0.14606507133564497f);
-    h = fmaf(h, t, 0.1471111567833028f);
-    return h * (t * e);
+    Pair p;
+    ptx::unpack_f32x2(v, p.lo, p.hi);
+    return p;
+}
+__device__ __forceinline__ uint64_t ex2_pair(uint64_t v)
+{
+    const Pair p = unpack(v);
+    return ptx::f32x2(ex2_approx(p.lo), ex2_approx(p.hi));
+}
+__device__ __forceinline__ uint64_t rcp_pair(uint64_t v)
+{
+    const Pair p = unpack(v);
+    return ptx::f32x2(rcp_approx(p.lo), rcp_approx(p.hi));
 }
 
-__device__ __forceinline__ float act_relu(float x) { return max_nan(x, 0.0f); }
+// 1 / (1 + 2^v)
+__device__ __forceinline__ uint64_t rcp_1p_ex2(uint64_t v) { return rcp_pair(ptx::add_f32x2(ex2_pair(v), both(1.0f))); }
+
+// Phi(-a) for 0 <= a <= 20, given -a; e receives exp(-a^2/2).
+__device__ __forceinline__ uint64_t normal_tail(uint64_t neg_a, uint64_t &e)
+{
+    const uint64_t t = rcp_pair(ptx::fma_f32x2(both(-0.36864640577302416f), neg_a, both(1.0f)));
+    e = ex2_pair(ptx::mul_f32x2(ptx::mul_f32x2(neg_a, neg_a), both(-0.5f * kLog2e)));
+    uint64_t h = both(0.04837304787388369f);
+    h = ptx::fma_f32x2(h, t, both(-0.17252712897935096f));
+    h = ptx::fma_f32x2(h, t, both(0.15209262775945798f));
+    h = ptx::fma_f32x2(h, t, both(0.0424434924047982f));
+    h = ptx::fma_f32x2(h, t, both(0.13644234400211985f));
+    h = ptx::fma_f32x2(h, t, both(0.14606507133564497f));
+    h = ptx::fma_f32x2(h, t, both(0.1471111567833028f));
+    return ptx::mul_f32x2(h, ptx::mul_f32x2(t, e));
+}
 
 // x Phi(x) = max(x, 0) - |x| Phi(-|x|); Phi(-20) is 0 in fp32.
-__device__ __forceinline__ float act_gelu(float x)
+__device__ __forceinline__ Pair act_gelu(Pair x)
 {
-    const float a = fminf(fabsf(x), 20.0f);
-    float e;
-    const float q = normal_tail(a, e);
-    return fmaf(-a, q, max_nan(x, 0.0f));
+    const uint64_t na = ptx::f32x2(fmaxf(-fabsf(x.lo), -20.0f), fmaxf(-fabsf(x.hi), -20.0f));
+    uint64_t e;
+    const uint64_t q = normal_tail(na, e);
+    return unpack(ptx::fma_f32x2(na, q, ptx::f32x2(max_nan(x.lo, 0.0f), max_nan(x.hi, 0.0f))));
 }
 
 constexpr float kGeluTanhC0 = 1.5957691216057308f;               // 2 sqrt(2/pi)
 constexpr float kGeluTanhC1 = 1.5957691216057308f * 0.044715f;
 
-__device__ __forceinline__ float act_gelu_tanh(float x)
+// s(2u) is 0 in fp32 at x = -20
+__device__ __forceinline__ Pair act_gelu_tanh(Pair x)
 {
-    x = max_nan(x, -20.0f);                                       // s(2u) is 0 there
-    return x * logistic(x * fmaf(kGeluTanhC1, x * x, kGeluTanhC0));
+    const uint64_t v = ptx::f32x2(max_nan(x.lo, -20.0f), max_nan(x.hi, -20.0f));
+    const uint64_t k = ptx::fma_f32x2(both(-kLog2e * kGeluTanhC1), ptx::mul_f32x2(v, v), both(-kLog2e * kGeluTanhC0));
+    return unpack(ptx::mul_f32x2(v, rcp_1p_ex2(ptx::mul_f32x2(v, k))));
 }
 
-__device__ __forceinline__ float act_silu(float x)
+// x s(x) is 0 in fp32 at x = -110
+__device__ __forceinline__ Pair act_silu(Pair x)
 {
-    x = max_nan(x, -110.0f);                                      // x s(x) is 0 there
-    return x * logistic(x);
+    const uint64_t v = ptx::f32x2(max_nan(x.lo, -110.0f), max_nan(x.hi, -110.0f));
+    return unpack(ptx::mul_f32x2(v, rcp_1p_ex2(ptx::mul_f32x2(v, both(-kLog2e)))));
 }
 
 // ------------------------------------------------------------- slopes ---
 
-__device__ __forceinline__ float slope_relu(float x) { return x > 0.0f ? 1.0f : (x != x ? x : 0.0f); }
+// v where x > 0, 0 elsewhere (also for an infinite v), NaN for a NaN x
+__device__ __forceinline__ float times_slope_relu(float v, float x) { return x > 0.0f ? v : (x != x ? x : 0.0f); }
 
 // Phi(x) + x exp(-x^2/2) / sqrt(2 pi)
-__device__ __forceinline__ float slope_gelu(float x)
+__device__ __forceinline__ uint64_t slope_gelu(Pair x)
 {
-    x = clamp_nan(x, 20.0f);
-    float e;
-    const float q = normal_tail(fabsf(x), e);
-    return fmaf(x * 0.3989422804014327f, e, x > 0.0f ? 1.0f - q : q);
+    x.lo = clamp_nan(x.lo, 20.0f);
+    x.hi = clamp_nan(x.hi, 20.0f);
+    uint64_t e;
+    const uint64_t q2 = normal_tail(ptx::f32x2(-fabsf(x.lo), -fabsf(x.hi)), e);
+    const Pair q = unpack(q2), p = unpack(ptx::fma_f32x2(q2, both(-1.0f), both(1.0f)));
+    const uint64_t phi = ptx::f32x2(x.lo > 0.0f ? p.lo : q.lo, x.hi > 0.0f ? p.hi : q.hi);
+    return ptx::fma_f32x2(ptx::mul_f32x2(pack(x), both(0.3989422804014327f)), e, phi);
 }
 
 // s + x s (1 - s) (2u)'
-__device__ __forceinline__ float slope_gelu_tanh(float x)
+__device__ __forceinline__ uint64_t slope_gelu_tanh(Pair x)
 {
-    x = clamp_nan(x, 20.0f);
-    const float x2 = x * x;
-    const float s = logistic(x * fmaf(kGeluTanhC1, x2, kGeluTanhC0));
-    const float d = fmaf(3.0f * kGeluTanhC1, x2, kGeluTanhC0);
-    return fmaf(s * (1.0f - s), x * d, s);
+    const uint64_t v = ptx::f32x2(clamp_nan(x.lo, 20.0f), clamp_nan(x.hi, 20.0f));
+    const uint64_t v2 = ptx::mul_f32x2(v, v);
+    const uint64_t k = ptx::fma_f32x2(both(-kLog2e * kGeluTanhC1), v2, both(-kLog2e * kGeluTanhC0));
+    const uint64_t s = rcp_1p_ex2(ptx::mul_f32x2(v, k));
+    const uint64_t d = ptx::fma_f32x2(both(3.0f * kGeluTanhC1), v2, both(kGeluTanhC0));
+    const uint64_t r = ptx::mul_f32x2(s, ptx::fma_f32x2(s, both(-1.0f), both(1.0f)));
+    return ptx::fma_f32x2(r, ptx::mul_f32x2(v, d), s);
 }
 
 // s (1 + x (1 - s))
-__device__ __forceinline__ float slope_silu(float x)
+__device__ __forceinline__ uint64_t slope_silu(Pair x)
 {
-    x = clamp_nan(x, 110.0f);
-    const float s = logistic(x);
-    return s * fmaf(x, 1.0f - s, 1.0f);
+    const uint64_t v = ptx::f32x2(clamp_nan(x.lo, 110.0f), clamp_nan(x.hi, 110.0f));
+    const uint64_t s = rcp_1p_ex2(ptx::mul_f32x2(v, both(-kLog2e)));
+    return ptx::mul_f32x2(s, ptx::fma_f32x2(v, ptx::fma_f32x2(s, both(-1.0f), both(1.0f)), both(1.0f)));
 }
 
 // One switch for a whole array, so that the unrolled loops hold no branches.
 template <int CH>
 __device__ __forceinline__ void apply_act(int act, float (&v)[CH])
 {
+    static_assert(CH % 2 == 0, "pairs");
+#define FP8MM_EACH_PAIR(expr)                      \
+    _Pragma("unroll") for (int j = 0; j < CH; j += 2) \
+    {                                              \
+        const Pair r = expr(Pair{v[j], v[j + 1]}); \
+        v[j] = r.lo;                               \
+        v[j + 1] = r.hi;                           \
+    }
     switch (act) {
     case kActRelu:
 #pragma unroll
         for (int j = 0; j < CH; ++j)
-            v[j] = act_relu(v[j]);
+            v[j] = max_nan(v[j], 0.0f);
         break;
-    case kActGelu:
-#pragma unroll
-        for (int j = 0; j < CH; ++j)
-            v[j] = act_gelu(v[j]);
-        break;
-    case kActGeluTanh:
-#pragma unroll
-        for (int j = 0; j < CH; ++j)
-            v[j] = act_gelu_tanh(v[j]);
-        break;
-    case kActSilu:
-#pragma unroll
-        for (int j = 0; j < CH; ++j)
-            v[j] = act_silu(v[j]);
-        break;
+    case kActGelu: FP8MM_EACH_PAIR(act_gelu) break;
+    case kActGeluTanh: FP8MM_EACH_PAIR(act_gelu_tanh) break;
+    case kActSilu: FP8MM_EACH_PAIR(act_silu) break;
     default: break;
     }
+#undef FP8MM_EACH_PAIR
 }
 
 // v *= slope(z)
 template <int CH>
 __device__ __forceinline__ void apply_slope(int act, float (&v)[CH], const float (&z)[CH])
 {
+    static_assert(CH % 2 == 0, "pairs");
+#define FP8MM_EACH_PAIR(expr)                                                                       \
+    _Pragma("unroll") for (int j = 0; j < CH; j += 2)                                               \
+    {                                                                                               \
+        const Pair r = unpack(ptx::mul_f32x2(ptx::f32x2(v[j], v[j + 1]), expr(Pair{z[j], z[j + 1]}))); \
+        v[j] = r.lo;                                                                                \
+        v[j + 1] = r.hi;                                                                            \
+    }
     switch (act) {
     case kActRelu:
 #pragma unroll
         for (int j = 0; j < CH; ++j)
-            v[j] = z[j] <= 0.0f ? 0.0f : v[j] * slope_relu(z[j]);   // 0 below the kink, also for an infinite v
+            v[j] = times_slope_relu(v[j], z[j]);
         break;
-    case kActGelu:
-#pragma unroll
-        for (int j = 0; j < CH; ++j)
-            v[j] *= slope_gelu(z[j]);
-        break;
-    case kActGeluTanh:
-#pragma unroll
-        for (int j = 0; j < CH; ++j)
-            v[j] *= slope_gelu_tanh(z[j]);
-        break;
-    case kActSilu:
-#pragma unroll
-        for (int j = 0; j < CH; ++j)
-            v[j] *= slope_silu(z[j]);
-        break;
+    case kActGelu: FP8MM_EACH_PAIR(slope_gelu) break;
+    case kActGeluTanh: FP8MM_EACH_PAIR(slope_gelu_tanh) break;
+    case kActSilu: FP8MM_EACH_PAIR(slope_silu) break;
     default: break;
     }
+#undef FP8MM_EACH_PAIR
 }
 
 }  // namespace fp8mm

@@ -7,28 +7,34 @@ namespace {
 using namespace fp8mm_host;
 using fp8act::ActGradParams;
 
+// Lanes of a warp across the columns, 8 columns each.
+int lanes_for(int64_t N) { return N <= 64 ? 8 : N <= 128 ? 16 : 32; }
+
 // Row slabs of a call on [M, N]: enough CTAs to fill the SMs, each with at
-// least as many rows as it has warps.
+// least a few turns of its warps.
 int64_t slabs_for(int64_t M, int64_t N, int sms)
 {
-    const int64_t strips = cdiv(N, 256);
-    return std::max<int64_t>(1, std::min<int64_t>({cdiv(M, 8), cdiv(static_cast<int64_t>(sms) * 16, strips), 65535}));
+    const int lanes = lanes_for(N);
+    const int64_t strips = cdiv(N, 8 * lanes), turn = fp8act::kWarps * (32 / lanes);
+    // four CTAs fit an SM: up to four whole waves of them
+    return std::max<int64_t>(1, std::min<int64_t>({cdiv(M, 2 * turn), static_cast<int64_t>(sms) * 16 / strips, 65535}));
+}
+
+template <int ES, int G, int LANES>
+int launch_lanes(const ActGradParams &p, int64_t slabs, cudaStream_t stream)
+{
+    return launch_grid2(fp8act::act_grad_kernel<ES, G, LANES, (ES == 2 && G == 8) ? 2 : 1>, cdiv(p.N, 8 * LANES), slabs,
+                        fp8act::kThreads, stream, "activation gradient launch", p);
 }
 
 template <int ES, int G>
 int launch(const ActGradParams &p, int64_t slabs, cudaStream_t stream)
 {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(cdiv(p.N, 256)), static_cast<unsigned>(slabs), 1);
-    cfg.blockDim = dim3(fp8act::kThreads, 1, 1);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8act::act_grad_kernel<ES, G>, p);
-    return e == cudaSuccess ? FP8MM_OK : cuda_fail(e, "activation gradient launch");
+    switch (lanes_for(p.N)) {
+    case 8: return launch_lanes<ES, G, 8>(p, slabs, stream);
+    case 16: return launch_lanes<ES, G, 16>(p, slabs, stream);
+    default: return launch_lanes<ES, G, 32>(p, slabs, stream);
+    }
 }
 
 bool shape_ok(int64_t M, int64_t N)
@@ -115,8 +121,7 @@ int fp8_act_grad(const void *dy, int64_t lddy, const void *z, int64_t ldz, int t
     sum.C = N;
     sum.P = static_cast<int>(slabs);
     sum.K = 1;
-    return launch_pdl(fp8rows::partial_sum_kernel, static_cast<int>(cdiv(N, 32)), fp8rows::kSumThreads, 0, s,
-                      "bias sum launch", sum);
+    return launch_grid2(fp8rows::partial_sum_kernel, cdiv(N, 32), 1, fp8rows::kSumThreads, s, "bias sum launch", sum);
 }
 
 }  // extern "C"

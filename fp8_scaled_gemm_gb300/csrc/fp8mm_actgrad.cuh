@@ -3,11 +3,13 @@
 //   dz = dy * act'(z)            one rounding
 //   dbias[n] = sum over m of dy act'(z), from the unrounded products
 //
-// Bound by HBM: two reads and one write per element. A CTA takes a strip of
-// 32 G columns and the rows of its slab (blockIdx.y), warp w rows w, w + 8,
-// ...; each lane keeps the sums of its columns in registers, the CTA's warps
-// add theirs in order, and the slabs' partials are added by
-// fp8rows::partial_sum_kernel.
+// Bound by HBM: two reads and one write per element, and about 20
+// instructions for the slope. A warp covers 8 LANES columns and 32 / LANES
+// rows at a time (LANES < 32 for narrow matrices), NR times over, so that
+// enough loads are in flight (16384 x 14336 bf16 gelu: one row of 256 columns
+// per warp 296 us, two NOTE); each lane keeps the sums of its columns in
+// registers over the rows of its slab (blockIdx.y). The CTA's warps add theirs
+// in order, and the slabs' partials are added by fp8rows::partial_sum_kernel.
 #pragma once
 
 #include "fp8mm_act.cuh"
@@ -29,72 +31,99 @@ struct ActGradParams {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
-template <int ES, int G>
+// G = 8: a lane's columns are neighbours; G = 1: LANES apart.
+template <int ES, int G, int LANES, int NR>
 __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradParams p)
 {
-    // lane's columns: G neighbours (G = 8) or 8 columns 32 apart (G = 1)
-    constexpr int K = G == 8 ? 1 : 8;
-    constexpr int kCols = 256;
+    constexpr int K = 8 / G;                     // loads of a lane per row and operand
+    constexpr int kCols = 8 * LANES, kRows = 32 / LANES;
+    constexpr int kStep = G == 8 ? 0 : LANES;    // columns between them
     __shared__ float cols[kWarps][kCols];
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long n0 = static_cast<long long>(blockIdx.x) * kCols;
+    const long long n0 = static_cast<long long>(blockIdx.x) * kCols + (lane % LANES) * G;
+    const int left = static_cast<int>(min(p.N - n0, 1ll << 20));   // columns from n0 on
     const long long slabs = gridDim.y, r0 = p.M * blockIdx.y / slabs, r1 = p.M * (blockIdx.y + 1) / slabs;
     const bool f16 = p.type == kF16;
-    float sum[K][G] = {};
-    for (long long row = r0 + warp; row < r1; row += kWarps) {
-        float v[K * G], z[K * G];
-        Raw<ES, G> rd[K], rz[K];
+    constexpr int kTurn = kWarps * kRows;        // rows of the CTA at a time
+    float sum[8] = {};
+    long long row = r0 + warp * kRows + lane / LANES;
+    const uint8_t *dy = static_cast<const uint8_t *>(p.dy) + (row * p.ldy + n0) * ES;
+    const uint8_t *z = static_cast<const uint8_t *>(p.z) + (row * p.ldz + n0) * ES;
+    uint8_t *dz = static_cast<uint8_t *>(p.dz) + (row * p.ldd + n0) * ES;
+    for (; row < r1; row += kTurn * NR) {
+        Raw<ES, G> rd[NR][K], rz[NR][K];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const long long n = n0 + (k * 32 + lane) * G;
-            if (n < p.N) {
-                load_raw<ES, G>(rd[k], p.dy, row * p.ldy + n);
-                if (p.z)
-                    load_raw<ES, G>(rz[k], p.z, row * p.ldz + n);
+        for (int r = 0; r < NR; ++r) {
+            const bool in_row = row + r * kTurn < r1;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const bool in = in_row && k * kStep < left;
+                if (in)
+                    load_raw<ES, G>(rd[r][k], dy + r * kTurn * p.ldy * ES, k * kStep);
                 else
-                    clear_raw<ES, G>(rz[k]);
+                    clear_raw<ES, G>(rd[r][k]);
+                if (in && p.z)
+                    load_raw<ES, G>(rz[r][k], z + r * kTurn * p.ldz * ES, k * kStep);
+                else
+                    clear_raw<ES, G>(rz[r][k]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            float v[8], x[8];
+            if constexpr (G == 8) {
+                to_float<ES, 8>(rd[r][0], f16, v);
+                to_float<ES, 8>(rz[r][0], f16, x);
             } else {
-                clear_raw<ES, G>(rd[k]);
-                clear_raw<ES, G>(rz[k]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    float a[1], b[1];
+                    to_float<ES, 1>(rd[r][k], f16, a);
+                    to_float<ES, 1>(rz[r][k], f16, b);
+                    v[k] = a[0];
+                    x[k] = b[0];
+                }
+            }
+            fp8mm::apply_slope<8>(p.act, v, x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                sum[k] += v[k];
+            if (p.dz && row + r * kTurn < r1) {
+                uint8_t *o = dz + r * kTurn * p.ldd * ES;
+                if constexpr (G == 8) {
+                    if (left > 0)
+                        store_group<8>(o, p.type, 0, v);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k * kStep < left) {
+                            const float one[1] = {v[k]};
+                            store_group<1>(o, p.type, k * kStep, one);
+                        }
+                }
             }
         }
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float a[G], b[G];
-            to_float<ES, G>(rd[k], f16, a);
-            to_float<ES, G>(rz[k], f16, b);
-#pragma unroll
-            for (int i = 0; i < G; ++i) {
-                v[k * G + i] = a[i];
-                z[k * G + i] = b[i];
-            }
-        }
-        fp8mm::apply_slope<K * G>(p.act, v, z);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const long long n = n0 + (k * 32 + lane) * G;
-            float o[G];
-#pragma unroll
-            for (int i = 0; i < G; ++i) {
-                o[i] = v[k * G + i];
-                sum[k][i] += o[i];
-            }
-            if (p.dz && n < p.N)
-                store_group<G>(p.dz, p.type, row * p.ldd + n, o);
-        }
+        dy += kTurn * NR * p.ldy * ES;
+        z += kTurn * NR * p.ldz * ES;
+        dz += kTurn * NR * p.ldd * ES;
     }
     if (p.partial == nullptr)
         return;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int o = LANES; o < 32; o <<= 1)
 #pragma unroll
-        for (int i = 0; i < G; ++i)
-            cols[warp][(k * 32 + lane) * G + i] = sum[k][i];
+        for (int k = 0; k < 8; ++k)
+            sum[k] += __shfl_xor_sync(0xFFFFFFFFu, sum[k], o);
+    if (lane < LANES) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            cols[warp][G == 8 ? lane * 8 + k : lane + k * LANES] = sum[k];
+    }
     __syncthreads();
-    const long long n = n0 + threadIdx.x;
-    if (n < p.N) {
+    const long long n = static_cast<long long>(blockIdx.x) * kCols + threadIdx.x;
+    if (threadIdx.x < kCols && n < p.N) {
         float a = cols[0][threadIdx.x];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w)

@@ -65,11 +65,13 @@ int launch_pdl(Kern kern, int grid, int threads, int smem, cudaStream_t stream, 
 
 // The same with the grid in clusters of `cluster` CTAs.
 template <typename Kern, typename... Args>
-int launch_clusters(Kern kern, int grid, int cluster, int threads, cudaStream_t stream, const char *what, Args... args)
+int launch_clusters(Kern kern, int grid, int cluster, int threads, int smem, cudaStream_t stream, const char *what,
+                    Args... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -45,11 +45,10 @@ using namespace fp8rows;
 constexpr int kMaxCluster = 8;       // CTAs that share a row (backward)
 
 // Kinds of team: LANES 4 .. 32 lanes of a warp; kCta all threads of a CTA;
-// kTeams some warps of a CTA, with a named barrier of their own; kCluster all
-// threads of a cluster's CTAs. (A barrier number that is not a constant makes
-// a CTA hold all 16 of its barriers, and 4 such CTAs are all that fit an SM:
-// small CTAs use kCta.)
-constexpr int kCta = 0, kCluster = -1, kTeams = -2;
+// kCluster all threads of a cluster's CTAs. (Several teams in a CTA, each
+// with a named barrier, were slower: a barrier number that is not a constant
+// makes a CTA hold all 16 of its barriers, so 4 CTAs fill an SM.)
+constexpr int kCta = 0, kCluster = -1;
 
 // A thread's columns: E = 8 CH of them from c0 on. G = 8: groups of 8
 // neighbours, 8 x (lanes) apart; G = 1: single columns 32 apart. `left`
@@ -274,8 +273,7 @@ __device__ __forceinline__ float sum_pairs(const uint64_t (&v)[N])
 
 struct Team {
     int T, warps;        // threads and warps of the team in this CTA
-    int id;              // team within the CTA: barrier id + 1 of it
-    int warp0;           // its first warp
+    int id;              // team within the CTA
     uint32_t rank, ctas; // place in the cluster
 };
 
@@ -284,10 +282,8 @@ __device__ __forceinline__ void team_barrier(const Team &tm)
 {
     if constexpr (KIND == kCluster)
         ptx::cluster_sync();
-    else if constexpr (KIND == kCta)
-        __syncthreads();
     else
-        asm volatile("bar.sync %0, %1;" ::"r"(tm.id + 1), "r"(tm.T) : "memory");
+        __syncthreads();
 }
 
 // Words of one reduction's exchange buffer for NV values.
@@ -320,7 +316,6 @@ __device__ __forceinline__ void team_sum8(float (&v)[NV], const Team &tm, float 
             }
             n *= static_cast<int>(tm.ctas);
         } else {
-            mine = red + tm.warp0 * NV;
             if (lane == 0) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
@@ -377,7 +372,6 @@ __device__ __forceinline__ void team_amax8(float (&v)[NV], const Team &tm, float
             }
             n *= static_cast<int>(tm.ctas);
         } else {
-            mine = red + tm.warp0 * NV;
             if (lane == 0) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
@@ -403,7 +397,7 @@ __device__ __forceinline__ void team_amax8(float (&v)[NV], const Team &tm, float
 
 // The team this thread belongs to, and which of all teams it is.
 template <int KIND>
-__device__ __forceinline__ Team this_team(int team_threads, int &t, long long &first, long long &stride)
+__device__ __forceinline__ Team this_team(int &t, long long &first, long long &stride)
 {
     Team tm{};
     if constexpr (KIND > 0) {
@@ -414,15 +408,12 @@ __device__ __forceinline__ Team this_team(int team_threads, int &t, long long &f
         t = static_cast<int>(threadIdx.x) % KIND;
         first = static_cast<long long>(blockIdx.x) * per_cta + tm.id;
         stride = static_cast<long long>(gridDim.x) * per_cta;
-    } else if constexpr (KIND == kCta || KIND == kTeams) {
-        tm.T = team_threads;
-        tm.warps = team_threads >> 5;
-        const int per_cta = static_cast<int>(blockDim.x) / team_threads;
-        tm.id = static_cast<int>(threadIdx.x) / team_threads;
-        tm.warp0 = tm.id * tm.warps;
-        t = static_cast<int>(threadIdx.x) % team_threads;
-        first = static_cast<long long>(blockIdx.x) * per_cta + tm.id;
-        stride = static_cast<long long>(gridDim.x) * per_cta;
+    } else if constexpr (KIND == kCta) {
+        tm.T = static_cast<int>(blockDim.x);
+        tm.warps = tm.T >> 5;
+        t = static_cast<int>(threadIdx.x);
+        first = blockIdx.x;
+        stride = gridDim.x;
     } else {
         tm.T = static_cast<int>(blockDim.x);
         tm.warps = tm.T >> 5;
@@ -541,7 +532,7 @@ __global__ void __launch_bounds__(KIND > 0 ? 256 : 1024, KIND > 0 ? (CH == 4 ? 3
     ptx::grid_launch_dependents();
     int t;
     long long first, stride;
-    const Team tm = this_team<KIND>(static_cast<int>(blockDim.x), t, first, stride);
+    const Team tm = this_team<KIND>(t, first, stride);
     const Place<G, KIND, CH> pl(0, p.C, t);
     float4 *const my_gamma = params + t, *const my_beta = my_gamma + 2 * CH * tm.T;
     ptx::grid_dependency_wait();
@@ -721,31 +712,35 @@ struct NormGradParams {
     float *partial;            // [CTAs or clusters][2][C]: dgamma and dbeta sums of their rows, or nullptr
     long long R, C;
     long long groups;          // long kernels: element groups per row
-    int team_threads;          // kTeams: threads of a team
     long long slice_cols;      // kCluster: columns of each CTA
 };
 
 // Columns per thread over 8 (CH) and threads of a CTA: two 16-bit operands in
-// 16-byte groups leave room for 16 columns; rows of up to 256 columns take
-// one group per thread.
+// 16-byte groups leave room for 16 columns.
 constexpr int kGradThreads = 512;
 template <int ES, int DES, int G, int KIND>
-constexpr int kGradCh = (ES == 2 && DES == 2 && G == 8 && (KIND <= 0 || KIND == 32)) ? 2 : 1;
+constexpr int kGradCh = (ES == 2 && DES == 2 && G == 8 && KIND <= 0) ? 2 : 1;
 
 // Each thread keeps the dgamma and dbeta sums of its columns in registers over
-// all its rows; a CTA's teams then add theirs in order through shared memory.
+// all its rows; teams of lanes then add theirs in order through shared memory.
+// Teams of lanes: CTAs of 256 threads, 4 on an SM (3 where registers hold fp32 rows).
+constexpr int kGradLaneThreads = 256;
+template <int ES, int DES>
+constexpr int kGradLaneCtas = ES == 2 && DES == 2 ? 4 : 3;
+
 template <int ES, int DES, int G, int KIND, int CH>
-__global__ void __launch_bounds__(kGradThreads, 1) norm_grad_kernel(const NormGradParams p)
+__global__ void __launch_bounds__(KIND > 0 ? kGradLaneThreads : kGradThreads, KIND > 0 ? kGradLaneCtas<ES, DES> : 1)
+    norm_grad_kernel(const NormGradParams p)
 {
     constexpr int P = 4 * CH;
     __shared__ float red[2][kRedWords<KIND, 2>];
-    // gamma (keep_params); after the rows, the teams' sums meet here
-    __shared__ float4 params[kGradThreads * 2 * CH];
+    // gamma (keep_params: 2 CH float4s per thread); after the rows, the teams' sums meet here
+    extern __shared__ float4 params[];
     float *const cols = reinterpret_cast<float *>(params);
     ptx::grid_launch_dependents();
     int t;
     long long first, stride, begin = 0, end = p.C;
-    const Team tm = this_team<KIND>(p.team_threads, t, first, stride);
+    const Team tm = this_team<KIND>(t, first, stride);
     if constexpr (KIND == kCluster) {
         begin = min(p.C, tm.rank * p.slice_cols);
         end = min(p.C, begin + p.slice_cols);
@@ -858,36 +853,30 @@ __global__ void __launch_bounds__(kGradThreads, 1) norm_grad_kernel(const NormGr
                     for (int i = 0; i < 2 * P; ++i)
                         f[i] += __shfl_xor_sync(0xFFFFFFFFu, f[i], o);
             }
-            // then the teams (or warps of teams) in order
-            int teams = 1, mine = 0;
-            bool speaks = true;
+            bool writes = true;
             if constexpr (KIND > 0) {
-                teams = static_cast<int>(blockDim.x) / 32;
-                mine = static_cast<int>(threadIdx.x) >> 5;
-                speaks = static_cast<int>(threadIdx.x & 31) < KIND;
-            } else if constexpr (KIND == kTeams) {
-                teams = static_cast<int>(blockDim.x) / tm.T;
-                mine = tm.id;
-            }
-            if constexpr (KIND != kCluster) {
-                for (int m = 0; m + 1 < teams; ++m) {
+                // then the warps in order
+                const int warps = static_cast<int>(blockDim.x) / 32, warp = static_cast<int>(threadIdx.x) >> 5;
+                const bool speaks = static_cast<int>(threadIdx.x & 31) < KIND;
+                writes = speaks && warp == warps - 1;
+                for (int m = 0; m + 1 < warps; ++m) {
                     __syncthreads();
-                    if (mine == m && speaks) {
+                    if (warp == m && speaks) {
 #pragma unroll
                         for (int i = 0; i < 2 * P; ++i) {
-                            const int at = i * tm.T + t;
+                            const int at = i * KIND + t;
                             cols[at] = m == 0 ? f[i] : cols[at] + f[i];
                         }
                     }
                 }
                 __syncthreads();
-                if (teams > 1 && mine == teams - 1 && speaks) {
+                if (writes && warps > 1) {
 #pragma unroll
                     for (int i = 0; i < 2 * P; ++i)
-                        f[i] += cols[i * tm.T + t];
+                        f[i] += cols[i * KIND + t];
                 }
             }
-            if (mine == teams - 1 && speaks) {
+            if (writes) {
                 uint64_t v[P];
 #pragma unroll
                 for (int i = 0; i < P; ++i)

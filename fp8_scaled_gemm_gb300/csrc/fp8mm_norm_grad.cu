@@ -7,11 +7,16 @@ namespace {
 using namespace fp8mm_host;
 using fp8norm::NormGradParams;
 
-// CTAs per SM of the row kernels, and so of the partial sums.
-constexpr int kCtasPerSm = 2;
+// Threads of the row kernels on an SM (their registers allow 512), and so, at
+// 64 threads for the smallest CTA with a row of its own, CTAs and partial sums.
+constexpr int kMostPerSm = fp8norm::kGradThreads / 64;
+
+// Rows each team takes at least, where there are enough: a team's column sums
+// cost as much traffic as two to four rows.
+constexpr int kRowsPerTeam = 4;
 
 // Partial sums of dgamma and dbeta a call on R rows may write.
-int64_t max_partials(int64_t R, int sms) { return std::min<int64_t>(R, static_cast<int64_t>(sms) * kCtasPerSm); }
+int64_t max_partials(int64_t R, int sms) { return std::min<int64_t>(R, static_cast<int64_t>(sms) * kMostPerSm); }
 
 int sum_partials(const NormGradParams &p, int P, float *dgamma, float *dbeta, cudaStream_t stream)
 {
@@ -22,22 +27,32 @@ int sum_partials(const NormGradParams &p, int P, float *dgamma, float *dbeta, cu
     s.C = p.C;
     s.P = P;
     s.K = 2;
-    return launch_pdl(fp8rows::partial_sum_kernel, static_cast<int>(cdiv(p.C, 32)), fp8rows::kSumThreads, 0, stream,
-                      "parameter sum launch", s);
+    return launch_grid2(fp8rows::partial_sum_kernel, cdiv(p.C, 32), 2, fp8rows::kSumThreads, stream,
+                        "parameter sum launch", s);
 }
 
-// Teams of LANES lanes of a warp, or of some warps of a CTA: one CTA per SM,
-// so that few column sums are left to add.
-template <int ES, int DES, int G, int KIND>
-int launch_cta(NormGradParams p, int team, int sms, cudaStream_t stream, int *partials)
+// Teams of LANES lanes of a warp.
+template <int ES, int DES, int G, int LANES>
+int launch_lanes(const NormGradParams &p, int sms, cudaStream_t stream, int *partials)
 {
-    constexpr int most = fp8norm::kGradThreads;
-    p.team_threads = team;
-    const int teams = KIND > 0 ? most / team : std::min(most / team, 15);   // named barriers 1 .. 15
-    const int64_t grid = std::min<int64_t>(cdiv(p.R, teams), sms);
+    constexpr int CH = fp8norm::kGradCh<ES, DES, G, LANES>, threads = fp8norm::kGradLaneThreads;
+    const int64_t grid = std::min<int64_t>(cdiv(p.R, kRowsPerTeam * (threads / LANES)),
+                                           static_cast<int64_t>(sms) * fp8norm::kGradLaneCtas<ES, DES>);
     *partials = static_cast<int>(grid);
-    return launch_pdl(fp8norm::norm_grad_kernel<ES, DES, G, KIND, fp8norm::kGradCh<ES, DES, G, KIND>>,
-                      static_cast<int>(grid), teams * team, 0, stream, "layer norm gradient launch", p);
+    return launch_pdl(fp8norm::norm_grad_kernel<ES, DES, G, LANES, CH>, static_cast<int>(grid), threads,
+                      threads * 2 * 16 * CH, stream, "layer norm gradient launch", p);
+}
+
+// A CTA per row, as many of them on an SM as make 512 threads.
+template <int ES, int DES, int G>
+int launch_cta(const NormGradParams &p, int threads, int sms, cudaStream_t stream, int *partials)
+{
+    constexpr int CH = fp8norm::kGradCh<ES, DES, G, fp8norm::kCta>;
+    const int64_t grid = std::min<int64_t>(
+        cdiv(p.R, kRowsPerTeam), static_cast<int64_t>(sms) * std::min(kMostPerSm, fp8norm::kGradThreads / threads));
+    *partials = static_cast<int>(grid);
+    return launch_pdl(fp8norm::norm_grad_kernel<ES, DES, G, fp8norm::kCta, CH>, static_cast<int>(grid), threads,
+                      threads * 2 * 16 * CH, stream, "layer norm gradient launch", p);
 }
 
 // A cluster of `ctas` CTAs per row.
@@ -50,7 +65,8 @@ int launch_cluster(NormGradParams p, int ctas, int64_t slice_cols, int threads, 
     *partials = static_cast<int>(clusters);
     constexpr int CH = fp8norm::kGradCh<ES, DES, G, fp8norm::kCluster>;
     return launch_clusters(fp8norm::norm_grad_kernel<ES, DES, G, fp8norm::kCluster, CH>,
-                           static_cast<int>(clusters) * ctas, ctas, threads, stream, "layer norm gradient launch", p);
+                           static_cast<int>(clusters) * ctas, ctas, threads, threads * 2 * 16 * CH, stream,
+                           "layer norm gradient launch", p);
 }
 
 template <int ES, int DES, int G>
@@ -67,22 +83,18 @@ int launch_long(const NormGradParams &p, int sms, cudaStream_t stream, int *part
     const int64_t slabs = std::max<int64_t>(
         1, std::min<int64_t>(max_partials(p.R, sms), static_cast<int64_t>(sms) * 8 / strips));
     *partials = static_cast<int>(slabs);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(strips), static_cast<unsigned>(slabs), 1);
-    cfg.blockDim = dim3(256, 1, 1);
-    cfg.stream = stream;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8norm::norm_grad_cols_kernel<ES, DES, G>, p);
-    return e == cudaSuccess ? FP8MM_OK : cuda_fail(e, "layer norm parameter launch");
+    return launch_grid2(fp8norm::norm_grad_cols_kernel<ES, DES, G>, strips, slabs, 256, stream,
+                        "layer norm parameter launch", p);
 }
 
 template <int ES, int DES, int G>
 int launch_wide(const NormGradParams &p, int sms, cudaStream_t stream, int *P)
 {
-    constexpr int warp_cols = 32 * 8 * fp8norm::kGradCh<ES, DES, G, fp8norm::kTeams>;
+    constexpr int warp_cols = 32 * 8 * fp8norm::kGradCh<ES, DES, G, fp8norm::kCta>;
     constexpr int most = fp8norm::kGradThreads / 32;
     const int64_t warps = cdiv(p.C, warp_cols);
     if (warps <= most)
-        return launch_cta<ES, DES, G, fp8norm::kTeams>(p, static_cast<int>(warps) * 32, sms, stream, P);
+        return launch_cta<ES, DES, G>(p, static_cast<int>(warps) * 32, sms, stream, P);
     for (int ctas = 2; ctas <= fp8norm::kMaxCluster; ctas *= 2)
         if (warps <= most * ctas) {
             const int64_t each = cdiv(warps, ctas);
@@ -96,14 +108,14 @@ int launch(const NormGradParams &p, bool vec, int sms, cudaStream_t stream, int 
 {
     const int64_t C = p.C;
     if (vec) {
-        if (C <= 32) return launch_cta<ES, DES, 8, 4>(p, 4, sms, stream, P);
-        if (C <= 64) return launch_cta<ES, DES, 8, 8>(p, 8, sms, stream, P);
-        if (C <= 128) return launch_cta<ES, DES, 8, 16>(p, 16, sms, stream, P);
-        if (C <= 256 * fp8norm::kGradCh<ES, DES, 8, 32>) return launch_cta<ES, DES, 8, 32>(p, 32, sms, stream, P);
+        if (C <= 32) return launch_lanes<ES, DES, 8, 4>(p, sms, stream, P);
+        if (C <= 64) return launch_lanes<ES, DES, 8, 8>(p, sms, stream, P);
+        if (C <= 128) return launch_lanes<ES, DES, 8, 16>(p, sms, stream, P);
+        if (C <= 256) return launch_lanes<ES, DES, 8, 32>(p, sms, stream, P);
         return launch_wide<ES, DES, 8>(p, sms, stream, P);
     }
     if (C <= 256)
-        return launch_cta<ES, DES, 1, 32>(p, 32, sms, stream, P);
+        return launch_lanes<ES, DES, 1, 32>(p, sms, stream, P);
     return launch_wide<ES, DES, 1>(p, sms, stream, P);
 }
 

@@ -214,10 +214,10 @@ __device__ __forceinline__ float team_max(float v, float *red)
 }
 
 // ------------------------------------------------- sums of column partials ---
-// out_k[c] = sum over p < P of partial[(p * K + k) * C + c], k < K <= 2, in
-// the order of p within each of 8 interleaved chains that are then added in
-// order: the result depends on P and C only. One CTA per 32 columns; warp w
-// adds partials w, w + 8, ...
+// out_k[c] = sum over p < P of partial[(p * K + k) * C + c], k = blockIdx.y
+// < K <= 2. One CTA per 32 columns: warp w adds partials w, w + 32, ..., then
+// the 32 sums of a column are added over the lanes of one warp: the order
+// depends on P only.
 
 struct PartialSumParams {
     const float *partial;
@@ -226,32 +226,32 @@ struct PartialSumParams {
     int P, K;
 };
 
-constexpr int kSumThreads = 256;
+constexpr int kSumThreads = 1024;
 
 static __global__ void __launch_bounds__(kSumThreads) partial_sum_kernel(const PartialSumParams p)
 {
-    __shared__ float part[8][33];
+    __shared__ float part[32][33];
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = blockIdx.y;
     const long long c = static_cast<long long>(blockIdx.x) * 32 + lane;
-    for (int k = 0; k < p.K; ++k) {
-        float s = 0.0f;
-        if (c < p.C) {
+    float s = 0.0f;
+    if (c < p.C) {
+        const float *src = p.partial + (static_cast<long long>(warp) * p.K + k) * p.C + c;
+        const long long step = 32ll * p.K * p.C;
 #pragma unroll 8
-            for (int i = warp; i < p.P; i += 8)
-                s += __ldcg(p.partial + (static_cast<long long>(i) * p.K + k) * p.C + c);
-        }
-        part[warp][lane] = s;
-        __syncthreads();
-        if (warp == 0 && c < p.C) {
-#pragma unroll
-            for (int w = 1; w < 8; ++w)
-                s += part[w][lane];
-            (k == 0 ? p.out0 : p.out1)[c] = s;
-        }
-        __syncthreads();
+        for (int i = warp; i < p.P; i += 32, src += step)
+            s += __ldcg(src);
     }
+    part[warp][lane] = s;
+    __syncthreads();
+    s = part[lane][warp];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    const long long mine = static_cast<long long>(blockIdx.x) * 32 + warp;
+    if (lane == 0 && mine < p.C)
+        (k == 0 ? p.out0 : p.out1)[mine] = s;
 }
 
 }  // namespace fp8rows

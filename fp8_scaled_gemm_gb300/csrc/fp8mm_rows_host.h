@@ -29,4 +29,21 @@ inline bool rows_vec(const void *p, int64_t ld, int type)
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * row_type_bytes(type)) % 16 == 0;
 }
 
+// Launch on a two-dimensional grid with programmatic stream serialization.
+template <typename Kern, typename... Args>
+int launch_grid2(Kern kern, int64_t gx, int64_t gy, int threads, cudaStream_t stream, const char *what, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy), 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    return e == cudaSuccess ? FP8MM_OK : cuda_fail(e, what);
+}
+
 }  // namespace fp8mm_host
