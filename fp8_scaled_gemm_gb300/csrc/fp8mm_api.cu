@@ -790,7 +790,26 @@ int encode_and_dispatch(const Choice &c, const void *A, const void *B, void *out
     rc = cached_operand_map(&mq, swap ? A : B, swap ? M : N, K, q_box, batch);
     if (rc != FP8MM_OK)
         return rc;
-    return epi ? dispatch_epilogue(c, mp, mq, mo, kp, stream) : dispatch<false>(c, mp, mq, mo, kp, stream);
+    if (!epi)
+        return dispatch<false>(c, mp, mq, mo, kp, nullptr, stream);
+    // The row-major kernels move the epilogue's 16-bit matrices through TMA
+    // under the output's conditions.
+    fp8mm::EpiMaps<true> em;
+    std::memset(&em, 0, sizeof em);
+    if (!swap && out16 && c.split == 1 && (N % 8) == 0) {
+        const bool f16 = kp.out_type == FP8MM_OUT_F16;
+        if (kp.e.in && kp.e.vec_in) {
+            if ((rc = cached_out_map(&em.in, const_cast<void *>(kp.e.in), M, N, f16, 1, kp.e.ld_in)) != FP8MM_OK)
+                return rc;
+            kp.e.in_tma = 1;
+        }
+        if (kp.e.pre && kp.e.vec_pre) {
+            if ((rc = cached_out_map(&em.pre, kp.e.pre, M, N, f16, 1, kp.e.ld_pre)) != FP8MM_OK)
+                return rc;
+            kp.e.pre_tma = 1;
+        }
+    }
+    return dispatch_epilogue(c, mp, mq, mo, kp, em, stream);
 }
 
 int check_args(const void *A, const void *B, const float *sa, const float *sb, int scale_mode,

@@ -5,9 +5,9 @@
 namespace fp8mm_host {
 
 int dispatch_epilogue(const Choice &c, const CUtensorMap &mp, const CUtensorMap &mq, const CUtensorMap &mo,
-                      const fp8mm::KernelParams &kp, cudaStream_t stream)
+                      const fp8mm::KernelParams &kp, const fp8mm::EpiMaps<true> &em, cudaStream_t stream)
 {
-    return dispatch<true>(c, mp, mq, mo, kp, stream);
+    return dispatch<true>(c, mp, mq, mo, kp, &em, stream);
 }
 
 }  // namespace fp8mm_host

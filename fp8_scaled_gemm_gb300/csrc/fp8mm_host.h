@@ -10,6 +10,8 @@
 
 namespace fp8mm {
 struct KernelParams;
+template <bool EPI>
+struct EpiMaps;
 }
 
 namespace fp8mm_host {
@@ -39,7 +41,7 @@ struct Choice {
 // The launch of a chosen kernel with the extended epilogue
 // (KernelParams::e), compiled in a translation unit of its own.
 int dispatch_epilogue(const Choice &c, const CUtensorMap &mp, const CUtensorMap &mq, const CUtensorMap &mo,
-                      const fp8mm::KernelParams &kp, cudaStream_t stream);
+                      const fp8mm::KernelParams &kp, const fp8mm::EpiMaps<true> &em, cudaStream_t stream);
 
 // Launch with programmatic stream serialization: the kernel may start its
 // set-up while the previous kernel in the stream finishes; it calls

@@ -96,6 +96,15 @@ struct EpiParams {
     void *pre;                      // forward: where z goes; nullptr: nowhere
     long long ld_pre;
     int vec_in, vec_pre;            // 16-byte accesses allowed: base and row pitch aligned
+    int in_tma, pre_tma;            // EpiMaps::in / pre are valid: 16-bit blocks move through TMA
+};
+
+// Tensor maps of the extended epilogue's matrices, blocks as the output's.
+template <bool EPI>
+struct EpiMaps {};
+template <>
+struct EpiMaps<true> {
+    CUtensorMap in, pre;
 };
 
 // A batch of `batch` independent problems of one shape: operand tensor maps
@@ -137,7 +146,7 @@ struct KernelParams {
 // WIDE: the 256-wide row-major kernel with 16 epilogue warps (four per TMEM
 // lane quarter, one 64-column block each) for very shallow K, where the
 // epilogue, not the MMA, sets the time per tile.
-template <int BN, bool SWAP, bool WIDE = false>
+template <int BN, bool SWAP, bool WIDE = false, bool EPI = false>
 struct TileCfg {
     static_assert(!WIDE || (!SWAP && BN == 256), "the 16-warp epilogue is for the 256-wide row-major kernel");
     static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256, "MMA N for M=128 is 16..256 step 16");
@@ -153,17 +162,20 @@ struct TileCfg {
     static constexpr int kEpiWarps = SWAP ? 4 : (WIDE ? 16 : 8);
     static constexpr int kThreads = 64 + 32 * kEpiWarps;
     // 4 KB epilogue stages per warp (16 warps: one each, to fit the ring)
-    static constexpr int kStageBufs = (!SWAP && BN >= 256 && !WIDE) ? 2 : 1;
+    // (the extended epilogue: two, see epilogue_rows_ext)
+    static constexpr int kStageBufs = (!SWAP && (BN >= 256 || EPI) && !WIDE) ? 2 : 1;
     static constexpr int kPBytes = kTileP * kBlockK;
     static constexpr int kQBytes = BN * kBlockK;
     static constexpr int kStageBytes = kPBytes + kQBytes;
     static constexpr int kStageBufBytes = 4096;
     static constexpr int kStagingBytes = SWAP ? 0 : kEpiWarps * kStageBufBytes * kStageBufs;
     // per row-epilogue warp: one 64-column block's scales and biases (fp32)
-    static constexpr int kColBytes = SWAP ? 0 : kEpiWarps * 512;
+    static constexpr int kColBytes = SWAP || EPI ? 0 : kEpiWarps * 512;
     static constexpr int kTmemCols =
         (2 * BN <= 32) ? 32 : (2 * BN <= 64) ? 64 : (2 * BN <= 128) ? 128 : (2 * BN <= 256) ? 256 : 512;
-    static constexpr int kBarBytes = 256;
+    static constexpr int kBarBytes = 256;   // 8 (2 kStages + 6), and 8 x 2 per epilogue warp at +128 with EPI
+    static constexpr int kEpiBarOffset = 128;
+    static_assert(SWAP || 8 * (2 * kStages + 6) <= kEpiBarOffset, "barrier area");
     static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + kColBytes + kBarBytes;
     static constexpr int kChunk = BN < 32 ? BN : 32;   // TMEM columns per tcgen05.ld
     static_assert(kQBytes % 1024 == 0, "stage tiles must stay 1024-byte aligned");
@@ -546,30 +558,33 @@ __device__ __forceinline__ void epi_col(const KernelParams &p, float (&y)[CH], i
     }
 }
 
-// The same for four consecutive columns n .. n + 3 of row m < M.
-__device__ __forceinline__ void epi_quad(const KernelParams &p, float (&y)[4], int m, int n)
+// Four consecutive elements n .. n + 3 (n % 4 == 0) of row m < M of p.e.in; 0 past N.
+__device__ __forceinline__ void epi_load_quad(const KernelParams &p, int m, int n, float (&r)[4])
 {
-    float r[4] = {};
-    if (p.e.in != nullptr) {
-        const size_t at = static_cast<size_t>(m) * p.e.ld_in + n;
-        if (p.e.vec_in && n + 3 < p.N) {   // n % 4 == 0
-            if (p.out_type == kOutF32) {
-                const float4 x = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.e.in) + at);
-                r[0] = x.x;
-                r[1] = x.y;
-                r[2] = x.z;
-                r[3] = x.w;
-            } else {
-                const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const unsigned short *>(p.e.in) + at);
-                aux_unpack2(w.x, p.out_type == kOutF16, r[0], r[1]);
-                aux_unpack2(w.y, p.out_type == kOutF16, r[2], r[3]);
-            }
+    const size_t at = static_cast<size_t>(m) * p.e.ld_in + n;
+    if (p.e.vec_in && n + 3 < p.N) {
+        if (p.out_type == kOutF32) {
+            const float4 x = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.e.in) + at);
+            r[0] = x.x;
+            r[1] = x.y;
+            r[2] = x.z;
+            r[3] = x.w;
         } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                r[i] = n + i < p.N ? aux_load1(p, p.e.in, at + i) : 0.0f;
+            const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const unsigned short *>(p.e.in) + at);
+            aux_unpack2(w.x, p.out_type == kOutF16, r[0], r[1]);
+            aux_unpack2(w.y, p.out_type == kOutF16, r[2], r[3]);
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r[i] = n + i < p.N ? aux_load1(p, p.e.in, at + i) : 0.0f;
     }
+}
+
+// z values of four consecutive columns n .. n + 3 of row m < M to output
+// values; r holds p.e.in's (0 without).
+__device__ __forceinline__ void epi_quad(const KernelParams &p, float (&y)[4], int m, int n, const float (&r)[4])
+{
     if (p.e.grad) {
         apply_slope<4>(p.e.act, y, r);
         return;
@@ -950,7 +965,7 @@ __device__ __forceinline__ ColPre<BN> load_col_pre(const KernelParams &p, int n0
     return c;
 }
 
-template <int BN, int NBUF, bool EPI, bool PRE = false, bool FAST_PLAIN = false>
+template <int BN, int NBUF, bool PRE = false, bool FAST_PLAIN = false>
 __device__ __forceinline__ void epilogue_rows_staged(const KernelParams &p, const CUtensorMap *tmap_out,
                                                      uint32_t trow, int m_row0, int n0, int lane,
                                                      uint8_t *stage, uint32_t stage_smem, uint32_t &chunks,
@@ -958,7 +973,7 @@ __device__ __forceinline__ void epilogue_rows_staged(const KernelParams &p, cons
                                                      ColPre<BN> pre = ColPre<BN>{}, float *colv = nullptr)
 {
     if (p.out_type == kOutF32 || p.out_type == kOutE4M3) {
-        epilogue_rows_wide<BN, EPI>(p, trow, m_row0, n0, lane, s_tensor, add);
+        epilogue_rows_wide<BN, false>(p, trow, m_row0, n0, lane, s_tensor, add);
         return;
     }
     constexpr unsigned kAll = 0xffffffffu;
@@ -1034,19 +1049,7 @@ __device__ __forceinline__ void epilogue_rows_staged(const KernelParams &p, cons
                 }
             }
             uint32_t w[16];
-            if constexpr (EPI) {
-                // z of the half block, then the extended epilogue on it
-                float y[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const float s = p.rowwise ? sa * __shfl_sync(kAll, sbl2[h], j) : s_tensor;
-                    y[j] = fmaf(v[j], s, __shfl_sync(kAll, bl2[h], j));
-                }
-                epi_row<32>(p, y, m, nb + h * 32);
-#pragma unroll
-                for (int j = 0; j < 32; j += 2)
-                    w[j / 2] = pack_out2(y[j], y[j + 1], p.out_type);
-            } else if (colv != nullptr) {
+            if (colv != nullptr) {
                 convert_row32_any(p, v, w, p.rowwise ? sa : s_tensor, colv + h * 32, colv + 64 + h * 32);
             } else {
             const float sbl = sbl2[h];
@@ -1148,6 +1151,263 @@ __device__ __forceinline__ void epilogue_rows_staged(const KernelParams &p, cons
     }
 }
 
+// ------------------------------------- extended epilogue, row-major kernels ---
+//
+// The 16-bit matrices beside the output move like the output: 32 x 64 blocks
+// between global memory and a warp's two 4 KB buffers (128-byte swizzle, one
+// row per thread), by TMA when their rows are 16-byte aligned, otherwise by
+// element accesses of neighbouring lanes to neighbouring columns. (Loads and
+// stores of a thread's own row touched 32 lines per instruction: 8192 x 8192 x
+// 1024 gelu with residual and pre took 186 us, the plain product 61.)
+//
+// Buffers: `in` arrives in the one its block's output is built in. Without
+// `pre` the two alternate, and the next block's `in` is under way while a
+// block is worked on; with `pre` the second holds z. The first block's `in` is
+// asked for before the accumulator is waited for.
+struct EpiPipe {
+    uint32_t bar;        // two mbarriers of this warp: loads into buffer 0, 1
+    uint32_t phases;     // their phase bits
+    uint32_t seq;        // blocks done
+    uint32_t pending;    // loads in flight, by buffer
+};
+
+// Buffer of a block's output (and `in`).
+__device__ __forceinline__ uint32_t epi_buffer(const KernelParams &p, const EpiPipe &e, uint32_t ahead)
+{
+    return p.e.pre != nullptr ? 0u : ((e.seq + ahead) & 1u);
+}
+
+// Ask for a block of `in`. The stores out of the warp's buffers must have
+// read them, except those of the block that is being worked on.
+__device__ __forceinline__ void epi_fetch(const KernelParams &p, const EpiMaps<true> &maps, EpiPipe &e, uint32_t buf,
+                                          uint32_t stage_smem, int nb, int m_row0, int lane)
+{
+    if (lane == 0) {
+        ptx::bulk_wait_group_read<0>();
+        ptx::mbar_arrive_expect_tx(e.bar + 8u * buf, 4096u);
+        ptx::tma_load_3d(stage_smem + buf * 4096u, &maps.in, e.bar + 8u * buf, nb, m_row0, 0);
+    }
+    e.pending |= 1u << buf;
+    __syncwarp();
+}
+
+// A block of a [M, N] matrix of 16-bit elements whose rows are not 16-byte
+// aligned, to or from a buffer: lane l moves columns nb + 2l and nb + 2l + 1.
+__device__ __forceinline__ void epi_plain_load(const KernelParams &p, const void *base, long long ld, uint8_t *buf,
+                                               int m_row0, int nb, int lane)
+{
+    const int col = nb + 2 * lane, rows = min(32, p.M - m_row0);
+    const bool in0 = col < p.N, in1 = col + 1 < p.N;
+    const unsigned short *src = static_cast<const unsigned short *>(base) + static_cast<size_t>(m_row0) * ld + col;
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+        uint32_t lo = 0, hi = 0;
+        if (r < rows && in0)
+            lo = src[static_cast<size_t>(r) * ld];
+        if (r < rows && in1)
+            hi = src[static_cast<size_t>(r) * ld + 1];
+        *reinterpret_cast<uint32_t *>(buf + r * 128 + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4) = lo | (hi << 16);
+    }
+    __syncwarp();
+}
+
+__device__ __forceinline__ void epi_plain_store(const KernelParams &p, void *base, long long ld, const uint8_t *buf,
+                                                int m_row0, int nb, int lane)
+{
+    __syncwarp();
+    const int col = nb + 2 * lane, rows = min(32, p.M - m_row0);
+    const bool in0 = col < p.N, in1 = col + 1 < p.N;
+    unsigned short *dst = static_cast<unsigned short *>(base) + static_cast<size_t>(m_row0) * ld + col;
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+        const uint32_t w =
+            *reinterpret_cast<const uint32_t *>(buf + r * 128 + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4);
+        if (r < rows && in0)
+            dst[static_cast<size_t>(r) * ld] = static_cast<unsigned short>(w & 0xFFFFu);
+        if (r < rows && in1)
+            dst[static_cast<size_t>(r) * ld + 1] = static_cast<unsigned short>(w >> 16);
+    }
+    __syncwarp();
+}
+
+// Before the accumulator wait: the tile's first block of `in`.
+__device__ __forceinline__ void epi_begin_tile(const KernelParams &p, const EpiMaps<true> &maps, EpiPipe &e,
+                                               uint32_t stage_smem, int m_row0, int n0, int lane)
+{
+    if (p.e.in_tma)
+        epi_fetch(p, maps, e, epi_buffer(p, e, 0), stage_smem, n0, m_row0, lane);
+}
+
+// Loads still in flight land before the CTA may leave.
+__device__ __forceinline__ void epi_drain(const Waiter &W, EpiPipe &e)
+{
+#pragma unroll
+    for (uint32_t b = 0; b < 2; ++b)
+        if (e.pending >> b & 1u)
+            W.drain(e.bar + 8u * b, e.phases >> b & 1u, 9);
+}
+
+// The extended form of epilogue_rows_staged: one warp's 32 accumulator rows x
+// BN columns, 64 at a time. Returns false when a wait ran out.
+template <int BN>
+__device__ __forceinline__ bool epilogue_rows_ext(const KernelParams &p, const CUtensorMap *tmap_out,
+                                                  const EpiMaps<true> &maps, const Waiter &W, EpiPipe &e, uint32_t trow,
+                                                  int m_row0, int n0, int lane, uint8_t *stage, uint32_t stage_smem,
+                                                  float s_tensor, const PartialSrc add)
+{
+    if (p.out_type == kOutF32 || p.out_type == kOutE4M3) {
+        epilogue_rows_wide<BN, true>(p, trow, m_row0, n0, lane, s_tensor, add);
+        return true;
+    }
+    constexpr unsigned kAll = 0xffffffffu;
+    const int m = m_row0 + lane;
+    const float sa = (p.rowwise && m < p.M) ? __ldg(p.scale_a + m) : 0.0f;
+    const bool f16 = p.out_type == kOutF16, has_in = p.e.in != nullptr, has_pre = p.e.pre != nullptr;
+#pragma unroll 1
+    for (int c = 0; c < BN / 64; ++c) {
+        const int nb = n0 + c * 64;
+        const uint32_t buf = epi_buffer(p, e, 0);
+        if (p.e.in_tma && !has_pre && c + 1 < BN / 64)
+            epi_fetch(p, maps, e, epi_buffer(p, e, 1), stage_smem, nb + 64, m_row0, lane);
+        float sbl2[2] = {0.0f, 0.0f}, bl2[2] = {0.0f, 0.0f};
+        if (p.rowwise || p.bias != nullptr) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int nl = nb + h * 32 + lane;
+                const bool in = nl < p.N;
+                sbl2[h] = (p.rowwise && in) ? __ldg(p.scale_b + nl) : 0.0f;
+                bl2[h] = (p.bias != nullptr && in) ? bias_value(p, nl) : 0.0f;
+            }
+        }
+        uint8_t *const rowp = stage + buf * 4096u + lane * 128;
+        uint8_t *const rowq = stage + 4096 + lane * 128;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            const float sbl = h ? sbl2[1] : sbl2[0], bl = h ? bl2[1] : bl2[0];
+            float y[32];
+            ptx::tmem_ld_32cols(trow + static_cast<uint32_t>(c * 64 + h * 32), y);
+            for (int k = 0; k < add.count; ++k) {
+                const float4 *src = add.chunk(k, add.colt0 + c * 64 + h * 32);
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    const float4 x = add.ring == nullptr ? __ldcg(src + g * 128) : src[g * 128];
+                    y[4 * g] += x.x;
+                    y[4 * g + 1] += x.y;
+                    y[4 * g + 2] += x.z;
+                    y[4 * g + 3] += x.w;
+                }
+            }
+            // z = fma(acc, scale, bias), the plain epilogue's roundings
+            if (p.rowwise && p.bias != nullptr) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    y[j] = fmaf(y[j], sa * __shfl_sync(kAll, sbl, j), __shfl_sync(kAll, bl, j));
+            } else if (p.rowwise) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    y[j] *= sa * __shfl_sync(kAll, sbl, j);
+            } else if (p.bias != nullptr) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    y[j] = fmaf(y[j], s_tensor, __shfl_sync(kAll, bl, j));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    y[j] *= s_tensor;
+            }
+            if (h == 0) {
+                // the buffers are free: their last stores have read them. With
+                // a fetch of this block that wait came before the fetch.
+                if (!p.e.in_tma) {
+                    if (lane == 0) {
+                        if (has_pre || has_in)
+                            ptx::bulk_wait_group_read<0>();
+                        else
+                            ptx::bulk_wait_group_read<1>();
+                    }
+                    __syncwarp();
+                    if (has_in)
+                        epi_plain_load(p, p.e.in, p.e.ld_in, stage + buf * 4096u, m_row0, nb, lane);
+                } else {
+                    if (!W.wait(e.bar + 8u * buf, e.phases >> buf & 1u, 9))
+                        return false;
+                    e.pending &= ~(1u << buf);
+                    e.phases ^= 1u << buf;
+                }
+            }
+            auto chunk = [&](uint8_t *row, int i) {   // the thread's 16-byte chunk i of this half block
+                return reinterpret_cast<uint4 *>(row + (((h * 4 + i) ^ (lane & 7)) * 16));
+            };
+            auto pack8 = [&](int i) {
+                uint4 w;
+                w.x = pack_out2(y[8 * i], y[8 * i + 1], p.out_type);
+                w.y = pack_out2(y[8 * i + 2], y[8 * i + 3], p.out_type);
+                w.z = pack_out2(y[8 * i + 4], y[8 * i + 5], p.out_type);
+                w.w = pack_out2(y[8 * i + 6], y[8 * i + 7], p.out_type);
+                return w;
+            };
+            auto in8 = [&](int i, float (&r)[8]) {
+                const uint4 w = *chunk(rowp, i);
+                aux_unpack2(w.x, f16, r[0], r[1]);
+                aux_unpack2(w.y, f16, r[2], r[3]);
+                aux_unpack2(w.z, f16, r[4], r[5]);
+                aux_unpack2(w.w, f16, r[6], r[7]);
+            };
+            if (p.e.grad) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float r[8], v[8];
+                    in8(i, r);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[j] = y[8 * i + j];
+                    apply_slope<8>(p.e.act, v, r);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        y[8 * i + j] = v[j];
+                }
+            } else {
+                if (has_pre) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *chunk(rowq, i) = pack8(i);
+                }
+                apply_act<32>(p.e.act, y);
+                if (has_in) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float r[8];
+                        in8(i, r);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            y[8 * i + j] += r[j];
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *chunk(rowp, i) = pack8(i);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (p.out_tma)
+                ptx::tma_store_3d(tmap_out, stage_smem + buf * 4096u, nb, m_row0, 0);
+            if (p.e.pre_tma)
+                ptx::tma_store_3d(&maps.pre, stage_smem + 4096u, nb, m_row0, 0);
+            ptx::bulk_commit_group();
+        }
+        if (!p.out_tma)
+            epi_plain_store(p, p.out, p.ldo, stage + buf * 4096u, m_row0, nb, lane);
+        if (has_pre && !p.e.pre_tma)
+            epi_plain_store(p, p.e.pre, p.e.ld_pre, stage + 4096, m_row0, nb, lane);
+        ++e.seq;
+        if (p.e.in_tma && has_pre && c + 1 < BN / 64)
+            epi_fetch(p, maps, e, epi_buffer(p, e, 0), stage_smem, nb + 64, m_row0, lane);
+    }
+    return true;
+}
+
 template <int CH>
 __device__ __forceinline__ void tmem_load_chunk(uint32_t taddr, float (&v)[CH])
 {
@@ -1161,9 +1421,10 @@ template <int BN, bool SWAP, bool WIDE, bool EPI>
 __global__ void __launch_bounds__(TileCfg<BN, SWAP, WIDE>::kThreads, 1)
     fp8mm_tc_kernel(const __grid_constant__ CUtensorMap tmap_p,
                     const __grid_constant__ CUtensorMap tmap_q,
-                    const __grid_constant__ CUtensorMap tmap_out, const KernelParams p)
+                    const __grid_constant__ CUtensorMap tmap_out, const KernelParams p,
+                    const __grid_constant__ EpiMaps<EPI && !SWAP> epi_maps)
 {
-    using C = TileCfg<BN, SWAP, WIDE>;
+    using C = TileCfg<BN, SWAP, WIDE, EPI>;
     constexpr int CH = C::kChunk;
     constexpr int S = C::kStages;
     constexpr int kEpiWarps = C::kEpiWarps;
@@ -1201,6 +1462,9 @@ __global__ void __launch_bounds__(TileCfg<BN, SWAP, WIDE>::kThreads, 1)
             ptx::mbar_init(tempty_bar(a), 32 * kEpiWarps);
         }
         ptx::mbar_init(done_bar, 1);
+        if constexpr (EPI && !SWAP)
+            for (int i = 0; i < 2 * kEpiWarps; ++i)
+                ptx::mbar_init(bar0 + C::kEpiBarOffset + 8u * i, 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&tmap_p);
@@ -1324,6 +1588,7 @@ __global__ void __launch_bounds__(TileCfg<BN, SWAP, WIDE>::kThreads, 1)
         uint8_t *stage = smem + (staging0 - sbase) + ew * C::kStageBufBytes * C::kStageBufs;
         const uint32_t stage_smem = staging0 + static_cast<uint32_t>(ew * C::kStageBufBytes * C::kStageBufs);
         uint32_t chunks = 0;
+        EpiPipe pipe{bar0 + C::kEpiBarOffset + 16u * ew, 0, 0, 0};
         int acc = 0;
         uint32_t acc_phase = 0;
         // SWAP: the CTA's last tile is staged in the drained operand ring and
@@ -1351,7 +1616,11 @@ __global__ void __launch_bounds__(TileCfg<BN, SWAP, WIDE>::kThreads, 1)
             // TILE: this warp's column scales and biases for the tile, in flight
             // during the wait (per-tensor without bias has none to load)
             ColPre<kWarpCols> pre{};
-            if (!SWAP && p.splits == 1 && (p.rowwise || p.bias != nullptr))
+            if constexpr (EPI && !SWAP) {
+                if (p.splits == 1)
+                    epi_begin_tile(pb, epi_maps, pipe, stage_smem, w.tp * kTileP + q * 32, w.tq * BN + col0, lane);
+            }
+            if (!EPI && !SWAP && p.splits == 1 && (p.rowwise || p.bias != nullptr))
                 pre = load_col_pre<kWarpCols>(pb, w.tq * BN + col0, lane);
             if (!W.wait(tfull_bar(acc), acc_phase, 5))
                 break;
@@ -1359,10 +1628,15 @@ __global__ void __launch_bounds__(TileCfg<BN, SWAP, WIDE>::kThreads, 1)
             const uint32_t trow =
                 tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
             if (p.splits == 1) {
-                if constexpr (!SWAP) {
+                if constexpr (EPI && !SWAP) {
+                    if (!epilogue_rows_ext<kWarpCols>(pb, &tmap_out, epi_maps, W, pipe, trow + col0,
+                                                      w.tp * kTileP + q * 32, w.tq * BN + col0, lane, stage, stage_smem,
+                                                      s_tensor, PartialSrc{}))
+                        break;
+                } else if constexpr (!SWAP) {
                     // the grouped plain-store loop: the 256-wide kernels, which
                     // take the output-bound shallow-K launches
-                    epilogue_rows_staged<kWarpCols, C::kStageBufs, EPI, true, (BN >= 256)>(
+                    epilogue_rows_staged<kWarpCols, C::kStageBufs, true, (BN >= 256)>(
                         pb, &tmap_out, trow + col0, w.tp * kTileP + q * 32, w.tq * BN + col0, lane, stage,
                         stage_smem, chunks, s_tensor, w.b, PartialSrc{}, pre,
                         reinterpret_cast<float *>(smem + (colv0 - sbase)) + ew * 128);
@@ -1512,7 +1786,9 @@ __global__ void __launch_bounds__(TileCfg<BN, SWAP, WIDE>::kThreads, 1)
             }
         }
         // TMA stores must have finished reading the stage before the CTA exits
-        if (!SWAP && p.out_tma && lane == 0)
+        if constexpr (EPI && !SWAP)
+            epi_drain(W, pipe);
+        if (!SWAP && (EPI || p.out_tma) && lane == 0)
             ptx::bulk_wait_group_all();
         __syncwarp();
     }

@@ -254,6 +254,21 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
 
+        // The epilogue's inputs of this thread's columns, under way during the wait below
+        constexpr int kTurns = (C::kCols + 3) / 4;
+        float aux[EPI ? kTurns : 1][4] = {};
+        if constexpr (EPI) {
+            if (p.e.in != nullptr) {
+                const int t = threadIdx.x - 64;
+#pragma unroll
+                for (int i = 0; i < kTurns; ++i) {
+                    const int c = (t >> 5) + 4 * i, m = tq * BN + rank * C::kCols + c;
+                    if (c < C::kCols && m < p.M)
+                        epi_load_quad(p, m, tp * kTileP + 4 * (t & 31), aux[i]);
+                }
+            }
+        }
+
         // Every epilogue thread waits (bounded) for the peers' copies into this
         // CTA, even after an abort here: the peers send regardless, and the CTA
         // must not leave while those copies land in its shared memory.
@@ -266,8 +281,11 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(kThreads, 1)
             const int t = threadIdx.x - 64;                     // 0..127
             const int rl = 4 * (t & 31);                        // first of the lane's four tile rows
             const int n = tp * kTileP + rl;
-#pragma unroll 1
-            for (int c = t >> 5; c < C::kCols; c += 4) {
+#pragma unroll(EPI ? kTurns : 1)
+            for (int turn = 0; turn < kTurns; ++turn) {
+                const int c = (t >> 5) + 4 * turn;
+                if (c >= C::kCols)
+                    break;
                 const int col = rank * C::kCols + c;            // column of the tile
                 const int m = tq * BN + col;                    // its output row
                 if (m >= p.M)
@@ -294,7 +312,7 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 4; ++i)
                     y[i] = fmaf(y[i], pb.rowwise ? sa * red_sb[i] : red_stensor, red_bias[i]);
                 if constexpr (EPI)
-                    epi_quad(pb, y, m, n);
+                    epi_quad(pb, y, m, n, aux[turn]);
                 // (Staging these rows for one TMA store instead measured 3-5 %
                 // slower here: 16 and 128 x 4096 x 4096.)
                 store_out4(pb, m, n, y);

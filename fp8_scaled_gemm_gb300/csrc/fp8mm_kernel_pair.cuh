@@ -43,18 +43,21 @@
 
 namespace fp8mm {
 
-template <int BN, bool SWAP>
+template <int BN, bool SWAP, bool EPI = false>
 struct PairCfg {
     static_assert(SWAP ? (BN == 16 || BN == 32 || BN == 64 || BN == 128) : (BN == 256 || BN == 128),
                   "pair tile N");
     static constexpr int kABytes = 128 * kBlockK;             // this CTA's half of the P block
     static constexpr int kBBytes = (BN / 2) * kBlockK;        // this CTA's half of the Q block
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = SWAP ? 196608 / kStageBytes : 6;
+    // the extended epilogue trades a ring stage for a second buffer per warp
+    static constexpr int kStageBufs = EPI && !SWAP ? 2 : 1;
+    static constexpr int kStages = SWAP ? 196608 / kStageBytes : EPI ? 5 : 6;
     static constexpr int kTmemCols = (2 * BN < 32) ? 32 : 2 * BN;   // two fp32 accumulators
     static constexpr int kEpiWarps = EpiShape<SWAP>::kWarps;
-    static constexpr int kStagingBytes = SWAP ? 0 : kEpiWarps * 4096;   // 4 KB per row-epilogue warp
+    static constexpr int kStagingBytes = SWAP ? 0 : kEpiWarps * 4096 * kStageBufs;   // 4 KB buffers of the row-epilogue warps
     static constexpr int kBarBytes = 512;
+    static constexpr int kEpiBarOffset = 256;   // 8 x 2 per epilogue warp, with EPI
     static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + kBarBytes;
     static_assert(kBBytes % 1024 == 0, "stage tiles must stay 1024-byte aligned");
     static_assert(kSmemBytes <= 232448, "exceeds 227 KB of shared memory");
@@ -141,9 +144,10 @@ template <int BN, bool SWAP, bool EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThreads, 1)
     fp8mm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                       const __grid_constant__ CUtensorMap tmap_b,
-                      const __grid_constant__ CUtensorMap tmap_out, const KernelParams p)
+                      const __grid_constant__ CUtensorMap tmap_out, const KernelParams p,
+                      const __grid_constant__ EpiMaps<EPI && !SWAP> epi_maps)
 {
-    using C = PairCfg<BN, SWAP>;
+    using C = PairCfg<BN, SWAP, EPI>;
     constexpr int S = C::kStages;
     constexpr int kWarpCols = BN / (C::kEpiWarps / 4);   // columns of one epilogue warp
     constexpr int CH = BN < 32 ? BN : 32;
@@ -164,7 +168,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThr
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + (bar0 - sbase) + 8 * (2 * S + 5));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const uint32_t sk_bar = bar0 + 8u * (2 * S + 6);   // stream-K partial copied into the ring
-    static_assert(8 * (2 * S + 7) <= C::kBarBytes, "barrier area");
+    static_assert(8 * (2 * S + 7) <= (EPI && !SWAP ? C::kEpiBarOffset : C::kBarBytes), "barrier area");
+    static_assert(C::kEpiBarOffset + 16 * C::kEpiWarps <= C::kBarBytes, "epilogue barriers");
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -183,6 +188,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThr
         }
         ptx::mbar_init(done_bar, 1);
         ptx::mbar_init(sk_bar, 1);
+        if constexpr (EPI && !SWAP)
+            for (int i = 0; i < 2 * C::kEpiWarps; ++i)
+                ptx::mbar_init(bar0 + C::kEpiBarOffset + 8u * i, 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&tmap_a);
@@ -349,9 +357,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThr
         const int q = warp & 3;
         const int ew = warp - 2;
         const int col0 = (ew / 4) * kWarpCols;
-        uint8_t *stage = smem + (staging0 - sbase) + ew * 4096;
-        const uint32_t stage_smem = staging0 + static_cast<uint32_t>(ew * 4096);
+        uint8_t *stage = smem + (staging0 - sbase) + ew * 4096 * C::kStageBufs;
+        const uint32_t stage_smem = staging0 + static_cast<uint32_t>(ew * 4096 * C::kStageBufs);
         uint32_t chunks = 0;
+        EpiPipe pipe{bar0 + C::kEpiBarOffset + 16u * ew, 0, 0, 0};
         int acc = 0;
         uint32_t acc_phase = 0;
         PairSchedule sched(p, cluster_id, num_clusters);
@@ -362,6 +371,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThr
             kb_total += w.kb1 - w.kb0;
             const KernelParams pb = for_item(p, w.b);
             const float s_tensor = tensor_scale(pb);
+            if constexpr (EPI && !SWAP) {
+                if (pw.kind != 2 && p.splits == 1)
+                    epi_begin_tile(pb, epi_maps, pipe, stage_smem, w.tp * 256 + static_cast<int>(rank) * 128 + q * 32,
+                                   w.tq * BN + col0, lane);
+            }
             if (!W.wait(tfull_bar(acc), acc_phase, 5))
                 break;
             ptx::tc_fence_after();
@@ -422,10 +436,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThr
                         }
                         add.count = ok_all ? n_add : 0;
                     }
-                    epilogue_rows_staged<kWarpCols, 1, EPI>(pb, &tmap_out, trow + col0,
-                                                    w.tp * 256 + static_cast<int>(rank) * 128 + q * 32,
-                                                    w.tq * BN + col0, lane, stage, stage_smem, chunks, s_tensor,
-                                                    w.b, add);
+                    if constexpr (EPI) {
+                        // a wait that ran out leaves the flags to fp8mm_device_status
+                        if (!epilogue_rows_ext<kWarpCols>(pb, &tmap_out, epi_maps, W, pipe, trow + col0,
+                                                          w.tp * 256 + static_cast<int>(rank) * 128 + q * 32,
+                                                          w.tq * BN + col0, lane, stage, stage_smem, s_tensor, add))
+                            break;
+                    } else {
+                        epilogue_rows_staged<kWarpCols, 1>(pb, &tmap_out, trow + col0,
+                                                        w.tp * 256 + static_cast<int>(rank) * 128 + q * 32,
+                                                        w.tq * BN + col0, lane, stage, stage_smem, chunks, s_tensor,
+                                                        w.b, add);
+                    }
                     if (pw.kind == 1) {
                         __syncwarp();
                         if (lane == 0)
@@ -530,7 +552,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThr
                 acc_phase ^= 1u;
             }
         }
-        if (!SWAP && p.out_tma && lane == 0)
+        if constexpr (EPI && !SWAP)
+            epi_drain(W, pipe);
+        if (!SWAP && (EPI || p.out_tma) && lane == 0)
             ptx::bulk_wait_group_all();
         __syncwarp();
     }

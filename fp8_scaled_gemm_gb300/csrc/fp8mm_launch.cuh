@@ -19,6 +19,16 @@ namespace fp8mm_host {
 // 141.1, 4096 x 4096 x 1024 21.3 -> 23.2).
 constexpr int64_t kTileWideMaxK = 512;
 
+// A kernel's argument of the extended epilogue's tensor maps.
+template <bool EPI>
+fp8mm::EpiMaps<EPI> maps_for(const fp8mm::EpiMaps<true> *em)
+{
+    if constexpr (EPI)
+        return *em;
+    else
+        return {};
+}
+
 template <int BN, int CS, bool EPI>
 int launch_swapk(const CUtensorMap &mp, const CUtensorMap &mq, const fp8mm::KernelParams &kp, int grid,
                  cudaStream_t stream)
@@ -39,9 +49,9 @@ int launch_swapk(const CUtensorMap &mp, const CUtensorMap &mq, const fp8mm::Kern
 
 template <int BN, bool SWAP, bool WIDE, bool EPI>
 int launch_kernel(const CUtensorMap &mp, const CUtensorMap &mq, const CUtensorMap &mo,
-                  const fp8mm::KernelParams &kp, int grid, cudaStream_t stream)
+                  const fp8mm::KernelParams &kp, const fp8mm::EpiMaps<true> *em, int grid, cudaStream_t stream)
 {
-    using C = fp8mm::TileCfg<BN, SWAP, WIDE>;
+    using C = fp8mm::TileCfg<BN, SWAP, WIDE, EPI>;
     auto kern = fp8mm::fp8mm_tc_kernel<BN, SWAP, WIDE, EPI>;
     static bool attr_set[kMaxDevices] = {};
     int dev = 0;
@@ -53,14 +63,14 @@ int launch_kernel(const CUtensorMap &mp, const CUtensorMap &mq, const CUtensorMa
         attr_set[dev] = true;
     }
     return launch_pdl(kern, grid, C::kThreads, C::kSmemBytes, stream, "kernel launch", mp, mq,
-                      mo, kp);
+                      mo, kp, maps_for<EPI && !SWAP>(em));
 }
 
 template <int BN, bool SWAP, bool EPI>
 int launch_pair(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo,
-                const fp8mm::KernelParams &kp, int grid, cudaStream_t stream)
+                const fp8mm::KernelParams &kp, const fp8mm::EpiMaps<true> *em, int grid, cudaStream_t stream)
 {
-    using C = fp8mm::PairCfg<BN, SWAP>;
+    using C = fp8mm::PairCfg<BN, SWAP, EPI>;
     auto kern = fp8mm::fp8mm_pair_kernel<BN, SWAP, EPI>;
     static bool attr_set[kMaxDevices] = {};
     int dev = 0;
@@ -72,12 +82,12 @@ int launch_pair(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap 
         attr_set[dev] = true;
     }
     return launch_pdl(kern, grid, fp8mm::EpiShape<SWAP>::kThreads, C::kSmemBytes, stream, "pair kernel launch",
-                      ma, mb, mo, kp);
+                      ma, mb, mo, kp, maps_for<EPI && !SWAP>(em));
 }
 
 template <bool EPI>
 int dispatch(const Choice &c, const CUtensorMap &mp, const CUtensorMap &mq, const CUtensorMap &mo,
-             const fp8mm::KernelParams &kp, cudaStream_t stream)
+             const fp8mm::KernelParams &kp, const fp8mm::EpiMaps<true> *em, cudaStream_t stream)
 {
     if (c.variant == FP8MM_VARIANT_SWAPK) {
         switch (c.tile_n * 10 + c.split) {
@@ -98,32 +108,35 @@ int dispatch(const Choice &c, const CUtensorMap &mp, const CUtensorMap &mq, cons
     }
     if (c.variant == FP8MM_VARIANT_PAIR) {
         switch (c.tile_n) {
-        case 128: return launch_pair<128, false, EPI>(mp, mq, mo, kp, c.grid, stream);
-        case 256: return launch_pair<256, false, EPI>(mp, mq, mo, kp, c.grid, stream);
+        case 128: return launch_pair<128, false, EPI>(mp, mq, mo, kp, em, c.grid, stream);
+        case 256: return launch_pair<256, false, EPI>(mp, mq, mo, kp, em, c.grid, stream);
         }
     } else if (c.variant == FP8MM_VARIANT_SWAPPAIR) {
         switch (c.tile_n) {
-        case 16: return launch_pair<16, true, EPI>(mp, mq, mo, kp, c.grid, stream);
-        case 32: return launch_pair<32, true, EPI>(mp, mq, mo, kp, c.grid, stream);
-        case 64: return launch_pair<64, true, EPI>(mp, mq, mo, kp, c.grid, stream);
-        case 128: return launch_pair<128, true, EPI>(mp, mq, mo, kp, c.grid, stream);
+        case 16: return launch_pair<16, true, EPI>(mp, mq, mo, kp, em, c.grid, stream);
+        case 32: return launch_pair<32, true, EPI>(mp, mq, mo, kp, em, c.grid, stream);
+        case 64: return launch_pair<64, true, EPI>(mp, mq, mo, kp, em, c.grid, stream);
+        case 128: return launch_pair<128, true, EPI>(mp, mq, mo, kp, em, c.grid, stream);
         }
     } else if (c.variant == FP8MM_VARIANT_TILE) {
         switch (c.tile_n) {
-        case 128: return launch_kernel<128, false, false, EPI>(mp, mq, mo, kp, c.grid, stream);
+        case 128: return launch_kernel<128, false, false, EPI>(mp, mq, mo, kp, em, c.grid, stream);
         case 256:
             // shallow K: 16 epilogue warps (the epilogue sets the time per
             // tile); deeper K keeps 8 and two stage buffers per warp
-            if (kp.K <= kTileWideMaxK)
-                return launch_kernel<256, false, true, EPI>(mp, mq, mo, kp, c.grid, stream);
-            return launch_kernel<256, false, false, EPI>(mp, mq, mo, kp, c.grid, stream);
+            // (the extended epilogue has two buffers per warp: 8 warps)
+            if constexpr (!EPI) {
+                if (kp.K <= kTileWideMaxK)
+                    return launch_kernel<256, false, true, EPI>(mp, mq, mo, kp, em, c.grid, stream);
+            }
+            return launch_kernel<256, false, false, EPI>(mp, mq, mo, kp, em, c.grid, stream);
         }
     } else {
         switch (c.tile_n) {
-        case 16: return launch_kernel<16, true, false, EPI>(mp, mq, mo, kp, c.grid, stream);
-        case 32: return launch_kernel<32, true, false, EPI>(mp, mq, mo, kp, c.grid, stream);
-        case 64: return launch_kernel<64, true, false, EPI>(mp, mq, mo, kp, c.grid, stream);
-        case 128: return launch_kernel<128, true, false, EPI>(mp, mq, mo, kp, c.grid, stream);
+        case 16: return launch_kernel<16, true, false, EPI>(mp, mq, mo, kp, em, c.grid, stream);
+        case 32: return launch_kernel<32, true, false, EPI>(mp, mq, mo, kp, em, c.grid, stream);
+        case 64: return launch_kernel<64, true, false, EPI>(mp, mq, mo, kp, em, c.grid, stream);
+        case 128: return launch_kernel<128, true, false, EPI>(mp, mq, mo, kp, em, c.grid, stream);
         }
     }
     return FP8MM_ERR_MODE;
