@@ -234,16 +234,19 @@ int encode_operand_map(CUtensorMap *map, const void *base, int64_t rows, int64_t
 }
 
 // 16-bit output [batch, M, N] (N contiguous) written in boxes of 32 rows x
-// 64 columns of one item from a 128-byte-swizzled shared-memory stage.
-int encode_out_map(CUtensorMap *map, void *out, int64_t M, int64_t N, bool f16, int64_t batch, int64_t ldo)
+// box_n columns of one item from a swizzled shared-memory stage: 64 columns
+// (128-byte swizzle), or 32 (64-byte) for the matrices of the extended
+// epilogue.
+int encode_out_map(CUtensorMap *map, void *out, int64_t M, int64_t N, bool f16, int64_t batch, int64_t ldo, int box_n)
 {
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M), static_cast<cuuint64_t>(batch)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(ldo) * 2, static_cast<cuuint64_t>(ldo) * 2 * static_cast<cuuint64_t>(M)};
-    cuuint32_t box[3] = {64, 32, 1};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(box_n), 32, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = g_encode(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, out,
                           dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          box_n == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         char buf[128];
@@ -322,14 +325,14 @@ int cached_operand_map(CUtensorMap *map, const void *base, int64_t rows, int64_t
     return rc;
 }
 
-int cached_out_map(CUtensorMap *map, void *out, int64_t M, int64_t N, bool f16, int64_t batch, int64_t ldo)
+int cached_out_map(CUtensorMap *map, void *out, int64_t M, int64_t N, bool f16, int64_t batch, int64_t ldo, int box_n = 64)
 {
-    const MapKey k{current_device(), f16 ? 2 : 1, out, M, N, batch, ldo, 32};
+    const MapKey k{current_device(), f16 ? 2 : 1, out, M, N, batch, ldo, box_n};
     if (const CUtensorMap *m = map_lookup(k)) {
         *map = *m;
         return FP8MM_OK;
     }
-    const int rc = encode_out_map(map, out, M, N, f16, batch, ldo);
+    const int rc = encode_out_map(map, out, M, N, f16, batch, ldo, box_n);
     if (rc == FP8MM_OK)
         map_insert(k, *map);
     return rc;
@@ -760,7 +763,7 @@ int encode_and_dispatch(const Choice &c, const void *A, const void *B, void *out
     const bool out16 = kp.out_type == FP8MM_OUT_BF16 || kp.out_type == FP8MM_OUT_F16;
     if (!swap && out16 && c.split == 1 && (N % 8) == 0 && (kp.ldo % 8) == 0 &&
         (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
-        int rc = cached_out_map(&mo, out, M, N, kp.out_type == FP8MM_OUT_F16, batch, kp.ldo);
+        int rc = cached_out_map(&mo, out, M, N, kp.out_type == FP8MM_OUT_F16, batch, kp.ldo, epi ? 32 : 64);
         if (rc != FP8MM_OK)
             return rc;
         kp.out_tma = 1;
@@ -799,12 +802,12 @@ int encode_and_dispatch(const Choice &c, const void *A, const void *B, void *out
     if (!swap && out16 && c.split == 1 && (N % 8) == 0) {
         const bool f16 = kp.out_type == FP8MM_OUT_F16;
         if (kp.e.in && kp.e.vec_in) {
-            if ((rc = cached_out_map(&em.in, const_cast<void *>(kp.e.in), M, N, f16, 1, kp.e.ld_in)) != FP8MM_OK)
+            if ((rc = cached_out_map(&em.in, const_cast<void *>(kp.e.in), M, N, f16, 1, kp.e.ld_in, 32)) != FP8MM_OK)
                 return rc;
             kp.e.in_tma = 1;
         }
         if (kp.e.pre && kp.e.vec_pre) {
-            if ((rc = cached_out_map(&em.pre, kp.e.pre, M, N, f16, 1, kp.e.ld_pre)) != FP8MM_OK)
+            if ((rc = cached_out_map(&em.pre, kp.e.pre, M, N, f16, 1, kp.e.ld_pre, 32)) != FP8MM_OK)
                 return rc;
             kp.e.pre_tma = 1;
         }

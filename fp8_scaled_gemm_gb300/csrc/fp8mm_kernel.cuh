@@ -158,12 +158,12 @@ struct TileCfg {
     // the epilogue dominates: 3 stages leave room for two stage buffers per
     // epilogue warp.
     static constexpr int kStages = SWAP ? (BN >= 128 ? 6 : BN >= 64 ? 4 : BN >= 32 ? 5 : 6)
-                                        : (BN >= 256 ? 3 : 5);
+                                        : (BN >= 256 ? (WIDE && EPI ? 2 : 3) : 5);
     static constexpr int kEpiWarps = SWAP ? 4 : (WIDE ? 16 : 8);
     static constexpr int kThreads = 64 + 32 * kEpiWarps;
     // 4 KB epilogue stages per warp (16 warps: one each, to fit the ring)
-    // (the extended epilogue: two, see epilogue_rows_ext)
-    static constexpr int kStageBufs = (!SWAP && (BN >= 256 || EPI) && !WIDE) ? 2 : 1;
+    // (the extended epilogue: 8 KB in four buffers, see epilogue_rows_ext)
+    static constexpr int kStageBufs = !SWAP && (EPI || (BN >= 256 && !WIDE)) ? 2 : 1;
     static constexpr int kPBytes = kTileP * kBlockK;
     static constexpr int kQBytes = BN * kBlockK;
     static constexpr int kStageBytes = kPBytes + kQBytes;
@@ -173,8 +173,8 @@ struct TileCfg {
     static constexpr int kColBytes = SWAP || EPI ? 0 : kEpiWarps * 512;
     static constexpr int kTmemCols =
         (2 * BN <= 32) ? 32 : (2 * BN <= 64) ? 64 : (2 * BN <= 128) ? 128 : (2 * BN <= 256) ? 256 : 512;
-    static constexpr int kBarBytes = 256;   // 8 (2 kStages + 6), and 8 x 2 per epilogue warp at +128 with EPI
-    static constexpr int kEpiBarOffset = 128;
+    static constexpr int kEpiBarOffset = 128;   // EPI: four barriers per epilogue warp
+    static constexpr int kBarBytes = EPI && !SWAP ? kEpiBarOffset + 32 * kEpiWarps : 256;
     static_assert(SWAP || 8 * (2 * kStages + 6) <= kEpiBarOffset, "barrier area");
     static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + kColBytes + kBarBytes;
     static constexpr int kChunk = BN < 32 ? BN : 32;   // TMEM columns per tcgen05.ld
@@ -581,34 +581,23 @@ __device__ __forceinline__ void epi_load_quad(const KernelParams &p, int m, int 
     }
 }
 
-// z values of four consecutive columns n .. n + 3 of row m < M to output
-// values; r holds p.e.in's (0 without).
-__device__ __forceinline__ void epi_quad(const KernelParams &p, float (&y)[4], int m, int n, const float (&r)[4])
+// Four consecutive z values of row m < M to p.e.pre.
+__device__ __forceinline__ void epi_store_quad(const KernelParams &p, int m, int n, float a, float b, float c, float d)
 {
-    if (p.e.grad) {
-        apply_slope<4>(p.e.act, y, r);
-        return;
-    }
-    if (p.e.pre != nullptr) {
-        const size_t at = static_cast<size_t>(m) * p.e.ld_pre + n;
-        if (p.e.vec_pre && n + 3 < p.N) {
-            if (p.out_type == kOutF32) {
-                *reinterpret_cast<float4 *>(static_cast<float *>(p.e.pre) + at) = make_float4(y[0], y[1], y[2], y[3]);
-            } else {
-                *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(p.e.pre) + at) =
-                    make_uint2(pack_out2(y[0], y[1], p.out_type), pack_out2(y[2], y[3], p.out_type));
-            }
-        } else {
+    const size_t at = static_cast<size_t>(m) * p.e.ld_pre + n;
+    if (p.e.vec_pre && n + 3 < p.N) {
+        if (p.out_type == kOutF32)
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.e.pre) + at) = make_float4(a, b, c, d);
+        else
+            *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(p.e.pre) + at) =
+                make_uint2(pack_out2(a, b, p.out_type), pack_out2(c, d, p.out_type));
+    } else {
+        const float y[4] = {a, b, c, d};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (n + i < p.N)
-                    aux_store1(p, p.e.pre, at + i, y[i]);
-        }
+        for (int i = 0; i < 4; ++i)
+            if (n + i < p.N)
+                aux_store1(p, p.e.pre, at + i, y[i]);
     }
-    apply_act<4>(p.e.act, y);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        y[i] += r[i];
 }
 
 // CH consecutive values of output row m from column n0, for the fp32 and
@@ -1153,60 +1142,71 @@ __device__ __forceinline__ void epilogue_rows_staged(const KernelParams &p, cons
 
 // ------------------------------------- extended epilogue, row-major kernels ---
 //
-// The 16-bit matrices beside the output move like the output: 32 x 64 blocks
-// between global memory and a warp's two 4 KB buffers (128-byte swizzle, one
-// row per thread), by TMA when their rows are 16-byte aligned, otherwise by
-// element accesses of neighbouring lanes to neighbouring columns. (Loads and
-// stores of a thread's own row touched 32 lines per instruction: 8192 x 8192 x
-// 1024 gelu with residual and pre took 186 us, the plain product 61.)
+// The 16-bit matrices beside the output move like the output: 32 x 32 blocks
+// between global memory and a warp's four 2 KB buffers (one 64-byte row per
+// thread, 64-byte swizzle: the eight threads of a quarter-warp hit distinct
+// banks), by TMA when their rows are 16-byte aligned, otherwise by element
+// accesses of neighbouring lanes to neighbouring columns. (Loads and stores of
+// a thread's own row touched 32 lines per instruction: 8192 x 8192 x 1024 gelu
+// with residual and z took 186 us; 32 x 64 blocks in two buffers, with z
+// nothing under way ahead, 144.)
 //
-// Buffers: `in` arrives in the one its block's output is built in. Without
-// `pre` the two alternate, and the next block's `in` is under way while a
-// block is worked on; with `pre` the second holds z. The first block's `in` is
+// `in` arrives in the buffer its block's output is built in. Without z the
+// four buffers go round and two blocks of `in` are under way ahead; with z
+// they make two pairs (output, z) and one block is. The first blocks' `in` is
 // asked for before the accumulator is waited for.
 struct EpiPipe {
-    uint32_t bar;        // two mbarriers of this warp: loads into buffer 0, 1
+    uint32_t bar;        // four mbarriers of this warp: loads into its buffers
     uint32_t phases;     // their phase bits
     uint32_t seq;        // blocks done
     uint32_t pending;    // loads in flight, by buffer
 };
 
-// Buffer of a block's output (and `in`).
+constexpr uint32_t kEpiBuf = 2048;
+
+// Buffer of the output (and `in`) of the block `ahead` blocks from now; z's is
+// the next one.
 __device__ __forceinline__ uint32_t epi_buffer(const KernelParams &p, const EpiPipe &e, uint32_t ahead)
 {
-    return p.e.pre != nullptr ? 0u : ((e.seq + ahead) & 1u);
+    return p.e.pre != nullptr ? ((e.seq + ahead) & 1u) * 2u : ((e.seq + ahead) & 3u);
 }
 
-// Ask for a block of `in`. The stores out of the warp's buffers must have
-// read them, except those of the block that is being worked on.
-__device__ __forceinline__ void epi_fetch(const KernelParams &p, const EpiMaps<true> &maps, EpiPipe &e, uint32_t buf,
+// Blocks of `in` under way ahead of the one that is worked on.
+__device__ __forceinline__ int epi_ahead(const KernelParams &p) { return p.e.pre != nullptr ? 1 : 2; }
+
+// Ask for a block of `in`, `ahead` blocks from now. The last stores out of its
+// buffers have read them: those of the previous block with pairs, of the one
+// before without (one younger group may still read).
+__device__ __forceinline__ void epi_fetch(const KernelParams &p, const EpiMaps<true> &maps, EpiPipe &e, uint32_t ahead,
                                           uint32_t stage_smem, int nb, int m_row0, int lane)
 {
+    const uint32_t buf = epi_buffer(p, e, ahead);
     if (lane == 0) {
-        ptx::bulk_wait_group_read<0>();
-        ptx::mbar_arrive_expect_tx(e.bar + 8u * buf, 4096u);
-        ptx::tma_load_3d(stage_smem + buf * 4096u, &maps.in, e.bar + 8u * buf, nb, m_row0, 0);
+        if (p.e.pre != nullptr)
+            ptx::bulk_wait_group_read<0>();
+        else
+            ptx::bulk_wait_group_read<1>();
+        ptx::mbar_arrive_expect_tx(e.bar + 8u * buf, kEpiBuf);
+        ptx::tma_load_3d(stage_smem + buf * kEpiBuf, &maps.in, e.bar + 8u * buf, nb, m_row0, 0);
     }
     e.pending |= 1u << buf;
     __syncwarp();
 }
 
+// Byte offset of 16-byte chunk i of row r of a buffer.
+__device__ __forceinline__ int epi_chunk(int r, int i) { return r * 64 + ((i ^ ((r >> 1) & 3)) * 16); }
+
 // A block of a [M, N] matrix of 16-bit elements whose rows are not 16-byte
-// aligned, to or from a buffer: lane l moves columns nb + 2l and nb + 2l + 1.
+// aligned, to or from a buffer: lane l moves column nb + l.
 __device__ __forceinline__ void epi_plain_load(const KernelParams &p, const void *base, long long ld, uint8_t *buf,
                                                int m_row0, int nb, int lane)
 {
-    const int col = nb + 2 * lane, rows = min(32, p.M - m_row0);
-    const bool in0 = col < p.N, in1 = col + 1 < p.N;
+    const int col = nb + lane, rows = col < p.N ? min(32, p.M - m_row0) : 0;
     const unsigned short *src = static_cast<const unsigned short *>(base) + static_cast<size_t>(m_row0) * ld + col;
-#pragma unroll 8
+#pragma unroll 16
     for (int r = 0; r < 32; ++r) {
-        uint32_t lo = 0, hi = 0;
-        if (r < rows && in0)
-            lo = src[static_cast<size_t>(r) * ld];
-        if (r < rows && in1)
-            hi = src[static_cast<size_t>(r) * ld + 1];
-        *reinterpret_cast<uint32_t *>(buf + r * 128 + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4) = lo | (hi << 16);
+        const unsigned short v = r < rows ? src[static_cast<size_t>(r) * ld] : static_cast<unsigned short>(0);
+        *reinterpret_cast<unsigned short *>(buf + epi_chunk(r, lane >> 3) + (lane & 7) * 2) = v;
     }
     __syncwarp();
 }
@@ -1214,41 +1214,36 @@ __device__ __forceinline__ void epi_plain_load(const KernelParams &p, const void
 __device__ __forceinline__ void epi_plain_store(const KernelParams &p, void *base, long long ld, const uint8_t *buf,
                                                 int m_row0, int nb, int lane)
 {
-    __syncwarp();
-    const int col = nb + 2 * lane, rows = min(32, p.M - m_row0);
-    const bool in0 = col < p.N, in1 = col + 1 < p.N;
+    const int col = nb + lane, rows = col < p.N ? min(32, p.M - m_row0) : 0;
     unsigned short *dst = static_cast<unsigned short *>(base) + static_cast<size_t>(m_row0) * ld + col;
-#pragma unroll 8
+#pragma unroll 16
     for (int r = 0; r < 32; ++r) {
-        const uint32_t w =
-            *reinterpret_cast<const uint32_t *>(buf + r * 128 + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4);
-        if (r < rows && in0)
-            dst[static_cast<size_t>(r) * ld] = static_cast<unsigned short>(w & 0xFFFFu);
-        if (r < rows && in1)
-            dst[static_cast<size_t>(r) * ld + 1] = static_cast<unsigned short>(w >> 16);
+        const unsigned short v = *reinterpret_cast<const unsigned short *>(buf + epi_chunk(r, lane >> 3) + (lane & 7) * 2);
+        if (r < rows)
+            dst[static_cast<size_t>(r) * ld] = v;
     }
-    __syncwarp();
 }
 
-// Before the accumulator wait: the tile's first block of `in`.
+// Before the accumulator wait: the tile's first blocks of `in`.
 __device__ __forceinline__ void epi_begin_tile(const KernelParams &p, const EpiMaps<true> &maps, EpiPipe &e,
                                                uint32_t stage_smem, int m_row0, int n0, int lane)
 {
     if (p.e.in_tma)
-        epi_fetch(p, maps, e, epi_buffer(p, e, 0), stage_smem, n0, m_row0, lane);
+        for (int b = 0; b < epi_ahead(p); ++b)
+            epi_fetch(p, maps, e, b, stage_smem, n0 + 32 * b, m_row0, lane);
 }
 
 // Loads still in flight land before the CTA may leave.
 __device__ __forceinline__ void epi_drain(const Waiter &W, EpiPipe &e)
 {
 #pragma unroll
-    for (uint32_t b = 0; b < 2; ++b)
+    for (uint32_t b = 0; b < 4; ++b)
         if (e.pending >> b & 1u)
             W.drain(e.bar + 8u * b, e.phases >> b & 1u, 9);
 }
 
 // The extended form of epilogue_rows_staged: one warp's 32 accumulator rows x
-// BN columns, 64 at a time. Returns false when a wait ran out.
+// BN columns, 32 at a time. Returns false when a wait ran out.
 template <int BN>
 __device__ __forceinline__ bool epilogue_rows_ext(const KernelParams &p, const CUtensorMap *tmap_out,
                                                   const EpiMaps<true> &maps, const Waiter &W, EpiPipe &e, uint32_t trow,
@@ -1263,147 +1258,131 @@ __device__ __forceinline__ bool epilogue_rows_ext(const KernelParams &p, const C
     const int m = m_row0 + lane;
     const float sa = (p.rowwise && m < p.M) ? __ldg(p.scale_a + m) : 0.0f;
     const bool f16 = p.out_type == kOutF16, has_in = p.e.in != nullptr, has_pre = p.e.pre != nullptr;
+    const int ahead = epi_ahead(p);
 #pragma unroll 1
-    for (int c = 0; c < BN / 64; ++c) {
-        const int nb = n0 + c * 64;
+    for (int c = 0; c < BN / 32; ++c) {
+        const int nb = n0 + c * 32;
         const uint32_t buf = epi_buffer(p, e, 0);
-        if (p.e.in_tma && !has_pre && c + 1 < BN / 64)
-            epi_fetch(p, maps, e, epi_buffer(p, e, 1), stage_smem, nb + 64, m_row0, lane);
-        float sbl2[2] = {0.0f, 0.0f}, bl2[2] = {0.0f, 0.0f};
-        if (p.rowwise || p.bias != nullptr) {
+        if (p.e.in_tma && c + ahead < BN / 32)
+            epi_fetch(p, maps, e, ahead, stage_smem, nb + 32 * ahead, m_row0, lane);
+        const int nl = nb + lane;
+        const float sbl = (p.rowwise && nl < p.N) ? __ldg(p.scale_b + nl) : 0.0f;
+        const float bl = (p.bias != nullptr && nl < p.N) ? bias_value(p, nl) : 0.0f;
+        uint8_t *const out_buf = stage + buf * kEpiBuf;
+        float y[32];
+        ptx::tmem_ld_32cols(trow + static_cast<uint32_t>(c * 32), y);
+        for (int k = 0; k < add.count; ++k) {
+            const float4 *src = add.chunk(k, add.colt0 + c * 32);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int nl = nb + h * 32 + lane;
-                const bool in = nl < p.N;
-                sbl2[h] = (p.rowwise && in) ? __ldg(p.scale_b + nl) : 0.0f;
-                bl2[h] = (p.bias != nullptr && in) ? bias_value(p, nl) : 0.0f;
+            for (int g = 0; g < 8; ++g) {
+                const float4 x = add.ring == nullptr ? __ldcg(src + g * 128) : src[g * 128];
+                y[4 * g] += x.x;
+                y[4 * g + 1] += x.y;
+                y[4 * g + 2] += x.z;
+                y[4 * g + 3] += x.w;
             }
         }
-        uint8_t *const rowp = stage + buf * 4096u + lane * 128;
-        uint8_t *const rowq = stage + 4096 + lane * 128;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-            const float sbl = h ? sbl2[1] : sbl2[0], bl = h ? bl2[1] : bl2[0];
-            float y[32];
-            ptx::tmem_ld_32cols(trow + static_cast<uint32_t>(c * 64 + h * 32), y);
-            for (int k = 0; k < add.count; ++k) {
-                const float4 *src = add.chunk(k, add.colt0 + c * 64 + h * 32);
+        // z = fma(acc, scale, bias), the plain epilogue's roundings
+        if (p.rowwise && p.bias != nullptr) {
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    const float4 x = add.ring == nullptr ? __ldcg(src + g * 128) : src[g * 128];
-                    y[4 * g] += x.x;
-                    y[4 * g + 1] += x.y;
-                    y[4 * g + 2] += x.z;
-                    y[4 * g + 3] += x.w;
-                }
+            for (int j = 0; j < 32; ++j)
+                y[j] = fmaf(y[j], sa * __shfl_sync(kAll, sbl, j), __shfl_sync(kAll, bl, j));
+        } else if (p.rowwise) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                y[j] *= sa * __shfl_sync(kAll, sbl, j);
+        } else if (p.bias != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                y[j] = fmaf(y[j], s_tensor, __shfl_sync(kAll, bl, j));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                y[j] *= s_tensor;
+        }
+        if (p.e.in_tma) {
+            // (the buffers were free before the fetch)
+            if (!W.wait(e.bar + 8u * buf, e.phases >> buf & 1u, 9))
+                return false;
+            e.pending &= ~(1u << buf);
+            e.phases ^= 1u << buf;
+        } else {
+            // the last stores out of this block's buffers have read them
+            if (lane == 0) {
+                if (has_pre)
+                    ptx::bulk_wait_group_read<1>();
+                else
+                    ptx::bulk_wait_group_read<3>();
             }
-            // z = fma(acc, scale, bias), the plain epilogue's roundings
-            if (p.rowwise && p.bias != nullptr) {
+            __syncwarp();
+            if (has_in)
+                epi_plain_load(p, p.e.in, p.e.ld_in, out_buf, m_row0, nb, lane);
+        }
+        auto chunk = [&](uint8_t *b, int i) { return reinterpret_cast<uint4 *>(b + epi_chunk(lane, i)); };
+        auto pack8 = [&](int i) {
+            uint4 w;
+            w.x = pack_out2(y[8 * i], y[8 * i + 1], p.out_type);
+            w.y = pack_out2(y[8 * i + 2], y[8 * i + 3], p.out_type);
+            w.z = pack_out2(y[8 * i + 4], y[8 * i + 5], p.out_type);
+            w.w = pack_out2(y[8 * i + 6], y[8 * i + 7], p.out_type);
+            return w;
+        };
+        auto in8 = [&](int i, float (&r)[8]) {
+            const uint4 w = *chunk(out_buf, i);
+            aux_unpack2(w.x, f16, r[0], r[1]);
+            aux_unpack2(w.y, f16, r[2], r[3]);
+            aux_unpack2(w.z, f16, r[4], r[5]);
+            aux_unpack2(w.w, f16, r[6], r[7]);
+        };
+        if (p.e.grad) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    y[j] = fmaf(y[j], sa * __shfl_sync(kAll, sbl, j), __shfl_sync(kAll, bl, j));
-            } else if (p.rowwise) {
+            for (int i = 0; i < 4; ++i) {
+                float r[8], v[8];
+                in8(i, r);
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    y[j] *= sa * __shfl_sync(kAll, sbl, j);
-            } else if (p.bias != nullptr) {
+                for (int j = 0; j < 8; ++j)
+                    v[j] = y[8 * i + j];
+                apply_slope<8>(p.e.act, v, r);
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    y[j] = fmaf(y[j], s_tensor, __shfl_sync(kAll, bl, j));
-            } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    y[j] *= s_tensor;
+                for (int j = 0; j < 8; ++j)
+                    y[8 * i + j] = v[j];
             }
-            if (h == 0) {
-                // the buffers are free: their last stores have read them. With
-                // a fetch of this block that wait came before the fetch.
-                if (!p.e.in_tma) {
-                    if (lane == 0) {
-                        if (has_pre || has_in)
-                            ptx::bulk_wait_group_read<0>();
-                        else
-                            ptx::bulk_wait_group_read<1>();
-                    }
-                    __syncwarp();
-                    if (has_in)
-                        epi_plain_load(p, p.e.in, p.e.ld_in, stage + buf * 4096u, m_row0, nb, lane);
-                } else {
-                    if (!W.wait(e.bar + 8u * buf, e.phases >> buf & 1u, 9))
-                        return false;
-                    e.pending &= ~(1u << buf);
-                    e.phases ^= 1u << buf;
-                }
+        } else {
+            if (has_pre) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *chunk(out_buf + kEpiBuf, i) = pack8(i);
             }
-            auto chunk = [&](uint8_t *row, int i) {   // the thread's 16-byte chunk i of this half block
-                return reinterpret_cast<uint4 *>(row + (((h * 4 + i) ^ (lane & 7)) * 16));
-            };
-            auto pack8 = [&](int i) {
-                uint4 w;
-                w.x = pack_out2(y[8 * i], y[8 * i + 1], p.out_type);
-                w.y = pack_out2(y[8 * i + 2], y[8 * i + 3], p.out_type);
-                w.z = pack_out2(y[8 * i + 4], y[8 * i + 5], p.out_type);
-                w.w = pack_out2(y[8 * i + 6], y[8 * i + 7], p.out_type);
-                return w;
-            };
-            auto in8 = [&](int i, float (&r)[8]) {
-                const uint4 w = *chunk(rowp, i);
-                aux_unpack2(w.x, f16, r[0], r[1]);
-                aux_unpack2(w.y, f16, r[2], r[3]);
-                aux_unpack2(w.z, f16, r[4], r[5]);
-                aux_unpack2(w.w, f16, r[6], r[7]);
-            };
-            if (p.e.grad) {
+            apply_act<32>(p.e.act, y);
+            if (has_in) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float r[8], v[8];
+                    float r[8];
                     in8(i, r);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        v[j] = y[8 * i + j];
-                    apply_slope<8>(p.e.act, v, r);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        y[8 * i + j] = v[j];
-                }
-            } else {
-                if (has_pre) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *chunk(rowq, i) = pack8(i);
-                }
-                apply_act<32>(p.e.act, y);
-                if (has_in) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float r[8];
-                        in8(i, r);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            y[8 * i + j] += r[j];
-                    }
+                        y[8 * i + j] += r[j];
                 }
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *chunk(rowp, i) = pack8(i);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *chunk(out_buf, i) = pack8(i);
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
             if (p.out_tma)
-                ptx::tma_store_3d(tmap_out, stage_smem + buf * 4096u, nb, m_row0, 0);
+                ptx::tma_store_3d(tmap_out, stage_smem + buf * kEpiBuf, nb, m_row0, 0);
             if (p.e.pre_tma)
-                ptx::tma_store_3d(&maps.pre, stage_smem + 4096u, nb, m_row0, 0);
+                ptx::tma_store_3d(&maps.pre, stage_smem + (buf + 1) * kEpiBuf, nb, m_row0, 0);
             ptx::bulk_commit_group();
         }
         if (!p.out_tma)
-            epi_plain_store(p, p.out, p.ldo, stage + buf * 4096u, m_row0, nb, lane);
+            epi_plain_store(p, p.out, p.ldo, out_buf, m_row0, nb, lane);
         if (has_pre && !p.e.pre_tma)
-            epi_plain_store(p, p.e.pre, p.e.ld_pre, stage + 4096, m_row0, nb, lane);
+            epi_plain_store(p, p.e.pre, p.e.ld_pre, out_buf + kEpiBuf, m_row0, nb, lane);
+        __syncwarp();
         ++e.seq;
-        if (p.e.in_tma && has_pre && c + 1 < BN / 64)
-            epi_fetch(p, maps, e, epi_buffer(p, e, 0), stage_smem, nb + 64, m_row0, lane);
     }
     return true;
 }
@@ -1463,7 +1442,7 @@ __global__ void __launch_bounds__(TileCfg<BN, SWAP, WIDE>::kThreads, 1)
         }
         ptx::mbar_init(done_bar, 1);
         if constexpr (EPI && !SWAP)
-            for (int i = 0; i < 2 * kEpiWarps; ++i)
+            for (int i = 0; i < 4 * kEpiWarps; ++i)
                 ptx::mbar_init(bar0 + C::kEpiBarOffset + 8u * i, 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
@@ -1588,7 +1567,7 @@ __global__ void __launch_bounds__(TileCfg<BN, SWAP, WIDE>::kThreads, 1)
         uint8_t *stage = smem + (staging0 - sbase) + ew * C::kStageBufBytes * C::kStageBufs;
         const uint32_t stage_smem = staging0 + static_cast<uint32_t>(ew * C::kStageBufBytes * C::kStageBufs);
         uint32_t chunks = 0;
-        EpiPipe pipe{bar0 + C::kEpiBarOffset + 16u * ew, 0, 0, 0};
+        EpiPipe pipe{bar0 + C::kEpiBarOffset + 32u * ew, 0, 0, 0};
         int acc = 0;
         uint32_t acc_phase = 0;
         // SWAP: the CTA's last tile is staged in the drained operand ring and

@@ -59,7 +59,7 @@ struct ClusterKCfg {
 };
 
 template <int BN, int CS, bool EPI>
-__global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(kThreads, EPI && BN <= 64 ? 2 : 1)
     fp8mm_swap_ck_kernel(const __grid_constant__ CUtensorMap tmap_p,
                          const __grid_constant__ CUtensorMap tmap_q, const KernelParams p)
 {
@@ -254,19 +254,23 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
 
-        // The epilogue's inputs of this thread's columns, under way during the wait below
-        constexpr int kTurns = (C::kCols + 3) / 4;
-        float aux[EPI ? kTurns : 1][4] = {};
-        if constexpr (EPI) {
-            if (p.e.in != nullptr) {
-                const int t = threadIdx.x - 64;
+        // EPI: the reduction below takes kGroup columns at a time; their
+        // epilogue inputs are under way during the wait, the next group's
+        // during a group's work.
+        constexpr int kTurns = (C::kCols + 3) / 4, kGroup = EPI ? (kTurns < 4 ? kTurns : 4) : 1;
+        float aux[kGroup][4] = {};
+        auto load_aux = [&](int first_turn) {
+            const int t = threadIdx.x - 64;
 #pragma unroll
-                for (int i = 0; i < kTurns; ++i) {
-                    const int c = (t >> 5) + 4 * i, m = tq * BN + rank * C::kCols + c;
-                    if (c < C::kCols && m < p.M)
-                        epi_load_quad(p, m, tp * kTileP + 4 * (t & 31), aux[i]);
-                }
+            for (int i = 0; i < kGroup; ++i) {
+                const int c = (t >> 5) + 4 * (first_turn + i), m = tq * BN + rank * C::kCols + c;
+                if (c < C::kCols && m < p.M)
+                    epi_load_quad(p, m, tp * kTileP + 4 * (t & 31), aux[i]);
             }
+        };
+        if constexpr (EPI) {
+            if (p.e.in != nullptr)
+                load_aux(0);
         }
 
         // Every epilogue thread waits (bounded) for the peers' copies into this
@@ -281,41 +285,66 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(kThreads, 1)
             const int t = threadIdx.x - 64;                     // 0..127
             const int rl = 4 * (t & 31);                        // first of the lane's four tile rows
             const int n = tp * kTileP + rl;
-#pragma unroll(EPI ? kTurns : 1)
-            for (int turn = 0; turn < kTurns; ++turn) {
-                const int c = (t >> 5) + 4 * turn;
-                if (c >= C::kCols)
-                    break;
-                const int col = rank * C::kCols + c;            // column of the tile
-                const int m = tq * BN + col;                    // its output row
-                if (m >= p.M)
-                    break;
-                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+            for (int turn = 0; turn < kTurns; turn += kGroup) {
+                float y[4 * kGroup], r[4 * kGroup];
 #pragma unroll
-                for (int sl = 0; sl < CS; ++sl) {
-                    const float4 v = sl == rank
-                                         ? *reinterpret_cast<const float4 *>(partial + col * kTileP + rl)
-                                         : *reinterpret_cast<const float4 *>(
-                                               received + ((sl < rank ? sl : sl - 1) * C::kCols + c) * kTileP + rl);
-                    if (sl == 0) {
-                        acc = v;
-                    } else {
-                        acc.x += v.x;
-                        acc.y += v.y;
-                        acc.z += v.z;
-                        acc.w += v.w;
+                for (int g = 0; g < kGroup; ++g) {
+                    const int c = min((t >> 5) + 4 * (turn + g), C::kCols - 1);
+                    const int col = rank * C::kCols + c;            // column of the tile
+                    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int sl = 0; sl < CS; ++sl) {
+                        const float4 v = sl == rank
+                                             ? *reinterpret_cast<const float4 *>(partial + col * kTileP + rl)
+                                             : *reinterpret_cast<const float4 *>(
+                                                   received + ((sl < rank ? sl : sl - 1) * C::kCols + c) * kTileP + rl);
+                        if (sl == 0) {
+                            acc = v;
+                        } else {
+                            acc.x += v.x;
+                            acc.y += v.y;
+                            acc.z += v.z;
+                            acc.w += v.w;
+                        }
+                    }
+                    const float sa = pb.rowwise ? scale_a_tile[col] : 0.0f;
+                    const float a4[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        y[4 * g + i] = fmaf(a4[i], pb.rowwise ? sa * red_sb[i] : red_stensor, red_bias[i]);
+                        r[4 * g + i] = aux[g][i];
                     }
                 }
-                const float sa = pb.rowwise ? scale_a_tile[col] : 0.0f;
-                float y[4] = {acc.x, acc.y, acc.z, acc.w};
+                if constexpr (EPI) {
+                    if (p.e.in != nullptr && turn + kGroup < kTurns)
+                        load_aux(turn + kGroup);
+                    if (pb.e.grad) {
+                        apply_slope<4 * kGroup>(pb.e.act, y, r);
+                    } else {
+                        if (pb.e.pre != nullptr) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    y[i] = fmaf(y[i], pb.rowwise ? sa * red_sb[i] : red_stensor, red_bias[i]);
-                if constexpr (EPI)
-                    epi_quad(pb, y, m, n, aux[turn]);
-                // (Staging these rows for one TMA store instead measured 3-5 %
-                // slower here: 16 and 128 x 4096 x 4096.)
-                store_out4(pb, m, n, y);
+                            for (int g = 0; g < kGroup; ++g) {
+                                const int c = (t >> 5) + 4 * (turn + g), m = tq * BN + rank * C::kCols + c;
+                                if (c < C::kCols && m < pb.M)
+                                    epi_store_quad(pb, m, n, y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]);
+                            }
+                        }
+                        apply_act<4 * kGroup>(pb.e.act, y);
+#pragma unroll
+                        for (int i = 0; i < 4 * kGroup; ++i)
+                            y[i] += r[i];
+                    }
+                }
+#pragma unroll
+                for (int g = 0; g < kGroup; ++g) {
+                    const int c = (t >> 5) + 4 * (turn + g), m = tq * BN + rank * C::kCols + c;   // the output row
+                    const float o[4] = {y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]};
+                    // (Staging these rows for one TMA store instead measured 3-5 %
+                    // slower here: 16 and 128 x 4096 x 4096.)
+                    if (c < C::kCols && m < pb.M)
+                        store_out4(pb, m, n, o);
+                }
             }
         }
         __syncwarp();

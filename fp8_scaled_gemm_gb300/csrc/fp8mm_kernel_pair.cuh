@@ -57,7 +57,7 @@ struct PairCfg {
     static constexpr int kEpiWarps = EpiShape<SWAP>::kWarps;
     static constexpr int kStagingBytes = SWAP ? 0 : kEpiWarps * 4096 * kStageBufs;   // 4 KB buffers of the row-epilogue warps
     static constexpr int kBarBytes = 512;
-    static constexpr int kEpiBarOffset = 256;   // 8 x 2 per epilogue warp, with EPI
+    static constexpr int kEpiBarOffset = 256;   // EPI: four barriers per epilogue warp
     static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + kBarBytes;
     static_assert(kBBytes % 1024 == 0, "stage tiles must stay 1024-byte aligned");
     static_assert(kSmemBytes <= 232448, "exceeds 227 KB of shared memory");
@@ -169,7 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThr
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const uint32_t sk_bar = bar0 + 8u * (2 * S + 6);   // stream-K partial copied into the ring
     static_assert(8 * (2 * S + 7) <= (EPI && !SWAP ? C::kEpiBarOffset : C::kBarBytes), "barrier area");
-    static_assert(C::kEpiBarOffset + 16 * C::kEpiWarps <= C::kBarBytes, "epilogue barriers");
+    static_assert(C::kEpiBarOffset + 32 * C::kEpiWarps <= C::kBarBytes, "epilogue barriers");
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -189,7 +189,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThr
         ptx::mbar_init(done_bar, 1);
         ptx::mbar_init(sk_bar, 1);
         if constexpr (EPI && !SWAP)
-            for (int i = 0; i < 2 * C::kEpiWarps; ++i)
+            for (int i = 0; i < 4 * C::kEpiWarps; ++i)
                 ptx::mbar_init(bar0 + C::kEpiBarOffset + 8u * i, 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
@@ -360,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThr
         uint8_t *stage = smem + (staging0 - sbase) + ew * 4096 * C::kStageBufs;
         const uint32_t stage_smem = staging0 + static_cast<uint32_t>(ew * 4096 * C::kStageBufs);
         uint32_t chunks = 0;
-        EpiPipe pipe{bar0 + C::kEpiBarOffset + 16u * ew, 0, 0, 0};
+        EpiPipe pipe{bar0 + C::kEpiBarOffset + 32u * ew, 0, 0, 0};
         int acc = 0;
         uint32_t acc_phase = 0;
         PairSchedule sched(p, cluster_id, num_clusters);

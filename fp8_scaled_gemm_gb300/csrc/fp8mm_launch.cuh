@@ -18,6 +18,9 @@ namespace fp8mm_host {
 // 54.8 -> 46.1; at K = 1024 16 warps lost (16384 x 8192 x 1024 127.7 ->
 // 141.1, 4096 x 4096 x 1024 21.3 -> 23.2).
 constexpr int64_t kTileWideMaxK = 512;
+// The same with the extended epilogue, whose 16 warps leave a ring of two
+// stages. Measured: NOTE.
+constexpr int64_t kTileWideMaxKExt = 1024;
 
 // A kernel's argument of the extended epilogue's tensor maps.
 template <bool EPI>
@@ -124,11 +127,8 @@ int dispatch(const Choice &c, const CUtensorMap &mp, const CUtensorMap &mq, cons
         case 256:
             // shallow K: 16 epilogue warps (the epilogue sets the time per
             // tile); deeper K keeps 8 and two stage buffers per warp
-            // (the extended epilogue has two buffers per warp: 8 warps)
-            if constexpr (!EPI) {
-                if (kp.K <= kTileWideMaxK)
-                    return launch_kernel<256, false, true, EPI>(mp, mq, mo, kp, em, c.grid, stream);
-            }
+            if (kp.K <= (EPI ? kTileWideMaxKExt : kTileWideMaxK))
+                return launch_kernel<256, false, true, EPI>(mp, mq, mo, kp, em, c.grid, stream);
             return launch_kernel<256, false, false, EPI>(mp, mq, mo, kp, em, c.grid, stream);
         }
     } else {
