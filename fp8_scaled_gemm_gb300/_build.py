@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libfp8mm.so")
 
-SOURCES = ["fp8mm_epilogue.cu", "fp8mm_api.cu", "fp8mm_norm_grad.cu", "fp8mm_norm.cu", "fp8mm_actgrad.cu"]
+SOURCES = ["fp8mm_epilogue.cu", "fp8mm_epilogue_swap.cu", "fp8mm_api.cu", "fp8mm_norm_grad.cu", "fp8mm_norm.cu", "fp8mm_actgrad.cu"]
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 

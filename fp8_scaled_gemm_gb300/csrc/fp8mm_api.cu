@@ -234,19 +234,24 @@ int encode_operand_map(CUtensorMap *map, const void *base, int64_t rows, int64_t
 }
 
 // 16-bit output [batch, M, N] (N contiguous) written in boxes of 32 rows x
-// box_n columns of one item from a swizzled shared-memory stage: 64 columns
-// (128-byte swizzle), or 32 (64-byte) for the matrices of the extended
-// epilogue.
-int encode_out_map(CUtensorMap *map, void *out, int64_t M, int64_t N, bool f16, int64_t batch, int64_t ldo, int box_n)
+// 64 columns of one item from a 128-byte-swizzled shared-memory stage; with
+// `ext` a matrix of the extended epilogue (16-bit or fp32), read or written in
+// boxes of 32 x 32 with the swizzle of its 64- or 128-byte rows.
+int encode_out_map(CUtensorMap *map, void *out, int64_t M, int64_t N, int out_type, int64_t batch, int64_t ldo,
+                   bool ext)
 {
+    const bool f32 = out_type == FP8MM_OUT_F32;
+    const cuuint64_t es = f32 ? 4 : 2;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M), static_cast<cuuint64_t>(batch)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ldo) * 2, static_cast<cuuint64_t>(ldo) * 2 * static_cast<cuuint64_t>(M)};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(box_n), 32, 1};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ldo) * es, static_cast<cuuint64_t>(ldo) * es * static_cast<cuuint64_t>(M)};
+    cuuint32_t box[3] = {ext ? 32u : 64u, 32, 1};
     cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = g_encode(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, out,
-                          dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          box_n == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+    CUresult r = g_encode(map,
+                          f32                            ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                          : out_type == FP8MM_OUT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                          3, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          ext && !f32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         char buf[128];
@@ -265,7 +270,7 @@ int encode_out_map(CUtensorMap *map, void *out, int64_t M, int64_t N, bool f16, 
 // buffers (a training or serving loop) skip it. Entries are replaced round
 // robin.
 struct MapKey {
-    int dev, kind;            // kind 0: fp8 operand; 1: bf16 output; 2: fp16 output
+    int dev, kind;            // kind 0: fp8 operand; 1 + type: output; 10 + type: output columns
     const void *base;
     int64_t rows, cols, batch, ld;
     int box_rows;
@@ -325,14 +330,15 @@ int cached_operand_map(CUtensorMap *map, const void *base, int64_t rows, int64_t
     return rc;
 }
 
-int cached_out_map(CUtensorMap *map, void *out, int64_t M, int64_t N, bool f16, int64_t batch, int64_t ldo, int box_n = 64)
+int cached_out_map(CUtensorMap *map, void *out, int64_t M, int64_t N, int out_type, int64_t batch, int64_t ldo,
+                   bool ext)
 {
-    const MapKey k{current_device(), f16 ? 2 : 1, out, M, N, batch, ldo, box_n};
+    const MapKey k{current_device(), 1 + out_type, out, M, N, batch, ldo, ext ? 33 : 32};
     if (const CUtensorMap *m = map_lookup(k)) {
         *map = *m;
         return FP8MM_OK;
     }
-    const int rc = encode_out_map(map, out, M, N, f16, batch, ldo, box_n);
+    const int rc = encode_out_map(map, out, M, N, out_type, batch, ldo, ext);
     if (rc == FP8MM_OK)
         map_insert(k, *map);
     return rc;
@@ -761,9 +767,11 @@ int encode_and_dispatch(const Choice &c, const void *A, const void *B, void *out
     // rows are 16-byte aligned (TILE without split-K, PAIR); otherwise, and
     // for fp32 / e4m3 outputs, through plain stores.
     const bool out16 = kp.out_type == FP8MM_OUT_BF16 || kp.out_type == FP8MM_OUT_F16;
-    if (!swap && out16 && c.split == 1 && (N % 8) == 0 && (kp.ldo % 8) == 0 &&
-        (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
-        int rc = cached_out_map(&mo, out, M, N, kp.out_type == FP8MM_OUT_F16, batch, kp.ldo, epi ? 32 : 64);
+    // (The extended epilogue moves fp32 outputs that way too.)
+    const bool rows_tma = !swap && c.split == 1 && (out16 || (epi && kp.out_type == FP8MM_OUT_F32));
+    const int64_t per16 = kp.out_type == FP8MM_OUT_F32 ? 4 : 8;   // elements in 16 bytes
+    if (rows_tma && (N % per16) == 0 && (kp.ldo % per16) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+        int rc = cached_out_map(&mo, out, M, N, kp.out_type, batch, kp.ldo, epi);
         if (rc != FP8MM_OK)
             return rc;
         kp.out_tma = 1;
@@ -794,20 +802,20 @@ int encode_and_dispatch(const Choice &c, const void *A, const void *B, void *out
     if (rc != FP8MM_OK)
         return rc;
     if (!epi)
-        return dispatch<false>(c, mp, mq, mo, kp, nullptr, stream);
-    // The row-major kernels move the epilogue's 16-bit matrices through TMA
-    // under the output's conditions.
+        return dispatch<false, kRowKernels | kSwapKernels>(c, mp, mq, mo, kp, nullptr, stream);
+    // The row-major kernels move the epilogue's matrices through TMA under the
+    // output's conditions.
     fp8mm::EpiMaps<true> em;
     std::memset(&em, 0, sizeof em);
-    if (!swap && out16 && c.split == 1 && (N % 8) == 0) {
-        const bool f16 = kp.out_type == FP8MM_OUT_F16;
+    if (rows_tma && (N % per16) == 0) {
         if (kp.e.in && kp.e.vec_in) {
-            if ((rc = cached_out_map(&em.in, const_cast<void *>(kp.e.in), M, N, f16, 1, kp.e.ld_in, 32)) != FP8MM_OK)
+            if ((rc = cached_out_map(&em.in, const_cast<void *>(kp.e.in), M, N, kp.out_type, 1, kp.e.ld_in, true)) !=
+                FP8MM_OK)
                 return rc;
             kp.e.in_tma = 1;
         }
         if (kp.e.pre && kp.e.vec_pre) {
-            if ((rc = cached_out_map(&em.pre, kp.e.pre, M, N, f16, 1, kp.e.ld_pre, 32)) != FP8MM_OK)
+            if ((rc = cached_out_map(&em.pre, kp.e.pre, M, N, kp.out_type, 1, kp.e.ld_pre, true)) != FP8MM_OK)
                 return rc;
             kp.e.pre_tma = 1;
         }

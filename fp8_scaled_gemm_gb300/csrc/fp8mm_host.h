@@ -39,9 +39,11 @@ struct Choice {
 };
 
 // The launch of a chosen kernel with the extended epilogue
-// (KernelParams::e), compiled in a translation unit of its own.
+// (KernelParams::e), compiled in translation units of their own.
 int dispatch_epilogue(const Choice &c, const CUtensorMap &mp, const CUtensorMap &mq, const CUtensorMap &mo,
                       const fp8mm::KernelParams &kp, const fp8mm::EpiMaps<true> &em, cudaStream_t stream);
+int dispatch_epilogue_swap(const Choice &c, const CUtensorMap &mp, const CUtensorMap &mq, const CUtensorMap &mo,
+                           const fp8mm::KernelParams &kp, const fp8mm::EpiMaps<true> &em, cudaStream_t stream);
 
 // Launch with programmatic stream serialization: the kernel may start its
 // set-up while the previous kernel in the stream finishes; it calls

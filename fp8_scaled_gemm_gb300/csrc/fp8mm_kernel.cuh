@@ -45,6 +45,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -96,7 +97,7 @@ struct EpiParams {
     void *pre;                      // forward: where z goes; nullptr: nowhere
     long long ld_pre;
     int vec_in, vec_pre;            // 16-byte accesses allowed: base and row pitch aligned
-    int in_tma, pre_tma;            // EpiMaps::in / pre are valid: 16-bit blocks move through TMA
+    int in_tma, pre_tma;            // EpiMaps::in / pre are valid: blocks move through TMA
 };
 
 // Tensor maps of the extended epilogue's matrices, blocks as the output's.
@@ -529,33 +530,66 @@ __device__ __forceinline__ void epi_row(const KernelParams &p, float (&y)[CH], i
 }
 
 // The same for a thread that holds one column n, rows m0 .. m0 + CH - 1
-// (neighbouring lanes hold neighbouring columns).
+// (neighbouring lanes hold neighbouring columns). The type is tested once per
+// chunk, so that the loads go out together.
 template <int CH>
 __device__ __forceinline__ void epi_col(const KernelParams &p, float (&y)[CH], int n, int m0)
 {
-    const bool n_in = n < p.N;
-    float r[CH];
+    const int rows = n < p.N ? min(CH, p.M - m0) : 0;
+    float r[CH] = {};
     if (p.e.in != nullptr) {
+        const size_t at = static_cast<size_t>(m0) * p.e.ld_in + n;
+        if (p.out_type == kOutF32) {
+            const float *src = static_cast<const float *>(p.e.in) + at;
 #pragma unroll
-        for (int j = 0; j < CH; ++j)
-            r[j] = (n_in && m0 + j < p.M) ? aux_load1(p, p.e.in, static_cast<size_t>(m0 + j) * p.e.ld_in + n) : 0.0f;
+            for (int j = 0; j < CH; ++j)
+                if (j < rows)
+                    r[j] = src[static_cast<size_t>(j) * p.e.ld_in];
+        } else {
+            const unsigned short *src = static_cast<const unsigned short *>(p.e.in) + at;
+            unsigned short raw[CH];
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+                raw[j] = j < rows ? src[static_cast<size_t>(j) * p.e.ld_in] : static_cast<unsigned short>(0);
+            if (p.out_type == kOutF16) {
+#pragma unroll
+                for (int j = 0; j < CH; ++j)
+                    r[j] = __half2float(__ushort_as_half(raw[j]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < CH; ++j)
+                    r[j] = __bfloat162float(__ushort_as_bfloat16(raw[j]));
+            }
+        }
     }
     if (p.e.grad) {
         apply_slope<CH>(p.e.act, y, r);
         return;
     }
     if (p.e.pre != nullptr) {
+        const size_t at = static_cast<size_t>(m0) * p.e.ld_pre + n;
+        if (p.out_type == kOutF32) {
+            float *dst = static_cast<float *>(p.e.pre) + at;
 #pragma unroll
-        for (int j = 0; j < CH; ++j)
-            if (n_in && m0 + j < p.M)
-                aux_store1(p, p.e.pre, static_cast<size_t>(m0 + j) * p.e.ld_pre + n, y[j]);
+            for (int j = 0; j < CH; ++j)
+                if (j < rows)
+                    dst[static_cast<size_t>(j) * p.e.ld_pre] = y[j];
+        } else {
+            unsigned short *dst = static_cast<unsigned short *>(p.e.pre) + at;
+#pragma unroll
+            for (int j = 0; j < CH; j += 2) {
+                const uint32_t w = pack_out2(y[j], y[j + 1], p.out_type);
+                if (j < rows)
+                    dst[static_cast<size_t>(j) * p.e.ld_pre] = static_cast<unsigned short>(w & 0xFFFFu);
+                if (j + 1 < rows)
+                    dst[static_cast<size_t>(j + 1) * p.e.ld_pre] = static_cast<unsigned short>(w >> 16);
+            }
+        }
     }
     apply_act<CH>(p.e.act, y);
-    if (p.e.in != nullptr) {
 #pragma unroll
-        for (int j = 0; j < CH; ++j)
-            y[j] += r[j];
-    }
+    for (int j = 0; j < CH; ++j)
+        y[j] += r[j];
 }
 
 // Four consecutive elements n .. n + 3 (n % 4 == 0) of row m < M of p.e.in; 0 past N.
@@ -1142,95 +1176,173 @@ __device__ __forceinline__ void epilogue_rows_staged(const KernelParams &p, cons
 
 // ------------------------------------- extended epilogue, row-major kernels ---
 //
-// The 16-bit matrices beside the output move like the output: 32 x 32 blocks
-// between global memory and a warp's four 2 KB buffers (one 64-byte row per
-// thread, 64-byte swizzle: the eight threads of a quarter-warp hit distinct
-// banks), by TMA when their rows are 16-byte aligned, otherwise by element
-// accesses of neighbouring lanes to neighbouring columns. (Loads and stores of
-// a thread's own row touched 32 lines per instruction: 8192 x 8192 x 1024 gelu
-// with residual and z took 186 us; 32 x 64 blocks in two buffers, with z
-// nothing under way ahead, 144.)
+// The matrices beside the output move like the output: 32 x 32 blocks between
+// global memory and a warp's 8 KB of buffers (one row of 64 bytes, or 128 of
+// fp32, per thread, swizzled so that the eight threads of a quarter-warp hit
+// distinct banks), by TMA when their rows are 16-byte aligned, otherwise by
+// element accesses of neighbouring lanes to neighbouring columns. (Loads and
+// stores of a thread's own row touched 32 lines per instruction: 8192 x 8192 x
+// 1024 gelu with residual and z took 186 us; 32 x 64 blocks in two buffers,
+// with z nothing under way ahead, 144; this form 122.)
 //
-// `in` arrives in the buffer its block's output is built in. Without z the
-// four buffers go round and two blocks of `in` are under way ahead; with z
-// they make two pairs (output, z) and one block is. The first blocks' `in` is
-// asked for before the accumulator is waited for.
+// `in` arrives in the buffer its block's output is built in; with z a slot is
+// a pair of buffers (output, z). Four 2 KB slots go round with two blocks of
+// `in` under way ahead, two slots with one, a single slot (fp32 with z) with
+// none. The first blocks' `in` is asked for before the accumulator is waited
+// for.
 struct EpiPipe {
     uint32_t bar;        // four mbarriers of this warp: loads into its buffers
-    uint32_t phases;     // their phase bits
+    uint32_t phases;     // their phase bits, by slot
     uint32_t seq;        // blocks done
-    uint32_t pending;    // loads in flight, by buffer
+    uint32_t pending;    // loads in flight, by slot
 };
 
-constexpr uint32_t kEpiBuf = 2048;
+constexpr uint32_t kEpiBytes = 8192;   // buffers of a warp
 
-// Buffer of the output (and `in`) of the block `ahead` blocks from now; z's is
-// the next one.
-__device__ __forceinline__ uint32_t epi_buffer(const KernelParams &p, const EpiPipe &e, uint32_t ahead)
+__device__ __forceinline__ bool epi_f32(const KernelParams &p) { return p.out_type == kOutF32; }
+__device__ __forceinline__ uint32_t epi_block_bytes(const KernelParams &p) { return epi_f32(p) ? 4096u : 2048u; }
+// Slots less one (a mask), and a slot's bytes.
+__device__ __forceinline__ uint32_t epi_slot_mask(const KernelParams &p)
 {
-    return p.e.pre != nullptr ? ((e.seq + ahead) & 1u) * 2u : ((e.seq + ahead) & 3u);
+    return (epi_f32(p) ? 2u : 4u) / (p.e.pre != nullptr ? 2u : 1u) - 1u;
+}
+__device__ __forceinline__ uint32_t epi_slot_bytes(const KernelParams &p) { return kEpiBytes / (epi_slot_mask(p) + 1u); }
+// Blocks of `in` under way ahead of the one that is worked on: 2, 1, 0.
+__device__ __forceinline__ int epi_ahead(const KernelParams &p) { return static_cast<int>(epi_slot_mask(p) + 1u) >> 1; }
+
+// At most n of the lane's store groups still read their buffers.
+__device__ __forceinline__ void epi_wait_reads(uint32_t n)
+{
+    if (n == 0)
+        ptx::bulk_wait_group_read<0>();
+    else if (n == 1)
+        ptx::bulk_wait_group_read<1>();
+    else
+        ptx::bulk_wait_group_read<3>();
 }
 
-// Blocks of `in` under way ahead of the one that is worked on.
-__device__ __forceinline__ int epi_ahead(const KernelParams &p) { return p.e.pre != nullptr ? 1 : 2; }
-
-// Ask for a block of `in`, `ahead` blocks from now. The last stores out of its
-// buffers have read them: those of the previous block with pairs, of the one
-// before without (one younger group may still read).
+// Ask for the block of `in` that lies `ahead` blocks from now. The last stores
+// out of its slot have read it: with four slots one younger group may still
+// read, with two or one it is the youngest.
 __device__ __forceinline__ void epi_fetch(const KernelParams &p, const EpiMaps<true> &maps, EpiPipe &e, uint32_t ahead,
                                           uint32_t stage_smem, int nb, int m_row0, int lane)
 {
-    const uint32_t buf = epi_buffer(p, e, ahead);
+    const uint32_t mask = epi_slot_mask(p), slot = (e.seq + ahead) & mask;
     if (lane == 0) {
-        if (p.e.pre != nullptr)
-            ptx::bulk_wait_group_read<0>();
-        else
-            ptx::bulk_wait_group_read<1>();
-        ptx::mbar_arrive_expect_tx(e.bar + 8u * buf, kEpiBuf);
-        ptx::tma_load_3d(stage_smem + buf * kEpiBuf, &maps.in, e.bar + 8u * buf, nb, m_row0, 0);
+        epi_wait_reads(mask == 3u ? 1u : 0u);
+        ptx::mbar_arrive_expect_tx(e.bar + 8u * slot, epi_block_bytes(p));
+        ptx::tma_load_3d(stage_smem + slot * epi_slot_bytes(p), &maps.in, e.bar + 8u * slot, nb, m_row0, 0);
     }
-    e.pending |= 1u << buf;
+    e.pending |= 1u << slot;
     __syncwarp();
 }
 
 // Byte offset of 16-byte chunk i of row r of a buffer.
-__device__ __forceinline__ int epi_chunk(int r, int i) { return r * 64 + ((i ^ ((r >> 1) & 3)) * 16); }
+__device__ __forceinline__ int epi_chunk(bool f32, int r, int i)
+{
+    return f32 ? r * 128 + ((i ^ (r & 7)) * 16) : r * 64 + ((i ^ ((r >> 1) & 3)) * 16);
+}
 
-// A block of a [M, N] matrix of 16-bit elements whose rows are not 16-byte
-// aligned, to or from a buffer: lane l moves column nb + l.
+// A block of a [M, N] matrix whose rows are not 16-byte aligned, to or from a
+// buffer: lane l moves column nb + l.
+template <typename T>
 __device__ __forceinline__ void epi_plain_load(const KernelParams &p, const void *base, long long ld, uint8_t *buf,
                                                int m_row0, int nb, int lane)
 {
+    constexpr bool f32 = sizeof(T) == 4;
+    constexpr int per = 16 / static_cast<int>(sizeof(T));
     const int col = nb + lane, rows = col < p.N ? min(32, p.M - m_row0) : 0;
-    const unsigned short *src = static_cast<const unsigned short *>(base) + static_cast<size_t>(m_row0) * ld + col;
-#pragma unroll 16
+    const T *src = static_cast<const T *>(base) + static_cast<size_t>(m_row0) * ld + col;
+#pragma unroll
     for (int r = 0; r < 32; ++r) {
-        const unsigned short v = r < rows ? src[static_cast<size_t>(r) * ld] : static_cast<unsigned short>(0);
-        *reinterpret_cast<unsigned short *>(buf + epi_chunk(r, lane >> 3) + (lane & 7) * 2) = v;
+        const T v = r < rows ? src[static_cast<size_t>(r) * ld] : static_cast<T>(0);
+        *reinterpret_cast<T *>(buf + epi_chunk(f32, r, lane / per) + (lane % per) * static_cast<int>(sizeof(T))) = v;
     }
     __syncwarp();
 }
 
+template <typename T>
 __device__ __forceinline__ void epi_plain_store(const KernelParams &p, void *base, long long ld, const uint8_t *buf,
                                                 int m_row0, int nb, int lane)
 {
+    constexpr bool f32 = sizeof(T) == 4;
+    constexpr int per = 16 / static_cast<int>(sizeof(T));
     const int col = nb + lane, rows = col < p.N ? min(32, p.M - m_row0) : 0;
-    unsigned short *dst = static_cast<unsigned short *>(base) + static_cast<size_t>(m_row0) * ld + col;
+    T *dst = static_cast<T *>(base) + static_cast<size_t>(m_row0) * ld + col;
 #pragma unroll 16
     for (int r = 0; r < 32; ++r) {
-        const unsigned short v = *reinterpret_cast<const unsigned short *>(buf + epi_chunk(r, lane >> 3) + (lane & 7) * 2);
+        const T v = *reinterpret_cast<const T *>(buf + epi_chunk(f32, r, lane / per) +
+                                                 (lane % per) * static_cast<int>(sizeof(T)));
         if (r < rows)
             dst[static_cast<size_t>(r) * ld] = v;
     }
 }
 
-// Before the accumulator wait: the tile's first blocks of `in`.
-__device__ __forceinline__ void epi_begin_tile(const KernelParams &p, const EpiMaps<true> &maps, EpiPipe &e,
-                                               uint32_t stage_smem, int m_row0, int n0, int lane)
+// 8 columns 8 i .. 8 i + 7 of the thread's row of a buffer.
+template <bool F32>
+__device__ __forceinline__ void epi_read8(bool f16, const uint8_t *buf, int lane, int i, float (&r)[8])
+{
+    if constexpr (F32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 x = *reinterpret_cast<const float4 *>(buf + epi_chunk(true, lane, 2 * i + h));
+            r[4 * h] = x.x;
+            r[4 * h + 1] = x.y;
+            r[4 * h + 2] = x.z;
+            r[4 * h + 3] = x.w;
+        }
+    } else {
+        const uint4 w = *reinterpret_cast<const uint4 *>(buf + epi_chunk(false, lane, i));
+        aux_unpack2(w.x, f16, r[0], r[1]);
+        aux_unpack2(w.y, f16, r[2], r[3]);
+        aux_unpack2(w.z, f16, r[4], r[5]);
+        aux_unpack2(w.w, f16, r[6], r[7]);
+    }
+}
+
+// The thread's row of 32 values to a buffer, one rounding.
+template <bool F32>
+__device__ __forceinline__ void epi_write_row(int out_type, uint8_t *buf, int lane, const float (&y)[32])
+{
+    if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4 *>(buf + epi_chunk(true, lane, i)) =
+                make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint4 w;
+            w.x = pack_out2(y[8 * i], y[8 * i + 1], out_type);
+            w.y = pack_out2(y[8 * i + 2], y[8 * i + 3], out_type);
+            w.z = pack_out2(y[8 * i + 4], y[8 * i + 5], out_type);
+            w.w = pack_out2(y[8 * i + 6], y[8 * i + 7], out_type);
+            *reinterpret_cast<uint4 *>(buf + epi_chunk(false, lane, i)) = w;
+        }
+    }
+}
+
+// A warp's scales and biases for one tile, loaded before the accumulator wait
+// (they cost a launch with one tile per CTA 1.3 us after it).
+template <int BN>
+struct EpiPre {
+    ColPre<BN> col;
+    float sa;
+};
+
+// Before the accumulator wait: the scales and biases, and the first blocks of `in`.
+template <int BN>
+__device__ __forceinline__ EpiPre<BN> epi_begin_tile(const KernelParams &p, const EpiMaps<true> &maps, EpiPipe &e,
+                                                     uint32_t stage_smem, int m_row0, int n0, int lane)
 {
     if (p.e.in_tma)
-        for (int b = 0; b < epi_ahead(p); ++b)
+        for (int b = 0; b < max(1, epi_ahead(p)); ++b)
             epi_fetch(p, maps, e, b, stage_smem, n0 + 32 * b, m_row0, lane);
+    EpiPre<BN> pre{};
+    if (p.rowwise || p.bias != nullptr)
+        pre.col = load_col_pre<BN>(p, n0, lane);
+    pre.sa = (p.rowwise && m_row0 + lane < p.M) ? __ldg(p.scale_a + m_row0 + lane) : 0.0f;
+    return pre;
 }
 
 // Loads still in flight land before the CTA may leave.
@@ -1242,33 +1354,43 @@ __device__ __forceinline__ void epi_drain(const Waiter &W, EpiPipe &e)
             W.drain(e.bar + 8u * b, e.phases >> b & 1u, 9);
 }
 
-// The extended form of epilogue_rows_staged: one warp's 32 accumulator rows x
-// BN columns, 32 at a time. Returns false when a wait ran out.
-template <int BN>
-__device__ __forceinline__ bool epilogue_rows_ext(const KernelParams &p, const CUtensorMap *tmap_out,
+// The extended form of epilogue_rows_staged for fp32 (F32) or 16-bit matrices:
+// one warp's 32 accumulator rows x BN columns, 32 at a time. Returns false when
+// a wait ran out.
+template <int BN, bool F32>
+__device__ __forceinline__ bool epilogue_blocks(const KernelParams &p, const CUtensorMap *tmap_out,
                                                   const EpiMaps<true> &maps, const Waiter &W, EpiPipe &e, uint32_t trow,
                                                   int m_row0, int n0, int lane, uint8_t *stage, uint32_t stage_smem,
-                                                  float s_tensor, const PartialSrc add)
+                                                  float s_tensor, const PartialSrc add, EpiPre<BN> pre)
 {
-    if (p.out_type == kOutF32 || p.out_type == kOutE4M3) {
-        epilogue_rows_wide<BN, true>(p, trow, m_row0, n0, lane, s_tensor, add);
-        return true;
-    }
     constexpr unsigned kAll = 0xffffffffu;
-    const int m = m_row0 + lane;
-    const float sa = (p.rowwise && m < p.M) ? __ldg(p.scale_a + m) : 0.0f;
+    constexpr uint32_t block_bytes = F32 ? 4096u : 2048u;
+    using Bits = typename std::conditional<F32, uint32_t, unsigned short>::type;
     const bool f16 = p.out_type == kOutF16, has_in = p.e.in != nullptr, has_pre = p.e.pre != nullptr;
     const int ahead = epi_ahead(p);
+    const uint32_t mask = epi_slot_mask(p), slot_bytes = epi_slot_bytes(p);
 #pragma unroll 1
     for (int c = 0; c < BN / 32; ++c) {
         const int nb = n0 + c * 32;
-        const uint32_t buf = epi_buffer(p, e, 0);
-        if (p.e.in_tma && c + ahead < BN / 32)
+        const uint32_t slot = e.seq & mask;
+        if (p.e.in_tma && ahead > 0 && c + ahead < BN / 32)
             epi_fetch(p, maps, e, ahead, stage_smem, nb + 32 * ahead, m_row0, lane);
-        const int nl = nb + lane;
-        const float sbl = (p.rowwise && nl < p.N) ? __ldg(p.scale_b + nl) : 0.0f;
-        const float bl = (p.bias != nullptr && nl < p.N) ? bias_value(p, nl) : 0.0f;
-        uint8_t *const out_buf = stage + buf * kEpiBuf;
+        // the front of a register queue that moves on after every block
+        const float sbl = pre.col.sb[0], bl = pre.col.b[0];
+#pragma unroll
+        for (int i = 0; i + 1 < ColPre<BN>::kN; ++i) {
+            pre.col.sb[i] = pre.col.sb[i + 1];
+            pre.col.b[i] = pre.col.b[i + 1];
+        }
+        uint8_t *const out_buf = stage + slot * slot_bytes, *const z_buf = out_buf + block_bytes;
+        if (!p.e.in_tma) {
+            // the last stores out of this slot have read it
+            if (lane == 0)
+                epi_wait_reads(mask);
+            __syncwarp();
+            if (has_in)
+                epi_plain_load<Bits>(p, p.e.in, p.e.ld_in, out_buf, m_row0, nb, lane);
+        }
         float y[32];
         ptx::tmem_ld_32cols(trow + static_cast<uint32_t>(c * 32), y);
         for (int k = 0; k < add.count; ++k) {
@@ -1286,11 +1408,11 @@ __device__ __forceinline__ bool epilogue_rows_ext(const KernelParams &p, const C
         if (p.rowwise && p.bias != nullptr) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                y[j] = fmaf(y[j], sa * __shfl_sync(kAll, sbl, j), __shfl_sync(kAll, bl, j));
+                y[j] = fmaf(y[j], pre.sa * __shfl_sync(kAll, sbl, j), __shfl_sync(kAll, bl, j));
         } else if (p.rowwise) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                y[j] *= sa * __shfl_sync(kAll, sbl, j);
+                y[j] *= pre.sa * __shfl_sync(kAll, sbl, j);
         } else if (p.bias != nullptr) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -1301,44 +1423,17 @@ __device__ __forceinline__ bool epilogue_rows_ext(const KernelParams &p, const C
                 y[j] *= s_tensor;
         }
         if (p.e.in_tma) {
-            // (the buffers were free before the fetch)
-            if (!W.wait(e.bar + 8u * buf, e.phases >> buf & 1u, 9))
+            // (the slot was free before the fetch)
+            if (!W.wait(e.bar + 8u * slot, e.phases >> slot & 1u, 9))
                 return false;
-            e.pending &= ~(1u << buf);
-            e.phases ^= 1u << buf;
-        } else {
-            // the last stores out of this block's buffers have read them
-            if (lane == 0) {
-                if (has_pre)
-                    ptx::bulk_wait_group_read<1>();
-                else
-                    ptx::bulk_wait_group_read<3>();
-            }
-            __syncwarp();
-            if (has_in)
-                epi_plain_load(p, p.e.in, p.e.ld_in, out_buf, m_row0, nb, lane);
+            e.pending &= ~(1u << slot);
+            e.phases ^= 1u << slot;
         }
-        auto chunk = [&](uint8_t *b, int i) { return reinterpret_cast<uint4 *>(b + epi_chunk(lane, i)); };
-        auto pack8 = [&](int i) {
-            uint4 w;
-            w.x = pack_out2(y[8 * i], y[8 * i + 1], p.out_type);
-            w.y = pack_out2(y[8 * i + 2], y[8 * i + 3], p.out_type);
-            w.z = pack_out2(y[8 * i + 4], y[8 * i + 5], p.out_type);
-            w.w = pack_out2(y[8 * i + 6], y[8 * i + 7], p.out_type);
-            return w;
-        };
-        auto in8 = [&](int i, float (&r)[8]) {
-            const uint4 w = *chunk(out_buf, i);
-            aux_unpack2(w.x, f16, r[0], r[1]);
-            aux_unpack2(w.y, f16, r[2], r[3]);
-            aux_unpack2(w.z, f16, r[4], r[5]);
-            aux_unpack2(w.w, f16, r[6], r[7]);
-        };
         if (p.e.grad) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float r[8], v[8];
-                in8(i, r);
+                epi_read8<F32>(f16, out_buf, lane, i, r);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     v[j] = y[8 * i + j];
@@ -1348,43 +1443,57 @@ __device__ __forceinline__ bool epilogue_rows_ext(const KernelParams &p, const C
                     y[8 * i + j] = v[j];
             }
         } else {
-            if (has_pre) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *chunk(out_buf + kEpiBuf, i) = pack8(i);
-            }
+            if (has_pre)
+                epi_write_row<F32>(p.out_type, z_buf, lane, y);
             apply_act<32>(p.e.act, y);
             if (has_in) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float r[8];
-                    in8(i, r);
+                    epi_read8<F32>(f16, out_buf, lane, i, r);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         y[8 * i + j] += r[j];
                 }
             }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *chunk(out_buf, i) = pack8(i);
+        epi_write_row<F32>(p.out_type, out_buf, lane, y);
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
             if (p.out_tma)
-                ptx::tma_store_3d(tmap_out, stage_smem + buf * kEpiBuf, nb, m_row0, 0);
+                ptx::tma_store_3d(tmap_out, stage_smem + slot * slot_bytes, nb, m_row0, 0);
             if (p.e.pre_tma)
-                ptx::tma_store_3d(&maps.pre, stage_smem + (buf + 1) * kEpiBuf, nb, m_row0, 0);
+                ptx::tma_store_3d(&maps.pre, stage_smem + slot * slot_bytes + block_bytes, nb, m_row0, 0);
             ptx::bulk_commit_group();
         }
         if (!p.out_tma)
-            epi_plain_store(p, p.out, p.ldo, out_buf, m_row0, nb, lane);
+            epi_plain_store<Bits>(p, p.out, p.ldo, out_buf, m_row0, nb, lane);
         if (has_pre && !p.e.pre_tma)
-            epi_plain_store(p, p.e.pre, p.e.ld_pre, out_buf + kEpiBuf, m_row0, nb, lane);
+            epi_plain_store<Bits>(p, p.e.pre, p.e.ld_pre, z_buf, m_row0, nb, lane);
         __syncwarp();
         ++e.seq;
+        if (p.e.in_tma && ahead == 0 && c + 1 < BN / 32)
+            epi_fetch(p, maps, e, 0, stage_smem, nb + 32, m_row0, lane);
     }
     return true;
+}
+
+template <int BN>
+__device__ __forceinline__ bool epilogue_rows_ext(const KernelParams &p, const CUtensorMap *tmap_out,
+                                                  const EpiMaps<true> &maps, const Waiter &W, EpiPipe &e, uint32_t trow,
+                                                  int m_row0, int n0, int lane, uint8_t *stage, uint32_t stage_smem,
+                                                  float s_tensor, const PartialSrc &add, const EpiPre<BN> &pre)
+{
+    if (p.out_type == kOutE4M3) {
+        epilogue_rows_wide<BN, true>(p, trow, m_row0, n0, lane, s_tensor, add);
+        return true;
+    }
+    if (p.out_type == kOutF32)
+        return epilogue_blocks<BN, true>(p, tmap_out, maps, W, e, trow, m_row0, n0, lane, stage, stage_smem, s_tensor,
+                                         add, pre);
+    return epilogue_blocks<BN, false>(p, tmap_out, maps, W, e, trow, m_row0, n0, lane, stage, stage_smem, s_tensor,
+                                      add, pre);
 }
 
 template <int CH>
@@ -1450,6 +1559,12 @@ __global__ void __launch_bounds__(TileCfg<BN, SWAP, WIDE>::kThreads, 1)
         ptx::prefetch_tmap(&tmap_q);
         if (p.out_tma)
             ptx::prefetch_tmap(&tmap_out);
+        if constexpr (EPI && !SWAP) {
+            if (p.e.in_tma)
+                ptx::prefetch_tmap(&epi_maps.in);
+            if (p.e.pre_tma)
+                ptx::prefetch_tmap(&epi_maps.pre);
+        }
     }
     if (warp == 1) {
         ptx::tmem_alloc(ptx::smem_addr(tmem_slot), C::kTmemCols);
@@ -1595,9 +1710,11 @@ __global__ void __launch_bounds__(TileCfg<BN, SWAP, WIDE>::kThreads, 1)
             // TILE: this warp's column scales and biases for the tile, in flight
             // during the wait (per-tensor without bias has none to load)
             ColPre<kWarpCols> pre{};
+            EpiPre<kWarpCols> epre{};
             if constexpr (EPI && !SWAP) {
                 if (p.splits == 1)
-                    epi_begin_tile(pb, epi_maps, pipe, stage_smem, w.tp * kTileP + q * 32, w.tq * BN + col0, lane);
+                    epre = epi_begin_tile<kWarpCols>(pb, epi_maps, pipe, stage_smem, w.tp * kTileP + q * 32,
+                                                     w.tq * BN + col0, lane);
             }
             if (!EPI && !SWAP && p.splits == 1 && (p.rowwise || p.bias != nullptr))
                 pre = load_col_pre<kWarpCols>(pb, w.tq * BN + col0, lane);
@@ -1610,7 +1727,7 @@ __global__ void __launch_bounds__(TileCfg<BN, SWAP, WIDE>::kThreads, 1)
                 if constexpr (EPI && !SWAP) {
                     if (!epilogue_rows_ext<kWarpCols>(pb, &tmap_out, epi_maps, W, pipe, trow + col0,
                                                       w.tp * kTileP + q * 32, w.tq * BN + col0, lane, stage, stage_smem,
-                                                      s_tensor, PartialSrc{}))
+                                                      s_tensor, PartialSrc{}, epre))
                         break;
                 } else if constexpr (!SWAP) {
                     // the grouped plain-store loop: the 256-wide kernels, which

@@ -197,6 +197,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThr
         ptx::prefetch_tmap(&tmap_b);
         if (!SWAP && p.out_tma)
             ptx::prefetch_tmap(&tmap_out);
+        if constexpr (EPI && !SWAP) {
+            if (p.e.in_tma)
+                ptx::prefetch_tmap(&epi_maps.in);
+            if (p.e.pre_tma)
+                ptx::prefetch_tmap(&epi_maps.pre);
+        }
     }
     if (warp == 1) {
         ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), C::kTmemCols);
@@ -371,10 +377,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThr
             kb_total += w.kb1 - w.kb0;
             const KernelParams pb = for_item(p, w.b);
             const float s_tensor = tensor_scale(pb);
+            EpiPre<kWarpCols> epre{};
             if constexpr (EPI && !SWAP) {
                 if (pw.kind != 2 && p.splits == 1)
-                    epi_begin_tile(pb, epi_maps, pipe, stage_smem, w.tp * 256 + static_cast<int>(rank) * 128 + q * 32,
-                                   w.tq * BN + col0, lane);
+                    epre = epi_begin_tile<kWarpCols>(pb, epi_maps, pipe, stage_smem,
+                                                     w.tp * 256 + static_cast<int>(rank) * 128 + q * 32,
+                                                     w.tq * BN + col0, lane);
             }
             if (!W.wait(tfull_bar(acc), acc_phase, 5))
                 break;
@@ -440,7 +448,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EpiShape<SWAP>::kThr
                         // a wait that ran out leaves the flags to fp8mm_device_status
                         if (!epilogue_rows_ext<kWarpCols>(pb, &tmap_out, epi_maps, W, pipe, trow + col0,
                                                           w.tp * 256 + static_cast<int>(rank) * 128 + q * 32,
-                                                          w.tq * BN + col0, lane, stage, stage_smem, s_tensor, add))
+                                                          w.tq * BN + col0, lane, stage, stage_smem, s_tensor, add, epre))
                             break;
                     } else {
                         epilogue_rows_staged<kWarpCols, 1>(pb, &tmap_out, trow + col0,
