@@ -589,7 +589,7 @@ def fp8_act_grad(dy, z, activation: int, dz=None, dbias=None, stream=None, retur
     if dbias is not None:
         _vector("dbias", dbias, N, (torch.float32,))
         ws_bytes = _workspace_bytes("fp8_act_grad_workspace", dy.get_device(), M, N)
-        ws = _new(dy, ws_bytes, torch.uint8, stream)
+        ws = _new(dy, ws_bytes, torch.uint8, stream) if ws_bytes else None
     _check(load().fp8_act_grad(_ptr(dy), lddy, _ptr(z), ldz, _ROW[dy.dtype], int(activation), _ptr(dz), lddz,
                                _ptr(dbias), M, N, _ptr(ws), ws_bytes, _stream_handle(stream)))
     return dz, dbias
@@ -659,7 +659,7 @@ def fp8_layer_norm_grad(dy, x, gamma, mean, rstd, residual_grad=None, dx=None, s
         ws_bytes = _workspace_bytes("fp8_layer_norm_grad_workspace", x.get_device(), R, C)
         dgamma = _new(x, C, torch.float32, stream)
         dbeta = _new(x, C, torch.float32, stream)
-        ws = _new(x, ws_bytes, torch.uint8, stream)
+        ws = _new(x, ws_bytes, torch.uint8, stream) if ws_bytes else None
     _check(load().fp8_layer_norm_grad(_ptr(dy), _ROW[dy.dtype], lddy, _ptr(x), _ROW[x.dtype], ldx, _ptr(gamma),
                                       OUT_F32 if gamma is None else _ROW[gamma.dtype], _ptr(mean), _ptr(rstd),
                                       _ptr(residual_grad), lddres, _ptr(dx), lddx, _ptr(dgamma), _ptr(dbeta), R, C,

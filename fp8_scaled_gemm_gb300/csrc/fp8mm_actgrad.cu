@@ -20,6 +20,13 @@ int64_t slabs_for(int64_t M, int64_t N, int sms)
     return std::max<int64_t>(1, std::min<int64_t>({cdiv(M, 2 * turn), static_cast<int64_t>(sms) * 16 / strips, 65535}));
 }
 
+// A single slab's sums go straight to dbias (one token of 4096: 1.9 us, through
+// a workspace and a second launch 3.5).
+int64_t partial_bytes(int64_t slabs, int64_t N)
+{
+    return slabs == 1 ? 0 : slabs * N * static_cast<int64_t>(sizeof(float));
+}
+
 template <int ES, int G, int LANES>
 int launch_lanes(const ActGradParams &p, int64_t slabs, cudaStream_t stream)
 {
@@ -54,7 +61,7 @@ int64_t fp8_act_grad_workspace(int64_t M, int64_t N)
     const int rc = device_sms(&sms);
     if (rc != FP8MM_OK)
         return rc;
-    return M == 0 || N == 0 ? 0 : slabs_for(M, N, sms) * N * static_cast<int64_t>(sizeof(float));
+    return M == 0 || N == 0 ? 0 : partial_bytes(slabs_for(M, N, sms), N);
 }
 
 int fp8_act_grad(const void *dy, int64_t lddy, const void *z, int64_t ldz, int type, int activation, void *dz,
@@ -101,11 +108,12 @@ int fp8_act_grad(const void *dy, int64_t lddy, const void *z, int64_t ldz, int t
         return rc;
     const int64_t slabs = slabs_for(M, N, sms);
     if (dbias) {
-        if (!workspace)
+        const int64_t need = partial_bytes(slabs, N);
+        if (need > 0 && !workspace)
             return FP8MM_ERR_NULL;
-        if (workspace_bytes < slabs * N * static_cast<int64_t>(sizeof(float)))
+        if (workspace_bytes < need)
             return FP8MM_ERR_SHAPE;
-        p.partial = static_cast<float *>(workspace);
+        p.partial = need > 0 ? static_cast<float *>(workspace) : dbias;
     }
     const bool vec = N % 8 == 0 && rows_vec(dy, p.ldy, type) && (!p.z || rows_vec(z, p.ldz, type)) &&
                      (!dz || rows_vec(dz, p.ldd, type));
@@ -113,7 +121,7 @@ int fp8_act_grad(const void *dy, int64_t lddy, const void *z, int64_t ldz, int t
         rc = vec ? launch<4, 8>(p, slabs, s) : launch<4, 1>(p, slabs, s);
     else
         rc = vec ? launch<2, 8>(p, slabs, s) : launch<2, 1>(p, slabs, s);
-    if (rc != FP8MM_OK || !dbias)
+    if (rc != FP8MM_OK || !dbias || slabs == 1)
         return rc;
     fp8rows::PartialSumParams sum{};
     sum.partial = p.partial;

@@ -7,7 +7,7 @@
 // instructions for the slope. A warp covers 8 LANES columns and 32 / LANES
 // rows at a time (LANES < 32 for narrow matrices), NR times over, so that
 // enough loads are in flight (16384 x 14336 bf16 gelu: one row of 256 columns
-// per warp 296 us, two NOTE); each lane keeps the sums of its columns in
+// per warp 296 us, two 279; with the slabs in whole waves of CTAs 240); each lane keeps the sums of its columns in
 // registers over the rows of its slab (blockIdx.y). The CTA's warps add theirs
 // in order, and the slabs' partials are added by fp8rows::partial_sum_kernel.
 #pragma once
@@ -25,7 +25,7 @@ struct ActGradParams {
     int type, act;
     void *dz;                  // nullptr: not wanted
     long long ldd;
-    float *partial;            // [slabs][N], or nullptr
+    float *partial;            // [slabs][N] (one slab: dbias itself), or nullptr
     long long M, N;
 };
 

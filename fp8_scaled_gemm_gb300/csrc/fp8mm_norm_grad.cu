@@ -153,6 +153,8 @@ int fp8_layer_norm_grad(const void *dy, int dy_type, int64_t lddy, const void *x
                           static_cast<const void *>(workspace)})
         if ((rc = check_rows(f, 0, C, FP8MM_OUT_F32)) != FP8MM_OK)
             return rc;
+    if (reinterpret_cast<uintptr_t>(workspace) & 15)
+        return FP8MM_ERR_ALIGN;
     if (!dgamma != !dbeta)
         return FP8MM_ERR_NULL;
     if (C == 0 || (R == 0 && !dgamma))

@@ -412,8 +412,8 @@ int fp8_scaled_mm_act_grad(const void *A, const void *B,
  *              be NULL (not wanted), or dy or z itself with the same stride.
  *   dbias      fp32 [N], or NULL (not wanted).
  *   workspace  device memory of at least fp8_act_grad_workspace(M, N) bytes,
- *              4-byte aligned, when dbias is wanted; its contents are
- *              scratch of this call. Calls on different streams with
+ *              4-byte aligned, when dbias is wanted (NULL where that is 0);
+ *              its contents are scratch of this call. Calls on different streams with
  *              workspaces of their own do not interfere.
  *
  * M == 0 gives a dbias of zeros. The sums are added in an order that depends
@@ -472,8 +472,8 @@ int fp8_layer_norm(const void *x, int x_type, int64_t ldx,
  *              with the same stride, but not x or dy.
  *   dgamma, dbeta  both or neither.
  *   workspace  device memory of at least fp8_layer_norm_grad_workspace(R, C)
- *              bytes, 4-byte aligned, when dgamma and dbeta are wanted;
- *              scratch of this call.
+ *              bytes, 16-byte aligned, when dgamma and dbeta are wanted (NULL
+ *              where that is 0); scratch of this call.
  *
  * R == 0 gives parameter gradients of zeros. The sums are added in an order
  * that depends on the sizes, alignment and SM count only, so results repeat.

@@ -83,7 +83,8 @@ def test_parts(dz, dbias, act, N):
 
 
 @pytest.mark.parametrize("N,ld,shift", [(264, (272, 280, 288), 0), (264, (265, 270, 271), 0), (264, (264, 264, 264), 1),
-                                        (263, (263, 300, 302), 3)])
+                                        (263, (263, 300, 302), 3), (264, (265, 267, 269), 0),
+                                        (264, (265, 267, 269), 1), (100, (101, 101, 103), 0)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_strides_and_alignment(N, ld, shift, dtype):
     _need_gpu()

@@ -77,7 +77,7 @@ def forward(R, C, *, x_dtype=BF16, y_dtype=None, p_dtype=F32, q_dtype=torch.floa
 
 
 WIDTHS = [1, 2, 7, 8, 24, 33, 64, 120, 255, 256, 264, 512, 520, 1000, 1024, 1032, 2048, 2056, 4095, 4096, 4104, 8192,
-          8200, 8193, 16384, 16385, 16392, 32768, 32776, 40000, 65544, 70001]
+          8200, 8193, 16384, 16385, 16392, 20001, 32768, 32776, 33001, 40000, 65544, 70001]
 
 
 @pytest.mark.parametrize("C", WIDTHS)
@@ -98,6 +98,8 @@ def test_forward_many_rows():
     _need_gpu()
     forward(40000, 24, q_dtype=torch.float8_e5m2)
     forward(20000, 33)
+    forward(2001, 1001)
+    forward(1500, 4999)
 
 
 @pytest.mark.parametrize("p_dtype", [BF16, F16, F32])
@@ -209,6 +211,10 @@ def test_backward_many_rows():
     backward(20000, 33)
     backward(3000, 520, x_dtype=F32)
     backward(700, 16392)
+    backward(700, 16391)
+    backward(301, 8195)
+    backward(2001, 255)
+    backward(2000, 1001)
 
 
 @pytest.mark.parametrize("C", [264, 265, 40000])
@@ -220,6 +226,8 @@ def test_backward_parts(C, gamma, residual, params, p_dtype):
 
 
 @pytest.mark.parametrize("C,ld,shift", [(264, (272, 280, 288, 296), 0), (264, (265, 264, 270, 271), 0),
+                                        (264, (265, 265, 267, 269), 0), (264, (265, 265, 267, 269), 1),
+                                        (1264, (1265, 1265, 1267, 1269), 0),
                                         (264, (264, 264, 264, 264), 1), (263, (263, 300, 301, 302), 3),
                                         (40000, (40008, 40000, 40016, 40000), 0)])
 @pytest.mark.parametrize("x_dtype", [BF16, F32])
@@ -242,7 +250,7 @@ def test_backward_of_no_rows_and_repeatability():
     assert dx.shape == (0, 40) and not dg.any() and not db.any()
     y, mean, rstd = fm.fp8_layer_norm(e)
     assert y.shape == (0, 40) and mean.numel() == 0
-    for C in (1000, 1001, 40000):
+    for C in (1000, 1001, 5001, 40000):
         x, dy = rows(700, C, BF16, 1).cuda(), rows(700, C, BF16, 2).cuda()
         y, mean, rstd = fm.fp8_layer_norm(x)
         first = fm.fp8_layer_norm_grad(dy, x, None, mean, rstd)

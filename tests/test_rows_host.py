@@ -69,6 +69,11 @@ def test_layer_norm_grad_refusals(lib, kw, code):
     assert norm_grad(lib, **kw) == code
 
 
+@pytest.mark.parametrize("off", [4, 8, 12])
+def test_layer_norm_grad_workspace_is_stored_to_in_16_bytes(lib, off):
+    assert norm_grad(lib, ws=AT + 4096 + off) == -3
+
+
 def test_empty_gradient_is_a_noop(lib):
     assert norm_grad(lib, C=0) == 0
     assert norm_grad(lib, R=0, dg=None, db=None) == 0
