@@ -1180,7 +1180,8 @@ __device__ __forceinline__ void epilogue_rows_staged(const KernelParams &p, cons
 // global memory and a warp's 8 KB of buffers (one row of 64 bytes, or 128 of
 // fp32, per thread, swizzled so that the eight threads of a quarter-warp hit
 // distinct banks), by TMA when their rows are 16-byte aligned, otherwise by
-// element accesses of neighbouring lanes to neighbouring columns. (Loads and
+// 4-byte asynchronous copies in and element stores of neighbouring lanes to
+// neighbouring columns out. (Loads and
 // stores of a thread's own row touched 32 lines per instruction: 8192 x 8192 x
 // 1024 gelu with residual and z took 186 us; 32 x 64 blocks in two buffers,
 // with z nothing under way ahead, 144; this form 122.)
@@ -1221,46 +1222,81 @@ __device__ __forceinline__ void epi_wait_reads(uint32_t n)
         ptx::bulk_wait_group_read<3>();
 }
 
-// Ask for the block of `in` that lies `ahead` blocks from now. The last stores
-// out of its slot have read it: with four slots one younger group may still
-// read, with two or one it is the youngest.
-__device__ __forceinline__ void epi_fetch(const KernelParams &p, const EpiMaps<true> &maps, EpiPipe &e, uint32_t ahead,
-                                          uint32_t stage_smem, int nb, int m_row0, int lane)
-{
-    const uint32_t mask = epi_slot_mask(p), slot = (e.seq + ahead) & mask;
-    if (lane == 0) {
-        epi_wait_reads(mask == 3u ? 1u : 0u);
-        ptx::mbar_arrive_expect_tx(e.bar + 8u * slot, epi_block_bytes(p));
-        ptx::tma_load_3d(stage_smem + slot * epi_slot_bytes(p), &maps.in, e.bar + 8u * slot, nb, m_row0, 0);
-    }
-    e.pending |= 1u << slot;
-    __syncwarp();
-}
-
 // Byte offset of 16-byte chunk i of row r of a buffer.
 __device__ __forceinline__ int epi_chunk(bool f32, int r, int i)
 {
     return f32 ? r * 128 + ((i ^ (r & 7)) * 16) : r * 64 + ((i ^ ((r >> 1) & 3)) * 16);
 }
 
-// A block of a [M, N] matrix whose rows are not 16-byte aligned, to or from a
-// buffer: lane l moves column nb + l.
-template <typename T>
-__device__ __forceinline__ void epi_plain_load(const KernelParams &p, const void *base, long long ld, uint8_t *buf,
-                                               int m_row0, int nb, int lane)
+// `in` whose rows are not 16-byte aligned comes in 4-byte copies, under way as
+// far ahead as TMA's. 16-bit rows that start between words arrive one element
+// late (their word i holds columns 2 i + 1 and 2 i + 2; epi_read8 puts them
+// right), so no copy starts before its row. (Element loads, waited for block by
+// block, and the same in bf16 at 8192 x 8191 x 512: gelu with residual and z 282
+// us, now 212; residual alone 198 and 147; gradient 217 and 156.)
+__device__ __forceinline__ bool epi_late(const KernelParams &p, int m, int nb)
 {
-    constexpr bool f32 = sizeof(T) == 4;
-    constexpr int per = 16 / static_cast<int>(sizeof(T));
-    const int col = nb + lane, rows = col < p.N ? min(32, p.M - m_row0) : 0;
-    const T *src = static_cast<const T *>(base) + static_cast<size_t>(m_row0) * ld + col;
-#pragma unroll
-    for (int r = 0; r < 32; ++r) {
-        const T v = r < rows ? src[static_cast<size_t>(r) * ld] : static_cast<T>(0);
-        *reinterpret_cast<T *>(buf + epi_chunk(f32, r, lane / per) + (lane % per) * static_cast<int>(sizeof(T))) = v;
-    }
-    __syncwarp();
+    return !epi_f32(p) &&
+           (((reinterpret_cast<uintptr_t>(p.e.in) >> 1) + static_cast<uintptr_t>(m) * p.e.ld_in + nb) & 1u) != 0;
 }
 
+__device__ __forceinline__ void epi_fetch_words(const KernelParams &p, uint32_t dst, int nb, int m_row0, int lane)
+{
+    if (epi_f32(p)) {
+        const int rows = nb + lane < p.N ? p.M - m_row0 : 0;
+        const float *src = static_cast<const float *>(p.e.in) + static_cast<long long>(m_row0) * p.e.ld_in + nb + lane;
+        dst += (lane & 3) * 4;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+            if (r < rows)
+                ptx::cp_async4(dst + epi_chunk(true, r, lane >> 2), src, 4);
+            src += p.e.ld_in;
+        }
+    } else {
+        // two rows at a time; every second row starts alike
+        const int h = lane >> 4, w = lane & 15;
+        const int e0 = 2 * w + (epi_late(p, m_row0 + h, nb) ? 1 : 0), left = p.N - nb - e0;
+        const int rows = left > 0 ? p.M - m_row0 - h : 0;
+        const uint32_t bytes = left > 1 ? 4 : 2;
+        const unsigned short *src =
+            static_cast<const unsigned short *>(p.e.in) + static_cast<long long>(m_row0 + h) * p.e.ld_in + nb + e0;
+        dst += (w & 3) * 4;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            if (2 * j < rows)
+                ptx::cp_async4(dst + epi_chunk(false, 2 * j + h, w >> 2), src, bytes);
+            src += 2 * p.e.ld_in;
+        }
+    }
+}
+
+// Ask for the block of `in` that lies `ahead` blocks from now. The last stores
+// out of its slot have read it: with four slots one younger group may still
+// read, with two or one it is the youngest.
+template <bool WORDS>
+__device__ __forceinline__ void epi_fetch(const KernelParams &p, const EpiMaps<true> &maps, EpiPipe &e, uint32_t ahead,
+                                          uint32_t stage_smem, int nb, int m_row0, int lane)
+{
+    const uint32_t mask = epi_slot_mask(p), slot = (e.seq + ahead) & mask;
+    if constexpr (WORDS) {
+        if (lane == 0)
+            epi_wait_reads(mask == 3u ? 1u : 0u);
+        __syncwarp();
+        epi_fetch_words(p, stage_smem + slot * epi_slot_bytes(p), nb, m_row0, lane);
+        ptx::cp_async_commit();
+    } else {
+        if (lane == 0) {
+            epi_wait_reads(mask == 3u ? 1u : 0u);
+            ptx::mbar_arrive_expect_tx(e.bar + 8u * slot, epi_block_bytes(p));
+            ptx::tma_load_3d(stage_smem + slot * epi_slot_bytes(p), &maps.in, e.bar + 8u * slot, nb, m_row0, 0);
+        }
+        e.pending |= 1u << slot;
+        __syncwarp();
+    }
+}
+
+// A block of an output whose rows are not 16-byte aligned, from a buffer: lane
+// l moves column nb + l.
 template <typename T>
 __device__ __forceinline__ void epi_plain_store(const KernelParams &p, void *base, long long ld, const uint8_t *buf,
                                                 int m_row0, int nb, int lane)
@@ -1274,13 +1310,17 @@ __device__ __forceinline__ void epi_plain_store(const KernelParams &p, void *bas
         const T v = *reinterpret_cast<const T *>(buf + epi_chunk(f32, r, lane / per) +
                                                  (lane % per) * static_cast<int>(sizeof(T)));
         if (r < rows)
-            dst[static_cast<size_t>(r) * ld] = v;
+            *dst = v;
+        dst += ld;
     }
 }
 
-// 8 columns 8 i .. 8 i + 7 of the thread's row of a buffer.
-template <bool F32>
-__device__ __forceinline__ void epi_read8(bool f16, const uint8_t *buf, int lane, int i, float (&r)[8])
+// 8 columns 8 i .. 8 i + 7 of the thread's row of a buffer. 16-bit rows of 4-byte
+// copies (words): `select` is 0x5432 for a row that is one element late, else
+// 0x7654, and prev the word before.
+template <bool F32, bool WORDS>
+__device__ __forceinline__ void epi_read8(bool f16, const uint8_t *buf, int lane, int i, float (&r)[8], uint32_t select,
+                                          uint32_t &prev)
 {
     if constexpr (F32) {
 #pragma unroll
@@ -1292,7 +1332,15 @@ __device__ __forceinline__ void epi_read8(bool f16, const uint8_t *buf, int lane
             r[4 * h + 3] = x.w;
         }
     } else {
-        const uint4 w = *reinterpret_cast<const uint4 *>(buf + epi_chunk(false, lane, i));
+        uint4 w = *reinterpret_cast<const uint4 *>(buf + epi_chunk(false, lane, i));
+        if constexpr (WORDS) {
+            const uint32_t next = w.w;
+            w.w = __byte_perm(w.z, w.w, select);
+            w.z = __byte_perm(w.y, w.z, select);
+            w.y = __byte_perm(w.x, w.y, select);
+            w.x = __byte_perm(prev, w.x, select);
+            prev = next;
+        }
         aux_unpack2(w.x, f16, r[0], r[1]);
         aux_unpack2(w.y, f16, r[2], r[3]);
         aux_unpack2(w.z, f16, r[4], r[5]);
@@ -1328,17 +1376,32 @@ template <int BN>
 struct EpiPre {
     ColPre<BN> col;
     float sa;
+    uint32_t first;      // bits of the thread's first element of `in`, where its row is late
 };
+
+// Whether `in` moves in blocks.
+__device__ __forceinline__ bool epi_blocks_in(const KernelParams &p) { return p.e.in != nullptr && p.out_type != kOutE4M3; }
 
 // Before the accumulator wait: the scales and biases, and the first blocks of `in`.
 template <int BN>
 __device__ __forceinline__ EpiPre<BN> epi_begin_tile(const KernelParams &p, const EpiMaps<true> &maps, EpiPipe &e,
                                                      uint32_t stage_smem, int m_row0, int n0, int lane)
 {
-    if (p.e.in_tma)
-        for (int b = 0; b < max(1, epi_ahead(p)); ++b)
-            epi_fetch(p, maps, e, b, stage_smem, n0 + 32 * b, m_row0, lane);
     EpiPre<BN> pre{};
+    if (epi_blocks_in(p)) {
+        const int blocks = max(1, epi_ahead(p));
+        if (p.e.in_tma) {
+            for (int b = 0; b < blocks; ++b)
+                epi_fetch<false>(p, maps, e, b, stage_smem, n0 + 32 * b, m_row0, lane);
+        } else {
+#pragma unroll 1
+            for (int b = 0; b < blocks; ++b)
+                epi_fetch<true>(p, maps, e, b, stage_smem, n0 + 32 * b, m_row0, lane);
+            if (m_row0 + lane < p.M && n0 < p.N && epi_late(p, m_row0 + lane, n0))
+                pre.first = __ldg(static_cast<const unsigned short *>(p.e.in) +
+                                  static_cast<long long>(m_row0 + lane) * p.e.ld_in + n0);
+        }
+    }
     if (p.rowwise || p.bias != nullptr)
         pre.col = load_col_pre<BN>(p, n0, lane);
     pre.sa = (p.rowwise && m_row0 + lane < p.M) ? __ldg(p.scale_a + m_row0 + lane) : 0.0f;
@@ -1348,6 +1411,7 @@ __device__ __forceinline__ EpiPre<BN> epi_begin_tile(const KernelParams &p, cons
 // Loads still in flight land before the CTA may leave.
 __device__ __forceinline__ void epi_drain(const Waiter &W, EpiPipe &e)
 {
+    ptx::cp_async_wait<0>();
 #pragma unroll
     for (uint32_t b = 0; b < 4; ++b)
         if (e.pending >> b & 1u)
@@ -1355,9 +1419,10 @@ __device__ __forceinline__ void epi_drain(const Waiter &W, EpiPipe &e)
 }
 
 // The extended form of epilogue_rows_staged for fp32 (F32) or 16-bit matrices:
-// one warp's 32 accumulator rows x BN columns, 32 at a time. Returns false when
-// a wait ran out.
-template <int BN, bool F32>
+// one warp's 32 accumulator rows x BN columns, 32 at a time. WORDS: `in` comes in
+// 4-byte copies (else by TMA, or there is none). Returns false when a wait ran
+// out.
+template <int BN, bool F32, bool WORDS>
 __device__ __forceinline__ bool epilogue_blocks(const KernelParams &p, const CUtensorMap *tmap_out,
                                                   const EpiMaps<true> &maps, const Waiter &W, EpiPipe &e, uint32_t trow,
                                                   int m_row0, int n0, int lane, uint8_t *stage, uint32_t stage_smem,
@@ -1369,12 +1434,14 @@ __device__ __forceinline__ bool epilogue_blocks(const KernelParams &p, const CUt
     const bool f16 = p.out_type == kOutF16, has_in = p.e.in != nullptr, has_pre = p.e.pre != nullptr;
     const int ahead = epi_ahead(p);
     const uint32_t mask = epi_slot_mask(p), slot_bytes = epi_slot_bytes(p);
+    const uint32_t select = WORDS && epi_late(p, m_row0 + lane, n0) ? 0x5432u : 0x7654u;
+    uint32_t prev = pre.first << 16;
 #pragma unroll 1
     for (int c = 0; c < BN / 32; ++c) {
         const int nb = n0 + c * 32;
         const uint32_t slot = e.seq & mask;
-        if (p.e.in_tma && ahead > 0 && c + ahead < BN / 32)
-            epi_fetch(p, maps, e, ahead, stage_smem, nb + 32 * ahead, m_row0, lane);
+        if ((WORDS || p.e.in_tma) && ahead > 0 && c + ahead < BN / 32)
+            epi_fetch<WORDS>(p, maps, e, ahead, stage_smem, nb + 32 * ahead, m_row0, lane);
         // the front of a register queue that moves on after every block
         const float sbl = pre.col.sb[0], bl = pre.col.b[0];
 #pragma unroll
@@ -1383,13 +1450,11 @@ __device__ __forceinline__ bool epilogue_blocks(const KernelParams &p, const CUt
             pre.col.b[i] = pre.col.b[i + 1];
         }
         uint8_t *const out_buf = stage + slot * slot_bytes, *const z_buf = out_buf + block_bytes;
-        if (!p.e.in_tma) {
+        if (!WORDS && !p.e.in_tma) {
             // the last stores out of this slot have read it
             if (lane == 0)
                 epi_wait_reads(mask);
             __syncwarp();
-            if (has_in)
-                epi_plain_load<Bits>(p, p.e.in, p.e.ld_in, out_buf, m_row0, nb, lane);
         }
         float y[32];
         ptx::tmem_ld_32cols(trow + static_cast<uint32_t>(c * 32), y);
@@ -1422,18 +1487,29 @@ __device__ __forceinline__ bool epilogue_blocks(const KernelParams &p, const CUt
             for (int j = 0; j < 32; ++j)
                 y[j] *= s_tensor;
         }
-        if (p.e.in_tma) {
+        if (!WORDS && p.e.in_tma) {
             // (the slot was free before the fetch)
             if (!W.wait(e.bar + 8u * slot, e.phases >> slot & 1u, 9))
                 return false;
             e.pending &= ~(1u << slot);
             e.phases ^= 1u << slot;
         }
+        if constexpr (WORDS) {
+            // blocks asked for after this one may be under way
+            const int younger = min(ahead, BN / 32 - 1 - c);
+            if (younger >= 2)
+                ptx::cp_async_wait<2>();
+            else if (younger == 1)
+                ptx::cp_async_wait<1>();
+            else
+                ptx::cp_async_wait<0>();
+            __syncwarp();
+        }
         if (p.e.grad) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float r[8], v[8];
-                epi_read8<F32>(f16, out_buf, lane, i, r);
+                epi_read8<F32, WORDS>(f16, out_buf, lane, i, r, select, prev);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     v[j] = y[8 * i + j];
@@ -1450,7 +1526,7 @@ __device__ __forceinline__ bool epilogue_blocks(const KernelParams &p, const CUt
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float r[8];
-                    epi_read8<F32>(f16, out_buf, lane, i, r);
+                    epi_read8<F32, WORDS>(f16, out_buf, lane, i, r, select, prev);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         y[8 * i + j] += r[j];
@@ -1473,8 +1549,8 @@ __device__ __forceinline__ bool epilogue_blocks(const KernelParams &p, const CUt
             epi_plain_store<Bits>(p, p.e.pre, p.e.ld_pre, z_buf, m_row0, nb, lane);
         __syncwarp();
         ++e.seq;
-        if (p.e.in_tma && ahead == 0 && c + 1 < BN / 32)
-            epi_fetch(p, maps, e, 0, stage_smem, nb + 32, m_row0, lane);
+        if ((WORDS || p.e.in_tma) && ahead == 0 && c + 1 < BN / 32)
+            epi_fetch<WORDS>(p, maps, e, 0, stage_smem, nb + 32, m_row0, lane);
     }
     return true;
 }
@@ -1489,11 +1565,16 @@ __device__ __forceinline__ bool epilogue_rows_ext(const KernelParams &p, const C
         epilogue_rows_wide<BN, true>(p, trow, m_row0, n0, lane, s_tensor, add);
         return true;
     }
+    const bool words = p.e.in != nullptr && !p.e.in_tma;
     if (p.out_type == kOutF32)
-        return epilogue_blocks<BN, true>(p, tmap_out, maps, W, e, trow, m_row0, n0, lane, stage, stage_smem, s_tensor,
-                                         add, pre);
-    return epilogue_blocks<BN, false>(p, tmap_out, maps, W, e, trow, m_row0, n0, lane, stage, stage_smem, s_tensor,
-                                      add, pre);
+        return words ? epilogue_blocks<BN, true, true>(p, tmap_out, maps, W, e, trow, m_row0, n0, lane, stage, stage_smem,
+                                                       s_tensor, add, pre)
+                     : epilogue_blocks<BN, true, false>(p, tmap_out, maps, W, e, trow, m_row0, n0, lane, stage, stage_smem,
+                                                        s_tensor, add, pre);
+    return words ? epilogue_blocks<BN, false, true>(p, tmap_out, maps, W, e, trow, m_row0, n0, lane, stage, stage_smem,
+                                                    s_tensor, add, pre)
+                 : epilogue_blocks<BN, false, false>(p, tmap_out, maps, W, e, trow, m_row0, n0, lane, stage, stage_smem,
+                                                     s_tensor, add, pre);
 }
 
 template <int CH>

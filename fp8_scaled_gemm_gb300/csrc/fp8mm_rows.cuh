@@ -36,9 +36,7 @@ __device__ __forceinline__ void load_raw(Raw<ES, G> &r, const void *base, long l
     const uint8_t *p = static_cast<const uint8_t *>(base) + elem * ES;
     if constexpr (G == 1) {
         if constexpr (ES == 2) {
-            unsigned short h;
-            asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(h) : "l"(p));
-            r.w[0] = h;
+            asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=r"(r.w[0]) : "l"(p));   // zero-extends
         } else {
             asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(r.w[0]) : "l"(p));
         }

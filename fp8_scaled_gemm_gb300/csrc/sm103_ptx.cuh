@@ -371,6 +371,23 @@ __device__ __forceinline__ void bulk_wait_group_all()
 }
 
 
+// Asynchronous copy of `bytes` (0 .. 4, the rest zero) from global memory to 4
+// bytes of shared memory; both addresses 4-byte aligned.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(__cvta_generic_to_global(src)), "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// At most N of this thread's groups of copies are still under way.
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Store a float to the shared memory of a CTA in the cluster (address from mapa).
 __device__ __forceinline__ void st_shared_cluster_f32(uint32_t cluster_addr, float v)
 {
