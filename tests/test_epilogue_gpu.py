@@ -52,7 +52,7 @@ def strided(t, ld, shift=0):
 
 def forward(M, N, K, *, rowwise=True, act="gelu", bias=True, residual=True, preact=True, dtype=torch.bfloat16,
             a_dtype="e4m3", variant=AUTO, tile_n=0, split_k=0, ldr=None, ldp=None, ldo=None, shift=0, in_place=False,
-            seed=3):
+            seed=3, rshift=0):
     import fp8_scaled_gemm_gb300 as fm
     A, Bt, sa, sb = problem(M, N, K, rowwise, seed, a_dtype)
     aux = AUX[dtype]
@@ -74,7 +74,7 @@ def forward(M, N, K, *, rowwise=True, act="gelu", bias=True, residual=True, prea
         out.copy_(r)
         rg = out
     else:
-        rg = strided(r, ldr or N, shift) if residual else None
+        rg = strided(r, ldr or N, shift + rshift) if residual else None
     pg = strided(torch.full((M, N), float("nan")).to(aux), ldp or N, shift) if preact else None
     ret = fm.fp8_scaled_mm_epilogue(A.cuda(), Bt.cuda().t(), sa.cuda(), sb.cuda(), int(rowwise), bias=d(b),
                                     activation=r64.ACTS[act], residual=rg, preact=pg, out=out, variant=variant,
@@ -168,7 +168,7 @@ def test_forward_non_finite_values(M, act):
 
 
 def gradient(M, N, K, *, act="gelu", dtype=torch.bfloat16, rowwise=True, variant=AUTO, tile_n=0, split_k=0, ldz=None,
-             seed=11, in_place=False):
+             seed=11, in_place=False, zshift=0):
     import fp8_scaled_gemm_gb300 as fm
     A, Bt, sa, sb = problem(M, N, K, rowwise, seed, "e5m2")
     z = randn((M, N), AUX[dtype], seed + 1, 2.0)
@@ -176,7 +176,7 @@ def gradient(M, N, K, *, act="gelu", dtype=torch.bfloat16, rowwise=True, variant
     d = r64.slope(r64.f64(z), act)
     want = acc * d
     tol = 1.13 * 2.0 ** -20 * absum + r64.ACT_ERR * np.abs(acc) + 2.0 ** -22 * np.abs(want)
-    zg = strided(z, ldz or N)
+    zg = strided(z, ldz or N, zshift)
     out = zg if in_place else None
     got = fm.fp8_scaled_mm_act_grad(A.cuda(), Bt.cuda().t(), sa.cuda(), sb.cuda(), int(rowwise), zg, r64.ACTS[act],
                                     out=out, out_dtype=dtype, variant=variant, tile_n=tile_n, split_k=split_k)
@@ -280,3 +280,35 @@ def test_results_repeat_and_follow_the_callers_stream():
             outs.append(fm.fp8_scaled_mm_epilogue(t[0], t[1].t(), t[2], t[3], 1, activation=2, residual=t[4]))
         s.synchronize()
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+# Matrices whose rows start between words, between 16-byte pieces, or both in
+# turn, over several column blocks and tiles, the last ones cut.
+UNALIGNED = [(TILE, 128, 300, 421, 272), (TILE, 256, 300, 803, 272), (TILE, 256, 300, 803, 1040),
+             (PAIR, 256, 520, 803, 272), (PAIR, 128, 300, 421, 272), (PAIR, 256, 300, 2600, 4112)]
+
+
+@pytest.mark.parametrize("variant,tile_n,M,N,K", UNALIGNED)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("pad,rshift", [(0, 0), (1, 0), (1, 1), (2, 1), (5, 3)])
+def test_forward_unaligned_residual(variant, tile_n, M, N, K, dtype, pad, rshift):
+    _need_gpu()
+    split = -1 if K > 4000 else 0
+    forward(M, N, K, act="silu", dtype=dtype, preact=pad != 2, ldr=N + pad, rshift=rshift, variant=variant,
+            tile_n=tile_n, split_k=split)
+
+
+@pytest.mark.parametrize("variant,tile_n,M,N,K", UNALIGNED)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_unaligned_in_place(variant, tile_n, M, N, K, dtype):
+    _need_gpu()
+    forward(M, N | 1, K, act="gelu", dtype=dtype, preact=False, in_place=True, variant=variant, tile_n=tile_n)
+    gradient(M, N | 1, K, act="gelu", dtype=dtype, in_place=True, variant=variant, tile_n=tile_n)
+
+
+@pytest.mark.parametrize("variant,tile_n,M,N,K", UNALIGNED)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("pad,zshift", [(0, 1), (1, 0), (2, 1)])
+def test_gradient_unaligned(variant, tile_n, M, N, K, dtype, pad, zshift):
+    _need_gpu()
+    gradient(M, N, K, act="silu", dtype=dtype, ldz=N + pad, zshift=zshift, variant=variant, tile_n=tile_n)
