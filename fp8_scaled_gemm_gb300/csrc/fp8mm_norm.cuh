@@ -709,7 +709,8 @@ struct NormGradParams {
     void *dx;                  // nullptr: not wanted
     long long lddx;
     int x_type;
-    float *partial;            // [CTAs or clusters][2][C]: dgamma and dbeta sums of their rows, or nullptr
+    float *partial, *partial1; // dgamma and dbeta sums of CTA's or cluster's i rows at [i * partial_step], or nullptr
+    long long partial_step;    // (a single one: the results themselves)
     long long R, C;
     long long groups;          // long kernels: element groups per row
     long long slice_cols;      // kCluster: columns of each CTA
@@ -881,7 +882,9 @@ __global__ void __launch_bounds__(KIND > 0 ? kGradLaneThreads : kGradThreads, KI
 #pragma unroll
                 for (int i = 0; i < P; ++i)
                     v[i] = ptx::f32x2(f[2 * i], f[2 * i + 1]);
-                store_e<G, KIND, CH>(reinterpret_cast<uint8_t *>(p.partial + (slot * 2 + k) * p.C + pl.c0), kF32, pl, v);
+                store_e<G, KIND, CH>(
+                    reinterpret_cast<uint8_t *>((k == 0 ? p.partial : p.partial1) + slot * p.partial_step + pl.c0), kF32, pl,
+                    v);
             }
             __syncthreads();
         }
@@ -976,11 +979,11 @@ __global__ void __launch_bounds__(256) norm_grad_cols_kernel(const NormGradParam
             dbe[i] += d[i];
         }
     }
-    float *dst = p.partial + static_cast<long long>(blockIdx.y) * 2 * p.C + g * G;
+    const long long at = static_cast<long long>(blockIdx.y) * p.partial_step + g * G;
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-        dst[i] = dga[i];
-        dst[p.C + i] = dbe[i];
+        p.partial[at + i] = dga[i];
+        p.partial1[at + i] = dbe[i];
     }
 }
 

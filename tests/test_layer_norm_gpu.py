@@ -205,6 +205,14 @@ def test_backward_row_counts(R, C):
     backward(R, C)
 
 
+@pytest.mark.parametrize("R", [1, 2, 4, 5])
+@pytest.mark.parametrize("C", [24, 255, 4096, 4097, 16384, 40000, 40001])
+def test_backward_few_rows(R, C):
+    _need_gpu()
+    backward(R, C)
+    backward(R, C, x_dtype=F32)
+
+
 def test_backward_many_rows():
     _need_gpu()
     backward(40000, 24)
