@@ -1389,6 +1389,17 @@ int device_sms(int *sms)
     return rc;
 }
 
+int device_limit(int **status, unsigned long long *clocks)
+{
+    DeviceState *d = nullptr;
+    const int rc = device_state(&d);
+    if (rc == FP8MM_OK) {
+        *status = d->status;
+        *clocks = wait_limit();
+    }
+    return rc;
+}
+
 }  // namespace fp8mm_host
 
 extern "C" {

@@ -28,6 +28,9 @@ int cuda_fail(cudaError_t e, const char *what);
 // device) and returns its SM count.
 int device_sms(int *sms);
 
+// The current device's status word and the clocks a wait in a kernel may take.
+int device_limit(int **status, unsigned long long *clocks);
+
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Choice {

@@ -32,6 +32,9 @@ int launch_lanes(const NormParams &p, int sms, cudaStream_t stream)
         p, std::min<int64_t>(cdiv(p.R, 256 / LANES), static_cast<int64_t>(sms) * (CH == 4 ? 3 : 4)), 256, stream);
 }
 
+// Longer rows go through the long kernel.
+constexpr int64_t kMostColumns = 1024 * 16 * fp8norm::kMaxCluster;
+
 // A CTA per row, as many of them on an SM as make 1024 threads.
 template <int ES, int G, int CH>
 int launch_cta(const NormParams &p, int sms, cudaStream_t stream)
@@ -39,6 +42,37 @@ int launch_cta(const NormParams &p, int sms, cudaStream_t stream)
     const int threads = static_cast<int>(cdiv(p.C, 32 * 8 * CH)) * 32;
     return launch_norm<ES, G, fp8norm::kCta, CH>(
         p, std::min<int64_t>(p.R, static_cast<int64_t>(sms) * (1024 / threads)), threads, stream);
+}
+
+// A cluster of CTAs per row, two as long as they suffice, else eight (32768
+// bf16 columns with codes: two 194 us, four 298; 65536: four 386, eight 325).
+// The long kernel, which reads the row once per quantity, took 428 and 455.
+template <int ES, int G>
+int launch_cluster(NormParams p, int sms, cudaStream_t stream)
+{
+    constexpr int warp_cols = 32 * 8 * 2;
+    const int64_t warps = cdiv(p.C, warp_cols);
+    const int ctas = warps <= 64 ? 2 : fp8norm::kMaxCluster;
+    const int64_t each = cdiv(warps, ctas);
+    p.slice_cols = each * warp_cols;
+    int rc = device_limit(&p.limit.status, &p.limit.clocks);
+    if (rc != FP8MM_OK)
+        return rc;
+    const int threads = static_cast<int>(each) * 32;
+    const int64_t clusters =
+        std::min<int64_t>(p.R, std::max<int64_t>(1, static_cast<int64_t>(sms) * (1024 / threads) / ctas));
+    auto kern = fp8norm::norm_kernel<ES, G, fp8norm::kCluster, 2>;
+    const int smem = threads * 4 * 2 * 16;
+    static bool attr_set[kMaxDevices] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!attr_set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 * 4 * 2 * 16);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "cudaFuncSetAttribute");
+        attr_set[dev] = true;
+    }
+    return launch_clusters(kern, static_cast<int>(clusters) * ctas, ctas, threads, smem, stream, "layer norm launch", p);
 }
 
 template <int ES>
@@ -53,11 +87,13 @@ int launch(const NormParams &p, bool vec, int sms, cudaStream_t stream)
         if (C <= 512) return launch_lanes<ES, 8, 32, 2>(p, sms, stream);
         if (C <= 1024) return launch_lanes<ES, 8, 32, 4>(p, sms, stream);
         if (C <= 16384) return launch_cta<ES, 8, 2>(p, sms, stream);
+        if (C <= kMostColumns) return launch_cluster<ES, 8>(p, sms, stream);
     } else {
         if (C <= 256) return launch_lanes<ES, 1, 32, 1>(p, sms, stream);
         if (C <= 512) return launch_lanes<ES, 1, 32, 2>(p, sms, stream);
         if (C <= 1024) return launch_lanes<ES, 1, 32, 4>(p, sms, stream);
         if (C <= 16384) return launch_cta<ES, 1, 2>(p, sms, stream);
+        if (C <= kMostColumns) return launch_cluster<ES, 1>(p, sms, stream);
     }
     const int grid = static_cast<int>(std::min<int64_t>(p.R, static_cast<int64_t>(sms) * 8));
     if (vec)

@@ -17,9 +17,9 @@
 //  - A team of threads takes a row and goes on to other rows with the same
 //    columns, E = 8 CH per thread, so that backward's column sums stay in
 //    registers and the next row's loads are issued before the present row's
-//    reductions. A team is 4 to 32 lanes of a warp, some warps of a CTA, or
-//    (backward, wide rows) the CTAs of a cluster, each with a slice of the
-//    columns, that exchange their sums through distributed shared memory.
+//    reductions. A team is 4 to 32 lanes of a warp, a CTA, or (wide rows) the
+//    CTAs of a cluster, each with a slice of the columns, that exchange their
+//    sums through distributed shared memory.
 //  - E is as large as the registers allow: a reduction costs a warp about 30
 //    instructions whatever E is (with E = 8, 43 instructions per element ran
 //    the forward pass at 47 % of HBM; with 32 it is about 12).
@@ -28,8 +28,8 @@
 //    differ by constants. Rows that start on 16 bytes take 16-byte loads of
 //    8 elements; other rows take single elements, neighbouring lanes
 //    neighbouring ones.
-// Rows too long for a team go through the long kernels, which read the row
-// again from L2 for each pass.
+// Rows of more than 131072 columns (backward: of a cluster's eight CTAs) go
+// through the long kernels, which read the row again from L2 for each pass.
 #pragma once
 
 #include "fp8mm_act.cuh"
@@ -42,7 +42,8 @@ using namespace fp8rows;
 
 // ------------------------------------------------------------------ teams ---
 
-constexpr int kMaxCluster = 8;       // CTAs that share a row (backward)
+constexpr int kMaxCluster = 8;       // CTAs that share a row
+constexpr int kStatusTimeout = 0x10b;
 
 // Kinds of team: LANES 4 .. 32 lanes of a warp; kCta all threads of a CTA;
 // kCluster all threads of a cluster's CTAs. (Several teams in a CTA, each
@@ -271,19 +272,55 @@ __device__ __forceinline__ float sum_pairs(const uint64_t (&v)[N])
     return lo + hi;
 }
 
+// What bounds a wait: clocks, and the word that says that one ran out.
+struct Limit {
+    int *status;
+    unsigned long long clocks;
+};
+
 struct Team {
     int T, warps;        // threads and warps of the team in this CTA
     int id;              // team within the CTA
     uint32_t rank, ctas; // place in the cluster
+    uint32_t bar;        // kCluster: mbarriers of its exchanges, 8 bytes each
+    Limit limit;
 };
 
-template <int KIND>
-__device__ __forceinline__ void team_barrier(const Team &tm)
+// Exchange k of a cluster's team: every warp's values go to all its CTAs, into
+// the slot of the warp in their buffer `red`, and are counted there on mbarrier
+// k. (A cluster barrier per exchange waits for the row's global stores as well:
+// forward 4096 x 32768 bf16 with codes 290 us, now 194; backward 8192 x 8192
+// fp32 268, now 177.) An exchange's buffer is free for the one after next: a warp sends for
+// the next one after it has read this one, and this CTA passes the next one
+// with all warps' values. False when the wait ran out.
+template <int NV>
+__device__ __forceinline__ bool cluster_exchange(const float (&v)[NV], const Team &tm, float *red, int k, uint32_t parity)
 {
-    if constexpr (KIND == kCluster)
-        ptx::cluster_sync();
-    else
-        __syncthreads();
+    const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
+    const uint32_t bar = tm.bar + 8u * k;
+    if (threadIdx.x == 0)
+        ptx::mbar_arrive_expect_tx(bar, tm.ctas * tm.warps * NV * 4u);
+    if (lane < static_cast<int>(tm.ctas)) {
+        const uint32_t at = ptx::mapa_shared(ptx::smem_addr(red + (tm.rank * tm.warps + warp) * NV),
+                                             static_cast<uint32_t>(lane)),
+                       there = ptx::mapa_shared(bar, static_cast<uint32_t>(lane));
+        if constexpr (NV == 2)
+            ptx::st_async_f32x2(at, v[0], v[1], there);
+        else
+            ptx::st_async_f32(at, v[0], there);
+    }
+    __syncwarp();
+    bool here = ptx::mbar_try_wait_cluster(bar, parity);
+    if (!here) {
+        const unsigned long long t0 = static_cast<unsigned long long>(clock64());
+        while (!(here = ptx::mbar_try_wait_cluster(bar, parity))) {
+            if (static_cast<unsigned long long>(clock64()) - t0 > tm.limit.clocks) {
+                atomicCAS(tm.limit.status, 0, kStatusTimeout);
+                break;
+            }
+        }
+    }
+    return __all_sync(0xFFFFFFFFu, here);   // the warp stays together
 }
 
 // Words of one reduction's exchange buffer for NV values.
@@ -292,8 +329,9 @@ constexpr int kRedWords = KIND == kCluster ? kMaxCluster * 32 * NV : 32 * NV;
 
 // Sums of NV values over the team, the same bits in every thread. The caller
 // alternates between buffers so that two barriers lie between uses of one.
+// (k, parity: cluster_exchange's; false when its wait ran out.)
 template <int KIND, int NV>
-__device__ __forceinline__ void team_sum8(float (&v)[NV], const Team &tm, float *red)
+__device__ __forceinline__ bool team_sum8(float (&v)[NV], const Team &tm, float *red, int k, uint32_t parity)
 {
     constexpr int L = KIND > 0 ? KIND : 32;
 #pragma unroll
@@ -306,14 +344,8 @@ __device__ __forceinline__ void team_sum8(float (&v)[NV], const Team &tm, float 
         int n = tm.warps;
         const float *mine = red;
         if constexpr (KIND == kCluster) {
-            // lane r hands the warp's sums to CTA r
-            if (lane < static_cast<int>(tm.ctas)) {
-                const uint32_t at = ptx::mapa_shared(
-                    ptx::smem_addr(red + (tm.rank * tm.warps + warp) * NV), static_cast<uint32_t>(lane));
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    ptx::st_shared_cluster_f32(at + 4 * i, v[i]);
-            }
+            if (!cluster_exchange<NV>(v, tm, red, k, parity))
+                return false;
             n *= static_cast<int>(tm.ctas);
         } else {
             if (lane == 0) {
@@ -321,8 +353,8 @@ __device__ __forceinline__ void team_sum8(float (&v)[NV], const Team &tm, float 
                 for (int i = 0; i < NV; ++i)
                     red[warp * NV + i] = v[i];
             }
+            __syncthreads();
         }
-        team_barrier<KIND>(tm);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             v[i] = 0.0f;
@@ -336,12 +368,13 @@ __device__ __forceinline__ void team_sum8(float (&v)[NV], const Team &tm, float 
             for (int i = 0; i < NV; ++i)
                 v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
     }
+    return true;
 }
 
 // Largest of NV magnitudes over the team, on their bit patterns: unsigned
 // order is the order of |v| with NaN above infinity.
 template <int KIND, int NV>
-__device__ __forceinline__ void team_amax8(float (&v)[NV], const Team &tm, float *red)
+__device__ __forceinline__ bool team_amax8(float (&v)[NV], const Team &tm, float *red, int k, uint32_t parity)
 {
     uint32_t u[NV];
 #pragma unroll
@@ -363,13 +396,11 @@ __device__ __forceinline__ void team_amax8(float (&v)[NV], const Team &tm, float
         int n = tm.warps;
         const float *mine = red;
         if constexpr (KIND == kCluster) {
-            if (lane < static_cast<int>(tm.ctas)) {
-                const uint32_t at = ptx::mapa_shared(
-                    ptx::smem_addr(red + (tm.rank * tm.warps + warp) * NV), static_cast<uint32_t>(lane));
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    ptx::st_shared_cluster_f32(at + 4 * i, __uint_as_float(u[i]));
-            }
+            for (int i = 0; i < NV; ++i)
+                v[i] = __uint_as_float(u[i]);
+            if (!cluster_exchange<NV>(v, tm, red, k, parity))
+                return false;
             n *= static_cast<int>(tm.ctas);
         } else {
             if (lane == 0) {
@@ -377,8 +408,8 @@ __device__ __forceinline__ void team_amax8(float (&v)[NV], const Team &tm, float
                 for (int i = 0; i < NV; ++i)
                     red[warp * NV + i] = __uint_as_float(u[i]);
             }
+            __syncthreads();
         }
-        team_barrier<KIND>(tm);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             u[i] = 0;
@@ -393,11 +424,13 @@ __device__ __forceinline__ void team_amax8(float (&v)[NV], const Team &tm, float
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         v[i] = __uint_as_float(u[i]);
+    return true;
 }
 
-// The team this thread belongs to, and which of all teams it is.
-template <int KIND>
-__device__ __forceinline__ Team this_team(int &t, long long &first, long long &stride)
+// The team this thread belongs to, and which of all teams it is. bars: room for
+// a cluster's mbarriers.
+template <int KIND, int BARS>
+__device__ __forceinline__ Team this_team(int &t, long long &first, long long &stride, uint64_t *bars, const Limit &limit)
 {
     Team tm{};
     if constexpr (KIND > 0) {
@@ -422,6 +455,14 @@ __device__ __forceinline__ Team this_team(int &t, long long &first, long long &s
         t = static_cast<int>(threadIdx.x);
         first = blockIdx.x / tm.ctas;
         stride = gridDim.x / tm.ctas;
+        tm.bar = ptx::smem_addr(bars);
+        tm.limit = limit;
+        if (t == 0) {
+#pragma unroll
+            for (int i = 0; i < BARS; ++i)
+                ptx::mbar_init(tm.bar + 8 * i, 1);
+            ptx::fence_mbar_init();
+        }
         ptx::cluster_sync();             // no remote store before every CTA runs
     }
     return tm;
@@ -445,6 +486,8 @@ struct NormParams {
     float *q_scale;
     long long R, C;
     long long groups;          // long kernel: element groups per row
+    long long slice_cols;      // kCluster: columns of each CTA
+    Limit limit;               // kCluster
 };
 
 // The fp8 codes of G values of a row, C ABI semantics of fp8_quantize.
@@ -528,12 +571,19 @@ __global__ void __launch_bounds__(KIND > 0 ? 256 : 1024, KIND > 0 ? (CH == 4 ? 3
     norm_kernel(const NormParams p)
 {
     __shared__ float red[3][kRedWords<KIND, 1>];
+    __shared__ uint64_t bars[3];
     extern __shared__ float4 params[];
     ptx::grid_launch_dependents();
     int t;
     long long first, stride;
-    const Team tm = this_team<KIND>(t, first, stride);
-    const Place<G, KIND, CH> pl(0, p.C, t);
+    const Team tm = this_team<KIND, 3>(t, first, stride, bars, p.limit);
+    long long begin = 0, end = p.C;
+    if constexpr (KIND == kCluster) {
+        begin = min(p.C, tm.rank * p.slice_cols);
+        end = min(p.C, begin + p.slice_cols);
+    }
+    const Place<G, KIND, CH> pl(begin, end, t);
+    const bool speaks = t == 0 && (KIND != kCluster || tm.rank == 0);   // for the team
     float4 *const my_gamma = params + t, *const my_beta = my_gamma + 2 * CH * tm.T;
     ptx::grid_dependency_wait();
 
@@ -558,13 +608,15 @@ __global__ void __launch_bounds__(KIND > 0 ? 256 : 1024, KIND > 0 ? (CH == 4 ? 3
     const long long first0 = KIND > 0 ? first - tm.id : first;
     for (long long turn = 0; first0 + turn * stride < p.R; ++turn) {
         const long long row = first + turn * stride;
+        const uint32_t parity = static_cast<uint32_t>(turn) & 1u;
         uint64_t v[4 * CH];
         to_pairs<ES, G, CH>(raw, p.x_f16, v);
         x += x_step;
         if (row + stride < p.R)
             load_e<ES, G, KIND, CH>(raw, x, pl);
         float s[1] = {sum_pairs(v)};
-        team_sum8<KIND, 1>(s, tm, red[0]);
+        if (!team_sum8<KIND, 1>(s, tm, red[0], 0, parity))
+            break;                       // the results are void
         const float mean = s[0] * inv_c;
         const uint64_t m2 = ptx::f32x2(-mean, -mean);
 #pragma unroll
@@ -580,7 +632,8 @@ __global__ void __launch_bounds__(KIND > 0 ? 256 : 1024, KIND > 0 ? (CH == 4 ? 3
         }
         const uint64_t q2[2] = {q0, q1};
         s[0] = sum_pairs(q2);
-        team_sum8<KIND, 1>(s, tm, red[1]);
+        if (!team_sum8<KIND, 1>(s, tm, red[1], 1, parity))
+            break;
         const float rstd = rsqrtf(fmaf(s[0], inv_c, p.eps));
         const uint64_t r2 = ptx::f32x2(rstd, rstd);
 #pragma unroll
@@ -592,7 +645,7 @@ __global__ void __launch_bounds__(KIND > 0 ? 256 : 1024, KIND > 0 ? (CH == 4 ? 3
         }
         const bool valid = row < p.R;
         if (valid) {
-            if (t == 0) {
+            if (speaks) {
                 if (p.mean)
                     p.mean[row] = mean;
                 if (p.rstd)
@@ -611,15 +664,18 @@ __global__ void __launch_bounds__(KIND > 0 ? 256 : 1024, KIND > 0 ? (CH == 4 ? 3
                 amax[0] = fp8mm::max_nan(amax[0], fabsf(a));
                 amax[0] = fp8mm::max_nan(amax[0], fabsf(b));
             }
-            team_amax8<KIND, 1>(amax, tm, red[2]);
+            if (!team_amax8<KIND, 1>(amax, tm, red[2], 2, parity))
+                break;
             const float scale = amax[0] * (p.q_type == 0 ? 1.0f / 448.0f : 1.0f / 57344.0f);
             if (valid) {
-                if (t == 0)
+                if (speaks)
                     p.q_scale[row] = scale;
                 store_codes_e<G, KIND, CH>(p.q + row * p.C + pl.c0, pl, scale, v, p.q_type);
             }
         }
     }
+    if constexpr (KIND == kCluster)
+        ptx::cluster_sync();             // no CTA leaves while a peer's stores may reach it
 }
 
 // Rows of any length: one CTA per row, one pass over the row per quantity.
@@ -714,6 +770,7 @@ struct NormGradParams {
     long long R, C;
     long long groups;          // long kernels: element groups per row
     long long slice_cols;      // kCluster: columns of each CTA
+    Limit limit;               // kCluster
 };
 
 // Columns per thread over 8 (CH) and threads of a CTA: two 16-bit operands in
@@ -734,14 +791,15 @@ __global__ void __launch_bounds__(KIND > 0 ? kGradLaneThreads : kGradThreads, KI
     norm_grad_kernel(const NormGradParams p)
 {
     constexpr int P = 4 * CH;
-    __shared__ float red[2][kRedWords<KIND, 2>];
+    __shared__ __align__(8) float red[2][kRedWords<KIND, 2>];
+    __shared__ uint64_t bars[2];
     // gamma (keep_params: 2 CH float4s per thread); after the rows, the teams' sums meet here
     extern __shared__ float4 params[];
     float *const cols = reinterpret_cast<float *>(params);
     ptx::grid_launch_dependents();
     int t;
     long long first, stride, begin = 0, end = p.C;
-    const Team tm = this_team<KIND>(t, first, stride);
+    const Team tm = this_team<KIND, 2>(t, first, stride, bars, p.limit);
     if constexpr (KIND == kCluster) {
         begin = min(p.C, tm.rank * p.slice_cols);
         end = min(p.C, begin + p.slice_cols);
@@ -823,7 +881,8 @@ __global__ void __launch_bounds__(KIND > 0 ? kGradLaneThreads : kGradThreads, KI
         }
         if (p.dx == nullptr)
             continue;                    // parameter sums only
-        team_sum8<KIND, 2>(s, tm, red[flip]);
+        if (!team_sum8<KIND, 2>(s, tm, red[flip], flip, static_cast<uint32_t>(turn >> 1) & 1u))
+            break;                       // the results are void
         flip ^= 1;
         const float a = -s[0] * inv_c, b = -s[1] * inv_c;
         const uint64_t a2 = ptx::f32x2(a, a), b2 = ptx::f32x2(b, b);

@@ -73,7 +73,13 @@ int launch_cluster(NormGradParams p, int ctas, int64_t slice_cols, int threads, 
 {
     p.slice_cols = slice_cols;
     const int64_t clusters =
-        p.R <= kRowsPerTeam ? 1 : std::min<int64_t>(p.R, std::max(1, sms / ctas));
+        p.R <= kRowsPerTeam
+            ? 1
+            : std::min<int64_t>(p.R, std::max<int64_t>(1, static_cast<int64_t>(sms) *
+                                                              std::min(kMostPerSm, fp8norm::kGradThreads / threads) / ctas));
+    const int rc = device_limit(&p.limit.status, &p.limit.clocks);
+    if (rc != FP8MM_OK)
+        return rc;
     *partials = static_cast<int>(clusters);
     constexpr int CH = fp8norm::kGradCh<ES, DES, G, fp8norm::kCluster>;
     return launch_clusters(fp8norm::norm_grad_kernel<ES, DES, G, fp8norm::kCluster, CH>,
@@ -107,7 +113,9 @@ int launch_wide(const NormGradParams &p, int sms, cudaStream_t stream, int *P)
     const int64_t warps = cdiv(p.C, warp_cols);
     if (warps <= most)
         return launch_cta<ES, DES, G>(p, static_cast<int>(warps) * 32, sms, stream, P);
-    for (int ctas = 2; ctas <= fp8norm::kMaxCluster; ctas *= 2)
+    // two CTAs as long as they suffice, else eight (4096 x 20000 bf16: four 422
+    // us, eight 292)
+    for (int ctas : {2, fp8norm::kMaxCluster})
         if (warps <= most * ctas) {
             const int64_t each = cdiv(warps, ctas);
             return launch_cluster<ES, DES, G>(p, ctas, each * warp_cols, static_cast<int>(each) * 32, sms, stream, P);

@@ -388,10 +388,19 @@ __device__ __forceinline__ void cp_async_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Store a float to the shared memory of a CTA in the cluster (address from mapa).
-__device__ __forceinline__ void st_shared_cluster_f32(uint32_t cluster_addr, float v)
+// Asynchronous stores to the shared memory of a CTA in the cluster that count
+// their bytes on an mbarrier beside it (both addresses from mapa, of one CTA).
+__device__ __forceinline__ void st_async_f32(uint32_t cluster_addr, float v, uint32_t bar_cluster)
 {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(cluster_addr), "f"(v),
+                 "r"(bar_cluster)
+                 : "memory");
+}
+__device__ __forceinline__ void st_async_f32x2(uint32_t cluster_addr, float v0, float v1, uint32_t bar_cluster)
+{
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(cluster_addr),
+                 "f"(v0), "f"(v1), "r"(bar_cluster)
+                 : "memory");
 }
 
 // Load a float from the shared memory of a CTA in the cluster (address from mapa).

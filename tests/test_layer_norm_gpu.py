@@ -205,6 +205,19 @@ def test_backward_row_counts(R, C):
     backward(R, C)
 
 
+@pytest.mark.parametrize("C", [16392, 20000, 20001, 32768, 33000])
+@pytest.mark.parametrize("x_dtype", [BF16, F32])
+def test_wide_rows_many_turns(C, x_dtype):
+    """Clusters that take several rows each, with and without codes."""
+    _need_gpu()
+    import fp8_scaled_gemm_gb300 as fm
+    forward(500, C, x_dtype=x_dtype)
+    forward(500, C, x_dtype=x_dtype, q_dtype=None)
+    backward(500, C, x_dtype=x_dtype)
+    backward(500, C // 2, x_dtype=x_dtype)
+    assert fm.fp8mm_device_status() == 0
+
+
 @pytest.mark.parametrize("R", [1, 2, 4, 5])
 @pytest.mark.parametrize("C", [24, 255, 4096, 4097, 16384, 40000, 40001])
 def test_backward_few_rows(R, C):
