@@ -212,7 +212,7 @@ def _validate(A, B, scale_a, scale_b, scale_mode, bias, out, device_side: bool, 
     K2, N = B.shape
     if K2 != K:
         raise ValueError(f"inner dimensions differ: A is {tuple(A.shape)}, B is {tuple(B.shape)}")
-    fp8 = tuple(_FP8) if typed else (torch.float8_e4m3fn,)
+    fp8 = _FP8 if typed else (torch.float8_e4m3fn,)
     if A.dtype not in fp8 or B.dtype not in fp8:
         raise ValueError("A and B must be torch.float8_e4m3fn" + (" or float8_e5m2" if typed else ""))
     if A.stride() != (K, 1) and M > 1:
@@ -226,10 +226,10 @@ def _validate(A, B, scale_a, scale_b, scale_mode, bias, out, device_side: bool, 
     for name, s, n in (("scale_a", scale_a, want_a), ("scale_b", scale_b, want_b)):
         if s.dtype != torch.float32 or s.numel() != n or not s.is_contiguous():
             raise ValueError(f"{name} must be a contiguous float32 tensor of {n} values")
-    outs = tuple(_OUT) if typed else (torch.bfloat16,)
+    outs = _OUT if typed else (torch.bfloat16,)
     # typed calls also take a row-strided out (row stride >= N, columns contiguous)
-    strided_ok = typed and out.dim() == 2 and (out.stride(1) == 1 or N == 1) and out.stride(0) >= N
-    if out.dtype not in outs or tuple(out.shape) != (M, N) or not (out.is_contiguous() or strided_ok):
+    if out.dtype not in outs or out.shape != (M, N) or not (
+            out.is_contiguous() or (typed and (out.stride(1) == 1 or N == 1) and out.stride(0) >= N)):
         raise ValueError("out must be a [M, N] tensor of " +
                          ("bfloat16, float16, float32 or float8_e4m3fn with contiguous rows" if typed
                           else "bfloat16, contiguous"))
@@ -237,12 +237,13 @@ def _validate(A, B, scale_a, scale_b, scale_mode, bias, out, device_side: bool, 
                              not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous tensor of N values of out's dtype "
                          "(bfloat16 for a float8_e4m3fn output)")
-    tensors = [A, B, scale_a, scale_b, out] + ([bias] if bias is not None else [])
-    for t in tensors:
-        if device_side and not t.is_cuda:
+    if device_side:
+        if not (A.is_cuda and B.is_cuda and scale_a.is_cuda and scale_b.is_cuda and out.is_cuda and
+                (bias is None or bias.is_cuda)):
             raise ValueError("fp8_scaled_mm takes CUDA tensors (use fp8_scaled_mm_host for host memory)")
-        if not device_side and t.is_cuda:
-            raise ValueError("fp8_scaled_mm_host takes host (CPU) tensors")
+    elif A.is_cuda or B.is_cuda or scale_a.is_cuda or scale_b.is_cuda or out.is_cuda or (
+            bias is not None and bias.is_cuda):
+        raise ValueError("fp8_scaled_mm_host takes host (CPU) tensors")
     return M, N, K
 
 
