@@ -542,11 +542,58 @@ int ck_ctas_per_sm(int tile_n) { return tile_n <= 64 ? 2 : 1; }
 
 int swap_tile_for(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
-Choice choose(int64_t M, int64_t N, int64_t K, int sms, int variant, int tile_n, int split, int64_t batch = 1)
+// Kernel for a product of M <= 128 rows with the extended epilogue. Its work
+// and its loads come after the accumulator, so a thread's outputs (tile_n /
+// split of them in the cluster-K kernel) weigh more than in the plain product:
+// narrower tiles, wider clusters, and the row-major kernel for wide N. Times in
+// us, fitted to 2868 timings of 461 shapes (M 1 .. 128, N 256 .. 16384, K 128 ..
+// 14336; gelu and a residual, bf16): its choice is 1.2 % slower than the fastest
+// measured configuration on average, 18 % at worst; the plain product's choice
+// 22 % and 2.9x (128 x 8192 x 4096: 16.5 us, 20.7 with that; 128 x 1024 x 512:
+// 4.5, 11.4).
+void choose_epilogue(int64_t M, int64_t N, int64_t K, int sms, int *variant, int *tile_n, int *split)
+{
+    const int64_t nt = cdiv(N, fp8mm::kTileP), kb = cdiv(K, fp8mm::kBlockK);
+    const double tile_waves = static_cast<double>(cdiv(nt, sms));
+    double best = -7.9 + tile_waves * (14.4 + 0.292 * kb);
+    *variant = FP8MM_VARIANT_TILE;
+    *tile_n = 128;
+    *split = 1;
+    for (int t : {16, 32, 64, 128}) {
+        if (t > 16 && t >= 2 * M)
+            break;
+        const int64_t tiles = nt * cdiv(M, t);
+        const double swap = 3.2 + static_cast<double>(cdiv(tiles, sms)) * (kb * (0.283 + 0.0001 * t) + 0.0594 * t);
+        if (tiles <= 4 * sms && swap < best) {
+            best = swap;
+            *variant = FP8MM_VARIANT_SWAP;
+            *tile_n = t;
+            *split = 1;
+        }
+        for (int s : {2, 4, 8}) {
+            if (t > 64 || s > kb || tiles * s > 2 * sms)
+                break;
+            const double shared = std::max(0.0, static_cast<double>(tiles * s) / sms - 1.0);   // SMs with two CTAs
+            const double cluster = 1.85 + cdiv(kb, s) * (0.241 + 0.002 * t) * (1.0 + 1.57 * shared) +
+                                   0.151 * t / s + 0.188 * s;
+            if (cluster < best) {
+                best = cluster;
+                *variant = FP8MM_VARIANT_SWAPK;
+                *tile_n = t;
+                *split = s;
+            }
+        }
+    }
+}
+
+Choice choose(int64_t M, int64_t N, int64_t K, int sms, int variant, int tile_n, int split, int64_t batch = 1,
+              bool epilogue = false)
 {
     Choice c{};
     c.kblocks = static_cast<int>(cdiv(K, fp8mm::kBlockK));
-    if (variant == FP8MM_VARIANT_AUTO) {
+    if (variant == FP8MM_VARIANT_AUTO && epilogue && M <= 128 && batch == 1) {
+        choose_epilogue(M, N, K, sms, &variant, &tile_n, &split);
+    } else if (variant == FP8MM_VARIANT_AUTO) {
         split = 0;
         if (M <= 128) {
             // Unsplit persistent SWAP kernel, or K spread over a cluster of
@@ -898,7 +945,7 @@ int run(const void *A, const void *B, const float *sa, const float *sb, int scal
             tuned = true;
         }
     }
-    const Choice c = choose(M, N, K, d->sms, variant, tile_n, split, batch);
+    const Choice c = choose(M, N, K, d->sms, variant, tile_n, split, batch, epi != nullptr);
     if (log_enabled())
         log_choice(current_device(), batch, M, N, K, scale_mode, a_type, b_type, out_type, req_variant, req_tile_n,
                    req_split, c, tuned);
