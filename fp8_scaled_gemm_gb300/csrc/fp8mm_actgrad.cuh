@@ -7,9 +7,12 @@
 // instructions for the slope. A warp covers 8 LANES columns and 32 / LANES
 // rows at a time (LANES < 32 for narrow matrices), NR times over, so that
 // enough loads are in flight (16384 x 14336 bf16 gelu: one row of 256 columns
-// per warp 296 us, two 279; with the slabs in whole waves of CTAs 240); each lane keeps the sums of its columns in
-// registers over the rows of its slab (blockIdx.y). The CTA's warps add theirs
-// in order, and the slabs' partials are added by fp8rows::partial_sum_kernel.
+// per warp 296 us, two 279; with the slabs in whole waves of CTAs 240, 5.9 TB/s,
+// 88 % of a copy; relu 219). Rows that are not 16-byte aligned go element by
+// element (14335 columns 316 us, 67 %; two rows per warp 316). Each lane keeps
+// the sums of its columns in registers over the rows of its slab (blockIdx.y).
+// The CTA's warps add theirs in order, and the slabs' partials are added by
+// fp8rows::partial_sum_kernel.
 #pragma once
 
 #include "fp8mm_act.cuh"
