@@ -2,10 +2,12 @@
 
     out[M, N] = bf16( (A[M, K] . B[K, N]) * (scale_a (x) scale_b) + bias[N] )
 
-A thin ctypes binding over ``libfp8mm.so`` (``include/fp8mm.h``): each
-function has the name of the C entry point it calls and only checks and
-marshals arguments; every step of the computation runs in the CUDA kernels.
-There is no CPU fallback: if the library cannot be loaded, calls raise.
+A thin binding over ``libfp8mm.so`` (``include/fp8mm.h``): each function has
+the name of the C entry point it calls and only checks and marshals
+arguments; every step of the computation runs in the CUDA kernels. Most go
+through ctypes; the operators of an MLP block, whose small calls take the host
+longer than the GPU, through a native module (``csrc/fp8mm_torch.cpp``).
+There is no CPU fallback: if a library cannot be loaded, calls raise.
 
 Operation sources: gist "matmul_fp8.py" (FP8 Matmul), ``matmul_fp8_kernel``
 (scale epilogue) and ``benchmark()`` (B column-major); PyTorch PR #125204,
@@ -15,7 +17,8 @@ Summary (bias).
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from typing import Optional
@@ -187,6 +190,32 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         return lib
 
 
+_native = None
+
+
+def _load_native():
+    """The native module that binds the MLP block's operators."""
+    global _native
+    lib = load()
+    with _lock:
+        if _native is None:
+            path = _build.BINDING_PATH
+            if not os.path.exists(path):
+                raise RuntimeError(f"extension module {path} is missing; build it with "
+                                   "`python -c 'import __graft_entry__ as g; g.build()'`")
+            spec = importlib.util.spec_from_file_location(
+                _build.BINDING, path, loader=importlib.machinery.ExtensionFileLoader(_build.BINDING, path))
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.init(_check, tuple(
+                ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                for name in ("fp8_scaled_mm_epilogue", "fp8_scaled_mm_act_grad", "fp8_act_grad",
+                             "fp8_act_grad_workspace", "fp8_layer_norm", "fp8_layer_norm_grad",
+                             "fp8_layer_norm_grad_workspace")))
+            _native = module
+    return _native
+
+
 def _check(rc: int):
     if rc != 0:
         detail = load().fp8mm_last_cuda_error().decode(errors="replace")
@@ -288,17 +317,6 @@ def fp8_scaled_mm_ex(A, B, scale_a, scale_b, scale_mode: int, bias=None, out=Non
     return out
 
 
-def _aux_matrix(name, t, M, N, dtype) -> int:
-    """Leading dimension of a [M, N] matrix beside out (residual, preact, z)."""
-    if t.dtype != dtype or tuple(t.shape) != (M, N) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA [M, N] tensor of out's dtype (bfloat16 for a float8_e4m3fn output)")
-    if t.is_contiguous():
-        return N
-    if (t.stride(1) != 1 and N > 1) or (t.stride(0) < N and M > 1):
-        raise ValueError(f"{name}'s rows must be contiguous, their stride at least N")
-    return max(N, t.stride(0))
-
-
 def fp8_scaled_mm_epilogue(A, B, scale_a, scale_b, scale_mode: int, bias=None, activation: int = ACT_NONE,
                            residual=None, preact=None, out=None, stream=None, out_dtype=torch.bfloat16,
                            return_preact: bool = False, variant: int = VARIANT_AUTO, tile_n: int = 0,
@@ -309,21 +327,12 @@ def fp8_scaled_mm_epilogue(A, B, scale_a, scale_b, scale_mode: int, bias=None, a
     output) and may be ``out``; ``preact`` receives z. Returns out, or
     (out, preact) with ``return_preact`` (preact is then made if not given).
     """
-    if out is None:
-        out = _new(A, (A.shape[0], B.shape[1]), out_dtype, stream)
-    M, N, K = _validate(A, B, scale_a, scale_b, scale_mode, bias, out, True, typed=True)
-    if return_preact and preact is None:
-        preact = _new(A, (M, N), _BIAS[out.dtype], stream)
-    ldr = 0 if residual is None else _aux_matrix("residual", residual, M, N, _BIAS[out.dtype])
-    ldp = 0 if preact is None else _aux_matrix("preact", preact, M, N, _BIAS[out.dtype])
-    ldo = 0 if out.is_contiguous() else int(out.stride(0))
-    opt = Options(_FP8[A.dtype], _FP8[B.dtype], _OUT[out.dtype], int(variant), int(tile_n), int(split_k), ldo)
-    epi = Epilogue(int(activation), None if residual is None else residual.data_ptr(), ldr,
-                   None if preact is None else preact.data_ptr(), ldp)
-    _check(load().fp8_scaled_mm_epilogue(_ptr(A), _ptr(B), _ptr(scale_a), _ptr(scale_b), scale_mode, _ptr(bias),
-                                         _ptr(out), M, N, K, _stream_handle(stream), ctypes.byref(opt),
-                                         ctypes.byref(epi)))
-    return (out, preact) if return_preact else out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fp8_scaled_mm_epilogue(A, B, scale_a, scale_b, scale_mode, bias, activation, residual, preact, out,
+                                          None, out_dtype, return_preact, variant, tile_n, split_k)
+    return (_native or _load_native()).mm_epilogue(A, B, scale_a, scale_b, scale_mode, bias, activation, residual,
+                                                   preact, out, out_dtype, return_preact, variant, tile_n, split_k)
 
 
 def fp8_scaled_mm_act_grad(A, B, scale_a, scale_b, scale_mode: int, z, activation: int, out=None, stream=None,
@@ -331,16 +340,12 @@ def fp8_scaled_mm_act_grad(A, B, scale_a, scale_b, scale_mode: int, z, activatio
     """dz = (A.B * scale) * act'(z): a backward product with the gradient of
     the activation before it. ``z`` [M, N] is what fp8_scaled_mm_epilogue
     returned as preact; out has z's dtype unless given otherwise."""
-    if out is None:
-        out = _new(A, (A.shape[0], B.shape[1]), out_dtype or z.dtype, stream)
-    M, N, K = _validate(A, B, scale_a, scale_b, scale_mode, None, out, True, typed=True)
-    ldz = _aux_matrix("z", z, M, N, _BIAS[out.dtype])
-    ldo = 0 if out.is_contiguous() else int(out.stride(0))
-    opt = Options(_FP8[A.dtype], _FP8[B.dtype], _OUT[out.dtype], int(variant), int(tile_n), int(split_k), ldo)
-    _check(load().fp8_scaled_mm_act_grad(_ptr(A), _ptr(B), _ptr(scale_a), _ptr(scale_b), scale_mode,
-                                         int(activation), _ptr(z), ldz, _ptr(out), M, N, K, _stream_handle(stream),
-                                         ctypes.byref(opt)))
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fp8_scaled_mm_act_grad(A, B, scale_a, scale_b, scale_mode, z, activation, out, None, out_dtype,
+                                          variant, tile_n, split_k)
+    return (_native or _load_native()).mm_act_grad(A, B, scale_a, scale_b, scale_mode, z, activation, out, out_dtype,
+                                                   variant, tile_n, split_k)
 
 
 def _major(t, k_stride_dim: int) -> int:
@@ -526,50 +531,6 @@ def fp8_scaled_mm_bf16(A, B, scale_mode: int, bias=None, out=None, stream=None,
     return out
 
 
-_ROW = {torch.bfloat16: OUT_BF16, torch.float16: OUT_F16, torch.float32: OUT_F32}
-
-
-def _rows(name, t, shape=None, dtype=None) -> int:
-    """Row stride of a 2-D bf16 / fp16 / fp32 CUDA matrix with contiguous rows."""
-    if t.dim() != 2 or t.dtype not in _ROW or not t.is_cuda:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor of bfloat16, float16 or float32")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    if t.is_contiguous():
-        return t.shape[1]
-    R, C = t.shape
-    if (C > 1 and t.stride(1) != 1) or (R > 1 and t.stride(0) < C):
-        raise ValueError(f"{name}'s rows must be contiguous, their stride at least {C}")
-    return t.stride(0) if R > 1 else C
-
-
-def _vector(name, t, n, dtypes):
-    if t is not None and (t.dtype not in dtypes or t.numel() != n or not t.is_contiguous() or not t.is_cuda):
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} values of " +
-                         " or ".join(str(d) for d in dtypes))
-
-
-def _new(like, shape, dtype, stream):
-    """An output or workspace on ``like``'s device, made on the stream the
-    call runs on, so that its memory is not handed out again before the call
-    is done with it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
-
-
-@functools.lru_cache(maxsize=4096)
-def _workspace_bytes(entry: str, device: int, rows: int, cols: int) -> int:
-    """A workspace query's answer: it depends on the sizes and the device only."""
-    n = int(getattr(load(), entry)(rows, cols))
-    if n < 0:
-        _check(n)
-    return n
-
-
 def fp8_act_grad(dy, z, activation: int, dz=None, dbias=None, stream=None, return_dz: bool = True,
                  return_dbias: bool = True):
     """(dz, dbias) with dz = dy * act'(z) and dbias = its fp32 sum over rows.
@@ -578,22 +539,10 @@ def fp8_act_grad(dy, z, activation: int, dz=None, dbias=None, stream=None, retur
     be None with ACT_NONE. dz has their dtype. A result that is not asked for
     (``return_dz``, ``return_dbias``) is None.
     """
-    lddy = _rows("dy", dy)
-    M, N = dy.shape
-    ldz = 0 if z is None else _rows("z", z, dy.shape, dy.dtype)
-    if dz is None and return_dz:
-        dz = _new(dy, (M, N), dy.dtype, stream)
-    lddz = 0 if dz is None else _rows("dz", dz, dy.shape, dy.dtype)
-    if dbias is None and return_dbias:
-        dbias = _new(dy, N, torch.float32, stream)
-    ws, ws_bytes = None, 0
-    if dbias is not None:
-        _vector("dbias", dbias, N, (torch.float32,))
-        ws_bytes = _workspace_bytes("fp8_act_grad_workspace", dy.get_device(), M, N)
-        ws = _new(dy, ws_bytes, torch.uint8, stream) if ws_bytes else None
-    _check(load().fp8_act_grad(_ptr(dy), lddy, _ptr(z), ldz, _ROW[dy.dtype], int(activation), _ptr(dz), lddz,
-                               _ptr(dbias), M, N, _ptr(ws), ws_bytes, _stream_handle(stream)))
-    return dz, dbias
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fp8_act_grad(dy, z, activation, dz, dbias, None, return_dz, return_dbias)
+    return (_native or _load_native()).act_grad(dy, z, activation, dz, dbias, return_dz, return_dbias)
 
 
 def fp8_layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, y=None, y_dtype=None, q_dtype=None, stream=None,
@@ -606,32 +555,10 @@ def fp8_layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, y=None, y_dtype=
     one of these dtypes (both the same) or None; y has x's dtype unless
     ``y_dtype`` says otherwise, and is None with ``return_y`` false.
     """
-    ldx = _rows("x", x)
-    R, C = x.shape
-    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
-        raise ValueError("gamma and beta must have one dtype")
-    _vector("gamma", gamma, C, _ROW)
-    _vector("beta", beta, C, _ROW)
-    params = gamma if gamma is not None else beta
-    if y is None:
-        y_ld = C
-        if return_y:
-            y = _new(x, (R, C), y_dtype or x.dtype, stream)
-    else:
-        y_ld = _rows("y", y, x.shape, y_dtype)
-    mean = _new(x, R, torch.float32, stream)
-    rstd = _new(x, R, torch.float32, stream)
-    q = q_scale = None
-    if q_dtype is not None:
-        if q_dtype not in _FP8:
-            raise ValueError("q_dtype must be torch.float8_e4m3fn or torch.float8_e5m2")
-        q = _new(x, (R, C), q_dtype, stream)
-        q_scale = _new(x, R, torch.float32, stream)
-    _check(load().fp8_layer_norm(_ptr(x), _ROW[x.dtype], ldx, _ptr(gamma), _ptr(beta),
-                                 OUT_F32 if params is None else _ROW[params.dtype], eps, _ptr(y),
-                                 OUT_F32 if y is None else _ROW[y.dtype], y_ld, _ptr(mean), _ptr(rstd), _ptr(q),
-                                 _FP8.get(q_dtype, 0), _ptr(q_scale), R, C, _stream_handle(stream)))
-    return (y, mean, rstd) if q is None else (y, mean, rstd, q, q_scale)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fp8_layer_norm(x, gamma, beta, eps, y, y_dtype, q_dtype, None, return_y)
+    return (_native or _load_native()).layer_norm(x, gamma, beta, eps, y, y_dtype, q_dtype, return_y)
 
 
 def fp8_layer_norm_grad(dy, x, gamma, mean, rstd, residual_grad=None, dx=None, stream=None,
@@ -643,29 +570,10 @@ def fp8_layer_norm_grad(dy, x, gamma, mean, rstd, residual_grad=None, dx=None, s
     ``dx``). dx has x's dtype, dgamma and dbeta are fp32 (None without
     ``return_params``).
     """
-    lddy = _rows("dy", dy)
-    ldx = _rows("x", x, dy.shape)
-    R, C = x.shape
-    _vector("gamma", gamma, C, _ROW)
-    _vector("mean", mean, R, (torch.float32,))
-    _vector("rstd", rstd, R, (torch.float32,))
-    lddres = 0 if residual_grad is None else _rows("residual_grad", residual_grad, x.shape, x.dtype)
-    if dx is None:
-        dx, lddx = _new(x, (R, C), x.dtype, stream), C
-    else:
-        lddx = _rows("dx", dx, x.shape, x.dtype)
-    dgamma = dbeta = ws = None
-    ws_bytes = 0
-    if return_params:
-        ws_bytes = _workspace_bytes("fp8_layer_norm_grad_workspace", x.get_device(), R, C)
-        dgamma = _new(x, C, torch.float32, stream)
-        dbeta = _new(x, C, torch.float32, stream)
-        ws = _new(x, ws_bytes, torch.uint8, stream) if ws_bytes else None
-    _check(load().fp8_layer_norm_grad(_ptr(dy), _ROW[dy.dtype], lddy, _ptr(x), _ROW[x.dtype], ldx, _ptr(gamma),
-                                      OUT_F32 if gamma is None else _ROW[gamma.dtype], _ptr(mean), _ptr(rstd),
-                                      _ptr(residual_grad), lddres, _ptr(dx), lddx, _ptr(dgamma), _ptr(dbeta), R, C,
-                                      _ptr(ws), ws_bytes, _stream_handle(stream)))
-    return dx, dgamma, dbeta
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fp8_layer_norm_grad(dy, x, gamma, mean, rstd, residual_grad, dx, None, return_params)
+    return (_native or _load_native()).layer_norm_grad(dy, x, gamma, mean, rstd, residual_grad, dx, return_params)
 
 
 def fp8mm_reserve_workspace(nbytes: int) -> None:

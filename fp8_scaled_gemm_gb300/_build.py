@@ -1,4 +1,6 @@
-"""Build the sm_103a shared library ``libfp8mm.so`` in-tree with nvcc.
+"""Build the sm_103a shared library ``libfp8mm.so`` in-tree with nvcc, and
+the extension module that binds the MLP block's operators to PyTorch tensors
+(``_fp8mm_torch.so``, host C++ only) with the host compiler.
 
 The library statically links the CUDA runtime and reaches the driver's
 tensor-map encoder through the runtime's driver entry-point query, so the
@@ -11,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libfp8mm.so")
+BINDING = "_fp8mm_torch"
+BINDING_PATH = os.path.join(BUILD_DIR, BINDING + ".so")
 
 SOURCES = ["fp8mm_epilogue.cu", "fp8mm_epilogue_swap.cu", "fp8mm_api.cu", "fp8mm_norm_grad.cu", "fp8mm_norm.cu", "fp8mm_actgrad.cu"]
 GENCODE = "arch=compute_103a,code=sm_103a"
@@ -39,10 +44,25 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not (os.path.exists(LIB_PATH) and os.path.exists(BINDING_PATH)):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def _binding_command(out: str) -> list:
+    """The host compiler's command for the extension module. PyTorch's
+    libraries are loaded by ``import torch`` before the module is."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    include = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            *[f for d in include for f in ("-isystem" if d != INCLUDE else "-I", d)],
+            os.path.join(CSRC, "fp8mm_torch.cpp"), "-o", out, "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch_python"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -57,16 +77,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with tempfile.TemporaryDirectory(dir=BUILD_DIR) as work:
         # one nvcc per translation unit, all at once, then the link
         jobs = []
+        module = os.path.join(work, BINDING + ".so")
+        cmd = _binding_command(module)
+        binding = (module, cmd, subprocess.Popen(cmd))
         for src in SOURCES:
             obj = os.path.join(work, src + ".o")
             cmd = [nvcc_path(), *flags, "-c", os.path.join(CSRC, src), "-o", obj]
             if verbose:
                 print(" ".join(cmd), file=sys.stderr)
             jobs.append((obj, cmd, subprocess.Popen(cmd)))
-        failed = [(p.returncode, cmd) for _, cmd, p in jobs if p.wait() != 0]
+        failed = [(p.returncode, cmd) for _, cmd, p in [*jobs, binding] if p.wait() != 0]
         if failed:
             raise subprocess.CalledProcessError(*failed[0])
         subprocess.run([nvcc_path(), *flags, "-shared", *[obj for obj, _, _ in jobs], "-o", tmp], check=True)
+        os.replace(module, BINDING_PATH)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

@@ -58,12 +58,22 @@ def test_act_grad_product_refusals(lib, kw, code):
                                       P(AT + 64), 64, 64, a["K"], None, ctypes.byref(o)) == code
 
 
-def test_binding_refuses_wrong_matrices():
+def test_binding_refuses_wrong_operands():
     A = torch.zeros((4, 16)).to(torch.float8_e4m3fn)
-    Bt = torch.zeros((8, 16)).to(torch.float8_e4m3fn)
-    one = torch.ones(1)
-    with pytest.raises(ValueError):       # host tensors
-        fm.fp8_scaled_mm_epilogue(A, Bt.t(), one, one, 0, residual=torch.zeros((4, 8), dtype=torch.bfloat16))
-    for bad in (torch.zeros((4, 7), dtype=torch.bfloat16), torch.zeros((4, 8)), torch.zeros((4, 8), dtype=torch.bfloat16)):
+    B = torch.zeros((8, 16)).to(torch.float8_e4m3fn).t()
+    one, z = torch.ones(1), torch.zeros((4, 8), dtype=torch.bfloat16)
+    for a, b, sa, sb, mode in ((A, B, one, one, 0),                        # host tensors
+                               (A[0], B, one, one, 0), (A, B[:8], one, one, 0), (A.float(), B, one, one, 0),
+                               (A.t().contiguous().t(), B, one, one, 0), (A, B.contiguous(), one, one, 0),
+                               (A, B, one, one, 2), (A, B, one, one, 1), (A, B, one.double(), one, 0),
+                               (A, B, one, torch.ones(2), 0)):
         with pytest.raises(ValueError):
-            fm._aux_matrix("residual", bad, 4, 8, torch.bfloat16)
+            fm.fp8_scaled_mm_epilogue(a, b, sa, sb, mode)
+        with pytest.raises(ValueError):
+            fm.fp8_scaled_mm_act_grad(a, b, sa, sb, mode, z, 2)
+    for call in (lambda: fm.fp8_scaled_mm_epilogue(None, B, one, one, 0),
+                 lambda: fm.fp8_scaled_mm_epilogue(A, B, one, one, "row"),
+                 lambda: fm.fp8_scaled_mm_act_grad(A, B, one, 1.0, 0, z, 2),
+                 lambda: fm.fp8_layer_norm(3), lambda: fm.fp8_act_grad(z, "z", 1)):
+        with pytest.raises(TypeError):
+            call()
