@@ -4,12 +4,12 @@
 // These calls make up to five new tensors each, and with few rows their
 // kernels take 2 to 10 us, so the host's time is the call's time. Through
 // ctypes, with the checks and torch.empty in Python, one token's layer norm
-// with codes took 21 us a call, here 7.8 (Grace); a
-// product with a new output 14 and 3.7. The module checks arguments, makes the
-// tensors that are not given, and calls the C entries, whose addresses it is
-// handed (init); it runs nothing on the device itself. Errors are ValueError
-// for arguments and what `check` raises for a status. Tensors are made and
-// kernels launched on the current stream.
+// with codes took 21 us a call on a Grace core, here 7.8; a product with a new
+// output 14, here 3.7. The module checks arguments, makes the tensors that are
+// not given, and calls the C entries, whose addresses it is handed (init); it
+// runs nothing on the device itself. Errors are ValueError for arguments
+// (TypeError for what is no tensor) and what `check` raises for a status.
+// Tensors are made and kernels launched on the current stream.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
