@@ -542,46 +542,51 @@ int ck_ctas_per_sm(int tile_n) { return tile_n <= 64 ? 2 : 1; }
 
 int swap_tile_for(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
-// Kernel for a product of M <= 128 rows with the extended epilogue. Its work
-// and its loads come after the accumulator, so a thread's outputs (tile_n /
-// split of them in the cluster-K kernel) weigh more than in the plain product:
-// narrower tiles, wider clusters, and the row-major kernel for wide N. Times in
-// us, fitted to 2868 timings of 461 shapes (M 1 .. 128, N 256 .. 16384, K 128 ..
-// 14336; gelu and a residual, bf16): its choice is 1.2 % slower than the fastest
-// measured configuration on average, 18 % at worst; the plain product's choice
-// 22 % and 2.9x (128 x 8192 x 4096: 16.5 us, 20.7 with that; 128 x 1024 x 512:
-// 4.5, 11.4).
+// Kernel for a product with the extended epilogue and at most two waves of
+// 128 x 128 tiles. The epilogue's work and its loads come after the accumulator,
+// so a thread's outputs (tile_n / split of them in the cluster-K kernel) weigh
+// more than in the plain product: narrower tiles and wider clusters win, also
+// where M is above 128 and there are few tiles. Times in us, fitted to 5843
+// timings of 859 shapes (M 1 .. 12000, N 70 .. 16384, K 64 .. 14336; gelu and a
+// residual, bf16). Its choice is 1 % slower than the fastest measured
+// configuration on average, 20 % at worst; the plain product's choice 22 % for M
+// <= 128 and 41 % above, 5.9x at worst (128 x 8192 x 4096: 16.5 us, with that
+// 20.7; 384 x 128 x 6016: 5.3, with that 19.0).
 void choose_epilogue(int64_t M, int64_t N, int64_t K, int sms, int *variant, int *tile_n, int *split)
 {
     const int64_t nt = cdiv(N, fp8mm::kTileP), kb = cdiv(K, fp8mm::kBlockK);
-    const double tile_waves = static_cast<double>(cdiv(nt, sms));
-    double best = -7.9 + tile_waves * (14.4 + 0.292 * kb);
-    *variant = FP8MM_VARIANT_TILE;
-    *tile_n = 128;
-    *split = 1;
-    for (int t : {16, 32, 64, 128}) {
-        if (t > 16 && t >= 2 * M)
-            break;
-        const int64_t tiles = nt * cdiv(M, t);
-        const double swap = 3.2 + static_cast<double>(cdiv(tiles, sms)) * (kb * (0.283 + 0.0001 * t) + 0.0594 * t);
-        if (tiles <= 4 * sms && swap < best) {
-            best = swap;
-            *variant = FP8MM_VARIANT_SWAP;
-            *tile_n = t;
-            *split = 1;
+    const bool unaligned = N % 8 != 0;
+    double best = 1e300;
+    auto offer = [&](double t, int v, int n, int s) {
+        if (t < best) {
+            best = t;
+            *variant = v;
+            *tile_n = n;
+            *split = s;
         }
+    };
+    auto waves = [](int64_t units, int places) { return static_cast<double>(cdiv(units, places)); };
+    offer(2.27 + waves(nt * cdiv(M, 128), sms) * (kb * 0.283 + 4.37 + (unaligned ? 1.03 : 0.0)), FP8MM_VARIANT_TILE, 128, 1);
+    if (M > 128 && 2 * nt * cdiv(M, 128) <= sms)      // deep K, half of the SMs without a tile
+        offer(16.6 + cdiv(kb, 2) * 0.283, FP8MM_VARIANT_TILE, 128, 2);
+    if (M > 128) {
+        offer(2.94 + waves(cdiv(N, 256) * cdiv(M, 128), sms) * (kb * 0.38 + 6.61 + (unaligned ? 1.45 : 0.0)),
+              FP8MM_VARIANT_TILE, 256, 1);
+        offer(2.29 + waves(cdiv(N, 256) * cdiv(M, 256), sms / 2) * (kb * 0.283 + 9.70 + (unaligned ? 2.29 : 0.0)),
+              FP8MM_VARIANT_PAIR, 256, 1);
+    }
+    for (int t : {16, 32, 64, 128}) {
+        if (t == 16 ? M > 128 : t >= 2 * M)
+            continue;
+        const int64_t tiles = nt * cdiv(M, t);
+        if (tiles <= 4 * sms)
+            offer(3.1 + waves(tiles, sms) * (kb * 0.284 + 0.064 * t), FP8MM_VARIANT_SWAP, t, 1);
         for (int s : {2, 4, 8}) {
             if (t > 64 || s > kb || tiles * s > 2 * sms)
                 break;
             const double shared = std::max(0.0, static_cast<double>(tiles * s) / sms - 1.0);   // SMs with two CTAs
-            const double cluster = 1.85 + cdiv(kb, s) * (0.241 + 0.002 * t) * (1.0 + 1.57 * shared) +
-                                   0.151 * t / s + 0.188 * s;
-            if (cluster < best) {
-                best = cluster;
-                *variant = FP8MM_VARIANT_SWAPK;
-                *tile_n = t;
-                *split = s;
-            }
+            offer(1.69 + cdiv(kb, s) * (0.257 + 0.0009 * t) * (1.0 + 1.23 * shared) + 0.17 * t / s + 0.212 * s,
+                  FP8MM_VARIANT_SWAPK, t, s);
         }
     }
 }
@@ -591,7 +596,8 @@ Choice choose(int64_t M, int64_t N, int64_t K, int sms, int variant, int tile_n,
 {
     Choice c{};
     c.kblocks = static_cast<int>(cdiv(K, fp8mm::kBlockK));
-    if (variant == FP8MM_VARIANT_AUTO && epilogue && M <= 128 && batch == 1) {
+    if (variant == FP8MM_VARIANT_AUTO && epilogue && batch == 1 &&
+        (M <= 128 || cdiv(M, 128) * cdiv(N, 128) <= 2 * static_cast<int64_t>(sms))) {
         choose_epilogue(M, N, K, sms, &variant, &tile_n, &split);
     } else if (variant == FP8MM_VARIANT_AUTO) {
         split = 0;
