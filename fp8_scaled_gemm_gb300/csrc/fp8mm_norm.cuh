@@ -286,15 +286,13 @@ struct Team {
     Limit limit;
 };
 
-// Exchange k of a cluster's team: every warp's values go to all its CTAs, into
+// Exchanges of a cluster's team: every warp's values go to all its CTAs, into
 // the slot of the warp in their buffer `red`, and are counted there on mbarrier
 // k. (A cluster barrier per exchange waits for the row's global stores as well:
 // forward 4096 x 32768 bf16 with codes 290 us, now 194; backward 8192 x 8192
-// fp32 268, now 177.) An exchange's buffer is free for the one after next: a warp sends for
-// the next one after it has read this one, and this CTA passes the next one
-// with all warps' values. False when the wait ran out.
+// fp32 268, now 177.)
 template <int NV>
-__device__ __forceinline__ bool cluster_exchange(const float (&v)[NV], const Team &tm, float *red, int k, uint32_t parity)
+__device__ __forceinline__ void cluster_send(const float (&v)[NV], const Team &tm, float *red, int k)
 {
     const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
     const uint32_t bar = tm.bar + 8u * k;
@@ -310,6 +308,12 @@ __device__ __forceinline__ bool cluster_exchange(const float (&v)[NV], const Tea
             ptx::st_async_f32(at, v[0], there);
     }
     __syncwarp();
+}
+
+// False when the wait ran out.
+__device__ __forceinline__ bool cluster_wait(const Team &tm, int k, uint32_t parity)
+{
+    const uint32_t bar = tm.bar + 8u * k;
     bool here = ptx::mbar_try_wait_cluster(bar, parity);
     if (!here) {
         const unsigned long long t0 = static_cast<unsigned long long>(clock64());
@@ -321,6 +325,16 @@ __device__ __forceinline__ bool cluster_exchange(const float (&v)[NV], const Tea
         }
     }
     return __all_sync(0xFFFFFFFFu, here);   // the warp stays together
+}
+
+// Both. An exchange's buffer is free for the one after next: a warp sends for
+// the next one after it has read this one, and this CTA passes the next one
+// with all warps' values.
+template <int NV>
+__device__ __forceinline__ bool cluster_exchange(const float (&v)[NV], const Team &tm, float *red, int k, uint32_t parity)
+{
+    cluster_send<NV>(v, tm, red, k);
+    return cluster_wait(tm, k, parity);
 }
 
 // Words of one reduction's exchange buffer for NV values.
@@ -791,13 +805,100 @@ constexpr int kGradCh = (ES == 2 && DES == 2 && G == 8 && KIND <= 0) ? 2 : 1;
 // 16384 x 8192 bf16 with a residual gradient takes 175 us, 6.1 TB/s (92 % of a
 // copy), 8192 x 8192 fp32 178 (91 %). Registers (128 per thread) hold one row at
 // work, one on its way and the sums, so an SM has 512 threads and wide rows one
-// or two teams: 8192 x 16384 bf16 runs at 64 %, 4096 x 32768 at 36 %, waiting for
+// or two teams: 8192 x 16384 bf16 runs at 73 %, 4096 x 32768 at 42 %, waiting for
 // exchanges. Unaligned rows hold 8 columns per thread (16384 x 4095 bf16 129 us,
-// 62 %).
+// 62 %; over 4096 columns, in clusters, 19 to 39 %).
 // Teams of lanes: CTAs of 256 threads, 4 on an SM (3 where registers hold fp32 rows).
 constexpr int kGradLaneThreads = 256;
 template <int ES, int DES>
 constexpr int kGradLaneCtas = ES == 2 && DES == 2 ? 4 : 3;
+
+// The team's column sums to its slot of the partial sums (cols: shared memory
+// of kGradLaneThreads x 8 floats).
+template <int G, int KIND, int CH>
+__device__ __forceinline__ void store_column_sums(const NormGradParams &p, long long slot, int t,
+                                                  const Place<G, KIND, CH> &pl, const uint64_t (&dga)[4 * CH],
+                                                  const uint64_t (&dbe)[4 * CH], float *cols)
+{
+    constexpr int P = 4 * CH;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        float f[2 * P];
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            ptx::unpack_f32x2(k == 0 ? dga[i] : dbe[i], f[2 * i], f[2 * i + 1]);
+        if constexpr (KIND > 0 && KIND < 32) {
+            // teams of one warp first
+#pragma unroll
+            for (int o = KIND; o < 32; o <<= 1)
+#pragma unroll
+                for (int i = 0; i < 2 * P; ++i)
+                    f[i] += __shfl_xor_sync(0xFFFFFFFFu, f[i], o);
+        }
+        bool writes = true;
+        if constexpr (KIND > 0) {
+            // then the warps in order
+            const int warps = static_cast<int>(blockDim.x) / 32, warp = static_cast<int>(threadIdx.x) >> 5;
+            const bool speaks = static_cast<int>(threadIdx.x & 31) < KIND;
+            writes = speaks && warp == warps - 1;
+            for (int m = 0; m + 1 < warps; ++m) {
+                __syncthreads();
+                if (warp == m && speaks) {
+#pragma unroll
+                    for (int i = 0; i < 2 * P; ++i) {
+                        const int at = i * KIND + t;
+                        cols[at] = m == 0 ? f[i] : cols[at] + f[i];
+                    }
+                }
+            }
+            __syncthreads();
+            if (writes && warps > 1) {
+#pragma unroll
+                for (int i = 0; i < 2 * P; ++i)
+                    f[i] += cols[i * KIND + t];
+            }
+        }
+        if (writes) {
+            uint64_t v[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                v[i] = ptx::f32x2(f[2 * i], f[2 * i + 1]);
+            store_e<G, KIND, CH>(
+                reinterpret_cast<uint8_t *>((k == 0 ? p.partial : p.partial1) + slot * p.partial_step + pl.c0), kF32, pl,
+                v);
+        }
+        __syncthreads();
+    }
+}
+
+// A row's terms of the column sums, and its two sums: s1 of w = dy gamma, s2 of
+// w xhat. h: x, then xhat; w: dy, then w. m2, r2: -mean and rstd twice.
+template <int CH>
+__device__ __forceinline__ void grad_terms(uint64_t (&h)[4 * CH], uint64_t (&w)[4 * CH], uint64_t m2, uint64_t r2,
+                                           const float4 *my_gamma, int threads, uint64_t (&dga)[4 * CH],
+                                           uint64_t (&dbe)[4 * CH], float (&s)[2])
+{
+    constexpr int P = 4 * CH;
+    uint64_t s1 = 0, s2 = 0;
+#pragma unroll
+    for (int j = 0; j < P / 2; ++j) {
+        const float4 g4 = my_gamma[j * threads];
+#pragma unroll
+        for (int i = 2 * j; i < 2 * j + 2; ++i) {
+            h[i] = ptx::mul_f32x2(ptx::add_f32x2(h[i], m2), r2);
+            dga[i] = ptx::fma_f32x2(w[i], h[i], dga[i]);
+            dbe[i] = ptx::add_f32x2(dbe[i], w[i]);
+            w[i] = ptx::mul_f32x2(w[i], i == 2 * j ? ptx::f32x2(g4.x, g4.y) : ptx::f32x2(g4.z, g4.w));
+            s1 = ptx::add_f32x2(s1, w[i]);
+            s2 = ptx::fma_f32x2(w[i], h[i], s2);
+        }
+    }
+    float lo, hi;
+    ptx::unpack_f32x2(s1, lo, hi);
+    s[0] = lo + hi;
+    ptx::unpack_f32x2(s2, lo, hi);
+    s[1] = lo + hi;
+}
 
 template <int ES, int DES, int G, int KIND, int CH>
 __global__ void __launch_bounds__(KIND > 0 ? kGradLaneThreads : kGradThreads, KIND > 0 ? kGradLaneCtas<ES, DES> : 1)
@@ -871,27 +972,8 @@ __global__ void __launch_bounds__(KIND > 0 ? kGradLaneThreads : kGradThreads, KI
             nrstd = __ldg(p.rstd + row + stride);
         }
         float s[2] = {0.0f, 0.0f};
-        if (valid) {
-            uint64_t s1 = 0, s2 = 0;
-#pragma unroll
-            for (int j = 0; j < P / 2; ++j) {
-                const float4 g4 = my_gamma[j * threads];
-#pragma unroll
-                for (int i = 2 * j; i < 2 * j + 2; ++i) {
-                    h[i] = ptx::mul_f32x2(ptx::add_f32x2(h[i], m2), r2);
-                    dga[i] = ptx::fma_f32x2(w[i], h[i], dga[i]);
-                    dbe[i] = ptx::add_f32x2(dbe[i], w[i]);
-                    w[i] = ptx::mul_f32x2(w[i], i == 2 * j ? ptx::f32x2(g4.x, g4.y) : ptx::f32x2(g4.z, g4.w));
-                    s1 = ptx::add_f32x2(s1, w[i]);
-                    s2 = ptx::fma_f32x2(w[i], h[i], s2);
-                }
-            }
-            float lo, hi;
-            ptx::unpack_f32x2(s1, lo, hi);
-            s[0] = lo + hi;
-            ptx::unpack_f32x2(s2, lo, hi);
-            s[1] = lo + hi;
-        }
+        if (valid)
+            grad_terms<CH>(h, w, m2, r2, my_gamma, threads, dga, dbe, s);
         if (p.dx == nullptr)
             continue;                    // parameter sums only
         if (!team_sum8<KIND, 2>(s, tm, red[flip], flip, static_cast<uint32_t>(turn >> 1) & 1u))
@@ -910,59 +992,140 @@ __global__ void __launch_bounds__(KIND > 0 ? kGradLaneThreads : kGradThreads, KI
         pr += r_step;
         po += o_step;
     }
-    if (p.partial != nullptr) {
-        const long long slot = KIND == kCluster ? blockIdx.x / tm.ctas : blockIdx.x;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float f[2 * P];
-#pragma unroll
-            for (int i = 0; i < P; ++i)
-                ptx::unpack_f32x2(k == 0 ? dga[i] : dbe[i], f[2 * i], f[2 * i + 1]);
-            if constexpr (KIND > 0 && KIND < 32) {
-                // teams of one warp first
-#pragma unroll
-                for (int o = KIND; o < 32; o <<= 1)
-#pragma unroll
-                    for (int i = 0; i < 2 * P; ++i)
-                        f[i] += __shfl_xor_sync(0xFFFFFFFFu, f[i], o);
-            }
-            bool writes = true;
-            if constexpr (KIND > 0) {
-                // then the warps in order
-                const int warps = static_cast<int>(blockDim.x) / 32, warp = static_cast<int>(threadIdx.x) >> 5;
-                const bool speaks = static_cast<int>(threadIdx.x & 31) < KIND;
-                writes = speaks && warp == warps - 1;
-                for (int m = 0; m + 1 < warps; ++m) {
-                    __syncthreads();
-                    if (warp == m && speaks) {
-#pragma unroll
-                        for (int i = 0; i < 2 * P; ++i) {
-                            const int at = i * KIND + t;
-                            cols[at] = m == 0 ? f[i] : cols[at] + f[i];
-                        }
-                    }
-                }
-                __syncthreads();
-                if (writes && warps > 1) {
-#pragma unroll
-                    for (int i = 0; i < 2 * P; ++i)
-                        f[i] += cols[i * KIND + t];
-                }
-            }
-            if (writes) {
-                uint64_t v[P];
-#pragma unroll
-                for (int i = 0; i < P; ++i)
-                    v[i] = ptx::f32x2(f[2 * i], f[2 * i + 1]);
-                store_e<G, KIND, CH>(
-                    reinterpret_cast<uint8_t *>((k == 0 ? p.partial : p.partial1) + slot * p.partial_step + pl.c0), kF32, pl,
-                    v);
-            }
-            __syncthreads();
-        }
-    }
+    if (p.partial != nullptr)
+        store_column_sums<G, KIND, CH>(p, KIND == kCluster ? blockIdx.x / tm.ctas : blockIdx.x, t, pl, dga, dbe, cols);
     if constexpr (KIND == kCluster)
         ptx::cluster_sync();             // no CTA leaves while a peer's stores may reach it
+}
+
+// The same for a cluster's CTAs and 16-byte groups of 16-bit elements: a row's
+// sums are sent before the row before it is finished, so that an exchange has a
+// row's work to hide behind; until then the row is kept as loaded, and it is
+// converted twice. bf16 with a residual gradient, norm_grad_kernel and this one:
+// 8192 x 16384 250 and 221 us, 12000 x 12288 324 and 278, 4096 x 32768 441 and 383.
+// Other operands lost with it (16384 x 9132 unaligned 653 and 762, 4096 x 16384
+// fp32 284 and 303: 8 columns per thread leave less work to hide behind, and more
+// of the second conversion's). Four buffers: a warp sends for row n after it has
+// passed row n - 2's exchange, and every warp sent for that after it had read row
+// n - 4's.
+template <int ES, int DES, int G, int CH>
+__global__ void __launch_bounds__(kGradThreads) norm_grad_cluster_kernel(const NormGradParams p)
+{
+    constexpr int P = 4 * CH, KIND = kCluster;
+    __shared__ __align__(8) float red[4][kMaxCluster * (kGradThreads / 32) * 2];
+    __shared__ uint64_t bars[4];
+    extern __shared__ float4 params[];           // gamma (keep_params: 2 CH float4s per thread)
+    ptx::grid_launch_dependents();
+    int t;
+    long long row, stride;
+    const Team tm = this_team<KIND, 4>(t, row, stride, bars, p.limit);
+    const long long begin = min(p.C, tm.rank * p.slice_cols), end = min(p.C, begin + p.slice_cols);
+    const Place<G, KIND, CH> pl(begin, end, t);
+    ptx::grid_dependency_wait();
+
+    const float inv_c = 1.0f / static_cast<float>(p.C);
+    const uint8_t *px = static_cast<const uint8_t *>(p.x) + (row * p.ldx + pl.c0) * ES;
+    const uint8_t *pd = static_cast<const uint8_t *>(p.dy) + (row * p.lddy + pl.c0) * DES;
+    const uint8_t *pr = static_cast<const uint8_t *>(p.dres) + (row * p.lddres + pl.c0) * ES;
+    uint8_t *po = static_cast<uint8_t *>(p.dx) + (row * p.lddx + pl.c0) * ES;
+    RawE<ES, G, CH> lx, cx;                      // on its way; sent for, to be finished
+    RawE<DES, G, CH> ld, cd;
+    float lmean = 0.0f, lrstd = 0.0f, cmean = 0.0f, crstd = 0.0f;
+    clear_e<ES, G, CH>(lx);
+    clear_e<DES, G, CH>(ld);
+    auto load = [&](long long r) {
+        load_e<ES, G, KIND, CH>(lx, px, pl);
+        load_e<DES, G, KIND, CH>(ld, pd, pl);
+        lmean = __ldg(p.mean + r);
+        lrstd = __ldg(p.rstd + r);
+        px += stride * p.ldx * ES;
+        pd += stride * p.lddy * DES;
+    };
+    if (row < p.R)
+        load(row);
+    uint64_t dga[P] = {}, dbe[P] = {};
+    const int threads = static_cast<int>(blockDim.x);
+    float4 *const my_gamma = params + threadIdx.x;
+    {
+        uint64_t ga[P];
+        param_e<G, KIND, CH>(p.gamma, p.param_type, pl, 1.0f, ga);
+        keep_params<CH>(my_gamma, threads, ga);
+    }
+    // turn n sends row n's sums, then finishes row n - 1
+    const bool dx = p.dx != nullptr;
+    bool sent = false;
+    for (uint32_t n = 0; sent || row < p.R; ++n) {
+        RawE<ES, G, CH> nx = lx;
+        RawE<DES, G, CH> nd = ld;
+        const float nmean = lmean, nrstd = lrstd;
+        const bool more = row < p.R;
+        if (more) {
+            if (row + stride < p.R)
+                load(row + stride);
+            uint64_t h[P], w[P];
+            float s[2];
+            to_pairs<ES, G, CH>(nx, p.x_f16, h);
+            to_pairs<DES, G, CH>(nd, p.dy_f16, w);
+            grad_terms<CH>(h, w, ptx::f32x2(-nmean, -nmean), ptx::f32x2(nrstd, nrstd), my_gamma, threads, dga, dbe, s);
+            row += stride;
+            if (dx) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    s[0] += __shfl_xor_sync(0xFFFFFFFFu, s[0], o);
+                    s[1] += __shfl_xor_sync(0xFFFFFFFFu, s[1], o);
+                }
+                cluster_send<2>(s, tm, red[n & 3], static_cast<int>(n & 3));
+            }
+        }
+        if (sent) {
+            RawE<ES, G, CH> rr;
+            if (p.dres)
+                load_e<ES, G, KIND, CH>(rr, pr, pl);
+            else
+                clear_e<ES, G, CH>(rr);
+            const uint32_t k = (n - 1) & 3;
+            if (!cluster_wait(tm, static_cast<int>(k), ((n - 1) >> 2) & 1u))
+                break;                           // the results are void
+            float s[2] = {0.0f, 0.0f};
+            for (int e = static_cast<int>(threadIdx.x) & 31; e < static_cast<int>(tm.ctas) * tm.warps; e += 32) {
+                s[0] += red[k][2 * e];
+                s[1] += red[k][2 * e + 1];
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                s[0] += __shfl_xor_sync(0xFFFFFFFFu, s[0], o);
+                s[1] += __shfl_xor_sync(0xFFFFFFFFu, s[1], o);
+            }
+            const float a = -s[0] * inv_c, b = -s[1] * inv_c;
+            const uint64_t a2 = ptx::f32x2(a, a), b2 = ptx::f32x2(b, b), m2 = ptx::f32x2(-cmean, -cmean),
+                           r2 = ptx::f32x2(crstd, crstd);
+            uint64_t h[P], w[P], r[P];
+            to_pairs<ES, G, CH>(cx, p.x_f16, h);
+            to_pairs<DES, G, CH>(cd, p.dy_f16, w);
+            to_pairs<ES, G, CH>(rr, p.x_f16, r);
+#pragma unroll
+            for (int j = 0; j < P / 2; ++j) {
+                const float4 g4 = my_gamma[j * threads];
+#pragma unroll
+                for (int i = 2 * j; i < 2 * j + 2; ++i) {
+                    h[i] = ptx::mul_f32x2(ptx::add_f32x2(h[i], m2), r2);
+                    w[i] = ptx::fma_f32x2(w[i], i == 2 * j ? ptx::f32x2(g4.x, g4.y) : ptx::f32x2(g4.z, g4.w), a2);
+                    w[i] = ptx::fma_f32x2(ptx::fma_f32x2(h[i], b2, w[i]), r2, r[i]);
+                }
+            }
+            store_e<G, KIND, CH>(po, p.x_type, pl, w);
+            pr += stride * p.lddres * ES;
+            po += stride * p.lddx * ES;
+        }
+        cx = nx;
+        cd = nd;
+        cmean = nmean;
+        crstd = nrstd;
+        sent = more && dx;
+    }
+    if (p.partial != nullptr)
+        store_column_sums<G, KIND, CH>(p, blockIdx.x / tm.ctas, t, pl, dga, dbe, nullptr);
+    ptx::cluster_sync();                 // no CTA leaves while a peer's stores may reach it
 }
 
 // Rows of any length: dx by one CTA per row. The parameter sums come from

@@ -82,8 +82,12 @@ int launch_cluster(NormGradParams p, int ctas, int64_t slice_cols, int threads, 
         return rc;
     *partials = static_cast<int>(clusters);
     constexpr int CH = fp8norm::kGradCh<ES, DES, G, fp8norm::kCluster>;
-    return launch_clusters(fp8norm::norm_grad_kernel<ES, DES, G, fp8norm::kCluster, CH>,
-                           static_cast<int>(clusters) * ctas, ctas, threads, threads * 2 * 16 * CH, stream,
+    void (*kern)(NormGradParams);
+    if constexpr (CH == 2)
+        kern = fp8norm::norm_grad_cluster_kernel<ES, DES, G, CH>;
+    else
+        kern = fp8norm::norm_grad_kernel<ES, DES, G, fp8norm::kCluster, CH>;
+    return launch_clusters(kern, static_cast<int>(clusters) * ctas, ctas, threads, threads * 2 * 16 * CH, stream,
                            "layer norm gradient launch", p);
 }
 
