@@ -30,7 +30,7 @@ int64_t partial_bytes(int64_t slabs, int64_t N)
 template <int ES, int G, int LANES>
 int launch_lanes(const ActGradParams &p, int64_t slabs, cudaStream_t stream)
 {
-    return launch_grid2(fp8act::act_grad_kernel<ES, G, LANES, (ES == 2 && G == 8) ? 2 : 1>, cdiv(p.N, 8 * LANES), slabs,
+    return launch_grid2(fp8act::act_grad_kernel<ES, G, LANES, (ES == 2 && G > 1) ? 2 : 1>, cdiv(p.N, 8 * LANES), slabs,
                         fp8act::kThreads, stream, "activation gradient launch", p);
 }
 
@@ -117,10 +117,12 @@ int fp8_act_grad(const void *dy, int64_t lddy, const void *z, int64_t ldz, int t
     }
     const bool vec = N % 8 == 0 && rows_vec(dy, p.ldy, type) && (!p.z || rows_vec(z, p.ldz, type)) &&
                      (!dz || rows_vec(dz, p.ldd, type));
+    const bool pairs = N % 2 == 0 && rows_pairs(dy, p.ldy, type) && (!p.z || rows_pairs(z, p.ldz, type)) &&
+                       (!dz || rows_pairs(dz, p.ldd, type));
     if (type == FP8MM_OUT_F32)
         rc = vec ? launch<4, 8>(p, slabs, s) : launch<4, 1>(p, slabs, s);
     else
-        rc = vec ? launch<2, 8>(p, slabs, s) : launch<2, 1>(p, slabs, s);
+        rc = vec ? launch<2, 8>(p, slabs, s) : pairs ? launch<2, 2>(p, slabs, s) : launch<2, 1>(p, slabs, s);
     if (rc != FP8MM_OK || !dbias || slabs == 1)
         return rc;
     fp8rows::PartialSumParams sum{};

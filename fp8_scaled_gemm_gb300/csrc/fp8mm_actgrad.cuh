@@ -8,8 +8,9 @@
 // rows at a time (LANES < 32 for narrow matrices), NR times over, so that
 // enough loads are in flight (16384 x 14336 bf16 gelu: one row of 256 columns
 // per warp 296 us, two 279; with the slabs in whole waves of CTAs 240, 5.9 TB/s,
-// 88 % of a copy; relu 219). Rows that are not 16-byte aligned go element by
-// element (14335 columns 316 us, 67 %; two rows per warp 316). Each lane keeps
+// 88 % of a copy; relu 219). 16-bit rows without 16-byte groups go in pairs where
+// they start on 4 bytes (14334 columns 256 us, 82 %), else element by element
+// (14335 columns 316 us, 67 %; two rows per warp 316). Each lane keeps
 // the sums of its columns in registers over the rows of its slab (blockIdx.y).
 // The CTA's warps add theirs in order, and the slabs' partials are added by
 // fp8rows::partial_sum_kernel.
@@ -34,13 +35,14 @@ struct ActGradParams {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
-// G = 8: a lane's columns are neighbours; G = 1: LANES apart.
+// G = 8: a lane's columns are neighbours; G = 2 and 1: pairs and single columns,
+// lane by lane (pairs: an even number of columns).
 template <int ES, int G, int LANES, int NR>
 __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradParams p)
 {
     constexpr int K = 8 / G;                     // loads of a lane per row and operand
     constexpr int kCols = 8 * LANES, kRows = 32 / LANES;
-    constexpr int kStep = G == 8 ? 0 : LANES;    // columns between them
+    constexpr int kStep = G * LANES;             // columns between them
     __shared__ float cols[kWarps][kCols];
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
@@ -81,12 +83,15 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradParams 
                 to_float<ES, 8>(rz[r][0], f16, x);
             } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    float a[1], b[1];
-                    to_float<ES, 1>(rd[r][k], f16, a);
-                    to_float<ES, 1>(rz[r][k], f16, b);
-                    v[k] = a[0];
-                    x[k] = b[0];
+                for (int k = 0; k < K; ++k) {
+                    float a[G], b[G];
+                    to_float<ES, G>(rd[r][k], f16, a);
+                    to_float<ES, G>(rz[r][k], f16, b);
+#pragma unroll
+                    for (int e = 0; e < G; ++e) {
+                        v[G * k + e] = a[e];
+                        x[G * k + e] = b[e];
+                    }
                 }
             }
             fp8mm::apply_slope<8>(p.act, v, x);
@@ -98,6 +103,11 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradParams 
                 if constexpr (G == 8) {
                     if (left > 0)
                         store_group<8>(o, p.type, 0, v);
+                } else if constexpr (G == 2) {
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        if (k * kStep < left)
+                            *reinterpret_cast<uint32_t *>(o + k * kStep * 2) = pack2(v[2 * k], v[2 * k + 1], p.type);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
@@ -122,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradParams 
     if (lane < LANES) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            cols[warp][G == 8 ? lane * 8 + k : lane + k * LANES] = sum[k];
+            cols[warp][lane * G + k / G * kStep + k % G] = sum[k];
     }
     __syncthreads();
     const long long n = static_cast<long long>(blockIdx.x) * kCols + threadIdx.x;

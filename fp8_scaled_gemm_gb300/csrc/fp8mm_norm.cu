@@ -75,8 +75,20 @@ int launch_cluster(NormParams p, int sms, cudaStream_t stream)
     return launch_clusters(kern, static_cast<int>(clusters) * ctas, ctas, threads, smem, stream, "layer norm launch", p);
 }
 
+// Rows without 16-byte groups: pairs (G = 2) or single elements.
+template <int ES, int G>
+int launch_narrow(const NormParams &p, int sms, cudaStream_t stream)
+{
+    const int64_t C = p.C;
+    if (C <= 256) return launch_lanes<ES, G, 32, 1>(p, sms, stream);
+    if (C <= 512) return launch_lanes<ES, G, 32, 2>(p, sms, stream);
+    if (C <= 1024) return launch_lanes<ES, G, 32, 4>(p, sms, stream);
+    if (C <= 16384) return launch_cta<ES, G, 2>(p, sms, stream);
+    return launch_cluster<ES, G>(p, sms, stream);
+}
+
 template <int ES>
-int launch(const NormParams &p, bool vec, int sms, cudaStream_t stream)
+int launch(const NormParams &p, bool vec, bool pairs, int sms, cudaStream_t stream)
 {
     const int64_t C = p.C;
     if (vec) {
@@ -88,12 +100,11 @@ int launch(const NormParams &p, bool vec, int sms, cudaStream_t stream)
         if (C <= 1024) return launch_lanes<ES, 8, 32, 4>(p, sms, stream);
         if (C <= 16384) return launch_cta<ES, 8, 2>(p, sms, stream);
         if (C <= kMostColumns) return launch_cluster<ES, 8>(p, sms, stream);
-    } else {
-        if (C <= 256) return launch_lanes<ES, 1, 32, 1>(p, sms, stream);
-        if (C <= 512) return launch_lanes<ES, 1, 32, 2>(p, sms, stream);
-        if (C <= 1024) return launch_lanes<ES, 1, 32, 4>(p, sms, stream);
-        if (C <= 16384) return launch_cta<ES, 1, 2>(p, sms, stream);
-        if (C <= kMostColumns) return launch_cluster<ES, 1>(p, sms, stream);
+    } else if (C <= kMostColumns) {
+        if constexpr (ES == 2)
+            if (pairs)
+                return launch_narrow<ES, 2>(p, sms, stream);
+        return launch_narrow<ES, 1>(p, sms, stream);
     }
     const int grid = static_cast<int>(std::min<int64_t>(p.R, static_cast<int64_t>(sms) * 8));
     if (vec)
@@ -151,7 +162,10 @@ extern "C" int fp8_layer_norm(const void *x, int x_type, int64_t ldx, const void
     const bool vec = C % 8 == 0 && rows_vec(x, p.ldx, x_type) && (!y || rows_vec(y, p.ldy, y_type)) &&
                      rows_vec(gamma, 0, param_type) && rows_vec(beta, 0, param_type) &&
                      (reinterpret_cast<uintptr_t>(q) & 7) == 0;
+    const bool pairs = C % 2 == 0 && rows_pairs(x, p.ldx, x_type) && (!y || rows_pairs(y, p.ldy, y_type)) &&
+                       rows_pairs(gamma, 0, param_type) && rows_pairs(beta, 0, param_type) &&
+                       (reinterpret_cast<uintptr_t>(q) & 1) == 0;
     p.groups = vec ? C / 8 : C;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return x_type == FP8MM_OUT_F32 ? launch<4>(p, vec, sms, s) : launch<2>(p, vec, sms, s);
+    return x_type == FP8MM_OUT_F32 ? launch<4>(p, vec, pairs, sms, s) : launch<2>(p, vec, pairs, sms, s);
 }

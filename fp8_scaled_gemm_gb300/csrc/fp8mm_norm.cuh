@@ -26,8 +26,8 @@
 //  - Arithmetic goes two columns at a time (f32x2).
 //  - Every warp covers 32 E neighbouring columns, so a thread's addresses
 //    differ by constants. Rows that start on 16 bytes take 16-byte loads of
-//    8 elements; other rows take single elements, neighbouring lanes
-//    neighbouring ones.
+//    8 elements; others single elements or, 16-bit ones of even width that
+//    start on 4 bytes, pairs, neighbouring lanes neighbouring ones.
 // Rows of more than 131072 columns (backward: of a cluster's eight CTAs) go
 // through the long kernels, which read the row again from L2 for each pass.
 #pragma once
@@ -52,13 +52,14 @@ constexpr int kStatusTimeout = 0x10b;
 constexpr int kCta = 0, kCluster = -1;
 
 // A thread's columns: E = 8 CH of them from c0 on. G = 8: groups of 8
-// neighbours, 8 x (lanes) apart; G = 1: single columns 32 apart. `left`
+// neighbours, 8 x (lanes) apart; G = 2 and 1: pairs and single columns, lane by
+// lane (pairs: an even number of columns). `left`
 // columns lie between c0 and the end of the row (of the CTA's slice).
 template <int G, int KIND, int CH>
 struct Place {
     static constexpr int E = 8 * CH;
     static constexpr int kLanes = KIND > 0 ? KIND : 32;
-    static constexpr int kStep = G == 8 ? 8 * kLanes : kLanes;   // between a thread's groups
+    static constexpr int kStep = G * kLanes;   // between a thread's groups
     long long c0;
     int left;
 
@@ -109,8 +110,8 @@ __device__ __forceinline__ void to_pairs(const RawE<ES, G, CH> &r, bool f16, uin
 #pragma unroll
             for (int i = 0; i < 4 * CH; ++i) {
                 float lo, hi;
-                if constexpr (G == 8) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r.r[i / 4].w[i % 4]));
+                if constexpr (G > 1) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r.r[2 * i / G].w[i % (G / 2)]));
                     lo = f.x;
                     hi = f.y;
                 } else {
@@ -122,9 +123,9 @@ __device__ __forceinline__ void to_pairs(const RawE<ES, G, CH> &r, bool f16, uin
         } else {
 #pragma unroll
             for (int i = 0; i < 4 * CH; ++i) {
-                if constexpr (G == 8)
-                    v[i] = ptx::f32x2(__uint_as_float(r.r[i / 4].w[i % 4] << 16),
-                                      __uint_as_float(r.r[i / 4].w[i % 4] & 0xFFFF0000u));
+                if constexpr (G > 1)
+                    v[i] = ptx::f32x2(__uint_as_float(r.r[2 * i / G].w[i % (G / 2)] << 16),
+                                      __uint_as_float(r.r[2 * i / G].w[i % (G / 2)] & 0xFFFF0000u));
                 else
                     v[i] = ptx::f32x2(__uint_as_float(r.r[2 * i].w[0] << 16), __uint_as_float(r.r[2 * i + 1].w[0] << 16));
             }
@@ -159,10 +160,10 @@ __device__ __forceinline__ void store_e(uint8_t *p, int type, const Place<G, KIN
             } else {
                 float a, b;
                 ptx::unpack_f32x2(v[i], a, b);
-                if (pl.in(2 * i))
-                    o[2 * i * step] = a;
-                if (pl.in(2 * i + 1))
-                    o[(2 * i + 1) * step] = b;
+                if (pl.in(2 * i / G))
+                    o[2 * i / G * step] = a;
+                if (pl.in((2 * i + 1) / G))
+                    o[(2 * i + 1) / G * step + (G == 2)] = b;
             }
         }
         return;
@@ -183,6 +184,11 @@ __device__ __forceinline__ void store_e(uint8_t *p, int type, const Place<G, KIN
         for (int k = 0; k < CH; ++k)
             if (pl.in(k))
                 *reinterpret_cast<uint4 *>(o + k * step) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    } else if constexpr (G == 2) {
+#pragma unroll
+        for (int i = 0; i < 4 * CH; ++i)
+            if (pl.in(i))
+                *reinterpret_cast<uint32_t *>(o + i * step) = w[i];
     } else {
 #pragma unroll
         for (int i = 0; i < 4 * CH; ++i) {
@@ -216,8 +222,8 @@ __device__ __forceinline__ void param_e(const void *base, int type, const Place<
                     v[i + 1] = ptx::f32x2(f.z, f.w);
                 }
             } else {
-                v[i] = ptx::f32x2(pl.in(2 * i) ? __ldg(p + 2 * i * step) : 0.0f,
-                                  pl.in(2 * i + 1) ? __ldg(p + (2 * i + 1) * step) : 0.0f);
+                v[i] = ptx::f32x2(pl.in(2 * i / G) ? __ldg(p + 2 * i / G * step) : 0.0f,
+                                  pl.in((2 * i + 1) / G) ? __ldg(p + (2 * i + 1) / G * step + (G == 2)) : 0.0f);
             }
         }
     } else {
@@ -247,8 +253,8 @@ __device__ __forceinline__ void mask_e(uint64_t (&v)[4 * CH], const Place<G, KIN
 {
 #pragma unroll
     for (int i = 0; i < 4 * CH; ++i) {
-        if constexpr (G == 8) {
-            v[i] = pl.in(i / 4) ? v[i] : 0ull;
+        if constexpr (G > 1) {
+            v[i] = pl.in(2 * i / G) ? v[i] : 0ull;
         } else {
             float a, b;
             ptx::unpack_f32x2(v[i], a, b);
@@ -564,6 +570,9 @@ __device__ __forceinline__ void store_codes_e(uint8_t *p, const Place<G, KIND, C
             if (i % 4 == 0 && pl.in(i / 4))
                 *reinterpret_cast<uint2 *>(p + (i / 4) * step) =
                     make_uint2(c[i] | (c[i + 1] << 16), c[i + 2] | (c[i + 3] << 16));
+        } else if constexpr (G == 2) {
+            if (pl.in(i))
+                *reinterpret_cast<unsigned short *>(p + i * step) = static_cast<unsigned short>(c[i]);
         } else {
             if (pl.in(2 * i))
                 p[2 * i * step] = static_cast<uint8_t>(c[i] & 0xFFu);
@@ -582,11 +591,12 @@ __device__ __forceinline__ void store_codes_e(uint8_t *p, const Place<G, KIND, C
 // registers 119 to 121; several rows' teams in one CTA 155; gamma and beta from
 // global memory (L1) for every row 174 (they are kept in shared memory,
 // keep_params); against 113: the warps' own means and differences joined in one
-// exchange instead of two 116. Rows that are not 16-byte aligned: 34 instructions
-// per element, 16384 x 4999 bf16 122 us (50 %) against 73 at 5000 columns;
-// pairs of elements by 4-byte accesses with single ones at the edges took 134
-// to 158, accesses without bounds tests in all but the last warp 118 (35
-// instead of 26 at 1001 columns).
+// exchange instead of two 116. Rows of 16-bit elements without 16-byte groups:
+// 16384 x 4998 bf16 in pairs 86 us (71 %; single elements 121), 16384 x 4999 in
+// single elements (34 instructions each) 122 us (50 %), against 73 at 5000
+// columns. For odd widths, pairs with single elements at the edges took 134 to
+// 158, accesses without bounds tests in all but the last warp 118 (35 instead
+// of 26 at 1001 columns).
 template <int ES, int G, int KIND, int CH>
 __global__ void __launch_bounds__(KIND > 0 ? 256 : 1024, KIND > 0 ? (CH == 4 ? 3 : 4) : 1)
     norm_kernel(const NormParams p)
@@ -798,7 +808,7 @@ struct NormGradParams {
 // 16-byte groups leave room for 16 columns.
 constexpr int kGradThreads = 512;
 template <int ES, int DES, int G, int KIND>
-constexpr int kGradCh = (ES == 2 && DES == 2 && G == 8 && KIND <= 0) ? 2 : 1;
+constexpr int kGradCh = (ES == 2 && DES == 2 && G > 1 && KIND <= 0) ? 2 : 1;
 
 // Each thread keeps the dgamma and dbeta sums of its columns in registers over
 // all its rows; teams of lanes then add theirs in order through shared memory.
@@ -806,8 +816,9 @@ constexpr int kGradCh = (ES == 2 && DES == 2 && G == 8 && KIND <= 0) ? 2 : 1;
 // copy), 8192 x 8192 fp32 178 (91 %). Registers (128 per thread) hold one row at
 // work, one on its way and the sums, so an SM has 512 threads and wide rows one
 // or two teams: 8192 x 16384 bf16 runs at 73 %, 4096 x 32768 at 42 %, waiting for
-// exchanges. Unaligned rows hold 8 columns per thread (16384 x 4095 bf16 129 us,
-// 62 %; over 4096 columns, in clusters, 19 to 39 %).
+// exchanges. In pairs 16384 x 4094 takes 113 us (71 %), 12782 x 10500 361 (45 %;
+// single elements 728). Single elements leave registers for 8 columns per thread
+// (16384 x 4095 bf16 129 us, 62 %; over 4096 columns, in clusters, 19 to 39 %).
 // Teams of lanes: CTAs of 256 threads, 4 on an SM (3 where registers hold fp32 rows).
 constexpr int kGradLaneThreads = 256;
 template <int ES, int DES>

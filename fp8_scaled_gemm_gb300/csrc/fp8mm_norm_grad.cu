@@ -124,11 +124,11 @@ int launch_wide(const NormGradParams &p, int sms, cudaStream_t stream, int *P)
             const int64_t each = cdiv(warps, ctas);
             return launch_cluster<ES, DES, G>(p, ctas, each * warp_cols, static_cast<int>(each) * 32, sms, stream, P);
         }
-    return launch_long<ES, DES, G>(p, sms, stream, P);
+    return launch_long<ES, DES, G == 8 ? 8 : 1>(p, sms, stream, P);
 }
 
 template <int ES, int DES>
-int launch(const NormGradParams &p, bool vec, int sms, cudaStream_t stream, int *P)
+int launch(const NormGradParams &p, bool vec, bool pairs, int sms, cudaStream_t stream, int *P)
 {
     const int64_t C = p.C;
     if (vec) {
@@ -138,6 +138,9 @@ int launch(const NormGradParams &p, bool vec, int sms, cudaStream_t stream, int 
         if (C <= 256) return launch_lanes<ES, DES, 8, 32>(p, sms, stream, P);
         return launch_wide<ES, DES, 8>(p, sms, stream, P);
     }
+    if constexpr (ES == 2 && DES == 2)
+        if (pairs)
+            return C <= 256 ? launch_lanes<ES, DES, 2, 32>(p, sms, stream, P) : launch_wide<ES, DES, 2>(p, sms, stream, P);
     if (C <= 256)
         return launch_lanes<ES, DES, 1, 32>(p, sms, stream, P);
     return launch_wide<ES, DES, 1>(p, sms, stream, P);
@@ -234,11 +237,14 @@ int fp8_layer_norm_grad(const void *dy, int dy_type, int64_t lddy, const void *x
                      (!p.dres || rows_vec(dres, ldr, x_type)) && (!dx || rows_vec(dx, ldd, x_type)) &&
                      rows_vec(gamma, 0, param_type) &&
                      (!direct || (rows_vec(dgamma, 0, FP8MM_OUT_F32) && rows_vec(dbeta, 0, FP8MM_OUT_F32)));
+    const bool pairs = C % 2 == 0 && rows_pairs(x, p.ldx, x_type) && rows_pairs(dy, p.lddy, dy_type) &&
+                       (!p.dres || rows_pairs(dres, ldr, x_type)) && (!dx || rows_pairs(dx, ldd, x_type)) &&
+                       rows_pairs(gamma, 0, param_type);
     p.groups = vec ? C / 8 : C;
     int P = 0;
     const bool x4 = x_type == FP8MM_OUT_F32, d4 = dy_type == FP8MM_OUT_F32;
-    rc = x4 ? (d4 ? launch<4, 4>(p, vec, sms, s, &P) : launch<4, 2>(p, vec, sms, s, &P))
-            : (d4 ? launch<2, 4>(p, vec, sms, s, &P) : launch<2, 2>(p, vec, sms, s, &P));
+    rc = x4 ? (d4 ? launch<4, 4>(p, vec, pairs, sms, s, &P) : launch<4, 2>(p, vec, pairs, sms, s, &P))
+            : (d4 ? launch<2, 4>(p, vec, pairs, sms, s, &P) : launch<2, 2>(p, vec, pairs, sms, s, &P));
     if (rc != FP8MM_OK || !dgamma || direct)
         return rc;
     return sum_partials(p, P, dgamma, dbeta, s);

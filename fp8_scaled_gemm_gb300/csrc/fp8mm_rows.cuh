@@ -22,10 +22,11 @@ namespace ptx = fp8mm::ptx;
 constexpr int kBF16 = 0, kF16 = 1, kF32 = 2;
 
 // G consecutive elements of ES bytes as loaded: 16-byte words for G = 8
-// (16-byte aligned), one element for G = 1.
+// (16-byte aligned), one word for a pair of 16-bit elements (G = 2, 4-byte
+// aligned), one element for G = 1.
 template <int ES, int G>
 struct Raw {
-    static_assert((ES == 2 || ES == 4) && (G == 8 || G == 1), "element group");
+    static_assert((ES == 2 || ES == 4) && (G == 8 || G == 1 || (G == 2 && ES == 2)), "element group");
     static constexpr int kWords = G == 1 ? 1 : G * ES / 4;
     uint32_t w[kWords];
 };
@@ -40,6 +41,8 @@ __device__ __forceinline__ void load_raw(Raw<ES, G> &r, const void *base, long l
         } else {
             asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(r.w[0]) : "l"(p));
         }
+    } else if constexpr (G == 2) {
+        asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(r.w[0]) : "l"(p));
     } else {
 #pragma unroll
         for (int i = 0; i < Raw<ES, G>::kWords; i += 4)

@@ -29,6 +29,12 @@ inline bool rows_vec(const void *p, int64_t ld, int type)
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * row_type_bytes(type)) % 16 == 0;
 }
 
+// Whether pairs of 16-bit elements of every row start on 4 bytes (fp32 rows do).
+inline bool rows_pairs(const void *p, int64_t ld, int type)
+{
+    return type == FP8MM_OUT_F32 || ((reinterpret_cast<uintptr_t>(p) & 3) == 0 && ld % 2 == 0);
+}
+
 // Launch on a two-dimensional grid with programmatic stream serialization.
 template <typename Kern, typename... Args>
 int launch_grid2(Kern kern, int64_t gx, int64_t gy, int threads, cudaStream_t stream, const char *what, Args... args)

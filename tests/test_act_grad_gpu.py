@@ -143,3 +143,16 @@ def test_stray_writes():
         fm.fp8_act_grad(dy, z, 2, dz=buf[1:1 + M, 8:8 + N], dbias=sums[4:4 + N])
         assert bool((buf[keep] == 9.0).all())
         assert bool((sums[:4] == 9.0).all()) and bool((sums[4 + N:] == 9.0).all())
+
+
+@pytest.mark.parametrize("N,ld,shift", [(2, None, 0), (62, None, 0), (90, None, 0), (130, None, 0), (1002, None, 0),
+                                        (1002, (1004, 1006, 1010), 0), (1002, (1004, 1006, 1010), 2),
+                                        (1002, (1002, 1002, 1002), 1), (1002, (1003, 1004, 1002), 0)])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_even_widths(N, ld, shift, dtype):
+    """Pairs of 16-bit elements where rows start on 4 bytes."""
+    _need_gpu()
+    kw = {} if ld is None else dict(ld=ld, shift=shift)
+    for M in (1, 37, 700):
+        run(M, N, dtype=dtype, **kw)
+

@@ -325,3 +325,35 @@ def test_stray_writes():
         buf.fill_(9.0)
         fm.fp8_layer_norm_grad(dy, x, None, mean, rstd, dx=inner)
         assert bool((buf[keep] == 9.0).all())
+
+
+# Even widths that are not multiples of 8: pairs of 16-bit elements where rows
+# start on 4 bytes, single elements where they do not.
+EVEN = [2, 6, 90, 202, 258, 514, 1002, 1026, 4094, 4998, 8190, 8194, 9132, 16386, 20002]
+
+
+@pytest.mark.parametrize("C", EVEN)
+@pytest.mark.parametrize("x_dtype,y_dtype", [(BF16, None), (F16, F32), (F32, BF16)])
+def test_forward_even_widths(C, x_dtype, y_dtype):
+    _need_gpu()
+    forward(300, C, x_dtype=x_dtype, y_dtype=y_dtype, p_dtype=F32 if y_dtype else BF16)
+    forward(9, C, x_dtype=x_dtype, y_dtype=y_dtype, q_dtype=None, gamma=False)
+
+
+@pytest.mark.parametrize("C", EVEN)
+@pytest.mark.parametrize("x_dtype,dy_dtype", [(BF16, BF16), (F16, BF16), (BF16, F32)])
+def test_backward_even_widths(C, x_dtype, dy_dtype):
+    _need_gpu()
+    backward(300, C, x_dtype=x_dtype, dy_dtype=dy_dtype)
+    backward(9, C, x_dtype=x_dtype, dy_dtype=dy_dtype, p_dtype=BF16, residual=False)
+
+
+@pytest.mark.parametrize("C,ld,shift", [(1002, (1002, 1004, 1006, 1008), 2), (1002, (1002, 1004, 1005, 1008), 0),
+                                        (1002, (1002, 1002, 1002, 1002), 1), (1002, (1003, 1003, 1003, 1003), 0),
+                                        (4998, (4998, 5000, 5002, 4998), 0), (9132, (9132, 9134, 9136, 9138), 0)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_even_widths_strides_and_alignment(C, ld, shift, in_place):
+    _need_gpu()
+    forward(60, C, ldx=ld[1], shift=shift)
+    backward(60, C, ld=ld, shift=shift, in_place=in_place)
+
