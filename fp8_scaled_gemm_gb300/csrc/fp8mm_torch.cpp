@@ -4,8 +4,8 @@
 // These calls make up to five new tensors each, and with few rows their
 // kernels take 2 to 10 us, so the host's time is the call's time. Through
 // ctypes, with the checks and torch.empty in Python, one token's layer norm
-// with codes took 21 us a call on a Grace core, here 7.8; a product with a new
-// output 14, here 3.7. The module checks arguments, makes the tensors that are
+// with codes took 21 us a call on a Grace core, here 9.0; a product with a new
+// output 14, here 3.9. The module checks arguments, makes the tensors that are
 // not given, and calls the C entries, whose addresses it is handed (init); it
 // runs nothing on the device itself. Errors are ValueError for arguments
 // (TypeError for what is no tensor) and what `check` raises for a status.
@@ -66,6 +66,14 @@ void checked(int64_t rc)
     }
     throw Raised{};
 }
+
+// Other Python threads run while this one makes its tensors and launches
+// (either can wait: for memory, for room in the stream's queue). Once per call:
+// it costs 0.4 us.
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
 
 void *stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
 
@@ -167,22 +175,41 @@ Tensor empty(const Tensor &like, at::IntArrayRef shape, ScalarType type)
     return at::empty(shape, like.options().dtype(type));
 }
 
-// A result: the tensor that was given, a new one, or None.
+// A result: the tensor that was given, one to be made, or None.
 struct Result {
     PyObject *given = nullptr;
+    const Tensor *t = nullptr;       // given or made
     Tensor made;
-    const Tensor *t = nullptr;
+    const Tensor *like = nullptr;    // to be made: of this one's device, [rows, cols] or [rows]
+    int64_t rows = 0, cols = 0;
+    ScalarType type = ScalarType::Float;
 
     void take(const char *name, PyObject *o)
     {
         t = tensor(name, o, true);
         given = t ? o : nullptr;
+        if (t)
+            type = t->scalar_type();
     }
-    void make(const Tensor &like, at::IntArrayRef shape, ScalarType type)
+    void plan(const Tensor &x, ScalarType ty, int64_t r, int64_t c = -1)
     {
-        made = empty(like, shape, type);
-        t = &made;
+        like = &x;
+        type = ty;
+        rows = r;
+        cols = c;
     }
+    bool wanted() const { return t || like; }
+    // (without the interpreter's lock)
+    void *make()
+    {
+        if (!t && like) {
+            const int64_t shape[2] = {rows, cols};
+            made = empty(*like, at::IntArrayRef(shape, cols < 0 ? 1 : 2), type);
+            t = &made;
+        }
+        return t ? t->data_ptr() : nullptr;
+    }
+    float *make_floats() { return static_cast<float *>(make()); }
     PyObject *object()
     {
         PyObject *o = !t ? Py_None : given;
@@ -282,7 +309,7 @@ void product_out(Product &p, Result &out, PyObject *given, ScalarType type)
     if (!out.t) {
         if (out_code(type) < 0)
             refuse("out must be a [M, N] tensor of bfloat16, float16, float32 or float8_e4m3fn with contiguous rows");
-        out.make(*p.A, {p.M, p.N}, type);
+        out.plan(*p.A, type, p.M, p.N);
     } else {
         const Tensor &t = *out.t;
         if (out_code(t.scalar_type()) < 0 || t.dim() != 2 || t.size(0) != p.M || t.size(1) != p.N ||
@@ -292,12 +319,12 @@ void product_out(Product &p, Result &out, PyObject *given, ScalarType type)
             refuse("fp8_scaled_mm takes CUDA tensors (use fp8_scaled_mm_host for host memory)");
         p.options.ldo = t.is_contiguous() ? 0 : t.stride(0);
     }
-    p.options.out_type = out_code(out.t->scalar_type());
+    p.options.out_type = out_code(out.type);
 }
 
-ScalarType aux_type(const Tensor &out)
+ScalarType aux_type(const Result &out)
 {
-    return out.scalar_type() == ScalarType::Float8_e4m3fn ? ScalarType::BFloat16 : out.scalar_type();
+    return out.type == ScalarType::Float8_e4m3fn ? ScalarType::BFloat16 : out.type;
 }
 
 // Leading dimension of a [M, N] matrix beside out (residual, preact, z).
@@ -323,22 +350,28 @@ PyObject *mm_epilogue(PyObject *const *a)
     const bool return_preact = truth(a[11]);
     Result out, preact;
     product_out(p, out, a[9], dtype("out_dtype", a[10]));
-    const ScalarType type = aux_type(*out.t);
+    const ScalarType type = aux_type(out);
     if (bias && (bias->scalar_type() != type || bias->numel() != p.N || !bias->is_contiguous()))
         refuse("bias must be a contiguous tensor of N values of out's dtype (bfloat16 for a float8_e4m3fn output)");
     if (bias && !bias->is_cuda())
         refuse("fp8_scaled_mm takes CUDA tensors (use fp8_scaled_mm_host for host memory)");
     preact.take("preact", a[8]);
     if (return_preact && !preact.t)
-        preact.make(*p.A, {p.M, p.N}, type);
+        preact.plan(*p.A, type, p.M, p.N);
     fp8mm_epilogue e{};
     e.activation = integer(a[6]);
     e.residual = data(residual);
     e.ldr = aux("residual", p, residual, type);
-    e.preact = data(preact.t);
     e.ldp = aux("preact", p, preact.t, type);
-    checked(api.mm_epilogue(data(p.A), data(p.B), floats(p.scale_a), floats(p.scale_b), p.mode, data(bias), data(out.t),
-                            p.M, p.N, p.K, stream(), &p.options, &e));
+    int64_t rc;
+    {
+        Unlocked u;
+        void *to = out.make();
+        e.preact = preact.make();
+        rc = api.mm_epilogue(data(p.A), data(p.B), floats(p.scale_a), floats(p.scale_b), p.mode, data(bias), to, p.M, p.N,
+                             p.K, stream(), &p.options, &e);
+    }
+    checked(rc);
     return return_preact ? tuple({&out, &preact}) : out.object();
 }
 
@@ -350,9 +383,16 @@ PyObject *mm_act_grad(PyObject *const *a)
     const Tensor *z = tensor("z", a[5]);
     Result out;
     product_out(p, out, a[7], a[8] == Py_None ? z->scalar_type() : dtype("out_dtype", a[8]));
-    const int64_t ldz = aux("z", p, z, aux_type(*out.t));
-    checked(api.mm_act_grad(data(p.A), data(p.B), floats(p.scale_a), floats(p.scale_b), p.mode, integer(a[6]), data(z),
-                            ldz, data(out.t), p.M, p.N, p.K, stream(), &p.options));
+    const int64_t ldz = aux("z", p, z, aux_type(out));
+    const int activation = integer(a[6]);
+    int64_t rc;
+    {
+        Unlocked u;
+        void *to = out.make();
+        rc = api.mm_act_grad(data(p.A), data(p.B), floats(p.scale_a), floats(p.scale_b), p.mode, activation, data(z), ldz,
+                             to, p.M, p.N, p.K, stream(), &p.options);
+    }
+    checked(rc);
     return out.object();
 }
 
@@ -367,22 +407,28 @@ PyObject *act_grad(PyObject *const *a)
     const int64_t ldz = z ? rows("z", *z, &dy, &type) : 0;
     Result dz, dbias;
     dz.take("dz", a[3]);
-    if (!dz.t && truth(a[5]))
-        dz.make(dy, {M, N}, type);
     const int64_t lddz = dz.t ? rows("dz", *dz.t, &dy, &type) : 0;
+    if (!dz.t && truth(a[5]))
+        dz.plan(dy, type, M, N);
     dbias.take("dbias", a[4]);
+    vector("dbias", dbias.t, N, false);
     if (!dbias.t && truth(a[6]))
-        dbias.make(dy, {N}, ScalarType::Float);
-    Tensor ws;
-    int64_t bytes = 0;
-    if (dbias.t) {
-        vector("dbias", dbias.t, N, false);
+        dbias.plan(dy, ScalarType::Float, N);
+    const int activation = integer(a[2]);
+    int64_t bytes = 0, rc;
+    if (dbias.wanted())
         checked(bytes = api.act_grad_workspace(M, N));
+    {
+        Unlocked u;
+        void *to = dz.make();
+        float *sums = dbias.make_floats();
+        Tensor ws;
         if (bytes > 0)
             ws = empty(dy, {bytes}, ScalarType::Byte);
+        rc = api.act_grad(data(&dy), lddy, data(z), ldz, row_code(type), activation, to, lddz, sums, M, N,
+                          bytes > 0 ? data(&ws) : nullptr, bytes, stream());
     }
-    checked(api.act_grad(data(&dy), lddy, data(z), ldz, row_code(type), integer(a[2]), data(dz.t), lddz, floats(dbias.t),
-                         M, N, bytes > 0 ? data(&ws) : nullptr, bytes, stream()));
+    checked(rc);
     return tuple({&dz, &dbias});
 }
 
@@ -408,21 +454,29 @@ PyObject *layer_norm(PyObject *const *a)
     } else if (truth(a[7])) {
         if (row_code(y_type) < 0)
             refuse("y_dtype must be torch.bfloat16, torch.float16 or torch.float32");
-        y.make(x, {R, C}, y_type);
+        y.plan(x, y_type, R, C);
     }
-    const int q_type = a[6] == Py_None ? 0 : fp8_code(dtype("q_dtype", a[6]));
-    if (q_type < 0)
+    const bool codes = a[6] != Py_None;
+    const ScalarType code_type = codes ? dtype("q_dtype", a[6]) : ScalarType::Float8_e4m3fn;
+    if (fp8_code(code_type) < 0)
         refuse("q_dtype must be torch.float8_e4m3fn or torch.float8_e5m2");
-    mean.make(x, {R}, ScalarType::Float);
-    rstd.make(x, {R}, ScalarType::Float);
-    if (a[6] != Py_None) {
-        q.make(x, {R, C}, dtype("q_dtype", a[6]));
-        q_scale.make(x, {R}, ScalarType::Float);
+    mean.plan(x, ScalarType::Float, R);
+    rstd.plan(x, ScalarType::Float, R);
+    if (codes) {
+        q.plan(x, code_type, R, C);
+        q_scale.plan(x, ScalarType::Float, R);
     }
-    checked(api.layer_norm(data(&x), row_code(x.scalar_type()), ldx, data(gamma), data(beta),
-                           params ? row_code(params->scalar_type()) : FP8MM_OUT_F32, static_cast<float>(eps), data(y.t),
-                           y.t ? row_code(y.t->scalar_type()) : FP8MM_OUT_F32, ldy, floats(mean.t), floats(rstd.t),
-                           data(q.t), q_type, floats(q_scale.t), R, C, stream()));
+    int64_t rc;
+    {
+        Unlocked u;
+        void *to = y.make(), *to_q = q.make();
+        float *means = mean.make_floats(), *rstds = rstd.make_floats(), *scales = q_scale.make_floats();
+        rc = api.layer_norm(data(&x), row_code(x.scalar_type()), ldx, data(gamma), data(beta),
+                            params ? row_code(params->scalar_type()) : FP8MM_OUT_F32, static_cast<float>(eps), to,
+                            y.t ? row_code(y.type) : FP8MM_OUT_F32, ldy, means, rstds, to_q, fp8_code(code_type), scales,
+                            R, C, stream());
+    }
+    checked(rc);
     return q.t ? tuple({&y, &mean, &rstd, &q, &q_scale}) : tuple({&y, &mean, &rstd});
 }
 
@@ -443,20 +497,26 @@ PyObject *layer_norm_grad(PyObject *const *a)
     if (dx.t)
         lddx = rows("dx", *dx.t, &x, &type);
     else
-        dx.make(x, {R, C}, type);
-    Tensor ws;
-    int64_t bytes = 0;
+        dx.plan(x, type, R, C);
+    int64_t bytes = 0, rc;
     if (truth(a[7])) {
         checked(bytes = api.layer_norm_grad_workspace(R, C));
-        dgamma.make(x, {C}, ScalarType::Float);
-        dbeta.make(x, {C}, ScalarType::Float);
+        dgamma.plan(x, ScalarType::Float, C);
+        dbeta.plan(x, ScalarType::Float, C);
+    }
+    {
+        Unlocked u;
+        void *to = dx.make();
+        float *to_gamma = dgamma.make_floats(), *to_beta = dbeta.make_floats();
+        Tensor ws;
         if (bytes > 0)
             ws = empty(x, {bytes}, ScalarType::Byte);
+        rc = api.layer_norm_grad(data(&dy), row_code(dy.scalar_type()), lddy, data(&x), row_code(type), ldx, data(gamma),
+                                 gamma ? row_code(gamma->scalar_type()) : FP8MM_OUT_F32, floats(mean), floats(rstd),
+                                 data(res), lddres, to, lddx, to_gamma, to_beta, R, C, bytes > 0 ? data(&ws) : nullptr,
+                                 bytes, stream());
     }
-    checked(api.layer_norm_grad(data(&dy), row_code(dy.scalar_type()), lddy, data(&x), row_code(type), ldx, data(gamma),
-                                gamma ? row_code(gamma->scalar_type()) : FP8MM_OUT_F32, floats(mean), floats(rstd),
-                                data(res), lddres, data(dx.t), lddx, floats(dgamma.t), floats(dbeta.t), R, C,
-                                bytes > 0 ? data(&ws) : nullptr, bytes, stream()));
+    checked(rc);
     return tuple({&dx, &dgamma, &dbeta});
 }
 

@@ -147,3 +147,37 @@ def test_new_outputs_on_the_callers_stream(ops):
     torch.cuda.synchronize()
     assert torch.equal(want, got) and torch.equal(want, inside)
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(norm, on))
+
+
+def test_threads_with_streams_of_their_own(ops):
+    """Calls of several threads at once give the results of one."""
+    import threading
+    o = ops
+
+    def once():
+        r = [fm.fp8_scaled_mm_epilogue(o["A"], o["B"], o["sa"], o["sb"], 1, activation=2, residual=o["z"])]
+        r += fm.fp8_act_grad(o["dy"], o["z"], fm.ACT_SILU)
+        r += fm.fp8_layer_norm(o["x"], o["gamma"])
+        r += fm.fp8_layer_norm_grad(o["dy"], o["x"], o["gamma"], o["mean"], o["rstd"])
+        return r
+    want = once()
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(60):
+                    got = once()
+                s.synchronize()
+            bad.extend(i for i, (a, b) in enumerate(zip(want, got)) if not torch.equal(a, b))
+        except Exception as e:      # reported by the main thread
+            bad.append(e)
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=60)
+    assert not any(t.is_alive() for t in threads) and not bad, bad
+
