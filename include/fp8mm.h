@@ -450,7 +450,9 @@ int64_t fp8_act_grad_workspace(int64_t M, int64_t N);
  *
  * A NaN or infinity makes its whole row NaN. Rows of zeros in y give the
  * codes of zeros and a zero scale. Any C >= 1; rows whose x, y, gamma and
- * beta start on 16 bytes (q on 8) with C % 8 == 0 run fastest.
+ * beta start on 16 bytes (q on 8) with C % 8 == 0 run fastest. A wait of wide
+ * rows' CTAs for one another is bounded; fp8mm_device_status reports one that
+ * ran out.
  * R * C <= 2^40. Asynchronous on `stream`, one launch, no workspace.
  */
 int fp8_layer_norm(const void *x, int x_type, int64_t ldx,
@@ -477,6 +479,7 @@ int fp8_layer_norm(const void *x, int x_type, int64_t ldx,
  *
  * R == 0 gives parameter gradients of zeros. The sums are added in an order
  * that depends on the sizes, alignment and SM count only, so results repeat.
+ * Bounded waits as in fp8_layer_norm.
  */
 int fp8_layer_norm_grad(const void *dy, int dy_type, int64_t lddy, const void *x, int x_type, int64_t ldx,
                         const void *gamma, int param_type, const float *mean, const float *rstd,
@@ -647,7 +650,8 @@ const char *fp8mm_last_error(void);
  * stream_k_tiles (tiles whose K blocks are spread over all CTA pairs) and
  * group (tile rows per group of the tile order, when not 8). Example:
  * "pair tile_n=256 split=1 tiles=32x32 units=912 grid=152
- * stream_k_tiles=112 group=16". */
+ * stream_k_tiles=112 group=16". The plain product's choice: the extended
+ * epilogue's differs up to two waves of tiles. */
 const char *fp8mm_describe_choice(int64_t M, int64_t N, int64_t K, int scale_mode);
 
 /* The same for a batch of `batch` products (fp8_scaled_bmm); tiles are per
