@@ -244,9 +244,10 @@ def _validate(A, B, scale_a, scale_b, scale_mode, bias, out, device_side: bool, 
     fp8 = _FP8 if typed else (torch.float8_e4m3fn,)
     if A.dtype not in fp8 or B.dtype not in fp8:
         raise ValueError("A and B must be torch.float8_e4m3fn" + (" or float8_e5m2" if typed else ""))
-    if A.stride() != (K, 1) and M > 1:
+    # (one row or one column: the outer stride does not matter, the inner one does)
+    if A.stride() != (K, 1) and (M > 1 or (M == 1 and A.stride(1) != 1)):
         raise ValueError("A must be row-major contiguous [M, K]")
-    if B.stride() != (1, K) and N > 1:
+    if B.stride() != (1, K) and (N > 1 or (N == 1 and B.stride(0) != 1)):
         raise ValueError("B must be column-major [K, N] (B.t() contiguous)")
     if scale_mode not in (SCALE_TENSOR, SCALE_ROWWISE):
         raise ValueError("scale_mode must be 0 (per-tensor) or 1 (row-wise)")

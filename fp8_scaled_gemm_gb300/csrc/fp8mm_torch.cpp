@@ -257,7 +257,12 @@ std::string shape_of(const Tensor &t)
     return s + (t.dim() == 1 ? ",)" : ")");
 }
 
-bool strides_are(const Tensor &t, int64_t s0, int64_t s1) { return t.stride(0) == s0 && t.stride(1) == s1; }
+// Whether n rows (columns) of K elements lie back to back: dimension `inner` of
+// t runs along K. With one of them the other stride does not matter.
+bool back_to_back(const Tensor &t, int inner, int64_t n, int64_t K)
+{
+    return n == 0 || (t.stride(inner) == 1 && (n == 1 || t.stride(1 - inner) == K));
+}
 
 // The operands and options of a product: A, B, scale_a, scale_b, scale_mode
 // from a[0], variant, tile_n, split_k from o[0].
@@ -281,9 +286,9 @@ Product product(PyObject *const *a, PyObject *const *o)
     p.options.b_type = fp8_code(B.scalar_type());
     if (p.options.a_type < 0 || p.options.b_type < 0)
         refuse("A and B must be torch.float8_e4m3fn or float8_e5m2");
-    if (p.M > 1 && !strides_are(A, p.K, 1))
+    if (!back_to_back(A, 1, p.M, p.K))
         refuse("A must be row-major contiguous [M, K]");
-    if (p.N > 1 && !strides_are(B, 1, p.K))
+    if (!back_to_back(B, 0, p.N, p.K))
         refuse("B must be column-major [K, N] (B.t() contiguous)");
     if (p.mode != FP8MM_SCALE_TENSOR && p.mode != FP8MM_SCALE_ROWWISE)
         refuse("scale_mode must be 0 (per-tensor) or 1 (row-wise)");
