@@ -882,21 +882,37 @@ __device__ __forceinline__ void store_column_sums(const NormGradParams &p, long 
     }
 }
 
+// Whether a thread has several groups of columns: some can lie in the row and others not.
+template <int G, int CH>
+constexpr bool kMixed = 8 * CH / G > 1;
+
 // A row's terms of the column sums, and its two sums: s1 of w = dy gamma, s2 of
-// w xhat. h: x, then xhat; w: dy, then w. m2, r2: -mean and rstd twice.
-template <int CH>
+// w xhat. h: x, then xhat; w: dy, then w. m2, r2: -mean and rstd twice. Outside
+// the row w is 0, but xhat would be -mean rstd, which can leave fp32's range and
+// make w xhat NaN. So a thread of one group takes 0 for both outside the row
+// (the callers see to it), and one of several sets xhat to 0 there (1 to 3 % of
+// those kernels).
+template <int G, int KIND, int CH>
 __device__ __forceinline__ void grad_terms(uint64_t (&h)[4 * CH], uint64_t (&w)[4 * CH], uint64_t m2, uint64_t r2,
-                                           const float4 *my_gamma, int threads, uint64_t (&dga)[4 * CH],
-                                           uint64_t (&dbe)[4 * CH], float (&s)[2])
+                                           const float4 *my_gamma, int threads, const Place<G, KIND, CH> &pl,
+                                           uint64_t (&dga)[4 * CH], uint64_t (&dbe)[4 * CH], float (&s)[2])
 {
     constexpr int P = 4 * CH;
     uint64_t s1 = 0, s2 = 0;
+    if constexpr (kMixed<G, CH>) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            h[i] = ptx::mul_f32x2(ptx::add_f32x2(h[i], m2), r2);
+        if (!pl.in(8 * CH / G - 1))
+            mask_e<G, KIND, CH>(h, pl);
+    }
 #pragma unroll
     for (int j = 0; j < P / 2; ++j) {
         const float4 g4 = my_gamma[j * threads];
 #pragma unroll
         for (int i = 2 * j; i < 2 * j + 2; ++i) {
-            h[i] = ptx::mul_f32x2(ptx::add_f32x2(h[i], m2), r2);
+            if constexpr (!kMixed<G, CH>)
+                h[i] = ptx::mul_f32x2(ptx::add_f32x2(h[i], m2), r2);
             dga[i] = ptx::fma_f32x2(w[i], h[i], dga[i]);
             dbe[i] = ptx::add_f32x2(dbe[i], w[i]);
             w[i] = ptx::mul_f32x2(w[i], i == 2 * j ? ptx::f32x2(g4.x, g4.y) : ptx::f32x2(g4.z, g4.w));
@@ -947,8 +963,10 @@ __global__ void __launch_bounds__(KIND > 0 ? kGradLaneThreads : kGradThreads, KI
     if (first < p.R) {
         load_e<ES, G, KIND, CH>(nx, px, pl);
         load_e<DES, G, KIND, CH>(nd, pd, pl);
-        nmean = __ldg(p.mean + first);
-        nrstd = __ldg(p.rstd + first);
+        if (kMixed<G, CH> || pl.in(0)) {
+            nmean = __ldg(p.mean + first);
+            nrstd = __ldg(p.rstd + first);
+        }
     }
     uint64_t dga[P] = {}, dbe[P] = {};
     const int threads = static_cast<int>(blockDim.x);
@@ -979,12 +997,14 @@ __global__ void __launch_bounds__(KIND > 0 ? kGradLaneThreads : kGradThreads, KI
         if (row + stride < p.R) {
             load_e<ES, G, KIND, CH>(nx, px, pl);
             load_e<DES, G, KIND, CH>(nd, pd, pl);
-            nmean = __ldg(p.mean + row + stride);
-            nrstd = __ldg(p.rstd + row + stride);
+            if (kMixed<G, CH> || pl.in(0)) {
+                nmean = __ldg(p.mean + row + stride);
+                nrstd = __ldg(p.rstd + row + stride);
+            }
         }
         float s[2] = {0.0f, 0.0f};
         if (valid)
-            grad_terms<CH>(h, w, m2, r2, my_gamma, threads, dga, dbe, s);
+            grad_terms<G, KIND, CH>(h, w, m2, r2, my_gamma, threads, pl, dga, dbe, s);
         if (p.dx == nullptr)
             continue;                    // parameter sums only
         if (!team_sum8<KIND, 2>(s, tm, red[flip], flip, static_cast<uint32_t>(turn >> 1) & 1u))
@@ -1077,7 +1097,8 @@ __global__ void __launch_bounds__(kGradThreads) norm_grad_cluster_kernel(const N
             float s[2];
             to_pairs<ES, G, CH>(nx, p.x_f16, h);
             to_pairs<DES, G, CH>(nd, p.dy_f16, w);
-            grad_terms<CH>(h, w, ptx::f32x2(-nmean, -nmean), ptx::f32x2(nrstd, nrstd), my_gamma, threads, dga, dbe, s);
+            grad_terms<G, KIND, CH>(h, w, ptx::f32x2(-nmean, -nmean), ptx::f32x2(nrstd, nrstd), my_gamma, threads, pl, dga,
+                                    dbe, s);
             row += stride;
             if (dx) {
 #pragma unroll
