@@ -528,30 +528,38 @@ __device__ __forceinline__ void store_codes(uint8_t *dst, const fp8q::Divider &d
     }
 }
 
-// The codes of the thread's values: with a scale in the normal range by its
-// reciprocal (the unrounded y is off by more than that product's rounding),
-// else by division, as fp8_quantize does.
+// The codes of the thread's values, those of fp8_quantize (a y of -0 may give +0).
+// With a scale in the reciprocal's range the quotients come from the reciprocal in
+// two parts: r, the nearest fp32 value to 1 / scale (rcp.approx and one step of
+// Newton's iteration, which gave __frcp_rn's for every mantissa), and rl, what is
+// left of 1 / scale, so that v r + v rl is rounded once but for 2^-46 of it. On a CPU
+// every mantissa of the scale, with every value within 12 units of its product with
+// every tie between two codes, gave the code of the correctly rounded quotient.
+// (16384 x 8192 bf16: the reciprocal alone, which is on the wrong side of some
+// ties, with a scale of one product 116 us, this 123, div_fast's correction 127.)
 template <int G, int KIND, int CH>
 __device__ __forceinline__ void store_codes_e(uint8_t *p, const Place<G, KIND, CH> &pl, float scale,
                                               const uint64_t (&v)[4 * CH], int q_type)
 {
     constexpr int step = Place<G, KIND, CH>::kStep;
     uint32_t c[4 * CH];                  // two codes each
-    if (scale >= 0x1p-80f && scale < 0x1p100f) {
-        const float r = fp8mm::rcp_approx(scale);
-        const uint64_t r2 = ptx::f32x2(r, r);
+    if (fp8q::in_reciprocal_range(scale)) {
+        const float r0 = fp8mm::rcp_approx(scale), r = fmaf(fmaf(-scale, r0, 1.0f), r0, r0);
+        const float e = fmaf(-scale, r, 1.0f), rl = fmaf(e, e, e) * r;
+        const uint64_t r2 = ptx::f32x2(r, r), l2 = ptx::f32x2(rl, rl);
+        // one branch for all
         if (q_type == 0) {
 #pragma unroll
             for (int i = 0; i < 4 * CH; ++i) {
                 float a, b;
-                ptx::unpack_f32x2(ptx::mul_f32x2(v[i], r2), a, b);
+                ptx::unpack_f32x2(ptx::fma_f32x2(v[i], r2, ptx::mul_f32x2(v[i], l2)), a, b);
                 c[i] = fp8q::cvt_pair(a, b, 0);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 4 * CH; ++i) {
                 float a, b;
-                ptx::unpack_f32x2(ptx::mul_f32x2(v[i], r2), a, b);
+                ptx::unpack_f32x2(ptx::fma_f32x2(v[i], r2, ptx::mul_f32x2(v[i], l2)), a, b);
                 c[i] = fp8q::cvt_pair(a, b, 1);
             }
         }
@@ -584,8 +592,9 @@ __device__ __forceinline__ void store_codes_e(uint8_t *p, const Place<G, KIND, C
 
 // One row per CTA at a time (KIND > 0: per team of lanes), 64 registers, and
 // as many CTAs on an SM as make 1024 threads: they hide each other's barriers.
-// 16 columns per thread. 16384 x 8192 bf16 with codes takes 113 us, 5.9 TB/s (89 %
-// of a copy; 20 instructions per element, issue slots 60 % busy). Measured there
+// 16 columns per thread. 16384 x 8192 bf16 with codes takes 123 us, 5.5 TB/s (82 %
+// of a copy; 113 to 116 before the codes were made of correctly rounded quotients:
+// 20 instructions per element then, issue slots 60 % busy). Measured there
 // against 121 us of an earlier form: 8 columns 177; 32 columns and 768 threads
 // 150; the next two rows in shared memory (cp.async) instead of the next one in
 // registers 119 to 121; several rows' teams in one CTA 155; gamma and beta from
@@ -697,7 +706,7 @@ __global__ void __launch_bounds__(KIND > 0 ? 256 : 1024, KIND > 0 ? (CH == 4 ? 3
             }
             if (!team_amax8<KIND, 1>(amax, tm, red[2], 2, parity))
                 break;
-            const float scale = amax[0] * (p.q_type == 0 ? 1.0f / 448.0f : 1.0f / 57344.0f);
+            const float scale = fp8q::row_scale(amax[0], p.q_type);
             if (valid) {
                 if (speaks)
                     p.q_scale[row] = scale;

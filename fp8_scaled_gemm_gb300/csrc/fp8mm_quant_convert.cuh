@@ -22,6 +22,18 @@ namespace fp8q {
 
 __device__ __forceinline__ float qmax_of(int q_type) { return q_type == 0 ? 448.0f : 57344.0f; }
 
+__device__ __forceinline__ bool in_reciprocal_range(float s) { return s >= 0x1p-80f && s < 0x1p100f; }
+
+// amax / qmax, correctly rounded: in the reciprocal's range as a quotient by 7 x
+// 2^n through the rounded reciprocal and one correction, which was compared with
+// the division for every mantissa.
+__device__ __forceinline__ float row_scale(float amax, int q_type)
+{
+    const float qmax = qmax_of(q_type), c = q_type == 0 ? 1.0f / 448.0f : 1.0f / 57344.0f;
+    const float s0 = __fmul_rn(amax, c), s = __fmaf_rn(__fmaf_rn(s0, -qmax, amax), c, s0);
+    return in_reciprocal_range(s) ? s : __fdiv_rn(amax, qmax);
+}
+
 struct Divider {
     float s, r;
     int mode;   // 0: zero scale, 1: reciprocal + one correction, 2: IEEE division
@@ -34,7 +46,7 @@ __device__ __forceinline__ Divider make_divider(float s)
     d.r = 0.0f;
     if (s == 0.0f) {
         d.mode = 0;
-    } else if (s >= 0x1p-80f && s < 0x1p100f) {
+    } else if (in_reciprocal_range(s)) {
         d.r = __frcp_rn(s);
         d.mode = 1;
     } else {

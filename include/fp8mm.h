@@ -436,7 +436,8 @@ int64_t fp8_act_grad_workspace(int64_t M, int64_t N);
  *   y    = (x - mean) rstd gamma + beta
  *   q_scale = max |y| / qmax,  q = fp8( y / q_scale )      as fp8_quantize, row-wise
  *
- * in fp32; q is made from the unrounded y. q [R, C] with q_scale [R] is the A
+ * in fp32; q is made from the unrounded y: scale and codes of correctly rounded
+ * quotients (a y of -0 may give the code of +0). q [R, C] with q_scale [R] is the A
  * operand of fp8_scaled_mm with FP8MM_SCALE_ROWWISE.
  *
  *   x          [R, C] of x_type, row stride ldx (0 = C); types
