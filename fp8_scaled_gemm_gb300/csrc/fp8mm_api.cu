@@ -209,6 +209,19 @@ int grow_workspace(DeviceState &d, size_t ws_bytes, size_t counters)
     return FP8MM_OK;
 }
 
+// cuTensorMapEncodeTiled needs a context bound to the host thread, which a
+// thread without a CUDA call of its own has not: cudaSetDevice binds the current
+// device's.
+template <typename... Args>
+CUresult encode_map(Args... args)
+{
+    CUresult r = g_encode(args...);
+    int dev = 0;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
+        r = g_encode(args...);
+    return r;
+}
+
 // 3-D fp8 tensor [batch, rows, K] (K contiguous, items back to back) read in
 // boxes of [1, box_rows, 128] with 128-byte swizzling; out-of-range elements
 // (rows or K beyond the item's extent) read as 0.
@@ -220,7 +233,7 @@ int encode_operand_map(CUtensorMap *map, const void *base, int64_t rows, int64_t
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(K) * static_cast<cuuint64_t>(rows)};
     cuuint32_t box[3] = {static_cast<cuuint32_t>(fp8mm::kBlockK), static_cast<cuuint32_t>(box_rows), 1};
     cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides,
+    CUresult r = encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides,
                           box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
@@ -246,7 +259,7 @@ int encode_out_map(CUtensorMap *map, void *out, int64_t M, int64_t N, int out_ty
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(ldo) * es, static_cast<cuuint64_t>(ldo) * es * static_cast<cuuint64_t>(M)};
     cuuint32_t box[3] = {ext ? 32u : 64u, 32, 1};
     cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = g_encode(map,
+    CUresult r = encode_map(map,
                           f32                            ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                           : out_type == FP8MM_OUT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -360,7 +373,7 @@ int encode_col_out_map(CUtensorMap *map, void *out, int64_t M, int64_t N, int ou
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(ldo) * es, static_cast<cuuint64_t>(ldo) * es * static_cast<cuuint64_t>(M)};
     cuuint32_t box[3] = {static_cast<cuuint32_t>(fp8mm::kTileP), static_cast<cuuint32_t>(box_m), 1};
     cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = g_encode(map, dt, 3, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    CUresult r = encode_map(map, dt, 3, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         char buf[128];
