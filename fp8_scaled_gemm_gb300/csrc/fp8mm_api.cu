@@ -46,12 +46,8 @@ thread_local std::string t_describe;
 std::mutex g_mu;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-struct DeviceState {
-    bool ready = false;
-    int sms = 0;
-    int cc_major = 0, cc_minor = 0;
-    int *status = nullptr;               // in-kernel status word
-    unsigned int *qscratch = nullptr;    // per-tensor quantisation: per-CTA maxima + counter
+// Device memory that split-K and stream-K kernels pass partial tiles through.
+struct Scratch {
     float *sk_ws = nullptr;              // stream-K: one fp32 partial tile per CTA pair
     size_t sk_ws_bytes = 0;
     unsigned int *sk_flags = nullptr;    // stream-K: 16 flags per CTA pair (zero between launches)
@@ -59,6 +55,19 @@ struct DeviceState {
     size_t ws_bytes = 0;
     unsigned int *counters = nullptr;    // split-K arrivals
     size_t counter_count = 0;
+};
+// Guards every Scratch: held while one is grown, and from reading its addresses
+// to the launch that takes them, so that another host thread cannot free them
+// in between.
+std::mutex g_scratch_mu;
+
+struct DeviceState {
+    bool ready = false;
+    int sms = 0;
+    int cc_major = 0, cc_minor = 0;
+    int *status = nullptr;               // in-kernel status word
+    unsigned int *qscratch = nullptr;    // per-tensor quantisation: per-CTA maxima + counter
+    Scratch scratch;                     // shared by all streams
     void *stage[8] = {};                 // staging: host entry point [0..5], K-major operand copies [6..7]
     size_t stage_bytes[8] = {};
 };
@@ -170,41 +179,69 @@ int device_state(DeviceState **out)
     return FP8MM_OK;
 }
 
-int grow_workspace(DeviceState &d, size_t ws_bytes, size_t counters)
+// The split-K part of a scratch, grown to what is asked for. (g_scratch_mu is held.)
+int grow_split(Scratch &sc, size_t ws_bytes, size_t counters)
 {
-    std::lock_guard<std::mutex> lock(g_mu);
-    if (ws_bytes > d.ws_bytes) {
+    if (ws_bytes > sc.ws_bytes) {
         // The old buffer may still be in use by queued work on any stream.
         cudaError_t e = cudaDeviceSynchronize();
         if (e != cudaSuccess)
             return cuda_fail(e, "cudaDeviceSynchronize");
-        if (d.ws)
-            cudaFree(d.ws);
-        d.ws = nullptr;
-        d.ws_bytes = 0;
-        e = cudaMalloc(&d.ws, ws_bytes);
+        if (sc.ws)
+            cudaFree(sc.ws);
+        sc.ws = nullptr;
+        sc.ws_bytes = 0;
+        e = cudaMalloc(&sc.ws, ws_bytes);
         if (e != cudaSuccess)
             return cuda_fail(e, "cudaMalloc(workspace)");
-        d.ws_bytes = ws_bytes;
+        sc.ws_bytes = ws_bytes;
     }
-    if (counters > d.counter_count) {
+    if (counters > sc.counter_count) {
         cudaError_t e = cudaDeviceSynchronize();
         if (e != cudaSuccess)
             return cuda_fail(e, "cudaDeviceSynchronize");
-        if (d.counters)
-            cudaFree(d.counters);
-        d.counters = nullptr;
-        d.counter_count = 0;
-        e = cudaMalloc(&d.counters, counters * sizeof(unsigned int));
+        if (sc.counters)
+            cudaFree(sc.counters);
+        sc.counters = nullptr;
+        sc.counter_count = 0;
+        e = cudaMalloc(&sc.counters, counters * sizeof(unsigned int));
         if (e != cudaSuccess)
             return cuda_fail(e, "cudaMalloc(counters)");
-        e = cudaMemset(d.counters, 0, counters * sizeof(unsigned int));
+        e = cudaMemset(sc.counters, 0, counters * sizeof(unsigned int));
         if (e != cudaSuccess)
             return cuda_fail(e, "cudaMemset(counters)");
         e = cudaDeviceSynchronize();
         if (e != cudaSuccess)
             return cuda_fail(e, "cudaDeviceSynchronize");
-        d.counter_count = counters;
+        sc.counter_count = counters;
+    }
+    return FP8MM_OK;
+}
+
+// The stream-K part, for `pairs` CTA pairs. (g_scratch_mu is held.)
+int grow_stream_k(Scratch &sc, int pairs, size_t ws_bytes)
+{
+    if (!sc.sk_flags) {
+        cudaError_t e = cudaMalloc(&sc.sk_flags, static_cast<size_t>(pairs) * 16 * sizeof(unsigned int));
+        if (e != cudaSuccess)
+            return cuda_fail(e, "cudaMalloc(stream-K flags)");
+        e = cudaMemset(sc.sk_flags, 0, static_cast<size_t>(pairs) * 16 * sizeof(unsigned int));
+        if (e == cudaSuccess)
+            e = cudaDeviceSynchronize();
+        if (e != cudaSuccess)
+            return cuda_fail(e, "cudaMemset(stream-K flags)");
+    }
+    if (ws_bytes > sc.sk_ws_bytes) {
+        cudaError_t e = cudaDeviceSynchronize();
+        if (e == cudaSuccess && sc.sk_ws)
+            e = cudaFree(sc.sk_ws);
+        sc.sk_ws = nullptr;
+        sc.sk_ws_bytes = 0;
+        if (e == cudaSuccess)
+            e = cudaMalloc(&sc.sk_ws, ws_bytes);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "cudaMalloc(stream-K workspace)");
+        sc.sk_ws_bytes = ws_bytes;
     }
     return FP8MM_OK;
 }
@@ -1002,45 +1039,27 @@ int run(const void *A, const void *B, const float *sa, const float *sb, int scal
     }
     kp.timeout_cycles = wait_limit();
     kp.inject_stop_after = static_cast<int>(g_inject_stop_after.load());
+    std::unique_lock<std::mutex> scratch_lock;
     if (c.sk_tiles > 0) {
         const int pairs = d->sms / 2;
-        const size_t ws_bytes = static_cast<size_t>(pairs) * 256 * c.tile_n * sizeof(float);
-        std::lock_guard<std::mutex> lock(g_mu);
-        if (!d->sk_flags) {
-            cudaError_t e = cudaMalloc(&d->sk_flags, static_cast<size_t>(pairs) * 16 * sizeof(unsigned int));
-            if (e != cudaSuccess)
-                return cuda_fail(e, "cudaMalloc(stream-K flags)");
-            e = cudaMemset(d->sk_flags, 0, static_cast<size_t>(pairs) * 16 * sizeof(unsigned int));
-            if (e == cudaSuccess)
-                e = cudaDeviceSynchronize();
-            if (e != cudaSuccess)
-                return cuda_fail(e, "cudaMemset(stream-K flags)");
-        }
-        if (ws_bytes > d->sk_ws_bytes) {
-            cudaError_t e = cudaDeviceSynchronize();
-            if (e == cudaSuccess && d->sk_ws)
-                e = cudaFree(d->sk_ws);
-            d->sk_ws = nullptr;
-            d->sk_ws_bytes = 0;
-            if (e == cudaSuccess)
-                e = cudaMalloc(&d->sk_ws, ws_bytes);
-            if (e != cudaSuccess)
-                return cuda_fail(e, "cudaMalloc(stream-K workspace)");
-            d->sk_ws_bytes = ws_bytes;
-        }
+        scratch_lock = std::unique_lock<std::mutex>(g_scratch_mu);
+        rc = grow_stream_k(d->scratch, pairs, static_cast<size_t>(pairs) * 256 * c.tile_n * sizeof(float));
+        if (rc != FP8MM_OK)
+            return rc;
         kp.sk_tiles = c.sk_tiles;
-        kp.sk_ws = d->sk_ws;
-        kp.sk_flags = d->sk_flags;
+        kp.sk_ws = d->scratch.sk_ws;
+        kp.sk_flags = d->scratch.sk_flags;
     }
     if (c.split > 1 && c.variant != FP8MM_VARIANT_SWAPK) {
         const int64_t tiles = static_cast<int64_t>(c.tiles_p) * c.tiles_q * batch;
         const size_t tile_rows = c.variant == FP8MM_VARIANT_PAIR ? 256 : fp8mm::kTileP;
         const size_t ws = static_cast<size_t>(tiles) * c.split * tile_rows * c.tile_n * sizeof(float);
-        rc = grow_workspace(*d, ws, static_cast<size_t>(tiles) * fp8mm::kCountersPerTile);
+        scratch_lock = std::unique_lock<std::mutex>(g_scratch_mu);
+        rc = grow_split(d->scratch, ws, static_cast<size_t>(tiles) * fp8mm::kCountersPerTile);
         if (rc != FP8MM_OK)
             return rc;
-        kp.ws = d->ws;
-        kp.counters = d->counters;
+        kp.ws = d->scratch.ws;
+        kp.counters = d->scratch.counters;
     }
 
     if (epi)
@@ -1770,7 +1789,8 @@ int fp8mm_reserve_workspace(int64_t bytes)
         return rc;
     // Smallest partial tile is 128 x 16 fp32: bounds the tiles this can hold.
     const size_t tiles = static_cast<size_t>(bytes) / (fp8mm::kTileP * 16 * sizeof(float)) + 1;
-    return grow_workspace(*d, static_cast<size_t>(bytes), tiles * fp8mm::kCountersPerTile);
+    std::lock_guard<std::mutex> lock(g_scratch_mu);
+    return grow_split(d->scratch, static_cast<size_t>(bytes), tiles * fp8mm::kCountersPerTile);
 }
 
 int fp8mm_device_status(void *stream)
@@ -1792,8 +1812,9 @@ int fp8mm_device_status(void *stream)
     e = cudaMemset(d->status, 0, sizeof(int));
     if (e != cudaSuccess)
         return cuda_fail(e, "cudaMemset(status)");
-    if (d->counters) {
-        e = cudaMemset(d->counters, 0, d->counter_count * sizeof(unsigned int));
+    std::lock_guard<std::mutex> lock(g_scratch_mu);
+    if (d->scratch.counters) {
+        e = cudaMemset(d->scratch.counters, 0, d->scratch.counter_count * sizeof(unsigned int));
         if (e != cudaSuccess)
             return cuda_fail(e, "cudaMemset(counters)");
     }
@@ -1802,8 +1823,8 @@ int fp8mm_device_status(void *stream)
                    (fp8q::kScratchWords - fp8q::kCounterWord) * sizeof(unsigned int));
     if (e != cudaSuccess)
         return cuda_fail(e, "cudaMemset(quantisation counter)");
-    if (d->sk_flags) {   // a stream-K owner that gave up leaves its flags set
-        e = cudaMemset(d->sk_flags, 0, static_cast<size_t>(d->sms / 2) * 16 * sizeof(unsigned int));
+    if (d->scratch.sk_flags) {   // a stream-K owner that gave up leaves its flags set
+        e = cudaMemset(d->scratch.sk_flags, 0, static_cast<size_t>(d->sms / 2) * 16 * sizeof(unsigned int));
         if (e != cudaSuccess)
             return cuda_fail(e, "cudaMemset(stream-K flags)");
     }
