@@ -327,6 +327,8 @@ def fp8_scaled_mm_epilogue(A, B, scale_a, scale_b, scale_mode: int, bias=None, a
     ``residual`` [M, N] (or None) has out's dtype (bf16 for a float8_e4m3fn
     output) and may be ``out``; ``preact`` receives z. Returns out, or
     (out, preact) with ``return_preact`` (preact is then made if not given).
+    Calls on different streams do not interfere; a call that is captured in a
+    graph may sum in another order than the same call outside.
     """
     if stream is not None:
         with torch.cuda.stream(stream):
@@ -340,7 +342,8 @@ def fp8_scaled_mm_act_grad(A, B, scale_a, scale_b, scale_mode: int, z, activatio
                            out_dtype=None, variant: int = VARIANT_AUTO, tile_n: int = 0, split_k: int = 0):
     """dz = (A.B * scale) * act'(z): a backward product with the gradient of
     the activation before it. ``z`` [M, N] is what fp8_scaled_mm_epilogue
-    returned as preact; out has z's dtype unless given otherwise."""
+    returned as preact; out has z's dtype unless given otherwise. Streams and
+    graphs as for fp8_scaled_mm_epilogue."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return fp8_scaled_mm_act_grad(A, B, scale_a, scale_b, scale_mode, z, activation, out, None, out_dtype,

@@ -68,6 +68,7 @@ struct DeviceState {
     int *status = nullptr;               // in-kernel status word
     unsigned int *qscratch = nullptr;    // per-tensor quantisation: per-CTA maxima + counter
     Scratch scratch;                     // shared by all streams
+    std::map<unsigned long long, Scratch> own;   // by stream: the extended epilogue's
     void *stage[8] = {};                 // staging: host entry point [0..5], K-major operand copies [6..7]
     size_t stage_bytes[8] = {};
 };
@@ -179,60 +180,71 @@ int device_state(DeviceState **out)
     return FP8MM_OK;
 }
 
-// The split-K part of a scratch, grown to what is asked for. (g_scratch_mu is held.)
-int grow_split(Scratch &sc, size_t ws_bytes, size_t counters)
+// What may still use a scratch's buffers is over, and what was cleared is clear:
+// on the stream that owns it, else (nullptr) on the whole device.
+cudaError_t settle(const cudaStream_t *owner)
 {
+    return owner ? cudaStreamSynchronize(*owner) : cudaDeviceSynchronize();
+}
+
+// Words of zeros for a scratch.
+int zeroed_words(unsigned int **words, size_t n, const cudaStream_t *owner, const char *what)
+{
+    cudaError_t e = cudaMalloc(words, n * sizeof(unsigned int));
+    if (e == cudaSuccess)
+        e = owner ? cudaMemsetAsync(*words, 0, n * sizeof(unsigned int), *owner)
+                  : cudaMemset(*words, 0, n * sizeof(unsigned int));
+    if (e == cudaSuccess && !owner)
+        e = settle(owner);               // the owner's stream is in order
+    if (e == cudaSuccess)
+        return FP8MM_OK;
+    const int rc = cuda_fail(e, what);
+    if (*words)
+        cudaFree(*words);
+    *words = nullptr;
+    return rc;
+}
+
+// The split-K part of a scratch, grown to what is asked for. (g_scratch_mu is held.)
+int grow_split(Scratch &sc, const cudaStream_t *owner, size_t ws_bytes, size_t counters)
+{
+    cudaError_t e;
     if (ws_bytes > sc.ws_bytes) {
-        // The old buffer may still be in use by queued work on any stream.
-        cudaError_t e = cudaDeviceSynchronize();
-        if (e != cudaSuccess)
-            return cuda_fail(e, "cudaDeviceSynchronize");
+        if ((e = settle(owner)) != cudaSuccess)
+            return cuda_fail(e, "synchronising before the workspace grows");
         if (sc.ws)
             cudaFree(sc.ws);
         sc.ws = nullptr;
         sc.ws_bytes = 0;
-        e = cudaMalloc(&sc.ws, ws_bytes);
-        if (e != cudaSuccess)
+        if ((e = cudaMalloc(&sc.ws, ws_bytes)) != cudaSuccess)
             return cuda_fail(e, "cudaMalloc(workspace)");
         sc.ws_bytes = ws_bytes;
     }
     if (counters > sc.counter_count) {
-        cudaError_t e = cudaDeviceSynchronize();
-        if (e != cudaSuccess)
-            return cuda_fail(e, "cudaDeviceSynchronize");
+        if ((e = settle(owner)) != cudaSuccess)
+            return cuda_fail(e, "synchronising before the counters grow");
         if (sc.counters)
             cudaFree(sc.counters);
         sc.counters = nullptr;
         sc.counter_count = 0;
-        e = cudaMalloc(&sc.counters, counters * sizeof(unsigned int));
-        if (e != cudaSuccess)
-            return cuda_fail(e, "cudaMalloc(counters)");
-        e = cudaMemset(sc.counters, 0, counters * sizeof(unsigned int));
-        if (e != cudaSuccess)
-            return cuda_fail(e, "cudaMemset(counters)");
-        e = cudaDeviceSynchronize();
-        if (e != cudaSuccess)
-            return cuda_fail(e, "cudaDeviceSynchronize");
+        const int rc = zeroed_words(&sc.counters, counters, owner, "allocating the split-K counters");
+        if (rc != FP8MM_OK)
+            return rc;
         sc.counter_count = counters;
     }
     return FP8MM_OK;
 }
 
 // The stream-K part, for `pairs` CTA pairs. (g_scratch_mu is held.)
-int grow_stream_k(Scratch &sc, int pairs, size_t ws_bytes)
+int grow_stream_k(Scratch &sc, const cudaStream_t *owner, int pairs, size_t ws_bytes)
 {
     if (!sc.sk_flags) {
-        cudaError_t e = cudaMalloc(&sc.sk_flags, static_cast<size_t>(pairs) * 16 * sizeof(unsigned int));
-        if (e != cudaSuccess)
-            return cuda_fail(e, "cudaMalloc(stream-K flags)");
-        e = cudaMemset(sc.sk_flags, 0, static_cast<size_t>(pairs) * 16 * sizeof(unsigned int));
-        if (e == cudaSuccess)
-            e = cudaDeviceSynchronize();
-        if (e != cudaSuccess)
-            return cuda_fail(e, "cudaMemset(stream-K flags)");
+        const int rc = zeroed_words(&sc.sk_flags, static_cast<size_t>(pairs) * 16, owner, "allocating the stream-K flags");
+        if (rc != FP8MM_OK)
+            return rc;
     }
     if (ws_bytes > sc.sk_ws_bytes) {
-        cudaError_t e = cudaDeviceSynchronize();
+        cudaError_t e = settle(owner);
         if (e == cudaSuccess && sc.sk_ws)
             e = cudaFree(sc.sk_ws);
         sc.sk_ws = nullptr;
@@ -244,6 +256,27 @@ int grow_stream_k(Scratch &sc, int pairs, size_t ws_bytes)
         sc.sk_ws_bytes = ws_bytes;
     }
     return FP8MM_OK;
+}
+
+// The extended epilogue's scratch is its stream's own, so that its calls on
+// different streams do not meet. Streams are told apart by their id, which is not
+// given twice (a handle can be). None (nullptr) for a stream that is being
+// captured, whose graph may run on several streams at once, and past kOwnScratch
+// streams. (g_scratch_mu is held.)
+constexpr size_t kOwnScratch = 16;
+
+Scratch *own_scratch(DeviceState &d, cudaStream_t stream)
+{
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone ||
+        cudaStreamGetId(stream, &id) != cudaSuccess) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    if (d.own.size() >= kOwnScratch && d.own.find(id) == d.own.end())
+        return nullptr;
+    return &d.own[id];
 }
 
 // cuTensorMapEncodeTiled needs a context bound to the host thread, which a
@@ -602,7 +635,7 @@ int swap_tile_for(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64
 // configuration on average, 20 % at worst; the plain product's choice 22 % for M
 // <= 128 and 41 % above, 5.9x at worst (128 x 8192 x 4096: 16.5 us, with that
 // 20.7; 384 x 128 x 6016: 5.3, with that 19.0).
-void choose_epilogue(int64_t M, int64_t N, int64_t K, int sms, int *variant, int *tile_n, int *split)
+void choose_epilogue(int64_t M, int64_t N, int64_t K, int sms, bool scratch, int *variant, int *tile_n, int *split)
 {
     const int64_t nt = cdiv(N, fp8mm::kTileP), kb = cdiv(K, fp8mm::kBlockK);
     const bool unaligned = N % 8 != 0;
@@ -617,7 +650,7 @@ void choose_epilogue(int64_t M, int64_t N, int64_t K, int sms, int *variant, int
     };
     auto waves = [](int64_t units, int places) { return static_cast<double>(cdiv(units, places)); };
     offer(2.27 + waves(nt * cdiv(M, 128), sms) * (kb * 0.283 + 4.37 + (unaligned ? 1.03 : 0.0)), FP8MM_VARIANT_TILE, 128, 1);
-    if (M > 128 && 2 * nt * cdiv(M, 128) <= sms)      // deep K, half of the SMs without a tile
+    if (scratch && M > 128 && 2 * nt * cdiv(M, 128) <= sms)      // deep K, half of the SMs without a tile
         offer(16.6 + cdiv(kb, 2) * 0.283, FP8MM_VARIANT_TILE, 128, 2);
     if (M > 128) {
         offer(2.94 + waves(cdiv(N, 256) * cdiv(M, 128), sms) * (kb * 0.38 + 6.61 + (unaligned ? 1.45 : 0.0)),
@@ -641,14 +674,16 @@ void choose_epilogue(int64_t M, int64_t N, int64_t K, int sms, int *variant, int
     }
 }
 
+// The kernel for a problem. scratch: whether the automatic choice may pass
+// partial tiles through device memory (split-K, stream-K).
 Choice choose(int64_t M, int64_t N, int64_t K, int sms, int variant, int tile_n, int split, int64_t batch = 1,
-              bool epilogue = false)
+              bool epilogue = false, bool scratch = true)
 {
     Choice c{};
     c.kblocks = static_cast<int>(cdiv(K, fp8mm::kBlockK));
     if (variant == FP8MM_VARIANT_AUTO && epilogue && batch == 1 &&
         (M <= 128 || cdiv(M, 128) * cdiv(N, 128) <= 2 * static_cast<int64_t>(sms))) {
-        choose_epilogue(M, N, K, sms, &variant, &tile_n, &split);
+        choose_epilogue(M, N, K, sms, scratch, &variant, &tile_n, &split);
     } else if (variant == FP8MM_VARIANT_AUTO) {
         split = 0;
         if (M <= 128) {
@@ -725,19 +760,21 @@ Choice choose(int64_t M, int64_t N, int64_t K, int sms, int variant, int tile_n,
             // stage buffers per epilogue warp measured 7-15 % faster
             variant = FP8MM_VARIANT_TILE;
             tile_n = 256;
+            split = scratch ? 0 : 1;
         } else {
             // the pair kernel or the 1-SM 128 x 128 kernel, each with its best
             // split, whichever the time model says finishes first
             const int kb = static_cast<int>(cdiv(K, fp8mm::kBlockK));
             const int64_t pt = cdiv(M, 256) * cdiv(N, 256) * batch;
             const int64_t tt = cdiv(M, 128) * cdiv(N, 128) * batch;
-            const int ps = pick_pair_split(pt, kb, sms / 2);
-            const int ts = pick_tile128_split(tt, kb, sms);
-            const double t_pair = std::min(pair_time(pt, kb, ps, sms / 2), pair_sk_time(pt, kb, sms / 2));
+            const int ps = scratch ? pick_pair_split(pt, kb, sms / 2) : 1;
+            const int ts = scratch ? pick_tile128_split(tt, kb, sms) : 1;
+            const double t_sk = scratch ? pair_sk_time(pt, kb, sms / 2) : 1e300;
+            const double t_pair = std::min(pair_time(pt, kb, ps, sms / 2), t_sk);
             if (t_pair <= tile128_time(tt, kb, ts, sms)) {
                 variant = FP8MM_VARIANT_PAIR;
                 tile_n = 256;
-                split = pair_sk_time(pt, kb, sms / 2) < pair_time(pt, kb, ps, sms / 2) ? -1 : ps;   // -1: stream-K
+                split = t_sk < pair_time(pt, kb, ps, sms / 2) ? -1 : ps;   // -1: stream-K
             } else {
                 variant = FP8MM_VARIANT_TILE;
                 tile_n = 128;
@@ -802,6 +839,35 @@ Choice choose(int64_t M, int64_t N, int64_t K, int sms, int variant, int tile_n,
     c.units = static_cast<int>(tiles * split);
     c.grid = static_cast<int>(std::min<int64_t>(c.units, sms));
     return c;
+}
+
+// Whether a choice passes partial tiles through device memory.
+bool needs_scratch(const Choice &c) { return c.sk_tiles > 0 || (c.split > 1 && c.variant != FP8MM_VARIANT_SWAPK); }
+
+// The scratch of a choice that needs one, grown, into the launch's parameters.
+// (g_scratch_mu is held.)
+int take_scratch(const Choice &c, int64_t batch, int sms, Scratch &sc, const cudaStream_t *owner,
+                 fp8mm::KernelParams &kp)
+{
+    if (c.sk_tiles > 0) {
+        const int pairs = sms / 2;
+        const int rc = grow_stream_k(sc, owner, pairs, static_cast<size_t>(pairs) * 256 * c.tile_n * sizeof(float));
+        if (rc != FP8MM_OK)
+            return rc;
+        kp.sk_tiles = c.sk_tiles;
+        kp.sk_ws = sc.sk_ws;
+        kp.sk_flags = sc.sk_flags;
+        return FP8MM_OK;
+    }
+    const int64_t tiles = static_cast<int64_t>(c.tiles_p) * c.tiles_q * batch;
+    const size_t tile_rows = c.variant == FP8MM_VARIANT_PAIR ? 256 : fp8mm::kTileP;
+    const size_t ws = static_cast<size_t>(tiles) * c.split * tile_rows * c.tile_n * sizeof(float);
+    const int rc = grow_split(sc, owner, ws, static_cast<size_t>(tiles) * fp8mm::kCountersPerTile);
+    if (rc != FP8MM_OK)
+        return rc;
+    kp.ws = sc.ws;
+    kp.counters = sc.counters;
+    return FP8MM_OK;
 }
 
 // The text form of a kernel choice (fp8mm_describe_choice's format).
@@ -1001,11 +1067,33 @@ int run(const void *A, const void *B, const float *sa, const float *sb, int scal
             tuned = true;
         }
     }
-    const Choice c = choose(M, N, K, d->sms, variant, tile_n, split, batch, epi != nullptr);
+    Choice c = choose(M, N, K, d->sms, variant, tile_n, split, batch, epi != nullptr);
+    fp8mm::KernelParams kp{};
+    std::unique_lock<std::mutex> scratch_lock;   // until the launch
+    if (needs_scratch(c)) {
+        scratch_lock = std::unique_lock<std::mutex>(g_scratch_mu);
+        Scratch *const own = epi ? own_scratch(*d, stream) : nullptr;
+        const bool optional = epi && variant == FP8MM_VARIANT_AUTO;
+        if (own)
+            rc = take_scratch(c, batch, d->sms, *own, &stream, kp);
+        else if (!optional)
+            rc = take_scratch(c, batch, d->sms, d->scratch, nullptr, kp);
+        if (optional && (!own || rc != FP8MM_OK)) {
+            // The extended epilogue shares no scratch that its caller did not ask
+            // for. (In a graph 512 x 2048 x 14336 takes 45.1 us, split 38.4;
+            // 16384 x 4096 x 14336 634 and 622; 3000 x 5000 x 4112 71.7 and 76.1.)
+            cudaGetLastError();
+            c = choose(M, N, K, d->sms, variant, tile_n, split, batch, true, false);
+            kp = fp8mm::KernelParams{};
+            scratch_lock.unlock();
+            rc = FP8MM_OK;
+        }
+        if (rc != FP8MM_OK)
+            return rc;
+    }
     if (log_enabled())
         log_choice(current_device(), batch, M, N, K, scale_mode, a_type, b_type, out_type, req_variant, req_tile_n,
                    req_split, c, tuned);
-    fp8mm::KernelParams kp{};
     kp.scale_a = sa;
     kp.scale_b = sb;
     kp.bias = bias;
@@ -1039,29 +1127,6 @@ int run(const void *A, const void *B, const float *sa, const float *sb, int scal
     }
     kp.timeout_cycles = wait_limit();
     kp.inject_stop_after = static_cast<int>(g_inject_stop_after.load());
-    std::unique_lock<std::mutex> scratch_lock;
-    if (c.sk_tiles > 0) {
-        const int pairs = d->sms / 2;
-        scratch_lock = std::unique_lock<std::mutex>(g_scratch_mu);
-        rc = grow_stream_k(d->scratch, pairs, static_cast<size_t>(pairs) * 256 * c.tile_n * sizeof(float));
-        if (rc != FP8MM_OK)
-            return rc;
-        kp.sk_tiles = c.sk_tiles;
-        kp.sk_ws = d->scratch.sk_ws;
-        kp.sk_flags = d->scratch.sk_flags;
-    }
-    if (c.split > 1 && c.variant != FP8MM_VARIANT_SWAPK) {
-        const int64_t tiles = static_cast<int64_t>(c.tiles_p) * c.tiles_q * batch;
-        const size_t tile_rows = c.variant == FP8MM_VARIANT_PAIR ? 256 : fp8mm::kTileP;
-        const size_t ws = static_cast<size_t>(tiles) * c.split * tile_rows * c.tile_n * sizeof(float);
-        scratch_lock = std::unique_lock<std::mutex>(g_scratch_mu);
-        rc = grow_split(d->scratch, ws, static_cast<size_t>(tiles) * fp8mm::kCountersPerTile);
-        if (rc != FP8MM_OK)
-            return rc;
-        kp.ws = d->scratch.ws;
-        kp.counters = d->scratch.counters;
-    }
-
     if (epi)
         kp.e = *epi;
     return encode_and_dispatch(c, A, B, out, M, N, K, kp, stream, batch, epi != nullptr);
@@ -1790,7 +1855,7 @@ int fp8mm_reserve_workspace(int64_t bytes)
     // Smallest partial tile is 128 x 16 fp32: bounds the tiles this can hold.
     const size_t tiles = static_cast<size_t>(bytes) / (fp8mm::kTileP * 16 * sizeof(float)) + 1;
     std::lock_guard<std::mutex> lock(g_scratch_mu);
-    return grow_split(d->scratch, static_cast<size_t>(bytes), tiles * fp8mm::kCountersPerTile);
+    return grow_split(d->scratch, nullptr, static_cast<size_t>(bytes), tiles * fp8mm::kCountersPerTile);
 }
 
 int fp8mm_device_status(void *stream)
@@ -1812,22 +1877,28 @@ int fp8mm_device_status(void *stream)
     e = cudaMemset(d->status, 0, sizeof(int));
     if (e != cudaSuccess)
         return cuda_fail(e, "cudaMemset(status)");
+    // a product that gave up leaves arrivals counted, or a stream-K owner its flags
+    // set; other streams' products are over first
     std::lock_guard<std::mutex> lock(g_scratch_mu);
-    if (d->scratch.counters) {
-        e = cudaMemset(d->scratch.counters, 0, d->scratch.counter_count * sizeof(unsigned int));
+    e = cudaDeviceSynchronize();
+    if (e != cudaSuccess)
+        return cuda_fail(e, "cudaDeviceSynchronize");
+    std::vector<Scratch *> all{&d->scratch};
+    for (auto &o : d->own)
+        all.push_back(&o.second);
+    for (Scratch *sc : all) {
+        if (sc->counters)
+            e = cudaMemset(sc->counters, 0, sc->counter_count * sizeof(unsigned int));
+        if (e == cudaSuccess && sc->sk_flags)
+            e = cudaMemset(sc->sk_flags, 0, static_cast<size_t>(d->sms / 2) * 16 * sizeof(unsigned int));
         if (e != cudaSuccess)
-            return cuda_fail(e, "cudaMemset(counters)");
+            return cuda_fail(e, "cudaMemset(counters and flags)");
     }
     // a per-tensor quantisation that gave up leaves arrivals counted and an amax slot set
     e = cudaMemset(d->qscratch + fp8q::kCounterWord, 0,
                    (fp8q::kScratchWords - fp8q::kCounterWord) * sizeof(unsigned int));
     if (e != cudaSuccess)
         return cuda_fail(e, "cudaMemset(quantisation counter)");
-    if (d->scratch.sk_flags) {   // a stream-K owner that gave up leaves its flags set
-        e = cudaMemset(d->scratch.sk_flags, 0, static_cast<size_t>(d->sms / 2) * 16 * sizeof(unsigned int));
-        if (e != cudaSuccess)
-            return cuda_fail(e, "cudaMemset(stream-K flags)");
-    }
     e = cudaDeviceSynchronize();
     if (e != cudaSuccess)
         return cuda_fail(e, "cudaDeviceSynchronize");

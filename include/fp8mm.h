@@ -53,7 +53,8 @@
  *
  * Threading: calls may come from any host thread. Calls that use the split-K
  * workspace and run concurrently on different streams of one device race on
- * it; issue them on one stream.
+ * it; issue them on one stream. (fp8_scaled_mm_epilogue and
+ * fp8_scaled_mm_act_grad keep workspaces of their own per stream, see there.)
  *
  * Errors: argument errors are found on the host before anything is enqueued
  * and come back as a negative fp8mm_status; nothing is launched then. A
@@ -369,8 +370,14 @@ typedef struct fp8mm_epilogue {
  * an e4m3fn output): the sum then replaces it. Otherwise out, preact and
  * every input must not overlap.
  *
- * Other arguments, kernels, choice, workspace and errors as
- * fp8_scaled_mm_ex; options may be NULL. FP8MM_ERR_NULL without epilogue,
+ * Other arguments, kernels and errors as fp8_scaled_mm_ex; options may be
+ * NULL. Calls on different streams and threads do not interfere: a kernel that
+ * passes partial sums through device memory has a workspace of the stream's
+ * own, allocated on the first call that needs it and kept until the process
+ * exits. While a stream is captured, past 16 such streams, and where the
+ * allocation fails, the automatic choice takes a kernel without one (and so
+ * another order of summation); a split-K or stream-K kernel that the caller
+ * asks for then uses the device's, like fp8_scaled_mm_ex. FP8MM_ERR_NULL without epilogue,
  * FP8MM_ERR_MODE for an unknown activation or a forbidden aliasing,
  * FP8MM_ERR_SHAPE / _ALIGN for ldr, ldp and the two pointers.
  */
