@@ -7,7 +7,9 @@ the name of the C entry point it calls and only checks and marshals
 arguments; every step of the computation runs in the CUDA kernels. Most go
 through ctypes; the operators of an MLP block, whose small calls take the host
 longer than the GPU, through a native module (``csrc/fp8mm_torch.cpp``).
-There is no CPU fallback: if a library cannot be loaded, calls raise.
+There is no CPU fallback: if a library cannot be loaded, calls raise. A call's
+tensors are on one device: the current one, or for the native module's operators
+any.
 
 Operation sources: gist "matmul_fp8.py" (FP8 Matmul), ``matmul_fp8_kernel``
 (scale epilogue) and ``benchmark()`` (B column-major); PyTorch PR #125204,
@@ -226,12 +228,33 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _stream_handle(stream) -> int:
+def _stream_handle(stream, on: Optional[torch.Tensor] = None) -> int:
+    """The stream of a call: the given one or the current one. The library works
+    on the current device, so ``on``, one of the call's tensors, has to be there."""
+    device = torch._C._cuda_getDevice()
+    if on is not None and on.get_device() != device:
+        raise ValueError(f"the tensors are on cuda:{on.get_device()}, the current device is cuda:{device}")
     if stream is None:
-        # the current stream of the current device, without the Stream object
-        # torch.cuda.current_stream() makes (3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        # without the Stream object torch.cuda.current_stream() makes (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(device)
     return int(stream.cuda_stream)
+
+
+def _on(stream, t):
+    """``stream`` as the current one, for a call on ``t``'s device."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.device != stream.device:
+        raise ValueError(f"the tensors are on {t.device}, the stream is of {stream.device}")
+    return torch.cuda.stream(stream)
+
+
+def _one_device(what, tensors):
+    """Refuses host tensors and tensors on different devices."""
+    device = tensors[0].get_device()
+    for t in tensors:
+        if not t.is_cuda:
+            raise ValueError(f"{what} takes CUDA tensors")
+        if t.get_device() != device:
+            raise ValueError(f"{what} takes tensors of one device")
 
 
 def _validate(A, B, scale_a, scale_b, scale_mode, bias, out, device_side: bool, typed: bool = False):
@@ -268,8 +291,11 @@ def _validate(A, B, scale_a, scale_b, scale_mode, bias, out, device_side: bool, 
         raise ValueError("bias must be a contiguous tensor of N values of out's dtype "
                          "(bfloat16 for a float8_e4m3fn output)")
     if device_side:
-        if not (A.is_cuda and B.is_cuda and scale_a.is_cuda and scale_b.is_cuda and out.is_cuda and
-                (bias is None or bias.is_cuda)):
+        device = A.get_device()          # -1: host memory
+        if not (0 <= device == B.get_device() == scale_a.get_device() == scale_b.get_device() == out.get_device() and
+                (bias is None or bias.get_device() == device)):
+            if all(t is None or t.is_cuda for t in (A, B, scale_a, scale_b, out, bias)):
+                raise ValueError("fp8_scaled_mm takes tensors of one device")
             raise ValueError("fp8_scaled_mm takes CUDA tensors (use fp8_scaled_mm_host for host memory)")
     elif A.is_cuda or B.is_cuda or scale_a.is_cuda or scale_b.is_cuda or out.is_cuda or (
             bias is not None and bias.is_cuda):
@@ -283,7 +309,7 @@ def fp8_scaled_mm(A, B, scale_a, scale_b, scale_mode: int, bias=None, out=None, 
         out = torch.empty((A.shape[0], B.shape[1]), dtype=torch.bfloat16, device=A.device)
     M, N, K = _validate(A, B, scale_a, scale_b, scale_mode, bias, out, True)
     _check(load().fp8_scaled_mm(_ptr(A), _ptr(B), _ptr(scale_a), _ptr(scale_b), scale_mode,
-                                _ptr(bias), _ptr(out), M, N, K, _stream_handle(stream)))
+                                _ptr(bias), _ptr(out), M, N, K, _stream_handle(stream, A)))
     return out
 
 
@@ -295,7 +321,7 @@ def fp8_scaled_mm_config(A, B, scale_a, scale_b, scale_mode: int, bias=None, out
         out = torch.empty((A.shape[0], B.shape[1]), dtype=torch.bfloat16, device=A.device)
     M, N, K = _validate(A, B, scale_a, scale_b, scale_mode, bias, out, True)
     _check(load().fp8_scaled_mm_config(_ptr(A), _ptr(B), _ptr(scale_a), _ptr(scale_b), scale_mode,
-                                       _ptr(bias), _ptr(out), M, N, K, _stream_handle(stream),
+                                       _ptr(bias), _ptr(out), M, N, K, _stream_handle(stream, A),
                                        int(variant), int(tile_n), int(split_k)))
     return out
 
@@ -313,7 +339,7 @@ def fp8_scaled_mm_ex(A, B, scale_a, scale_b, scale_mode: int, bias=None, out=Non
     ldo = 0 if out.is_contiguous() else int(out.stride(0))
     opt = Options(_FP8[A.dtype], _FP8[B.dtype], _OUT[out.dtype], int(variant), int(tile_n), int(split_k), ldo)
     _check(load().fp8_scaled_mm_ex(_ptr(A), _ptr(B), _ptr(scale_a), _ptr(scale_b), scale_mode,
-                                   _ptr(bias), _ptr(out), M, N, K, _stream_handle(stream),
+                                   _ptr(bias), _ptr(out), M, N, K, _stream_handle(stream, A),
                                    ctypes.byref(opt)))
     return out
 
@@ -331,7 +357,7 @@ def fp8_scaled_mm_epilogue(A, B, scale_a, scale_b, scale_mode: int, bias=None, a
     graph may sum in another order than the same call outside.
     """
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, A):
             return fp8_scaled_mm_epilogue(A, B, scale_a, scale_b, scale_mode, bias, activation, residual, preact, out,
                                           None, out_dtype, return_preact, variant, tile_n, split_k)
     return (_native or _load_native()).mm_epilogue(A, B, scale_a, scale_b, scale_mode, bias, activation, residual,
@@ -345,7 +371,7 @@ def fp8_scaled_mm_act_grad(A, B, scale_a, scale_b, scale_mode: int, z, activatio
     returned as preact; out has z's dtype unless given otherwise. Streams and
     graphs as for fp8_scaled_mm_epilogue."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, A):
             return fp8_scaled_mm_act_grad(A, B, scale_a, scale_b, scale_mode, z, activation, out, None, out_dtype,
                                           variant, tile_n, split_k)
     return (_native or _load_native()).mm_act_grad(A, B, scale_a, scale_b, scale_mode, z, activation, out, out_dtype,
@@ -389,12 +415,10 @@ def fp8_scaled_mm_layout(A, B, scale_a, scale_b, scale_mode: int, bias=None, out
         raise ValueError("out must be a contiguous [M, N] bfloat16, float16, float32 or float8_e4m3fn tensor")
     if bias is not None and (bias.dtype != _BIAS.get(out.dtype) or bias.numel() != N or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous tensor of N values with out's dtype")
-    for t in [A, B, scale_a, scale_b, out] + ([bias] if bias is not None else []):
-        if not t.is_cuda:
-            raise ValueError("fp8_scaled_mm_layout takes CUDA tensors")
+    _one_device("fp8_scaled_mm_layout", [A, B, scale_a, scale_b, out] + ([bias] if bias is not None else []))
     opt = Options(_FP8[A.dtype], _FP8[B.dtype], _OUT[out.dtype], int(variant), int(tile_n), int(split_k))
     _check(load().fp8_scaled_mm_layout(_ptr(A), a_major, _ptr(B), b_major, _ptr(scale_a), _ptr(scale_b),
-                                       scale_mode, _ptr(bias), _ptr(out), M, N, K, _stream_handle(stream),
+                                       scale_mode, _ptr(bias), _ptr(out), M, N, K, _stream_handle(stream, A),
                                        ctypes.byref(opt)))
     return out
 
@@ -430,12 +454,10 @@ def fp8_scaled_bmm(A, B, scale_a, scale_b, scale_mode: int, bias=None, out=None,
         raise ValueError("out must be a contiguous [batch, M, N] bfloat16, float16, float32 or float8_e4m3fn tensor")
     if bias is not None and (bias.dtype != _BIAS.get(out.dtype) or bias.numel() != N or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous tensor of N values with out's dtype")
-    for t in [A, B, scale_a, scale_b, out] + ([bias] if bias is not None else []):
-        if not t.is_cuda:
-            raise ValueError("fp8_scaled_bmm takes CUDA tensors")
+    _one_device("fp8_scaled_bmm", [A, B, scale_a, scale_b, out] + ([bias] if bias is not None else []))
     opt = Options(_FP8[A.dtype], _FP8[B.dtype], _OUT[out.dtype], int(variant), int(tile_n), int(split_k))
     _check(load().fp8_scaled_bmm(_ptr(A), _ptr(B), _ptr(scale_a), _ptr(scale_b), scale_mode, _ptr(bias),
-                                 _ptr(out), nb, M, N, K, _stream_handle(stream), ctypes.byref(opt)))
+                                 _ptr(out), nb, M, N, K, _stream_handle(stream, A), ctypes.byref(opt)))
     return out
 
 
@@ -461,7 +483,7 @@ def fp8_scaled_mm_noalloc(A, B, scale_a, scale_b, scale_mode: int, bias=None, ou
         raise ValueError("fp8_scaled_mm_noalloc needs a preallocated out tensor")
     M, N, K = _validate(A, B, scale_a, scale_b, scale_mode, bias, out, True)
     _check(load().fp8_scaled_mm_noalloc(_ptr(A), _ptr(B), _ptr(scale_a), _ptr(scale_b), scale_mode,
-                                        _ptr(bias), _ptr(out), M, N, K, _stream_handle(stream)))
+                                        _ptr(bias), _ptr(out), M, N, K, _stream_handle(stream, A)))
     return out
 
 
@@ -497,8 +519,9 @@ def fp8_quantize(x, scale_mode: int, dtype=torch.float8_e4m3fn, out=None, scale=
     n_scale = 1 if scale_mode == SCALE_TENSOR else R
     if scale.dtype != torch.float32 or scale.numel() != n_scale or not scale.is_contiguous() or not scale.is_cuda:
         raise ValueError(f"scale must be a contiguous CUDA float32 tensor of {n_scale} values")
+    _one_device("fp8_quantize", (x, out, scale))
     _check(load().fp8_quantize(_ptr(x), R, C, int(scale_mode), _FP8[dtype], _ptr(out), _ptr(scale),
-                               _stream_handle(stream)))
+                               _stream_handle(stream, x)))
     return out, scale
 
 
@@ -514,6 +537,7 @@ def fp8_scaled_mm_bf16(A, B, scale_mode: int, bias=None, out=None, stream=None,
     Bt = B.t()
     _validate_bf16_rows("A", A)
     _validate_bf16_rows("B.t()", Bt)
+    _one_device("fp8_scaled_mm_bf16", (A, B))
     M, K = A.shape
     N = B.shape[1]
     dev = A.device
@@ -529,7 +553,7 @@ def fp8_scaled_mm_bf16(A, B, scale_mode: int, bias=None, out=None, stream=None,
     opt = Options(_FP8[a_dtype], _FP8[b_dtype], _OUT[out.dtype], int(variant), int(tile_n), int(split_k), ldo)
     _check(load().fp8_scaled_mm_bf16(_ptr(A), _ptr(Bt), int(scale_mode), _ptr(bias), _ptr(out), M, N, K,
                                      _ptr(a_q), _ptr(bt_q), _ptr(scale_a), _ptr(scale_b),
-                                     _stream_handle(stream), ctypes.byref(opt)))
+                                     _stream_handle(stream, A), ctypes.byref(opt)))
     if return_quantized:
         return out, a_q, bt_q.t(), scale_a, scale_b
     return out
@@ -544,7 +568,7 @@ def fp8_act_grad(dy, z, activation: int, dz=None, dbias=None, stream=None, retur
     (``return_dz``, ``return_dbias``) is None.
     """
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, dy):
             return fp8_act_grad(dy, z, activation, dz, dbias, None, return_dz, return_dbias)
     return (_native or _load_native()).act_grad(dy, z, activation, dz, dbias, return_dz, return_dbias)
 
@@ -560,7 +584,7 @@ def fp8_layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, y=None, y_dtype=
     ``y_dtype`` says otherwise, and is None with ``return_y`` false.
     """
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return fp8_layer_norm(x, gamma, beta, eps, y, y_dtype, q_dtype, None, return_y)
     return (_native or _load_native()).layer_norm(x, gamma, beta, eps, y, y_dtype, q_dtype, return_y)
 
@@ -575,7 +599,7 @@ def fp8_layer_norm_grad(dy, x, gamma, mean, rstd, residual_grad=None, dx=None, s
     ``return_params``).
     """
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return fp8_layer_norm_grad(dy, x, gamma, mean, rstd, residual_grad, dx, None, return_params)
     return (_native or _load_native()).layer_norm_grad(dy, x, gamma, mean, rstd, residual_grad, dx, return_params)
 

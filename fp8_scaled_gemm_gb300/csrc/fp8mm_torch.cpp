@@ -9,12 +9,14 @@
 // not given, and calls the C entries, whose addresses it is handed (init); it
 // runs nothing on the device itself. Errors are ValueError for arguments
 // (TypeError for what is no tensor) and what `check` raises for a status.
-// Tensors are made and kernels launched on the current stream.
+// All tensors of a call are on one device; what is made is made there, and the
+// kernels run on that device's current stream.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -73,6 +75,16 @@ void checked(int64_t rc)
 struct Unlocked {
     PyThreadState *state = PyEval_SaveThread();
     ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// The call's device as the current one.
+struct Guard {
+    c10::cuda::OptionalCUDAGuard guard;
+    explicit Guard(at::Device d)
+    {
+        if (d.index() != c10::cuda::current_device())
+            guard.set_device(d);
+    }
 };
 
 void *stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
@@ -139,12 +151,21 @@ const char *row_name(ScalarType t)
     return t == ScalarType::BFloat16 ? "torch.bfloat16" : t == ScalarType::Half ? "torch.float16" : "torch.float32";
 }
 
+// A call's tensors are on one device: that of its first one.
+void beside(const char *name, const Tensor &t, const Tensor &first)
+{
+    if (t.device() != first.device())
+        refuse("%s is on another device than the first operand", name);
+}
+
 // Row stride of a 2-D bf16, fp16 or fp32 CUDA matrix with contiguous rows; its
 // shape and type as `like`'s, where given.
 int64_t rows(const char *name, const Tensor &t, const Tensor *like = nullptr, const ScalarType *type = nullptr)
 {
     if (t.dim() != 2 || row_code(t.scalar_type()) < 0 || !t.is_cuda())
         refuse("%s must be a 2-D CUDA tensor of bfloat16, float16 or float32", name);
+    if (like)
+        beside(name, t, *like);
     const int64_t R = t.size(0), C = t.size(1);
     if (like && (R != like->size(0) || C != like->size(1)))
         refuse("%s must have shape (%lld, %lld)", name, static_cast<long long>(like->size(0)),
@@ -158,13 +179,15 @@ int64_t rows(const char *name, const Tensor &t, const Tensor *like = nullptr, co
     return R > 1 ? t.stride(0) : C;
 }
 
-// A contiguous vector of n values, fp32 or (any) of any row type.
-void vector(const char *name, const Tensor *t, int64_t n, bool any)
+// A contiguous vector of n values, fp32 or (any) of any row type, on first's device.
+void vector(const char *name, const Tensor *t, int64_t n, bool any, const Tensor &first)
 {
     if (t && ((any ? row_code(t->scalar_type()) < 0 : t->scalar_type() != ScalarType::Float) || t->numel() != n ||
               !t->is_contiguous() || !t->is_cuda()))
         refuse("%s must be a contiguous CUDA tensor of %lld values of %s", name, static_cast<long long>(n),
                any ? "torch.bfloat16 or torch.float16 or torch.float32" : "torch.float32");
+    if (t)
+        beside(name, *t, first);
 }
 
 void *data(const Tensor *t) { return t ? t->data_ptr() : nullptr; }
@@ -301,6 +324,9 @@ Product product(PyObject *const *a, PyObject *const *o)
     }
     if (!A.is_cuda() || !B.is_cuda() || !p.scale_a->is_cuda() || !p.scale_b->is_cuda())
         refuse("fp8_scaled_mm takes CUDA tensors (use fp8_scaled_mm_host for host memory)");
+    beside("B", B, A);
+    beside("scale_a", *p.scale_a, A);
+    beside("scale_b", *p.scale_b, A);
     p.options.variant = integer(o[0]);
     p.options.tile_n = integer(o[1]);
     p.options.split_k = integer(o[2]);
@@ -322,6 +348,7 @@ void product_out(Product &p, Result &out, PyObject *given, ScalarType type)
             refuse("out must be a [M, N] tensor of bfloat16, float16, float32 or float8_e4m3fn with contiguous rows");
         if (!t.is_cuda())
             refuse("fp8_scaled_mm takes CUDA tensors (use fp8_scaled_mm_host for host memory)");
+        beside("out", t, *p.A);
         p.options.ldo = t.is_contiguous() ? 0 : t.stride(0);
     }
     p.options.out_type = out_code(out.type);
@@ -339,6 +366,7 @@ int64_t aux(const char *name, const Product &p, const Tensor *t, ScalarType type
         return 0;
     if (t->scalar_type() != type || t->dim() != 2 || t->size(0) != p.M || t->size(1) != p.N || !t->is_cuda())
         refuse("%s must be a CUDA [M, N] tensor of out's dtype (bfloat16 for a float8_e4m3fn output)", name);
+    beside(name, *t, *p.A);
     if (t->is_contiguous())
         return p.N;
     if ((t->stride(1) != 1 && p.N > 1) || (t->stride(0) < p.N && p.M > 1))
@@ -360,6 +388,8 @@ PyObject *mm_epilogue(PyObject *const *a)
         refuse("bias must be a contiguous tensor of N values of out's dtype (bfloat16 for a float8_e4m3fn output)");
     if (bias && !bias->is_cuda())
         refuse("fp8_scaled_mm takes CUDA tensors (use fp8_scaled_mm_host for host memory)");
+    if (bias)
+        beside("bias", *bias, *p.A);
     preact.take("preact", a[8]);
     if (return_preact && !preact.t)
         preact.plan(*p.A, type, p.M, p.N);
@@ -368,6 +398,7 @@ PyObject *mm_epilogue(PyObject *const *a)
     e.residual = data(residual);
     e.ldr = aux("residual", p, residual, type);
     e.ldp = aux("preact", p, preact.t, type);
+    const Guard guard(p.A->device());
     int64_t rc;
     {
         Unlocked u;
@@ -390,6 +421,7 @@ PyObject *mm_act_grad(PyObject *const *a)
     product_out(p, out, a[7], a[8] == Py_None ? z->scalar_type() : dtype("out_dtype", a[8]));
     const int64_t ldz = aux("z", p, z, aux_type(out));
     const int activation = integer(a[6]);
+    const Guard guard(p.A->device());
     int64_t rc;
     {
         Unlocked u;
@@ -416,10 +448,11 @@ PyObject *act_grad(PyObject *const *a)
     if (!dz.t && truth(a[5]))
         dz.plan(dy, type, M, N);
     dbias.take("dbias", a[4]);
-    vector("dbias", dbias.t, N, false);
+    vector("dbias", dbias.t, N, false, dy);
     if (!dbias.t && truth(a[6]))
         dbias.plan(dy, ScalarType::Float, N);
     const int activation = integer(a[2]);
+    const Guard guard(dy.device());
     int64_t bytes = 0, rc;
     if (dbias.wanted())
         checked(bytes = api.act_grad_workspace(M, N));
@@ -444,8 +477,8 @@ PyObject *layer_norm(PyObject *const *a)
     const int64_t ldx = rows("x", x), R = x.size(0), C = x.size(1);
     if (gamma && beta && gamma->scalar_type() != beta->scalar_type())
         refuse("gamma and beta must have one dtype");
-    vector("gamma", gamma, C, true);
-    vector("beta", beta, C, true);
+    vector("gamma", gamma, C, true, x);
+    vector("beta", beta, C, true, x);
     const Tensor *params = gamma ? gamma : beta;
     const double eps = PyFloat_AsDouble(a[3]);
     if (eps == -1.0 && PyErr_Occurred())
@@ -471,6 +504,7 @@ PyObject *layer_norm(PyObject *const *a)
         q.plan(x, code_type, R, C);
         q_scale.plan(x, ScalarType::Float, R);
     }
+    const Guard guard(x.device());
     int64_t rc;
     {
         Unlocked u;
@@ -492,9 +526,9 @@ PyObject *layer_norm_grad(PyObject *const *a)
                  *mean = tensor("mean", a[3]), *rstd = tensor("rstd", a[4]), *res = tensor("residual_grad", a[5], true);
     const int64_t lddy = rows("dy", dy), ldx = rows("x", x, &dy), R = x.size(0), C = x.size(1);
     const ScalarType type = x.scalar_type();
-    vector("gamma", gamma, C, true);
-    vector("mean", mean, R, false);
-    vector("rstd", rstd, R, false);
+    vector("gamma", gamma, C, true, dy);
+    vector("mean", mean, R, false, dy);
+    vector("rstd", rstd, R, false, dy);
     const int64_t lddres = res ? rows("residual_grad", *res, &x, &type) : 0;
     Result dx, dgamma, dbeta;
     dx.take("dx", a[6]);
@@ -503,6 +537,7 @@ PyObject *layer_norm_grad(PyObject *const *a)
         lddx = rows("dx", *dx.t, &x, &type);
     else
         dx.plan(x, type, R, C);
+    const Guard guard(x.device());
     int64_t bytes = 0, rc;
     if (truth(a[7])) {
         checked(bytes = api.layer_norm_grad_workspace(R, C));
