@@ -579,9 +579,9 @@ def fp8_layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, y=None, y_dtype=
     ``q_dtype`` also (q, q_scale), the rows' fp8 codes and fp32 scales (the A
     operand of a row-wise product), made from the unrounded y in the same pass.
 
-    x is bf16, fp16 or fp32 with contiguous rows; gamma and beta are [C] of
-    one of these dtypes (both the same) or None; y has x's dtype unless
-    ``y_dtype`` says otherwise, and is None with ``return_y`` false.
+    x is bf16, fp16 or fp32 with contiguous rows of at least one column; gamma
+    and beta are [C] of one of these dtypes (both the same) or None; y has x's
+    dtype unless ``y_dtype`` says otherwise, and is None with ``return_y`` false.
     """
     if stream is not None:
         with _on(stream, x):

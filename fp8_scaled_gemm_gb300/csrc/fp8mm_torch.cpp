@@ -475,6 +475,8 @@ PyObject *layer_norm(PyObject *const *a)
 {
     const Tensor &x = *tensor("x", a[0]), *gamma = tensor("gamma", a[1], true), *beta = tensor("beta", a[2], true);
     const int64_t ldx = rows("x", x), R = x.size(0), C = x.size(1);
+    if (R > 0 && C == 0)
+        refuse("x's rows must have at least one column");
     if (gamma && beta && gamma->scalar_type() != beta->scalar_type())
         refuse("gamma and beta must have one dtype");
     vector("gamma", gamma, C, true, x);

@@ -457,7 +457,8 @@ int64_t fp8_act_grad_workspace(int64_t M, int64_t N);
  *              or q NULL (not wanted).
  *
  * A NaN or infinity makes its whole row NaN. Rows of zeros in y give the
- * codes of zeros and a zero scale. Any C >= 1; rows whose x, y, gamma and
+ * codes of zeros and a zero scale. Any C >= 1 (with R == 0 or C == 0 the call
+ * returns FP8MM_OK and writes nothing); rows whose x, y, gamma and
  * beta start on 16 bytes (q on 8) with C % 8 == 0 run fastest. A wait of wide
  * rows' CTAs for one another is bounded; fp8mm_device_status reports one that
  * ran out.
