@@ -870,8 +870,9 @@ int take_scratch(const Choice &c, int64_t batch, int sms, Scratch &sc, const cud
     return FP8MM_OK;
 }
 
-// The text form of a kernel choice (fp8mm_describe_choice's format).
-std::string describe(const Choice &c)
+// The text form of a kernel choice (fp8mm_describe_choice's format); epilogue: with
+// the extended one.
+std::string describe(const Choice &c, bool epilogue = false)
 {
     char buf[160];
     snprintf(buf, sizeof buf, "%s tile_n=%d split=%d tiles=%dx%d units=%d grid=%d%s",
@@ -885,7 +886,8 @@ std::string describe(const Choice &c)
     std::string d = buf;
     if (tile_group(c) != 8)
         d += " group=" + std::to_string(tile_group(c));
-    if (c.variant == FP8MM_VARIANT_TILE && c.tile_n == 256 && c.kblocks * int64_t(fp8mm::kBlockK) <= kTileWideMaxK)
+    if (c.variant == FP8MM_VARIANT_TILE && c.tile_n == 256 &&
+        c.kblocks * int64_t(fp8mm::kBlockK) <= (epilogue ? kTileWideMaxKExt : kTileWideMaxK))
         d += " epilogue_warps=16";
     return d;
 }
@@ -903,21 +905,22 @@ bool log_enabled()
 }
 
 void log_choice(int dev, int64_t batch, int64_t M, int64_t N, int64_t K, int mode, int a_type, int b_type,
-                int out_type, int req_variant, int req_tile_n, int req_split, const Choice &c, bool tuned)
+                int out_type, int req_variant, int req_tile_n, int req_split, const Choice &c, bool tuned,
+                bool epilogue)
 {
     static std::mutex mu;
     static std::set<std::vector<int64_t>> seen;
     const std::vector<int64_t> key{dev, batch, M, N, K, mode, a_type, b_type, out_type, req_variant, req_tile_n,
-                                   req_split};
+                                   req_split, epilogue};
     std::lock_guard<std::mutex> lock(mu);
     if (!seen.insert(key).second)
         return;
     static const char *types[] = {"e4m3", "e5m2"};
     static const char *outs[] = {"bf16", "fp16", "fp32", "e4m3"};
-    fprintf(stderr, "fp8mm: device %d batch %lld %lldx%lldx%lld %s %s x %s -> %s: %s (%s)\n", dev,
+    fprintf(stderr, "fp8mm: device %d batch %lld %lldx%lldx%lld %s %s x %s -> %s%s: %s (%s)\n", dev,
             static_cast<long long>(batch), static_cast<long long>(M), static_cast<long long>(N),
             static_cast<long long>(K), mode == FP8MM_SCALE_ROWWISE ? "row-wise" : "per-tensor", types[a_type & 1],
-            types[b_type & 1], outs[out_type & 3], describe(c).c_str(),
+            types[b_type & 1], outs[out_type & 3], epilogue ? " epilogue" : "", describe(c, epilogue).c_str(),
             req_variant != FP8MM_VARIANT_AUTO ? "requested" : tuned ? "tuned" : "model");
 }
 
@@ -1057,7 +1060,7 @@ int run(const void *A, const void *B, const float *sa, const float *sb, int scal
 
     const int req_variant = variant, req_tile_n = tile_n, req_split = split;
     bool tuned = false;
-    if (variant == FP8MM_VARIANT_AUTO) {
+    if (variant == FP8MM_VARIANT_AUTO && !epi) {   // tuned entries are timings of the plain product
         TuneVal tv;
         const TuneKey key{d->cc_major, d->cc_minor, d->sms, batch, M, N, K, scale_mode, a_type, b_type, out_type};
         if (tuned_lookup(key, &tv)) {
@@ -1093,7 +1096,7 @@ int run(const void *A, const void *B, const float *sa, const float *sb, int scal
     }
     if (log_enabled())
         log_choice(current_device(), batch, M, N, K, scale_mode, a_type, b_type, out_type, req_variant, req_tile_n,
-                   req_split, c, tuned);
+                   req_split, c, tuned, epi != nullptr);
     kp.scale_a = sa;
     kp.scale_b = sb;
     kp.bias = bias;

@@ -49,7 +49,8 @@
  * Logging: with FP8MM_LOG=1 in the environment, the first call of each
  * problem (device, batch, shape, scaling, element types, requested kernel)
  * prints one line on stderr naming the kernel chosen and whether the time
- * model, a tuned entry (fp8mm_autotune) or the caller chose it.
+ * model, a tuned entry (fp8mm_autotune) or the caller chose it. The extended
+ * epilogue's problems are their own, and no tuned entry is theirs.
  *
  * Threading: calls may come from any host thread. Calls that use the split-K
  * workspace and run concurrently on different streams of one device race on
@@ -548,7 +549,8 @@ int fp8_scaled_mm_noalloc(const void *A, const void *B,
  * for e4m3 operands and bf16 output); batch >= 1. Returns FP8MM_OK, an
  * argument error, FP8MM_ERR_CUDA, or FP8MM_ERR_TIMEOUT if a candidate's
  * bounded wait ran out. fp8_scaled_mm_noalloc ignores tuned choices (its
- * scratch bound is that of the built-in choice).
+ * scratch bound is that of the built-in choice), and so do the products with
+ * the extended epilogue (the candidates are timed without it).
  */
 int fp8mm_autotune(int64_t batch, int64_t M, int64_t N, int64_t K, int scale_mode,
                    const fp8mm_options *options, void *stream);
