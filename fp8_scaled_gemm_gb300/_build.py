@@ -65,7 +65,21 @@ def _binding_command(out: str) -> list:
             "-ltorch_cpu", "-ltorch_python"]
 
 
+def _start_binding(work: str):
+    """(path, command, process) of the extension module's compilation; an
+    exception in the process's place where it cannot start."""
+    module, cmd = os.path.join(work, BINDING + ".so"), []
+    try:
+        cmd = _binding_command(module)
+        return module, cmd, subprocess.Popen(cmd)
+    except (ImportError, OSError) as e:     # no PyTorch, no host compiler
+        return module, cmd, e
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Builds what is out of date. The library needs neither PyTorch nor
+    Python's headers: it is built and put in place also where the extension
+    module cannot be, and the module's failure is raised after that."""
     if not force and up_to_date():
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -75,23 +89,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         flags.insert(0, "-Xptxas=-v")
     with tempfile.TemporaryDirectory(dir=BUILD_DIR) as work:
-        # one nvcc per translation unit, all at once, then the link
+        # one compiler per translation unit, all at once, then the link
+        module, module_cmd, binding = _start_binding(work)
         jobs = []
-        module = os.path.join(work, BINDING + ".so")
-        cmd = _binding_command(module)
-        binding = (module, cmd, subprocess.Popen(cmd))
         for src in SOURCES:
             obj = os.path.join(work, src + ".o")
             cmd = [nvcc_path(), *flags, "-c", os.path.join(CSRC, src), "-o", obj]
             if verbose:
                 print(" ".join(cmd), file=sys.stderr)
             jobs.append((obj, cmd, subprocess.Popen(cmd)))
-        failed = [(p.returncode, cmd) for _, cmd, p in [*jobs, binding] if p.wait() != 0]
+        failed = [(p.returncode, cmd) for _, cmd, p in jobs if p.wait() != 0]
+        module_rc = None if isinstance(binding, Exception) else binding.wait()
         if failed:
             raise subprocess.CalledProcessError(*failed[0])
         subprocess.run([nvcc_path(), *flags, "-shared", *[obj for obj, _, _ in jobs], "-o", tmp], check=True)
-        os.replace(module, BINDING_PATH)
-    os.replace(tmp, LIB_PATH)
+        if module_rc == 0:
+            os.replace(module, BINDING_PATH)
+        os.replace(tmp, LIB_PATH)
+    if module_rc is None:
+        raise RuntimeError(f"{LIB_PATH} is built; the extension module {BINDING} cannot be") from binding
+    if module_rc != 0:
+        raise subprocess.CalledProcessError(module_rc, module_cmd)
     return LIB_PATH
 
 
