@@ -205,6 +205,10 @@ def _load_native():
             if not os.path.exists(path):
                 raise RuntimeError(f"extension module {path} is missing; build it with "
                                    "`python -c 'import __graft_entry__ as g; g.build()'`")
+            if _build.binding_is_for() != _build.binding_abi():
+                raise RuntimeError(f"extension module {path} was built for '{_build.binding_is_for()}', this is "
+                                   f"'{_build.binding_abi()}'; build it again with "
+                                   "`python -c 'import __graft_entry__ as g; g.build()'`")
             spec = importlib.util.spec_from_file_location(
                 _build.BINDING, path, loader=importlib.machinery.ExtensionFileLoader(_build.BINDING, path))
             module = importlib.util.module_from_spec(spec)

@@ -43,11 +43,27 @@ def _inputs():
     return files
 
 
+def binding_abi() -> str:
+    """What the extension module is bound to: PyTorch's C++ interface, which
+    changes from version to version, and Python's."""
+    import torch
+    return f"{torch.__version__} {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_is_for() -> str:
+    """The binding_abi() the module was built for; "" without a module."""
+    try:
+        with open(BINDING_PATH + ".abi") as f:
+            return f.read() if os.path.exists(BINDING_PATH) else ""
+    except OSError:
+        return ""
+
+
 def up_to_date() -> bool:
     if not (os.path.exists(LIB_PATH) and os.path.exists(BINDING_PATH)):
         return False
     t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return all(os.path.getmtime(f) <= t for f in _inputs()) and binding_is_for() == binding_abi()
 
 
 def _binding_command(out: str) -> list:
@@ -104,7 +120,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise subprocess.CalledProcessError(*failed[0])
         subprocess.run([nvcc_path(), *flags, "-shared", *[obj for obj, _, _ in jobs], "-o", tmp], check=True)
         if module_rc == 0:
+            with open(module + ".abi", "w") as f:
+                f.write(binding_abi())
             os.replace(module, BINDING_PATH)
+            os.replace(module + ".abi", BINDING_PATH + ".abi")
         os.replace(tmp, LIB_PATH)
     if module_rc is None:
         raise RuntimeError(f"{LIB_PATH} is built; the extension module {BINDING} cannot be") from binding

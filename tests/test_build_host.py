@@ -6,7 +6,9 @@ import stat
 import subprocess
 
 import pytest
+import torch
 
+import fp8_scaled_gemm_gb300 as fm
 from fp8_scaled_gemm_gb300 import _build
 
 COMPILER = """#!/bin/sh
@@ -71,3 +73,23 @@ def test_a_failed_source_leaves_no_library(stand_ins, monkeypatch):
     with pytest.raises(subprocess.CalledProcessError):
         _build.build()
     assert not os.path.exists(_build.LIB_PATH)
+
+
+def test_a_module_of_another_pytorch_is_stale(stand_ins, monkeypatch):
+    _build.build()
+    os.utime(_build.BINDING_PATH, (1e9, 1e9))
+    assert not _build.up_to_date()
+    _build.build()
+    assert _build.up_to_date()
+    monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    assert not _build.up_to_date()
+    _build.build()
+    assert _build.up_to_date()
+
+
+def test_a_module_of_another_pytorch_is_not_loaded(monkeypatch):
+    _build.build()
+    monkeypatch.setattr(fm, "_native", None)
+    monkeypatch.setattr(_build, "binding_abi", lambda: "0.0.1+other")
+    with pytest.raises(RuntimeError, match="build it again"):
+        fm._load_native()
