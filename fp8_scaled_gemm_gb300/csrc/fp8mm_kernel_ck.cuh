@@ -287,6 +287,9 @@ __global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(kThreads, EPI && BN
             const int n = tp * kTileP + rl;
 #pragma unroll 1
             for (int turn = 0; turn < kTurns; turn += kGroup) {
+                const int c0 = (t >> 5) + 4 * turn;
+                if (c0 >= C::kCols || tq * BN + rank * C::kCols + c0 >= p.M)
+                    break;                                      // and so are the later ones
                 float y[4 * kGroup], r[4 * kGroup];
 #pragma unroll
                 for (int g = 0; g < kGroup; ++g) {
