@@ -295,7 +295,7 @@ struct Team {
 // Exchanges of a cluster's team: every warp's values go to all its CTAs, into
 // the slot of the warp in their buffer `red`, and are counted there on mbarrier
 // k. (A cluster barrier per exchange waits for the row's global stores as well:
-// forward 4096 x 32768 bf16 with codes 290 us, now 194; backward 8192 x 8192
+// forward 4096 x 32768 bf16 with codes 290 us, then 194; backward 8192 x 8192
 // fp32 268, now 177.)
 template <int NV>
 __device__ __forceinline__ void cluster_send(const float (&v)[NV], const Team &tm, float *red, int k)
@@ -528,6 +528,37 @@ __device__ __forceinline__ void store_codes(uint8_t *dst, const fp8q::Divider &d
     }
 }
 
+// The codes of the thread's values, two from each pair by `code`.
+template <int G, int KIND, int CH, typename Code>
+__device__ __forceinline__ void put_codes(uint8_t *p, const Place<G, KIND, CH> &pl, const uint64_t (&v)[4 * CH],
+                                          const Code &code)
+{
+    constexpr int step = Place<G, KIND, CH>::kStep;
+    if constexpr (G == 8) {
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const uint2 w = make_uint2(code(v[4 * k]) | (code(v[4 * k + 1]) << 16),
+                                       code(v[4 * k + 2]) | (code(v[4 * k + 3]) << 16));
+            if (pl.in(k))
+                *reinterpret_cast<uint2 *>(p + k * step) = w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4 * CH; ++i) {
+            const uint32_t c = code(v[i]);
+            if constexpr (G == 2) {
+                if (pl.in(i))
+                    *reinterpret_cast<unsigned short *>(p + i * step) = static_cast<unsigned short>(c);
+            } else {
+                if (pl.in(2 * i))
+                    p[2 * i * step] = static_cast<uint8_t>(c & 0xFFu);
+                if (pl.in(2 * i + 1))
+                    p[(2 * i + 1) * step] = static_cast<uint8_t>(c >> 8);
+            }
+        }
+    }
+}
+
 // The codes of the thread's values, those of fp8_quantize (a y of -0 may give +0).
 // With a scale in the reciprocal's range the quotients come from the reciprocal in
 // two parts: r, the nearest fp32 value to 1 / scale (rcp.approx and one step of
@@ -536,73 +567,55 @@ __device__ __forceinline__ void store_codes(uint8_t *dst, const fp8q::Divider &d
 // every mantissa of the scale, with every value within 12 units of its product with
 // every tie between two codes, gave the code of the correctly rounded quotient.
 // (16384 x 8192 bf16: the reciprocal alone, which is on the wrong side of some
-// ties, with a scale of one product 116 us, this 123, div_fast's correction 127.)
+// ties, with a scale of one product 116 us; this 121, with all codes made before
+// the first is stored 123, with div_fast's correction instead 127.)
 template <int G, int KIND, int CH>
 __device__ __forceinline__ void store_codes_e(uint8_t *p, const Place<G, KIND, CH> &pl, float scale,
                                               const uint64_t (&v)[4 * CH], int q_type)
 {
-    constexpr int step = Place<G, KIND, CH>::kStep;
-    uint32_t c[4 * CH];                  // two codes each
     if (fp8q::in_reciprocal_range(scale)) {
         const float r0 = fp8mm::rcp_approx(scale), r = fmaf(fmaf(-scale, r0, 1.0f), r0, r0);
         const float e = fmaf(-scale, r, 1.0f), rl = fmaf(e, e, e) * r;
         const uint64_t r2 = ptx::f32x2(r, r), l2 = ptx::f32x2(rl, rl);
+        auto quotient = [&](uint64_t x, float &lo, float &hi) {
+            ptx::unpack_f32x2(ptx::fma_f32x2(x, r2, ptx::mul_f32x2(x, l2)), lo, hi);
+        };
         // one branch for all
-        if (q_type == 0) {
-#pragma unroll
-            for (int i = 0; i < 4 * CH; ++i) {
-                float a, b;
-                ptx::unpack_f32x2(ptx::fma_f32x2(v[i], r2, ptx::mul_f32x2(v[i], l2)), a, b);
-                c[i] = fp8q::cvt_pair(a, b, 0);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4 * CH; ++i) {
-                float a, b;
-                ptx::unpack_f32x2(ptx::fma_f32x2(v[i], r2, ptx::mul_f32x2(v[i], l2)), a, b);
-                c[i] = fp8q::cvt_pair(a, b, 1);
-            }
-        }
-    } else {
-        const fp8q::Divider d = fp8q::make_divider(scale);
-#pragma unroll
-        for (int i = 0; i < 4 * CH; ++i) {
-            float a, b;
-            ptx::unpack_f32x2(v[i], a, b);
-            c[i] = fp8q::cvt_pair(fp8q::div_slow(d, a), fp8q::div_slow(d, b), q_type);
-        }
+        if (q_type == 0)
+            put_codes<G, KIND, CH>(p, pl, v, [&](uint64_t x) {
+                float lo, hi;
+                quotient(x, lo, hi);
+                return fp8q::cvt_pair(lo, hi, 0);
+            });
+        else
+            put_codes<G, KIND, CH>(p, pl, v, [&](uint64_t x) {
+                float lo, hi;
+                quotient(x, lo, hi);
+                return fp8q::cvt_pair(lo, hi, 1);
+            });
+        return;
     }
-#pragma unroll
-    for (int i = 0; i < 4 * CH; ++i) {
-        if constexpr (G == 8) {
-            if (i % 4 == 0 && pl.in(i / 4))
-                *reinterpret_cast<uint2 *>(p + (i / 4) * step) =
-                    make_uint2(c[i] | (c[i + 1] << 16), c[i + 2] | (c[i + 3] << 16));
-        } else if constexpr (G == 2) {
-            if (pl.in(i))
-                *reinterpret_cast<unsigned short *>(p + i * step) = static_cast<unsigned short>(c[i]);
-        } else {
-            if (pl.in(2 * i))
-                p[2 * i * step] = static_cast<uint8_t>(c[i] & 0xFFu);
-            if (pl.in(2 * i + 1))
-                p[(2 * i + 1) * step] = static_cast<uint8_t>(c[i] >> 8);
-        }
-    }
+    const fp8q::Divider d = fp8q::make_divider(scale);
+    put_codes<G, KIND, CH>(p, pl, v, [&](uint64_t x) {
+        float lo, hi;
+        ptx::unpack_f32x2(x, lo, hi);
+        return fp8q::cvt_pair(fp8q::div_slow(d, lo), fp8q::div_slow(d, hi), q_type);
+    });
 }
 
 // One row per CTA at a time (KIND > 0: per team of lanes), 64 registers, and
 // as many CTAs on an SM as make 1024 threads: they hide each other's barriers.
-// 16 columns per thread. 16384 x 8192 bf16 with codes takes 123 us, 5.5 TB/s (82 %
-// of a copy; 113 to 116 before the codes were made of correctly rounded quotients:
-// 20 instructions per element then, issue slots 60 % busy). Measured there
-// against 121 us of an earlier form: 8 columns 177; 32 columns and 768 threads
+// 16 columns per thread. 16384 x 8192 bf16 with codes takes 121 us, 5.5 TB/s (83 %
+// of a copy; 22 instructions per element, issue slots 62 % busy; 113 to 116 us and
+// 20 before the codes were made of correctly rounded quotients, which the next
+// figures are without). Measured there against 121 us of an earlier form: 8 columns 177; 32 columns and 768 threads
 // 150; the next two rows in shared memory (cp.async) instead of the next one in
 // registers 119 to 121; several rows' teams in one CTA 155; gamma and beta from
 // global memory (L1) for every row 174 (they are kept in shared memory,
 // keep_params); against 113: the warps' own means and differences joined in one
 // exchange instead of two 116. Rows of 16-bit elements without 16-byte groups:
-// 16384 x 4998 bf16 in pairs 86 us (71 %; single elements 121), 16384 x 4999 in
-// single elements (34 instructions each) 122 us (50 %), against 73 at 5000
+// 16384 x 4998 bf16 in pairs 90 us (68 %; single elements 121), 16384 x 4999 in
+// single elements (34 instructions each) 123 us (50 %), against 80 at 5000
 // columns. For odd widths, pairs with single elements at the edges took 134 to
 // 158, accesses without bounds tests in all but the last warp 118 (35 instead
 // of 26 at 1001 columns).
@@ -821,13 +834,13 @@ constexpr int kGradCh = (ES == 2 && DES == 2 && G > 1 && KIND <= 0) ? 2 : 1;
 
 // Each thread keeps the dgamma and dbeta sums of its columns in registers over
 // all its rows; teams of lanes then add theirs in order through shared memory.
-// 16384 x 8192 bf16 with a residual gradient takes 175 us, 6.1 TB/s (92 % of a
+// 16384 x 8192 bf16 with a residual gradient takes 177 us, 6.1 TB/s (91 % of a
 // copy), 8192 x 8192 fp32 178 (91 %). Registers (128 per thread) hold one row at
 // work, one on its way and the sums, so an SM has 512 threads and wide rows one
-// or two teams: 8192 x 16384 bf16 runs at 73 %, 4096 x 32768 at 42 %, waiting for
-// exchanges. In pairs 16384 x 4094 takes 113 us (71 %), 12782 x 10500 361 (45 %;
+// or two teams: 8192 x 16384 bf16 runs at 70 %, 4096 x 32768 at 41 %, waiting for
+// exchanges. In pairs 16384 x 4094 takes 116 us (70 %), 12782 x 10500 361 (45 %;
 // single elements 728). Single elements leave registers for 8 columns per thread
-// (16384 x 4095 bf16 129 us, 62 %; over 4096 columns, in clusters, 19 to 39 %).
+// (16384 x 4095 bf16 135 us, 60 %; over 4096 columns, in clusters, 19 to 39 %).
 // Teams of lanes: CTAs of 256 threads, 4 on an SM (3 where registers hold fp32 rows).
 constexpr int kGradLaneThreads = 256;
 template <int ES, int DES>
@@ -1042,7 +1055,8 @@ __global__ void __launch_bounds__(KIND > 0 ? kGradLaneThreads : kGradThreads, KI
 // sums are sent before the row before it is finished, so that an exchange has a
 // row's work to hide behind; until then the row is kept as loaded, and it is
 // converted twice. bf16 with a residual gradient, norm_grad_kernel and this one:
-// 8192 x 16384 250 and 221 us, 12000 x 12288 324 and 278, 4096 x 32768 441 and 383.
+// 8192 x 16384 250 and 221 us (228 since columns past the row's end are left out of
+// its sums), 12000 x 12288 324 and 278 (287), 4096 x 32768 441 and 383 (388).
 // Other operands lost with it (16384 x 9132 unaligned 653 and 762, 4096 x 16384
 // fp32 284 and 303: 8 columns per thread leave less work to hide behind, and more
 // of the second conversion's). Four buffers: a warp sends for row n after it has
