@@ -67,23 +67,34 @@ def test_threads_with_streams_of_their_own():
     assert fm.fp8mm_device_status() == 0, fm.fp8mm_last_error()
 
 
+MANY = r"""
+import sys
+import torch
+sys.path.insert(0, sys.argv[1])
+import fp8_scaled_gemm_gb300 as fm
+from tests.test_epilogue_streams_gpu import SHAPES, both, problem
+p = problem(*SHAPES[0], seed=1)
+want = both(p)
+streams = [torch.cuda.Stream() for _ in range(24)]
+torch.cuda.synchronize()
+got = []
+for s in streams:
+    with torch.cuda.stream(s):
+        got.append(both(p))
+torch.cuda.synchronize()
+assert fm.fp8mm_device_status() == 0, fm.fp8mm_last_error()
+for g in got:
+    for a, b in zip(g, want):
+        # one rounding to bf16 apart, and the fp32 sums' order
+        assert torch.allclose(a.float(), b.float(), rtol=2.0 ** -7, atol=2.0 ** -10)
+"""
+
+
 def test_more_streams_than_there_is_scratch_for():
     """Past 16 streams the kernels that need none are taken: the same sums in
-    another order."""
-    p = problem(*SHAPES[0], seed=1)
-    want = both(p)
-    streams = [torch.cuda.Stream() for _ in range(24)]
-    torch.cuda.synchronize()
-    got = []
-    for s in streams:
-        with torch.cuda.stream(s):
-            got.append(both(p))
-    torch.cuda.synchronize()
-    assert fm.fp8mm_device_status() == 0, fm.fp8mm_last_error()
-    for g in got:
-        for a, b in zip(g, want):
-            # one rounding to bf16 apart, and the fp32 sums' order
-            assert torch.allclose(a.float(), b.float(), rtol=2.0 ** -7, atol=2.0 ** -10)
+    another order. (A process of its own: the workspaces stay.)"""
+    r = subprocess.run([sys.executable, "-c", MANY, ROOT], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
 
 
 SCRIPT = r"""
