@@ -5,8 +5,8 @@
 A thin binding over ``libfp8mm.so`` (``include/fp8mm.h``): each function has
 the name of the C entry point it calls and only checks and marshals
 arguments; every step of the computation runs in the CUDA kernels. Most go
-through ctypes; the operators of an MLP block, whose small calls take the host
-longer than the GPU, through a native module (``csrc/fp8mm_torch.cpp``).
+through ctypes; the operators of a training step (MLP block, loss, update),
+whose small calls take the host longer than the GPU, through a native module (``csrc/fp8mm_torch.cpp``).
 There is no CPU fallback: if a library cannot be loaded, calls raise. A call's
 tensors are on one device: the current one, or for the native module's operators
 any.
@@ -66,6 +66,21 @@ class Epilogue(ctypes.Structure):
                 ("preact", ctypes.c_void_p), ("ldp", ctypes.c_int64)]
 
 
+class AdamwTensor(ctypes.Structure):
+    """fp8mm_adamw_tensor of include/fp8mm.h."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("count", ctypes.c_int64)]
+
+
+class AdamwOptions(ctypes.Structure):
+    """fp8mm_adamw_options of include/fp8mm.h."""
+    _fields_ = [("param_type", ctypes.c_int), ("grad_type", ctypes.c_int), ("state_bits", ctypes.c_int),
+                ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64), ("lr_device", ctypes.c_void_p),
+                ("step_device", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p)]
+
+
 STATUS = {
     0: "FP8MM_OK", -1: "FP8MM_ERR_NULL", -2: "FP8MM_ERR_SHAPE", -3: "FP8MM_ERR_ALIGN",
     -4: "FP8MM_ERR_MODE", -5: "FP8MM_ERR_CUDA", -6: "FP8MM_ERR_NODEV", -7: "FP8MM_ERR_TIMEOUT",
@@ -78,6 +93,8 @@ EXPORTS = (
     "fp8_scaled_mm_layout", "fp8_scaled_mm_epilogue", "fp8_scaled_mm_act_grad",
     "fp8_act_grad", "fp8_act_grad_workspace", "fp8_layer_norm", "fp8_layer_norm_grad",
     "fp8_layer_norm_grad_workspace",
+    "fp8_cross_entropy", "fp8_cross_entropy_workspace", "fp8_cross_entropy_grad", "fp8_cross_entropy_grad_workspace",
+    "fp8_adamw",
     "fp8mm_reserve_workspace", "fp8mm_device_status", "fp8mm_status_string",
     "fp8mm_last_cuda_error", "fp8mm_last_error", "fp8mm_describe_choice", "fp8mm_describe_bmm_choice", "fp8mm_debug_inject", "fp8mm_debug_quant", "fp8mm_describe_model_choice",
     "fp8mm_describe_quant_plan",
@@ -151,6 +168,18 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.fp8_layer_norm_grad.restype = i32
         lib.fp8_layer_norm_grad_workspace.argtypes = [i64, i64]
         lib.fp8_layer_norm_grad_workspace.restype = i64
+        lib.fp8_cross_entropy.argtypes = [vp, i32, vp, i32, vp, vp, i32, vp, i32, vp, i64, vp, vp, i64, i64, i64, vp, i64,
+                                          vp]
+        lib.fp8_cross_entropy.restype = i32
+        lib.fp8_cross_entropy_workspace.argtypes = [i64, i64]
+        lib.fp8_cross_entropy_workspace.restype = i64
+        lib.fp8_cross_entropy_grad.argtypes = [vp, i32, vp, i32, vp, vp, i32, vp, i32, vp, i64, vp, vp, i64, vp, vp, i32, vp,
+                                               i64, i64, i64, vp, i64, vp]
+        lib.fp8_cross_entropy_grad.restype = i32
+        lib.fp8_cross_entropy_grad_workspace.argtypes = [i64, i64, i64, i32, i32, i32]
+        lib.fp8_cross_entropy_grad_workspace.restype = i64
+        lib.fp8_adamw.argtypes = [ctypes.POINTER(AdamwTensor), i64, ctypes.POINTER(AdamwOptions), vp]
+        lib.fp8_adamw.restype = i32
         lib.fp8_quantize.argtypes = [vp, i64, i64, i32, i32, vp, vp, vp]
         lib.fp8_quantize.restype = i32
         lib.fp8_scaled_mm_bf16.argtypes = [vp, vp, i32, vp, vp, i64, i64, i64, vp, vp, vp, vp, vp,
@@ -196,7 +225,7 @@ _native = None
 
 
 def _load_native():
-    """The native module that binds the MLP block's operators."""
+    """The native module that binds the operators of a training step."""
     global _native
     lib = load()
     with _lock:
@@ -217,7 +246,8 @@ def _load_native():
                 ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
                 for name in ("fp8_scaled_mm_epilogue", "fp8_scaled_mm_act_grad", "fp8_act_grad",
                              "fp8_act_grad_workspace", "fp8_layer_norm", "fp8_layer_norm_grad",
-                             "fp8_layer_norm_grad_workspace")))
+                             "fp8_layer_norm_grad_workspace", "fp8_cross_entropy", "fp8_cross_entropy_workspace",
+                             "fp8_cross_entropy_grad", "fp8_cross_entropy_grad_workspace", "fp8_adamw")))
             _native = module
     return _native
 
@@ -606,6 +636,61 @@ def fp8_layer_norm_grad(dy, x, gamma, mean, rstd, residual_grad=None, dx=None, s
         with _on(stream, x):
             return fp8_layer_norm_grad(dy, x, gamma, mean, rstd, residual_grad, dx, None, return_params)
     return (_native or _load_native()).layer_norm_grad(dy, x, gamma, mean, rstd, residual_grad, dx, return_params)
+
+
+def fp8_cross_entropy(A, B, scale_a, scale_b, scale_mode: int, target, bias=None, ignore_index: int = -100, stream=None):
+    """(loss, lse): softmax cross entropy of each row of z = A.B * scale + bias,
+    without z being stored.
+
+    A and B are the operands of fp8_scaled_mm_ex; ``target`` int64 [M] holds
+    columns of z, or ``ignore_index`` (loss 0); ``bias`` [N] is bf16, fp16 or
+    fp32. loss and lse = log(sum(exp(z))) are fp32 [M].
+    """
+    if stream is not None:
+        with _on(stream, A):
+            return fp8_cross_entropy(A, B, scale_a, scale_b, scale_mode, target, bias, ignore_index, None)
+    return (_native or _load_native()).cross_entropy(A, B, scale_a, scale_b, scale_mode, target, bias, ignore_index)
+
+
+def fp8_cross_entropy_grad(A, B, scale_a, scale_b, scale_mode: int, target, lse, dloss, bias=None,
+                           ignore_index: int = -100, da=None, db=None, stream=None, out_dtype=torch.bfloat16,
+                           return_da: bool = True, return_db: bool = True, return_dbias: bool = False):
+    """Backward pass of fp8_cross_entropy: (da, db, dbias).
+
+    ``lse`` is what the forward pass returned; ``dloss`` fp32 [M], or one value
+    for all rows. da [M, K] and db [N, K] (of B's columns, the layout of
+    ``B.t()``) are the gradients of scale_a * A and scale_b * B in
+    ``out_dtype`` (bf16, fp16 or fp32), dbias fp32 [N]. A result that is not
+    asked for is None.
+    """
+    if stream is not None:
+        with _on(stream, A):
+            return fp8_cross_entropy_grad(A, B, scale_a, scale_b, scale_mode, target, lse, dloss, bias, ignore_index, da,
+                                          db, None, out_dtype, return_da, return_db, return_dbias)
+    return (_native or _load_native()).cross_entropy_grad(A, B, scale_a, scale_b, scale_mode, target, lse, dloss, bias,
+                                                          ignore_index, da, db, out_dtype, return_da, return_db,
+                                                          return_dbias)
+
+
+def fp8_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, beta1: float = 0.9, beta2: float = 0.999,
+              eps: float = 1e-8, weight_decay: float = 1e-2, masters=None, exp_avg_scales=None, exp_avg_sq_scales=None,
+              grad_scale=None, stream=None) -> None:
+    """One AdamW step over lists of contiguous tensors, in place.
+
+    ``params`` (bf16, fp16 or fp32, all of one dtype) are updated, or, with
+    ``masters`` (fp32), receive the rounding of the updated masters. The states
+    are fp32, or float8_e4m3fn (of m and of sqrt(v)) with fp32 scales, one for
+    each 256 elements. Zeros are the states to begin with. ``step`` counts from
+    1; it (int64) and ``lr`` (fp32) may be CUDA tensors of one value, which a
+    captured call reads when it is replayed. ``grad_scale``, a CUDA tensor of
+    one fp32 value, multiplies the gradients.
+    """
+    if stream is not None:
+        with _on(stream, params[0] if len(params) else None):
+            return fp8_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr, beta1, beta2, eps, weight_decay, masters,
+                             exp_avg_scales, exp_avg_sq_scales, grad_scale, None)
+    (_native or _load_native()).adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr, beta1, beta2, eps, weight_decay,
+                                      masters, exp_avg_scales, exp_avg_sq_scales, grad_scale)
 
 
 def fp8mm_reserve_workspace(nbytes: int) -> None:

@@ -25,7 +25,8 @@ LIB_PATH = os.path.join(BUILD_DIR, "libfp8mm.so")
 BINDING = "_fp8mm_torch"
 BINDING_PATH = os.path.join(BUILD_DIR, BINDING + ".so")
 
-SOURCES = ["fp8mm_epilogue.cu", "fp8mm_epilogue_swap.cu", "fp8mm_api.cu", "fp8mm_norm_grad.cu", "fp8mm_norm.cu", "fp8mm_actgrad.cu"]
+SOURCES = ["fp8mm_epilogue.cu", "fp8mm_epilogue_swap.cu", "fp8mm_api.cu", "fp8mm_norm_grad.cu", "fp8mm_norm.cu", "fp8mm_actgrad.cu",
+           "fp8mm_loss.cu", "fp8mm_adamw.cu"]
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 

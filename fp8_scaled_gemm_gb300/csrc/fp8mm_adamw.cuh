@@ -1,0 +1,336 @@
+// fp8mm_adamw.cuh -- one AdamW step over many tensors.
+//
+//   g  = grad * grad_scale
+//   m' = b1 m + (1 - b1) g          v' = b2 v + (1 - b2) g^2
+//   w' = w (1 - lr wd) - lr / (1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps)
+//
+// in fp32, every operation rounded by itself (no contraction), so that a step
+// gives the same bits as its formula written out in single operations.
+//
+// States in 8 bits: e4m3 codes in blocks of 256 elements with an fp32 scale
+// each (largest magnitude / 448), m as itself and v as its root: the root
+// halves the exponents v spans, and e4m3 with the block's scale then reaches
+// 2^-18 of the block's largest. m is rounded to the nearest code: a step moves it
+// by about a tenth of its distance to g. The root of v moves by less than
+// 0.05 % of itself in a step with b2 = 0.999, codes are 6 to 12 % apart, and the
+// nearest one would be the old one for ever; it is rounded up or down with the
+// probabilities that keep its mean, by a hash of the element's place and of the
+// step. A root that is not zero does not become zero, since it divides.
+//
+// Bound by memory: with bf16 weights and gradients, fp32 originals and 8-bit
+// states 16 bytes an element. A warp takes a block of 256 elements, 8
+// consecutive ones a lane (16-byte accesses), so that a block's scale needs
+// shuffles only. The tensors' addresses come in the kernel's parameters: no
+// copy to the device, nothing kept, and a captured launch holds its own table.
+#pragma once
+
+#include "fp8mm_quant_convert.cuh"
+#include "fp8mm_rows.cuh"
+
+namespace fp8adam {
+
+namespace ptx = fp8mm::ptx;
+
+constexpr int kBlock = 256;            // elements of a block, of one warp
+constexpr int kThreads = 256;
+
+struct Tensor {
+    void *param;
+    const void *grad;
+    float *master;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    long long count;
+    long long first;                   // its first block in the launch's order
+    int vec;                           // 16-byte accesses allowed (codes: 8)
+};
+
+struct Hyper {
+    // 1 - lr wd, b1, 1 - b1, b2, 1 - b2, eps, lr / (1 - b1^t), 1 / sqrt(1 - b2^t);
+    // made anew on the device where it holds lr or the step
+    float keep, b1, b1c, b2, b2c, eps, step_size, root;
+    double lr, rest1, beta1, beta2, weight_decay;      // rest1 = 1 - b1^t
+    const float *lr_device;
+    const int64_t *step_device;
+    uint32_t step;                     // low bits, for the rounding
+    const float *grad_scale;
+};
+
+// T tensors by value: 32 or as many as 32 KB of parameters hold.
+template <int T>
+struct Params {
+    Hyper h;
+    int tensors, param_type, grad_type, has_master;
+    long long blocks;
+    Tensor t[T];
+};
+
+constexpr int kFew = 32, kMany = 400;
+static_assert(sizeof(Params<kMany>) <= 32764, "kernel parameters");
+
+// Eight elements of a lane as loaded, 2 or 4 bytes each.
+struct Eight {
+    uint32_t w[8];
+};
+
+__device__ __forceinline__ void load8(Eight &r, const void *base, int type, long long e)
+{
+    if (type == fp8rows::kF32) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + e);
+        const uint4 a = __ldcs(p), b = __ldcs(p + 1);
+        r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+        r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
+    } else {
+        const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(base) + e));
+        r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+    }
+}
+
+__device__ __forceinline__ void floats8(const Eight &r, int type, float (&v)[8])
+{
+    if (type == fp8rows::kF32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = __uint_as_float(r.w[i]);
+    } else {
+        fp8rows::Raw<2, 8> raw;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            raw.w[i] = r.w[i];
+        fp8rows::to_float<2, 8>(raw, type == fp8rows::kF16, v);
+    }
+}
+
+__device__ __forceinline__ float load1(const void *base, int type, long long e)
+{
+    return type == fp8rows::kF32 ? static_cast<const float *>(base)[e]
+                                 : fp8rows::half_bits(static_cast<const unsigned short *>(base)[e], type == fp8rows::kF16);
+}
+
+__device__ __forceinline__ void store8(void *base, int type, long long e, const float (&v)[8])
+{
+    if (type == fp8rows::kF32) {
+        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + e);
+        __stcs(p, make_float4(v[0], v[1], v[2], v[3]));
+        __stcs(p + 1, make_float4(v[4], v[5], v[6], v[7]));
+    } else {
+        __stcs(reinterpret_cast<uint4 *>(static_cast<unsigned short *>(base) + e),
+               make_uint4(fp8rows::pack2(v[0], v[1], type), fp8rows::pack2(v[2], v[3], type),
+                          fp8rows::pack2(v[4], v[5], type), fp8rows::pack2(v[6], v[7], type)));
+    }
+}
+
+// Two e4m3 codes (low half first) to fp32.
+__device__ __forceinline__ float2 decode2(uint32_t codes)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+__device__ __forceinline__ float decode1(uint8_t code) { return decode2(code).x; }
+
+__device__ __forceinline__ float quotient(const fp8q::Divider &d, float x)
+{
+    // (the reciprocal path's residual needs a finite x)
+    return d.mode == 1 && fabsf(x) < 0x1p100f ? fp8q::div_fast(d, x) : d.mode == 0 ? 0.0f : __fdiv_rn(x, d.s);
+}
+
+// 20 bits for the rounding of element e at a step.
+__device__ __forceinline__ uint32_t dither(uint32_t e, uint32_t step)
+{
+    uint32_t x = e * 0x9E3779B1u + step * 0x85EBCA77u;
+    x = (x ^ (x >> 15)) * 0x2C1B3C6Du;
+    x = (x ^ (x >> 13)) * 0x297A2D39u;
+    return (x ^ (x >> 16)) >> 12;
+}
+
+// q >= 0 (or NaN) to a value that e4m3 holds, up or down by u. Codes are 2^-3 of
+// the power of two apart, 20 bits of an fp32 mantissa, and 2^-9 below 2^-6.
+__device__ __forceinline__ float round_by(float q, uint32_t u)
+{
+    q = q > 448.0f ? 448.0f : q;
+    if (q < 0x1p-6f)
+        return q > 0.0f ? fmaxf(floorf(__fadd_rn(q * 512.0f, static_cast<float>(u) * 0x1p-20f)) * 0x1p-9f, 0x1p-9f) : q;
+    return q == q ? __uint_as_float((__float_as_uint(q) + u) & ~0xFFFFFu) : q;
+}
+
+// The largest of a warp's values, NaN if one is.
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v = fp8mm::max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+
+template <int BITS, int T>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Params<T> p)
+{
+    __shared__ float shared_hyper[3];
+    __shared__ uint32_t shared_step;
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    float keep = p.h.keep, step_size = p.h.step_size, root = p.h.root;
+    uint32_t step = p.h.step;
+    if (p.h.step_device || p.h.lr_device) {
+        // (the same for every CTA; in double, as the host does it)
+        if (threadIdx.x == 0) {
+            double lr = p.h.lr, rest1 = p.h.rest1;
+            shared_hyper[2] = root;
+            shared_step = step;
+            if (p.h.lr_device)
+                lr = static_cast<double>(__ldcg(p.h.lr_device));
+            if (p.h.step_device) {
+                const long long t = __ldcg(reinterpret_cast<const long long *>(p.h.step_device));
+                rest1 = 1.0 - pow(p.h.beta1, static_cast<double>(t));
+                shared_hyper[2] = static_cast<float>(1.0 / sqrt(1.0 - pow(p.h.beta2, static_cast<double>(t))));
+                shared_step = static_cast<uint32_t>(t);
+            }
+            shared_hyper[0] = static_cast<float>(1.0 - lr * p.h.weight_decay);
+            shared_hyper[1] = static_cast<float>(lr / rest1);
+        }
+        __syncthreads();
+        keep = shared_hyper[0];
+        step_size = shared_hyper[1];
+        root = shared_hyper[2];
+        step = shared_step;
+    }
+    const float gs = p.h.grad_scale ? __ldcg(p.h.grad_scale) : 1.0f;
+    const int lane = threadIdx.x & 31;
+    const long long warps = static_cast<long long>(gridDim.x) * (kThreads / 32);
+    int k = 0;
+    for (long long b = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); b < p.blocks; b += warps) {
+        while (k + 1 < p.tensors && b >= p.t[k + 1].first)
+            ++k;
+        const Tensor &t = p.t[k];
+        const long long block = b - t.first, e0 = block * kBlock;
+        const bool vec = t.vec && e0 + kBlock <= t.count;
+        // lane's elements: 8 neighbours, or (without 16-byte accesses) every 32nd
+        const long long at = vec ? e0 + lane * 8 : e0 + lane;
+        const int stride = vec ? 1 : 32;
+        const int n = vec ? 8 : static_cast<int>(min(8ll, (t.count - at + 31) / 32));   // (<= 0: none)
+        const float *w_from = p.has_master ? t.master : nullptr;
+        float w[8], g[8], m[8], v[8];
+        float old_ms = 0.0f, old_vs = 0.0f;
+        if (BITS == 8) {
+            old_ms = __ldcg(t.m_scale + block);
+            old_vs = __ldcg(t.v_scale + block);
+        }
+        if (vec) {
+            Eight rw, rg, rm, rv;
+            load8(rw, p.has_master ? static_cast<const void *>(w_from) : t.param, p.has_master ? fp8rows::kF32 : p.param_type, at);
+            load8(rg, t.grad, p.grad_type, at);
+            if constexpr (BITS == 32) {
+                load8(rm, t.m, fp8rows::kF32, at);
+                load8(rv, t.v, fp8rows::kF32, at);
+            } else {
+                const uint2 a = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(t.m) + at));
+                const uint2 c = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(t.v) + at));
+                rm.w[0] = a.x; rm.w[1] = a.y;
+                rv.w[0] = c.x; rv.w[1] = c.y;
+            }
+            floats8(rw, p.has_master ? fp8rows::kF32 : p.param_type, w);
+            floats8(rg, p.grad_type, g);
+            if constexpr (BITS == 32) {
+                floats8(rm, fp8rows::kF32, m);
+                floats8(rv, fp8rows::kF32, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 x = decode2(rm.w[i / 2] >> (16 * (i % 2))), y = decode2(rv.w[i / 2] >> (16 * (i % 2)));
+                    m[2 * i] = x.x;
+                    m[2 * i + 1] = x.y;
+                    v[2 * i] = y.x;
+                    v[2 * i + 1] = y.y;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const long long e = at + 32 * i;
+                const bool in = i < n;
+                w[i] = in ? (p.has_master ? w_from[e] : load1(t.param, p.param_type, e)) : 0.0f;
+                g[i] = in ? load1(t.grad, p.grad_type, e) : 0.0f;
+                m[i] = !in ? 0.0f : BITS == 32 ? static_cast<const float *>(t.m)[e] : decode1(static_cast<const uint8_t *>(t.m)[e]);
+                v[i] = !in ? 0.0f : BITS == 32 ? static_cast<const float *>(t.v)[e] : decode1(static_cast<const uint8_t *>(t.v)[e]);
+            }
+        }
+        float r[8];
+        float most_m = 0.0f, most_r = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (p.h.grad_scale)
+                g[i] = __fmul_rn(g[i], gs);
+            if constexpr (BITS == 8) {
+                m[i] = __fmul_rn(m[i], old_ms);
+                v[i] = __fmul_rn(v[i], old_vs);
+                v[i] = __fmul_rn(v[i], v[i]);
+            }
+            m[i] = __fadd_rn(__fmul_rn(m[i], p.h.b1), __fmul_rn(g[i], p.h.b1c));
+            v[i] = __fadd_rn(__fmul_rn(v[i], p.h.b2), __fmul_rn(__fmul_rn(g[i], g[i]), p.h.b2c));
+            if (!vec && i >= n) {
+                m[i] = 0.0f;           // (behind the tensor's end: a NaN scale's 0 x NaN)
+                v[i] = 0.0f;
+            }
+            r[i] = __fsqrt_rn(v[i]);
+            w[i] = __fsub_rn(__fmul_rn(w[i], keep),
+                             __fmul_rn(__fdiv_rn(m[i], __fadd_rn(__fmul_rn(r[i], root), p.h.eps)), step_size));
+            if constexpr (BITS == 8) {
+                most_m = fp8mm::max_nan(most_m, fabsf(m[i]));
+                most_r = fp8mm::max_nan(most_r, r[i]);
+            }
+        }
+        if constexpr (BITS == 8) {
+            const float ms = __fdiv_rn(warp_max(most_m), 448.0f), vs = __fdiv_rn(warp_max(most_r), 448.0f);
+            const fp8q::Divider dm = fp8q::make_divider(ms), dv = fp8q::make_divider(vs);
+            if (lane == 0) {
+                t.m_scale[block] = ms;
+                t.v_scale[block] = vs;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                m[i] = quotient(dm, m[i]);
+                v[i] = round_by(quotient(dv, r[i]), dither(static_cast<uint32_t>(at + stride * i), step));
+            }
+        }
+        if (vec) {
+            if (p.has_master)
+                store8(t.master, fp8rows::kF32, at, w);
+            store8(t.param, p.param_type, at, w);
+            if constexpr (BITS == 32) {
+                store8(t.m, fp8rows::kF32, at, m);
+                store8(t.v, fp8rows::kF32, at, v);
+            } else {
+                uint32_t cm[4], cv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    cm[i] = fp8q::cvt_pair(m[2 * i], m[2 * i + 1], 0);
+                    cv[i] = fp8q::cvt_pair(v[2 * i], v[2 * i + 1], 0);
+                }
+                __stcs(reinterpret_cast<uint2 *>(static_cast<uint8_t *>(t.m) + at), make_uint2(cm[0] | cm[1] << 16, cm[2] | cm[3] << 16));
+                __stcs(reinterpret_cast<uint2 *>(static_cast<uint8_t *>(t.v) + at), make_uint2(cv[0] | cv[1] << 16, cv[2] | cv[3] << 16));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const long long e = at + 32 * i;
+                if (i >= n)
+                    break;
+                const float one[1] = {w[i]};
+                if (p.has_master)
+                    t.master[e] = w[i];
+                fp8rows::store_group<1>(t.param, p.param_type, e, one);
+                if constexpr (BITS == 32) {
+                    static_cast<float *>(t.m)[e] = m[i];
+                    static_cast<float *>(t.v)[e] = v[i];
+                } else {
+                    static_cast<uint8_t *>(t.m)[e] = static_cast<uint8_t>(fp8q::cvt_pair(m[i], 0.0f, 0));
+                    static_cast<uint8_t *>(t.v)[e] = static_cast<uint8_t>(fp8q::cvt_pair(v[i], 0.0f, 0));
+                }
+            }
+        }
+    }
+}
+
+}  // namespace fp8adam

@@ -1553,6 +1553,29 @@ int device_limit(int **status, unsigned long long *clocks)
     return rc;
 }
 
+int encode_tiles(CUtensorMap *map, CUtensorMapDataType type, const void *base, const int64_t (&dims)[3],
+                 const int64_t (&strides)[2], const int (&box)[3])
+{
+    cuuint64_t d[3], st[2];
+    cuuint32_t b[3], estr[3] = {1, 1, 1};
+    for (int i = 0; i < 3; ++i) {
+        d[i] = static_cast<cuuint64_t>(dims[i]);
+        b[i] = static_cast<cuuint32_t>(box[i]);
+        if (i < 2)
+            st[i] = static_cast<cuuint64_t>(strides[i]);
+    }
+    const CUresult r = encode_map(map, type, 3, const_cast<void *>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS)
+        return FP8MM_OK;
+    char buf[160];
+    snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled failed (%d) rows=%lld cols=%lld", static_cast<int>(r),
+             static_cast<long long>(dims[1]), static_cast<long long>(dims[0]));
+    t_last_error = buf;
+    return FP8MM_ERR_CUDA;
+}
+
 }  // namespace fp8mm_host
 
 extern "C" {

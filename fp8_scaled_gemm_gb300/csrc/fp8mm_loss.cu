@@ -1,0 +1,407 @@
+// fp8mm_loss.cu -- C entries of softmax cross entropy over an FP8 product and
+// of its gradients.
+#include "fp8mm_loss.cuh"
+#include "fp8mm_rows_host.h"
+
+namespace {
+
+using namespace fp8mm_host;
+using namespace fp8loss;
+
+constexpr int64_t kPieceBytes = int64_t(1) << 30;   // of dz, and of the piece of B in fp16
+
+int64_t aligned(int64_t bytes) { return cdiv(bytes, 256) * 256; }
+
+int check_problem(const void *A, const void *B, const float *sa, const float *sb, int scale_mode, int a_type, int b_type,
+                  const void *bias, int bias_type, const int64_t *target, int64_t M, int64_t N, int64_t K)
+{
+    if ((scale_mode != FP8MM_SCALE_TENSOR && scale_mode != FP8MM_SCALE_ROWWISE) ||
+        (a_type != FP8MM_TYPE_E4M3 && a_type != FP8MM_TYPE_E5M2) ||
+        (b_type != FP8MM_TYPE_E4M3 && b_type != FP8MM_TYPE_E5M2) || !row_type_known(bias_type))
+        return FP8MM_ERR_MODE;
+    if (M < 0 || N < 1 || M > INT32_MAX || N > INT32_MAX || K < 16 || K % 16 != 0 || K > (int64_t(1) << 24))
+        return FP8MM_ERR_SHAPE;
+    // tiles of 256 x 256 and their K slices are counted in int
+    if (cdiv(M, kTile) * cdiv(N, kTile) > (int64_t(1) << 24) || M > (int64_t(1) << 40) / N)
+        return FP8MM_ERR_SHAPE;
+    if (M == 0)
+        return FP8MM_OK;
+    if (!A || !B || !sa || !sb || !target)
+        return FP8MM_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(A) & 15) || (reinterpret_cast<uintptr_t>(B) & 15) ||
+        (reinterpret_cast<uintptr_t>(sa) & 3) || (reinterpret_cast<uintptr_t>(sb) & 3) ||
+        (reinterpret_cast<uintptr_t>(bias) & (row_type_bytes(bias_type) - 1)) || (reinterpret_cast<uintptr_t>(target) & 7))
+        return FP8MM_ERR_ALIGN;
+    return FP8MM_OK;
+}
+
+// A matrix of `rows` x `cols` elements, rows `ld` elements apart, `items` of
+// them `item` elements apart, in boxes of box_rows rows x 128 bytes.
+int map_matrix(CUtensorMap *map, CUtensorMapDataType type, int es, const void *base, int64_t rows, int64_t cols, int64_t ld,
+               int box_rows, int64_t items = 1, int64_t item = 0)
+{
+    const int64_t dims[3] = {cols, rows, items};
+    const int64_t strides[2] = {ld * es, (item ? item : ld * rows) * es};
+    const int box[3] = {128 / es, box_rows, 1};
+    return encode_tiles(map, type, base, dims, strides, box);
+}
+
+// Column of the instruction descriptor's formats.
+uint32_t formats(int a_type, int b_type)
+{
+    return (a_type == FP8MM_TYPE_E5M2 ? 1u << 7 : 0u) | (b_type == FP8MM_TYPE_E5M2 ? 1u << 10 : 0u);
+}
+
+// Fills the tile space of a launch.
+void tile_space(LossParams &p, int64_t rows, int64_t cols, int64_t kblocks, int splits)
+{
+    p.rows = static_cast<int>(rows);
+    p.cols = static_cast<int>(cols);
+    p.kblocks = static_cast<int>(kblocks);
+    p.tiles_p = static_cast<int>(cdiv(rows, kTile));
+    p.tiles_q = static_cast<int>(cdiv(cols, kTile));
+    p.group = std::min(p.tiles_p, 16);
+    p.splits = splits;
+    p.num_units = p.tiles_p * p.tiles_q * splits;
+}
+
+template <int KIND>
+int launch_tiles(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, LossParams &p, int sms,
+                 cudaStream_t stream)
+{
+    auto kern = loss_kernel<KIND>;
+    static bool attr_set[kMaxDevices] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!attr_set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<KIND>::kSmemBytes);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "cudaFuncSetAttribute");
+        attr_set[dev] = true;
+    }
+    const int rc = device_limit(&p.status, &p.timeout_cycles);
+    if (rc != FP8MM_OK)
+        return rc;
+    return launch_pdl(kern, 2 * std::min(sms / 2, p.num_units), kThreads, Cfg<KIND>::kSmemBytes, stream,
+                      "cross entropy launch", ma, mb, mo, p);
+}
+
+// K slices of a gradient product: as many as give every CTA pair a tile, each
+// with at least 8 blocks of 64.
+int slices(int64_t rows, int64_t cols, int64_t contraction, int sms)
+{
+    const int64_t tiles = cdiv(rows, kTile) * cdiv(cols, kTile);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / 2 / tiles, cdiv(contraction, 64) / 8)));
+}
+
+// How a gradient call goes through the vocabulary, and where its workspace's
+// parts are.
+struct GradPlan {
+    int64_t piece, pieces;                       // columns of a piece (a multiple of 256, or all), how many
+    int split_a, split_b;
+    bool parts_a, parts_b;                       // results pass through fp32 partials
+    int64_t norms, h16, w16, dz, colsum, parts_a_at, parts_b_at, bytes;
+};
+
+GradPlan plan_grad(int64_t M, int64_t N, int64_t K, bool da, bool db, bool dbias, int sms)
+{
+    GradPlan g{};
+    const int64_t most = std::max<int64_t>(2048, kPieceBytes / 2 / std::max(M, K) / kTile * kTile);
+    g.pieces = cdiv(N, most);
+    g.piece = cdiv(cdiv(N, g.pieces), kTile) * kTile;
+    g.pieces = cdiv(N, g.piece);
+    g.split_a = slices(M, K, std::min(N, g.piece), sms);
+    g.split_b = slices(std::min(N, g.piece), K, M, sms);
+    g.parts_a = da && (g.split_a > 1 || g.pieces > 1);
+    g.parts_b = db && g.split_b > 1;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += aligned(bytes);
+        return here;
+    };
+    g.norms = take(3 * kNormParts * 4);
+    g.dz = take(M * g.piece * 2);
+    g.h16 = take(db ? M * K * 2 : 0);
+    g.w16 = take(da ? g.piece * K * 2 : 0);
+    g.colsum = take(dbias ? cdiv(M, 32) * g.piece * 4 : 0);
+    g.parts_a_at = take(g.parts_a ? g.split_a * M * K * 4 : 0);
+    g.parts_b_at = take(g.parts_b ? g.split_b * g.piece * K * 4 : 0);
+    g.bytes = at;
+    return g;
+}
+
+int64_t stats_bytes(int64_t M, int64_t N) { return aligned(cdiv(N, kHalf) * M * 8); }
+
+int zero(void *p, int64_t bytes, cudaStream_t s)
+{
+    const cudaError_t e = p ? cudaMemsetAsync(p, 0, static_cast<size_t>(bytes), s) : cudaSuccess;
+    return e == cudaSuccess ? FP8MM_OK : cuda_fail(e, "cudaMemsetAsync(gradient)");
+}
+
+int expand(const void *codes, const float *scale, int rowwise, int type, int norm_of, const uint32_t *norms, void *out,
+           int64_t rows, int64_t K, int sms, cudaStream_t s)
+{
+    ExpandParams e{};
+    e.codes = static_cast<const uint8_t *>(codes);
+    e.scale = scale;
+    e.rowwise = rowwise;
+    e.type = type;
+    e.norm_of = norm_of;
+    e.norms = norms;
+    e.out = static_cast<__half *>(out);
+    e.groups = rows * (K / 16);
+    e.row_groups = static_cast<int>(K / 16);
+    return launch_grid2(expand_kernel, std::min<int64_t>(cdiv(e.groups, kExpandThreads), static_cast<int64_t>(sms) * 8), 1,
+                        kExpandThreads, s, "fp16 operand launch", e);
+}
+
+int finish(const void *parts, int64_t n, int count, int out_type, int norm_of, const uint32_t *norms, float factor,
+           void *out, int sms, cudaStream_t s)
+{
+    FinishParams f{};
+    f.parts = static_cast<const float *>(parts);
+    f.n = n;
+    f.count = count;
+    f.out_type = out_type;
+    f.norm_of = norm_of;
+    f.norms = norms;
+    f.factor = factor;
+    f.out = out;
+    return launch_grid2(finish_kernel, std::min<int64_t>(cdiv(n / 4, kFinishThreads), static_cast<int64_t>(sms) * 8), 1,
+                        kFinishThreads, s, "gradient sum launch", f);
+}
+
+constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, kF16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                              kF32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32, kB16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+
+}  // namespace
+
+extern "C" {
+
+int64_t fp8_cross_entropy_workspace(int64_t M, int64_t N)
+{
+    if (M < 0 || N < 1 || M > INT32_MAX || N > INT32_MAX || M > (int64_t(1) << 40) / N)
+        return FP8MM_ERR_SHAPE;
+    return M == 0 ? 0 : stats_bytes(M, N) + aligned(M * 4);
+}
+
+int fp8_cross_entropy(const void *A, int a_type, const void *B, int b_type, const float *scale_a, const float *scale_b,
+                      int scale_mode, const void *bias, int bias_type, const int64_t *target, int64_t ignore_index,
+                      float *loss, float *lse, int64_t M, int64_t N, int64_t K, void *workspace, int64_t workspace_bytes,
+                      void *stream)
+{
+    int rc = check_problem(A, B, scale_a, scale_b, scale_mode, a_type, b_type, bias, bias_type, target, M, N, K);
+    if (rc != FP8MM_OK || M == 0)
+        return rc;
+    if (!loss || !lse || !workspace)
+        return FP8MM_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(loss) & 3) || (reinterpret_cast<uintptr_t>(lse) & 3) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 15))
+        return FP8MM_ERR_ALIGN;
+    if (workspace_bytes < fp8_cross_entropy_workspace(M, N))
+        return FP8MM_ERR_SHAPE;
+    int sms = 0;
+    if ((rc = device_sms(&sms)) != FP8MM_OK)
+        return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    LossParams p{};
+    tile_space(p, M, N, cdiv(K, 128), 1);
+    p.idesc = fp8mm::ptx::idesc_e4m3_f32(kTile, kTile) | formats(a_type, b_type);
+    p.scale_a = scale_a;
+    p.scale_b = scale_b;
+    p.rowwise = scale_mode == FP8MM_SCALE_ROWWISE;
+    p.bias = bias;
+    p.bias_type = bias_type;
+    p.target = target;
+    p.ignore = ignore_index;
+    p.vocabulary = N;
+    p.stats = static_cast<float2 *>(workspace);
+    p.target_z = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + stats_bytes(M, N));
+    CUtensorMap ma, mb;
+    if ((rc = map_matrix(&ma, kU8, 1, A, M, K, K, 128)) != FP8MM_OK ||
+        (rc = map_matrix(&mb, kU8, 1, B, N, K, K, 128)) != FP8MM_OK)
+        return rc;
+    if ((rc = launch_tiles<kStats>(ma, mb, ma, p, sms, s)) != FP8MM_OK)
+        return rc;
+    CombineParams c{};
+    c.stats = p.stats;
+    c.target_z = p.target_z;
+    c.target = target;
+    c.ignore = ignore_index;
+    c.vocabulary = N;
+    c.loss = loss;
+    c.lse = lse;
+    c.rows = static_cast<int>(M);
+    c.parts = static_cast<int>(cdiv(N, kHalf));
+    return launch_grid2(combine_kernel, cdiv(M, 32), 1, kCombineThreads, s, "cross entropy sum launch", c);
+}
+
+int64_t fp8_cross_entropy_grad_workspace(int64_t M, int64_t N, int64_t K, int want_da, int want_db, int want_dbias)
+{
+    if (M < 0 || N < 1 || M > INT32_MAX || N > INT32_MAX || K < 16 || K % 16 != 0 || K > (int64_t(1) << 24) ||
+        cdiv(M, kTile) * cdiv(N, kTile) > (int64_t(1) << 24) || M > (int64_t(1) << 40) / N)
+        return FP8MM_ERR_SHAPE;
+    if (M == 0 || !(want_da || want_db || want_dbias))
+        return 0;
+    int sms = 0;
+    const int rc = device_sms(&sms);
+    if (rc != FP8MM_OK)
+        return rc;
+    return plan_grad(M, N, K, want_da != 0, want_db != 0, want_dbias != 0, sms).bytes;
+}
+
+int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type, const float *scale_a,
+                           const float *scale_b, int scale_mode, const void *bias, int bias_type, const int64_t *target,
+                           int64_t ignore_index, const float *lse, const float *dloss, int64_t dloss_count, void *da,
+                           void *db, int out_type, float *dbias, int64_t M, int64_t N, int64_t K, void *workspace,
+                           int64_t workspace_bytes, void *stream)
+{
+    int rc = check_problem(A, B, scale_a, scale_b, scale_mode, a_type, b_type, bias, bias_type, target, M, N, K);
+    if (rc != FP8MM_OK)
+        return rc;
+    if (!row_type_known(out_type))
+        return FP8MM_ERR_MODE;
+    if (dloss_count != 1 && dloss_count != M)
+        return FP8MM_ERR_SHAPE;
+    if ((reinterpret_cast<uintptr_t>(lse) & 3) || (reinterpret_cast<uintptr_t>(dloss) & 3) ||
+        (reinterpret_cast<uintptr_t>(dbias) & 3) || (reinterpret_cast<uintptr_t>(da) & 15) ||
+        (reinterpret_cast<uintptr_t>(db) & 15) || (reinterpret_cast<uintptr_t>(workspace) & 15))
+        return FP8MM_ERR_ALIGN;
+    if (!da && !db && !dbias)
+        return FP8MM_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int sms = 0;
+    const int es = static_cast<int>(row_type_bytes(out_type));
+    if (M == 0) {
+        // sums over no rows
+        if ((rc = device_sms(&sms)) != FP8MM_OK || (rc = zero(db, N * K * es, s)) != FP8MM_OK)
+            return rc;
+        return zero(dbias, N * 4, s);
+    }
+    if (!lse || !dloss || !workspace)
+        return FP8MM_ERR_NULL;
+    if ((rc = device_sms(&sms)) != FP8MM_OK)
+        return rc;
+    const GradPlan g = plan_grad(M, N, K, da != nullptr, db != nullptr, dbias != nullptr, sms);
+    if (workspace_bytes < g.bytes)
+        return FP8MM_ERR_SHAPE;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    uint32_t *norms = reinterpret_cast<uint32_t *>(ws + g.norms);
+    const int rowwise = scale_mode == FP8MM_SCALE_ROWWISE;
+    const CUtensorMapDataType out_map = out_type == FP8MM_OUT_F32 ? kF32 : out_type == FP8MM_OUT_F16 ? kF16 : kB16;
+    const int out_box = 32;
+    // what comes off dz W16 and dz^T H16 beside the norms
+    const float factor_a = 1.0f / (kSlopeScale * code_scale(b_type)), factor_b = 1.0f / (kSlopeScale * code_scale(a_type));
+
+    NormsParams n{};
+    n.dloss = dloss;
+    n.dloss_step = dloss_count == 1 ? 0 : 1;
+    n.scale_b = scale_b;
+    n.scale_a = scale_a;
+    n.target = target;
+    n.ignore = ignore_index;
+    n.M = M;
+    n.count[kNormG] = dloss_count;
+    n.count[kNormB] = rowwise ? N : 1;
+    n.count[kNormA] = rowwise ? M : 1;
+    n.out = norms;
+    if ((rc = launch_grid2(norms_kernel, kNormParts, 3, kNormThreads, s, "cross entropy norms launch", n)) != FP8MM_OK)
+        return rc;
+    if (db && (rc = expand(A, scale_a, rowwise, a_type, kNormA, norms, ws + g.h16, M, K, sms, s)) != FP8MM_OK)
+        return rc;
+
+    CUtensorMap ma, mh, parts_a;
+    if ((rc = map_matrix(&ma, kU8, 1, A, M, K, K, 128)) != FP8MM_OK ||
+        (db && (rc = map_matrix(&mh, kF16, 2, ws + g.h16, M, K, K, 64)) != FP8MM_OK))
+        return rc;
+    if (da) {
+        rc = g.parts_a ? map_matrix(&parts_a, kF32, 4, ws + g.parts_a_at, M, K, K, out_box, g.split_a)
+                       : map_matrix(&parts_a, out_map, es, da, M, K, K, out_box);
+        if (rc != FP8MM_OK)
+            return rc;
+    }
+    for (int64_t i = 0; i < g.pieces; ++i) {
+        const int64_t n0 = i * g.piece, nv = std::min(g.piece, N - n0);
+        const uint8_t *Bi = static_cast<const uint8_t *>(B) + n0 * K;
+        const float *sbi = scale_b + (rowwise ? n0 : 0);
+        CUtensorMap mb, mdz;
+        LossParams p{};
+        tile_space(p, M, nv, cdiv(K, 128), 1);
+        p.idesc = fp8mm::ptx::idesc_e4m3_f32(kTile, kTile) | formats(a_type, b_type);
+        p.scale_a = scale_a;
+        p.scale_b = sbi;
+        p.rowwise = rowwise;
+        p.bias = bias ? static_cast<const uint8_t *>(bias) + n0 * row_type_bytes(bias_type) : nullptr;
+        p.bias_type = bias_type;
+        p.target = target;
+        p.ignore = ignore_index;
+        p.col0 = n0;
+        p.vocabulary = N;
+        p.lse = lse;
+        p.dloss = dloss;
+        p.dloss_step = n.dloss_step;
+        p.colsum = dbias ? reinterpret_cast<float *>(ws + g.colsum) : nullptr;
+        p.colsum_ld = g.piece;
+        p.norms = norms;
+        // dz [M, nv] with rows of `piece` elements, written in blocks of 32 x 64
+        if ((rc = map_matrix(&mb, kU8, 1, Bi, nv, K, K, 128)) != FP8MM_OK ||
+            (rc = map_matrix(&mdz, kF16, 2, ws + g.dz, M, nv, g.piece, out_box)) != FP8MM_OK ||
+            (rc = launch_tiles<kSlope>(ma, mb, mdz, p, sms, s)) != FP8MM_OK)
+            return rc;
+        if (dbias) {
+            ColumnsParams c{};
+            c.parts = p.colsum;
+            c.ld = g.piece;
+            c.cols = static_cast<int>(nv);
+            c.count = static_cast<int>(cdiv(M, 32));
+            c.norms = norms;
+            c.out = dbias + n0;
+            if ((rc = launch_grid2(columns_kernel, cdiv(nv, 32), 1, kColumnsThreads, s, "bias gradient sum launch", c)) != FP8MM_OK)
+                return rc;
+        }
+        LossParams o{};
+        o.norms = norms;
+        if (da) {
+            CUtensorMap mz, mw;
+            if ((rc = expand(Bi, sbi, rowwise, b_type, kNormB, norms, ws + g.w16, nv, K, sms, s)) != FP8MM_OK ||
+                (rc = map_matrix(&mz, kF16, 2, ws + g.dz, M, nv, g.piece, 128)) != FP8MM_OK ||
+                (rc = map_matrix(&mw, kF16, 2, ws + g.w16, nv, K, K, 64)) != FP8MM_OK)
+                return rc;
+            // (a last piece with fewer blocks than slices adds to the first partials only)
+            tile_space(o, M, K, cdiv(nv, 64), static_cast<int>(std::min<int64_t>(g.split_a, cdiv(nv, 64))));
+            o.idesc = fp8mm::ptx::idesc_f16_f32(kTile, kTile, false, true);
+            o.norms = g.parts_a ? nullptr : norms;
+            o.factor = factor_a;
+            o.norm_of = kNormB;
+            o.out_type = g.parts_a ? FP8MM_OUT_F32 : out_type;
+            o.add = i > 0;
+            if ((rc = launch_tiles<kGradA>(mz, mw, parts_a, o, sms, s)) != FP8MM_OK)
+                return rc;
+        }
+        if (db) {
+            uint8_t *dbi = static_cast<uint8_t *>(db) + n0 * K * es;
+            CUtensorMap mz, mo;
+            rc = g.parts_b ? map_matrix(&mo, kF32, 4, ws + g.parts_b_at, nv, K, K, out_box, g.split_b)
+                           : map_matrix(&mo, out_map, es, dbi, nv, K, K, out_box);
+            if (rc != FP8MM_OK || (rc = map_matrix(&mz, kF16, 2, ws + g.dz, M, nv, g.piece, 64)) != FP8MM_OK)
+                return rc;
+            tile_space(o, nv, K, cdiv(M, 64), g.split_b);
+            o.idesc = fp8mm::ptx::idesc_f16_f32(kTile, kTile, true, true);
+            o.norms = g.parts_b ? nullptr : norms;
+            o.factor = factor_b;
+            o.norm_of = kNormA;
+            o.out_type = g.parts_b ? FP8MM_OUT_F32 : out_type;
+            o.add = 0;
+            if ((rc = launch_tiles<kGradB>(mz, mh, mo, o, sms, s)) != FP8MM_OK)
+                return rc;
+            if (g.parts_b && (rc = finish(ws + g.parts_b_at, nv * K, g.split_b, out_type, kNormA, norms, factor_b, dbi, sms, s)) != FP8MM_OK)
+                return rc;
+        }
+    }
+    if (g.parts_a)
+        return finish(ws + g.parts_a_at, M * K, g.split_a, out_type, kNormB, norms, factor_a, da, sms, s);
+    return FP8MM_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,740 @@
+// fp8mm_loss.cuh -- softmax cross entropy over the columns of an FP8 product,
+// and its gradients, without the product ever being in memory.
+//
+//   z[m, n] = acc[m, n] (s_a[m] s_b[n]) + bias[n]
+//   lse[m]  = log sum_n exp z[m, n]
+//   loss[m] = lse[m] - z[m, t[m]]
+//   dz[m, n] = (exp(z[m, n] - lse[m]) - [n = t[m]]) g[m]
+//   dA = dz (s_b B)^T,   dB^T = dz^T (s_a A),   dbias = sum_m dz
+//
+// One kernel in four kinds, all with 2-SM MMAs on 256 x 256 tiles (a cluster of
+// two CTAs; roles, ring and barriers as in fp8mm_kernel_pair.cuh):
+//
+//   kStats  the product z of fp8 operands. Each epilogue warp reduces its 32
+//           rows x 128 columns to (max, sum of exp(z - max)) per row and writes
+//           those 8 bytes; the warp that meets a row's target writes its z.
+//           combine_kernel joins the pairs of a row in a fixed order.
+//   kSlope  the same product again for a piece of the vocabulary; the epilogue
+//           writes dz as fp16 (and sums of it over 32 rows for dbias).
+//   kGradA  dA = dz W16: the contraction runs over the vocabulary. dz is read
+//           K-major, W16 [n, K] (the piece of B in fp16) MN-major.
+//   kGradB  dB^T = dz^T H16 over the rows; both operands MN-major.
+//
+// Recomputing z costs 2 M N K flops at the fp8 rate; keeping it would cost
+// 2 to 4 bytes of memory per logit, written and read (M = 8192, N = 131072:
+// 2 GB and more), which the pieces bound instead. The gradients' products run on 16-bit
+// operands: fp8 codes of dz would leave 2 to 3 significant bits.
+//
+// dz in fp16: 11 significant bits against bf16's 8, one rounding of at most
+// 2^-12 relative per element of a long sum. Its narrow range is met by powers
+// of two: |dz| <= |g| is known before anything is computed, so rows are scaled
+// by 2^14 / G with G the largest |g|'s power of two; probabilities down to
+// 2^-28 keep all 11 bits, smaller ones are held to 2^-38 of the largest |g|.
+// W16 = code s_b and H16 = code s_a are scaled the same way by the largest
+// scale, so one dz serves both products; their fp16 rounding is 2^-12 again.
+// All scales are powers of two and come off, exactly, in fp32.
+#pragma once
+
+#include "fp8mm_kernel.cuh"
+#include "fp8mm_rows.cuh"
+
+namespace fp8loss {
+
+namespace ptx = fp8mm::ptx;
+using fp8mm::Waiter;
+
+enum Kind { kStats, kSlope, kGradA, kGradB };
+
+constexpr int kTile = 256;             // rows and columns of a CTA pair's tile
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kHalf = 128;             // columns of one epilogue warp
+constexpr int kNormParts = 32;         // partial maxima per norm
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int KIND>
+struct Cfg {
+    static constexpr bool kFp8 = KIND == kStats || KIND == kSlope;
+    static constexpr bool kAMn = KIND == kGradB, kBMn = !kFp8;
+    static constexpr int kABytes = 128 * 128;
+    static constexpr int kStageBytes = 2 * kABytes;                            // 128 rows of A, 128 of B
+    static constexpr int kStages = KIND == kSlope ? 5 : 6;
+    static constexpr int kStagingBytes = KIND == kStats ? 0 : kEpiWarps * 4096;   // one block of output per warp
+    static constexpr int kColBytes = kFp8 ? kEpiWarps * kHalf * 8 : 0;         // (scale, bias) per column and warp
+    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + kColBytes + 256;
+    static_assert(kSmemBytes <= 232448, "exceeds 227 KB of shared memory");
+};
+
+struct LossParams {
+    int rows, cols;                    // of the tile space: M x N (fp8 kinds), M x K (dA), n x K (dB)
+    int kblocks;                       // of 128 bytes of contraction
+    int tiles_p, tiles_q, group, splits, num_units;
+    uint32_t idesc;
+    int *status;
+    unsigned long long timeout_cycles;
+    // fp8 kinds (column vectors start at the piece)
+    const float *scale_a, *scale_b;
+    int rowwise;
+    const void *bias;
+    int bias_type;
+    const int64_t *target;
+    long long ignore, col0;            // col0: the piece's first column in the vocabulary
+    long long vocabulary;
+    // kStats
+    float2 *stats;                     // [ceil(N / 128)][M]
+    float *target_z;                   // [M]
+    // kSlope
+    const float *lse, *dloss;
+    int dloss_step;                    // 0: one value for all rows
+    float *colsum;                     // [ceil(M / 32)][n], or nullptr
+    long long colsum_ld;
+    // kSlope, kGradA, kGradB
+    const uint32_t *norms;             // see norm_scale
+    float factor;                      // of the result, beside the norms
+    int norm_of;                       // kGradA: kNormB, kGradB: kNormA
+    int out_type;
+    int add;                           // add to the output (fp32)
+};
+
+// ------------------------------------------------------------------ norms ---
+// Largest magnitudes of g (rows that have a target), s_b and s_a, as bit
+// patterns (which order like the magnitudes, NaN above everything), in
+// kNormParts partial maxima each.
+
+constexpr int kNormG = 0, kNormB = 1, kNormA = 2;
+
+struct NormsParams {
+    const float *dloss, *scale_b, *scale_a;
+    const int64_t *target;
+    long long ignore;
+    long long M;                       // rows of target
+    long long count[3];
+    int dloss_step;
+    uint32_t *out;                     // [3][kNormParts]
+};
+
+constexpr int kNormThreads = 256;
+
+static __global__ void __launch_bounds__(kNormThreads) norms_kernel(const NormsParams p)
+{
+    __shared__ uint32_t part[kNormThreads / 32];
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const int which = blockIdx.y;
+    const float *src = which == kNormG ? p.dloss : which == kNormB ? p.scale_b : p.scale_a;
+    uint32_t most = 0;
+    for (long long i = blockIdx.x * kNormThreads + threadIdx.x; i < p.count[which]; i += kNormThreads * kNormParts) {
+        if (which == kNormG && p.dloss_step && __ldg(p.target + i) == p.ignore)
+            continue;
+        most = max(most, __float_as_uint(__ldg(src + i)) & 0x7FFFFFFFu);
+    }
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    if ((threadIdx.x & 31) == 0)
+        part[threadIdx.x >> 5] = most;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kNormThreads / 32; ++w)
+            most = max(most, part[w]);
+        p.out[which * kNormParts + blockIdx.x] = most;
+    }
+}
+
+// The power of two at or below the largest magnitude (at least 2^-100, so that
+// its reciprocal is finite; infinite for an infinity or NaN, whose results are
+// then NaN). Every lane of a warp calls it.
+__device__ __forceinline__ float norm_scale(const uint32_t *norms, int which)
+{
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __ldcg(norms + which * kNormParts + (threadIdx.x & 31)));
+    return fmaxf(__uint_as_float(m & 0x7F800000u), 0x1p-100f);
+}
+
+constexpr float kSlopeScale = 0x1p14f;                // dz / G in (-2, 2): below fp16's 65504
+
+// Of the codes: below 2 x 448 x 2^6 and 2 x 57344 / 2.
+__host__ __device__ constexpr float code_scale(int fp8_type) { return fp8_type == 0 ? 0x1p6f : 0x1p-1f; }
+
+// ----------------------------------------------------- fp8 codes to fp16 ---
+// out[r, :] = fp16( code[r, :] s[r] f / S ): 16 codes a thread.
+
+struct ExpandParams {
+    const uint8_t *codes;
+    const float *scale;
+    int rowwise, type, norm_of;
+    const uint32_t *norms;
+    __half *out;
+    long long groups;                  // rows x K / 16
+    int row_groups;                    // K / 16
+};
+
+constexpr int kExpandThreads = 256;
+
+static __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const ExpandParams p)
+{
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const float f = code_scale(p.type) / norm_scale(p.norms, p.norm_of);
+    const long long step = static_cast<long long>(gridDim.x) * kExpandThreads;
+    for (long long i = static_cast<long long>(blockIdx.x) * kExpandThreads + threadIdx.x; i < p.groups; i += step) {
+        const uint4 in = __ldcg(reinterpret_cast<const uint4 *>(p.codes) + i);
+        const float s = __ldg(p.scale + (p.rowwise ? i / p.row_groups : 0)) * f;
+        uint32_t w[4] = {in.x, in.y, in.z, in.w}, o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint16_t two = static_cast<uint16_t>(w[k / 2] >> (16 * (k % 2)));
+            uint32_t h;
+            if (p.type == 0)
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+            else
+                asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(two));
+            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            o[k] = fp8rows::pack2(v.x * s, v.y * s, fp8rows::kF16);
+        }
+        uint4 *to = reinterpret_cast<uint4 *>(p.out) + 2 * i;
+        to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+}
+
+// ----------------------------------------------------------- tile kernel ---
+
+struct Work {
+    int tp, tq, split, kb0, kb1;
+};
+
+// Tiles in groups of `group` tile rows that sweep all tile columns, K slices
+// innermost: the operand rows in use at a time stay in L2.
+__device__ __forceinline__ Work decode(int u, const LossParams &p)
+{
+    Work w;
+    w.split = u % p.splits;
+    const int t = u / p.splits;
+    const int in_group = p.group * p.tiles_q;
+    const int first = t / in_group * p.group;
+    const int size = min(p.tiles_p - first, p.group);
+    const int r = t % in_group;
+    w.tp = first + r % size;
+    w.tq = r / size;
+    w.kb0 = static_cast<int>(static_cast<long long>(w.split) * p.kblocks / p.splits);
+    w.kb1 = static_cast<int>(static_cast<long long>(w.split + 1) * p.kblocks / p.splits);
+    return w;
+}
+
+__device__ __forceinline__ float bias_at(const LossParams &p, int n)
+{
+    float v[1];
+    fp8rows::load_param<1>(p.bias, p.bias_type, n, 0.0f, v);
+    return v[0];
+}
+
+// Sums of 32 columns over a warp's 32 rows: v[i] is this lane's row at column
+// i, the result column `lane`'s sum. Each step adds the halves that the other
+// lane keeps, so 31 shuffles serve all columns.
+__device__ __forceinline__ float sum_rows(float (&v)[32], int lane)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+        }
+    }
+    return v[0];
+}
+
+// One warp's block of 32 rows x 128 bytes into its swizzled stage: lane `row`
+// writes 16-byte chunk c at c ^ (row & 7).
+__device__ __forceinline__ void stage_chunk(uint8_t *stage, int lane, int c, uint4 w)
+{
+    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = w;
+}
+
+template <int KIND>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    loss_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                const __grid_constant__ CUtensorMap tmap_out, const LossParams p)
+{
+    using C = Cfg<KIND>;
+    constexpr int S = C::kStages;
+
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t sbase = raw + pad;
+    constexpr int kStagingAt = S * C::kStageBytes, kColsAt = kStagingAt + C::kStagingBytes, kBarsAt = kColsAt + C::kColBytes;
+    const uint32_t bar0 = sbase + kBarsAt;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
+    auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * S + a); };
+    auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * S + 2 + a); };
+    const uint32_t done_bar = bar0 + 8u * (2 * S + 4);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kBarsAt + 8 * (2 * S + 5));
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    static_assert(8 * (2 * S + 6) <= 256, "barrier area");
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(tfull_bar(a), 1);
+            ptx::mbar_init(tempty_bar(a), 2 * kEpiWarps);
+        }
+        ptx::mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tmap_a);
+        ptx::prefetch_tmap(&tmap_b);
+        if constexpr (KIND != kStats)
+            ptx::prefetch_tmap(&tmap_out);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), 2 * kTile);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    // no global memory before this
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+
+    const Waiter W{abort_flag, p.status, p.timeout_cycles};
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer ---
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int issued = 0;
+            bool ok = true;
+            for (int u = pair; ok && u < p.num_units; u += pairs) {
+                const Work w = decode(u, p);
+                const int row = w.tp * kTile + static_cast<int>(rank) * 128, col = w.tq * kTile + static_cast<int>(rank) * 128;
+                for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                    if (!W.wait(empty_bar(stage), phase ^ 1u, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sa = sbase + stage * C::kStageBytes, sb = sa + C::kABytes;
+                    const uint32_t full = ptx::mapa_shared(full_bar(stage), 0);
+                    if (rank == 0)
+                        ptx::mbar_arrive_expect_tx(full_bar(stage), 2u * C::kStageBytes);
+                    const int k = kb * (C::kFp8 ? 128 : 64);
+                    if constexpr (C::kAMn) {
+                        ptx::tma_load_3d_pair(sa, &tmap_a, full, row, k, 0);
+                        ptx::tma_load_3d_pair(sa + 8192, &tmap_a, full, row + 64, k, 0);
+                    } else {
+                        ptx::tma_load_3d_pair(sa, &tmap_a, full, k, row, 0);
+                    }
+                    if constexpr (C::kBMn) {
+                        ptx::tma_load_3d_pair(sb, &tmap_b, full, col, k, 0);
+                        ptx::tma_load_3d_pair(sb + 8192, &tmap_b, full, col + 64, k, 0);
+                    } else {
+                        ptx::tma_load_3d_pair(sb, &tmap_b, full, k, col, 0);
+                    }
+                    ++issued;
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // this CTA's copies land before it may exit (the even CTA sees both
+            // CTAs' bytes; the odd one waits until its stages were consumed)
+            const int n = issued < S ? issued : S;
+            int s = stage;
+            uint32_t ph = phase;
+            for (int i = 0; i < n; ++i) {
+                if (--s < 0) {
+                    s = S - 1;
+                    ph ^= 1u;
+                }
+                if (rank == 0)
+                    W.drain(full_bar(s), ph, 3);
+                else
+                    W.drain(empty_bar(s), ph, 6);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------- pair MMA (even CTA only) ---
+        if (lane == 0 && rank == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            bool ok = true;
+            for (int u = pair; ok && u < p.num_units; u += pairs) {
+                const Work w = decode(u, p);
+                if (!W.wait_cluster(tempty_bar(acc), acc_phase ^ 1u, 1))
+                    break;
+                ptx::tc_fence_after();
+                const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kTile);
+                for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                    if (!W.wait(full_bar(stage), phase, 2)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t sa = sbase + stage * C::kStageBytes, sb = sa + C::kABytes;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t more = (kb > w.kb0 || k > 0) ? 1u : 0u;
+                        const uint64_t da = C::kAMn ? ptx::sw128_mnmajor_desc(sa + k * 2048) : ptx::sw128_kmajor_desc(sa + k * 32);
+                        const uint64_t db = C::kBMn ? ptx::sw128_mnmajor_desc(sb + k * 2048) : ptx::sw128_kmajor_desc(sb + k * 32);
+                        if constexpr (C::kFp8)
+                            ptx::mma_e4m3_pair(d, da, db, p.idesc, more);
+                        else
+                            ptx::mma_f16_pair(d, da, db, p.idesc, more);
+                    }
+                    ptx::mma_commit_pair_multicast(empty_bar(stage), 0x3);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok)
+                    break;
+                ptx::mma_commit_pair_multicast(tfull_bar(acc), 0x3);
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            }
+            ptx::mma_commit_pair_multicast(done_bar, 0x1);
+            W.drain(done_bar, 0, 4);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------- epilogue ---
+        const int q = warp & 3, ew = warp - 2, half = ew / 4;
+        uint8_t *stage = smem + kStagingAt + ew * 4096;
+        const uint32_t stage_smem = sbase + kStagingAt + ew * 4096;
+        float *cols = reinterpret_cast<float *>(smem + kColsAt) + ew * 2 * kHalf;   // (s0, s1, b0, b1) per column pair
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        float row_scale = 1.0f;        // of kSlope's g
+        float out_scale = 1.0f;
+        if constexpr (KIND == kSlope)
+            row_scale = kSlopeScale / norm_scale(p.norms, kNormG);
+        if constexpr (KIND == kGradA || KIND == kGradB)
+            out_scale = p.norms ? p.factor * norm_scale(p.norms, kNormG) * norm_scale(p.norms, p.norm_of) : 1.0f;
+        const float s_tensor = C::kFp8 && !p.rowwise ? __ldg(p.scale_a) * __ldg(p.scale_b) : 1.0f;
+
+        // the stage is free for the next block, and a block in it goes out
+        auto stage_free = [&]() {
+            if (lane == 0)
+                ptx::bulk_wait_group_read<0>();
+            __syncwarp();
+        };
+        auto stage_out = [&](int x, int y, int z) {
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && x < p.cols && y < p.rows) {
+                if (KIND == kGradA && p.add)
+                    ptx::tma_add_3d(&tmap_out, stage_smem, x, y, z);
+                else
+                    ptx::tma_store_3d(&tmap_out, stage_smem, x, y, z);
+                ptx::bulk_commit_group();
+            }
+        };
+
+        for (int u = pair; u < p.num_units; u += pairs) {
+            const Work w = decode(u, p);
+            const int row0 = w.tp * kTile + static_cast<int>(rank) * 128 + q * 32, row = row0 + lane;
+            const int col0 = w.tq * kTile + half * kHalf;
+            const bool in = row < p.rows;
+            float rs = 1.0f, lse = 0.0f, gs = 0.0f;
+            long long at = -1;                       // the target's column in this warp's 128
+            bool live = false;
+            if constexpr (C::kFp8) {
+                // what the tile needs beside the accumulator, while the MMAs run
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < kHalf / 32; ++i) {
+                    const int c = i * 32 + lane, n = col0 + c;
+                    const bool there = n < p.cols;
+                    // columns past the end: z = -inf, which adds nothing
+                    cols[(c >> 1) * 4 + (c & 1)] = there ? (p.rowwise ? __ldg(p.scale_b + n) : s_tensor) : 0.0f;
+                    cols[(c >> 1) * 4 + 2 + (c & 1)] = there ? bias_at(p, n) : -INFINITY;
+                }
+                __syncwarp();
+                if (in) {
+                    if (p.rowwise)
+                        rs = __ldg(p.scale_a + row);
+                    const long long t = __ldg(p.target + row);
+                    live = t != p.ignore;
+                    at = live && t >= 0 && t < p.vocabulary ? t - p.col0 - col0 : -1;
+                    if constexpr (KIND == kSlope) {
+                        lse = __ldg(p.lse + row);
+                        gs = __ldg(p.dloss + static_cast<long long>(row) * p.dloss_step) * row_scale;
+                        if (live && (t < 0 || t >= p.vocabulary))
+                            gs = NAN;
+                    }
+                }
+            }
+            if (!W.wait(tfull_bar(acc), acc_phase, 5))
+                break;
+            ptx::tc_fence_after();
+            const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kTile + half * kHalf);
+
+            if constexpr (C::kFp8) {
+                float top = -INFINITY, sum = 0.0f;
+                const uint64_t rs2 = ptx::f32x2(rs, rs);
+#pragma unroll 1
+                for (int ch = 0; ch < kHalf / 32; ++ch) {
+                    if (col0 + ch * 32 >= p.cols)
+                        break;
+                    float v[32];
+                    ptx::tmem_ld_32cols(trow + ch * 32, v);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float4 c = *reinterpret_cast<const float4 *>(cols + (ch * 32 + i) * 2);
+                        const uint64_t s2 = ptx::mul_f32x2(rs2, ptx::f32x2(c.x, c.y));
+                        ptx::unpack_f32x2(ptx::fma_f32x2(ptx::f32x2(v[i], v[i + 1]), s2, ptx::f32x2(c.z, c.w)), v[i], v[i + 1]);
+                    }
+                    const bool mine = at >= ch * 32 && at < ch * 32 + 32;
+                    if constexpr (KIND == kStats) {
+                        if (mine) {
+                            float z = 0.0f;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                z = at == ch * 32 + i ? v[i] : z;
+                            p.target_z[row] = z;
+                        }
+                        float most = v[0];
+#pragma unroll
+                        for (int i = 1; i < 32; ++i)
+                            most = fmaxf(most, v[i]);
+                        most = fmaxf(most, top);
+                        // (a row without a finite value so far: exp(-inf - 0) = 0)
+                        const float ref = most == -INFINITY ? 0.0f : most;
+                        sum *= fp8mm::ex2_approx((top - ref) * kLog2e);
+                        top = most;
+                        float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            s4[i & 3] += fp8mm::ex2_approx((v[i] - ref) * kLog2e);
+                        sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = live ? fp8mm::ex2_approx((v[i] - lse) * kLog2e) * gs : 0.0f;
+                        if (mine) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v[i] = at == ch * 32 + i ? v[i] - gs : v[i];
+                        }
+                        if ((ch & 1) == 0)
+                            stage_free();
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            stage_chunk(stage, lane, (ch & 1) * 4 + i / 8,
+                                        make_uint4(fp8rows::pack2(v[i], v[i + 1], fp8rows::kF16),
+                                                   fp8rows::pack2(v[i + 2], v[i + 3], fp8rows::kF16),
+                                                   fp8rows::pack2(v[i + 4], v[i + 5], fp8rows::kF16),
+                                                   fp8rows::pack2(v[i + 6], v[i + 7], fp8rows::kF16)));
+                        // (the last columns may fill half a block: the store ends at p.cols)
+                        if ((ch & 1) == 1 || col0 + (ch + 1) * 32 >= p.cols)
+                            stage_out(col0 + (ch & ~1) * 32, row0, 0);
+                        if (p.colsum) {
+                            const float s = sum_rows(v, lane);
+                            const int n = col0 + ch * 32 + lane;
+                            if (row0 < p.rows && n < p.cols)
+                                __stcg(p.colsum + (row0 / 32) * p.colsum_ld + n, s);
+                        }
+                    }
+                }
+                if constexpr (KIND == kStats) {
+                    if (in && col0 < p.cols)
+                        __stcg(p.stats + static_cast<long long>(col0 / kHalf) * p.rows + row, make_float2(top, sum));
+                }
+            } else {
+                const bool f32 = p.out_type == fp8mm::kOutF32;
+#pragma unroll 1
+                for (int ch = 0; ch < kHalf / 32; ++ch) {
+                    float v[32];
+                    ptx::tmem_ld_32cols(trow + ch * 32, v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] *= out_scale;
+                    if (f32 || (ch & 1) == 0)
+                        stage_free();
+                    if (f32) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            stage_chunk(stage, lane, i / 4,
+                                        make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]),
+                                                   __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3])));
+                        stage_out(col0 + ch * 32, row0, w.split);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            stage_chunk(stage, lane, (ch & 1) * 4 + i / 8,
+                                        make_uint4(fp8rows::pack2(v[i], v[i + 1], p.out_type),
+                                                   fp8rows::pack2(v[i + 2], v[i + 3], p.out_type),
+                                                   fp8rows::pack2(v[i + 4], v[i + 5], p.out_type),
+                                                   fp8rows::pack2(v[i + 6], v[i + 7], p.out_type)));
+                        if (ch & 1)
+                            stage_out(col0 + (ch - 1) * 32, row0, w.split);
+                    }
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive_cluster(ptx::mapa_shared(tempty_bar(acc), 0));
+            if (++acc == 2) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+        if (KIND != kStats && lane == 0)
+            ptx::bulk_wait_group_all();
+        __syncwarp();
+    }
+
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem_base, 2 * kTile);
+    }
+}
+
+// ---------------------------------------------------------------- combine ---
+// lse and loss of 32 rows a CTA: warp w joins the row pairs w, w + 32, ..., the
+// first warp the 32 results of a row, always in this order.
+
+struct CombineParams {
+    const float2 *stats;
+    const float *target_z;
+    const int64_t *target;
+    long long ignore, vocabulary;
+    float *loss, *lse;
+    int rows, parts;
+};
+
+constexpr int kCombineThreads = 1024;
+
+// (top, sum) of two parts; without a finite value the reference is 0.
+__device__ __forceinline__ void join(float &top, float &sum, float2 b)
+{
+    const float most = fmaxf(top, b.x), ref = most == -INFINITY ? 0.0f : most;
+    sum = sum * fp8mm::ex2_approx((top - ref) * kLog2e) + b.y * fp8mm::ex2_approx((b.x - ref) * kLog2e);
+    top = most;
+}
+
+static __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineParams p)
+{
+    __shared__ float2 part[32][33];
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x * 32 + lane;
+    float top = -INFINITY, sum = 0.0f;
+    if (row < p.rows) {
+#pragma unroll 4
+        for (int i = warp; i < p.parts; i += 32)
+            join(top, sum, __ldcg(p.stats + static_cast<long long>(i) * p.rows + row));
+    }
+    part[warp][lane] = make_float2(top, sum);
+    __syncthreads();
+    if (warp != 0 || row >= p.rows)
+        return;
+    for (int i = 1; i < 32; ++i)
+        join(top, sum, part[i][lane]);
+    const float rest = logf(sum);
+    p.lse[row] = top + rest;
+    const long long t = p.target[row];
+    float loss = 0.0f;
+    if (t != p.ignore)
+        loss = t >= 0 && t < p.vocabulary ? (top - p.target_z[row]) + rest : NAN;
+    p.loss[row] = loss;
+}
+
+// ------------------------------------------------------- sums of partials ---
+// dA from its fp32 partials: out = cast( factor G S sum over s of part[s] ).
+
+struct FinishParams {
+    const float *parts;
+    long long n;                       // elements of one partial, a multiple of 4
+    int count, out_type, norm_of;
+    const uint32_t *norms;
+    float factor;
+    void *out;
+};
+
+constexpr int kFinishThreads = 256;
+
+static __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const FinishParams p)
+{
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const float f = p.factor * norm_scale(p.norms, kNormG) * norm_scale(p.norms, p.norm_of);
+    const long long step = static_cast<long long>(gridDim.x) * kFinishThreads;
+    for (long long i = static_cast<long long>(blockIdx.x) * kFinishThreads + threadIdx.x; i < p.n / 4; i += step) {
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int k = 0; k < p.count; ++k) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.parts + k * p.n) + i);
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+        if (p.out_type == fp8mm::kOutF32)
+            reinterpret_cast<float4 *>(p.out)[i] = make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
+        else
+            reinterpret_cast<uint2 *>(p.out)[i] = make_uint2(fp8rows::pack2(s.x * f, s.y * f, p.out_type),
+                                                             fp8rows::pack2(s.z * f, s.w * f, p.out_type));
+    }
+}
+
+// dbias of a piece: out[c] = f sum over p < count of part[p][c], warp w adding
+// parts w, w + 8, ... of 32 columns.
+struct ColumnsParams {
+    const float *parts;
+    long long ld;
+    int cols, count;
+    const uint32_t *norms;
+    float *out;
+};
+
+constexpr int kColumnsThreads = 256;
+
+static __global__ void __launch_bounds__(kColumnsThreads) columns_kernel(const ColumnsParams p)
+{
+    __shared__ float part[8][33];
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const float f = norm_scale(p.norms, kNormG) / kSlopeScale;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (c < p.cols) {
+#pragma unroll 8
+        for (int i = warp; i < p.count; i += 8)
+            s += __ldcg(p.parts + i * p.ld + c);
+    }
+    part[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < p.cols) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            s += part[i][lane];
+        p.out[c] = s * f;
+    }
+}
+
+}  // namespace fp8loss

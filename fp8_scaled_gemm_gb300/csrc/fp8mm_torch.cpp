@@ -1,5 +1,5 @@
-// fp8mm_torch.cpp -- the operators of an MLP block for PyTorch tensors, as a
-// CPython extension module.
+// fp8mm_torch.cpp -- the operators of an MLP block, of the loss behind it and of
+// the parameters' update for PyTorch tensors, as a CPython extension module.
 //
 // These calls make up to five new tensors each, and with few rows their
 // kernels take 2 to 10 us, so the host's time is the call's time. Through
@@ -25,6 +25,7 @@
 #include <cstdarg>
 #include <initializer_list>
 #include <string>
+#include <vector>
 
 #include "fp8mm.h"
 
@@ -54,6 +55,11 @@ struct {
     decltype(&fp8_layer_norm) layer_norm;
     decltype(&fp8_layer_norm_grad) layer_norm_grad;
     decltype(&fp8_layer_norm_grad_workspace) layer_norm_grad_workspace;
+    decltype(&fp8_cross_entropy) cross_entropy;
+    decltype(&fp8_cross_entropy_workspace) cross_entropy_workspace;
+    decltype(&fp8_cross_entropy_grad) cross_entropy_grad;
+    decltype(&fp8_cross_entropy_grad_workspace) cross_entropy_grad_workspace;
+    decltype(&fp8_adamw) adamw;
 } api;
 PyObject *check_status;      // raises for a status other than 0
 
@@ -288,7 +294,7 @@ bool back_to_back(const Tensor &t, int inner, int64_t n, int64_t K)
 }
 
 // The operands and options of a product: A, B, scale_a, scale_b, scale_mode
-// from a[0], variant, tile_n, split_k from o[0].
+// from a[0], variant, tile_n, split_k from o[0] (nullptr: the automatic choice).
 Product product(PyObject *const *a, PyObject *const *o)
 {
     Product p{};
@@ -327,9 +333,11 @@ Product product(PyObject *const *a, PyObject *const *o)
     beside("B", B, A);
     beside("scale_a", *p.scale_a, A);
     beside("scale_b", *p.scale_b, A);
-    p.options.variant = integer(o[0]);
-    p.options.tile_n = integer(o[1]);
-    p.options.split_k = integer(o[2]);
+    if (o) {
+        p.options.variant = integer(o[0]);
+        p.options.tile_n = integer(o[1]);
+        p.options.split_k = integer(o[2]);
+    }
     return p;
 }
 
@@ -562,6 +570,242 @@ PyObject *layer_norm_grad(PyObject *const *a)
     return tuple({&dx, &dgamma, &dbeta});
 }
 
+// ---------------------------------------------------------- cross entropy ---
+
+int64_t integer64(PyObject *o)
+{
+    PyObject *i = PyNumber_Index(o);
+    if (!i)
+        throw Raised{};
+    const long long v = PyLong_AsLongLong(i);
+    Py_DECREF(i);
+    if (v == -1 && PyErr_Occurred())
+        throw Raised{};
+    return v;
+}
+
+double number(PyObject *o)
+{
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred())
+        throw Raised{};
+    return v;
+}
+
+// target [M] and bias [N] of a product with a vocabulary.
+const int64_t *targets(const Product &p, PyObject *o)
+{
+    const Tensor &t = *tensor("target", o);
+    if (t.scalar_type() != ScalarType::Long || t.numel() != p.M || !t.is_contiguous() || !t.is_cuda())
+        refuse("target must be a contiguous CUDA tensor of %lld values of torch.int64", static_cast<long long>(p.M));
+    beside("target", t, *p.A);
+    return static_cast<const int64_t *>(t.data_ptr());
+}
+
+const Tensor *column_bias(const Product &p, PyObject *o)
+{
+    const Tensor *bias = tensor("bias", o, true);
+    vector("bias", bias, p.N, true, *p.A);
+    return bias;
+}
+
+// A, B, scale_a, scale_b, scale_mode, target, bias, ignore_index
+PyObject *cross_entropy(PyObject *const *a)
+{
+    const Product p = product(a, nullptr);
+    const int64_t *target = targets(p, a[5]), ignore = integer64(a[7]);
+    const Tensor *bias = column_bias(p, a[6]);
+    Result loss, lse;
+    loss.plan(*p.A, ScalarType::Float, p.M);
+    lse.plan(*p.A, ScalarType::Float, p.M);
+    const Guard guard(p.A->device());
+    int64_t bytes = 0, rc;
+    checked(bytes = api.cross_entropy_workspace(p.M, p.N));
+    {
+        Unlocked u;
+        float *to = loss.make_floats(), *to_lse = lse.make_floats();
+        Tensor ws = empty(*p.A, {bytes}, ScalarType::Byte);
+        rc = api.cross_entropy(data(p.A), p.options.a_type, data(p.B), p.options.b_type, floats(p.scale_a),
+                               floats(p.scale_b), p.mode, data(bias), bias ? row_code(bias->scalar_type()) : FP8MM_OUT_F32,
+                               target, ignore, to, to_lse, p.M, p.N, p.K, data(&ws), bytes, stream());
+    }
+    checked(rc);
+    return tuple({&loss, &lse});
+}
+
+// A contiguous [R, C] result of out_type, given or made where it is wanted.
+void gradient(Result &r, const char *name, PyObject *given, PyObject *wanted, const Product &p, int64_t R, int64_t C,
+              ScalarType type)
+{
+    r.take(name, given);
+    if (!r.t) {
+        if (truth(wanted))
+            r.plan(*p.A, type, R, C);
+        return;
+    }
+    if (r.t->scalar_type() != type || r.t->dim() != 2 || r.t->size(0) != R || r.t->size(1) != C ||
+        !r.t->is_contiguous() || !r.t->is_cuda())
+        refuse("%s must be a contiguous CUDA tensor of shape (%lld, %lld) and of out_dtype", name,
+               static_cast<long long>(R), static_cast<long long>(C));
+    beside(name, *r.t, *p.A);
+}
+
+// A, B, scale_a, scale_b, scale_mode, target, lse, dloss, bias, ignore_index,
+// da, db, out_dtype, return_da, return_db, return_dbias
+PyObject *cross_entropy_grad(PyObject *const *a)
+{
+    const Product p = product(a, nullptr);
+    const int64_t *target = targets(p, a[5]), ignore = integer64(a[9]);
+    const Tensor *lse = tensor("lse", a[6]), *dloss = tensor("dloss", a[7]), *bias = column_bias(p, a[8]);
+    vector("lse", lse, p.M, false, *p.A);
+    // one value, given as such or spread over the rows (the gradient of a mean)
+    const bool spread = dloss->dim() == 1 && dloss->size(0) == p.M && p.M > 0 && dloss->stride(0) == 0;
+    if (dloss->scalar_type() != ScalarType::Float || !dloss->is_cuda() ||
+        !(spread || (dloss->is_contiguous() && (dloss->numel() == p.M || dloss->numel() == 1))))
+        refuse("dloss must be a CUDA tensor of %lld values (contiguous) or one value of torch.float32",
+               static_cast<long long>(p.M));
+    beside("dloss", *dloss, *p.A);
+    const ScalarType type = dtype("out_dtype", a[12]);
+    if (row_code(type) < 0)
+        refuse("out_dtype must be torch.bfloat16, torch.float16 or torch.float32");
+    Result da, db, dbias;
+    gradient(da, "da", a[10], a[13], p, p.M, p.K, type);
+    gradient(db, "db", a[11], a[14], p, p.N, p.K, type);
+    if (truth(a[15]))
+        dbias.plan(*p.A, ScalarType::Float, p.N);
+    const Guard guard(p.A->device());
+    int64_t bytes = 0, rc;
+    checked(bytes = api.cross_entropy_grad_workspace(p.M, p.N, p.K, da.wanted(), db.wanted(), dbias.wanted()));
+    {
+        Unlocked u;
+        void *to_a = da.make(), *to_b = db.make();
+        float *to_bias = dbias.make_floats();
+        Tensor ws = empty(*p.A, {bytes}, ScalarType::Byte);
+        rc = api.cross_entropy_grad(data(p.A), p.options.a_type, data(p.B), p.options.b_type, floats(p.scale_a),
+                                    floats(p.scale_b), p.mode, data(bias),
+                                    bias ? row_code(bias->scalar_type()) : FP8MM_OUT_F32, target, ignore, floats(lse),
+                                    floats(dloss), spread ? 1 : dloss->numel(), to_a, to_b, row_code(type), to_bias, p.M, p.N,
+                                    p.K, data(&ws), bytes, stream());
+    }
+    checked(rc);
+    return tuple({&da, &db, &dbias});
+}
+
+// ------------------------------------------------------------------ AdamW ---
+
+// A list or tuple of tensors as such.
+struct Sequence {
+    PyObject *seq = nullptr;
+    Py_ssize_t n = 0;
+    const char *name;
+
+    Sequence(const char *what, PyObject *o) : name(what)
+    {
+        if (o == Py_None)
+            return;
+        seq = PySequence_Fast(o, "the tensors must be given in lists");
+        if (!seq)
+            throw Raised{};
+        n = PySequence_Fast_GET_SIZE(seq);
+    }
+    Sequence(const Sequence &) = delete;
+    ~Sequence() { Py_XDECREF(seq); }
+    explicit operator bool() const { return seq != nullptr; }
+    const Tensor &operator[](Py_ssize_t i) const { return *tensor(name, PySequence_Fast_GET_ITEM(seq, i)); }
+};
+
+// Element i of a sequence beside parameter p: contiguous, of p's device and as
+// many values; `type` where one is asked for.
+void *beside_param(const Sequence &s, Py_ssize_t i, const Tensor &p, ScalarType type, int64_t count)
+{
+    const Tensor &t = s[i];
+    if (t.scalar_type() != type)
+        refuse("%s must all have one dtype, that of a parameter's or of a state", s.name);
+    if (t.numel() != count || !t.is_contiguous() || !t.is_cuda() || t.device() != p.device())
+        refuse("%s[%zd] must be a contiguous CUDA tensor of %lld values beside its parameter", s.name, i,
+               static_cast<long long>(count));
+    return t.data_ptr();
+}
+
+// params, grads, exp_avgs, exp_avg_sqs, step, lr, beta1, beta2, eps,
+// weight_decay, masters, exp_avg_scales, exp_avg_sq_scales, grad_scale
+PyObject *adamw(PyObject *const *a)
+{
+    const Sequence params("params", a[0]), grads("grads", a[1]), ms("exp_avgs", a[2]), vs("exp_avg_sqs", a[3]),
+        masters("masters", a[10]), m_scales("exp_avg_scales", a[11]), v_scales("exp_avg_sq_scales", a[12]);
+    const Sequence *needed[] = {&params, &grads, &ms, &vs};
+    for (const Sequence *s : needed)
+        if (!*s || s->n != params.n)
+            refuse("%s must be a list of %zd tensors, one for each parameter", s->name, params.n);
+    if (params.n == 0)
+        Py_RETURN_NONE;
+    const Tensor &first = params[0];
+    const ScalarType type = first.scalar_type(), grad_type = grads[0].scalar_type(), state = ms[0].scalar_type();
+    const bool eight = state == ScalarType::Float8_e4m3fn;
+    if (row_code(type) < 0 || row_code(grad_type) < 0 || !first.is_cuda())
+        refuse("params and grads must be CUDA tensors of torch.bfloat16, torch.float16 or torch.float32");
+    if (!eight && state != ScalarType::Float)
+        refuse("exp_avgs and exp_avg_sqs must be torch.float32 or torch.float8_e4m3fn");
+    if (masters && masters.n != params.n)
+        refuse("masters must be a list of %zd tensors, one for each parameter", params.n);
+    for (const Sequence *s : {&m_scales, &v_scales})
+        if (eight ? s->n != params.n : static_cast<bool>(*s))
+            refuse("%s must be given for states of 8 bits, one for each parameter, and only there", s->name);
+    fp8mm_adamw_options o{};
+    o.param_type = row_code(type);
+    o.grad_type = row_code(grad_type);
+    o.state_bits = eight ? 8 : 32;
+    std::vector<fp8mm_adamw_tensor> all(static_cast<size_t>(params.n));
+    for (Py_ssize_t i = 0; i < params.n; ++i) {
+        const Tensor &p = params[i];
+        fp8mm_adamw_tensor &t = all[static_cast<size_t>(i)];
+        t.count = p.numel();
+        t.param = beside_param(params, i, first, type, t.count);
+        t.grad = beside_param(grads, i, p, grad_type, t.count);
+        t.exp_avg = beside_param(ms, i, p, state, t.count);
+        t.exp_avg_sq = beside_param(vs, i, p, state, t.count);
+        if (masters)
+            t.master = static_cast<float *>(beside_param(masters, i, p, ScalarType::Float, t.count));
+        if (eight) {
+            const int64_t blocks = (t.count + 255) / 256;
+            t.exp_avg_scale = static_cast<float *>(beside_param(m_scales, i, p, ScalarType::Float, blocks));
+            t.exp_avg_sq_scale = static_cast<float *>(beside_param(v_scales, i, p, ScalarType::Float, blocks));
+        }
+    }
+    // (a tensor: read by the kernel when it runs)
+    auto device_value = [&](const char *name, PyObject *object, ScalarType of) -> const void * {
+        if (!THPVariable_Check(object))
+            return nullptr;
+        const Tensor &t = THPVariable_Unpack(object);
+        if (t.scalar_type() != of || t.numel() != 1 || !t.is_cuda())
+            refuse("%s must be a number or a CUDA tensor of one value of %s", name,
+                   of == ScalarType::Long ? "torch.int64" : "torch.float32");
+        beside(name, t, first);
+        return t.data_ptr();
+    };
+    o.step_device = static_cast<const int64_t *>(device_value("step", a[4], ScalarType::Long));
+    o.step = o.step_device ? 1 : integer64(a[4]);
+    o.lr_device = static_cast<const float *>(device_value("lr", a[5], ScalarType::Float));
+    o.lr = o.lr_device ? 0.0 : number(a[5]);
+    o.beta1 = number(a[6]);
+    o.beta2 = number(a[7]);
+    o.eps = number(a[8]);
+    o.weight_decay = number(a[9]);
+    if (a[13] != Py_None) {
+        const Tensor &gs = *tensor("grad_scale", a[13]);
+        vector("grad_scale", &gs, 1, false, first);
+        o.grad_scale = floats(&gs);
+    }
+    const Guard guard(first.device());
+    int64_t rc;
+    {
+        Unlocked u;
+        rc = api.adamw(all.data(), static_cast<int64_t>(all.size()), &o, stream());
+    }
+    checked(rc);
+    Py_RETURN_NONE;
+}
+
 // ---------------------------------------------------------------- module ---
 
 // A function of N positional arguments.
@@ -590,8 +834,9 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
 PyObject *init(PyObject *, PyObject *args)
 {
     PyObject *check;
-    unsigned long long at[7];
-    if (!PyArg_ParseTuple(args, "O(KKKKKKK)", &check, &at[0], &at[1], &at[2], &at[3], &at[4], &at[5], &at[6]))
+    unsigned long long at[12];
+    if (!PyArg_ParseTuple(args, "O(KKKKKKKKKKKK)", &check, &at[0], &at[1], &at[2], &at[3], &at[4], &at[5], &at[6], &at[7],
+                          &at[8], &at[9], &at[10], &at[11]))
         return nullptr;
     int i = 0;
     auto next = [&](auto &f) { f = reinterpret_cast<std::decay_t<decltype(f)>>(static_cast<uintptr_t>(at[i++])); };
@@ -602,6 +847,11 @@ PyObject *init(PyObject *, PyObject *args)
     next(api.layer_norm);
     next(api.layer_norm_grad);
     next(api.layer_norm_grad_workspace);
+    next(api.cross_entropy);
+    next(api.cross_entropy_workspace);
+    next(api.cross_entropy_grad);
+    next(api.cross_entropy_grad_workspace);
+    next(api.adamw);
     Py_INCREF(check);
     Py_XDECREF(check_status);
     check_status = check;
@@ -621,6 +871,9 @@ PyMethodDef methods[] = {
     method<act_grad, 7>("act_grad"),
     method<layer_norm, 8>("layer_norm"),
     method<layer_norm_grad, 8>("layer_norm_grad"),
+    method<cross_entropy, 8>("cross_entropy"),
+    method<cross_entropy_grad, 16>("cross_entropy_grad"),
+    method<adamw, 14>("adamw"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -220,6 +220,30 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t smem_byte_addr)
     return d;
 }
 
+// Shared-memory matrix descriptor for an MN-major 16-bit operand tile written
+// by TMA with 128-byte swizzling in boxes of 64 MN elements (one 128-byte row)
+// x 64 K rows: groups of 8 K rows are 1024 bytes apart (stride byte offset),
+// the next 64 MN elements one box of 8192 bytes further (leading byte offset).
+// Advancing K by 16 adds two groups, 2048 bytes, to the start address.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_byte_addr)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_byte_addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(8192u >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+// Instruction descriptor for kind::f16: D fp32, A and B fp16 (format 0); bits
+// 15 and 16: A and B are MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n, bool a_mn, bool b_mn)
+{
+    return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
 // Instruction descriptor for kind::f8f6f4: D fp32 (bits 4-5 = 1), A and B
 // e4m3 (format 0 in bits 7-9 and 10-12), both K-major (bits 15, 16 = 0),
 // N >> 3 in bits 17-22, M >> 4 in bits 24-28.
@@ -320,6 +344,18 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, 
         : "memory");
 }
 
+// The same for one K=16 slice of 16-bit operands.
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Arrive once on the mbarrier at `bar` (same offset) in every CTA of `cta_mask`
 // when all pair MMAs issued so far by this thread have completed.
 __device__ __forceinline__ void mma_commit_pair_multicast(uint32_t bar, uint16_t cta_mask)
@@ -347,6 +383,15 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t sr
                                              int32_t z)
 {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+
+// As tma_store_3d, adding to the fp32 values that are there.
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap *map, uint32_t src, int32_t x, int32_t y, int32_t z)
+{
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
                  "r"(x), "r"(y), "r"(z), "r"(src)
                  : "memory");

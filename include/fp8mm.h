@@ -502,6 +502,135 @@ int fp8_layer_norm_grad(const void *dy, int dy_type, int64_t lddy, const void *x
 int64_t fp8_layer_norm_grad_workspace(int64_t R, int64_t C);
 
 /*
+ * Softmax cross entropy of each row over the columns of a product, without the
+ * product being stored: the end of a model's forward pass, where A holds the
+ * last layer's rows and B the vocabulary's weights.
+ *
+ *   z[m, n] = acc[m, n] (scale_a (x) scale_b) + bias[n]      fp32, not rounded
+ *   lse[m]  = log( sum over n of exp(z[m, n]) )
+ *   loss[m] = lse[m] - z[m, target[m]],  0 where target[m] == ignore_index
+ *
+ *   A, B, scale_a, scale_b, scale_mode, M, N, K   as in fp8_scaled_mm_ex, with
+ *              a_type, b_type (FP8MM_TYPE_*); N >= 1.
+ *   bias       [N] of bias_type (FP8MM_OUT_BF16, _F16 or _F32), or NULL. A
+ *              column whose bias is -inf (or the type's lowest value) is left
+ *              out of its rows' sums.
+ *   target     int64 [M]: a column, or ignore_index. Any other value makes its
+ *              row's loss NaN.
+ *   loss, lse  fp32 [M] (outputs). lse is given for ignored rows too; the
+ *              gradient takes it.
+ *   workspace  device memory of at least fp8_cross_entropy_workspace(M, N)
+ *              bytes, 16-byte aligned; scratch of this call, so that calls on
+ *              different streams with workspaces of their own do not interfere.
+ *
+ * A row whose every z is -inf has lse = -inf and a loss of NaN; a NaN or +inf
+ * among a row's z makes both NaN. M == 0 is a no-op. The sums are added in an
+ * order that depends on the sizes only, so results repeat.
+ * Asynchronous on `stream`, two launches; bounded waits and errors as above.
+ */
+int fp8_cross_entropy(const void *A, int a_type, const void *B, int b_type,
+                      const float *scale_a, const float *scale_b, int scale_mode,
+                      const void *bias, int bias_type, const int64_t *target, int64_t ignore_index,
+                      float *loss, float *lse, int64_t M, int64_t N, int64_t K,
+                      void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace fp8_cross_entropy needs, or a negative fp8mm_status. */
+int64_t fp8_cross_entropy_workspace(int64_t M, int64_t N);
+
+/*
+ * Its gradients, with respect to the values that the codes and scales stand for:
+ *
+ *   dz[m, n] = (exp(z[m, n] - lse[m]) - [n == target[m]]) dloss[m]
+ *   da       = cast( dz (scale_b B)^T )     [M, K]
+ *   db       = cast( dz^T (scale_a A) )     [N, K]: of B's columns, as Bt lies in memory
+ *   dbias    = sum over m of dz             fp32 [N]
+ *
+ * z is computed again in pieces of the vocabulary, of which dz is kept as fp16
+ * (scaled by a power of two: one rounding of 2^-12 relative, and what is under
+ * 2^-38 of the largest |dloss| is lost); the products of dz run on 16-bit
+ * tensor cores with fp16 operands (codes times scales, one rounding of 2^-12)
+ * and fp32 sums. dbias is the sum of the unrounded dz.
+ *
+ *   lse        what fp8_cross_entropy returned for the same operands.
+ *   dloss      fp32 [M], or one value for all rows (dloss_count M or 1).
+ *   da, db     contiguous, of out_type (FP8MM_OUT_BF16, _F16 or _F32), 16-byte
+ *              aligned; dbias fp32. Each may be NULL (not wanted). They must not
+ *              overlap the inputs.
+ *   workspace  device memory of at least fp8_cross_entropy_grad_workspace(...)
+ *              bytes for the outputs that are wanted, 16-byte aligned; at most
+ *              about 2 GiB beside fp16 copies of A and fp32 partial sums of da.
+ *   others     as in fp8_cross_entropy.
+ *
+ * Rows with target == ignore_index add nothing, whatever their lse and dloss; a
+ * target that is neither a column nor ignore_index makes the gradients NaN. An
+ * infinite or NaN dloss or scale makes the products NaN. M == 0 gives db and
+ * dbias of zeros. Sums in an order that depends on the sizes, on which outputs
+ * are wanted and on the SM count only, so results repeat.
+ */
+int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
+                           const float *scale_a, const float *scale_b, int scale_mode,
+                           const void *bias, int bias_type, const int64_t *target, int64_t ignore_index,
+                           const float *lse, const float *dloss, int64_t dloss_count,
+                           void *da, void *db, int out_type, float *dbias,
+                           int64_t M, int64_t N, int64_t K,
+                           void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace fp8_cross_entropy_grad needs on the current device for
+ * the outputs that are wanted (0: not wanted), or a negative fp8mm_status. */
+int64_t fp8_cross_entropy_grad_workspace(int64_t M, int64_t N, int64_t K, int want_da, int want_db, int want_dbias);
+
+/* One tensor of an AdamW step: `count` elements, contiguous. */
+typedef struct fp8mm_adamw_tensor {
+    void *param;               /* of param_type: updated, or, with a master, its rounding  */
+    const void *grad;          /* of grad_type                                             */
+    float *master;             /* fp32: the parameter itself, updated; NULL: none          */
+    void *exp_avg;             /* first moment: fp32, or e4m3 codes                        */
+    void *exp_avg_sq;          /* second moment: fp32, or e4m3 codes of its square root    */
+    float *exp_avg_scale;      /* 8 bits: fp32 [ceil(count / 256)], one per block of codes */
+    float *exp_avg_sq_scale;   /* likewise                                                 */
+    int64_t count;
+} fp8mm_adamw_tensor;
+
+typedef struct fp8mm_adamw_options {
+    int param_type, grad_type; /* FP8MM_OUT_BF16, _F16 or _F32, of all tensors             */
+    int state_bits;            /* 32 or 8                                                  */
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;              /* t, from 1                                                */
+    const float *lr_device;    /* device memory that holds lr instead, or NULL             */
+    const int64_t *step_device;/* device memory that holds t instead, or NULL              */
+    const float *grad_scale;   /* device memory: factor of all gradients, or NULL for 1    */
+} fp8mm_adamw_options;
+
+/*
+ * One AdamW step over n tensors, in place:
+ *
+ *   g = grad grad_scale
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   w = w (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *
+ * in fp32, each operation rounded by itself. w is the master where there is one
+ * (param receives its rounding), else param. All tensors have a master or none has.
+ *
+ * States in 8 bits are e4m3 codes with an fp32 scale per block of 256 elements
+ * (max / 448; a zero scale gives zeros; a NaN makes its block NaN): m rounded
+ * to the nearest code, sqrt(v) rounded up or down by a hash of the element's
+ * place in its tensor and of t, with the probabilities that keep its mean (to
+ * the nearest code it would not move), and to no less than 2^-9 of the scale
+ * unless it is zero. The update takes the unrounded m and v. Zeros are the
+ * states to begin with. Same arguments, same bits.
+ *
+ * lr_device and step_device let a captured step be replayed: the graph reads
+ * them when it runs (t as it is then; the call does not count it up).
+ *
+ * Tensors may have any alignment of their elements; 16-byte aligned ones (8 for
+ * codes) run fastest. Memory that is written must not be given twice nor
+ * overlap a gradient: FP8MM_ERR_MODE. beta1, beta2 in [0, 1), eps >= 0, t >= 1,
+ * else FP8MM_ERR_SHAPE. Asynchronous on `stream`, one launch for each 400
+ * tensors; the arrays are read before the call returns.
+ */
+int fp8_adamw(const fp8mm_adamw_tensor *tensors, int64_t n, const fp8mm_adamw_options *options, void *stream);
+
+/*
  * Allocation-free variant of fp8_scaled_mm. The pages have no counterpart:
  * this is an addition for callers that cannot allocate device memory while
  * they run (for example code running inside a memory pool it does not own,
