@@ -1554,7 +1554,7 @@ int device_limit(int **status, unsigned long long *clocks)
 }
 
 int encode_tiles(CUtensorMap *map, CUtensorMapDataType type, const void *base, const int64_t (&dims)[3],
-                 const int64_t (&strides)[2], const int (&box)[3])
+                 const int64_t (&strides)[2], const int (&box)[3], int swizzle)
 {
     cuuint64_t d[3], st[2];
     cuuint32_t b[3], estr[3] = {1, 1, 1};
@@ -1565,7 +1565,7 @@ int encode_tiles(CUtensorMap *map, CUtensorMapDataType type, const void *base, c
             st[i] = static_cast<cuuint64_t>(strides[i]);
     }
     const CUresult r = encode_map(map, type, 3, const_cast<void *>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                  swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r == CUDA_SUCCESS)
         return FP8MM_OK;

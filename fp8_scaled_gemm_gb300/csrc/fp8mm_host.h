@@ -31,11 +31,11 @@ int device_sms(int *sms);
 // The current device's status word and the clocks a wait in a kernel may take.
 int device_limit(int **status, unsigned long long *clocks);
 
-// A 3-D tensor map with 128-byte swizzle (after device_sms): dims and box in
-// elements, innermost first, strides of the outer two dimensions in bytes.
+// A 3-D tensor map with a swizzle of 128- or 64-byte rows (after device_sms): dims
+// and box in elements, innermost first, strides of the outer two dimensions in bytes.
 // Elements out of range read as 0 and are not written.
 int encode_tiles(CUtensorMap *map, CUtensorMapDataType type, const void *base, const int64_t (&dims)[3],
-                 const int64_t (&strides)[2], const int (&box)[3]);
+                 const int64_t (&strides)[2], const int (&box)[3], int swizzle);
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

@@ -36,33 +36,35 @@ int check_problem(const void *A, const void *B, const float *sa, const float *sb
 }
 
 // A matrix of `rows` x `cols` elements, rows `ld` elements apart, `items` of
-// them `item` elements apart, in boxes of box_rows rows x 128 bytes.
+// them `item` elements apart, in boxes of box_rows rows x 128 bytes (or 64).
 int map_matrix(CUtensorMap *map, CUtensorMapDataType type, int es, const void *base, int64_t rows, int64_t cols, int64_t ld,
-               int box_rows, int64_t items = 1, int64_t item = 0)
+               int box_rows, int64_t items = 1, int64_t item = 0, int box_bytes = 128)
 {
     const int64_t dims[3] = {cols, rows, items};
     const int64_t strides[2] = {ld * es, (item ? item : ld * rows) * es};
-    const int box[3] = {128 / es, box_rows, 1};
-    return encode_tiles(map, type, base, dims, strides, box);
+    const int box[3] = {box_bytes / es, box_rows, 1};
+    return encode_tiles(map, type, base, dims, strides, box, box_bytes);
 }
 
-// Column of the instruction descriptor's formats.
-uint32_t formats(int a_type, int b_type)
+// The instruction descriptor's operand formats: P gives the rows, Q the columns.
+uint32_t formats(int p_type, int q_type)
 {
-    return (a_type == FP8MM_TYPE_E5M2 ? 1u << 7 : 0u) | (b_type == FP8MM_TYPE_E5M2 ? 1u << 10 : 0u);
+    return (p_type == FP8MM_TYPE_E5M2 ? 1u << 7 : 0u) | (q_type == FP8MM_TYPE_E5M2 ? 1u << 10 : 0u);
 }
 
 // Fills the tile space of a launch.
-void tile_space(LossParams &p, int64_t rows, int64_t cols, int64_t kblocks, int splits)
+void tile_space(LossParams &p, int64_t rows, int64_t cols, int width, int64_t kblocks, int splits, int run)
 {
     p.rows = static_cast<int>(rows);
     p.cols = static_cast<int>(cols);
+    p.width = width;
     p.kblocks = static_cast<int>(kblocks);
     p.tiles_p = static_cast<int>(cdiv(rows, kTile));
-    p.tiles_q = static_cast<int>(cdiv(cols, kTile));
+    p.tiles_q = static_cast<int>(cdiv(cols, width));
     p.group = std::min(p.tiles_p, 16);
     p.splits = splits;
-    p.num_units = p.tiles_p * p.tiles_q * splits;
+    p.run = run;
+    p.num_units = p.tiles_p * static_cast<int>(cdiv(p.tiles_q, run)) * splits;
 }
 
 template <int KIND>
@@ -86,12 +88,68 @@ int launch_tiles(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap
                       "cross entropy launch", ma, mb, mo, p);
 }
 
-// K slices of a gradient product: as many as give every CTA pair a tile, each
-// with at least 8 blocks of 64.
-int slices(int64_t rows, int64_t cols, int64_t contraction, int sms)
+// Tiles of the product z [M, N]: their width, and how many of a row are one unit.
+struct TileChoice {
+    int width, run;
+};
+
+// The width that ends first, by what a CTA pair loads for its tiles in turn: its
+// rows of A (up to 256) and its columns of B (one row of 32000 columns: two turns of
+// 224 columns for 256).
+// With many tiles a pair takes several neighbours, over which a row's maximum and
+// sum stay in registers: 16 units a pair keep the last turn short.
+TileChoice choose_tiles(int64_t M, int64_t N, int sms)
 {
-    const int64_t tiles = cdiv(rows, kTile) * cdiv(cols, kTile);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / 2 / tiles, cdiv(contraction, 64) / 8)));
+    const int64_t pairs = sms / 2, rows = std::min<int64_t>(M, kTile);
+    TileChoice best{kTile, 1};
+    int64_t cost = INT64_MAX;
+    for (int width = kTile; width >= 128; width -= 32) {
+        const int64_t c = cdiv(cdiv(M, kTile) * cdiv(N, width), pairs) * (rows + width);
+        if (c < cost) {
+            cost = c;
+            best.width = width;
+        }
+    }
+    const int64_t tiles = cdiv(M, kTile) * cdiv(N, best.width);
+    while (best.run < 8 && tiles / (2 * best.run) >= 16 * pairs)
+        best.run *= 2;
+    return best;
+}
+
+// Parts of a row that kStats leaves, and the most there can be.
+int64_t parts_of(const TileChoice &t, int64_t N) { return cdiv(cdiv(N, t.width), t.run) * 4; }
+int64_t most_parts(int64_t N) { return cdiv(N, 128) * 4; }
+
+// The operands' maps and the tile space of z [M, N] (kStats, kSlope).
+int product_maps(const TileChoice &t, const void *A, int a_type, const void *B, int b_type, int64_t M, int64_t N, int64_t K,
+                 CUtensorMap &ma, CUtensorMap &mb, LossParams &p)
+{
+    constexpr CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    tile_space(p, M, N, t.width, cdiv(K, 128), 1, t.run);
+    p.idesc = fp8mm::ptx::idesc_e4m3_f32(kTile, t.width) | formats(a_type, b_type);
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    const int rc = map_matrix(&ma, u8, 1, A, M, K, K, 128);
+    return rc != FP8MM_OK ? rc : map_matrix(&mb, u8, 1, B, N, K, K, t.width / 2);
+}
+
+// K slices of a gradient product of `kblocks` blocks of 64: the number that
+// ends first. A block takes a pair 0.28 us, a tile's end about 2; every slice
+// writes fp32 partials, which another kernel reads (at 5.5 TB/s).
+int slices(int64_t rows, int64_t cols, int64_t kblocks, int sms)
+{
+    const int64_t tiles = cdiv(rows, kTile) * cdiv(cols, kTile), pairs = sms / 2;
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= 64 && s * 4 <= std::max<int64_t>(kblocks, 4); ++s) {
+        const double t = cdiv(tiles * s, pairs) * (cdiv(kblocks, s) * 0.28 + 2.0) +
+                         (s > 1 ? 3.0 + s * rows * cols * 8 / 5.5e6 : 0.0);
+        if (s == 1 || t < least) {
+            least = t;
+            best = s;
+        }
+    }
+    return best;
 }
 
 // How a gradient call goes through the vocabulary, and where its workspace's
@@ -110,8 +168,8 @@ GradPlan plan_grad(int64_t M, int64_t N, int64_t K, bool da, bool db, bool dbias
     g.pieces = cdiv(N, most);
     g.piece = cdiv(cdiv(N, g.pieces), kTile) * kTile;
     g.pieces = cdiv(N, g.piece);
-    g.split_a = slices(M, K, std::min(N, g.piece), sms);
-    g.split_b = slices(std::min(N, g.piece), K, M, sms);
+    g.split_a = slices(M, K, cdiv(std::min(N, g.piece), 64), sms);
+    g.split_b = slices(std::min(N, g.piece), K, cdiv(M, 64), sms);
     g.parts_a = da && (g.split_a > 1 || g.pieces > 1);
     g.parts_b = db && g.split_b > 1;
     int64_t at = 0;
@@ -131,7 +189,7 @@ GradPlan plan_grad(int64_t M, int64_t N, int64_t K, bool da, bool db, bool dbias
     return g;
 }
 
-int64_t stats_bytes(int64_t M, int64_t N) { return aligned(cdiv(N, kHalf) * M * 8); }
+int64_t stats_bytes(int64_t M, int64_t N) { return aligned(most_parts(N) * M * 8); }
 
 int zero(void *p, int64_t bytes, cudaStream_t s)
 {
@@ -140,7 +198,7 @@ int zero(void *p, int64_t bytes, cudaStream_t s)
 }
 
 int expand(const void *codes, const float *scale, int rowwise, int type, int norm_of, const uint32_t *norms, void *out,
-           int64_t rows, int64_t K, int sms, cudaStream_t s)
+           int64_t rows, int64_t K, int sms, cudaStream_t s)   // behind a kSlope kernel, or another of these
 {
     ExpandParams e{};
     e.codes = static_cast<const uint8_t *>(codes);
@@ -152,6 +210,18 @@ int expand(const void *codes, const float *scale, int rowwise, int type, int nor
     e.out = static_cast<__half *>(out);
     e.groups = rows * (K / 16);
     e.row_groups = static_cast<int>(K / 16);
+    e.early = 1;
+    // the same division of an SM's memory as the kernel it runs beside
+    static bool attr_set[kMaxDevices] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!attr_set[dev]) {
+        const cudaError_t err = cudaFuncSetAttribute(expand_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                     cudaSharedmemCarveoutMaxShared);
+        if (err != cudaSuccess)
+            return cuda_fail(err, "cudaFuncSetAttribute");
+        attr_set[dev] = true;
+    }
     return launch_grid2(expand_kernel, std::min<int64_t>(cdiv(e.groups, kExpandThreads), static_cast<int64_t>(sms) * 8), 1,
                         kExpandThreads, s, "fp16 operand launch", e);
 }
@@ -172,7 +242,7 @@ int finish(const void *parts, int64_t n, int count, int out_type, int norm_of, c
                         kFinishThreads, s, "gradient sum launch", f);
 }
 
-constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, kF16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+constexpr CUtensorMapDataType kF16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                               kF32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32, kB16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 
 }  // namespace
@@ -205,9 +275,11 @@ int fp8_cross_entropy(const void *A, int a_type, const void *B, int b_type, cons
     if ((rc = device_sms(&sms)) != FP8MM_OK)
         return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const TileChoice t = choose_tiles(M, N, sms);
     LossParams p{};
-    tile_space(p, M, N, cdiv(K, 128), 1);
-    p.idesc = fp8mm::ptx::idesc_e4m3_f32(kTile, kTile) | formats(a_type, b_type);
+    CUtensorMap mp, mq;
+    if ((rc = product_maps(t, A, a_type, B, b_type, M, N, K, mp, mq, p)) != FP8MM_OK)
+        return rc;
     p.scale_a = scale_a;
     p.scale_b = scale_b;
     p.rowwise = scale_mode == FP8MM_SCALE_ROWWISE;
@@ -218,11 +290,7 @@ int fp8_cross_entropy(const void *A, int a_type, const void *B, int b_type, cons
     p.vocabulary = N;
     p.stats = static_cast<float2 *>(workspace);
     p.target_z = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + stats_bytes(M, N));
-    CUtensorMap ma, mb;
-    if ((rc = map_matrix(&ma, kU8, 1, A, M, K, K, 128)) != FP8MM_OK ||
-        (rc = map_matrix(&mb, kU8, 1, B, N, K, K, 128)) != FP8MM_OK)
-        return rc;
-    if ((rc = launch_tiles<kStats>(ma, mb, ma, p, sms, s)) != FP8MM_OK)
+    if ((rc = launch_tiles<kStats>(mp, mq, mp, p, sms, s)) != FP8MM_OK)
         return rc;
     CombineParams c{};
     c.stats = p.stats;
@@ -233,7 +301,7 @@ int fp8_cross_entropy(const void *A, int a_type, const void *B, int b_type, cons
     c.loss = loss;
     c.lse = lse;
     c.rows = static_cast<int>(M);
-    c.parts = static_cast<int>(cdiv(N, kHalf));
+    c.parts = static_cast<int>(parts_of(t, N));
     return launch_grid2(combine_kernel, cdiv(M, 32), 1, kCombineThreads, s, "cross entropy sum launch", c);
 }
 
@@ -308,12 +376,9 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
     n.out = norms;
     if ((rc = launch_grid2(norms_kernel, kNormParts, 3, kNormThreads, s, "cross entropy norms launch", n)) != FP8MM_OK)
         return rc;
-    if (db && (rc = expand(A, scale_a, rowwise, a_type, kNormA, norms, ws + g.h16, M, K, sms, s)) != FP8MM_OK)
-        return rc;
 
-    CUtensorMap ma, mh, parts_a;
-    if ((rc = map_matrix(&ma, kU8, 1, A, M, K, K, 128)) != FP8MM_OK ||
-        (db && (rc = map_matrix(&mh, kF16, 2, ws + g.h16, M, K, K, 64)) != FP8MM_OK))
+    CUtensorMap mh, parts_a;
+    if (db && (rc = map_matrix(&mh, kF16, 2, ws + g.h16, M, K, K, 64)) != FP8MM_OK)
         return rc;
     if (da) {
         rc = g.parts_a ? map_matrix(&parts_a, kF32, 4, ws + g.parts_a_at, M, K, K, out_box, g.split_a)
@@ -325,10 +390,11 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
         const int64_t n0 = i * g.piece, nv = std::min(g.piece, N - n0);
         const uint8_t *Bi = static_cast<const uint8_t *>(B) + n0 * K;
         const float *sbi = scale_b + (rowwise ? n0 : 0);
-        CUtensorMap mb, mdz;
+        const TileChoice t = choose_tiles(M, nv, sms);
+        CUtensorMap mp, mq, mdz;
         LossParams p{};
-        tile_space(p, M, nv, cdiv(K, 128), 1);
-        p.idesc = fp8mm::ptx::idesc_e4m3_f32(kTile, kTile) | formats(a_type, b_type);
+        if ((rc = product_maps(t, A, a_type, Bi, b_type, M, nv, K, mp, mq, p)) != FP8MM_OK)
+            return rc;
         p.scale_a = scale_a;
         p.scale_b = sbi;
         p.rowwise = rowwise;
@@ -344,10 +410,14 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
         p.colsum = dbias ? reinterpret_cast<float *>(ws + g.colsum) : nullptr;
         p.colsum_ld = g.piece;
         p.norms = norms;
-        // dz [M, nv] with rows of `piece` elements, written in blocks of 32 x 64
-        if ((rc = map_matrix(&mb, kU8, 1, Bi, nv, K, K, 128)) != FP8MM_OK ||
-            (rc = map_matrix(&mdz, kF16, 2, ws + g.dz, M, nv, g.piece, out_box)) != FP8MM_OK ||
-            (rc = launch_tiles<kSlope>(ma, mb, mdz, p, sms, s)) != FP8MM_OK)
+        // dz [M, nv] with rows of `piece` elements, written in blocks of 32 x 32
+        if ((rc = map_matrix(&mdz, kF16, 2, ws + g.dz, M, nv, g.piece, 32, 1, 0, 64)) != FP8MM_OK)
+            return rc;
+        if ((rc = launch_tiles<kSlope>(mp, mq, mdz, p, sms, s)) != FP8MM_OK)
+            return rc;
+        if (da && (rc = expand(Bi, sbi, rowwise, b_type, kNormB, norms, ws + g.w16, nv, K, sms, s)) != FP8MM_OK)
+            return rc;
+        if (db && i == 0 && (rc = expand(A, scale_a, rowwise, a_type, kNormA, norms, ws + g.h16, M, K, sms, s)) != FP8MM_OK)
             return rc;
         if (dbias) {
             ColumnsParams c{};
@@ -361,15 +431,15 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
                 return rc;
         }
         LossParams o{};
-        o.norms = norms;
+        o.rowwise = rowwise;
         if (da) {
             CUtensorMap mz, mw;
-            if ((rc = expand(Bi, sbi, rowwise, b_type, kNormB, norms, ws + g.w16, nv, K, sms, s)) != FP8MM_OK ||
-                (rc = map_matrix(&mz, kF16, 2, ws + g.dz, M, nv, g.piece, 128)) != FP8MM_OK ||
+            if ((rc = map_matrix(&mz, kF16, 2, ws + g.dz, M, nv, g.piece, 128)) != FP8MM_OK ||
                 (rc = map_matrix(&mw, kF16, 2, ws + g.w16, nv, K, K, 64)) != FP8MM_OK)
                 return rc;
             // (a last piece with fewer blocks than slices adds to the first partials only)
-            tile_space(o, M, K, cdiv(nv, 64), static_cast<int>(std::min<int64_t>(g.split_a, cdiv(nv, 64))));
+            tile_space(o, M, K, kTile, cdiv(nv, 64), static_cast<int>(std::min<int64_t>(g.split_a, cdiv(nv, 64))), 1);
+            o.row_scale = scale_a;
             o.idesc = fp8mm::ptx::idesc_f16_f32(kTile, kTile, false, true);
             o.norms = g.parts_a ? nullptr : norms;
             o.factor = factor_a;
@@ -386,7 +456,8 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
                            : map_matrix(&mo, out_map, es, dbi, nv, K, K, out_box);
             if (rc != FP8MM_OK || (rc = map_matrix(&mz, kF16, 2, ws + g.dz, M, nv, g.piece, 64)) != FP8MM_OK)
                 return rc;
-            tile_space(o, nv, K, cdiv(M, 64), g.split_b);
+            tile_space(o, nv, K, kTile, cdiv(M, 64), g.split_b, 1);
+            o.row_scale = sbi;
             o.idesc = fp8mm::ptx::idesc_f16_f32(kTile, kTile, true, true);
             o.norms = g.parts_b ? nullptr : norms;
             o.factor = factor_b;

@@ -7,13 +7,14 @@
 //   dz[m, n] = (exp(z[m, n] - lse[m]) - [n = t[m]]) g[m]
 //   dA = dz (s_b B)^T,   dB^T = dz^T (s_a A),   dbias = sum_m dz
 //
-// One kernel in four kinds, all with 2-SM MMAs on 256 x 256 tiles (a cluster of
+// One kernel in four kinds, all with 2-SM MMAs on tiles of 256 rows (a cluster of
 // two CTAs; roles, ring and barriers as in fp8mm_kernel_pair.cuh):
 //
-//   kStats  the product z of fp8 operands. Each epilogue warp reduces its 32
-//           rows x 128 columns to (max, sum of exp(z - max)) per row and writes
-//           those 8 bytes; the warp that meets a row's target writes its z.
-//           combine_kernel joins the pairs of a row in a fixed order.
+//   kStats  the product z of fp8 operands. Each epilogue warp reduces its quarter
+//           of a row of the tile, over the tiles of a unit, to (max, sum of
+//           exp(z - max)) and writes those 8 bytes; the warp that meets a row's
+//           target writes its z. combine_kernel joins a row's parts in a fixed
+//           order.
 //   kSlope  the same product again for a piece of the vocabulary; the epilogue
 //           writes dz as fp16 (and sums of it over 32 rows for dbias).
 //   kGradA  dA = dz W16: the contraction runs over the vocabulary. dz is read
@@ -26,13 +27,19 @@
 // operands: fp8 codes of dz would leave 2 to 3 significant bits.
 //
 // dz in fp16: 11 significant bits against bf16's 8, one rounding of at most
-// 2^-12 relative per element of a long sum. Its narrow range is met by powers
-// of two: |dz| <= |g| is known before anything is computed, so rows are scaled
-// by 2^14 / G with G the largest |g|'s power of two; probabilities down to
-// 2^-28 keep all 11 bits, smaller ones are held to 2^-38 of the largest |g|.
-// W16 = code s_b and H16 = code s_a are scaled the same way by the largest
-// scale, so one dz serves both products; their fp16 rounding is 2^-12 again.
-// All scales are powers of two and come off, exactly, in fp32.
+// 2^-11 relative per element of a long sum, and the only one before the
+// output's. Its narrow range is met by powers of two: |dz| <= |g| is known
+// before anything is computed, so rows are scaled by 2^12 / G with G the largest
+// |g|'s power of two; probabilities down to 2^-26 keep all 11 bits, smaller ones
+// are held to 2^-37 of the largest |g|. A scale is split into its mantissa
+// (in [1, 2)) and its power of two. The powers, over the largest one, go
+// with the codes, which is exact: W16 = code 2^e(s_b), H16 = code 2^e(s_a). The
+// mantissas go with dz before it is rounded,
+//
+//   dz'[m, n] = dz[m, n] m(s_a[m]) m(s_b[n]),
+//
+// and since a product sums over one of its two indexes, the mantissa of the
+// other one comes off its row of the result in fp32: one dz' serves both.
 #pragma once
 
 #include "fp8mm_kernel.cuh"
@@ -46,9 +53,8 @@ using fp8mm::Waiter;
 enum Kind { kStats, kSlope, kGradA, kGradB };
 
 constexpr int kTile = 256;             // rows and columns of a CTA pair's tile
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;           // four per 32 rows of a tile, two blocks of 32 columns each (256 wide)
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kHalf = 128;             // columns of one epilogue warp
 constexpr int kNormParts = 32;         // partial maxima per norm
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -58,22 +64,29 @@ struct Cfg {
     static constexpr bool kFp8 = KIND == kStats || KIND == kSlope;
     static constexpr bool kAMn = KIND == kGradB, kBMn = !kFp8;
     static constexpr int kABytes = 128 * 128;
-    static constexpr int kStageBytes = 2 * kABytes;                            // 128 rows of A, 128 of B
-    static constexpr int kStages = KIND == kSlope ? 5 : 6;
-    static constexpr int kStagingBytes = KIND == kStats ? 0 : kEpiWarps * 4096;   // one block of output per warp
-    static constexpr int kColBytes = kFp8 ? kEpiWarps * kHalf * 8 : 0;         // (scale, bias) per column and warp
+    static constexpr int kStageBytes = 2 * kABytes;                            // 128 rows of A, up to 128 of B
+    static constexpr int kStages = KIND == kStats ? 6 : 5;
+    // per warp: a block of output (dz 32 x 32 fp16, gradients 32 rows x 128 bytes)
+    static constexpr int kBlockBytes = KIND == kStats ? 0 : KIND == kSlope ? 2048 : 4096;
+    static constexpr int kStagingBytes = kEpiWarps * kBlockBytes;
+    // per warp and column: scale and bias, kSlope: the scale's mantissa
+    static constexpr int kColFloats = KIND == kStats ? 2 : KIND == kSlope ? 3 : 0;
+    static constexpr int kCols = kTile / 4;
+    static constexpr int kColBytes = kEpiWarps * kCols * kColFloats * 4;
     static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + kColBytes + 256;
     static_assert(kSmemBytes <= 232448, "exceeds 227 KB of shared memory");
 };
 
 struct LossParams {
-    int rows, cols;                    // of the tile space: M x N (fp8 kinds), M x K (dA), n x K (dB)
+    // tile space: 256 rows x `width` columns a tile (a multiple of 32; 256 for the gradients)
+    int rows, cols, width;
     int kblocks;                       // of 128 bytes of contraction
-    int tiles_p, tiles_q, group, splits, num_units;
+    int tiles_p, tiles_q, group, splits, run, num_units;
     uint32_t idesc;
     int *status;
     unsigned long long timeout_cycles;
     // fp8 kinds (column vectors start at the piece)
+    int M, N;
     const float *scale_a, *scale_b;
     int rowwise;
     const void *bias;
@@ -82,7 +95,7 @@ struct LossParams {
     long long ignore, col0;            // col0: the piece's first column in the vocabulary
     long long vocabulary;
     // kStats
-    float2 *stats;                     // [ceil(N / 128)][M]
+    float2 *stats;                     // [parts][M]
     float *target_z;                   // [M]
     // kSlope
     const float *lse, *dloss;
@@ -90,11 +103,12 @@ struct LossParams {
     float *colsum;                     // [ceil(M / 32)][n], or nullptr
     long long colsum_ld;
     // kSlope, kGradA, kGradB
-    const uint32_t *norms;             // see norm_scale
+    const uint32_t *norms;             // see norm_scale; gradients: nullptr where a sum of partials applies them
     float factor;                      // of the result, beside the norms
     int norm_of;                       // kGradA: kNormB, kGradB: kNormA
+    const float *row_scale;            // of the result's rows: scale_a, or scale_b from the piece on
     int out_type;
-    int add;                           // add to the output (fp32)
+    int add;                           // kGradA: add to the output (fp32)
 };
 
 // ------------------------------------------------------------------ norms ---
@@ -149,13 +163,23 @@ __device__ __forceinline__ float norm_scale(const uint32_t *norms, int which)
     return fmaxf(__uint_as_float(m & 0x7F800000u), 0x1p-100f);
 }
 
-constexpr float kSlopeScale = 0x1p14f;                // dz / G in (-2, 2): below fp16's 65504
+// dz' / G is in (-8, 8): below fp16's 65504.
+constexpr float kSlopeScale = 0x1p12f;
 
-// Of the codes: below 2 x 448 x 2^6 and 2 x 57344 / 2.
-__host__ __device__ constexpr float code_scale(int fp8_type) { return fp8_type == 0 ? 0x1p6f : 0x1p-1f; }
+// Of the codes: 448 x 2^7 and 57344 are below it too.
+__host__ __device__ constexpr float code_scale(int fp8_type) { return fp8_type == 0 ? 0x1p7f : 1.0f; }
+
+// A scale's mantissa, with its sign, and its power of two. What is under 2^-126
+// counts as zero; an infinity's and a NaN's power is infinite.
+__device__ __forceinline__ float mantissa(float s)
+{
+    const uint32_t b = __float_as_uint(s);
+    return (b & 0x7F800000u) ? __uint_as_float((b & 0x807FFFFFu) | 0x3F800000u) : 1.0f;
+}
+__device__ __forceinline__ float power(float s) { return __uint_as_float(__float_as_uint(s) & 0x7F800000u); }
 
 // ----------------------------------------------------- fp8 codes to fp16 ---
-// out[r, :] = fp16( code[r, :] s[r] f / S ): 16 codes a thread.
+// out[r, :] = fp16( code[r, :] 2^e(s[r]) f / S ): 16 codes a thread.
 
 struct ExpandParams {
     const uint8_t *codes;
@@ -165,6 +189,7 @@ struct ExpandParams {
     __half *out;
     long long groups;                  // rows x K / 16
     int row_groups;                    // K / 16
+    int early;                         // nothing here depends on the kernel before it
 };
 
 constexpr int kExpandThreads = 256;
@@ -172,12 +197,18 @@ constexpr int kExpandThreads = 256;
 static __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const ExpandParams p)
 {
     ptx::grid_launch_dependents();
-    ptx::grid_dependency_wait();
+    // Behind a kSlope kernel, which lets it start once all of its own CTAs have
+    // seen what came before them complete: the operands and norms are there, and
+    // the buffer's last reader is done. It runs under that kernel's MMAs (in turn
+    // it added 300 us to 7.0 ms at 4096 x 131072 x 4096). What follows it waits
+    // for it, and it for that kernel, at its end.
+    if (!p.early)
+        ptx::grid_dependency_wait();
     const float f = code_scale(p.type) / norm_scale(p.norms, p.norm_of);
     const long long step = static_cast<long long>(gridDim.x) * kExpandThreads;
     for (long long i = static_cast<long long>(blockIdx.x) * kExpandThreads + threadIdx.x; i < p.groups; i += step) {
         const uint4 in = __ldcg(reinterpret_cast<const uint4 *>(p.codes) + i);
-        const float s = __ldg(p.scale + (p.rowwise ? i / p.row_groups : 0)) * f;
+        const float s = power(__ldg(p.scale + (p.rowwise ? i / p.row_groups : 0))) * f;
         uint32_t w[4] = {in.x, in.y, in.z, in.w}, o[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -194,31 +225,54 @@ static __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const Exp
         to[0] = make_uint4(o[0], o[1], o[2], o[3]);
         to[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
+    if (p.early)
+        ptx::grid_dependency_wait();
 }
 
 // ----------------------------------------------------------- tile kernel ---
 
 struct Work {
     int tp, tq, split, kb0, kb1;
+    int unit_q;                        // the unit's place among its tile row's
+    bool first, last;                  // of its unit
 };
 
-// Tiles in groups of `group` tile rows that sweep all tile columns, K slices
-// innermost: the operand rows in use at a time stay in L2.
-__device__ __forceinline__ Work decode(int u, const LossParams &p)
-{
-    Work w;
-    w.split = u % p.splits;
-    const int t = u / p.splits;
-    const int in_group = p.group * p.tiles_q;
-    const int first = t / in_group * p.group;
-    const int size = min(p.tiles_p - first, p.group);
-    const int r = t % in_group;
-    w.tp = first + r % size;
-    w.tq = r / size;
-    w.kb0 = static_cast<int>(static_cast<long long>(w.split) * p.kblocks / p.splits);
-    w.kb1 = static_cast<int>(static_cast<long long>(w.split + 1) * p.kblocks / p.splits);
-    return w;
-}
+// The tiles of one CTA pair, in order. A unit is `run` tiles of a tile row (the
+// last of a row may have fewer) or one K slice of a tile; units go round-robin, in
+// groups of `group` tile rows that sweep all columns, so that the operand
+// rows in use at a time stay in L2.
+struct Schedule {
+    const LossParams &p;
+    int u, step, t;
+    __device__ __forceinline__ Schedule(const LossParams &params, int pair, int pairs) : p(params), u(pair), step(pairs), t(0) {}
+
+    __device__ __forceinline__ bool next(Work &w)
+    {
+        if (u >= p.num_units)
+            return false;
+        const int units_q = (p.tiles_q + p.run - 1) / p.run;
+        w.split = u % p.splits;
+        const int v = u / p.splits;
+        const int in_group = p.group * units_q;
+        const int start = v / in_group * p.group;
+        const int size = min(p.tiles_p - start, p.group);
+        const int r = v % in_group;
+        w.tp = start + r % size;
+        w.unit_q = r / size;
+        w.tq = w.unit_q * p.run + t;
+        w.kb0 = static_cast<int>(static_cast<long long>(w.split) * p.kblocks / p.splits);
+        w.kb1 = static_cast<int>(static_cast<long long>(w.split + 1) * p.kblocks / p.splits);
+        w.first = t == 0;
+        w.last = t + 1 == p.run || w.tq + 1 == p.tiles_q;
+        if (w.last) {
+            t = 0;
+            u += step;
+        } else {
+            ++t;
+        }
+        return true;
+    }
+};
 
 __device__ __forceinline__ float bias_at(const LossParams &p, int n)
 {
@@ -244,11 +298,21 @@ __device__ __forceinline__ float sum_rows(float (&v)[32], int lane)
     return v[0];
 }
 
-// One warp's block of 32 rows x 128 bytes into its swizzled stage: lane `row`
-// writes 16-byte chunk c at c ^ (row & 7).
+// One warp's block of 32 rows into its swizzled stage: lane `row` writes the
+// 16-byte chunk c of rows of 128 bytes, or of 64.
 __device__ __forceinline__ void stage_chunk(uint8_t *stage, int lane, int c, uint4 w)
 {
     *reinterpret_cast<uint4 *>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = w;
+}
+__device__ __forceinline__ void stage_chunk64(uint8_t *stage, int lane, int c, uint4 w)
+{
+    *reinterpret_cast<uint4 *>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = w;
+}
+
+__device__ __forceinline__ uint4 pack8(const float *v, int type)
+{
+    return make_uint4(fp8rows::pack2(v[0], v[1], type), fp8rows::pack2(v[2], v[3], type),
+                      fp8rows::pack2(v[4], v[5], type), fp8rows::pack2(v[6], v[7], type));
 }
 
 template <int KIND>
@@ -264,7 +328,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
     uint8_t *smem = smem_raw + pad;
     const uint32_t sbase = raw + pad;
-    constexpr int kStagingAt = S * C::kStageBytes, kColsAt = kStagingAt + C::kStagingBytes, kBarsAt = kColsAt + C::kColBytes;
+    constexpr int kStagingAt = S * C::kStageBytes, kColsAt = kStagingAt + C::kStagingBytes;
+    constexpr int kBarsAt = kColsAt + C::kColBytes;
     const uint32_t bar0 = sbase + kBarsAt;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
@@ -307,8 +372,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem_base = *tmem_slot;
 
     // no global memory before this
-    ptx::grid_launch_dependents();
-    ptx::grid_dependency_wait();
+    if constexpr (KIND == kSlope) {
+        ptx::grid_dependency_wait();     // (in this order: see expand_kernel)
+        ptx::grid_launch_dependents();
+    } else {
+        ptx::grid_launch_dependents();
+        ptx::grid_dependency_wait();
+    }
 
     const Waiter W{abort_flag, p.status, p.timeout_cycles};
 
@@ -319,9 +389,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             int issued = 0;
             bool ok = true;
-            for (int u = pair; ok && u < p.num_units; u += pairs) {
-                const Work w = decode(u, p);
-                const int row = w.tp * kTile + static_cast<int>(rank) * 128, col = w.tq * kTile + static_cast<int>(rank) * 128;
+            Schedule tiles(p, pair, pairs);
+            Work w;
+            while (ok && tiles.next(w)) {
+                const int row = w.tp * kTile + static_cast<int>(rank) * 128;
+                const int col = w.tq * p.width + static_cast<int>(rank) * (p.width / 2);
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     if (!W.wait(empty_bar(stage), phase ^ 1u, 0)) {
                         ok = false;
@@ -330,7 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const uint32_t sa = sbase + stage * C::kStageBytes, sb = sa + C::kABytes;
                     const uint32_t full = ptx::mapa_shared(full_bar(stage), 0);
                     if (rank == 0)
-                        ptx::mbar_arrive_expect_tx(full_bar(stage), 2u * C::kStageBytes);
+                        ptx::mbar_arrive_expect_tx(full_bar(stage), 2u * C::kABytes + 128u * static_cast<uint32_t>(p.width));
                     const int k = kb * (C::kFp8 ? 128 : 64);
                     if constexpr (C::kAMn) {
                         ptx::tma_load_3d_pair(sa, &tmap_a, full, row, k, 0);
@@ -376,8 +448,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int acc = 0;
             uint32_t acc_phase = 0;
             bool ok = true;
-            for (int u = pair; ok && u < p.num_units; u += pairs) {
-                const Work w = decode(u, p);
+            Schedule tiles(p, pair, pairs);
+            Work w;
+            while (ok && tiles.next(w)) {
                 if (!W.wait_cluster(tempty_bar(acc), acc_phase ^ 1u, 1))
                     break;
                 ptx::tc_fence_after();
@@ -419,30 +492,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // ---------------------------------------------------- epilogue ---
-        const int q = warp & 3, ew = warp - 2, half = ew / 4;
-        uint8_t *stage = smem + kStagingAt + ew * 4096;
-        const uint32_t stage_smem = sbase + kStagingAt + ew * 4096;
-        float *cols = reinterpret_cast<float *>(smem + kColsAt) + ew * 2 * kHalf;   // (s0, s1, b0, b1) per column pair
+        // Warp (q, part) takes the rows 32 q.. and the columns 64 part.. of the
+        // tile, in blocks of 32. (With two warps per 32 rows, of 128 columns each,
+        // a tile took 3.6 us whatever it did, K = 512: too few to cover their own
+        // latencies.)
+        const int q = warp & 3, ew = warp - 2, part = ew / 4;
+        uint8_t *stage = smem + kStagingAt + ew * C::kBlockBytes;
+        const uint32_t stage_smem = sbase + kStagingAt + ew * C::kBlockBytes;
+        float *cols = reinterpret_cast<float *>(smem + kColsAt) + ew * C::kCols * C::kColFloats;   // (s0, s1, b0, b1) per pair
+        float *col_mantissa = cols + 2 * C::kCols;
         int acc = 0;
         uint32_t acc_phase = 0;
-        float row_scale = 1.0f;        // of kSlope's g
-        float out_scale = 1.0f;
+        float slope_scale = 1.0f, out_scale = 1.0f;
         if constexpr (KIND == kSlope)
-            row_scale = kSlopeScale / norm_scale(p.norms, kNormG);
-        if constexpr (KIND == kGradA || KIND == kGradB)
+            slope_scale = kSlopeScale / norm_scale(p.norms, kNormG);
+        if constexpr (!C::kFp8)
             out_scale = p.norms ? p.factor * norm_scale(p.norms, kNormG) * norm_scale(p.norms, p.norm_of) : 1.0f;
         const float s_tensor = C::kFp8 && !p.rowwise ? __ldg(p.scale_a) * __ldg(p.scale_b) : 1.0f;
+        const float ma_tensor = C::kFp8 && !p.rowwise ? mantissa(__ldg(p.scale_a)) : 1.0f;
+        const float mb_tensor = C::kFp8 && !p.rowwise ? mantissa(__ldg(p.scale_b)) : 1.0f;
 
-        // the stage is free for the next block, and a block in it goes out
+        // the block's place is free, and a block goes out
         auto stage_free = [&]() {
             if (lane == 0)
                 ptx::bulk_wait_group_read<0>();
             __syncwarp();
         };
-        auto stage_out = [&](int x, int y, int z) {
+        auto stage_out = [&](int x, int y, int z, int x_end, int y_end) {
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && x < p.cols && y < p.rows) {
+            if (lane == 0 && x < x_end && y < y_end) {
                 if (KIND == kGradA && p.add)
                     ptx::tma_add_3d(&tmap_out, stage_smem, x, y, z);
                 else
@@ -451,144 +530,177 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         };
 
-        for (int u = pair; u < p.num_units; u += pairs) {
-            const Work w = decode(u, p);
+        // what this lane knows of its row of A: scale, lse, g, where its target is
+        float rs = 1.0f, lse = 0.0f, gs = 0.0f, ma = 1.0f, row_factor = 1.0f;
+        long long at = -1;                       // (in the piece; -1: none in it)
+        bool live = false;
+        float top = -INFINITY, sum = 0.0f;       // of the row in this unit so far
+        Schedule tiles(p, pair, pairs);
+        Work w;
+        while (tiles.next(w)) {
             const int row0 = w.tp * kTile + static_cast<int>(rank) * 128 + q * 32, row = row0 + lane;
-            const int col0 = w.tq * kTile + half * kHalf;
-            const bool in = row < p.rows;
-            float rs = 1.0f, lse = 0.0f, gs = 0.0f;
-            long long at = -1;                       // the target's column in this warp's 128
-            bool live = false;
+            const int col0 = w.tq * p.width + part * 64;
+            // (a narrow tile's last warps have one block or none)
+            const int blocks = min(2, (min(p.width, p.cols - w.tq * p.width) - part * 64 + 31) / 32);
+            // what the tile needs beside the accumulator, while the MMAs run
             if constexpr (C::kFp8) {
-                // what the tile needs beside the accumulator, while the MMAs run
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < kHalf / 32; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     const int c = i * 32 + lane, n = col0 + c;
-                    const bool there = n < p.cols;
+                    const bool there = n < p.N;
+                    const float s = there && p.rowwise ? __ldg(p.scale_b + n) : s_tensor;
                     // columns past the end: z = -inf, which adds nothing
-                    cols[(c >> 1) * 4 + (c & 1)] = there ? (p.rowwise ? __ldg(p.scale_b + n) : s_tensor) : 0.0f;
+                    cols[(c >> 1) * 4 + (c & 1)] = there ? s : 0.0f;
                     cols[(c >> 1) * 4 + 2 + (c & 1)] = there ? bias_at(p, n) : -INFINITY;
+                    if constexpr (KIND == kSlope)
+                        col_mantissa[c] = p.rowwise ? mantissa(s) : mb_tensor;
                 }
                 __syncwarp();
-                if (in) {
-                    if (p.rowwise)
-                        rs = __ldg(p.scale_a + row);
-                    const long long t = __ldg(p.target + row);
-                    live = t != p.ignore;
-                    at = live && t >= 0 && t < p.vocabulary ? t - p.col0 - col0 : -1;
-                    if constexpr (KIND == kSlope) {
-                        lse = __ldg(p.lse + row);
-                        gs = __ldg(p.dloss + static_cast<long long>(row) * p.dloss_step) * row_scale;
-                        if (live && (t < 0 || t >= p.vocabulary))
-                            gs = NAN;
+                if (w.first) {
+                    rs = 1.0f;
+                    ma = ma_tensor;
+                    gs = 0.0f;
+                    at = -1;
+                    live = false;
+                    top = -INFINITY;
+                    sum = 0.0f;
+                    if (row < p.M) {
+                        if (p.rowwise) {
+                            rs = __ldg(p.scale_a + row);
+                            ma = mantissa(rs);
+                        }
+                        const long long t = __ldg(p.target + row);
+                        live = t != p.ignore;
+                        if (live && t >= 0 && t < p.vocabulary)
+                            at = t - p.col0;
+                        if constexpr (KIND == kSlope) {
+                            lse = __ldg(p.lse + row);
+                            gs = __ldg(p.dloss + static_cast<long long>(row) * p.dloss_step) * slope_scale * ma;
+                            if (live && (t < 0 || t >= p.vocabulary))
+                                gs = NAN;
+                        }
                     }
                 }
+            } else {
+                row_factor = out_scale;
+                if (row < p.rows)
+                    row_factor = out_scale / mantissa(__ldg(p.row_scale + (p.rowwise ? row : 0)));
             }
             if (!W.wait(tfull_bar(acc), acc_phase, 5))
                 break;
             ptx::tc_fence_after();
-            const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kTile + half * kHalf);
+            const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kTile + part * 64);
 
             if constexpr (C::kFp8) {
-                float top = -INFINITY, sum = 0.0f;
-                const uint64_t rs2 = ptx::f32x2(rs, rs);
 #pragma unroll 1
-                for (int ch = 0; ch < kHalf / 32; ++ch) {
-                    if (col0 + ch * 32 >= p.cols)
-                        break;
+                for (int i = 0; i < blocks; ++i) {
+                    const int n0 = col0 + i * 32;
+                    const float *here = cols + i * 64, *here_m = col_mantissa + i * 32;
+                    const uint64_t rs2 = ptx::f32x2(rs, rs);
                     float v[32];
-                    ptx::tmem_ld_32cols(trow + ch * 32, v);
+                    ptx::tmem_ld_32cols(trow + i * 32, v);
+                    uint64_t z[16];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float4 c = *reinterpret_cast<const float4 *>(cols + (ch * 32 + i) * 2);
+                    for (int k = 0; k < 16; ++k) {
+                        const float4 c = *reinterpret_cast<const float4 *>(here + k * 4);
                         const uint64_t s2 = ptx::mul_f32x2(rs2, ptx::f32x2(c.x, c.y));
-                        ptx::unpack_f32x2(ptx::fma_f32x2(ptx::f32x2(v[i], v[i + 1]), s2, ptx::f32x2(c.z, c.w)), v[i], v[i + 1]);
+                        z[k] = ptx::fma_f32x2(ptx::f32x2(v[2 * k], v[2 * k + 1]), s2, ptx::f32x2(c.z, c.w));
+                        ptx::unpack_f32x2(z[k], v[2 * k], v[2 * k + 1]);
                     }
-                    const bool mine = at >= ch * 32 && at < ch * 32 + 32;
+                    const bool mine = at >= n0 && at < n0 + 32;
+                    const uint64_t log2e2 = ptx::f32x2(kLog2e, kLog2e);
                     if constexpr (KIND == kStats) {
                         if (mine) {
-                            float z = 0.0f;
+                            float zt = 0.0f;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                z = at == ch * 32 + i ? v[i] : z;
-                            p.target_z[row] = z;
+                            for (int k = 0; k < 32; ++k)
+                                zt = at == n0 + k ? v[k] : zt;
+                            p.target_z[row] = zt;
                         }
-                        float most = v[0];
+                        float most = top;
 #pragma unroll
-                        for (int i = 1; i < 32; ++i)
-                            most = fmaxf(most, v[i]);
-                        most = fmaxf(most, top);
+                        for (int k = 0; k < 32; ++k)
+                            most = fmaxf(most, v[k]);
                         // (a row without a finite value so far: exp(-inf - 0) = 0)
                         const float ref = most == -INFINITY ? 0.0f : most;
-                        sum *= fp8mm::ex2_approx((top - ref) * kLog2e);
+                        const uint64_t off = ptx::f32x2(-ref, -ref);
+                        uint64_t s2[2] = {0, 0};
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            float lo, hi;
+                            ptx::unpack_f32x2(ptx::mul_f32x2(ptx::add_f32x2(z[k], off), log2e2), lo, hi);
+                            s2[k & 1] = ptx::add_f32x2(s2[k & 1], ptx::f32x2(fp8mm::ex2_approx(lo), fp8mm::ex2_approx(hi)));
+                        }
+                        float s0, s1;
+                        ptx::unpack_f32x2(ptx::add_f32x2(s2[0], s2[1]), s0, s1);
+                        sum = sum * fp8mm::ex2_approx((top - ref) * kLog2e) + (s0 + s1);
                         top = most;
-                        float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            s4[i & 3] += fp8mm::ex2_approx((v[i] - ref) * kLog2e);
-                        sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
                     } else {
+                        const uint64_t off = ptx::f32x2(-lse, -lse);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[i] = live ? fp8mm::ex2_approx((v[i] - lse) * kLog2e) * gs : 0.0f;
+                        for (int k = 0; k < 16; ++k) {
+                            float lo, hi;
+                            ptx::unpack_f32x2(ptx::mul_f32x2(ptx::add_f32x2(z[k], off), log2e2), lo, hi);
+                            v[2 * k] = live ? fp8mm::ex2_approx(lo) * gs : 0.0f;
+                            v[2 * k + 1] = live ? fp8mm::ex2_approx(hi) * gs : 0.0f;
+                        }
                         if (mine) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                v[i] = at == ch * 32 + i ? v[i] - gs : v[i];
+                            for (int k = 0; k < 32; ++k)
+                                v[k] = at == n0 + k ? v[k] - gs : v[k];
                         }
-                        if ((ch & 1) == 0)
-                            stage_free();
+                        stage_free();
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            stage_chunk(stage, lane, (ch & 1) * 4 + i / 8,
-                                        make_uint4(fp8rows::pack2(v[i], v[i + 1], fp8rows::kF16),
-                                                   fp8rows::pack2(v[i + 2], v[i + 3], fp8rows::kF16),
-                                                   fp8rows::pack2(v[i + 4], v[i + 5], fp8rows::kF16),
-                                                   fp8rows::pack2(v[i + 6], v[i + 7], fp8rows::kF16)));
-                        // (the last columns may fill half a block: the store ends at p.cols)
-                        if ((ch & 1) == 1 || col0 + (ch + 1) * 32 >= p.cols)
-                            stage_out(col0 + (ch & ~1) * 32, row0, 0);
+                        for (int k = 0; k < 32; k += 8) {
+                            const float4 x = *reinterpret_cast<const float4 *>(here_m + k);
+                            const float4 y = *reinterpret_cast<const float4 *>(here_m + k + 4);
+                            const float o[8] = {v[k] * x.x, v[k + 1] * x.y, v[k + 2] * x.z, v[k + 3] * x.w,
+                                                v[k + 4] * y.x, v[k + 5] * y.y, v[k + 6] * y.z, v[k + 7] * y.w};
+                            stage_chunk64(stage, lane, k / 8, pack8(o, fp8rows::kF16));
+                        }
+                        stage_out(n0, row0, 0, p.N, p.M);
                         if (p.colsum) {
+                            // (without the row's mantissa)
+                            const float back = 1.0f / ma;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                v[k] *= back;
                             const float s = sum_rows(v, lane);
-                            const int n = col0 + ch * 32 + lane;
-                            if (row0 < p.rows && n < p.cols)
-                                __stcg(p.colsum + (row0 / 32) * p.colsum_ld + n, s);
+                            if (row0 < p.M && n0 + lane < p.N)
+                                __stcg(p.colsum + (row0 / 32) * p.colsum_ld + n0 + lane, s);
                         }
                     }
                 }
                 if constexpr (KIND == kStats) {
-                    if (in && col0 < p.cols)
-                        __stcg(p.stats + static_cast<long long>(col0 / kHalf) * p.rows + row, make_float2(top, sum));
+                    if (w.last && row < p.M)
+                        __stcg(p.stats + static_cast<long long>(w.unit_q * 4 + part) * p.M + row, make_float2(top, sum));
                 }
             } else {
                 const bool f32 = p.out_type == fp8mm::kOutF32;
+                // 32 columns of fp32 make a block, 64 of 16 bits
 #pragma unroll 1
-                for (int ch = 0; ch < kHalf / 32; ++ch) {
+                for (int i = 0; i < 2; ++i) {
                     float v[32];
-                    ptx::tmem_ld_32cols(trow + ch * 32, v);
+                    ptx::tmem_ld_32cols(trow + i * 32, v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] *= out_scale;
-                    if (f32 || (ch & 1) == 0)
+                    for (int k = 0; k < 32; ++k)
+                        v[k] *= row_factor;
+                    if (f32 || i == 0)
                         stage_free();
                     if (f32) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            stage_chunk(stage, lane, i / 4,
-                                        make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]),
-                                                   __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3])));
-                        stage_out(col0 + ch * 32, row0, w.split);
+                        for (int k = 0; k < 32; k += 4)
+                            stage_chunk(stage, lane, k / 4,
+                                        make_uint4(__float_as_uint(v[k]), __float_as_uint(v[k + 1]),
+                                                   __float_as_uint(v[k + 2]), __float_as_uint(v[k + 3])));
+                        stage_out(col0 + i * 32, row0, w.split, p.cols, p.rows);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            stage_chunk(stage, lane, (ch & 1) * 4 + i / 8,
-                                        make_uint4(fp8rows::pack2(v[i], v[i + 1], p.out_type),
-                                                   fp8rows::pack2(v[i + 2], v[i + 3], p.out_type),
-                                                   fp8rows::pack2(v[i + 4], v[i + 5], p.out_type),
-                                                   fp8rows::pack2(v[i + 6], v[i + 7], p.out_type)));
-                        if (ch & 1)
-                            stage_out(col0 + (ch - 1) * 32, row0, w.split);
+                        for (int k = 0; k < 32; k += 8)
+                            stage_chunk(stage, lane, i * 4 + k / 8, pack8(v + k, p.out_type));
+                        if (i == 1)
+                            stage_out(col0, row0, w.split, p.cols, p.rows);
                     }
                 }
             }

@@ -545,11 +545,11 @@ int64_t fp8_cross_entropy_workspace(int64_t M, int64_t N);
  *   db       = cast( dz^T (scale_a A) )     [N, K]: of B's columns, as Bt lies in memory
  *   dbias    = sum over m of dz             fp32 [N]
  *
- * z is computed again in pieces of the vocabulary, of which dz is kept as fp16
- * (scaled by a power of two: one rounding of 2^-12 relative, and what is under
- * 2^-38 of the largest |dloss| is lost); the products of dz run on 16-bit
- * tensor cores with fp16 operands (codes times scales, one rounding of 2^-12)
- * and fp32 sums. dbias is the sum of the unrounded dz.
+ * z is computed again in pieces of the vocabulary, of which dz is kept as fp16,
+ * scaled: one rounding of at most 2^-11 relative, and what is under 2^-37 of the
+ * largest |dloss| is lost. Its products run on 16-bit tensor cores with fp32 sums;
+ * their other operand, codes times powers of two, is exact (down to 2^-31 of
+ * its largest value, e5m2: 2^-39). dbias is the sum of the unrounded dz.
  *
  *   lse        what fp8_cross_entropy returned for the same operands.
  *   dloss      fp32 [M], or one value for all rows (dloss_count M or 1).

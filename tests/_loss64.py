@@ -81,9 +81,10 @@ def loss64(p: Problem, ignore=IGNORE):
     return loss, lse, torch.where(live(p.target, ignore), loss_tol, 0.0), lse_tol
 
 
-# the kernels keep dz times 2^14 / (a power of two at or below the largest |dloss|) as fp16, and codes times scales times
-# this / (a power of two at or below the largest scale)
-CODE_SCALE = {E4M3: 2.0 ** 6, E5M2: 2.0 ** -1}
+# The kernels keep dz as fp16, times the mantissas of the two scales (together in [1, 4)) and 2^12 / (a power of two at or
+# below the largest |dloss|), and codes times their scales' powers of two and this / (the largest of these powers), which
+# is exact down to fp16's smallest step.
+CODE_SCALE = {E4M3: 2.0 ** 7, E5M2: 1.0}
 
 
 def _pow2(x):
@@ -91,9 +92,9 @@ def _pow2(x):
 
 
 def _half_tol(x, unit):
-    """Bound of x's rounding to fp16 when kept as x / unit: 2^-11 of it (half a step of its 11 bits is 2^-12 to 2^-11), or half of 2^-24 units. (Products with
-    scales in fp32 before it: two roundings, 2^-23.)"""
-    return x.abs() * (2.0 ** -11 + 2.0 ** -23) + 2.0 ** -25 * unit
+    """Bound of x's rounding to fp16 when kept as x / unit: 2^-11 of it (half a step of its 11 bits is 2^-12 to 2^-11), or
+    half of 2^-24 units. Before it, five products in fp32: 5 x 2^-24."""
+    return x.abs() * (2.0 ** -11 + 5 * 2.0 ** -24) + 2.0 ** -25 * unit
 
 
 def grad64(p: Problem, lse, dloss=None, ignore=IGNORE):
@@ -115,7 +116,7 @@ def grad64(p: Problem, lse, dloss=None, ignore=IGNORE):
     # (ex2 flushes what is under 2^-126)
     dz_tol = dz_tol + 2.0 ** -126 * g.abs()[:, None]
     g_most = dloss.abs().expand(p.M)[on].max() if bool(on.any()) else torch.tensor(2.0 ** -100)
-    g_unit = max(_pow2(g_most) if float(g_most) > 0 else 0.0, 2.0 ** -100) / 2.0 ** 14
+    g_unit = max(_pow2(g_most) if float(g_most) > 0 else 0.0, 2.0 ** -100) / 2.0 ** 12
     a_unit = _pow2(p.sa.abs().max()) / CODE_SCALE[p.A.dtype]
     w_unit = _pow2(p.sb.abs().max()) / CODE_SCALE[p.Bt.dtype]
     half = dz_tol + _half_tol(dz.abs() + dz_tol, g_unit)
@@ -125,10 +126,11 @@ def grad64(p: Problem, lse, dloss=None, ignore=IGNORE):
         to 76 parts, pieces and slices of each 2^-23 of the magnitudes, and four roundings of scales."""
         both = (left.abs() + left_tol) @ (right.abs() + right_tol)
         return left @ right, both - left.abs() @ right.abs() + ((terms / 16 + 80) * 2.0 ** -23) * both
-    da = product(dz, half, w, _half_tol(w, w_unit), p.N)
-    db = product(dz.t(), half.t(), a, _half_tol(a, a_unit), p.M)
-    # sums of 32 rows by halves, of parts in chains of M / 256 + 8
-    dbias = dz.sum(dim=0), dz_tol.sum(dim=0) + (5 + p.M / 256 + 8) * 2.0 ** -24 * (dz.abs() + dz_tol).sum(dim=0)
+    # (a mantissa of up to 2 is left with the code's error)
+    da = product(dz, half, w, torch.full_like(w, 2 * 2.0 ** -25 * w_unit), p.N)
+    db = product(dz.t(), half.t(), a, torch.full_like(a, 2 * 2.0 ** -25 * a_unit), p.M)
+    # sums of 32 rows by halves, of parts in chains of M / 256 + 8; dz with a mantissa and without it: 4 roundings
+    dbias = dz.sum(dim=0), dz_tol.sum(dim=0) + (5 + p.M / 256 + 8 + 4) * 2.0 ** -24 * (dz.abs() + dz_tol).sum(dim=0)
     return (da[0], db[0], dbias[0]), (da[1], db[1], dbias[1])
 
 

@@ -48,7 +48,7 @@ def check_grad(p, out_dtype=BF16, dloss=None, parts=(True, True, True), **kw):
 
 @pytest.mark.parametrize("M,N,K", [(1, 1, 16), (1, 1000, 64), (3, 127, 16), (31, 128, 32), (33, 129, 48), (128, 256, 128),
                                    (129, 257, 144), (255, 511, 512), (256, 512, 256), (257, 513, 272), (700, 2000, 400),
-                                   (40, 40000, 80)])
+                                   (40, 40000, 80), (300, 30000, 64), (1024, 1100, 64), (1025, 300, 64), (90, 10000, 2064)])
 @pytest.mark.parametrize("rowwise", [False, True])
 def test_loss_sizes(M, N, K, rowwise):
     check_loss(Problem(M, N, K, rowwise=rowwise))
@@ -142,7 +142,8 @@ def test_target_out_of_range():
 
 @pytest.mark.parametrize("M,N,K", [(1, 1, 16), (1, 1000, 64), (2, 130, 16), (31, 128, 32), (65, 63, 48), (128, 256, 128),
                                    (129, 257, 144), (257, 513, 272), (700, 2000, 400), (2100, 100, 64), (40, 20000, 80),
-                                   (10, 3000, 1040)])
+                                   (10, 3000, 1040), (300, 10000, 64), (1024, 500, 64), (1100, 2000, 528), (20, 20000, 16),
+                                   (5000, 300, 304)])
 @pytest.mark.parametrize("rowwise", [False, True])
 def test_grad_sizes(M, N, K, rowwise):
     check_grad(Problem(M, N, K, rowwise=rowwise))

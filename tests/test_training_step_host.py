@@ -44,7 +44,7 @@ COMMON = [
 ]
 
 
-@pytest.mark.parametrize("kw,code", COMMON + [(dict(loss=None), -1), (dict(loss=AT + 2), -3), (dict(wb=2 * 4 * 8 - 1), -2)])
+@pytest.mark.parametrize("kw,code", COMMON + [(dict(loss=None), -1), (dict(loss=AT + 2), -3), (dict(wb=4 * 4 * 8 - 1), -2)])
 def test_loss_refusals(lib, kw, code):
     assert loss(lib, **kw) == code
 
@@ -80,9 +80,9 @@ def test_workspace_sizes(lib):
     assert lib.fp8_cross_entropy_workspace(0, 10) == 0
     assert lib.fp8_cross_entropy_workspace(1, 0) == -2 and lib.fp8_cross_entropy_workspace(-1, 5) == -2
     assert lib.fp8_cross_entropy_workspace(1 << 20, 1 << 21) == -2
-    # 8 bytes for each row and 128 columns, 4 for each row
+    # 8 bytes for each row and 32 columns, 4 for each row
     for M, N in ((1, 1), (7, 1000), (8192, 131072)):
-        need = -(-N // 128) * M * 8 + M * 4
+        need = -(-N // 128) * M * 32 + M * 4
         assert need <= lib.fp8_cross_entropy_workspace(M, N) < need + 512
     assert lib.fp8_cross_entropy_grad_workspace(0, 10, 16, 1, 1, 1) == 0
     assert lib.fp8_cross_entropy_grad_workspace(5, 10, 16, 0, 0, 0) == 0
