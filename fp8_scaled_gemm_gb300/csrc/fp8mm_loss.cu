@@ -52,31 +52,34 @@ uint32_t formats(int p_type, int q_type)
     return (p_type == FP8MM_TYPE_E5M2 ? 1u << 7 : 0u) | (q_type == FP8MM_TYPE_E5M2 ? 1u << 10 : 0u);
 }
 
-// Fills the tile space of a launch.
-void tile_space(LossParams &p, int64_t rows, int64_t cols, int width, int64_t kblocks, int splits, int run)
+TileSpace tile_space(int64_t rows, int64_t cols, int width, int64_t kblocks, int splits, int run)
 {
-    p.rows = static_cast<int>(rows);
-    p.cols = static_cast<int>(cols);
-    p.width = width;
-    p.kblocks = static_cast<int>(kblocks);
-    p.tiles_p = static_cast<int>(cdiv(rows, kTile));
-    p.tiles_q = static_cast<int>(cdiv(cols, width));
-    p.group = std::min(p.tiles_p, 16);
-    p.splits = splits;
-    p.run = run;
-    p.num_units = p.tiles_p * static_cast<int>(cdiv(p.tiles_q, run)) * splits;
+    TileSpace t{};
+    t.rows = static_cast<int>(rows);
+    t.cols = static_cast<int>(cols);
+    t.width = width;
+    // tiles of equal rows, in whole blocks of 32 per CTA
+    t.half = static_cast<int>(cdiv(cdiv(rows, 2 * cdiv(rows, kTile)), 32)) * 32;
+    t.kblocks = static_cast<int>(kblocks);
+    t.tiles_p = static_cast<int>(cdiv(rows, kTile));
+    t.tiles_q = static_cast<int>(cdiv(cols, width));
+    t.group = std::min(t.tiles_p, 16);
+    t.splits = splits;
+    t.run = run;
+    t.num_units = t.tiles_p * static_cast<int>(cdiv(t.tiles_q, run)) * splits;
+    return t;
 }
 
 template <int KIND>
-int launch_tiles(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, LossParams &p, int sms,
-                 cudaStream_t stream)
+int launch_tiles(const AllMaps<KIND> &maps, LossParams &p, int sms, cudaStream_t stream)
 {
     auto kern = loss_kernel<KIND>;
+    using C = Cfg<KIND>;
     static bool attr_set[kMaxDevices] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (!attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<KIND>::kSmemBytes);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
         if (e != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute");
         attr_set[dev] = true;
@@ -84,8 +87,8 @@ int launch_tiles(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap
     const int rc = device_limit(&p.status, &p.timeout_cycles);
     if (rc != FP8MM_OK)
         return rc;
-    return launch_pdl(kern, 2 * std::min(sms / 2, p.num_units), kThreads, Cfg<KIND>::kSmemBytes, stream,
-                      "cross entropy launch", ma, mb, mo, p);
+    const int units = p.t[0].num_units + (KIND == kGrad ? p.t[1].num_units : 0);
+    return launch_pdl(kern, 2 * std::min(sms / 2, units), C::kThreads, C::kSmemBytes, stream, "cross entropy launch", maps, p);
 }
 
 // Tiles of the product z [M, N]: their width, and how many of a row are one unit.
@@ -100,7 +103,7 @@ struct TileChoice {
 // sum stay in registers: 16 units a pair keep the last turn short.
 TileChoice choose_tiles(int64_t M, int64_t N, int sms)
 {
-    const int64_t pairs = sms / 2, rows = std::min<int64_t>(M, kTile);
+    const int64_t pairs = sms / 2, rows = cdiv(cdiv(M, cdiv(M, kTile)), 64) * 64;
     TileChoice best{kTile, 1};
     int64_t cost = INT64_MAX;
     for (int width = kTile; width >= 128; width -= 32) {
@@ -122,15 +125,15 @@ int64_t most_parts(int64_t N) { return cdiv(N, 128) * 4; }
 
 // The operands' maps and the tile space of z [M, N] (kStats, kSlope).
 int product_maps(const TileChoice &t, const void *A, int a_type, const void *B, int b_type, int64_t M, int64_t N, int64_t K,
-                 CUtensorMap &ma, CUtensorMap &mb, LossParams &p)
+                 Maps &m, LossParams &p)
 {
     constexpr CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    tile_space(p, M, N, t.width, cdiv(K, 128), 1, t.run);
-    p.idesc = fp8mm::ptx::idesc_e4m3_f32(kTile, t.width) | formats(a_type, b_type);
+    p.t[0] = tile_space(M, N, t.width, cdiv(K, 128), 1, t.run);
+    p.t[0].idesc = fp8mm::ptx::idesc_e4m3_f32(kTile, t.width) | formats(a_type, b_type);
     p.M = static_cast<int>(M);
     p.N = static_cast<int>(N);
-    const int rc = map_matrix(&ma, u8, 1, A, M, K, K, 128);
-    return rc != FP8MM_OK ? rc : map_matrix(&mb, u8, 1, B, N, K, K, t.width / 2);
+    const int rc = map_matrix(&m.a, u8, 1, A, M, K, K, p.t[0].half);
+    return rc != FP8MM_OK ? rc : map_matrix(&m.b, u8, 1, B, N, K, K, t.width / 2);
 }
 
 // K slices of a gradient product of `kblocks` blocks of 64: the number that
@@ -197,35 +200,6 @@ int zero(void *p, int64_t bytes, cudaStream_t s)
     return e == cudaSuccess ? FP8MM_OK : cuda_fail(e, "cudaMemsetAsync(gradient)");
 }
 
-int expand(const void *codes, const float *scale, int rowwise, int type, int norm_of, const uint32_t *norms, void *out,
-           int64_t rows, int64_t K, int sms, cudaStream_t s)   // behind a kSlope kernel, or another of these
-{
-    ExpandParams e{};
-    e.codes = static_cast<const uint8_t *>(codes);
-    e.scale = scale;
-    e.rowwise = rowwise;
-    e.type = type;
-    e.norm_of = norm_of;
-    e.norms = norms;
-    e.out = static_cast<__half *>(out);
-    e.groups = rows * (K / 16);
-    e.row_groups = static_cast<int>(K / 16);
-    e.early = 1;
-    // the same division of an SM's memory as the kernel it runs beside
-    static bool attr_set[kMaxDevices] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (!attr_set[dev]) {
-        const cudaError_t err = cudaFuncSetAttribute(expand_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                                     cudaSharedmemCarveoutMaxShared);
-        if (err != cudaSuccess)
-            return cuda_fail(err, "cudaFuncSetAttribute");
-        attr_set[dev] = true;
-    }
-    return launch_grid2(expand_kernel, std::min<int64_t>(cdiv(e.groups, kExpandThreads), static_cast<int64_t>(sms) * 8), 1,
-                        kExpandThreads, s, "fp16 operand launch", e);
-}
-
 int finish(const void *parts, int64_t n, int count, int out_type, int norm_of, const uint32_t *norms, float factor,
            void *out, int sms, cudaStream_t s)
 {
@@ -277,8 +251,8 @@ int fp8_cross_entropy(const void *A, int a_type, const void *B, int b_type, cons
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const TileChoice t = choose_tiles(M, N, sms);
     LossParams p{};
-    CUtensorMap mp, mq;
-    if ((rc = product_maps(t, A, a_type, B, b_type, M, N, K, mp, mq, p)) != FP8MM_OK)
+    AllMaps<kStats> maps{};
+    if ((rc = product_maps(t, A, a_type, B, b_type, M, N, K, maps.of[0], p)) != FP8MM_OK)
         return rc;
     p.scale_a = scale_a;
     p.scale_b = scale_b;
@@ -290,7 +264,7 @@ int fp8_cross_entropy(const void *A, int a_type, const void *B, int b_type, cons
     p.vocabulary = N;
     p.stats = static_cast<float2 *>(workspace);
     p.target_z = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + stats_bytes(M, N));
-    if ((rc = launch_tiles<kStats>(mp, mq, mp, p, sms, s)) != FP8MM_OK)
+    if ((rc = launch_tiles<kStats>(maps, p, sms, s)) != FP8MM_OK)
         return rc;
     CombineParams c{};
     c.stats = p.stats;
@@ -358,7 +332,6 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
     uint32_t *norms = reinterpret_cast<uint32_t *>(ws + g.norms);
     const int rowwise = scale_mode == FP8MM_SCALE_ROWWISE;
     const CUtensorMapDataType out_map = out_type == FP8MM_OUT_F32 ? kF32 : out_type == FP8MM_OUT_F16 ? kF16 : kB16;
-    const int out_box = 32;
     // what comes off dz W16 and dz^T H16 beside the norms
     const float factor_a = 1.0f / (kSlopeScale * code_scale(b_type)), factor_b = 1.0f / (kSlopeScale * code_scale(a_type));
 
@@ -377,23 +350,13 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
     if ((rc = launch_grid2(norms_kernel, kNormParts, 3, kNormThreads, s, "cross entropy norms launch", n)) != FP8MM_OK)
         return rc;
 
-    CUtensorMap mh, parts_a;
-    if (db && (rc = map_matrix(&mh, kF16, 2, ws + g.h16, M, K, K, 64)) != FP8MM_OK)
-        return rc;
-    if (da) {
-        rc = g.parts_a ? map_matrix(&parts_a, kF32, 4, ws + g.parts_a_at, M, K, K, out_box, g.split_a)
-                       : map_matrix(&parts_a, out_map, es, da, M, K, K, out_box);
-        if (rc != FP8MM_OK)
-            return rc;
-    }
     for (int64_t i = 0; i < g.pieces; ++i) {
         const int64_t n0 = i * g.piece, nv = std::min(g.piece, N - n0);
         const uint8_t *Bi = static_cast<const uint8_t *>(B) + n0 * K;
         const float *sbi = scale_b + (rowwise ? n0 : 0);
-        const TileChoice t = choose_tiles(M, nv, sms);
-        CUtensorMap mp, mq, mdz;
         LossParams p{};
-        if ((rc = product_maps(t, A, a_type, Bi, b_type, M, nv, K, mp, mq, p)) != FP8MM_OK)
+        AllMaps<kSlope> maps{};
+        if ((rc = product_maps(choose_tiles(M, nv, sms), A, a_type, Bi, b_type, M, nv, K, maps.of[0], p)) != FP8MM_OK)
             return rc;
         p.scale_a = scale_a;
         p.scale_b = sbi;
@@ -410,14 +373,14 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
         p.colsum = dbias ? reinterpret_cast<float *>(ws + g.colsum) : nullptr;
         p.colsum_ld = g.piece;
         p.norms = norms;
+        p.w16 = da ? reinterpret_cast<__half *>(ws + g.w16) : nullptr;
+        p.h16 = db && i == 0 ? reinterpret_cast<__half *>(ws + g.h16) : nullptr;
+        p.K = static_cast<int>(K);
+        p.a_type = a_type;
+        p.b_type = b_type;
         // dz [M, nv] with rows of `piece` elements, written in blocks of 32 x 32
-        if ((rc = map_matrix(&mdz, kF16, 2, ws + g.dz, M, nv, g.piece, 32, 1, 0, 64)) != FP8MM_OK)
-            return rc;
-        if ((rc = launch_tiles<kSlope>(mp, mq, mdz, p, sms, s)) != FP8MM_OK)
-            return rc;
-        if (da && (rc = expand(Bi, sbi, rowwise, b_type, kNormB, norms, ws + g.w16, nv, K, sms, s)) != FP8MM_OK)
-            return rc;
-        if (db && i == 0 && (rc = expand(A, scale_a, rowwise, a_type, kNormA, norms, ws + g.h16, M, K, sms, s)) != FP8MM_OK)
+        if ((rc = map_matrix(&maps.of[0].out, kF16, 2, ws + g.dz, M, nv, g.piece, 32, 1, 0, 64)) != FP8MM_OK ||
+            (rc = launch_tiles<kSlope>(maps, p, sms, s)) != FP8MM_OK)
             return rc;
         if (dbias) {
             ColumnsParams c{};
@@ -430,45 +393,48 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
             if ((rc = launch_grid2(columns_kernel, cdiv(nv, 32), 1, kColumnsThreads, s, "bias gradient sum launch", c)) != FP8MM_OK)
                 return rc;
         }
+        if (!da && !db)
+            continue;
         LossParams o{};
+        AllMaps<kGrad> to{};
         o.rowwise = rowwise;
+        o.norms = norms;
         if (da) {
-            CUtensorMap mz, mw;
-            if ((rc = map_matrix(&mz, kF16, 2, ws + g.dz, M, nv, g.piece, 128)) != FP8MM_OK ||
-                (rc = map_matrix(&mw, kF16, 2, ws + g.w16, nv, K, K, 64)) != FP8MM_OK)
-                return rc;
             // (a last piece with fewer blocks than slices adds to the first partials only)
-            tile_space(o, M, K, kTile, cdiv(nv, 64), static_cast<int>(std::min<int64_t>(g.split_a, cdiv(nv, 64))), 1);
-            o.row_scale = scale_a;
-            o.idesc = fp8mm::ptx::idesc_f16_f32(kTile, kTile, false, true);
-            o.norms = g.parts_a ? nullptr : norms;
-            o.factor = factor_a;
-            o.norm_of = kNormB;
-            o.out_type = g.parts_a ? FP8MM_OUT_F32 : out_type;
-            o.add = i > 0;
-            if ((rc = launch_tiles<kGradA>(mz, mw, parts_a, o, sms, s)) != FP8MM_OK)
+            TileSpace &t = o.t[kOfA];
+            t = tile_space(M, K, kTile, cdiv(nv, 64), static_cast<int>(std::min<int64_t>(g.split_a, cdiv(nv, 64))), 1);
+            t.idesc = fp8mm::ptx::idesc_f16_f32(kTile, kTile, false, true);
+            Maps &m = to.of[kOfA];
+            if ((rc = map_matrix(&m.a, kF16, 2, ws + g.dz, M, nv, g.piece, t.half)) != FP8MM_OK ||
+                (rc = map_matrix(&m.b, kF16, 2, ws + g.w16, nv, K, K, 64)) != FP8MM_OK ||
+                (rc = g.parts_a ? map_matrix(&m.out, kF32, 4, ws + g.parts_a_at, M, K, K, 32, g.split_a)
+                                : map_matrix(&m.out, out_map, es, da, M, K, K, 32)) != FP8MM_OK)
                 return rc;
+            o.r[kOfA] = {!g.parts_a, factor_a, kNormB, scale_a, g.parts_a ? FP8MM_OUT_F32 : out_type, i > 0};
         }
+        uint8_t *dbi = db ? static_cast<uint8_t *>(db) + n0 * K * es : nullptr;
         if (db) {
-            uint8_t *dbi = static_cast<uint8_t *>(db) + n0 * K * es;
-            CUtensorMap mz, mo;
-            rc = g.parts_b ? map_matrix(&mo, kF32, 4, ws + g.parts_b_at, nv, K, K, out_box, g.split_b)
-                           : map_matrix(&mo, out_map, es, dbi, nv, K, K, out_box);
-            if (rc != FP8MM_OK || (rc = map_matrix(&mz, kF16, 2, ws + g.dz, M, nv, g.piece, 64)) != FP8MM_OK)
+            TileSpace &t = o.t[kOfB];
+            t = tile_space(nv, K, kTile, cdiv(M, 64), g.split_b, 1);
+            t.half = 128;              // (MN-major rows come in boxes of 64)
+            t.idesc = fp8mm::ptx::idesc_f16_f32(kTile, kTile, true, true);
+            Maps &m = to.of[kOfB];
+            if ((rc = map_matrix(&m.a, kF16, 2, ws + g.dz, M, nv, g.piece, 64)) != FP8MM_OK ||
+                (rc = map_matrix(&m.b, kF16, 2, ws + g.h16, M, K, K, 64)) != FP8MM_OK ||
+                (rc = g.parts_b ? map_matrix(&m.out, kF32, 4, ws + g.parts_b_at, nv, K, K, 32, g.split_b)
+                                : map_matrix(&m.out, out_map, es, dbi, nv, K, K, 32)) != FP8MM_OK)
                 return rc;
-            tile_space(o, nv, K, kTile, cdiv(M, 64), g.split_b, 1);
-            o.row_scale = sbi;
-            o.idesc = fp8mm::ptx::idesc_f16_f32(kTile, kTile, true, true);
-            o.norms = g.parts_b ? nullptr : norms;
-            o.factor = factor_b;
-            o.norm_of = kNormA;
-            o.out_type = g.parts_b ? FP8MM_OUT_F32 : out_type;
-            o.add = 0;
-            if ((rc = launch_tiles<kGradB>(mz, mh, mo, o, sms, s)) != FP8MM_OK)
-                return rc;
-            if (g.parts_b && (rc = finish(ws + g.parts_b_at, nv * K, g.split_b, out_type, kNormA, norms, factor_b, dbi, sms, s)) != FP8MM_OK)
-                return rc;
+            o.r[kOfB] = {!g.parts_b, factor_b, kNormA, sbi, g.parts_b ? FP8MM_OUT_F32 : out_type, 0};
         }
+        // (the maps of a product that is not wanted have no tiles)
+        if (!da)
+            to.of[kOfA] = to.of[kOfB];
+        if (!db)
+            to.of[kOfB] = to.of[kOfA];
+        if ((rc = launch_tiles<kGrad>(to, o, sms, s)) != FP8MM_OK)
+            return rc;
+        if (g.parts_b && (rc = finish(ws + g.parts_b_at, nv * K, g.split_b, out_type, kNormA, norms, factor_b, dbi, sms, s)) != FP8MM_OK)
+            return rc;
     }
     if (g.parts_a)
         return finish(ws + g.parts_a_at, M * K, g.split_a, out_type, kNormB, norms, factor_a, da, sms, s);

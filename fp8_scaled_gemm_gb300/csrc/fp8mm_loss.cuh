@@ -7,7 +7,7 @@
 //   dz[m, n] = (exp(z[m, n] - lse[m]) - [n = t[m]]) g[m]
 //   dA = dz (s_b B)^T,   dB^T = dz^T (s_a A),   dbias = sum_m dz
 //
-// One kernel in four kinds, all with 2-SM MMAs on tiles of 256 rows (a cluster of
+// One kernel in three kinds, all with 2-SM MMAs on tiles of 256 rows (a cluster of
 // two CTAs; roles, ring and barriers as in fp8mm_kernel_pair.cuh):
 //
 //   kStats  the product z of fp8 operands. Each epilogue warp reduces its quarter
@@ -16,10 +16,12 @@
 //           target writes its z. combine_kernel joins a row's parts in a fixed
 //           order.
 //   kSlope  the same product again for a piece of the vocabulary; the epilogue
-//           writes dz as fp16 (and sums of it over 32 rows for dbias).
-//   kGradA  dA = dz W16: the contraction runs over the vocabulary. dz is read
-//           K-major, W16 [n, K] (the piece of B in fp16) MN-major.
-//   kGradB  dB^T = dz^T H16 over the rows; both operands MN-major.
+//           writes dz as fp16 (and sums of it over 32 rows for dbias), and eight
+//           more warps write the other operands of kGrad, W16 and H16.
+//   kGrad   dA = dz W16, whose contraction runs over the vocabulary: dz K-major,
+//           W16 [n, K] (the piece of B in fp16) MN-major; and dB^T = dz^T H16 over
+//           the rows, both MN-major. One launch for both: the tiles of one fill what
+//           the other's last turn leaves, and few rows pay for one kernel's start.
 //
 // Recomputing z costs 2 M N K flops at the fp8 rate; keeping it would cost
 // 2 to 4 bytes of memory per logit, written and read (M = 8192, N = 131072:
@@ -42,6 +44,9 @@
 // other one comes off its row of the result in fp32: one dz' serves both.
 #pragma once
 
+#include <climits>
+#include <type_traits>
+
 #include "fp8mm_kernel.cuh"
 #include "fp8mm_rows.cuh"
 
@@ -50,19 +55,20 @@ namespace fp8loss {
 namespace ptx = fp8mm::ptx;
 using fp8mm::Waiter;
 
-enum Kind { kStats, kSlope, kGradA, kGradB };
+enum Kind { kStats, kSlope, kGrad };
+constexpr int kOfA = 0, kOfB = 1;      // kGrad's two products
 
 constexpr int kTile = 256;             // rows and columns of a CTA pair's tile
 constexpr int kEpiWarps = 16;           // four per 32 rows of a tile, two blocks of 32 columns each (256 wide)
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kConvertWarps = 8;       // kSlope
 constexpr int kNormParts = 32;         // partial maxima per norm
 
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int KIND>
 struct Cfg {
-    static constexpr bool kFp8 = KIND == kStats || KIND == kSlope;
-    static constexpr bool kAMn = KIND == kGradB, kBMn = !kFp8;
+    static constexpr bool kFp8 = KIND != kGrad;
+    static constexpr int kThreads = 64 + 32 * (kEpiWarps + (KIND == kSlope ? kConvertWarps : 0));
     static constexpr int kABytes = 128 * 128;
     static constexpr int kStageBytes = 2 * kABytes;                            // 128 rows of A, up to 128 of B
     static constexpr int kStages = KIND == kStats ? 6 : 5;
@@ -73,22 +79,49 @@ struct Cfg {
     static constexpr int kColFloats = KIND == kStats ? 2 : KIND == kSlope ? 3 : 0;
     static constexpr int kCols = kTile / 4;
     static constexpr int kColBytes = kEpiWarps * kCols * kColFloats * 4;
-    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + kColBytes + 256;
+    static constexpr int kPowerBytes = KIND == kSlope ? kConvertWarps * 32 * 4 : 0;   // see load_powers
+    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + kColBytes + kPowerBytes + 256;
     static_assert(kSmemBytes <= 232448, "exceeds 227 KB of shared memory");
 };
 
-struct LossParams {
-    // tile space: 256 rows x `width` columns a tile (a multiple of 32; 256 for the gradients)
-    int rows, cols, width;
+// The tensor maps of a product's operands and output.
+struct Maps {
+    CUtensorMap a, b, out;
+};
+template <int KIND>
+struct AllMaps {
+    Maps of[KIND == kGrad ? 2 : 1];
+};
+
+// Tiles of 2 x `half` rows (128, or less of few rows: a multiple of 32) and
+// `width` columns (a multiple of 32; 256 for the gradients). The MMA's other rows hold
+// what was in shared memory and are not looked at.
+struct TileSpace {
+    int rows, cols, half, width;
     int kblocks;                       // of 128 bytes of contraction
     int tiles_p, tiles_q, group, splits, run, num_units;
     uint32_t idesc;
+};
+
+// One of kGrad's products.
+struct Result {
+    int scaled;                        // apply the norms (else a sum of partials does)
+    float factor;                      // beside the norms
+    int norm_of;                       // dA: kNormB, dB: kNormA
+    const float *row_scale;            // of the result's rows: scale_a, or scale_b from the piece on
+    int out_type;
+    int add;                           // add to the output (fp32)
+};
+
+struct LossParams {
+    TileSpace t[2];                    // kGrad: of dA and dB; else the first
     int *status;
     unsigned long long timeout_cycles;
+    int rowwise;
+    const uint32_t *norms;             // see norm_scale
     // fp8 kinds (column vectors start at the piece)
     int M, N;
     const float *scale_a, *scale_b;
-    int rowwise;
     const void *bias;
     int bias_type;
     const int64_t *target;
@@ -102,13 +135,10 @@ struct LossParams {
     int dloss_step;                    // 0: one value for all rows
     float *colsum;                     // [ceil(M / 32)][n], or nullptr
     long long colsum_ld;
-    // kSlope, kGradA, kGradB
-    const uint32_t *norms;             // see norm_scale; gradients: nullptr where a sum of partials applies them
-    float factor;                      // of the result, beside the norms
-    int norm_of;                       // kGradA: kNormB, kGradB: kNormA
-    const float *row_scale;            // of the result's rows: scale_a, or scale_b from the piece on
-    int out_type;
-    int add;                           // kGradA: add to the output (fp32)
+    __half *w16, *h16;                 // [n, K] and [M, K], or nullptr: not wanted
+    int K, a_type, b_type;
+    // kGrad
+    Result r[2];
 };
 
 // ------------------------------------------------------------------ norms ---
@@ -178,60 +208,10 @@ __device__ __forceinline__ float mantissa(float s)
 }
 __device__ __forceinline__ float power(float s) { return __uint_as_float(__float_as_uint(s) & 0x7F800000u); }
 
-// ----------------------------------------------------- fp8 codes to fp16 ---
-// out[r, :] = fp16( code[r, :] 2^e(s[r]) f / S ): 16 codes a thread.
-
-struct ExpandParams {
-    const uint8_t *codes;
-    const float *scale;
-    int rowwise, type, norm_of;
-    const uint32_t *norms;
-    __half *out;
-    long long groups;                  // rows x K / 16
-    int row_groups;                    // K / 16
-    int early;                         // nothing here depends on the kernel before it
-};
-
-constexpr int kExpandThreads = 256;
-
-static __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const ExpandParams p)
-{
-    ptx::grid_launch_dependents();
-    // Behind a kSlope kernel, which lets it start once all of its own CTAs have
-    // seen what came before them complete: the operands and norms are there, and
-    // the buffer's last reader is done. It runs under that kernel's MMAs (in turn
-    // it added 300 us to 7.0 ms at 4096 x 131072 x 4096). What follows it waits
-    // for it, and it for that kernel, at its end.
-    if (!p.early)
-        ptx::grid_dependency_wait();
-    const float f = code_scale(p.type) / norm_scale(p.norms, p.norm_of);
-    const long long step = static_cast<long long>(gridDim.x) * kExpandThreads;
-    for (long long i = static_cast<long long>(blockIdx.x) * kExpandThreads + threadIdx.x; i < p.groups; i += step) {
-        const uint4 in = __ldcg(reinterpret_cast<const uint4 *>(p.codes) + i);
-        const float s = power(__ldg(p.scale + (p.rowwise ? i / p.row_groups : 0))) * f;
-        uint32_t w[4] = {in.x, in.y, in.z, in.w}, o[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint16_t two = static_cast<uint16_t>(w[k / 2] >> (16 * (k % 2)));
-            uint32_t h;
-            if (p.type == 0)
-                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-            else
-                asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(two));
-            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-            o[k] = fp8rows::pack2(v.x * s, v.y * s, fp8rows::kF16);
-        }
-        uint4 *to = reinterpret_cast<uint4 *>(p.out) + 2 * i;
-        to[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        to[1] = make_uint4(o[4], o[5], o[6], o[7]);
-    }
-    if (p.early)
-        ptx::grid_dependency_wait();
-}
-
 // ----------------------------------------------------------- tile kernel ---
 
 struct Work {
+    int of;                            // kGrad: kOfA or kOfB
     int tp, tq, split, kb0, kb1;
     int unit_q;                        // the unit's place among its tile row's
     bool first, last;                  // of its unit
@@ -241,6 +221,7 @@ struct Work {
 // last of a row may have fewer) or one K slice of a tile; units go round-robin, in
 // groups of `group` tile rows that sweep all columns, so that the operand
 // rows in use at a time stay in L2.
+template <int KIND>
 struct Schedule {
     const LossParams &p;
     int u, step, t;
@@ -248,22 +229,29 @@ struct Schedule {
 
     __device__ __forceinline__ bool next(Work &w)
     {
-        if (u >= p.num_units)
+        int v = u;
+        w.of = kOfA;
+        if (KIND == kGrad && v >= p.t[0].num_units) {
+            v -= p.t[0].num_units;
+            w.of = kOfB;
+        }
+        const TileSpace &s = p.t[KIND == kGrad ? w.of : 0];
+        if (v >= s.num_units)
             return false;
-        const int units_q = (p.tiles_q + p.run - 1) / p.run;
-        w.split = u % p.splits;
-        const int v = u / p.splits;
-        const int in_group = p.group * units_q;
-        const int start = v / in_group * p.group;
-        const int size = min(p.tiles_p - start, p.group);
+        const int units_q = (s.tiles_q + s.run - 1) / s.run;
+        w.split = v % s.splits;
+        v /= s.splits;
+        const int in_group = s.group * units_q;
+        const int start = v / in_group * s.group;
+        const int size = min(s.tiles_p - start, s.group);
         const int r = v % in_group;
         w.tp = start + r % size;
         w.unit_q = r / size;
-        w.tq = w.unit_q * p.run + t;
-        w.kb0 = static_cast<int>(static_cast<long long>(w.split) * p.kblocks / p.splits);
-        w.kb1 = static_cast<int>(static_cast<long long>(w.split + 1) * p.kblocks / p.splits);
+        w.tq = w.unit_q * s.run + t;
+        w.kb0 = static_cast<int>(static_cast<long long>(w.split) * s.kblocks / s.splits);
+        w.kb1 = static_cast<int>(static_cast<long long>(w.split + 1) * s.kblocks / s.splits);
         w.first = t == 0;
-        w.last = t + 1 == p.run || w.tq + 1 == p.tiles_q;
+        w.last = t + 1 == s.run || w.tq + 1 == s.tiles_q;
         if (w.last) {
             t = 0;
             u += step;
@@ -274,6 +262,81 @@ struct Schedule {
     }
 };
 
+// The K blocks of a tile that kSlope's converting warps take: of its rows of B and of
+// A. The tiles that share rows share their blocks in turn.
+struct Converted {
+    int a, b, step_a, step_b;
+    bool of_a, of_b;                   // of the block that has() was last asked for
+    __device__ __forceinline__ Converted(const LossParams &p, const Work &w)
+        : a(p.h16 ? w.tq : INT_MAX), b(p.w16 ? w.tp : INT_MAX), step_a(p.t[0].tiles_q), step_b(p.t[0].tiles_p), of_a(false), of_b(false)
+    {
+    }
+    // (for each block in order)
+    __device__ __forceinline__ bool has(int kb)
+    {
+        of_a = kb == a;
+        of_b = kb == b;
+        if (of_a)
+            a += step_a;
+        if (of_b)
+            b += step_b;
+        return of_a || of_b;
+    }
+};
+
+// A converting warp's rows of a stage are 16 i + 2 warp + (0 or 1), i < 8: 16 lanes a
+// row, 8 codes each, so that it writes 2 x 256 bytes at once. It takes its codes
+// into registers, which gives the stage back early, then converts and writes them.
+//
+// `powers` holds 2^e(scale) f / S of the warp's rows as two fp16 (below 2^-24: 0), row
+// 16 i + 2 warp + j at 2 i + j.
+__device__ __forceinline__ void load_powers(uint32_t *powers, int row0, int rows, const float *scale, int rowwise, float f,
+                                            int warp, int lane)
+{
+    if (lane >= 16)
+        return;
+    const int row = row0 + (lane >> 1) * 16 + 2 * warp + (lane & 1);
+    const __half2 s = __float2half2_rn(row < rows ? power(__ldg(scale + (rowwise ? row : 0))) * f : 0.0f);
+    powers[lane] = *reinterpret_cast<const uint32_t *>(&s);
+}
+
+__device__ __forceinline__ void take_rows(uint2 (&codes)[8], const uint8_t *stage, int warp, int lane)
+{
+    const int c = lane & 15, r = 2 * warp + (lane >> 4);
+    const uint8_t *from = stage + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        codes[i] = *reinterpret_cast<const uint2 *>(from + i * 2048);
+}
+
+template <bool E4M3>
+__device__ __forceinline__ void write_rows(const uint2 (&codes)[8], int count, __half *out, int row0, int rows, int k0, int K,
+                                           const uint32_t *powers, int warp, int lane)
+{
+    const int j = lane >> 4, r = 2 * warp + j, k = k0 + (lane & 15) * 8;
+    __half *to = out + static_cast<long long>(row0 + r) * K + k;
+    // this lane's rows: 16 i < left (K is a multiple of 16)
+    const int left = k < K ? min(count, rows - row0) - r : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (16 * i >= left)
+            break;
+        const uint32_t s = powers[2 * i + j];
+        uint32_t o[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const uint16_t two = static_cast<uint16_t>((h < 2 ? codes[i].x : codes[i].y) >> (16 * (h & 1)));
+            if constexpr (E4M3)
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[h]) : "h"(two));
+            else
+                asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(o[h]) : "h"(two));
+            const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&o[h]), *reinterpret_cast<const __half2 *>(&s));
+            o[h] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+        __stcg(reinterpret_cast<uint4 *>(to + static_cast<long long>(16 * i) * K), make_uint4(o[0], o[1], o[2], o[3]));
+    }
+}
+
 __device__ __forceinline__ float bias_at(const LossParams &p, int n)
 {
     float v[1];
@@ -281,13 +344,16 @@ __device__ __forceinline__ float bias_at(const LossParams &p, int n)
     return v[0];
 }
 
-// Sums of 32 columns over a warp's 32 rows: v[i] is this lane's row at column
-// i, the result column `lane`'s sum. Each step adds the halves that the other
-// lane keeps, so 31 shuffles serve all columns.
-__device__ __forceinline__ float sum_rows(float (&v)[32], int lane)
+// Sums of 16 columns over a warp's 32 rows: v[i] is this lane's row at column i,
+// the result column `lane & 15`'s sum. The lanes' halves are added, then each step
+// adds the half of the columns that the other lane keeps.
+__device__ __forceinline__ float sum_rows(float (&v)[16], int lane)
 {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int i = 0; i < 16; ++i)
+        v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
@@ -296,6 +362,25 @@ __device__ __forceinline__ float sum_rows(float (&v)[32], int lane)
         }
     }
     return v[0];
+}
+
+// z of N columns of a row from the accumulator: times the scales, plus the bias.
+template <int N>
+__device__ __forceinline__ void logits(float (&v)[N], const float *cols, float row_scale)
+{
+    const uint64_t rs2 = ptx::f32x2(row_scale, row_scale);
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+        const float4 c = *reinterpret_cast<const float4 *>(cols + k * 2);
+        const uint64_t s2 = ptx::mul_f32x2(rs2, ptx::f32x2(c.x, c.y));
+        ptx::unpack_f32x2(ptx::fma_f32x2(ptx::f32x2(v[k], v[k + 1]), s2, ptx::f32x2(c.z, c.w)), v[k], v[k + 1]);
+    }
+}
+
+// (v - off) log2(e) of two columns.
+__device__ __forceinline__ void exponents(float v0, float v1, uint64_t minus_off, float &lo, float &hi)
+{
+    ptx::unpack_f32x2(ptx::mul_f32x2(ptx::add_f32x2(ptx::f32x2(v0, v1), minus_off), ptx::f32x2(kLog2e, kLog2e)), lo, hi);
 }
 
 // One warp's block of 32 rows into its swizzled stage: lane `row` writes the
@@ -316,9 +401,8 @@ __device__ __forceinline__ uint4 pack8(const float *v, int type)
 }
 
 template <int KIND>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    loss_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-                const __grid_constant__ CUtensorMap tmap_out, const LossParams p)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads, 1)
+    loss_kernel(const __grid_constant__ AllMaps<KIND> maps, const __grid_constant__ LossParams p)
 {
     using C = Cfg<KIND>;
     constexpr int S = C::kStages;
@@ -329,7 +413,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t *smem = smem_raw + pad;
     const uint32_t sbase = raw + pad;
     constexpr int kStagingAt = S * C::kStageBytes, kColsAt = kStagingAt + C::kStagingBytes;
-    constexpr int kBarsAt = kColsAt + C::kColBytes;
+    constexpr int kPowersAt = kColsAt + C::kColBytes, kBarsAt = kPowersAt + C::kPowerBytes;
     const uint32_t bar0 = sbase + kBarsAt;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
@@ -338,7 +422,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t done_bar = bar0 + 8u * (2 * S + 4);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kBarsAt + 8 * (2 * S + 5));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    static_assert(8 * (2 * S + 6) <= 256, "barrier area");
+    // kSlope: the MMA is done with a stage that is to be converted; warps that have it
+    auto used_bar = [&](int s) { return bar0 + 8u * (2 * S + 6 + s); };
+    int *taken = reinterpret_cast<int *>(smem + kBarsAt + 8 * (3 * S + 6));
+    static_assert(8 * (3 * S + 6) + 4 * S <= 256, "barrier area");
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -348,7 +435,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             ptx::mbar_init(full_bar(s), 1);
+            // (one arrival: the MMA's, or of a converted stage the last warp's that took it)
             ptx::mbar_init(empty_bar(s), 1);
+            ptx::mbar_init(used_bar(s), 1);
+            taken[s] = 0;
         }
         for (int a = 0; a < 2; ++a) {
             ptx::mbar_init(tfull_bar(a), 1);
@@ -357,10 +447,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::mbar_init(done_bar, 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
-        ptx::prefetch_tmap(&tmap_a);
-        ptx::prefetch_tmap(&tmap_b);
-        if constexpr (KIND != kStats)
-            ptx::prefetch_tmap(&tmap_out);
+        for (const Maps &m : maps.of) {
+            ptx::prefetch_tmap(&m.a);
+            ptx::prefetch_tmap(&m.b);
+            if constexpr (KIND != kStats)
+                ptx::prefetch_tmap(&m.out);
+        }
     }
     if (warp == 1) {
         ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), 2 * kTile);
@@ -372,13 +464,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem_base = *tmem_slot;
 
     // no global memory before this
-    if constexpr (KIND == kSlope) {
-        ptx::grid_dependency_wait();     // (in this order: see expand_kernel)
-        ptx::grid_launch_dependents();
-    } else {
-        ptx::grid_launch_dependents();
-        ptx::grid_dependency_wait();
-    }
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
 
     const Waiter W{abort_flag, p.status, p.timeout_cycles};
 
@@ -389,39 +476,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             int issued = 0;
             bool ok = true;
-            Schedule tiles(p, pair, pairs);
+            Schedule<KIND> tiles(p, pair, pairs);
             Work w;
             while (ok && tiles.next(w)) {
-                const int row = w.tp * kTile + static_cast<int>(rank) * 128;
-                const int col = w.tq * p.width + static_cast<int>(rank) * (p.width / 2);
-                for (int kb = w.kb0; kb < w.kb1; ++kb) {
-                    if (!W.wait(empty_bar(stage), phase ^ 1u, 0)) {
-                        ok = false;
-                        break;
+                const TileSpace &t = p.t[KIND == kGrad ? w.of : 0];
+                const Maps &m = maps.of[KIND == kGrad ? w.of : 0];
+                const int row = (2 * w.tp + static_cast<int>(rank)) * t.half;
+                const int col = w.tq * t.width + static_cast<int>(rank) * (t.width / 2);
+                const uint32_t bytes = 128u * static_cast<uint32_t>(2 * t.half + t.width);
+                // (kGrad's two products in loops of their own: chosen within one, an
+                // iteration took 10 % longer than the MMAs)
+                auto load = [&](auto mn_major) {
+                    for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                        if (!W.wait(empty_bar(stage), phase ^ 1u, 0)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t sa = sbase + stage * C::kStageBytes, sb = sa + C::kABytes;
+                        const uint32_t full = ptx::mapa_shared(full_bar(stage), 0);
+                        if (rank == 0)
+                            ptx::mbar_arrive_expect_tx(full_bar(stage), bytes);
+                        const int k = kb * (C::kFp8 ? 128 : 64);
+                        if constexpr (decltype(mn_major)::value) {
+                            ptx::tma_load_3d_pair(sa, &m.a, full, row, k, 0);
+                            ptx::tma_load_3d_pair(sa + 8192, &m.a, full, row + 64, k, 0);
+                        } else {
+                            ptx::tma_load_3d_pair(sa, &m.a, full, k, row, 0);
+                        }
+                        if constexpr (KIND == kGrad) {
+                            ptx::tma_load_3d_pair(sb, &m.b, full, col, k, 0);
+                            ptx::tma_load_3d_pair(sb + 8192, &m.b, full, col + 64, k, 0);
+                        } else {
+                            ptx::tma_load_3d_pair(sb, &m.b, full, k, col, 0);
+                        }
+                        ++issued;
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
-                    const uint32_t sa = sbase + stage * C::kStageBytes, sb = sa + C::kABytes;
-                    const uint32_t full = ptx::mapa_shared(full_bar(stage), 0);
-                    if (rank == 0)
-                        ptx::mbar_arrive_expect_tx(full_bar(stage), 2u * C::kABytes + 128u * static_cast<uint32_t>(p.width));
-                    const int k = kb * (C::kFp8 ? 128 : 64);
-                    if constexpr (C::kAMn) {
-                        ptx::tma_load_3d_pair(sa, &tmap_a, full, row, k, 0);
-                        ptx::tma_load_3d_pair(sa + 8192, &tmap_a, full, row + 64, k, 0);
-                    } else {
-                        ptx::tma_load_3d_pair(sa, &tmap_a, full, k, row, 0);
-                    }
-                    if constexpr (C::kBMn) {
-                        ptx::tma_load_3d_pair(sb, &tmap_b, full, col, k, 0);
-                        ptx::tma_load_3d_pair(sb + 8192, &tmap_b, full, col + 64, k, 0);
-                    } else {
-                        ptx::tma_load_3d_pair(sb, &tmap_b, full, k, col, 0);
-                    }
-                    ++issued;
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
+                };
+                if (KIND == kGrad && w.of == kOfB)
+                    load(std::integral_constant<bool, KIND == kGrad>{});
+                else
+                    load(std::false_type{});
             }
             // this CTA's copies land before it may exit (the even CTA sees both
             // CTAs' bytes; the odd one waits until its stages were consumed)
@@ -448,36 +546,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int acc = 0;
             uint32_t acc_phase = 0;
             bool ok = true;
-            Schedule tiles(p, pair, pairs);
+            Schedule<KIND> tiles(p, pair, pairs);
             Work w;
             while (ok && tiles.next(w)) {
+                const uint32_t idesc = p.t[KIND == kGrad ? w.of : 0].idesc;
                 if (!W.wait_cluster(tempty_bar(acc), acc_phase ^ 1u, 1))
                     break;
                 ptx::tc_fence_after();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kTile);
-                for (int kb = w.kb0; kb < w.kb1; ++kb) {
-                    if (!W.wait(full_bar(stage), phase, 2)) {
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after();
-                    const uint32_t sa = sbase + stage * C::kStageBytes, sb = sa + C::kABytes;
+                Converted next(p, w);
+                auto multiply = [&](auto mn_major) {
+                    for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                        if (!W.wait(full_bar(stage), phase, 2)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                        const uint32_t sa = sbase + stage * C::kStageBytes, sb = sa + C::kABytes;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t more = (kb > w.kb0 || k > 0) ? 1u : 0u;
-                        const uint64_t da = C::kAMn ? ptx::sw128_mnmajor_desc(sa + k * 2048) : ptx::sw128_kmajor_desc(sa + k * 32);
-                        const uint64_t db = C::kBMn ? ptx::sw128_mnmajor_desc(sb + k * 2048) : ptx::sw128_kmajor_desc(sb + k * 32);
-                        if constexpr (C::kFp8)
-                            ptx::mma_e4m3_pair(d, da, db, p.idesc, more);
-                        else
-                            ptx::mma_f16_pair(d, da, db, p.idesc, more);
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t more = (kb > w.kb0 || k > 0) ? 1u : 0u;
+                            if constexpr (KIND == kGrad) {
+                                const uint64_t da = decltype(mn_major)::value ? ptx::sw128_mnmajor_desc(sa + k * 2048) : ptx::sw128_kmajor_desc(sa + k * 32);
+                                ptx::mma_f16_pair(d, da, ptx::sw128_mnmajor_desc(sb + k * 2048), idesc, more);
+                            } else {
+                                ptx::mma_e4m3_pair(d, ptx::sw128_kmajor_desc(sa + k * 32), ptx::sw128_kmajor_desc(sb + k * 32), idesc, more);
+                            }
+                        }
+                        const bool keep = KIND == kSlope && next.has(kb);
+                        ptx::mma_commit_pair_multicast(keep ? used_bar(stage) : empty_bar(stage), 0x3);
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
-                    ptx::mma_commit_pair_multicast(empty_bar(stage), 0x3);
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
+                };
+                if (KIND == kGrad && w.of == kOfB)
+                    multiply(std::integral_constant<bool, KIND == kGrad>{});
+                else
+                    multiply(std::false_type{});
                 if (!ok)
                     break;
                 ptx::mma_commit_pair_multicast(tfull_bar(acc), 0x3);
@@ -488,6 +595,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             ptx::mma_commit_pair_multicast(done_bar, 0x1);
             W.drain(done_bar, 0, 4);
+        }
+        __syncwarp();
+    } else if (KIND == kSlope && warp >= 2 + kEpiWarps) {
+        // ------------------------------------------- codes to fp16 ---
+        // From the stages, once the MMA is done with them. (By a kernel of its own, early
+        // and beside this one: 620 MB more of memory traffic at 300 x 50257 x 4112, 220 us
+        // for the two against 150.) The last warp that has its codes gives the stage back;
+        // taken[s] is 0 again before the stage can come round.
+        const int cw = warp - 2 - kEpiWarps;
+        const float fa = p.h16 ? code_scale(p.a_type) / norm_scale(p.norms, kNormA) : 0.0f;
+        const float fb = p.w16 ? code_scale(p.b_type) / norm_scale(p.norms, kNormB) : 0.0f;
+        const TileSpace &t = p.t[0];
+        uint32_t *powers = reinterpret_cast<uint32_t *>(smem + kPowersAt) + cw * 32;
+        int stage = 0;
+        uint32_t used = 0;             // bit s: parity of the next use of stage s that converts
+        bool ok = true;
+        Schedule<KIND> tiles(p, pair, pairs);
+        Work w;
+        while (ok && tiles.next(w)) {
+            const int row = (2 * w.tp + static_cast<int>(rank)) * t.half;
+            const int col = w.tq * t.width + static_cast<int>(rank) * (t.width / 2);
+            __syncwarp();
+            if (p.h16)
+                load_powers(powers, row, p.M, p.scale_a, p.rowwise, fa, cw, lane);
+            if (p.w16)
+                load_powers(powers + 16, col, p.N, p.scale_b, p.rowwise, fb, cw, lane);
+            __syncwarp();
+            Converted next(p, w);
+            for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                const int s = stage;
+                if (++stage == S)
+                    stage = 0;
+                if (!next.has(kb))
+                    continue;
+                if (!W.wait(used_bar(s), (used >> s) & 1u, 7)) {
+                    ok = false;
+                    break;
+                }
+                used ^= 1u << s;
+                const uint8_t *at = smem + s * C::kStageBytes;
+                uint2 a[8], b[8];
+                if (next.of_a)
+                    take_rows(a, at, cw, lane);
+                if (next.of_b)
+                    take_rows(b, at + C::kABytes, cw, lane);
+                __syncwarp();
+                if (lane == 0 && atomicAdd(taken + s, 1) == kConvertWarps - 1) {
+                    taken[s] = 0;
+                    ptx::mbar_arrive(empty_bar(s));
+                }
+                if (next.of_a) {
+                    if (p.a_type == 0)
+                        write_rows<true>(a, t.half, p.h16, row, p.M, kb * 128, p.K, powers, cw, lane);
+                    else
+                        write_rows<false>(a, t.half, p.h16, row, p.M, kb * 128, p.K, powers, cw, lane);
+                }
+                if (next.of_b) {
+                    if (p.b_type == 0)
+                        write_rows<true>(b, t.width / 2, p.w16, col, p.N, kb * 128, p.K, powers + 16, cw, lane);
+                    else
+                        write_rows<false>(b, t.width / 2, p.w16, col, p.N, kb * 128, p.K, powers + 16, cw, lane);
+                }
+            }
         }
         __syncwarp();
     } else {
@@ -503,11 +673,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float *col_mantissa = cols + 2 * C::kCols;
         int acc = 0;
         uint32_t acc_phase = 0;
-        float slope_scale = 1.0f, out_scale = 1.0f;
+        float slope_scale = 1.0f, out_scale[2] = {1.0f, 1.0f};
         if constexpr (KIND == kSlope)
             slope_scale = kSlopeScale / norm_scale(p.norms, kNormG);
-        if constexpr (!C::kFp8)
-            out_scale = p.norms ? p.factor * norm_scale(p.norms, kNormG) * norm_scale(p.norms, p.norm_of) : 1.0f;
+        if constexpr (KIND == kGrad) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (p.r[i].scaled)
+                    out_scale[i] = p.r[i].factor * norm_scale(p.norms, kNormG) * norm_scale(p.norms, p.r[i].norm_of);
+        }
         const float s_tensor = C::kFp8 && !p.rowwise ? __ldg(p.scale_a) * __ldg(p.scale_b) : 1.0f;
         const float ma_tensor = C::kFp8 && !p.rowwise ? mantissa(__ldg(p.scale_a)) : 1.0f;
         const float mb_tensor = C::kFp8 && !p.rowwise ? mantissa(__ldg(p.scale_b)) : 1.0f;
@@ -518,14 +692,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ptx::bulk_wait_group_read<0>();
             __syncwarp();
         };
-        auto stage_out = [&](int x, int y, int z, int x_end, int y_end) {
+        auto stage_out = [&](const CUtensorMap *out, bool add, int x, int y, int z, int x_end, int y_end) {
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0 && x < x_end && y < y_end) {
-                if (KIND == kGradA && p.add)
-                    ptx::tma_add_3d(&tmap_out, stage_smem, x, y, z);
+                if (KIND == kGrad && add)
+                    ptx::tma_add_3d(out, stage_smem, x, y, z);
                 else
-                    ptx::tma_store_3d(&tmap_out, stage_smem, x, y, z);
+                    ptx::tma_store_3d(out, stage_smem, x, y, z);
                 ptx::bulk_commit_group();
             }
         };
@@ -535,13 +709,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         long long at = -1;                       // (in the piece; -1: none in it)
         bool live = false;
         float top = -INFINITY, sum = 0.0f;       // of the row in this unit so far
-        Schedule tiles(p, pair, pairs);
+        Schedule<KIND> tiles(p, pair, pairs);
         Work w;
         while (tiles.next(w)) {
-            const int row0 = w.tp * kTile + static_cast<int>(rank) * 128 + q * 32, row = row0 + lane;
-            const int col0 = w.tq * p.width + part * 64;
+            const TileSpace &t = p.t[KIND == kGrad ? w.of : 0];
+            const Maps &m = maps.of[KIND == kGrad ? w.of : 0];
+            const int row0 = (2 * w.tp + static_cast<int>(rank)) * t.half + q * 32, row = row0 + lane;
+            const int col0 = w.tq * t.width + part * 64;
             // (a narrow tile's last warps have one block or none)
-            const int blocks = min(2, (min(p.width, p.cols - w.tq * p.width) - part * 64 + 31) / 32);
+            const int blocks = q * 32 >= t.half ? 0 : min(2, (min(t.width, t.cols - w.tq * t.width) - part * 64 + 31) / 32);
             // what the tile needs beside the accumulator, while the MMAs run
             if constexpr (C::kFp8) {
                 __syncwarp();
@@ -570,22 +746,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             rs = __ldg(p.scale_a + row);
                             ma = mantissa(rs);
                         }
-                        const long long t = __ldg(p.target + row);
-                        live = t != p.ignore;
-                        if (live && t >= 0 && t < p.vocabulary)
-                            at = t - p.col0;
+                        const long long to = __ldg(p.target + row);
+                        live = to != p.ignore;
+                        if (live && to >= 0 && to < p.vocabulary)
+                            at = to - p.col0;
                         if constexpr (KIND == kSlope) {
                             lse = __ldg(p.lse + row);
                             gs = __ldg(p.dloss + static_cast<long long>(row) * p.dloss_step) * slope_scale * ma;
-                            if (live && (t < 0 || t >= p.vocabulary))
+                            if (live && (to < 0 || to >= p.vocabulary))
                                 gs = NAN;
                         }
                     }
                 }
             } else {
-                row_factor = out_scale;
-                if (row < p.rows)
-                    row_factor = out_scale / mantissa(__ldg(p.row_scale + (p.rowwise ? row : 0)));
+                row_factor = w.of == kOfB ? out_scale[1] : out_scale[0];
+                if (row < t.rows)
+                    row_factor /= mantissa(__ldg(p.r[w.of].row_scale + (p.rowwise ? row : 0)));
             }
             if (!W.wait(tfull_bar(acc), acc_phase, 5))
                 break;
@@ -597,20 +773,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < blocks; ++i) {
                     const int n0 = col0 + i * 32;
                     const float *here = cols + i * 64, *here_m = col_mantissa + i * 32;
-                    const uint64_t rs2 = ptx::f32x2(rs, rs);
-                    float v[32];
-                    ptx::tmem_ld_32cols(trow + i * 32, v);
-                    uint64_t z[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float4 c = *reinterpret_cast<const float4 *>(here + k * 4);
-                        const uint64_t s2 = ptx::mul_f32x2(rs2, ptx::f32x2(c.x, c.y));
-                        z[k] = ptx::fma_f32x2(ptx::f32x2(v[2 * k], v[2 * k + 1]), s2, ptx::f32x2(c.z, c.w));
-                        ptx::unpack_f32x2(z[k], v[2 * k], v[2 * k + 1]);
-                    }
                     const bool mine = at >= n0 && at < n0 + 32;
-                    const uint64_t log2e2 = ptx::f32x2(kLog2e, kLog2e);
                     if constexpr (KIND == kStats) {
+                        float v[32];
+                        ptx::tmem_ld_32cols(trow + i * 32, v);
+                        logits(v, here, rs);
                         if (mine) {
                             float zt = 0.0f;
 #pragma unroll
@@ -629,7 +796,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
                             float lo, hi;
-                            ptx::unpack_f32x2(ptx::mul_f32x2(ptx::add_f32x2(z[k], off), log2e2), lo, hi);
+                            exponents(v[2 * k], v[2 * k + 1], off, lo, hi);
                             s2[k & 1] = ptx::add_f32x2(s2[k & 1], ptx::f32x2(fp8mm::ex2_approx(lo), fp8mm::ex2_approx(hi)));
                         }
                         float s0, s1;
@@ -637,50 +804,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         sum = sum * fp8mm::ex2_approx((top - ref) * kLog2e) + (s0 + s1);
                         top = most;
                     } else {
+                        // 16 columns at a time: 26 warps have 72 registers each
                         const uint64_t off = ptx::f32x2(-lse, -lse);
+#pragma unroll 1
+                        for (int j = 0; j < 2; ++j) {
+                            float v[16];
+                            ptx::tmem_ld_16cols(trow + i * 32 + j * 16, v);
+                            logits(v, here + j * 32, rs);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            float lo, hi;
-                            ptx::unpack_f32x2(ptx::mul_f32x2(ptx::add_f32x2(z[k], off), log2e2), lo, hi);
-                            v[2 * k] = live ? fp8mm::ex2_approx(lo) * gs : 0.0f;
-                            v[2 * k + 1] = live ? fp8mm::ex2_approx(hi) * gs : 0.0f;
-                        }
-                        if (mine) {
+                            for (int k = 0; k < 16; k += 2) {
+                                float lo, hi;
+                                exponents(v[k], v[k + 1], off, lo, hi);
+                                v[k] = live ? fp8mm::ex2_approx(lo) * gs : 0.0f;
+                                v[k + 1] = live ? fp8mm::ex2_approx(hi) * gs : 0.0f;
+                            }
+                            if (mine) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                v[k] = at == n0 + k ? v[k] - gs : v[k];
-                        }
-                        stage_free();
+                                for (int k = 0; k < 16; ++k)
+                                    v[k] = at == n0 + j * 16 + k ? v[k] - gs : v[k];
+                            }
+                            if (j == 0)
+                                stage_free();
 #pragma unroll
-                        for (int k = 0; k < 32; k += 8) {
-                            const float4 x = *reinterpret_cast<const float4 *>(here_m + k);
-                            const float4 y = *reinterpret_cast<const float4 *>(here_m + k + 4);
-                            const float o[8] = {v[k] * x.x, v[k + 1] * x.y, v[k + 2] * x.z, v[k + 3] * x.w,
-                                                v[k + 4] * y.x, v[k + 5] * y.y, v[k + 6] * y.z, v[k + 7] * y.w};
-                            stage_chunk64(stage, lane, k / 8, pack8(o, fp8rows::kF16));
-                        }
-                        stage_out(n0, row0, 0, p.N, p.M);
-                        if (p.colsum) {
-                            // (without the row's mantissa)
-                            const float back = 1.0f / ma;
+                            for (int k = 0; k < 16; k += 8) {
+                                const float4 x = *reinterpret_cast<const float4 *>(here_m + j * 16 + k);
+                                const float4 y = *reinterpret_cast<const float4 *>(here_m + j * 16 + k + 4);
+                                const float o[8] = {v[k] * x.x, v[k + 1] * x.y, v[k + 2] * x.z, v[k + 3] * x.w,
+                                                    v[k + 4] * y.x, v[k + 5] * y.y, v[k + 6] * y.z, v[k + 7] * y.w};
+                                stage_chunk64(stage, lane, j * 2 + k / 8, pack8(o, fp8rows::kF16));
+                            }
+                            if (p.colsum) {
+                                // (without the row's mantissa)
+                                const float back = 1.0f / ma;
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                v[k] *= back;
-                            const float s = sum_rows(v, lane);
-                            if (row0 < p.M && n0 + lane < p.N)
-                                __stcg(p.colsum + (row0 / 32) * p.colsum_ld + n0 + lane, s);
+                                for (int k = 0; k < 16; ++k)
+                                    v[k] *= back;
+                                const float s = sum_rows(v, lane);
+                                const int n = n0 + j * 16 + lane;
+                                if (row0 < p.M && lane < 16 && n < p.N)
+                                    __stcg(p.colsum + (row0 / 32) * p.colsum_ld + n, s);
+                            }
                         }
+                        stage_out(&m.out, false, n0, row0, 0, p.N, p.M);
                     }
                 }
                 if constexpr (KIND == kStats) {
-                    if (w.last && row < p.M)
+                    if (w.last && row < p.M && q * 32 < t.half)
                         __stcg(p.stats + static_cast<long long>(w.unit_q * 4 + part) * p.M + row, make_float2(top, sum));
                 }
             } else {
-                const bool f32 = p.out_type == fp8mm::kOutF32;
+                const Result &r = p.r[w.of];
+                const bool f32 = r.out_type == fp8mm::kOutF32;
                 // 32 columns of fp32 make a block, 64 of 16 bits
 #pragma unroll 1
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < 2 && q * 32 < t.half; ++i) {
                     float v[32];
                     ptx::tmem_ld_32cols(trow + i * 32, v);
 #pragma unroll
@@ -694,20 +871,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             stage_chunk(stage, lane, k / 4,
                                         make_uint4(__float_as_uint(v[k]), __float_as_uint(v[k + 1]),
                                                    __float_as_uint(v[k + 2]), __float_as_uint(v[k + 3])));
-                        stage_out(col0 + i * 32, row0, w.split, p.cols, p.rows);
+                        stage_out(&m.out, r.add, col0 + i * 32, row0, w.split, t.cols, t.rows);
                     } else {
 #pragma unroll
                         for (int k = 0; k < 32; k += 8)
-                            stage_chunk(stage, lane, i * 4 + k / 8, pack8(v + k, p.out_type));
+                            stage_chunk(stage, lane, i * 4 + k / 8, pack8(v + k, r.out_type));
                         if (i == 1)
-                            stage_out(col0, row0, w.split, p.cols, p.rows);
+                            stage_out(&m.out, r.add, col0, row0, w.split, t.cols, t.rows);
                     }
                 }
             }
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                ptx::mbar_arrive_cluster(ptx::mapa_shared(tempty_bar(acc), 0));
+                ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(tempty_bar(acc), 0));
             if (++acc == 2) {
                 acc = 0;
                 acc_phase ^= 1u;

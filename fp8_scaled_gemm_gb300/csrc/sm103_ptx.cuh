@@ -285,6 +285,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
                  : "memory");
 }
 
+// The same without releasing earlier memory accesses: for handing tensor memory
+// back, after tcgen05.wait and tc_fence_before(), where the wait for this thread's
+// global stores that a release at cluster scope takes is of no use.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // try_wait with cluster-scope acquire (for arrivals released by the peer CTA).
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
 {
