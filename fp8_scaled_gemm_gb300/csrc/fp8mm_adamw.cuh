@@ -164,6 +164,169 @@ __device__ __forceinline__ float warp_max(float v)
     return v;
 }
 
+// ------------------------------------------- roots and quotients of pairs ---
+// Correctly rounded, by P. Markstein's iterations ("Computation of elementary
+// functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990), on
+// two values at once: a root from an approximate reciprocal root refined together with
+// it, then corrected by its residual; a quotient from a refined reciprocal, corrected
+// by its residual. CUDA's __fsqrt_rn and __fdiv_rn take 12 and 18 issue slots a value,
+// these 5 and 4, and with the former the step with 8-bit states was bound by issue
+// (470 M elements 1950 us). Compared with them for every mantissa (roots, reciprocals)
+// in the operator's tests; a lane with a value outside their ranges takes CUDA's.
+constexpr float kRootFrom = 0x1p-96f, kRootTo = 0x1p96f;
+
+__device__ __forceinline__ uint64_t both(float v) { return ptx::f32x2(v, v); }
+__device__ __forceinline__ float rsqrt_approx(float x)
+{
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint64_t minus(uint64_t v) { return v ^ 0x8000000080000000ull; }
+
+// Sums of pairs one value at a time: ptxas contracts a packed product and the packed
+// sum behind it (also with -fmad=false), which would round once.
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    float a0, a1, b0, b1;
+    ptx::unpack_f32x2(a, a0, a1);
+    ptx::unpack_f32x2(b, b0, b1);
+    return ptx::f32x2(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
+}
+
+// x in [kRootFrom, kRootTo]
+__device__ __forceinline__ uint64_t root2(uint64_t x)
+{
+    float x0, x1;
+    ptx::unpack_f32x2(x, x0, x1);
+    const uint64_t y = ptx::f32x2(rsqrt_approx(x0), rsqrt_approx(x1));
+    uint64_t g = ptx::mul_f32x2(x, y), h = ptx::mul_f32x2(y, both(0.5f));
+    const uint64_t e = ptx::fma_f32x2(minus(h), g, both(0.5f));
+    g = ptx::fma_f32x2(g, e, g);
+    h = ptx::fma_f32x2(h, e, h);
+    return ptx::fma_f32x2(ptx::fma_f32x2(minus(g), g, x), h, g);
+}
+
+// The rounded reciprocal of d in [2^-60, 2^60].
+__device__ __forceinline__ uint64_t reciprocal2(uint64_t d)
+{
+    float d0, d1;
+    ptx::unpack_f32x2(d, d0, d1);
+    const uint64_t y = ptx::f32x2(rcp_approx(d0), rcp_approx(d1));
+    return ptx::fma_f32x2(y, ptx::fma_f32x2(minus(d), y, both(1.0f)), y);
+}
+
+// x / d with the rounded reciprocal y of d: |x| <= 2^60 (under 2^-90 the last bit may
+// be another)
+__device__ __forceinline__ uint64_t divide2(uint64_t x, uint64_t d, uint64_t y)
+{
+    const uint64_t q = ptx::mul_f32x2(x, y);
+    return ptx::fma_f32x2(ptx::fma_f32x2(minus(q), d, x), y, q);
+}
+
+// The step's constants and a tensor's scales, as the elements' arithmetic takes them.
+struct Factors {
+    float keep, step_size, root, gs, ms, vs;
+    uint32_t step;
+    bool scaled_grad;
+};
+
+// ------------------------------------------------------- the step of one lane ---
+// Eight elements: w, m and v (codes' values with BITS = 8) become the new ones, r the
+// root of v; two at a time, in single operations each rounded by itself.
+template <int BITS>
+__device__ __forceinline__ void update(float (&w)[8], float (&g)[8], float (&m)[8], float (&v)[8], float (&r)[8], const Hyper &h,
+                                       const Factors &f)
+{
+    uint64_t m2[4], v2[4];
+    float least = kRootTo, most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint64_t gi = ptx::f32x2(g[2 * i], g[2 * i + 1]);
+        m2[i] = ptx::f32x2(m[2 * i], m[2 * i + 1]);
+        v2[i] = ptx::f32x2(v[2 * i], v[2 * i + 1]);
+        if (f.scaled_grad)
+            gi = ptx::mul_f32x2(gi, both(f.gs));
+        if constexpr (BITS == 8) {
+            m2[i] = ptx::mul_f32x2(m2[i], both(f.ms));
+            v2[i] = ptx::mul_f32x2(v2[i], both(f.vs));
+            v2[i] = ptx::mul_f32x2(v2[i], v2[i]);
+        }
+        m2[i] = add2(ptx::mul_f32x2(m2[i], both(h.b1)), ptx::mul_f32x2(gi, both(h.b1c)));
+        v2[i] = add2(ptx::mul_f32x2(v2[i], both(h.b2)), ptx::mul_f32x2(ptx::mul_f32x2(gi, gi), both(h.b2c)));
+        ptx::unpack_f32x2(m2[i], m[2 * i], m[2 * i + 1]);
+        ptx::unpack_f32x2(v2[i], v[2 * i], v[2 * i + 1]);
+        least = fminf(least, fminf(v[2 * i], v[2 * i + 1]));
+        most = fp8mm::max_nan(most, fp8mm::max_nan(v[2 * i], v[2 * i + 1]));
+        most = fp8mm::max_nan(most, fp8mm::max_nan(fabsf(m[2 * i]), fabsf(m[2 * i + 1])));
+    }
+    // v and |m| at most 2^59: the root, the denominator and m are in the quotient's range
+    // when eps and the root's factor are (a NaN is not)
+    if (least >= kRootFrom && most <= 0x1p59f && h.eps >= 0x1p-60f && h.eps <= 0x1p59f && f.root <= 0x1p29f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t r2 = root2(v2[i]);
+            const uint64_t d = add2(ptx::mul_f32x2(r2, both(f.root)), both(h.eps));
+            const uint64_t q = divide2(m2[i], d, reciprocal2(d));
+            const uint64_t w2 = add2(ptx::mul_f32x2(ptx::f32x2(w[2 * i], w[2 * i + 1]), both(f.keep)),
+                                               minus(ptx::mul_f32x2(q, both(f.step_size))));
+            ptx::unpack_f32x2(r2, r[2 * i], r[2 * i + 1]);
+            ptx::unpack_f32x2(w2, w[2 * i], w[2 * i + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            r[i] = __fsqrt_rn(v[i]);
+            w[i] = __fsub_rn(__fmul_rn(w[i], f.keep),
+                             __fmul_rn(__fdiv_rn(m[i], __fadd_rn(__fmul_rn(r[i], f.root), h.eps)), f.step_size));
+        }
+    }
+}
+
+// Codes of a lane's eight m (in place: their quotients by the new scale, which a
+// conversion rounds) and r (to values that e4m3 holds).
+__device__ __forceinline__ void encode(float (&m)[8], float (&r)[8], float ms, float vs, uint32_t e0, int stride, uint32_t step)
+{
+    const fp8q::Divider dm = fp8q::make_divider(ms), dv = fp8q::make_divider(vs);
+    uint32_t u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        u[i] = dither(e0 + static_cast<uint32_t>(stride * i), step);
+    if (dm.mode == 1 && dv.mode == 1) {
+        // (the block's values are finite and at most 448 scales: the reciprocal's way,
+        // and no clamp but the conversion's)
+        uint32_t low = UINT32_MAX;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            ptx::unpack_f32x2(divide2(ptx::f32x2(m[i], m[i + 1]), both(dm.s), both(dm.r)), m[i], m[i + 1]);
+            ptx::unpack_f32x2(divide2(ptx::f32x2(r[i], r[i + 1]), both(dv.s), both(dv.r)), r[i], r[i + 1]);
+            low = min(low, min(__float_as_uint(r[i]) - 1u, __float_as_uint(r[i + 1]) - 1u));   // (0: the largest)
+        }
+        if (low >= 0x3C800000u - 1u) {
+            // none in (0, 2^-6): see round_by
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                r[i] = __uint_as_float((__float_as_uint(r[i]) + u[i]) & ~0xFFFFFu);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                r[i] = round_by(r[i], u[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            m[i] = quotient(dm, m[i]);
+            r[i] = round_by(quotient(dv, r[i]), u[i]);
+        }
+    }
+}
+
 template <int BITS, int T>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Params<T> p)
 {
@@ -257,42 +420,27 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
             }
         }
         float r[8];
-        float most_m = 0.0f, most_r = 0.0f;
+        update<BITS>(w, g, m, v, r, p.h, Factors{keep, step_size, root, gs, old_ms, old_vs, step, p.h.grad_scale != nullptr});
+        if constexpr (BITS == 8) {
+            float most_m = 0.0f, most_r = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (p.h.grad_scale)
-                g[i] = __fmul_rn(g[i], gs);
-            if constexpr (BITS == 8) {
-                m[i] = __fmul_rn(m[i], old_ms);
-                v[i] = __fmul_rn(v[i], old_vs);
-                v[i] = __fmul_rn(v[i], v[i]);
-            }
-            m[i] = __fadd_rn(__fmul_rn(m[i], p.h.b1), __fmul_rn(g[i], p.h.b1c));
-            v[i] = __fadd_rn(__fmul_rn(v[i], p.h.b2), __fmul_rn(__fmul_rn(g[i], g[i]), p.h.b2c));
-            if (!vec && i >= n) {
-                m[i] = 0.0f;           // (behind the tensor's end: a NaN scale's 0 x NaN)
-                v[i] = 0.0f;
-            }
-            r[i] = __fsqrt_rn(v[i]);
-            w[i] = __fsub_rn(__fmul_rn(w[i], keep),
-                             __fmul_rn(__fdiv_rn(m[i], __fadd_rn(__fmul_rn(r[i], root), p.h.eps)), step_size));
-            if constexpr (BITS == 8) {
+            for (int i = 0; i < 8; ++i) {
+                if (!vec && i >= n) {
+                    m[i] = 0.0f;       // (behind the tensor's end: a NaN scale's 0 x NaN)
+                    r[i] = 0.0f;
+                }
                 most_m = fp8mm::max_nan(most_m, fabsf(m[i]));
                 most_r = fp8mm::max_nan(most_r, r[i]);
             }
-        }
-        if constexpr (BITS == 8) {
             const float ms = __fdiv_rn(warp_max(most_m), 448.0f), vs = __fdiv_rn(warp_max(most_r), 448.0f);
-            const fp8q::Divider dm = fp8q::make_divider(ms), dv = fp8q::make_divider(vs);
             if (lane == 0) {
                 t.m_scale[block] = ms;
                 t.v_scale[block] = vs;
             }
+            encode(m, r, ms, vs, static_cast<uint32_t>(at), stride, step);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                m[i] = quotient(dm, m[i]);
-                v[i] = round_by(quotient(dv, r[i]), dither(static_cast<uint32_t>(at + stride * i), step));
-            }
+            for (int i = 0; i < 8; ++i)
+                v[i] = r[i];
         }
         if (vec) {
             if (p.has_master)
