@@ -22,8 +22,8 @@ struct Stretch {
 template <int BITS, int T>
 int launch(const Params<T> &p, int sms, cudaStream_t stream)
 {
-    // up to eight CTAs of eight warps on an SM, a block of 256 elements a warp
-    const int64_t grid = std::min<int64_t>(cdiv(p.blocks, kThreads / 32), static_cast<int64_t>(sms) * 8);
+    // as many CTAs as run at once, a block of 256 elements a warp and turn
+    const int64_t grid = std::min<int64_t>(cdiv(p.blocks, kThreads / 32), static_cast<int64_t>(sms) * kCtasPerSm);
     return launch_pdl(adamw_kernel<BITS, T>, static_cast<int>(grid), kThreads, 0, stream, "AdamW launch", p);
 }
 

@@ -33,6 +33,7 @@ namespace ptx = fp8mm::ptx;
 
 constexpr int kBlock = 256;            // elements of a block, of one warp
 constexpr int kThreads = 256;
+constexpr int kCtasPerSm = 4;          // 64 registers a thread; with 3 the loads' latency showed
 
 struct Tensor {
     void *param;
@@ -130,12 +131,6 @@ __device__ __forceinline__ float2 decode2(uint32_t codes)
 
 __device__ __forceinline__ float decode1(uint8_t code) { return decode2(code).x; }
 
-__device__ __forceinline__ float quotient(const fp8q::Divider &d, float x)
-{
-    // (the reciprocal path's residual needs a finite x)
-    return d.mode == 1 && fabsf(x) < 0x1p100f ? fp8q::div_fast(d, x) : d.mode == 0 ? 0.0f : __fdiv_rn(x, d.s);
-}
-
 // 20 bits for the rounding of element e at a step.
 __device__ __forceinline__ uint32_t dither(uint32_t e, uint32_t step)
 {
@@ -153,15 +148,6 @@ __device__ __forceinline__ float round_by(float q, uint32_t u)
     if (q < 0x1p-6f)
         return q > 0.0f ? fmaxf(floorf(__fadd_rn(q * 512.0f, static_cast<float>(u) * 0x1p-20f)) * 0x1p-9f, 0x1p-9f) : q;
     return q == q ? __uint_as_float((__float_as_uint(q) + u) & ~0xFFFFFu) : q;
-}
-
-// The largest of a warp's values, NaN if one is.
-__device__ __forceinline__ float warp_max(float v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v = fp8mm::max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return v;
 }
 
 // ------------------------------------------- roots and quotients of pairs ---
@@ -188,7 +174,20 @@ __device__ __forceinline__ float rcp_approx(float x)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint64_t minus(uint64_t v) { return v ^ 0x8000000080000000ull; }
+
+// The largest of three, NaN if one is; the least of three.
+__device__ __forceinline__ float max3_nan(float a, float b, float c)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+__device__ __forceinline__ float min3(float a, float b, float c)
+{
+    float y;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
 
 // Sums of pairs one value at a time: ptxas contracts a packed product and the packed
 // sum behind it (also with -fmad=false), which would round once.
@@ -200,34 +199,71 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return ptx::f32x2(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
 }
 
-// x in [kRootFrom, kRootTo]
+// x in [kRootFrom, kRootTo]. (The signs are such that no operand has to be negated:
+// h is minus half the reciprocal root, the residual is g^2 - x.)
 __device__ __forceinline__ uint64_t root2(uint64_t x)
 {
     float x0, x1;
     ptx::unpack_f32x2(x, x0, x1);
     const uint64_t y = ptx::f32x2(rsqrt_approx(x0), rsqrt_approx(x1));
-    uint64_t g = ptx::mul_f32x2(x, y), h = ptx::mul_f32x2(y, both(0.5f));
-    const uint64_t e = ptx::fma_f32x2(minus(h), g, both(0.5f));
+    uint64_t g = ptx::mul_f32x2(x, y), h = ptx::mul_f32x2(y, both(-0.5f));
+    const uint64_t e = ptx::fma_f32x2(h, g, both(0.5f));
     g = ptx::fma_f32x2(g, e, g);
     h = ptx::fma_f32x2(h, e, h);
-    return ptx::fma_f32x2(ptx::fma_f32x2(minus(g), g, x), h, g);
+    return ptx::fma_f32x2(ptx::fma_f32x2(g, g, ptx::mul_f32x2(x, both(-1.0f))), h, g);
 }
 
-// The rounded reciprocal of d in [2^-60, 2^60].
-__device__ __forceinline__ uint64_t reciprocal2(uint64_t d)
+// The rounded reciprocal of d in [2^-60, 2^60], from minus d.
+__device__ __forceinline__ uint64_t reciprocal2(uint64_t d, uint64_t minus_d)
 {
     float d0, d1;
     ptx::unpack_f32x2(d, d0, d1);
     const uint64_t y = ptx::f32x2(rcp_approx(d0), rcp_approx(d1));
-    return ptx::fma_f32x2(y, ptx::fma_f32x2(minus(d), y, both(1.0f)), y);
+    return ptx::fma_f32x2(y, ptx::fma_f32x2(minus_d, y, both(1.0f)), y);
 }
 
-// x / d with the rounded reciprocal y of d: |x| <= 2^60 (under 2^-90 the last bit may
-// be another)
-__device__ __forceinline__ uint64_t divide2(uint64_t x, uint64_t d, uint64_t y)
+// x / d from minus d and the rounded reciprocal y of d: |x| <= 2^60 (under 2^-90 the
+// last bit may be another)
+__device__ __forceinline__ uint64_t divide2(uint64_t x, uint64_t minus_d, uint64_t y)
 {
     const uint64_t q = ptx::mul_f32x2(x, y);
-    return ptx::fma_f32x2(ptx::fma_f32x2(minus(q), d, x), y, q);
+    return ptx::fma_f32x2(ptx::fma_f32x2(q, minus_d, x), y, q);
+}
+
+// A scale, largest value / 448, with what a quotient by it needs.
+struct Scale {
+    float s, r;                        // r: its reciprocal, where `fast`
+    bool fast;                         // see fp8q::Divider's mode 1
+};
+
+// The scales of a warp's block from every lane's largest |m| and v. The lower half of
+// the warp works on m, the upper one on v and its root, on one value a lane.
+__device__ __forceinline__ void block_scales(float most_m, float most_v, int lane, Scale &m, Scale &v)
+{
+    const bool upper = lane & 16;
+    float x = fp8mm::max_nan(upper ? most_v : most_m, __shfl_xor_sync(0xFFFFFFFFu, upper ? most_m : most_v, 16));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        x = fp8mm::max_nan(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+    if (upper) {
+        // (the largest root is the largest value's)
+        float r, other;
+        ptx::unpack_f32x2(root2(both(x)), r, other);
+        x = x >= kRootFrom && x <= kRootTo ? r : __fsqrt_rn(x);
+    }
+    const float s = fp8q::row_scale(x, 0);
+    float r = 0.0f;
+    const bool fast = s >= 0x1p-59f && s <= 0x1p59f;
+    if (fast) {
+        float other;
+        ptx::unpack_f32x2(reciprocal2(both(s), both(-s)), r, other);
+    }
+    m.s = __shfl_sync(0xFFFFFFFFu, s, 0);
+    m.r = __shfl_sync(0xFFFFFFFFu, r, 0);
+    v.s = __shfl_sync(0xFFFFFFFFu, s, 16);
+    v.r = __shfl_sync(0xFFFFFFFFu, r, 16);
+    m.fast = m.r != 0.0f;
+    v.fast = v.r != 0.0f;
 }
 
 // The step's constants and a tensor's scales, as the elements' arithmetic takes them.
@@ -235,17 +271,21 @@ struct Factors {
     float keep, step_size, root, gs, ms, vs;
     uint32_t step;
     bool scaled_grad;
+    bool pairs;                        // eps and the root's factor allow roots and quotients of pairs
 };
 
 // ------------------------------------------------------- the step of one lane ---
-// Eight elements: w, m and v (codes' values with BITS = 8) become the new ones, r the
-// root of v; two at a time, in single operations each rounded by itself.
+// Eight elements, of which n are there (the others count as zeros): w, m and v (codes'
+// values with BITS = 8) become the new ones, r the root of v; two at a time, in
+// single operations each rounded by itself. Gives the largest |m| and v and the least
+// v, of which the last is 0 where the pairs' range was left.
 template <int BITS>
-__device__ __forceinline__ void update(float (&w)[8], float (&g)[8], float (&m)[8], float (&v)[8], float (&r)[8], const Hyper &h,
-                                       const Factors &f)
+__device__ __forceinline__ void update(float (&w)[8], float (&g)[8], float (&m)[8], float (&v)[8], float (&r)[8], int n,
+                                       const Hyper &h, const Factors &f, float &most_m, float &most_v, float &least)
 {
     uint64_t m2[4], v2[4];
-    float least = kRootTo, most = 0.0f;
+    least = kRootTo;
+    most_m = most_v = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint64_t gi = ptx::f32x2(g[2 * i], g[2 * i + 1]);
@@ -262,24 +302,31 @@ __device__ __forceinline__ void update(float (&w)[8], float (&g)[8], float (&m)[
         v2[i] = add2(ptx::mul_f32x2(v2[i], both(h.b2)), ptx::mul_f32x2(ptx::mul_f32x2(gi, gi), both(h.b2c)));
         ptx::unpack_f32x2(m2[i], m[2 * i], m[2 * i + 1]);
         ptx::unpack_f32x2(v2[i], v[2 * i], v[2 * i + 1]);
-        least = fminf(least, fminf(v[2 * i], v[2 * i + 1]));
-        most = fp8mm::max_nan(most, fp8mm::max_nan(v[2 * i], v[2 * i + 1]));
-        most = fp8mm::max_nan(most, fp8mm::max_nan(fabsf(m[2 * i]), fabsf(m[2 * i + 1])));
+        if (n < 8) {
+            // (0 times a NaN scale)
+            for (int j = 2 * i; j < 2 * i + 2; ++j)
+                if (j >= n)
+                    m[j] = v[j] = 0.0f;
+        }
+        least = min3(least, v[2 * i], v[2 * i + 1]);
+        most_v = max3_nan(most_v, v[2 * i], v[2 * i + 1]);
+        most_m = max3_nan(most_m, fabsf(m[2 * i]), fabsf(m[2 * i + 1]));
     }
     // v and |m| at most 2^59: the root, the denominator and m are in the quotient's range
     // when eps and the root's factor are (a NaN is not)
-    if (least >= kRootFrom && most <= 0x1p59f && h.eps >= 0x1p-60f && h.eps <= 0x1p59f && f.root <= 0x1p29f) {
+    if (least >= kRootFrom && most_m <= 0x1p59f && most_v <= 0x1p59f && f.pairs) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint64_t r2 = root2(v2[i]);
-            const uint64_t d = add2(ptx::mul_f32x2(r2, both(f.root)), both(h.eps));
-            const uint64_t q = divide2(m2[i], d, reciprocal2(d));
+            const uint64_t d = add2(ptx::mul_f32x2(r2, both(f.root)), both(h.eps)), minus_d = ptx::mul_f32x2(d, both(-1.0f));
+            const uint64_t q = divide2(m2[i], minus_d, reciprocal2(d, minus_d));
             const uint64_t w2 = add2(ptx::mul_f32x2(ptx::f32x2(w[2 * i], w[2 * i + 1]), both(f.keep)),
-                                               minus(ptx::mul_f32x2(q, both(f.step_size))));
+                                     ptx::mul_f32x2(q, both(-f.step_size)));
             ptx::unpack_f32x2(r2, r[2 * i], r[2 * i + 1]);
             ptx::unpack_f32x2(w2, w[2 * i], w[2 * i + 1]);
         }
     } else {
+        least = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             r[i] = __fsqrt_rn(v[i]);
@@ -290,45 +337,40 @@ __device__ __forceinline__ void update(float (&w)[8], float (&g)[8], float (&m)[
 }
 
 // Codes of a lane's eight m (in place: their quotients by the new scale, which a
-// conversion rounds) and r (to values that e4m3 holds).
-__device__ __forceinline__ void encode(float (&m)[8], float (&r)[8], float ms, float vs, uint32_t e0, int stride, uint32_t step)
+// conversion rounds) and r (to values that e4m3 holds). `least`: of the r's squares,
+// or 0.
+__device__ __forceinline__ void encode(float (&m)[8], float (&r)[8], const Scale &ms, const Scale &vs, float least, uint32_t e0,
+                                       int stride, uint32_t step)
 {
-    const fp8q::Divider dm = fp8q::make_divider(ms), dv = fp8q::make_divider(vs);
-    uint32_t u[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        u[i] = dither(e0 + static_cast<uint32_t>(stride * i), step);
-    if (dm.mode == 1 && dv.mode == 1) {
+    if (ms.fast && vs.fast) {
         // (the block's values are finite and at most 448 scales: the reciprocal's way,
         // and no clamp but the conversion's)
-        uint32_t low = UINT32_MAX;
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            ptx::unpack_f32x2(divide2(ptx::f32x2(m[i], m[i + 1]), both(dm.s), both(dm.r)), m[i], m[i + 1]);
-            ptx::unpack_f32x2(divide2(ptx::f32x2(r[i], r[i + 1]), both(dv.s), both(dv.r)), r[i], r[i + 1]);
-            low = min(low, min(__float_as_uint(r[i]) - 1u, __float_as_uint(r[i + 1]) - 1u));   // (0: the largest)
+            ptx::unpack_f32x2(divide2(ptx::f32x2(m[i], m[i + 1]), both(-ms.s), both(ms.r)), m[i], m[i + 1]);
+            ptx::unpack_f32x2(divide2(ptx::f32x2(r[i], r[i + 1]), both(-vs.s), both(vs.r)), r[i], r[i + 1]);
         }
-        if (low >= 0x3C800000u - 1u) {
-            // none in (0, 2^-6): see round_by
+        if (least >= 0x1.01p-12f * vs.s * vs.s) {
+            // none under 2^-6: see round_by
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                r[i] = __uint_as_float((__float_as_uint(r[i]) + u[i]) & ~0xFFFFFu);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                r[i] = round_by(r[i], u[i]);
+                r[i] = __uint_as_float((__float_as_uint(r[i]) + dither(e0 + static_cast<uint32_t>(stride * i), step)) & ~0xFFFFFu);
+            return;
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            m[i] = quotient(dm, m[i]);
-            r[i] = round_by(quotient(dv, r[i]), u[i]);
+            m[i] = ms.s == 0.0f ? 0.0f : __fdiv_rn(m[i], ms.s);
+            r[i] = vs.s == 0.0f ? 0.0f : __fdiv_rn(r[i], vs.s);
         }
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        r[i] = round_by(r[i], dither(e0 + static_cast<uint32_t>(stride * i), step));
 }
 
 template <int BITS, int T>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Params<T> p)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) adamw_kernel(const __grid_constant__ Params<T> p)
 {
     __shared__ float shared_hyper[3];
     __shared__ uint32_t shared_step;
@@ -359,7 +401,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         root = shared_hyper[2];
         step = shared_step;
     }
-    const float gs = p.h.grad_scale ? __ldcg(p.h.grad_scale) : 1.0f;
+    Factors f{keep, step_size, root, p.h.grad_scale ? __ldcg(p.h.grad_scale) : 1.0f, 0.0f, 0.0f, step,
+              p.h.grad_scale != nullptr, p.h.eps >= 0x1p-60f && p.h.eps <= 0x1p59f && root <= 0x1p29f};
     const int lane = threadIdx.x & 31;
     const long long warps = static_cast<long long>(gridDim.x) * (kThreads / 32);
     int k = 0;
@@ -375,14 +418,14 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         const int n = vec ? 8 : static_cast<int>(min(8ll, (t.count - at + 31) / 32));   // (<= 0: none)
         const float *w_from = p.has_master ? t.master : nullptr;
         float w[8], g[8], m[8], v[8];
-        float old_ms = 0.0f, old_vs = 0.0f;
         if (BITS == 8) {
-            old_ms = __ldcg(t.m_scale + block);
-            old_vs = __ldcg(t.v_scale + block);
+            f.ms = __ldcg(t.m_scale + block);
+            f.vs = __ldcg(t.v_scale + block);
         }
         if (vec) {
             Eight rw, rg, rm, rv;
-            load8(rw, p.has_master ? static_cast<const void *>(w_from) : t.param, p.has_master ? fp8rows::kF32 : p.param_type, at);
+            const int w_type = p.has_master ? fp8rows::kF32 : p.param_type;
+            load8(rw, p.has_master ? static_cast<const void *>(w_from) : t.param, w_type, at);
             load8(rg, t.grad, p.grad_type, at);
             if constexpr (BITS == 32) {
                 load8(rm, t.m, fp8rows::kF32, at);
@@ -393,7 +436,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
                 rm.w[0] = a.x; rm.w[1] = a.y;
                 rv.w[0] = c.x; rv.w[1] = c.y;
             }
-            floats8(rw, p.has_master ? fp8rows::kF32 : p.param_type, w);
+            floats8(rw, w_type, w);
             floats8(rg, p.grad_type, g);
             if constexpr (BITS == 32) {
                 floats8(rm, fp8rows::kF32, m);
@@ -419,25 +462,16 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
                 v[i] = !in ? 0.0f : BITS == 32 ? static_cast<const float *>(t.v)[e] : decode1(static_cast<const uint8_t *>(t.v)[e]);
             }
         }
-        float r[8];
-        update<BITS>(w, g, m, v, r, p.h, Factors{keep, step_size, root, gs, old_ms, old_vs, step, p.h.grad_scale != nullptr});
+        float r[8], most_m, most_v, least;
+        update<BITS>(w, g, m, v, r, n, p.h, f, most_m, most_v, least);
         if constexpr (BITS == 8) {
-            float most_m = 0.0f, most_r = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (!vec && i >= n) {
-                    m[i] = 0.0f;       // (behind the tensor's end: a NaN scale's 0 x NaN)
-                    r[i] = 0.0f;
-                }
-                most_m = fp8mm::max_nan(most_m, fabsf(m[i]));
-                most_r = fp8mm::max_nan(most_r, r[i]);
-            }
-            const float ms = __fdiv_rn(warp_max(most_m), 448.0f), vs = __fdiv_rn(warp_max(most_r), 448.0f);
+            Scale ms, vs;
+            block_scales(most_m, most_v, lane, ms, vs);
             if (lane == 0) {
-                t.m_scale[block] = ms;
-                t.v_scale[block] = vs;
+                t.m_scale[block] = ms.s;
+                t.v_scale[block] = vs.s;
             }
-            encode(m, r, ms, vs, static_cast<uint32_t>(at), stride, step);
+            encode(m, r, ms, vs, least, static_cast<uint32_t>(at), stride, f.step);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] = r[i];
