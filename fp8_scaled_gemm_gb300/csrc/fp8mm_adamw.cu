@@ -19,12 +19,21 @@ struct Stretch {
     bool written;
 };
 
-template <int BITS, int T>
+template <int BITS, bool W32, bool MASTER, bool G32, int T>
 int launch(const Params<T> &p, int sms, cudaStream_t stream)
 {
     // as many CTAs as run at once, a block of 256 elements a warp and turn
     const int64_t grid = std::min<int64_t>(cdiv(p.blocks, kThreads / 32), static_cast<int64_t>(sms) * kCtasPerSm);
-    return launch_pdl(adamw_kernel<BITS, T>, static_cast<int>(grid), kThreads, 0, stream, "AdamW launch", p);
+    return launch_pdl(adamw_kernel<BITS, W32, MASTER, G32, T>, static_cast<int>(grid), kThreads, 0, stream, "AdamW launch", p);
+}
+
+template <int BITS, bool G32, int T>
+int launch_types(const Params<T> &p, bool masters, int sms, cudaStream_t stream)
+{
+    if (masters)
+        return launch<BITS, true, true, G32>(p, sms, stream);
+    return p.param_type == FP8MM_OUT_F32 ? launch<BITS, true, false, G32>(p, sms, stream)
+                                         : launch<BITS, false, false, G32>(p, sms, stream);
 }
 
 // Tensors [from, to) of the call, T at most, which hold anything.
@@ -36,6 +45,7 @@ int step_some(const fp8mm_adamw_tensor *tensors, int64_t from, int64_t to, const
     p.h = h;
     p.param_type = o.param_type;
     p.grad_type = o.grad_type;
+    bool masters = false;              // (all have one, or none)
     const int code = o.state_bits == 8 ? 8 : 16;      // alignment of 8 elements of a state
     for (int64_t i = from; i < to; ++i) {
         const fp8mm_adamw_tensor &a = tensors[i];
@@ -53,12 +63,14 @@ int step_some(const fp8mm_adamw_tensor *tensors, int64_t from, int64_t to, const
         t.first = p.blocks;
         t.vec = aligned_to(a.param, 16) && aligned_to(a.grad, 16) && aligned_to(a.master, 16) && aligned_to(t.m, code) &&
                 aligned_to(t.v, code);
-        p.has_master = a.master != nullptr;
+        masters = a.master != nullptr;
         p.blocks += cdiv(a.count, kBlock);
     }
     if (p.tensors == 0)
         return FP8MM_OK;
-    return o.state_bits == 8 ? launch<8>(p, sms, stream) : launch<32>(p, sms, stream);
+    if (p.grad_type == FP8MM_OUT_F32)
+        return o.state_bits == 8 ? launch_types<8, true>(p, masters, sms, stream) : launch_types<32, true>(p, masters, sms, stream);
+    return o.state_bits == 8 ? launch_types<8, false>(p, masters, sms, stream) : launch_types<32, false>(p, masters, sms, stream);
 }
 
 }  // namespace

@@ -61,7 +61,7 @@ struct Hyper {
 template <int T>
 struct Params {
     Hyper h;
-    int tensors, param_type, grad_type, has_master;
+    int tensors, param_type, grad_type;
     long long blocks;
     Tensor t[T];
 };
@@ -275,12 +275,11 @@ struct Factors {
 };
 
 // ------------------------------------------------------- the step of one lane ---
-// Eight elements, of which n are there (the others count as zeros): w, m and v (codes'
-// values with BITS = 8) become the new ones, r the root of v; two at a time, in
+// Eight elements: w, m and v (codes' values with BITS = 8) become the new ones, r the root of v; two at a time, in
 // single operations each rounded by itself. Gives the largest |m| and v and the least
 // v, of which the last is 0 where the pairs' range was left.
 template <int BITS>
-__device__ __forceinline__ void update(float (&w)[8], float (&g)[8], float (&m)[8], float (&v)[8], float (&r)[8], int n,
+__device__ __forceinline__ void update(float (&w)[8], const float (&g)[8], float (&m)[8], float (&v)[8], float (&r)[8],
                                        const Hyper &h, const Factors &f, float &most_m, float &most_v, float &least)
 {
     uint64_t m2[4], v2[4];
@@ -302,12 +301,6 @@ __device__ __forceinline__ void update(float (&w)[8], float (&g)[8], float (&m)[
         v2[i] = add2(ptx::mul_f32x2(v2[i], both(h.b2)), ptx::mul_f32x2(ptx::mul_f32x2(gi, gi), both(h.b2c)));
         ptx::unpack_f32x2(m2[i], m[2 * i], m[2 * i + 1]);
         ptx::unpack_f32x2(v2[i], v[2 * i], v[2 * i + 1]);
-        if (n < 8) {
-            // (0 times a NaN scale)
-            for (int j = 2 * i; j < 2 * i + 2; ++j)
-                if (j >= n)
-                    m[j] = v[j] = 0.0f;
-        }
         least = min3(least, v[2 * i], v[2 * i + 1]);
         most_v = max3_nan(most_v, v[2 * i], v[2 * i + 1]);
         most_m = max3_nan(most_m, fabsf(m[2 * i]), fabsf(m[2 * i + 1]));
@@ -369,7 +362,136 @@ __device__ __forceinline__ void encode(float (&m)[8], float (&r)[8], const Scale
         r[i] = round_by(r[i], dither(e0 + static_cast<uint32_t>(stride * i), step));
 }
 
-template <int BITS, int T>
+// -------------------------------------------------------------- blocks ---
+// W32: w is read as fp32 (from the master or an fp32 parameter), MASTER: there are
+// masters, G32: gradients are fp32; else 16-bit types, of which only the conversions
+// differ.
+
+// A whole block in 16-byte words, 8 neighbours a lane.
+template <int BITS, bool W32, bool MASTER, bool G32>
+__device__ __forceinline__ void whole_block(const Tensor &t, long long block, int param_type, int grad_type, const Hyper &h, Factors &f,
+                                            int lane)
+{
+    const long long at = block * kBlock + lane * 8;
+    const int w_type = W32 ? fp8rows::kF32 : param_type, g_type = G32 ? fp8rows::kF32 : grad_type;
+    Eight rw, rg, rm, rv;
+    load8(rw, MASTER ? static_cast<const void *>(t.master) : t.param, w_type, at);
+    load8(rg, t.grad, g_type, at);
+    if constexpr (BITS == 32) {
+        load8(rm, t.m, fp8rows::kF32, at);
+        load8(rv, t.v, fp8rows::kF32, at);
+    } else {
+        const uint2 a = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(t.m) + at));
+        const uint2 c = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(t.v) + at));
+        rm.w[0] = a.x; rm.w[1] = a.y;
+        rv.w[0] = c.x; rv.w[1] = c.y;
+        f.ms = __ldcg(t.m_scale + block);
+        f.vs = __ldcg(t.v_scale + block);
+    }
+    float w[8], g[8], m[8], v[8];
+    floats8(rw, w_type, w);
+    floats8(rg, g_type, g);
+    if constexpr (BITS == 32) {
+        floats8(rm, fp8rows::kF32, m);
+        floats8(rv, fp8rows::kF32, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = decode2(rm.w[i / 2] >> (16 * (i % 2))), y = decode2(rv.w[i / 2] >> (16 * (i % 2)));
+            m[2 * i] = x.x;
+            m[2 * i + 1] = x.y;
+            v[2 * i] = y.x;
+            v[2 * i + 1] = y.y;
+        }
+    }
+    float r[8], most_m, most_v, least;
+    update<BITS>(w, g, m, v, r, h, f, most_m, most_v, least);
+    if constexpr (MASTER)
+        store8(t.master, fp8rows::kF32, at, w);
+    store8(t.param, W32 && !MASTER ? fp8rows::kF32 : param_type, at, w);
+    if constexpr (BITS == 32) {
+        store8(t.m, fp8rows::kF32, at, m);
+        store8(t.v, fp8rows::kF32, at, v);
+    } else {
+        Scale ms, vs;
+        block_scales(most_m, most_v, lane, ms, vs);
+        if (lane == 0) {
+            t.m_scale[block] = ms.s;
+            t.v_scale[block] = vs.s;
+        }
+        encode(m, r, ms, vs, least, static_cast<uint32_t>(at), 1, f.step);
+        uint32_t cm[4], cv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            cm[i] = fp8q::cvt_pair(m[2 * i], m[2 * i + 1], 0);
+            cv[i] = fp8q::cvt_pair(r[2 * i], r[2 * i + 1], 0);
+        }
+        __stcs(reinterpret_cast<uint2 *>(static_cast<uint8_t *>(t.m) + at), make_uint2(cm[0] | cm[1] << 16, cm[2] | cm[3] << 16));
+        __stcs(reinterpret_cast<uint2 *>(static_cast<uint8_t *>(t.v) + at), make_uint2(cv[0] | cv[1] << 16, cv[2] | cv[3] << 16));
+    }
+}
+
+// A tensor's last block, or one of a tensor without that alignment: single elements,
+// every 32nd of the block a lane. What is behind the end counts as zeros.
+template <int BITS>
+__device__ __noinline__ void any_block(const Tensor &t, long long block, int param_type, int grad_type, bool master, const Hyper &h,
+                                       Factors f, int lane)
+{
+    const long long at = block * kBlock + lane;
+    const int n = static_cast<int>(min(8ll, (t.count - at + 31) / 32));    // (<= 0: none)
+    float w[8], g[8], m[8], v[8], r[8];
+    if constexpr (BITS == 8) {
+        f.ms = __ldcg(t.m_scale + block);
+        f.vs = __ldcg(t.v_scale + block);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const long long e = at + 32 * i;
+        const bool in = i < n;
+        w[i] = in ? (master ? t.master[e] : load1(t.param, param_type, e)) : 0.0f;
+        g[i] = in ? load1(t.grad, grad_type, e) : 0.0f;
+        m[i] = !in ? 0.0f : BITS == 32 ? static_cast<const float *>(t.m)[e] : decode1(static_cast<const uint8_t *>(t.m)[e]);
+        v[i] = !in ? 0.0f : BITS == 32 ? static_cast<const float *>(t.v)[e] : decode1(static_cast<const uint8_t *>(t.v)[e]);
+    }
+    float most_m, most_v, least;
+    update<BITS>(w, g, m, v, r, h, f, most_m, most_v, least);
+    if constexpr (BITS == 8) {
+        most_m = most_v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) {               // (behind the end, 0 times a NaN scale)
+                most_m = fp8mm::max_nan(most_m, fabsf(m[i]));
+                most_v = fp8mm::max_nan(most_v, v[i]);
+            }
+        __syncwarp();
+        Scale ms, vs;
+        block_scales(most_m, most_v, lane, ms, vs);
+        if (lane == 0) {
+            t.m_scale[block] = ms.s;
+            t.v_scale[block] = vs.s;
+        }
+        encode(m, r, ms, vs, least, static_cast<uint32_t>(at), 32, f.step);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const long long e = at + 32 * i;
+        if (i >= n)
+            break;
+        const float one[1] = {w[i]};
+        if (master)
+            t.master[e] = w[i];
+        fp8rows::store_group<1>(t.param, param_type, e, one);
+        if constexpr (BITS == 32) {
+            static_cast<float *>(t.m)[e] = m[i];
+            static_cast<float *>(t.v)[e] = v[i];
+        } else {
+            static_cast<uint8_t *>(t.m)[e] = static_cast<uint8_t>(fp8q::cvt_pair(m[i], 0.0f, 0));
+            static_cast<uint8_t *>(t.v)[e] = static_cast<uint8_t>(fp8q::cvt_pair(r[i], 0.0f, 0));
+        }
+    }
+}
+
+template <int BITS, bool W32, bool MASTER, bool G32, int T>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) adamw_kernel(const __grid_constant__ Params<T> p)
 {
     __shared__ float shared_hyper[3];
@@ -410,108 +532,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) adamw_kernel(const __gri
         while (k + 1 < p.tensors && b >= p.t[k + 1].first)
             ++k;
         const Tensor &t = p.t[k];
-        const long long block = b - t.first, e0 = block * kBlock;
-        const bool vec = t.vec && e0 + kBlock <= t.count;
-        // lane's elements: 8 neighbours, or (without 16-byte accesses) every 32nd
-        const long long at = vec ? e0 + lane * 8 : e0 + lane;
-        const int stride = vec ? 1 : 32;
-        const int n = vec ? 8 : static_cast<int>(min(8ll, (t.count - at + 31) / 32));   // (<= 0: none)
-        const float *w_from = p.has_master ? t.master : nullptr;
-        float w[8], g[8], m[8], v[8];
-        if (BITS == 8) {
-            f.ms = __ldcg(t.m_scale + block);
-            f.vs = __ldcg(t.v_scale + block);
-        }
-        if (vec) {
-            Eight rw, rg, rm, rv;
-            const int w_type = p.has_master ? fp8rows::kF32 : p.param_type;
-            load8(rw, p.has_master ? static_cast<const void *>(w_from) : t.param, w_type, at);
-            load8(rg, t.grad, p.grad_type, at);
-            if constexpr (BITS == 32) {
-                load8(rm, t.m, fp8rows::kF32, at);
-                load8(rv, t.v, fp8rows::kF32, at);
-            } else {
-                const uint2 a = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(t.m) + at));
-                const uint2 c = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(t.v) + at));
-                rm.w[0] = a.x; rm.w[1] = a.y;
-                rv.w[0] = c.x; rv.w[1] = c.y;
-            }
-            floats8(rw, w_type, w);
-            floats8(rg, p.grad_type, g);
-            if constexpr (BITS == 32) {
-                floats8(rm, fp8rows::kF32, m);
-                floats8(rv, fp8rows::kF32, v);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 x = decode2(rm.w[i / 2] >> (16 * (i % 2))), y = decode2(rv.w[i / 2] >> (16 * (i % 2)));
-                    m[2 * i] = x.x;
-                    m[2 * i + 1] = x.y;
-                    v[2 * i] = y.x;
-                    v[2 * i + 1] = y.y;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const long long e = at + 32 * i;
-                const bool in = i < n;
-                w[i] = in ? (p.has_master ? w_from[e] : load1(t.param, p.param_type, e)) : 0.0f;
-                g[i] = in ? load1(t.grad, p.grad_type, e) : 0.0f;
-                m[i] = !in ? 0.0f : BITS == 32 ? static_cast<const float *>(t.m)[e] : decode1(static_cast<const uint8_t *>(t.m)[e]);
-                v[i] = !in ? 0.0f : BITS == 32 ? static_cast<const float *>(t.v)[e] : decode1(static_cast<const uint8_t *>(t.v)[e]);
-            }
-        }
-        float r[8], most_m, most_v, least;
-        update<BITS>(w, g, m, v, r, n, p.h, f, most_m, most_v, least);
-        if constexpr (BITS == 8) {
-            Scale ms, vs;
-            block_scales(most_m, most_v, lane, ms, vs);
-            if (lane == 0) {
-                t.m_scale[block] = ms.s;
-                t.v_scale[block] = vs.s;
-            }
-            encode(m, r, ms, vs, least, static_cast<uint32_t>(at), stride, f.step);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = r[i];
-        }
-        if (vec) {
-            if (p.has_master)
-                store8(t.master, fp8rows::kF32, at, w);
-            store8(t.param, p.param_type, at, w);
-            if constexpr (BITS == 32) {
-                store8(t.m, fp8rows::kF32, at, m);
-                store8(t.v, fp8rows::kF32, at, v);
-            } else {
-                uint32_t cm[4], cv[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    cm[i] = fp8q::cvt_pair(m[2 * i], m[2 * i + 1], 0);
-                    cv[i] = fp8q::cvt_pair(v[2 * i], v[2 * i + 1], 0);
-                }
-                __stcs(reinterpret_cast<uint2 *>(static_cast<uint8_t *>(t.m) + at), make_uint2(cm[0] | cm[1] << 16, cm[2] | cm[3] << 16));
-                __stcs(reinterpret_cast<uint2 *>(static_cast<uint8_t *>(t.v) + at), make_uint2(cv[0] | cv[1] << 16, cv[2] | cv[3] << 16));
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const long long e = at + 32 * i;
-                if (i >= n)
-                    break;
-                const float one[1] = {w[i]};
-                if (p.has_master)
-                    t.master[e] = w[i];
-                fp8rows::store_group<1>(t.param, p.param_type, e, one);
-                if constexpr (BITS == 32) {
-                    static_cast<float *>(t.m)[e] = m[i];
-                    static_cast<float *>(t.v)[e] = v[i];
-                } else {
-                    static_cast<uint8_t *>(t.m)[e] = static_cast<uint8_t>(fp8q::cvt_pair(m[i], 0.0f, 0));
-                    static_cast<uint8_t *>(t.v)[e] = static_cast<uint8_t>(fp8q::cvt_pair(v[i], 0.0f, 0));
-                }
-            }
-        }
+        const long long block = b - t.first;
+        if (t.vec && (block + 1) * kBlock <= t.count)
+            whole_block<BITS, W32, MASTER, G32>(t, block, p.param_type, p.grad_type, p.h, f, lane);
+        else
+            any_block<BITS>(t, block, p.param_type, p.grad_type, MASTER, p.h, f, lane);
     }
 }
 
