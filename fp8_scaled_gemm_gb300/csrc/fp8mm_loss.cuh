@@ -364,23 +364,78 @@ __device__ __forceinline__ float sum_rows(float (&v)[16], int lane)
     return v[0];
 }
 
-// z of N columns of a row from the accumulator: times the scales, plus the bias.
-template <int N>
-__device__ __forceinline__ void logits(float (&v)[N], const float *cols, float row_scale)
+// z of N columns of a row from the accumulator: times the scales, plus the biases.
+template <bool BIASED, int N>
+__device__ __forceinline__ void logits(float (&v)[N], const float *scales, const float *biases, float row_scale)
 {
     const uint64_t rs2 = ptx::f32x2(row_scale, row_scale);
 #pragma unroll
-    for (int k = 0; k < N; k += 2) {
-        const float4 c = *reinterpret_cast<const float4 *>(cols + k * 2);
-        const uint64_t s2 = ptx::mul_f32x2(rs2, ptx::f32x2(c.x, c.y));
-        ptx::unpack_f32x2(ptx::fma_f32x2(ptx::f32x2(v[k], v[k + 1]), s2, ptx::f32x2(c.z, c.w)), v[k], v[k + 1]);
+    for (int k = 0; k < N; k += 4) {
+        const float4 s = *reinterpret_cast<const float4 *>(scales + k);
+        const uint64_t s0 = ptx::mul_f32x2(rs2, ptx::f32x2(s.x, s.y)), s1 = ptx::mul_f32x2(rs2, ptx::f32x2(s.z, s.w));
+        uint64_t z0 = ptx::f32x2(v[k], v[k + 1]), z1 = ptx::f32x2(v[k + 2], v[k + 3]);
+        if constexpr (BIASED) {
+            const float4 b = *reinterpret_cast<const float4 *>(biases + k);
+            z0 = ptx::fma_f32x2(z0, s0, ptx::f32x2(b.x, b.y));
+            z1 = ptx::fma_f32x2(z1, s1, ptx::f32x2(b.z, b.w));
+        } else {
+            z0 = ptx::mul_f32x2(z0, s0);
+            z1 = ptx::mul_f32x2(z1, s1);
+        }
+        ptx::unpack_f32x2(z0, v[k], v[k + 1]);
+        ptx::unpack_f32x2(z1, v[k + 2], v[k + 3]);
     }
 }
 
-// (v - off) log2(e) of two columns.
-__device__ __forceinline__ void exponents(float v0, float v1, uint64_t minus_off, float &lo, float &hi)
+// exp(z - off) of many z as 2^(z log2(e) - o) in one operation a value, with o = off
+// log2(e) rounded; the rounding is taken off by a factor `rest` of the results, so that
+// it does not show where their sum is close to 1. An off so large (a row whose every
+// column has the type's lowest value) that o overflows: `wild`, (z - off) log2(e).
+struct Offset {
+    uint64_t log2e2, add;              // wild: minus off, twice
+    float rest;
+    bool wild;
+    __device__ __forceinline__ explicit Offset(float off)
+    {
+        const float o = off * kLog2e;
+        wild = __any_sync(0xFFFFFFFFu, fabsf(off) > 0x1p126f);
+        rest = wild ? 1.0f : fp8mm::ex2_approx(-fmaf(off, kLog2e, -o));
+        add = wild ? ptx::f32x2(-off, -off) : ptx::f32x2(-o, -o);
+        log2e2 = ptx::f32x2(kLog2e, kLog2e);
+    }
+    template <bool WILD>
+    __device__ __forceinline__ void exponentials(float v0, float v1, float &e0, float &e1) const
+    {
+        const uint64_t v = ptx::f32x2(v0, v1);
+        float lo, hi;
+        if constexpr (WILD)
+            ptx::unpack_f32x2(ptx::mul_f32x2(ptx::add_f32x2(v, add), log2e2), lo, hi);
+        else
+            ptx::unpack_f32x2(ptx::fma_f32x2(v, log2e2, add), lo, hi);
+        e0 = fp8mm::ex2_approx(lo);
+        e1 = fp8mm::ex2_approx(hi);
+    }
+    // v = exp(v - off) / rest
+    template <int N>
+    __device__ __forceinline__ void exponentials(float (&v)[N]) const
+    {
+        if (wild) {
+#pragma unroll
+            for (int k = 0; k < N; k += 2)
+                exponentials<true>(v[k], v[k + 1], v[k], v[k + 1]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; k += 2)
+                exponentials<false>(v[k], v[k + 1], v[k], v[k + 1]);
+        }
+    }
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c)
 {
-    ptx::unpack_f32x2(ptx::mul_f32x2(ptx::add_f32x2(ptx::f32x2(v0, v1), minus_off), ptx::f32x2(kLog2e, kLog2e)), lo, hi);
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
 }
 
 // One warp's block of 32 rows into its swizzled stage: lane `row` writes the
@@ -669,8 +724,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
         const int q = warp & 3, ew = warp - 2, part = ew / 4;
         uint8_t *stage = smem + kStagingAt + ew * C::kBlockBytes;
         const uint32_t stage_smem = sbase + kStagingAt + ew * C::kBlockBytes;
-        float *cols = reinterpret_cast<float *>(smem + kColsAt) + ew * C::kCols * C::kColFloats;   // (s0, s1, b0, b1) per pair
-        float *col_mantissa = cols + 2 * C::kCols;
+        float *col_scale = reinterpret_cast<float *>(smem + kColsAt) + ew * C::kCols * C::kColFloats;
+        float *col_bias = col_scale + C::kCols, *col_mantissa = col_bias + C::kCols;
         int acc = 0;
         uint32_t acc_phase = 0;
         float slope_scale = 1.0f, out_scale[2] = {1.0f, 1.0f};
@@ -710,8 +765,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
         bool live = false;
         float top = -INFINITY, sum = 0.0f;       // of the row in this unit so far
         Schedule<KIND> tiles(p, pair, pairs);
-        Work w;
-        while (tiles.next(w)) {
+        Work w{}, ahead{};
+        // the columns' scales and biases of a tile, loaded while the one before it is
+        // worked on
+        float next_scale[2] = {}, next_bias[2] = {};
+        auto load_columns = [&]() {
+            const int first = ahead.tq * p.t[0].width + part * 64;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                // columns past the end: z = -inf, which adds nothing
+                const int n = first + i * 32 + lane;
+                const bool there = n < p.N;
+                next_scale[i] = there ? (p.rowwise ? __ldg(p.scale_b + n) : s_tensor) : 0.0f;
+                next_bias[i] = there ? bias_at(p, n) : -INFINITY;
+            }
+        };
+        bool more = tiles.next(ahead);
+        if (C::kFp8 && more)
+            load_columns();
+        while (more) {
+            w = ahead;
             const TileSpace &t = p.t[KIND == kGrad ? w.of : 0];
             const Maps &m = maps.of[KIND == kGrad ? w.of : 0];
             const int row0 = (2 * w.tp + static_cast<int>(rank)) * t.half + q * 32, row = row0 + lane;
@@ -719,21 +792,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
             // (a narrow tile's last warps have one block or none)
             const int blocks = q * 32 >= t.half ? 0 : min(2, (min(t.width, t.cols - w.tq * t.width) - part * 64 + 31) / 32);
             // what the tile needs beside the accumulator, while the MMAs run
+            const bool biased = p.bias || col0 + 64 > t.cols;
             if constexpr (C::kFp8) {
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int c = i * 32 + lane, n = col0 + c;
-                    const bool there = n < p.N;
-                    const float s = there && p.rowwise ? __ldg(p.scale_b + n) : s_tensor;
-                    // columns past the end: z = -inf, which adds nothing
-                    cols[(c >> 1) * 4 + (c & 1)] = there ? s : 0.0f;
-                    cols[(c >> 1) * 4 + 2 + (c & 1)] = there ? bias_at(p, n) : -INFINITY;
+                    col_scale[i * 32 + lane] = next_scale[i];
+                    col_bias[i * 32 + lane] = next_bias[i];
                     if constexpr (KIND == kSlope)
-                        col_mantissa[c] = p.rowwise ? mantissa(s) : mb_tensor;
+                        col_mantissa[i * 32 + lane] = p.rowwise ? mantissa(next_scale[i]) : mb_tensor;
                 }
                 __syncwarp();
+            }
+            more = tiles.next(ahead);
+            if (C::kFp8 && more)
+                load_columns();
+            if constexpr (C::kFp8) {
                 if (w.first) {
+                    // this row of A
                     rs = 1.0f;
                     ma = ma_tensor;
                     gs = 0.0f;
@@ -769,15 +845,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
             const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kTile + part * 64);
 
             if constexpr (C::kFp8) {
+                const Offset off(lse);           // (kSlope)
+                const float gs_rest = gs * off.rest;
 #pragma unroll 1
                 for (int i = 0; i < blocks; ++i) {
                     const int n0 = col0 + i * 32;
-                    const float *here = cols + i * 64, *here_m = col_mantissa + i * 32;
+                    const float *scales = col_scale + i * 32, *biases = col_bias + i * 32, *mantissas = col_mantissa + i * 32;
                     const bool mine = at >= n0 && at < n0 + 32;
                     if constexpr (KIND == kStats) {
                         float v[32];
                         ptx::tmem_ld_32cols(trow + i * 32, v);
-                        logits(v, here, rs);
+                        if (biased)
+                            logits<true>(v, scales, biases, rs);
+                        else
+                            logits<false>(v, scales, biases, rs);
                         if (mine) {
                             float zt = 0.0f;
 #pragma unroll
@@ -787,37 +868,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                         }
                         float most = top;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            most = fmaxf(most, v[k]);
+                        for (int k = 0; k < 32; k += 2)
+                            most = max3(most, v[k], v[k + 1]);
                         // (a row without a finite value so far: exp(-inf - 0) = 0)
                         const float ref = most == -INFINITY ? 0.0f : most;
-                        const uint64_t off = ptx::f32x2(-ref, -ref);
+                        const Offset from(ref);
+                        from.exponentials(v);
                         uint64_t s2[2] = {0, 0};
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            float lo, hi;
-                            exponents(v[2 * k], v[2 * k + 1], off, lo, hi);
-                            s2[k & 1] = ptx::add_f32x2(s2[k & 1], ptx::f32x2(fp8mm::ex2_approx(lo), fp8mm::ex2_approx(hi)));
-                        }
+                        for (int k = 0; k < 16; ++k)
+                            s2[k & 1] = ptx::add_f32x2(s2[k & 1], ptx::f32x2(v[2 * k], v[2 * k + 1]));
                         float s0, s1;
                         ptx::unpack_f32x2(ptx::add_f32x2(s2[0], s2[1]), s0, s1);
-                        sum = sum * fp8mm::ex2_approx((top - ref) * kLog2e) + (s0 + s1);
+                        sum = sum * fp8mm::ex2_approx((top - ref) * kLog2e) + (s0 + s1) * from.rest;
                         top = most;
                     } else {
                         // 16 columns at a time: 26 warps have 72 registers each
-                        const uint64_t off = ptx::f32x2(-lse, -lse);
 #pragma unroll 1
                         for (int j = 0; j < 2; ++j) {
                             float v[16];
                             ptx::tmem_ld_16cols(trow + i * 32 + j * 16, v);
-                            logits(v, here + j * 32, rs);
+                            if (biased)
+                                logits<true>(v, scales + j * 16, biases + j * 16, rs);
+                            else
+                                logits<false>(v, scales + j * 16, biases + j * 16, rs);
+                            off.exponentials(v);
 #pragma unroll
-                            for (int k = 0; k < 16; k += 2) {
-                                float lo, hi;
-                                exponents(v[k], v[k + 1], off, lo, hi);
-                                v[k] = live ? fp8mm::ex2_approx(lo) * gs : 0.0f;
-                                v[k + 1] = live ? fp8mm::ex2_approx(hi) * gs : 0.0f;
-                            }
+                            for (int k = 0; k < 16; ++k)
+                                v[k] = live ? v[k] * gs_rest : 0.0f;
                             if (mine) {
 #pragma unroll
                                 for (int k = 0; k < 16; ++k)
@@ -827,8 +905,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                                 stage_free();
 #pragma unroll
                             for (int k = 0; k < 16; k += 8) {
-                                const float4 x = *reinterpret_cast<const float4 *>(here_m + j * 16 + k);
-                                const float4 y = *reinterpret_cast<const float4 *>(here_m + j * 16 + k + 4);
+                                const float4 x = *reinterpret_cast<const float4 *>(mantissas + j * 16 + k);
+                                const float4 y = *reinterpret_cast<const float4 *>(mantissas + j * 16 + k + 4);
                                 const float o[8] = {v[k] * x.x, v[k + 1] * x.y, v[k + 2] * x.z, v[k + 3] * x.w,
                                                     v[k + 4] * y.x, v[k + 5] * y.y, v[k + 6] * y.z, v[k + 7] * y.w};
                                 stage_chunk64(stage, lane, j * 2 + k / 8, pack8(o, fp8rows::kF16));
