@@ -66,6 +66,7 @@ TileSpace tile_space(int64_t rows, int64_t cols, int width, int64_t kblocks, int
     t.group = std::min(t.tiles_p, 16);
     t.splits = splits;
     t.run = run;
+    t.units_in_group = t.group * static_cast<int>(cdiv(t.tiles_q, run));
     t.num_units = t.tiles_p * static_cast<int>(cdiv(t.tiles_q, run)) * splits;
     return t;
 }
