@@ -864,6 +864,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                 break;
             ptx::tc_fence_after();
             const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kTile + part * 64);
+            // the accumulator is the MMA's again as soon as this warp's last block of it is
+            // in registers
+            bool given_back = false;
+            auto give_back = [&]() {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(tempty_bar(acc), 0));
+                given_back = true;
+            };
 
             if constexpr (C::kFp8) {
                 const Offset off(lse);           // (kSlope)
@@ -876,6 +886,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                     if constexpr (KIND == kStats) {
                         float v[32];
                         ptx::tmem_ld_32cols(trow + i * 32, v);
+                        if (i + 1 == blocks)
+                            give_back();
                         if (biased)
                             logits<true>(v, scales, biases, rs);
                         else
@@ -909,6 +921,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                         for (int j = 0; j < 2; ++j) {
                             float v[16];
                             ptx::tmem_ld_16cols(trow + i * 32 + j * 16, v);
+                            if (j == 1 && i + 1 == blocks)
+                                give_back();
                             if (biased)
                                 logits<true>(v, scales + j * 16, biases + j * 16, rs);
                             else
@@ -959,6 +973,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                 for (int i = 0; i < 2 && q * 32 < t.half; ++i) {
                     float v[32];
                     ptx::tmem_ld_32cols(trow + i * 32, v);
+                    if (i == 1)
+                        give_back();
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
                         v[k] *= row_factor;
@@ -980,10 +996,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                     }
                 }
             }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(tempty_bar(acc), 0));
+            if (!given_back)
+                give_back();
             if (++acc == 2) {
                 acc = 0;
                 acc_phase ^= 1u;
