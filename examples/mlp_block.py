@@ -87,20 +87,20 @@ class MlpBlock:
 
 
 def train(tokens: int, width: int, hidden: int, steps: int, lr: float = 3e-3, device="cuda", log=print):
-    """Fit a block to a random linear map of its input with Adam; returns the losses."""
+    """Fit a block to a random linear map of its input with Adam (AdamW without decay); returns the losses."""
     g = torch.Generator(device=device).manual_seed(1)
     target = torch.randn(width, width, generator=g, device=device) * width ** -0.5
     block = MlpBlock(width, hidden, device)
-    adam = torch.optim.Adam(block.params.values(), lr=lr)
+    names = list(block.params)
+    params = [block.params[k] for k in names]
+    exp_avgs, exp_avg_sqs = ([torch.zeros_like(p) for p in params] for _ in range(2))
     losses = []
     for step in range(steps):
         x = torch.randn(tokens, width, generator=g, device=device).bfloat16()
         e = block.forward(x).float() - x.float() @ target
         losses.append(float(e.square().mean()))
         block.backward((e * (2.0 / (tokens * width))).bfloat16())
-        for k, v in block.params.items():
-            v.grad = block.grads[k]
-        adam.step()
+        fm.fp8_adamw(params, [block.grads[k] for k in names], exp_avgs, exp_avg_sqs, step + 1, lr=lr, weight_decay=0.0)
         if step % 10 == 0 or step == steps - 1:
             log(f"step {step:4d}  loss {losses[-1]:.4f}")
     return losses

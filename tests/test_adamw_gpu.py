@@ -236,6 +236,21 @@ def test_bits_of_single_operations(bits, param, master):
         assert s.same(plain)
 
 
+@pytest.mark.parametrize("numerators", ["ones", "random"])
+def test_roots_and_quotients_of_every_mantissa(numerators):
+    """v over all fp32 values in [1, 4): with beta1 = beta2 = 1/2, no gradient, eps of 2^-60 and t so large that the
+    corrections are 1, the new v and m are halves of the old and w becomes -m / sqrt(v), both correctly rounded."""
+    n = 1 << 24
+    v = (torch.arange(n, device="cuda", dtype=torch.int32) + 0x3F800000).view(F32)
+    m = torch.ones(n, device="cuda")
+    if numerators == "random":
+        m = torch.randn(n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+    w, want = torch.zeros(n, device="cuda"), -(m / torch.sqrt(v))
+    fm.fp8_adamw([w], [torch.zeros(n, device="cuda")], [2 * m], [2 * v], 200, lr=1.0, beta1=0.5, beta2=0.5, eps=2.0 ** -60,
+                 weight_decay=0.0)
+    assert torch.equal(w, want)
+
+
 def test_rounding_of_the_root_keeps_its_mean():
     """Roots that decay by 0.05 % a step beside one that stays: the nearest code would be the old one every time."""
     n = 256 * 400
