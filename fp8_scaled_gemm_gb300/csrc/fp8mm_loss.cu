@@ -3,12 +3,15 @@
 #include "fp8mm_loss.cuh"
 #include "fp8mm_rows_host.h"
 
+#include <initializer_list>
+
 namespace {
 
 using namespace fp8mm_host;
 using namespace fp8loss;
 
 constexpr int64_t kPieceBytes = int64_t(1) << 30;   // of dz, and of the piece of B in fp16
+constexpr int64_t kMostRows = INT32_MAX - 1024;     // of A and columns of B: tiles' coordinates are int
 
 int64_t aligned(int64_t bytes) { return cdiv(bytes, 256) * 256; }
 
@@ -19,7 +22,7 @@ int check_problem(const void *A, const void *B, const float *sa, const float *sb
         (a_type != FP8MM_TYPE_E4M3 && a_type != FP8MM_TYPE_E5M2) ||
         (b_type != FP8MM_TYPE_E4M3 && b_type != FP8MM_TYPE_E5M2) || !row_type_known(bias_type))
         return FP8MM_ERR_MODE;
-    if (M < 0 || N < 1 || M > INT32_MAX || N > INT32_MAX || K < 16 || K % 16 != 0 || K > (int64_t(1) << 24))
+    if (M < 0 || N < 1 || M > kMostRows || N > kMostRows || K < 16 || K % 16 != 0 || K > (int64_t(1) << 24))
         return FP8MM_ERR_SHAPE;
     // tiles of 256 x 256 and their K slices are counted in int
     if (cdiv(M, kTile) * cdiv(N, kTile) > (int64_t(1) << 24) || M > (int64_t(1) << 40) / N)
@@ -33,6 +36,30 @@ int check_problem(const void *A, const void *B, const float *sa, const float *sb
         (reinterpret_cast<uintptr_t>(bias) & (row_type_bytes(bias_type) - 1)) || (reinterpret_cast<uintptr_t>(target) & 7))
         return FP8MM_ERR_ALIGN;
     return FP8MM_OK;
+}
+
+// Memory of a call: what is written must not overlap anything else of it.
+struct Stretch {
+    const void *at;
+    int64_t bytes;
+};
+bool overlap(const Stretch &a, const Stretch &b)
+{
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.at), q = reinterpret_cast<uintptr_t>(b.at);
+    return a.at && b.at && a.bytes > 0 && b.bytes > 0 && p < q + static_cast<uintptr_t>(b.bytes) &&
+           q < p + static_cast<uintptr_t>(a.bytes);
+}
+bool written_apart(std::initializer_list<Stretch> written, std::initializer_list<Stretch> read)
+{
+    for (const Stretch *w = written.begin(); w != written.end(); ++w) {
+        for (const Stretch *o = w + 1; o != written.end(); ++o)
+            if (overlap(*w, *o))
+                return false;
+        for (const Stretch &r : read)
+            if (overlap(*w, r))
+                return false;
+    }
+    return true;
 }
 
 // A matrix of `rows` x `cols` elements, rows `ld` elements apart, `items` of
@@ -168,7 +195,7 @@ struct GradPlan {
 GradPlan plan_grad(int64_t M, int64_t N, int64_t K, bool da, bool db, bool dbias, int sms)
 {
     GradPlan g{};
-    const int64_t most = std::max<int64_t>(2048, kPieceBytes / 2 / std::max(M, K) / kTile * kTile);
+    const int64_t most = std::max<int64_t>(kTile, kPieceBytes / 2 / std::max(M, K) / kTile * kTile);
     g.pieces = cdiv(N, most);
     g.piece = cdiv(cdiv(N, g.pieces), kTile) * kTile;
     g.pieces = cdiv(N, g.piece);
@@ -226,7 +253,7 @@ extern "C" {
 
 int64_t fp8_cross_entropy_workspace(int64_t M, int64_t N)
 {
-    if (M < 0 || N < 1 || M > INT32_MAX || N > INT32_MAX || M > (int64_t(1) << 40) / N)
+    if (M < 0 || N < 1 || M > kMostRows || N > kMostRows || M > (int64_t(1) << 40) / N)
         return FP8MM_ERR_SHAPE;
     return M == 0 ? 0 : stats_bytes(M, N) + aligned(M * 4);
 }
@@ -244,8 +271,13 @@ int fp8_cross_entropy(const void *A, int a_type, const void *B, int b_type, cons
     if ((reinterpret_cast<uintptr_t>(loss) & 3) || (reinterpret_cast<uintptr_t>(lse) & 3) ||
         (reinterpret_cast<uintptr_t>(workspace) & 15))
         return FP8MM_ERR_ALIGN;
-    if (workspace_bytes < fp8_cross_entropy_workspace(M, N))
+    const int64_t need = fp8_cross_entropy_workspace(M, N), scales = scale_mode == FP8MM_SCALE_ROWWISE ? 4 : 0;
+    if (workspace_bytes < need)
         return FP8MM_ERR_SHAPE;
+    if (!written_apart({{loss, M * 4}, {lse, M * 4}, {workspace, need}},
+                       {{A, M * K}, {B, N * K}, {scale_a, std::max<int64_t>(4, scales * M)}, {scale_b, std::max<int64_t>(4, scales * N)},
+                        {bias, N * row_type_bytes(bias_type)}, {target, M * 8}}))
+        return FP8MM_ERR_MODE;
     int sms = 0;
     if ((rc = device_sms(&sms)) != FP8MM_OK)
         return rc;
@@ -282,7 +314,7 @@ int fp8_cross_entropy(const void *A, int a_type, const void *B, int b_type, cons
 
 int64_t fp8_cross_entropy_grad_workspace(int64_t M, int64_t N, int64_t K, int want_da, int want_db, int want_dbias)
 {
-    if (M < 0 || N < 1 || M > INT32_MAX || N > INT32_MAX || K < 16 || K % 16 != 0 || K > (int64_t(1) << 24) ||
+    if (M < 0 || N < 1 || M > kMostRows || N > kMostRows || K < 16 || K % 16 != 0 || K > (int64_t(1) << 24) ||
         cdiv(M, kTile) * cdiv(N, kTile) > (int64_t(1) << 24) || M > (int64_t(1) << 40) / N)
         return FP8MM_ERR_SHAPE;
     if (M == 0 || !(want_da || want_db || want_dbias))
@@ -316,6 +348,12 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int sms = 0;
     const int es = static_cast<int>(row_type_bytes(out_type));
+    const int64_t scales = scale_mode == FP8MM_SCALE_ROWWISE ? 4 : 0;
+    if (!written_apart({{da, M * K * es}, {db, N * K * es}, {dbias, N * 4}},
+                       {{A, M * K}, {B, N * K}, {scale_a, std::max<int64_t>(4, scales * M)}, {scale_b, std::max<int64_t>(4, scales * N)},
+                        {bias, N * row_type_bytes(bias_type)}, {target, M * 8}, {lse, M * 4}, {dloss, dloss_count * 4},
+                        {workspace, workspace_bytes}}))
+        return FP8MM_ERR_MODE;
     if (M == 0) {
         // sums over no rows
         if ((rc = device_sms(&sms)) != FP8MM_OK || (rc = zero(db, N * K * es, s)) != FP8MM_OK)

@@ -803,6 +803,10 @@ PyObject *adamw(PyObject *const *a)
         rc = api.adamw(all.data(), static_cast<int64_t>(all.size()), &o, stream());
     }
     checked(rc);
+    // (autograd: a graph that saved one of these has an older version of it)
+    for (const Sequence *s : {&params, &ms, &vs, &masters, &m_scales, &v_scales})
+        for (Py_ssize_t i = 0; i < s->n; ++i)
+            (*s)[i].unsafeGetTensorImpl()->bump_version();
     Py_RETURN_NONE;
 }
 

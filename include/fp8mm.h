@@ -511,7 +511,8 @@ int64_t fp8_layer_norm_grad_workspace(int64_t R, int64_t C);
  *   loss[m] = lse[m] - z[m, target[m]],  0 where target[m] == ignore_index
  *
  *   A, B, scale_a, scale_b, scale_mode, M, N, K   as in fp8_scaled_mm_ex, with
- *              a_type, b_type (FP8MM_TYPE_*); N >= 1.
+ *              a_type, b_type (FP8MM_TYPE_*); N >= 1, M and N under 2^31 - 1024,
+ *              at most 2^24 tiles of 256 x 256.
  *   bias       [N] of bias_type (FP8MM_OUT_BF16, _F16 or _F32), or NULL. A
  *              column whose bias is -inf (or the type's lowest value) is left
  *              out of its rows' sums.
@@ -524,7 +525,8 @@ int64_t fp8_layer_norm_grad_workspace(int64_t R, int64_t C);
  *              different streams with workspaces of their own do not interfere.
  *
  * A row whose every z is -inf has lse = -inf and a loss of NaN; a NaN or +inf
- * among a row's z makes both NaN. M == 0 is a no-op. The sums are added in an
+ * among a row's z makes both NaN. loss, lse and workspace must not overlap one
+ * another or an input (FP8MM_ERR_MODE). M == 0 is a no-op. The sums are added in an
  * order that depends on the sizes only, so results repeat.
  * Asynchronous on `stream`, two launches; bounded waits and errors as above.
  */
@@ -555,7 +557,7 @@ int64_t fp8_cross_entropy_workspace(int64_t M, int64_t N);
  *   dloss      fp32 [M], or one value for all rows (dloss_count M or 1).
  *   da, db     contiguous, of out_type (FP8MM_OUT_BF16, _F16 or _F32), 16-byte
  *              aligned; dbias fp32. Each may be NULL (not wanted). They must not
- *              overlap the inputs.
+ *              overlap one another, an input or the workspace (FP8MM_ERR_MODE).
  *   workspace  device memory of at least fp8_cross_entropy_grad_workspace(...)
  *              bytes for the outputs that are wanted, 16-byte aligned; at most
  *              about 2 GiB beside fp16 copies of A and fp32 partial sums of da.

@@ -353,6 +353,16 @@ def test_what_is_behind_a_tensor_stays():
             assert bool((a.float()[:50] == 7).all()) and bool((a.float()[1050:] == 7).all())
 
 
+def test_autograd_sees_the_update():
+    """A graph that saved a parameter refuses to go back through its updated values."""
+    s = State([256])
+    w = s.p[0].requires_grad_()
+    y = (w * w).sum()
+    s.call()
+    with pytest.raises(RuntimeError, match="modified"):
+        y.backward()
+
+
 def test_empty():
     fm.fp8_adamw([], [], [], [], 1)
     e = torch.empty(0, device="cuda")

@@ -318,6 +318,63 @@ def test_gradients_match_differences():
         assert abs(diff - float((grad.double() * d).sum())) < 3 * 2.0 ** -11 * size + 1e-6
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 33, 16), (33, 129, 48), (300, 1000, 272), (40, 20000, 80), (5000, 100, 64)])
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_what_lies_around_the_outputs_stays(M, N, K, out):
+    p = Problem(M, N, K)
+    lse = fm.fp8_cross_entropy(*p.operands, p.target)[1]
+    around = [torch.full((n + 8, K), 7.0, dtype=out, device="cuda") for n in (M, N)]
+    fm.fp8_cross_entropy_grad(*p.operands, p.target, lse, p.dloss, out_dtype=out, da=around[0][4:4 + M], db=around[1][4:4 + N])
+    want, tol = grad64(p, lse)
+    for a, n, w, t in zip(around, (M, N), want, tol):
+        assert bool((a[:4] == 7).all()) and bool((a[4 + n:] == 7).all())
+        assert_close(a[4:4 + n], w, t)
+
+
+def test_codes_that_are_nan_or_infinite():
+    p = Problem(40, 300, 64, b=E5M2, ignored=0.0)
+    p.target[3] = IGNORE
+    for code in (0x7C, 0x7E):           # infinity, NaN
+        Bt = p.Bt.clone()
+        Bt.view(torch.uint8)[17, 5] = code
+        mm = (p.A, Bt.t(), p.sa, p.sb, p.mode)
+        z = (p.A.double() @ Bt.double().t())[:, 17]
+        loss, lse = fm.fp8_cross_entropy(*mm, p.target)
+        # a column at minus infinity is left out, one at plus infinity or NaN makes the row NaN
+        assert torch.equal(lse.isnan(), z.isnan() | (z == math.inf))
+        da, db, _ = fm.fp8_cross_entropy_grad(*mm, p.target, lse, p.dloss)
+        assert bool(da[p.target != IGNORE][:, 5].isnan().all()) and bool(db.isnan().any())
+    A = p.A.clone()
+    A.view(torch.uint8)[7, 3] = 0x7F
+    mm = (A, p.B, p.sa, p.sb, p.mode)
+    loss, lse = fm.fp8_cross_entropy(*mm, p.target)
+    assert torch.equal(loss.isnan(), torch.arange(40, device="cuda") == 7) and torch.equal(lse.isnan(), loss.isnan())
+    da, db, _ = fm.fp8_cross_entropy_grad(*mm, p.target, lse, p.dloss)
+    assert torch.equal(da.isnan().any(dim=1), torch.arange(40, device="cuda") == 7) and bool(db.isnan().all())
+
+
+def test_infinite_and_nan_dloss_or_scales_show():
+    p = Problem(40, 300, 64, ignored=0.0)
+    lse = fm.fp8_cross_entropy(*p.operands, p.target)[1]
+    for bad in (math.inf, math.nan):
+        d = p.dloss.clone()
+        d[3] = bad
+        da, db, _ = fm.fp8_cross_entropy_grad(*p.operands, p.target, lse, d)
+        assert bool(da[3].isnan().all()) and bool(db.isnan().all())
+        for which in (2, 3):
+            mm = list(p.operands)
+            mm[which] = mm[which].clone()
+            mm[which][5] = bad
+            da, db, _ = fm.fp8_cross_entropy_grad(*mm, p.target, lse, p.dloss)
+            assert bool(da.isnan().any()) and bool(db.isnan().any())
+
+
+def test_large_vocabulary_and_one_row():
+    p = Problem(1, 1000003, 16, ignored=0.0)
+    check_loss(p)
+    check_grad(p)
+
+
 def test_no_rows():
     p = Problem(0, 300, 64)
     loss, lse = fm.fp8_cross_entropy(*p.operands, p.target)

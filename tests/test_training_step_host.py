@@ -26,8 +26,8 @@ def p(v):
 
 
 def loss(lib, **kw):
-    a = dict(A=AT, at=0, B=AT + 4096, bt=0, sa=AT + 64, sb=AT + 128, mode=1, bias=AT + 256, bias_t=2, t=AT + 512, ignore=-100,
-             loss=AT + 768, lse=AT + 1024, M=4, N=64, K=64, ws=AT + 8192, wb=1 << 40) | kw
+    a = dict(A=AT + (1 << 14), at=0, B=AT + (1 << 15), bt=0, sa=AT, sb=AT + 16, mode=1, bias=AT + 272, bias_t=2, t=AT + 528, ignore=-100,
+             loss=AT + 768, lse=AT + 1024, M=4, N=64, K=64, ws=AT + (1 << 20), wb=1 << 30) | kw
     return lib.fp8_cross_entropy(p(a["A"]), a["at"], p(a["B"]), a["bt"], p(a["sa"]), p(a["sb"]), a["mode"], p(a["bias"]),
                                  a["bias_t"], p(a["t"]), a["ignore"], p(a["loss"]), p(a["lse"]), a["M"], a["N"], a["K"],
                                  p(a["ws"]), a["wb"], None)
@@ -44,7 +44,9 @@ COMMON = [
 ]
 
 
-@pytest.mark.parametrize("kw,code", COMMON + [(dict(loss=None), -1), (dict(loss=AT + 2), -3), (dict(wb=4 * 4 * 8 - 1), -2)])
+@pytest.mark.parametrize("kw,code", COMMON + [(dict(loss=None), -1), (dict(loss=AT + 2), -3), (dict(loss=AT + 1024), -4),
+                                             (dict(lse=AT + 528), -4), (dict(loss=AT + (1 << 15) + 4092), -4), (dict(ws=AT), -4),
+                                             (dict(N=(1 << 31) - 1000, M=1), -2), (dict(wb=4 * 4 * 8 - 1), -2)])
 def test_loss_refusals(lib, kw, code):
     assert loss(lib, **kw) == code
 
@@ -54,9 +56,9 @@ def test_no_rows_is_a_noop(lib):
 
 
 def grad(lib, **kw):
-    a = dict(A=AT, at=0, B=AT + 4096, bt=0, sa=AT + 64, sb=AT + 128, mode=1, bias=AT + 256, bias_t=2, t=AT + 512, ignore=-100,
+    a = dict(A=AT + (1 << 14), at=0, B=AT + (1 << 15), bt=0, sa=AT, sb=AT + 16, mode=1, bias=AT + 272, bias_t=2, t=AT + 528, ignore=-100,
              lse=AT + 768, dl=AT + 1024, dn=4, da=AT + (1 << 16), db=AT + (1 << 17), ot=0, dbias=AT + (1 << 18), M=4, N=64,
-             K=64, ws=AT + 8192, wb=1 << 40) | kw
+             K=64, ws=AT + (1 << 20), wb=1 << 30) | kw
     return lib.fp8_cross_entropy_grad(p(a["A"]), a["at"], p(a["B"]), a["bt"], p(a["sa"]), p(a["sb"]), a["mode"], p(a["bias"]),
                                       a["bias_t"], p(a["t"]), a["ignore"], p(a["lse"]), p(a["dl"]), a["dn"], p(a["da"]),
                                       p(a["db"]), a["ot"], p(a["dbias"]), a["M"], a["N"], a["K"], p(a["ws"]), a["wb"], None)
@@ -65,6 +67,8 @@ def grad(lib, **kw):
 @pytest.mark.parametrize("kw,code", COMMON + [
     (dict(ot=3), -4), (dict(ot=-1), -4), (dict(dn=3), -2), (dict(dn=0), -2), (dict(dn=5), -2), (dict(dl=None), -1),
     (dict(dl=AT + 2), -3), (dict(da=AT + 8), -3), (dict(db=AT + 2), -3), (dict(dbias=AT + 2), -3),
+    (dict(db=AT + (1 << 16)), -4), (dict(da=AT + (1 << 17) + 8176), -4), (dict(db=AT + (1 << 15)), -4), (dict(dbias=AT + 768), -4),
+    (dict(dbias=AT + (1 << 17)), -4), (dict(da=AT + (1 << 20)), -4), (dict(lse=AT + (1 << 16)), -4),
 ])
 def test_grad_refusals(lib, kw, code):
     if "M" in kw:
