@@ -164,20 +164,41 @@ int product_maps(const TileChoice &t, const void *A, int a_type, const void *B, 
     return rc != FP8MM_OK ? rc : map_matrix(&m.b, u8, 1, B, N, K, K, t.width / 2);
 }
 
-// K slices of a gradient product of `kblocks` blocks of 64: the number that
-// ends first. A block takes a pair 0.28 us, a tile's end about 2; every slice
-// writes fp32 partials, which another kernel reads (at 5.5 TB/s).
-int slices(int64_t rows, int64_t cols, int64_t kblocks, int sms)
+// K slices of the gradients' products, which share one launch: tiles ta of ka blocks
+// of 64, tb of kb (0 tiles: not wanted). Chosen by when the last CTA pair ends: a block takes
+// a pair 0.28 us, a tile's end 1.5; sums of slices are written as fp32 partials and
+// read by another kernel (2 us and 5.5 TB/s). 2048 x 2048 x 512, 16 tiles each:
+// two slices each, one turn of 64 units (chosen apart: four each, two turns).
+struct Slices {
+    int a, b;
+};
+Slices choose_slices(int64_t ta, int64_t ka, int64_t out_a, int64_t tb, int64_t kb, int64_t out_b, int sms)
 {
-    const int64_t tiles = cdiv(rows, kTile) * cdiv(cols, kTile), pairs = sms / 2;
-    int best = 1;
+    constexpr int kCounts[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 19, 24, 32, 38, 48, 64};
+    const int64_t pairs = sms / 2;
+    auto unit = [](int64_t blocks, int slices) { return cdiv(blocks, slices) * 0.28 + 1.5; };
+    auto sums = [](int64_t out, int slices) { return slices > 1 ? 2.0 + static_cast<double>(out) * slices * 8 / 5.5e6 : 0.0; };
+    Slices best{1, 1};
     double least = 0.0;
-    for (int s = 1; s <= 64 && s * 4 <= std::max<int64_t>(kblocks, 4); ++s) {
-        const double t = cdiv(tiles * s, pairs) * (cdiv(kblocks, s) * 0.28 + 2.0) +
-                         (s > 1 ? 3.0 + s * rows * cols * 8 / 5.5e6 : 0.0);
-        if (s == 1 || t < least) {
-            least = t;
-            best = s;
+    for (int sa : kCounts) {
+        if (sa > 1 && (ta == 0 || sa * 4 > ka))
+            break;
+        for (int sb : kCounts) {
+            if (sb > 1 && (tb == 0 || sb * 4 > kb))
+                break;
+            // unit u goes to pair u % pairs, A's first: the pair with the most is the first
+            // one, or the first without A's odd unit
+            const int64_t ua = ta * sa, u = ua + tb * sb;
+            double t = 0.0;
+            for (int64_t p : {int64_t(0), ua % pairs}) {
+                const int64_t na = cdiv(std::max<int64_t>(ua - p, 0), pairs), n = cdiv(std::max<int64_t>(u - p, 0), pairs);
+                t = std::max(t, static_cast<double>(na) * unit(ka, sa) + static_cast<double>(n - na) * unit(kb, sb));
+            }
+            t += sums(out_a, sa) + sums(out_b, sb);
+            if ((sa == 1 && sb == 1) || t < least) {
+                least = t;
+                best = {sa, sb};
+            }
         }
     }
     return best;
@@ -199,8 +220,11 @@ GradPlan plan_grad(int64_t M, int64_t N, int64_t K, bool da, bool db, bool dbias
     g.pieces = cdiv(N, most);
     g.piece = cdiv(cdiv(N, g.pieces), kTile) * kTile;
     g.pieces = cdiv(N, g.piece);
-    g.split_a = slices(M, K, cdiv(std::min(N, g.piece), 64), sms);
-    g.split_b = slices(std::min(N, g.piece), K, cdiv(M, 64), sms);
+    const int64_t n = std::min(N, g.piece), across = cdiv(K, kTile);
+    const Slices s = choose_slices(da ? cdiv(M, kTile) * across : 0, cdiv(n, 64), M * K, db ? cdiv(n, kTile) * across : 0, cdiv(M, 64),
+                                   n * K, sms);
+    g.split_a = s.a;
+    g.split_b = s.b;
     g.parts_a = da && (g.split_a > 1 || g.pieces > 1);
     g.parts_b = db && g.split_b > 1;
     int64_t at = 0;
