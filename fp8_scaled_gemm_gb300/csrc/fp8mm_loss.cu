@@ -333,6 +333,10 @@ int fp8_cross_entropy(const void *A, int a_type, const void *B, int b_type, cons
     c.lse = lse;
     c.rows = static_cast<int>(M);
     c.parts = static_cast<int>(parts_of(t, N));
+    // (up to where the rows' CTAs are a few on every SM, and a sector's other rows are not
+    // read again too often)
+    if (M <= 4 * sms)
+        return launch_grid2(combine_row_kernel, M, 1, kRowThreads, s, "cross entropy sum launch", c);
     return launch_grid2(combine_kernel, cdiv(M, 32), 1, kCombineThreads, s, "cross entropy sum launch", c);
 }
 
