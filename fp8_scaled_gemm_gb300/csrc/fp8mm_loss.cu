@@ -11,6 +11,7 @@ using namespace fp8mm_host;
 using namespace fp8loss;
 
 constexpr int64_t kPieceBytes = int64_t(1) << 30;   // of dz, and of the piece of B in fp16
+constexpr int64_t kFewNorms = 8192;
 constexpr int64_t kMostRows = INT32_MAX - 1024;     // of A and columns of B: tiles' coordinates are int
 
 int64_t aligned(int64_t bytes) { return cdiv(bytes, 256) * 256; }
@@ -402,6 +403,9 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
     // what comes off dz W16 and dz^T H16 beside the norms
     const float factor_a = 1.0f / (kSlopeScale * code_scale(b_type)), factor_b = 1.0f / (kSlopeScale * code_scale(a_type));
 
+    // Few values' norms are found by each CTA of the first piece itself, beside its first
+    // loads: a launch less (128 x 4096 x 480 18.3 to 17.2 us).
+    const bool few = M <= kFewNorms && N <= kFewNorms && g.pieces == 1;
     NormsParams n{};
     n.dloss = dloss;
     n.dloss_step = dloss_count == 1 ? 0 : 1;
@@ -414,7 +418,7 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
     n.count[kNormB] = rowwise ? N : 1;
     n.count[kNormA] = rowwise ? M : 1;
     n.out = norms;
-    if ((rc = launch_grid2(norms_kernel, kNormParts, 3, kNormThreads, s, "cross entropy norms launch", n)) != FP8MM_OK)
+    if (!few && (rc = launch_grid2(norms_kernel, kNormParts, 3, kNormThreads, s, "cross entropy norms launch", n)) != FP8MM_OK)
         return rc;
 
     for (int64_t i = 0; i < g.pieces; ++i) {
@@ -440,6 +444,7 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
         p.colsum = dbias ? reinterpret_cast<float *>(ws + g.colsum) : nullptr;
         p.colsum_ld = g.piece;
         p.norms = norms;
+        p.norms_out = few ? norms : nullptr;
         p.w16 = da ? reinterpret_cast<__half *>(ws + g.w16) : nullptr;
         p.h16 = db && i == 0 ? reinterpret_cast<__half *>(ws + g.h16) : nullptr;
         p.K = static_cast<int>(K);

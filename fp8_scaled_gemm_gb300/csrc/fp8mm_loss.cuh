@@ -80,7 +80,8 @@ struct Cfg {
     static constexpr int kCols = kTile / 4;
     static constexpr int kColBytes = kEpiWarps * kCols * kColFloats * 4;
     static constexpr int kPowerBytes = KIND == kSlope ? kConvertWarps * 32 * 4 : 0;   // see load_powers
-    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + kColBytes + kPowerBytes + 256;
+    static constexpr int kNormBytes = KIND == kSlope ? 3 * 64 : 0;                    // see shared_norm
+    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + kColBytes + kPowerBytes + kNormBytes + 256;
     static_assert(kSmemBytes <= 232448, "exceeds 227 KB of shared memory");
 };
 
@@ -136,6 +137,7 @@ struct LossParams {
     int dloss_step;                    // 0: one value for all rows
     float *colsum;                     // [ceil(M / 32)][n], or nullptr
     long long colsum_ld;
+    uint32_t *norms_out;               // not nullptr: few values, of which this kernel finds the norms itself
     __half *w16, *h16;                 // [n, K] and [M, K], or nullptr: not wanted
     int K, a_type, b_type;
     // kGrad
@@ -185,13 +187,38 @@ static __global__ void __launch_bounds__(kNormThreads) norms_kernel(const NormsP
     }
 }
 
+__device__ __forceinline__ float norm_power(uint32_t most);
+
 // The power of two at or below the largest magnitude (at least 2^-100, so that
 // its reciprocal is finite; infinite for an infinity or NaN, whose results are
 // then NaN). Every lane of a warp calls it.
 __device__ __forceinline__ float norm_scale(const uint32_t *norms, int which)
 {
     const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __ldcg(norms + which * kNormParts + (threadIdx.x & 31)));
-    return fmaxf(__uint_as_float(m & 0x7F800000u), 0x1p-100f);
+    return norm_power(m);
+}
+
+// The power of two of a largest magnitude's bits (see norm_scale).
+__device__ __forceinline__ float norm_power(uint32_t most) { return fmaxf(__uint_as_float(most & 0x7F800000u), 0x1p-100f); }
+
+// The largest of the magnitudes (as bits) over `threads` threads of a CTA that call
+// it, on a hardware barrier of theirs: values i = thread, thread + threads, ... of
+// src, without those of rows to be ignored. `shared`: a word for each of their warps.
+template <int THREADS>
+__device__ __forceinline__ uint32_t shared_norm(const float *src, int count, const int64_t *target, long long ignore, int thread,
+                                                uint32_t *shared, int barrier)
+{
+    uint32_t most = 0;
+#pragma unroll 4
+    for (int i = thread; i < count; i += THREADS) {
+        const uint32_t v = __float_as_uint(__ldg(src + i)) & 0x7FFFFFFFu;
+        most = max(most, target && __ldg(target + i) == ignore ? 0u : v);
+    }
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    if ((thread & 31) == 0)
+        shared[thread >> 5] = most;
+    asm volatile("bar.sync %0, %1;" ::"r"(barrier), "n"(THREADS) : "memory");
+    return __reduce_max_sync(0xFFFFFFFFu, (thread & 31) < THREADS / 32 ? shared[thread & 31] : 0u);
 }
 
 // dz' / G is in (-8, 8): below fp16's 65504.
@@ -489,7 +516,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
     uint8_t *smem = smem_raw + pad;
     const uint32_t sbase = raw + pad;
     constexpr int kStagingAt = S * C::kStageBytes, kColsAt = kStagingAt + C::kStagingBytes;
-    constexpr int kPowersAt = kColsAt + C::kColBytes, kBarsAt = kPowersAt + C::kPowerBytes;
+    constexpr int kPowersAt = kColsAt + C::kColBytes, kNormsAt = kPowersAt + C::kPowerBytes;
+    constexpr int kBarsAt = kNormsAt + C::kNormBytes;
+    uint32_t *shared_norms = reinterpret_cast<uint32_t *>(smem + kNormsAt);
     const uint32_t bar0 = sbase + kBarsAt;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
@@ -680,8 +709,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
         // for the two against 150.) The last warp that has its codes gives the stage back;
         // taken[s] is 0 again before the stage can come round.
         const int cw = warp - 2 - kEpiWarps;
-        const float fa = p.h16 ? code_scale(p.a_type) / norm_scale(p.norms, kNormA) : 0.0f;
-        const float fb = p.w16 ? code_scale(p.b_type) / norm_scale(p.norms, kNormB) : 0.0f;
+        float norm_a, norm_b;
+        if (p.norms_out) {
+            const int thread = cw * 32 + lane;
+            const uint32_t a = shared_norm<32 * kConvertWarps>(p.scale_a, p.rowwise ? p.M : 1, nullptr, 0, thread, shared_norms, 1);
+            const uint32_t b =
+                shared_norm<32 * kConvertWarps>(p.scale_b, p.rowwise ? p.N : 1, nullptr, 0, thread, shared_norms + 16, 1);
+            if (blockIdx.x == 0 && cw == 0) {
+                p.norms_out[kNormA * kNormParts + lane] = a;
+                p.norms_out[kNormB * kNormParts + lane] = b;
+            }
+            norm_a = norm_power(a);
+            norm_b = norm_power(b);
+        } else {
+            norm_a = norm_scale(p.norms, kNormA);
+            norm_b = norm_scale(p.norms, kNormB);
+        }
+        const float fa = code_scale(p.a_type) / norm_a, fb = code_scale(p.b_type) / norm_b;
         const TileSpace &t = p.t[0];
         uint32_t *powers = reinterpret_cast<uint32_t *>(smem + kPowersAt) + cw * 32;
         int stage = 0;
@@ -750,8 +794,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
         int acc = 0;
         uint32_t acc_phase = 0;
         float slope_scale = 1.0f, out_scale[2] = {1.0f, 1.0f};
-        if constexpr (KIND == kSlope)
-            slope_scale = kSlopeScale / norm_scale(p.norms, kNormG);
+        if constexpr (KIND == kSlope) {
+            if (p.norms_out) {
+                const uint32_t g = shared_norm<32 * kEpiWarps>(p.dloss, p.dloss_step ? p.M : 1, p.dloss_step ? p.target : nullptr,
+                                                               p.ignore, ew * 32 + lane, shared_norms + 32, 2);
+                if (blockIdx.x == 0 && ew == 0)
+                    p.norms_out[kNormG * kNormParts + lane] = g;
+                slope_scale = kSlopeScale / norm_power(g);
+            } else {
+                slope_scale = kSlopeScale / norm_scale(p.norms, kNormG);
+            }
+        }
         if constexpr (KIND == kGrad) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
