@@ -91,7 +91,7 @@ extern "C" int fp8_adamw(const fp8mm_adamw_tensor *tensors, int64_t n, const fp8
     const int64_t state_bytes = o.state_bits / 8;
     std::vector<Stretch> all;
     try {
-        all.reserve(static_cast<size_t>(n) * 7);
+        all.reserve(static_cast<size_t>(n) * 7 + 3);
     } catch (const std::bad_alloc &) {
         set_error("fp8_adamw: no host memory for the check of the tensors");
         return FP8MM_ERR_CUDA;
@@ -127,6 +127,12 @@ extern "C" int fp8_adamw(const fp8mm_adamw_tensor *tensors, int64_t n, const fp8
             note(t.exp_avg_sq_scale, cdiv(t.count, kBlock) * 4, true);
         }
     }
+    if (all.empty())
+        return FP8MM_OK;
+    // (read when the CTAs begin, some after others have written)
+    note(o.lr_device, 4, false);
+    note(o.step_device, 8, false);
+    note(o.grad_scale, 4, false);
     // what is written belongs to one tensor: a tensor given twice would be updated
     // by two warps at once
     std::sort(all.begin(), all.end(), [](const Stretch &a, const Stretch &b) { return a.from < b.from; });
@@ -140,8 +146,6 @@ extern "C" int fp8_adamw(const fp8mm_adamw_tensor *tensors, int64_t n, const fp8
         if (s.written)
             written_end = std::max(written_end, s.to);
     }
-    if (all.empty())
-        return FP8MM_OK;
     int sms = 0;
     int rc = device_sms(&sms);
     if (rc != FP8MM_OK)

@@ -12,6 +12,7 @@ using namespace fp8loss;
 
 constexpr int64_t kPieceBytes = int64_t(1) << 30;   // of dz, and of the piece of B in fp16
 constexpr int64_t kFewNorms = 8192;
+constexpr int kLeastWidth = 128;                    // of a tile
 constexpr int64_t kMostRows = INT32_MAX - 1024;     // of A and columns of B: tiles' coordinates are int
 
 int64_t aligned(int64_t bytes) { return cdiv(bytes, 256) * 256; }
@@ -125,32 +126,46 @@ struct TileChoice {
     int width, run;
 };
 
+// With many tiles a CTA pair takes several neighbours, over which a row's maximum and
+// sum stay in registers: 16 units for each of 76 pairs keep the last turn short. (Not
+// of the device's SMs, so that the workspace's size does not depend on them.)
+int choose_run(int64_t M, int64_t N, int width)
+{
+    const int64_t tiles = cdiv(M, kTile) * cdiv(N, width);
+    int run = 1;
+    while (run < 8 && tiles / (2 * run) >= 16 * 76)
+        run *= 2;
+    return run;
+}
+
 // The width that ends first, by what a CTA pair loads for its tiles in turn: its
 // rows of A (up to 256) and its columns of B (one row of 32000 columns: two turns of
 // 224 columns for 256).
-// With many tiles a pair takes several neighbours, over which a row's maximum and
-// sum stay in registers: 16 units a pair keep the last turn short.
 TileChoice choose_tiles(int64_t M, int64_t N, int sms)
 {
     const int64_t pairs = sms / 2, rows = cdiv(cdiv(M, cdiv(M, kTile)), 64) * 64;
     TileChoice best{kTile, 1};
     int64_t cost = INT64_MAX;
-    for (int width = kTile; width >= 128; width -= 32) {
+    for (int width = kTile; width >= kLeastWidth; width -= 32) {
         const int64_t c = cdiv(cdiv(M, kTile) * cdiv(N, width), pairs) * (rows + width);
         if (c < cost) {
             cost = c;
             best.width = width;
         }
     }
-    const int64_t tiles = cdiv(M, kTile) * cdiv(N, best.width);
-    while (best.run < 8 && tiles / (2 * best.run) >= 16 * pairs)
-        best.run *= 2;
+    best.run = choose_run(M, N, best.width);
     return best;
 }
 
 // Parts of a row that kStats leaves, and the most there can be.
 int64_t parts_of(const TileChoice &t, int64_t N) { return cdiv(cdiv(N, t.width), t.run) * 4; }
-int64_t most_parts(int64_t N) { return cdiv(N, 128) * 4; }
+int64_t most_parts(int64_t M, int64_t N)
+{
+    int64_t most = 0;
+    for (int width = kLeastWidth; width <= kTile; width += 32)
+        most = std::max(most, parts_of({width, choose_run(M, N, width)}, N));
+    return most;
+}
 
 // The operands' maps and the tile space of z [M, N] (kStats, kSlope).
 int product_maps(const TileChoice &t, const void *A, int a_type, const void *B, int b_type, int64_t M, int64_t N, int64_t K,
@@ -245,7 +260,7 @@ GradPlan plan_grad(int64_t M, int64_t N, int64_t K, bool da, bool db, bool dbias
     return g;
 }
 
-int64_t stats_bytes(int64_t M, int64_t N) { return aligned(most_parts(N) * M * 8); }
+int64_t stats_bytes(int64_t M, int64_t N) { return aligned(most_parts(M, N) * M * 8); }
 
 int zero(void *p, int64_t bytes, cudaStream_t s)
 {
@@ -378,10 +393,11 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
     int sms = 0;
     const int es = static_cast<int>(row_type_bytes(out_type));
     const int64_t scales = scale_mode == FP8MM_SCALE_ROWWISE ? 4 : 0;
-    if (!written_apart({{da, M * K * es}, {db, N * K * es}, {dbias, N * 4}},
-                       {{A, M * K}, {B, N * K}, {scale_a, std::max<int64_t>(4, scales * M)}, {scale_b, std::max<int64_t>(4, scales * N)},
-                        {bias, N * row_type_bytes(bias_type)}, {target, M * 8}, {lse, M * 4}, {dloss, dloss_count * 4},
-                        {workspace, workspace_bytes}}))
+    const std::initializer_list<Stretch> inputs = {
+        {A, M * K}, {B, N * K}, {scale_a, std::max<int64_t>(4, scales * M)}, {scale_b, std::max<int64_t>(4, scales * N)},
+        {bias, N * row_type_bytes(bias_type)}, {target, M * 8}, {lse, M * 4}, {dloss, dloss_count * 4}};
+    const std::initializer_list<Stretch> outputs = {{da, M * K * es}, {db, N * K * es}, {dbias, N * 4}};
+    if (!written_apart(outputs, inputs) || !written_apart(outputs, {{workspace, workspace_bytes}}))
         return FP8MM_ERR_MODE;
     if (M == 0) {
         // sums over no rows
@@ -396,6 +412,8 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
     const GradPlan g = plan_grad(M, N, K, da != nullptr, db != nullptr, dbias != nullptr, sms);
     if (workspace_bytes < g.bytes)
         return FP8MM_ERR_SHAPE;
+    if (!written_apart({{workspace, g.bytes}}, inputs))
+        return FP8MM_ERR_MODE;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     uint32_t *norms = reinterpret_cast<uint32_t *>(ws + g.norms);
     const int rowwise = scale_mode == FP8MM_SCALE_ROWWISE;
@@ -409,12 +427,12 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
     NormsParams n{};
     n.dloss = dloss;
     n.dloss_step = dloss_count == 1 ? 0 : 1;
+    n.rowwise = rowwise;
     n.scale_b = scale_b;
     n.scale_a = scale_a;
     n.target = target;
     n.ignore = ignore_index;
-    n.M = M;
-    n.count[kNormG] = dloss_count;
+    n.count[kNormG] = M;
     n.count[kNormB] = rowwise ? N : 1;
     n.count[kNormA] = rowwise ? M : 1;
     n.out = norms;

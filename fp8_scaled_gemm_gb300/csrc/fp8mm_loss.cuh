@@ -145,7 +145,7 @@ struct LossParams {
 };
 
 // ------------------------------------------------------------------ norms ---
-// Largest magnitudes of g (rows that have a target), s_b and s_a, as bit
+// Largest magnitudes of g, s_b and s_a (without rows to be ignored), as bit
 // patterns (which order like the magnitudes, NaN above everything), in
 // kNormParts partial maxima each.
 
@@ -155,9 +155,8 @@ struct NormsParams {
     const float *dloss, *scale_b, *scale_a;
     const int64_t *target;
     long long ignore;
-    long long M;                       // rows of target
     long long count[3];
-    int dloss_step;
+    int dloss_step, rowwise;
     uint32_t *out;                     // [3][kNormParts]
 };
 
@@ -170,11 +169,13 @@ static __global__ void __launch_bounds__(kNormThreads) norms_kernel(const NormsP
     ptx::grid_dependency_wait();
     const int which = blockIdx.y;
     const float *src = which == kNormG ? p.dloss : which == kNormB ? p.scale_b : p.scale_a;
+    const bool by_row = which == kNormG || (which == kNormA && p.rowwise);
+    const int step = which == kNormG ? p.dloss_step : 1;
     uint32_t most = 0;
     for (long long i = blockIdx.x * kNormThreads + threadIdx.x; i < p.count[which]; i += kNormThreads * kNormParts) {
-        if (which == kNormG && p.dloss_step && __ldg(p.target + i) == p.ignore)
+        if (by_row && __ldg(p.target + i) == p.ignore)
             continue;
-        most = max(most, __float_as_uint(__ldg(src + i)) & 0x7FFFFFFFu);
+        most = max(most, __float_as_uint(__ldg(src + i * step)) & 0x7FFFFFFFu);
     }
     most = __reduce_max_sync(0xFFFFFFFFu, most);
     if ((threadIdx.x & 31) == 0)
@@ -202,16 +203,16 @@ __device__ __forceinline__ float norm_scale(const uint32_t *norms, int which)
 __device__ __forceinline__ float norm_power(uint32_t most) { return fmaxf(__uint_as_float(most & 0x7F800000u), 0x1p-100f); }
 
 // The largest of the magnitudes (as bits) over `threads` threads of a CTA that call
-// it, on a hardware barrier of theirs: values i = thread, thread + threads, ... of
-// src, without those of rows to be ignored. `shared`: a word for each of their warps.
+// it, on a hardware barrier of theirs: values i = thread, thread + threads, ..., `step`
+// apart in src, without those of rows to be ignored. `shared`: a word for each of their warps.
 template <int THREADS>
-__device__ __forceinline__ uint32_t shared_norm(const float *src, int count, const int64_t *target, long long ignore, int thread,
+__device__ __forceinline__ uint32_t shared_norm(const float *src, int step, int count, const int64_t *target, long long ignore, int thread,
                                                 uint32_t *shared, int barrier)
 {
     uint32_t most = 0;
 #pragma unroll 4
     for (int i = thread; i < count; i += THREADS) {
-        const uint32_t v = __float_as_uint(__ldg(src + i)) & 0x7FFFFFFFu;
+        const uint32_t v = __float_as_uint(__ldg(src + i * step)) & 0x7FFFFFFFu;
         most = max(most, target && __ldg(target + i) == ignore ? 0u : v);
     }
     most = __reduce_max_sync(0xFFFFFFFFu, most);
@@ -337,15 +338,17 @@ struct Converted {
 // into registers, which gives the stage back early, then converts and writes them.
 //
 // `powers` holds 2^e(scale) f / S of the warp's rows as two fp16 (below 2^-24: 0), row
-// 16 i + 2 warp + j at 2 i + j.
+// 16 i + 2 warp + j at 2 i + j; kNoRow for a row to be ignored, whose codes may be NaN.
+constexpr uint32_t kNoRow = 0x80008000u;
+
 __device__ __forceinline__ void load_powers(uint32_t *powers, int row0, int rows, const float *scale, int rowwise, float f,
-                                            int warp, int lane)
+                                            const int64_t *target, long long ignore, int warp, int lane)
 {
     if (lane >= 16)
         return;
     const int row = row0 + (lane >> 1) * 16 + 2 * warp + (lane & 1);
     const __half2 s = __float2half2_rn(row < rows ? power(__ldg(scale + (rowwise ? row : 0))) * f : 0.0f);
-    powers[lane] = *reinterpret_cast<const uint32_t *>(&s);
+    powers[lane] = target && row < rows && __ldg(target + row) == ignore ? kNoRow : *reinterpret_cast<const uint32_t *>(&s);
 }
 
 __device__ __forceinline__ void take_rows(uint2 (&codes)[8], const uint8_t *stage, int warp, int lane)
@@ -357,7 +360,7 @@ __device__ __forceinline__ void take_rows(uint2 (&codes)[8], const uint8_t *stag
         codes[i] = *reinterpret_cast<const uint2 *>(from + i * 2048);
 }
 
-template <bool E4M3>
+template <bool E4M3, bool ROWS>
 __device__ __forceinline__ void write_rows(const uint2 (&codes)[8], int count, __half *out, int row0, int rows, int k0, int K,
                                            const uint32_t *powers, int warp, int lane)
 {
@@ -379,7 +382,7 @@ __device__ __forceinline__ void write_rows(const uint2 (&codes)[8], int count, _
             else
                 asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(o[h]) : "h"(two));
             const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&o[h]), *reinterpret_cast<const __half2 *>(&s));
-            o[h] = *reinterpret_cast<const uint32_t *>(&v);
+            o[h] = ROWS && s == kNoRow ? 0u : *reinterpret_cast<const uint32_t *>(&v);
         }
         __stcg(reinterpret_cast<uint4 *>(to + static_cast<long long>(16 * i) * K), make_uint4(o[0], o[1], o[2], o[3]));
     }
@@ -712,9 +715,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
         float norm_a, norm_b;
         if (p.norms_out) {
             const int thread = cw * 32 + lane;
-            const uint32_t a = shared_norm<32 * kConvertWarps>(p.scale_a, p.rowwise ? p.M : 1, nullptr, 0, thread, shared_norms, 1);
+            const uint32_t a = shared_norm<32 * kConvertWarps>(p.scale_a, 1, p.rowwise ? p.M : 1, p.rowwise ? p.target : nullptr,
+                                                                p.ignore, thread, shared_norms, 1);
             const uint32_t b =
-                shared_norm<32 * kConvertWarps>(p.scale_b, p.rowwise ? p.N : 1, nullptr, 0, thread, shared_norms + 16, 1);
+                shared_norm<32 * kConvertWarps>(p.scale_b, 1, p.rowwise ? p.N : 1, nullptr, 0, thread, shared_norms + 16, 1);
             if (blockIdx.x == 0 && cw == 0) {
                 p.norms_out[kNormA * kNormParts + lane] = a;
                 p.norms_out[kNormB * kNormParts + lane] = b;
@@ -738,9 +742,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
             const int col = w.tq * t.width + static_cast<int>(rank) * (t.width / 2);
             __syncwarp();
             if (p.h16)
-                load_powers(powers, row, p.M, p.scale_a, p.rowwise, fa, cw, lane);
+                load_powers(powers, row, p.M, p.scale_a, p.rowwise, fa, p.target, p.ignore, cw, lane);
             if (p.w16)
-                load_powers(powers + 16, col, p.N, p.scale_b, p.rowwise, fb, cw, lane);
+                load_powers(powers + 16, col, p.N, p.scale_b, p.rowwise, fb, nullptr, 0, cw, lane);
             __syncwarp();
             Converted next(p, w);
             for (int kb = w.kb0; kb < w.kb1; ++kb) {
@@ -761,21 +765,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                 if (next.of_b)
                     take_rows(b, at + C::kABytes, cw, lane);
                 __syncwarp();
-                if (lane == 0 && atomicAdd(taken + s, 1) == kConvertWarps - 1) {
+                // (the others' reads before the last one's arrival)
+                if (lane == 0 && ptx::shared_inc_acq_rel(ptx::smem_addr(taken + s)) == kConvertWarps - 1) {
                     taken[s] = 0;
                     ptx::mbar_arrive(empty_bar(s));
                 }
                 if (next.of_a) {
                     if (p.a_type == 0)
-                        write_rows<true>(a, t.half, p.h16, row, p.M, kb * 128, p.K, powers, cw, lane);
+                        write_rows<true, true>(a, t.half, p.h16, row, p.M, kb * 128, p.K, powers, cw, lane);
                     else
-                        write_rows<false>(a, t.half, p.h16, row, p.M, kb * 128, p.K, powers, cw, lane);
+                        write_rows<false, true>(a, t.half, p.h16, row, p.M, kb * 128, p.K, powers, cw, lane);
                 }
                 if (next.of_b) {
                     if (p.b_type == 0)
-                        write_rows<true>(b, t.width / 2, p.w16, col, p.N, kb * 128, p.K, powers + 16, cw, lane);
+                        write_rows<true, false>(b, t.width / 2, p.w16, col, p.N, kb * 128, p.K, powers + 16, cw, lane);
                     else
-                        write_rows<false>(b, t.width / 2, p.w16, col, p.N, kb * 128, p.K, powers + 16, cw, lane);
+                        write_rows<false, false>(b, t.width / 2, p.w16, col, p.N, kb * 128, p.K, powers + 16, cw, lane);
                 }
             }
         }
@@ -796,8 +801,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
         float slope_scale = 1.0f, out_scale[2] = {1.0f, 1.0f};
         if constexpr (KIND == kSlope) {
             if (p.norms_out) {
-                const uint32_t g = shared_norm<32 * kEpiWarps>(p.dloss, p.dloss_step ? p.M : 1, p.dloss_step ? p.target : nullptr,
-                                                               p.ignore, ew * 32 + lane, shared_norms + 32, 2);
+                const uint32_t g = shared_norm<32 * kEpiWarps>(p.dloss, p.dloss_step, p.M, p.target, p.ignore, ew * 32 + lane, shared_norms + 32, 2);
                 if (blockIdx.x == 0 && ew == 0)
                     p.norms_out[kNormG * kNormParts + lane] = g;
                 slope_scale = kSlopeScale / norm_power(g);

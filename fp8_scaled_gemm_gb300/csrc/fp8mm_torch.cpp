@@ -693,7 +693,8 @@ PyObject *cross_entropy_grad(PyObject *const *a)
 
 // ------------------------------------------------------------------ AdamW ---
 
-// A list or tuple of tensors as such.
+// Tensors in a list or tuple, held as they are now: another thread may change a list
+// while the call runs without the interpreter's lock.
 struct Sequence {
     PyObject *seq = nullptr;
     Py_ssize_t n = 0;
@@ -703,15 +704,15 @@ struct Sequence {
     {
         if (o == Py_None)
             return;
-        seq = PySequence_Fast(o, "the tensors must be given in lists");
+        seq = PySequence_Tuple(o);
         if (!seq)
             throw Raised{};
-        n = PySequence_Fast_GET_SIZE(seq);
+        n = PyTuple_GET_SIZE(seq);
     }
     Sequence(const Sequence &) = delete;
     ~Sequence() { Py_XDECREF(seq); }
     explicit operator bool() const { return seq != nullptr; }
-    const Tensor &operator[](Py_ssize_t i) const { return *tensor(name, PySequence_Fast_GET_ITEM(seq, i)); }
+    const Tensor &operator[](Py_ssize_t i) const { return *tensor(name, PyTuple_GET_ITEM(seq, i)); }
 };
 
 // Element i of a sequence beside parameter p: contiguous, of p's device and as
@@ -772,6 +773,12 @@ PyObject *adamw(PyObject *const *a)
             t.exp_avg_sq_scale = static_cast<float *>(beside_param(v_scales, i, p, ScalarType::Float, blocks));
         }
     }
+    // autograd is told of the change afterwards, which an inference tensor has no place for
+    if (!c10::InferenceMode::is_enabled())
+        for (const Sequence *s : {&params, &ms, &vs, &masters, &m_scales, &v_scales})
+            for (Py_ssize_t i = 0; i < s->n; ++i)
+                if ((*s)[i].is_inference())
+                    refuse("%s[%zd] is an inference tensor, which is updated inside InferenceMode only", s->name, i);
     // (a tensor: read by the kernel when it runs)
     auto device_value = [&](const char *name, PyObject *object, ScalarType of) -> const void * {
         if (!THPVariable_Check(object))

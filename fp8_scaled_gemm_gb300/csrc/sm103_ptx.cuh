@@ -285,6 +285,15 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
                  : "memory");
 }
 
+// Adds 1 to a word of this CTA's shared memory, gives what it was; orders the memory
+// accesses of the threads that do so.
+__device__ __forceinline__ uint32_t shared_inc_acq_rel(uint32_t smem_byte_addr)
+{
+    uint32_t was;
+    asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(was) : "r"(smem_byte_addr) : "memory");
+    return was;
+}
+
 // The same without releasing earlier memory accesses: for handing tensor memory
 // back, after tcgen05.wait and tc_fence_before(), where the wait for this thread's
 // global stores that a release at cluster scope takes is of no use.

@@ -548,10 +548,12 @@ int64_t fp8_cross_entropy_workspace(int64_t M, int64_t N);
  *   dbias    = sum over m of dz             fp32 [N]
  *
  * z is computed again in pieces of the vocabulary, of which dz is kept as fp16,
- * scaled: one rounding of at most 2^-11 relative, and what is under 2^-37 of the
- * largest |dloss| is lost. Its products run on 16-bit tensor cores with fp32 sums;
- * their other operand, codes times powers of two, is exact (down to 2^-31 of
- * its largest value, e5m2: 2^-39). dbias is the sum of the unrounded dz.
+ * scaled: one rounding of at most 2^-11 relative or 2^-37 of the largest |dloss|.
+ * Its products run on 16-bit tensor cores with fp32 sums; their other operand,
+ * codes times powers of two, is exact but for values under 2^-36 of the largest
+ * that its codes and scales can have. Rows of A (for db) and columns of B (for
+ * da) whose scale is under 2^-31 of the largest one's (e5m2: 2^-24), or under
+ * 2^-126, count as zeros. dbias is the sum of the unrounded dz.
  *
  *   lse        what fp8_cross_entropy returned for the same operands.
  *   dloss      fp32 [M], or one value for all rows (dloss_count M or 1).
@@ -559,13 +561,15 @@ int64_t fp8_cross_entropy_workspace(int64_t M, int64_t N);
  *              aligned; dbias fp32. Each may be NULL (not wanted). They must not
  *              overlap one another, an input or the workspace (FP8MM_ERR_MODE).
  *   workspace  device memory of at least fp8_cross_entropy_grad_workspace(...)
- *              bytes for the outputs that are wanted, 16-byte aligned; at most
- *              about 2 GiB beside fp16 copies of A and fp32 partial sums of da.
+ *              bytes for the outputs that are wanted, 16-byte aligned, apart from
+ *              the inputs; about 2 GiB at most (M and K up to 2^21) beside an fp16
+ *              copy of A and fp32 partial sums of da.
  *   others     as in fp8_cross_entropy.
  *
- * Rows with target == ignore_index add nothing, whatever their lse and dloss; a
+ * Rows with target == ignore_index add nothing, whatever their codes, scale, lse
+ * and dloss (the rows behind a batch's last one may hold anything); a
  * target that is neither a column nor ignore_index makes the gradients NaN. An
- * infinite or NaN dloss or scale makes the products NaN. M == 0 gives db and
+ * infinite or NaN dloss or scale of another row makes the products NaN. M == 0 gives db and
  * dbias of zeros. Sums in an order that depends on the sizes, on which outputs
  * are wanted and on the SM count only, so results repeat.
  */
@@ -610,7 +614,8 @@ typedef struct fp8mm_adamw_options {
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
  *   w = w (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  *
- * in fp32, each operation rounded by itself. w is the master where there is one
+ * in fp32, each operation rounded by itself (the quotient of an |m| under 2^-90 may
+ * miss its last bit). w is the master where there is one
  * (param receives its rounding), else param. All tensors have a master or none has.
  *
  * States in 8 bits are e4m3 codes with an fp32 scale per block of 256 elements
@@ -626,7 +631,7 @@ typedef struct fp8mm_adamw_options {
  *
  * Tensors may have any alignment of their elements; 16-byte aligned ones (8 for
  * codes) run fastest. Memory that is written must not be given twice nor
- * overlap a gradient: FP8MM_ERR_MODE. beta1, beta2 in [0, 1), eps >= 0, t >= 1,
+ * overlap a gradient, lr_device, step_device or grad_scale: FP8MM_ERR_MODE. beta1, beta2 in [0, 1), eps >= 0, t >= 1,
  * else FP8MM_ERR_SHAPE. Asynchronous on `stream`, one launch for each 400
  * tensors; the arrays are read before the call returns.
  */

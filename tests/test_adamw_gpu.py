@@ -409,3 +409,24 @@ def test_refusals():
     shared = State([300, 300])
     shared.g[1] = shared.g[0]
     check(shared)
+
+
+def test_inference_tensors():
+    """They are refused before anything is written, and updated inside InferenceMode."""
+    with torch.inference_mode():
+        s = State([300])
+    old = s.copy()
+    with pytest.raises(ValueError, match="inference"):
+        s.call()
+    assert s.same(old)
+    with torch.inference_mode():
+        s.call()
+    old.call()
+    assert s.same(old)
+
+
+def test_tensors_in_any_sequence():
+    a, b = State([300, 5]), State([300, 5])
+    a.call()
+    fm.fp8_adamw(tuple(b.p), (g for g in b.g), tuple(b.m), iter(b.v), 7, **HYPER)
+    assert a.same(b)

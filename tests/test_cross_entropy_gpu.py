@@ -124,8 +124,10 @@ def test_every_row_ignored():
     loss, lse = fm.fp8_cross_entropy(*p.operands, p.target)
     assert not bool(loss.any())
     lse[3], p.dloss[4], p.dloss[5] = math.nan, math.inf, math.nan
-    for r in fm.fp8_cross_entropy_grad(*p.operands, p.target, lse, p.dloss, return_dbias=True):
-        assert not bool(r.any())
+    # (the last one: of a mean over no rows)
+    for dloss in (p.dloss, p.dloss[5:6], p.dloss[5].expand(50)):
+        for r in fm.fp8_cross_entropy_grad(*p.operands, p.target, lse, dloss, return_dbias=True):
+            assert not bool(r.any())
 
 
 def test_target_out_of_range():
@@ -351,6 +353,38 @@ def test_codes_that_are_nan_or_infinite():
     assert torch.equal(loss.isnan(), torch.arange(40, device="cuda") == 7) and torch.equal(lse.isnan(), loss.isnan())
     da, db, _ = fm.fp8_cross_entropy_grad(*mm, p.target, lse, p.dloss)
     assert torch.equal(da.isnan().any(dim=1), torch.arange(40, device="cuda") == 7) and bool(db.isnan().all())
+
+
+@pytest.mark.parametrize("M,N,K,a", [(90, 300, 64, E4M3), (300, 9000, 272, E5M2), (1, 40, 16, E4M3), (9000, 70, 48, E4M3)])
+@pytest.mark.parametrize("rowwise", [False, True])
+def test_ignored_rows_may_hold_anything(M, N, K, a, rowwise):
+    """NaN codes, scales, lse and dloss in the rows behind a batch's last one and between others."""
+    p = Problem(M, N, K, a=a, bias=F32, rowwise=rowwise)
+    p.target[M - M // 3 - 1:] = IGNORE
+    want = check_grad(p)
+    off = p.target == IGNORE
+    p.A.view(torch.uint8)[off] = 0x7F
+    if rowwise:
+        p.sa[off] = torch.where(torch.arange(M, device="cuda")[off] % 2 == 0, math.nan, math.inf)
+    p.dloss[off] = math.nan
+    loss, lse = fm.fp8_cross_entropy(*p.operands, p.target, bias=p.bias)
+    assert not bool(loss[off].any()) and bool(lse[off].isnan().all())
+    got = fm.fp8_cross_entropy_grad(*p.operands, p.target, lse, p.dloss, bias=p.bias, return_db=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and not bool(got[0][off].any())
+
+
+def test_a_workspace_in_an_input_is_refused():
+    p = Problem(40, 300, 64, bias=F32)
+    lse = fm.fp8_cross_entropy(*p.operands, p.target, bias=p.bias)[1]
+    da, lib = torch.empty(40, 64, dtype=BF16, device="cuda"), fm.load()
+    need = lib.fp8_cross_entropy_grad_workspace(40, 300, 64, 1, 0, 0)
+    memory = torch.zeros(need + 4096, dtype=torch.uint8, device="cuda")
+    for at in (0, need - 256):
+        A = memory[at:at + 40 * 64].view(E4M3)
+        rc = lib.fp8_cross_entropy_grad(A.data_ptr(), 0, p.Bt.data_ptr(), 0, p.sa.data_ptr(), p.sb.data_ptr(), p.mode,
+                                        p.bias.data_ptr(), 2, p.target.data_ptr(), IGNORE, lse.data_ptr(), p.dloss.data_ptr(),
+                                        40, da.data_ptr(), None, 0, None, 40, 300, 64, memory.data_ptr(), need, None)
+        assert rc == -4
 
 
 def test_infinite_and_nan_dloss_or_scales_show():

@@ -84,9 +84,9 @@ def test_workspace_sizes(lib):
     assert lib.fp8_cross_entropy_workspace(0, 10) == 0
     assert lib.fp8_cross_entropy_workspace(1, 0) == -2 and lib.fp8_cross_entropy_workspace(-1, 5) == -2
     assert lib.fp8_cross_entropy_workspace(1 << 20, 1 << 21) == -2
-    # 8 bytes for each row and 32 columns, 4 for each row
-    for M, N in ((1, 1), (7, 1000), (8192, 131072)):
-        need = -(-N // 128) * M * 32 + M * 4
+    # 8 bytes for each row and 32 columns (of many tiles: 256 columns), 4 for each row
+    for M, N, columns in ((1, 1, 32), (7, 1000, 32), (8192, 131072, 256)):
+        need = -(-N // (4 * columns)) * M * 32 + M * 4
         assert need <= lib.fp8_cross_entropy_workspace(M, N) < need + 512
     assert lib.fp8_cross_entropy_grad_workspace(0, 10, 16, 1, 1, 1) == 0
     assert lib.fp8_cross_entropy_grad_workspace(5, 10, 16, 0, 0, 0) == 0
@@ -139,6 +139,12 @@ def test_adamw_refuses_tensors_together(lib):
     eight = dict(exp_avg_scale=AT + (4 << 12), exp_avg_sq_scale=AT + (5 << 12))
     assert adamw(lib, [tensor(**{**eight, "exp_avg_sq_scale": AT + (4 << 12)})], state_bits=8) == -4
     assert adamw(lib, [tensor(**{**eight, "exp_avg_scale": AT + 2})], state_bits=8) == -3
+
+
+@pytest.mark.parametrize("what", ["lr_device", "step_device", "grad_scale"])
+def test_adamw_refuses_options_in_what_it_writes(lib, what):
+    assert adamw(lib, [tensor()], **{what: AT + 392}) == -4
+    assert adamw(lib, [tensor()], **{what: AT + (2 << 12)}) == -4
 
 
 def test_adamw_of_nothing_is_a_noop(lib):
