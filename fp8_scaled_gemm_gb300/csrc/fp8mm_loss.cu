@@ -127,15 +127,22 @@ struct TileChoice {
 };
 
 // With many tiles a CTA pair takes several neighbours, over which a row's maximum and
-// sum stay in registers: 16 units for each of 76 pairs keep the last turn short. (Not
-// of the device's SMs, so that the workspace's size does not depend on them.)
+// sum stay in registers and the tile's place is found once: a unit of `run` tiles costs
+// about as much as run + 0.2, in turns of 76 pairs. (Not of the device's SMs, so that
+// the workspace's size does not depend on them.) 16384 x 8192 x 512: units of 4.
 int choose_run(int64_t M, int64_t N, int width)
 {
-    const int64_t tiles = cdiv(M, kTile) * cdiv(N, width);
-    int run = 1;
-    while (run < 8 && tiles / (2 * run) >= 16 * 76)
-        run *= 2;
-    return run;
+    const int64_t rows = cdiv(M, kTile), across = cdiv(N, width);
+    int best = 1;
+    int64_t cost = INT64_MAX;
+    for (int run = 1; run <= 8; run *= 2) {
+        const int64_t c = cdiv(rows * cdiv(across, run), 76) * (5 * run + 1);
+        if (c < cost) {
+            cost = c;
+            best = run;
+        }
+    }
+    return best;
 }
 
 // The width that ends first, by what a CTA pair loads for its tiles in turn: its

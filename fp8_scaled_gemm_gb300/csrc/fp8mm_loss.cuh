@@ -956,10 +956,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                                 zt = at == n0 + k ? v[k] : zt;
                             p.target_z[row] = zt;
                         }
-                        float most = top;
+                        float most = top, most2 = -INFINITY;
 #pragma unroll
-                        for (int k = 0; k < 32; k += 2)
+                        for (int k = 0; k < 32; k += 4) {
                             most = max3(most, v[k], v[k + 1]);
+                            most2 = max3(most2, v[k + 2], v[k + 3]);
+                        }
+                        most = fmaxf(most, most2);
                         // (a row without a finite value so far: exp(-inf - 0) = 0)
                         const float ref = most == -INFINITY ? 0.0f : most;
                         const Offset from(ref);
