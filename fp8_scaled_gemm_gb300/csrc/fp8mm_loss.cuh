@@ -482,6 +482,10 @@ struct Offset {
     }
 };
 
+// How far a value may be above the maximum that a sum's terms are relative to: a new one
+// for each block of 32 columns costs a tenth of its instructions.
+constexpr float kAbove = 4.0f;
+
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float y;
@@ -841,7 +845,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
         float rs = 1.0f, lse = 0.0f, gs = 0.0f, ma = 1.0f, row_factor = 1.0f;
         long long at = -1;                       // (in the piece; -1: none in it)
         bool live = false;
-        float top = -INFINITY, sum = 0.0f;       // of the row in this unit so far
+        // of the row in this unit so far: sum of exp(z - top); top is a maximum, which later
+        // values exceed by kAbove at most
+        float top = -INFINITY, sum = 0.0f;
+        Offset from(0.0f);
         Schedule<KIND> tiles(p, pair, pairs);
         Work w{}, ahead{};
         // the columns' scales and biases of a tile, loaded while the one before it is
@@ -893,7 +900,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                     gs = 0.0f;
                     at = -1;
                     live = false;
-                    top = -INFINITY;
+                    top = -INFINITY;       // (and `from` anew with the first finite value)
                     sum = 0.0f;
                     if (row < p.M) {
                         if (p.rowwise) {
@@ -956,16 +963,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                                 zt = at == n0 + k ? v[k] : zt;
                             p.target_z[row] = zt;
                         }
-                        float most = top, most2 = -INFINITY;
+                        float most = -INFINITY, most2 = -INFINITY;
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
                             most = max3(most, v[k], v[k + 1]);
                             most2 = max3(most2, v[k + 2], v[k + 3]);
                         }
                         most = fmaxf(most, most2);
-                        // (a row without a finite value so far: exp(-inf - 0) = 0)
-                        const float ref = most == -INFINITY ? 0.0f : most;
-                        const Offset from(ref);
+                        if (__any_sync(0xFFFFFFFFu, most > top + kAbove)) {
+                            // (a row without a finite value so far: exp(-inf - 0) = 0)
+                            const float old = top;
+                            top = fmaxf(top, most);
+                            const float ref = top == -INFINITY ? 0.0f : top;
+                            sum *= fp8mm::ex2_approx((old - ref) * kLog2e);
+                            from = Offset(ref);
+                        }
                         from.exponentials(v);
                         uint64_t s2[2] = {0, 0};
 #pragma unroll
@@ -973,8 +985,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                             s2[k & 1] = ptx::add_f32x2(s2[k & 1], ptx::f32x2(v[2 * k], v[2 * k + 1]));
                         float s0, s1;
                         ptx::unpack_f32x2(ptx::add_f32x2(s2[0], s2[1]), s0, s1);
-                        sum = sum * fp8mm::ex2_approx((top - ref) * kLog2e) + (s0 + s1) * from.rest;
-                        top = most;
+                        sum = fmaf(s0 + s1, from.rest, sum);
                     } else {
                         // 16 columns at a time: 26 warps have 72 registers each
 #pragma unroll 1

@@ -72,8 +72,12 @@ def loss64(p: Problem, ignore=IGNORE):
     # with two more ex2: 46 x 2^-24 of additions, at most (4 + N / 4096 + 32) x (2^-22 + 2 x 2^-24) of joins
     joins = 4 + p.N / 4096 + 32
     rel = 2.0 ** -22 + 2.0 ** -23 + (12 + joins) * 2.0 ** -24 + joins * (2.0 ** -22 + 2.0 ** -23 + 2.0 ** -23)
-    # log: 2^-22 of its value at most; the last sum one rounding
-    lse_tol = err.masked_fill(z == -math.inf, 0).amax(dim=1) + rel + 2.0 ** -22 * rest.abs() + 2.0 ** -23 * lse.abs()
+    # log: 2^-22 of its value at most; the last sum one rounding. The maximum that terms are relative to is one of the
+    # z, `above` = 4 at most under the largest: a term grows with it as the sum does (rel stays), the log's value is
+    # up to 4 larger and the maximum 4 smaller, which adds 4 x 2^-22 and, in the sums with them, 2 x 4 x 2^-24
+    above = 4.0
+    lse_tol = (err.masked_fill(z == -math.inf, 0).amax(dim=1) + rel + 2.0 ** -22 * (rest.abs() + above) + above * 2.0 ** -23
+               + 2.0 ** -23 * lse.abs())
     at = torch.where(live(p.target, ignore), p.target, 0)[:, None]
     zt = z.gather(1, at)[:, 0]
     loss = torch.where(live(p.target, ignore), lse - zt, 0.0)
