@@ -287,8 +287,13 @@ int finish(const void *parts, int64_t n, int count, int out_type, int norm_of, c
     f.norms = norms;
     f.factor = factor;
     f.out = out;
-    return launch_grid2(finish_kernel, std::min<int64_t>(cdiv(n / 4, kFinishThreads), static_cast<int64_t>(sms) * 8), 1,
-                        kFinishThreads, s, "gradient sum launch", f);
+    // (where whole CTAs of elements are less than two turns of the SMs' eight)
+    const int64_t most = static_cast<int64_t>(sms) * 8;
+    if (count >= 8 && n / 4 < 2 * most * kFinishThreads)
+        return launch_grid2(finish_kernel<8>, std::min<int64_t>(cdiv(n / 4, kFinishThreads / 8), most), 1, kFinishThreads, s,
+                            "gradient sum launch", f);
+    return launch_grid2(finish_kernel<1>, std::min<int64_t>(cdiv(n / 4, kFinishThreads), most), 1, kFinishThreads, s,
+                        "gradient sum launch", f);
 }
 
 constexpr CUtensorMapDataType kF16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
