@@ -1205,7 +1205,7 @@ __device__ __forceinline__ void add4(float4 &s, float4 v)
 
 // SPLIT 1: a thread adds all partials of 4 elements. SPLIT 8: a warp adds every
 // eighth one, the first warp the eight sums; for few elements of many partials, whose loads
-// one thread would wait for in turn (128 x 1024 in 19: 8.8 to 4.9 us).
+// one thread would wait for in turn (the gradients of 128 x 4096 x 480, 17.2 to 16.7 us).
 template <int SPLIT>
 static __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const FinishParams p)
 {
