@@ -129,7 +129,8 @@ struct TileChoice {
 // With many tiles a CTA pair takes several neighbours, over which a row's maximum and
 // sum stay in registers and the tile's place is found once: a unit of `run` tiles costs
 // about as much as run + 0.2, in turns of 76 pairs. (Not of the device's SMs, so that
-// the workspace's size does not depend on them.) 16384 x 8192 x 512: units of 4.
+// the workspace's size does not depend on them.) 16384 x 8192 x 512: units of 4, 66 us
+// (of one tile 71).
 int choose_run(int64_t M, int64_t N, int width)
 {
     const int64_t rows = cdiv(M, kTile), across = cdiv(N, width);
