@@ -82,7 +82,7 @@ extern "C" int fp8_adamw(const fp8mm_adamw_tensor *tensors, int64_t n, const fp8
     const fp8mm_adamw_options &o = *options;
     if (!row_type_known(o.param_type) || !row_type_known(o.grad_type) || (o.state_bits != 8 && o.state_bits != 32))
         return FP8MM_ERR_MODE;
-    if (n < 0 || (!o.step_device && o.step < 1) || !std::isfinite(o.lr) || !(o.beta1 >= 0.0 && o.beta1 < 1.0) ||
+    if (n < 0 || n > (int64_t(1) << 32) || (!o.step_device && o.step < 1) || !std::isfinite(o.lr) || !(o.beta1 >= 0.0 && o.beta1 < 1.0) ||
         !(o.beta2 >= 0.0 && o.beta2 < 1.0) || !(o.eps >= 0.0 && std::isfinite(o.eps)) || !std::isfinite(o.weight_decay))
         return FP8MM_ERR_SHAPE;
     if (!aligned_to(o.lr_device, 4) || !aligned_to(o.step_device, 8) || !aligned_to(o.grad_scale, 4))

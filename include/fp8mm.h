@@ -631,8 +631,8 @@ typedef struct fp8mm_adamw_options {
  *
  * Tensors may have any alignment of their elements; 16-byte aligned ones (8 for
  * codes) run fastest. Memory that is written must not be given twice nor
- * overlap a gradient, lr_device, step_device or grad_scale: FP8MM_ERR_MODE. beta1, beta2 in [0, 1), eps >= 0, t >= 1,
- * else FP8MM_ERR_SHAPE. Asynchronous on `stream`, one launch for each 400
+ * overlap a gradient, lr_device, step_device or grad_scale: FP8MM_ERR_MODE.
+ * n at most 2^32, beta1, beta2 in [0, 1), eps >= 0, t >= 1, else FP8MM_ERR_SHAPE. Asynchronous on `stream`, one launch for each 400
  * tensors; the arrays are read before the call returns.
  */
 int fp8_adamw(const fp8mm_adamw_tensor *tensors, int64_t n, const fp8mm_adamw_options *options, void *stream);

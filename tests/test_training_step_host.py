@@ -110,7 +110,7 @@ def adamw(lib, tensors, n=None, **kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(param_type=3), -4), (dict(grad_type=-1), -4), (dict(state_bits=16), -4), (dict(state_bits=0), -4),
-    (dict(n=-1), -2), (dict(step=0), -2), (dict(step=-5), -2), (dict(lr=math.nan), -2), (dict(lr=math.inf), -2),
+    (dict(n=-1), -2), (dict(n=1 << 61), -2), (dict(n=(1 << 63) - 1), -2), (dict(step=0), -2), (dict(step=-5), -2), (dict(lr=math.nan), -2), (dict(lr=math.inf), -2),
     (dict(beta1=1.0), -2), (dict(beta1=-0.5), -2), (dict(beta2=1.0), -2), (dict(beta2=math.nan), -2), (dict(eps=-1.0), -2),
     (dict(eps=math.nan), -2), (dict(weight_decay=math.inf), -2), (dict(lr_device=AT + 2), -3), (dict(step_device=AT + 4), -3),
     (dict(grad_scale=AT + 1), -3), (dict(state_bits=8), -1),
