@@ -84,10 +84,12 @@ def test_workspace_sizes(lib):
     assert lib.fp8_cross_entropy_workspace(0, 10) == 0
     assert lib.fp8_cross_entropy_workspace(1, 0) == -2 and lib.fp8_cross_entropy_workspace(-1, 5) == -2
     assert lib.fp8_cross_entropy_workspace(1 << 20, 1 << 21) == -2
-    # 8 bytes for each row and 32 columns (of many tiles: 256 columns), 4 for each row
-    for M, N, columns in ((1, 1, 32), (7, 1000, 32), (8192, 131072, 256)):
-        need = -(-N // (4 * columns)) * M * 32 + M * 4
+    # 8 bytes for each row and 32 columns, 4 for each row; of many tiles a 64th of the logits in fp32 at most
+    for M, N in ((1, 1), (7, 1000)):
+        need = -(-N // 128) * M * 32 + M * 4
         assert need <= lib.fp8_cross_entropy_workspace(M, N) < need + 512
+    for M, N in ((8192, 131072), (16384, 50257), (3000, 200001)):
+        assert 0 < lib.fp8_cross_entropy_workspace(M, N) < M * N * 4 // 64
     assert lib.fp8_cross_entropy_grad_workspace(0, 10, 16, 1, 1, 1) == 0
     assert lib.fp8_cross_entropy_grad_workspace(5, 10, 16, 0, 0, 0) == 0
     for bad in ((-1, 10, 16), (5, 0, 16), (5, 10, 8), (5, 10, 24)):
