@@ -367,6 +367,25 @@ __device__ __forceinline__ void encode(float (&m)[8], float (&r)[8], const Scale
 // masters, G32: gradients are fp32; else 16-bit types, of which only the conversions
 // differ.
 
+// Asks for a whole block's inputs in L2 (their scales beside them gave nothing), while the
+// warp's block before it is worked on: from the 16 bytes that hold the first one, since codes
+// may be aligned to 8.
+__device__ __forceinline__ void fetch_l2(const void *p, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(p) & ~15ull), "r"(bytes) : "memory");
+}
+
+template <int BITS, bool W32, bool MASTER, bool G32>
+__device__ __forceinline__ void fetch_block(const Tensor &t, long long block)
+{
+    const long long at = block * kBlock;
+    const void *w = MASTER ? static_cast<const void *>(t.master) : t.param;
+    fetch_l2(static_cast<const char *>(w) + at * (W32 ? 4 : 2), kBlock * (W32 ? 4 : 2));
+    fetch_l2(static_cast<const char *>(t.grad) + at * (G32 ? 4 : 2), kBlock * (G32 ? 4 : 2));
+    fetch_l2(static_cast<const char *>(t.m) + at * (BITS / 8), kBlock * (BITS / 8));
+    fetch_l2(static_cast<const char *>(t.v) + at * (BITS / 8), kBlock * (BITS / 8));
+}
+
 // A whole block in 16-byte words, 8 neighbours a lane.
 template <int BITS, bool W32, bool MASTER, bool G32>
 __device__ __forceinline__ void whole_block(const Tensor &t, long long block, int param_type, int grad_type, const Hyper &h, Factors &f,
@@ -527,12 +546,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) adamw_kernel(const __gri
               p.h.grad_scale != nullptr, p.h.eps >= 0x1p-60f && p.h.eps <= 0x1p59f && root <= 0x1p29f};
     const int lane = threadIdx.x & 31;
     const long long warps = static_cast<long long>(gridDim.x) * (kThreads / 32);
+    // With 8-bit states a block takes arithmetic for as long as its loads' wait, which its being
+    // in L2 shortens from 2 us to a third (470 M elements 1430 to 1280 us). With 32-bit ones
+    // memory is the bound (268 M 1260 us, with it 1268), with 16-bit weights and no fp32 ones the
+    // instructions (268 M 717, 724).
+    constexpr bool kAhead = BITS == 8 && W32;
+    // (a warp's number that is known to be the same in its lanes: what follows from it is kept
+    // and computed once a warp, 470 M 1441 to 1430 us, 268 M of 32 bits 1281 to 1260)
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     int k = 0;
-    for (long long b = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); b < p.blocks; b += warps) {
+    for (long long b = static_cast<long long>(blockIdx.x) * (kThreads / 32) + warp; b < p.blocks; b += warps) {
         while (k + 1 < p.tensors && b >= p.t[k + 1].first)
             ++k;
         const Tensor &t = p.t[k];
         const long long block = b - t.first;
+        if (kAhead && t.vec && (block + warps + 1) * kBlock <= t.count && lane == 0)
+            fetch_block<BITS, W32, MASTER, G32>(t, block + warps);
         if (t.vec && (block + 1) * kBlock <= t.count)
             whole_block<BITS, W32, MASTER, G32>(t, block, p.param_type, p.grad_type, p.h, f, lane);
         else
