@@ -51,6 +51,7 @@ int step_some(const fp8mm_adamw_tensor *tensors, int64_t from, int64_t to, const
         const fp8mm_adamw_tensor &a = tensors[i];
         if (a.count == 0)
             continue;
+        p.first[p.tensors] = p.blocks;
         Tensor &t = p.t[p.tensors++];
         t.param = a.param;
         t.grad = a.grad;
@@ -60,7 +61,6 @@ int step_some(const fp8mm_adamw_tensor *tensors, int64_t from, int64_t to, const
         t.m_scale = a.exp_avg_scale;
         t.v_scale = a.exp_avg_sq_scale;
         t.count = a.count;
-        t.first = p.blocks;
         t.vec = aligned_to(a.param, 16) && aligned_to(a.grad, 16) && aligned_to(a.master, 16) && aligned_to(t.m, code) &&
                 aligned_to(t.v, code);
         masters = a.master != nullptr;
@@ -173,6 +173,8 @@ extern "C" int fp8_adamw(const fp8mm_adamw_tensor *tensors, int64_t n, const fp8
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (n <= kFew)
         return step_some<kFew>(tensors, 0, n, o, h, sms, s);
+    if (n <= kSome)
+        return step_some<kSome>(tensors, 0, n, o, h, sms, s);
     for (int64_t i = 0; i < n; i += kMany)
         if ((rc = step_some<kMany>(tensors, i, std::min<int64_t>(n, i + kMany), o, h, sms, s)) != FP8MM_OK)
             return rc;

@@ -42,7 +42,6 @@ struct Tensor {
     void *m, *v;
     float *m_scale, *v_scale;
     long long count;
-    long long first;                   // its first block in the launch's order
     int vec;                           // 16-byte accesses allowed (codes: 8)
 };
 
@@ -57,16 +56,17 @@ struct Hyper {
     const float *grad_scale;
 };
 
-// T tensors by value: 32 or as many as 32 KB of parameters hold.
+// T tensors by value: few, some, or as many as 32 KB of parameters hold.
 template <int T>
 struct Params {
     Hyper h;
     int tensors, param_type, grad_type;
     long long blocks;
+    long long first[T];                // a tensor's first block in the launch's order
     Tensor t[T];
 };
 
-constexpr int kFew = 32, kMany = 400;
+constexpr int kFew = 32, kSome = 96, kMany = 400;
 static_assert(sizeof(Params<kMany>) <= 32764, "kernel parameters");
 
 // Eight elements of a lane as loaded, 2 or 4 bytes each.
@@ -556,10 +556,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) adamw_kernel(const __gri
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     int k = 0;
     for (long long b = static_cast<long long>(blockIdx.x) * (kThreads / 32) + warp; b < p.blocks; b += warps) {
-        while (k + 1 < p.tensors && b >= p.t[k + 1].first)
-            ++k;
+        if (k + 1 < p.tensors && b >= p.first[k + 1]) {
+            // the last tensor that begins at b or before it, by halves: one after another, cold
+            // lines of the table took longer than the blocks of 48 small tensors
+            int end = p.tensors;
+            for (++k; end - k > 1;) {
+                const int middle = (k + end) / 2;
+                if (b >= p.first[middle])
+                    k = middle;
+                else
+                    end = middle;
+            }
+        }
         const Tensor &t = p.t[k];
-        const long long block = b - t.first;
+        const long long block = b - p.first[k];
         if (kAhead && t.vec && (block + warps + 1) * kBlock <= t.count && lane == 0)
             fetch_block<BITS, W32, MASTER, G32>(t, block + warps);
         if (t.vec && (block + 1) * kBlock <= t.count)
