@@ -440,16 +440,20 @@ __device__ __forceinline__ void logits(float (&v)[N], const float *scales, const
 
 // exp(z - off) of many z as 2^(z log2(e) - o) in one operation a value, with o = off
 // log2(e) rounded; the rounding is taken off by a factor `rest` of the results, so that
-// it does not show where their sum is close to 1. An off so large (a row whose every
-// column has the type's lowest value) that o overflows: `wild`, (z - off) log2(e).
+// it does not show where their sum is close to 1. It is up to half a unit in the last place
+// of o: 2^-4 at 2^20, where rest is within 5 % of 1, but hundreds from 2^31 on, which
+// neither factor would hold. An off beyond 2^20 (columns ruled out by a finite value, as far
+// as they are all that a sum has met) is `wild`: (z - off) log2(e), whose difference is
+// exact where it counts.
 struct Offset {
     uint64_t log2e2, add;              // wild: minus off, twice
     float rest;
     bool wild;
+    static constexpr float kWild = 0x1p20f;
     __device__ __forceinline__ explicit Offset(float off)
     {
         const float o = off * kLog2e;
-        wild = __any_sync(0xFFFFFFFFu, fabsf(off) > 0x1p126f);
+        wild = __any_sync(0xFFFFFFFFu, fabsf(off) > kWild);
         rest = wild ? 1.0f : fp8mm::ex2_approx(-fmaf(off, kLog2e, -o));
         add = wild ? ptx::f32x2(-off, -off) : ptx::f32x2(-o, -o);
         log2e2 = ptx::f32x2(kLog2e, kLog2e);
