@@ -962,6 +962,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                             logits<true>(v, scales, biases, rs);
                         else
                             logits<false>(v, scales, biases, rs);
+                        // (where the row has an infinite code or scale, a column past the end is
+                        // infinity times zero until here)
+                        if (n0 + 32 > t.cols) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                v[k] = n0 + k < t.cols ? v[k] : -INFINITY;
+                        }
                         if (mine) {
                             float zt = 0.0f;
 #pragma unroll

@@ -1,5 +1,6 @@
 """Cross entropy where whole stretches of the vocabulary are ruled out by a finite
-bias (a padded vocabulary, a range of special tokens), for any such value."""
+bias (a padded vocabulary, a range of special tokens), for any such value, and
+where rows are infinite up to the vocabulary's ragged end."""
 from __future__ import annotations
 
 import math
@@ -8,7 +9,7 @@ import pytest
 import torch
 
 import fp8_scaled_gemm_gb300 as fm
-from tests._loss64 import IGNORE, Problem, assert_close, grad64, loss64
+from tests._loss64 import E4M3, E5M2, IGNORE, Problem, assert_close, grad64, loss64
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +106,26 @@ def test_large_logits_of_both_signs():
         want = torch.where(p.target == IGNORE, 0.0, torch.logsumexp(z - top[:, None], dim=1) + (top - zt))
         # top - z is exact; a sum's relative error is that of loss64, 2.1e-5 at most
         assert_close(loss, want, 4e-5 + 2.0 ** -22 * want.abs(), f"loss at {shift}")
+
+
+@pytest.mark.parametrize("N", [1, 31, 32, 33, 300, 320, 5000])
+@pytest.mark.parametrize("how", ["code", "scale"])
+def test_rows_of_minus_infinity_up_to_a_ragged_end(N, how):
+    """Every z of a row is -inf: lse = -inf, whether the vocabulary ends inside a block of columns or not."""
+    p = Problem(40, N, 64, a=E5M2, b=E4M3, ignored=0.0)
+    # products of one sign
+    p.A.view(torch.uint8).bitwise_and_(0x7F)
+    p.A.view(torch.uint8)[p.A.view(torch.uint8) == 0] = 0x3C
+    p.Bt.view(torch.uint8).bitwise_or_(0x80)
+    p.Bt.view(torch.uint8)[p.Bt.view(torch.uint8) == 0x80] = 0xB8
+    p.target[3] = IGNORE
+    for row in (3, 7):
+        if how == "code":
+            p.A.view(torch.uint8)[row, 9] = 0x7C
+        else:
+            p.sa[row] = math.inf
+    loss, lse = fm.fp8_cross_entropy(*p.operands, p.target)
+    off = torch.zeros(40, dtype=torch.bool, device="cuda")
+    off[3] = off[7] = True
+    assert bool((lse[off] == -math.inf).all()) and bool(lse[~off].isfinite().all())
+    assert float(loss[3]) == 0.0 and bool(loss[7].isnan()) and bool(loss[~off].isfinite().all())
