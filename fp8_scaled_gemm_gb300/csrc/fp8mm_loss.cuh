@@ -918,7 +918,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                         if (live && to >= 0 && to < p.vocabulary)
                             at = to - p.col0;
                         if constexpr (KIND == kSlope) {
-                            lse = __ldg(p.lse + row);
+                            // (an ignored row's may be anything, and the warp's rows go one way)
+                            lse = live ? __ldg(p.lse + row) : 0.0f;
                             gs = __ldg(p.dloss + static_cast<long long>(row) * p.dloss_step) * slope_scale * ma;
                             if (live && (to < 0 || to >= p.vocabulary))
                                 gs = NAN;

@@ -1,6 +1,6 @@
 """Cross entropy where whole stretches of the vocabulary are ruled out by a finite
-bias (a padded vocabulary, a range of special tokens), for any such value, and
-where rows are infinite up to the vocabulary's ragged end."""
+bias (a padded vocabulary, a range of special tokens), for any such value;
+where rows are infinite up to the vocabulary's ragged end; and where ignored rows hold anything."""
 from __future__ import annotations
 
 import math
@@ -106,6 +106,18 @@ def test_large_logits_of_both_signs():
         want = torch.where(p.target == IGNORE, 0.0, torch.logsumexp(z - top[:, None], dim=1) + (top - zt))
         # top - z is exact; a sum's relative error is that of loss64, 2.1e-5 at most
         assert_close(loss, want, 4e-5 + 2.0 ** -22 * want.abs(), f"loss at {shift}")
+
+
+def test_an_ignored_rows_lse_does_not_change_others():
+    p = Problem(64, 600, 64)
+    p.target[5:9] = IGNORE
+    p.target[9] = 3
+    lse = fm.fp8_cross_entropy(*p.operands, p.target)[1]
+    want = fm.fp8_cross_entropy_grad(*p.operands, p.target, lse, p.dloss, return_dbias=True)
+    for v in (-1e30, 1e10, math.inf, -math.inf, math.nan):
+        lse[5:9] = v
+        got = fm.fp8_cross_entropy_grad(*p.operands, p.target, lse, p.dloss, return_dbias=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 @pytest.mark.parametrize("N", [1, 31, 32, 33, 300, 320, 5000])
