@@ -451,7 +451,7 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
     n.ignore = ignore_index;
     n.count[kNormG] = M;
     n.count[kNormB] = rowwise ? N : 1;
-    n.count[kNormA] = rowwise ? M : 1;
+    n.count[kNormH] = M;
     n.out = norms;
     if (!few && (rc = launch_grid2(norms_kernel, kNormParts, 3, kNormThreads, s, "cross entropy norms launch", n)) != FP8MM_OK)
         return rc;
@@ -506,6 +506,10 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
         AllMaps<kGrad> to{};
         o.rowwise = rowwise;
         o.norms = norms;
+        o.target = target;
+        o.ignore = ignore_index;
+        o.dloss = dloss;
+        o.dloss_step = n.dloss_step;
         if (da) {
             // (a last piece with fewer blocks than slices adds to the first partials only)
             TileSpace &t = o.t[kOfA];
@@ -531,7 +535,7 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
                 (rc = g.parts_b ? map_matrix(&m.out, kF32, 4, ws + g.parts_b_at, nv, K, K, 32, g.split_b)
                                 : map_matrix(&m.out, out_map, es, dbi, nv, K, K, 32)) != FP8MM_OK)
                 return rc;
-            o.r[kOfB] = {!g.parts_b, factor_b, kNormA, sbi, g.parts_b ? FP8MM_OUT_F32 : out_type, 0};
+            o.r[kOfB] = {!g.parts_b, factor_b, kNormH, sbi, g.parts_b ? FP8MM_OUT_F32 : out_type, 0};
         }
         // (the maps of a product that is not wanted have no tiles)
         if (!da)
@@ -540,7 +544,7 @@ int fp8_cross_entropy_grad(const void *A, int a_type, const void *B, int b_type,
             to.of[kOfB] = to.of[kOfA];
         if ((rc = launch_tiles<kGrad>(to, o, sms, s)) != FP8MM_OK)
             return rc;
-        if (g.parts_b && (rc = finish(ws + g.parts_b_at, nv * K, g.split_b, out_type, kNormA, norms, factor_b, dbi, sms, s)) != FP8MM_OK)
+        if (g.parts_b && (rc = finish(ws + g.parts_b_at, nv * K, g.split_b, out_type, kNormH, norms, factor_b, dbi, sms, s)) != FP8MM_OK)
             return rc;
     }
     if (g.parts_a)

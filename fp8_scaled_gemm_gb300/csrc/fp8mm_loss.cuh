@@ -31,17 +31,19 @@
 // dz in fp16: 11 significant bits against bf16's 8, one rounding of at most
 // 2^-11 relative per element of a long sum, and the only one before the
 // output's. Its narrow range is met by powers of two: |dz| <= |g| is known
-// before anything is computed, so rows are scaled by 2^12 / G with G the largest
-// |g|'s power of two; probabilities down to 2^-26 keep all 11 bits, smaller ones
-// are held to 2^-37 of the largest |g|. A scale is split into its mantissa
-// (in [1, 2)) and its power of two. The powers, over the largest one, go
-// with the codes, which is exact: W16 = code 2^e(s_b), H16 = code 2^e(s_a). The
-// mantissas go with dz before it is rounded,
+// before anything is computed, so a row is scaled by 2^12 / 2^e(g) of its own g;
+// probabilities down to 2^-26 keep all 11 bits, smaller ones are held to 2^-37 of
+// the row's |g|, whatever the other rows' (scaled by the largest |g| of all, a row with
+// a millionth of it had 5 % of error in dA with 131072 columns). A scale is split
+// into its mantissa (in [1, 2)) and its power of two. The powers, over the largest
+// one, go with the codes, which is exact: W16 = code 2^e(s_b), H16 = code
+// 2^(e(s_a) + e(g)). The mantissas of the scales go with dz before it is rounded,
 //
-//   dz'[m, n] = dz[m, n] m(s_a[m]) m(s_b[n]),
+//   dz'[m, n] = dz[m, n] 2^-e(g[m]) m(s_a[m]) m(s_b[n]),
 //
-// and since a product sums over one of its two indexes, the mantissa of the
-// other one comes off its row of the result in fp32: one dz' serves both.
+// and since a product sums over one of its two indexes, what belongs to the
+// other one comes off its row of the result in fp32: 1 / m(s_a) and 2^e(g) of dA's,
+// 1 / m(s_b) of dB's. One dz' serves both.
 #pragma once
 
 #include <climits>
@@ -109,7 +111,7 @@ struct TileSpace {
 struct Result {
     int scaled;                        // apply the norms (else a sum of partials does)
     float factor;                      // beside the norms
-    int norm_of;                       // dA: kNormB, dB: kNormA
+    int norm_of;                       // dA: kNormB, dB: kNormH
     const float *row_scale;            // of the result's rows: scale_a, or scale_b from the piece on
     int out_type;
     int add;                           // add to the output (fp32)
@@ -140,16 +142,33 @@ struct LossParams {
     uint32_t *norms_out;               // not nullptr: few values, of which this kernel finds the norms itself
     __half *w16, *h16;                 // [n, K] and [M, K], or nullptr: not wanted
     int K, a_type, b_type;
-    // kGrad
+    // kGrad (dA also: target, ignore, dloss, dloss_step)
     Result r[2];
 };
 
 // ------------------------------------------------------------------ norms ---
-// Largest magnitudes of g, s_b and s_a (without rows to be ignored), as bit
-// patterns (which order like the magnitudes, NaN above everything), in
+// The largest magnitudes of g and s_b as bit patterns (which order like the magnitudes, NaN
+// above everything) and the largest row_exponent(), without rows to be ignored, in
 // kNormParts partial maxima each.
 
-constexpr int kNormG = 0, kNormB = 1, kNormA = 2;
+constexpr int kNormG = 0, kNormB = 1, kNormH = 2;
+
+// The power of two of a magnitude's bits (at least 2^-100, so that its reciprocal is finite;
+// infinite for an infinity or NaN, whose results are then NaN).
+__device__ __forceinline__ float norm_power(uint32_t most) { return fmaxf(__uint_as_float(most & 0x7F800000u), 0x1p-100f); }
+
+// e(g) of a row, as a power of two.
+__device__ __forceinline__ float row_power(float g) { return norm_power(__float_as_uint(g)); }
+
+// e(s_a) + e(g) of a row, 254 above their value; 0 where s_a counts as zero (see power), and
+// more than any for an infinity or NaN.
+constexpr uint32_t kInfinite = 1024;
+
+__device__ __forceinline__ uint32_t row_exponent(float scale, float g)
+{
+    const uint32_t es = __float_as_uint(scale) >> 23 & 255, eg = __float_as_uint(row_power(g)) >> 23;
+    return es == 255 || eg == 255 ? kInfinite : es == 0 ? 0u : es + eg;
+}
 
 struct NormsParams {
     const float *dloss, *scale_b, *scale_a;
@@ -168,14 +187,16 @@ static __global__ void __launch_bounds__(kNormThreads) norms_kernel(const NormsP
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     const int which = blockIdx.y;
-    const float *src = which == kNormG ? p.dloss : which == kNormB ? p.scale_b : p.scale_a;
-    const bool by_row = which == kNormG || (which == kNormA && p.rowwise);
-    const int step = which == kNormG ? p.dloss_step : 1;
     uint32_t most = 0;
     for (long long i = blockIdx.x * kNormThreads + threadIdx.x; i < p.count[which]; i += kNormThreads * kNormParts) {
-        if (by_row && __ldg(p.target + i) == p.ignore)
+        if (which == kNormB) {
+            most = max(most, __float_as_uint(__ldg(p.scale_b + i)) & 0x7FFFFFFFu);
             continue;
-        most = max(most, __float_as_uint(__ldg(src + i * step)) & 0x7FFFFFFFu);
+        }
+        if (__ldg(p.target + i) == p.ignore)
+            continue;
+        const float g = __ldg(p.dloss + i * p.dloss_step);
+        most = max(most, which == kNormG ? __float_as_uint(g) & 0x7FFFFFFFu : row_exponent(__ldg(p.scale_a + (p.rowwise ? i : 0)), g));
     }
     most = __reduce_max_sync(0xFFFFFFFFu, most);
     if ((threadIdx.x & 31) == 0)
@@ -188,33 +209,32 @@ static __global__ void __launch_bounds__(kNormThreads) norms_kernel(const NormsP
     }
 }
 
-__device__ __forceinline__ float norm_power(uint32_t most);
-
-// The power of two at or below the largest magnitude (at least 2^-100, so that
-// its reciprocal is finite; infinite for an infinity or NaN, whose results are
-// then NaN). Every lane of a warp calls it.
-__device__ __forceinline__ float norm_scale(const uint32_t *norms, int which)
+// The largest of a norm's parts. Every lane of a warp calls it.
+__device__ __forceinline__ uint32_t norm_most(const uint32_t *norms, int which)
 {
-    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __ldcg(norms + which * kNormParts + (threadIdx.x & 31)));
-    return norm_power(m);
+    return __reduce_max_sync(0xFFFFFFFFu, __ldcg(norms + which * kNormParts + (threadIdx.x & 31)));
+}
+__device__ __forceinline__ float norm_scale(const uint32_t *norms, int which) { return norm_power(norm_most(norms, which)); }
+
+// What a result's sums have to be multiplied by beside its row's own factor: `factor`, a power
+// of two, times the norms that its operands were divided by.
+__device__ __forceinline__ float result_scale(const uint32_t *norms, int norm_of, float factor)
+{
+    if (norm_of == kNormB)
+        return factor * norm_scale(norms, kNormG) * norm_scale(norms, kNormB);
+    const uint32_t h = norm_most(norms, kNormH);
+    return h == kInfinite ? INFINITY : ldexpf(factor, static_cast<int>(h) - 254);
 }
 
-// The power of two of a largest magnitude's bits (see norm_scale).
-__device__ __forceinline__ float norm_power(uint32_t most) { return fmaxf(__uint_as_float(most & 0x7F800000u), 0x1p-100f); }
-
-// The largest of the magnitudes (as bits) over `threads` threads of a CTA that call
-// it, on a hardware barrier of theirs: values i = thread, thread + threads, ..., `step`
-// apart in src, without those of rows to be ignored. `shared`: a word for each of their warps.
-template <int THREADS>
-__device__ __forceinline__ uint32_t shared_norm(const float *src, int step, int count, const int64_t *target, long long ignore, int thread,
-                                                uint32_t *shared, int barrier)
+// The largest of value(i), i < count, over `threads` threads of a CTA that call it, on a
+// hardware barrier of theirs. `shared`: a word for each of their warps.
+template <int THREADS, typename F>
+__device__ __forceinline__ uint32_t shared_norm(int count, int thread, uint32_t *shared, int barrier, F value)
 {
     uint32_t most = 0;
 #pragma unroll 4
-    for (int i = thread; i < count; i += THREADS) {
-        const uint32_t v = __float_as_uint(__ldg(src + i * step)) & 0x7FFFFFFFu;
-        most = max(most, target && __ldg(target + i) == ignore ? 0u : v);
-    }
+    for (int i = thread; i < count; i += THREADS)
+        most = max(most, value(i));
     most = __reduce_max_sync(0xFFFFFFFFu, most);
     if ((thread & 31) == 0)
         shared[thread >> 5] = most;
@@ -222,7 +242,7 @@ __device__ __forceinline__ uint32_t shared_norm(const float *src, int step, int 
     return __reduce_max_sync(0xFFFFFFFFu, (thread & 31) < THREADS / 32 ? shared[thread & 31] : 0u);
 }
 
-// dz' / G is in (-8, 8): below fp16's 65504.
+// dz' is in (-8, 8) without it: below fp16's 65504.
 constexpr float kSlopeScale = 0x1p12f;
 
 // Of the codes: 448 x 2^7 and 57344 are below it too.
@@ -337,18 +357,47 @@ struct Converted {
 // row, 8 codes each, so that it writes 2 x 256 bytes at once. It takes its codes
 // into registers, which gives the stage back early, then converts and writes them.
 //
-// `powers` holds 2^e(scale) f / S of the warp's rows as two fp16 (below 2^-24: 0), row
-// 16 i + 2 warp + j at 2 i + j; kNoRow for a row to be ignored, whose codes may be NaN.
+// `powers` holds the powers of two of the warp's rows over the largest one, row 16 i + 2 warp
+// + j at 2 i + j, as two fp16: of W16 twice the same (below 2^-24: 0), of H16 two factors,
+// since a small one has to reach further, where its row's gradient is all that a column of dB
+// has (down to 2^-32); kNoRow for a row to be ignored, whose codes may be NaN.
 constexpr uint32_t kNoRow = 0x80008000u;
 
-__device__ __forceinline__ void load_powers(uint32_t *powers, int row0, int rows, const float *scale, int rowwise, float f,
-                                            const int64_t *target, long long ignore, int warp, int lane)
+// (the first one at least 2^-8: times a code it is exact)
+__device__ __forceinline__ uint32_t two_factors(float s)
 {
+    const float first = fmaxf(s, 0x1p-8f);
+    const __half2 h = __floats2half2_rn(first, s / first);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Of W16: 2^e(s_b) f.
+__device__ __forceinline__ void load_powers_b(uint32_t *powers, int row0, const LossParams &p, float f, int warp, int lane)
+{
+    const int row = row0 + (lane >> 1) * 16 + 2 * warp + (lane & 1);
     if (lane >= 16)
         return;
+    const __half2 s = __float2half2_rn(row < p.N ? power(__ldg(p.scale_b + (p.rowwise ? row : 0))) * f : 0.0f);
+    powers[lane] = *reinterpret_cast<const uint32_t *>(&s);
+}
+
+// Of H16: 2^(row_exponent - most) code_scale. (By exponents: s_a g may leave fp32's range.)
+__device__ __forceinline__ void load_powers_a(uint32_t *powers, int row0, const LossParams &p, uint32_t most, int warp, int lane)
+{
     const int row = row0 + (lane >> 1) * 16 + 2 * warp + (lane & 1);
-    const __half2 s = __float2half2_rn(row < rows ? power(__ldg(scale + (rowwise ? row : 0))) * f : 0.0f);
-    powers[lane] = target && row < rows && __ldg(target + row) == ignore ? kNoRow : *reinterpret_cast<const uint32_t *>(&s);
+    if (lane >= 16)
+        return;
+    uint32_t s = 0;
+    if (row < p.M) {
+        const uint32_t e = row_exponent(__ldg(p.scale_a + (p.rowwise ? row : 0)), __ldg(p.dloss + static_cast<long long>(row) * p.dloss_step));
+        if (__ldg(p.target + row) == p.ignore)
+            s = kNoRow;
+        else if (e == kInfinite)
+            s = 0x7E007E00u;           // NaN, as all of dB then
+        else if (e != 0)
+            s = two_factors(ldexpf(code_scale(p.a_type), static_cast<int>(e) - static_cast<int>(most)));
+    }
+    powers[lane] = s;
 }
 
 __device__ __forceinline__ void take_rows(uint2 (&codes)[8], const uint8_t *stage, int warp, int lane)
@@ -373,6 +422,8 @@ __device__ __forceinline__ void write_rows(const uint2 (&codes)[8], int count, _
         if (16 * i >= left)
             break;
         const uint32_t s = powers[2 * i + j];
+        const __half2 both = *reinterpret_cast<const __half2 *>(&s);
+        const __half2 s0 = ROWS ? __low2half2(both) : both, s1 = __high2half2(both);
         uint32_t o[4];
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
@@ -381,7 +432,9 @@ __device__ __forceinline__ void write_rows(const uint2 (&codes)[8], int count, _
                 asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[h]) : "h"(two));
             else
                 asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(o[h]) : "h"(two));
-            const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&o[h]), *reinterpret_cast<const __half2 *>(&s));
+            __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&o[h]), s0);
+            if constexpr (ROWS)
+                v = __hmul2(v, s1);
             o[h] = ROWS && s == kNoRow ? 0u : *reinterpret_cast<const uint32_t *>(&v);
         }
         __stcg(reinterpret_cast<uint4 *>(to + static_cast<long long>(16 * i) * K), make_uint4(o[0], o[1], o[2], o[3]));
@@ -722,24 +775,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
         // for the two against 150.) The last warp that has its codes gives the stage back;
         // taken[s] is 0 again before the stage can come round.
         const int cw = warp - 2 - kEpiWarps;
-        float norm_a, norm_b;
+        uint32_t most_h, most_b;
         if (p.norms_out) {
             const int thread = cw * 32 + lane;
-            const uint32_t a = shared_norm<32 * kConvertWarps>(p.scale_a, 1, p.rowwise ? p.M : 1, p.rowwise ? p.target : nullptr,
-                                                                p.ignore, thread, shared_norms, 1);
-            const uint32_t b =
-                shared_norm<32 * kConvertWarps>(p.scale_b, 1, p.rowwise ? p.N : 1, nullptr, 0, thread, shared_norms + 16, 1);
+            most_h = shared_norm<32 * kConvertWarps>(p.M, thread, shared_norms, 1, [&](int i) {
+                const uint32_t e = row_exponent(__ldg(p.scale_a + (p.rowwise ? i : 0)), __ldg(p.dloss + i * p.dloss_step));
+                return __ldg(p.target + i) == p.ignore ? 0u : e;
+            });
+            most_b = shared_norm<32 * kConvertWarps>(p.rowwise ? p.N : 1, thread, shared_norms + 16, 1,
+                                                     [&](int i) { return __float_as_uint(__ldg(p.scale_b + i)) & 0x7FFFFFFFu; });
             if (blockIdx.x == 0 && cw == 0) {
-                p.norms_out[kNormA * kNormParts + lane] = a;
-                p.norms_out[kNormB * kNormParts + lane] = b;
+                p.norms_out[kNormH * kNormParts + lane] = most_h;
+                p.norms_out[kNormB * kNormParts + lane] = most_b;
             }
-            norm_a = norm_power(a);
-            norm_b = norm_power(b);
         } else {
-            norm_a = norm_scale(p.norms, kNormA);
-            norm_b = norm_scale(p.norms, kNormB);
+            most_h = norm_most(p.norms, kNormH);
+            most_b = norm_most(p.norms, kNormB);
         }
-        const float fa = code_scale(p.a_type) / norm_a, fb = code_scale(p.b_type) / norm_b;
+        const float fb = code_scale(p.b_type) / norm_power(most_b);
         const TileSpace &t = p.t[0];
         uint32_t *powers = reinterpret_cast<uint32_t *>(smem + kPowersAt) + cw * 32;
         int stage = 0;
@@ -752,9 +805,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
             const int col = w.tq * t.width + static_cast<int>(rank) * (t.width / 2);
             __syncwarp();
             if (p.h16)
-                load_powers(powers, row, p.M, p.scale_a, p.rowwise, fa, p.target, p.ignore, cw, lane);
+                load_powers_a(powers, row, p, most_h, cw, lane);
             if (p.w16)
-                load_powers(powers + 16, col, p.N, p.scale_b, p.rowwise, fb, nullptr, 0, cw, lane);
+                load_powers_b(powers + 16, col, p, fb, cw, lane);
             __syncwarp();
             Converted next(p, w);
             for (int kb = w.kb0; kb < w.kb1; ++kb) {
@@ -808,22 +861,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
         float *col_bias = col_scale + C::kCols, *col_mantissa = col_bias + C::kCols;
         int acc = 0;
         uint32_t acc_phase = 0;
-        float slope_scale = 1.0f, out_scale[2] = {1.0f, 1.0f};
+        float norm_g = 1.0f, out_scale[2] = {1.0f, 1.0f};
         if constexpr (KIND == kSlope) {
             if (p.norms_out) {
-                const uint32_t g = shared_norm<32 * kEpiWarps>(p.dloss, p.dloss_step, p.M, p.target, p.ignore, ew * 32 + lane, shared_norms + 32, 2);
+                const uint32_t g = shared_norm<32 * kEpiWarps>(p.M, ew * 32 + lane, shared_norms + 32, 2, [&](int i) {
+                    const uint32_t v = __float_as_uint(__ldg(p.dloss + i * p.dloss_step)) & 0x7FFFFFFFu;
+                    return __ldg(p.target + i) == p.ignore ? 0u : v;
+                });
                 if (blockIdx.x == 0 && ew == 0)
                     p.norms_out[kNormG * kNormParts + lane] = g;
-                slope_scale = kSlopeScale / norm_power(g);
+                norm_g = norm_power(g);
             } else {
-                slope_scale = kSlopeScale / norm_scale(p.norms, kNormG);
+                norm_g = norm_scale(p.norms, kNormG);
             }
         }
         if constexpr (KIND == kGrad) {
+            norm_g = norm_scale(p.norms, kNormG);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (p.r[i].scaled)
-                    out_scale[i] = p.r[i].factor * norm_scale(p.norms, kNormG) * norm_scale(p.norms, p.r[i].norm_of);
+                    out_scale[i] = result_scale(p.norms, p.r[i].norm_of, p.r[i].factor);
         }
         const float s_tensor = C::kFp8 && !p.rowwise ? __ldg(p.scale_a) * __ldg(p.scale_b) : 1.0f;
         const float ma_tensor = C::kFp8 && !p.rowwise ? mantissa(__ldg(p.scale_a)) : 1.0f;
@@ -848,7 +905,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
         };
 
         // what this lane knows of its row of A: scale, lse, g, where its target is
-        float rs = 1.0f, lse = 0.0f, gs = 0.0f, ma = 1.0f, row_factor = 1.0f;
+        // (`back`: dz' without its columns' mantissas to dz / G)
+        float rs = 1.0f, lse = 0.0f, gs = 0.0f, back = 1.0f, row_factor = 1.0f;
         long long at = -1;                       // (in the piece; -1: none in it)
         bool live = false;
         // of the row in this unit so far: sum of exp(z - top); top is a maximum, which later
@@ -902,17 +960,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                 if (w.first) {
                     // this row of A
                     rs = 1.0f;
-                    ma = ma_tensor;
                     gs = 0.0f;
+                    back = 1.0f;           // (of rows without a dz)
                     at = -1;
                     live = false;
                     top = -INFINITY;       // (and `from` anew with the first finite value)
                     sum = 0.0f;
                     if (row < p.M) {
-                        if (p.rowwise) {
+                        if (p.rowwise)
                             rs = __ldg(p.scale_a + row);
-                            ma = mantissa(rs);
-                        }
                         const long long to = __ldg(p.target + row);
                         live = to != p.ignore;
                         if (live && to >= 0 && to < p.vocabulary)
@@ -920,7 +976,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                         if constexpr (KIND == kSlope) {
                             // (an ignored row's may be anything, and the warp's rows go one way)
                             lse = live ? __ldg(p.lse + row) : 0.0f;
-                            gs = __ldg(p.dloss + static_cast<long long>(row) * p.dloss_step) * slope_scale * ma;
+                            const float g = __ldg(p.dloss + static_cast<long long>(row) * p.dloss_step);
+                            const float ma = p.rowwise ? mantissa(rs) : ma_tensor, pg = row_power(g);
+                            gs = g * (kSlopeScale / pg) * ma;
+                            if (live)
+                                back = pg / norm_g / ma;
                             if (live && (to < 0 || to >= p.vocabulary))
                                 gs = NAN;
                         }
@@ -928,8 +988,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                 }
             } else {
                 row_factor = w.of == kOfB ? out_scale[1] : out_scale[0];
-                if (row < t.rows)
+                if (row < t.rows) {
                     row_factor /= mantissa(__ldg(p.r[w.of].row_scale + (p.rowwise ? row : 0)));
+                    // (dz' of a row to be ignored is zero)
+                    if (w.of == kOfA && __ldg(p.target + row) != p.ignore)
+                        row_factor *= row_power(__ldg(p.dloss + static_cast<long long>(row) * p.dloss_step)) / norm_g;
+                }
             }
             if (!W.wait(tfull_bar(acc), acc_phase, 5))
                 break;
@@ -1032,8 +1096,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<KIND>::kThreads,
                                 stage_chunk64(stage, lane, j * 2 + k / 8, pack8(o, fp8rows::kF16));
                             }
                             if (p.colsum) {
-                                // (without the row's mantissa)
-                                const float back = 1.0f / ma;
 #pragma unroll
                                 for (int k = 0; k < 16; ++k)
                                     v[k] *= back;
@@ -1196,7 +1258,7 @@ static __global__ void __launch_bounds__(kRowThreads) combine_row_kernel(const C
 }
 
 // ------------------------------------------------------- sums of partials ---
-// dA from its fp32 partials: out = cast( factor G S sum over s of part[s] ).
+// A result from its fp32 partials: out = cast( result_scale sum over s of part[s] ).
 
 struct FinishParams {
     const float *parts;
@@ -1226,7 +1288,7 @@ static __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const Fin
     __shared__ float4 part[SPLIT][32];
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    const float f = p.factor * norm_scale(p.norms, kNormG) * norm_scale(p.norms, p.norm_of);
+    const float f = result_scale(p.norms, p.norm_of, p.factor);
     constexpr int kWide = kFinishThreads / SPLIT;
     const int at = SPLIT == 1 ? threadIdx.x : threadIdx.x & 31, first = SPLIT == 1 ? 0 : threadIdx.x >> 5;
     const long long step = static_cast<long long>(gridDim.x) * kWide, end = p.n / 4;

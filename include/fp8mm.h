@@ -548,12 +548,14 @@ int64_t fp8_cross_entropy_workspace(int64_t M, int64_t N);
  *   dbias    = sum over m of dz             fp32 [N]
  *
  * z is computed again in pieces of the vocabulary, of which dz is kept as fp16,
- * scaled: one rounding of at most 2^-11 relative or 2^-37 of the largest |dloss|.
+ * scaled: one rounding of at most 2^-11 relative or 2^-37 of its row's |dloss|
+ * (of 2^-100, where that is larger).
  * Its products run on 16-bit tensor cores with fp32 sums; their other operand,
  * codes times powers of two, is exact but for values under 2^-36 of the largest
- * that its codes and scales can have. Rows of A (for db) and columns of B (for
- * da) whose scale is under 2^-31 of the largest one's (e5m2: 2^-24), or under
- * 2^-126, count as zeros. dbias is the sum of the unrounded dz.
+ * that it can have. Columns of B (for da) whose scale is under 2^-31 of the largest
+ * one's (e5m2: 2^-24), rows of A (for db) whose scale times |dloss| is under 2^-39 of
+ * the largest one's (e5m2: 2^-32), and those whose scale is under 2^-126 count as
+ * zeros there. dbias is the sum of the unrounded dz.
  *
  *   lse        what fp8_cross_entropy returned for the same operands.
  *   dloss      fp32 [M], or one value for all rows (dloss_count M or 1).
