@@ -688,6 +688,10 @@ PyObject *cross_entropy_grad(PyObject *const *a)
                                     p.K, data(&ws), bytes, stream());
     }
     checked(rc);
+    // (autograd: a graph that saved one that was given has an older version of it)
+    for (const Result *r : {&da, &db})
+        if (r->given && !r->t->is_inference())
+            r->t->unsafeGetTensorImpl()->bump_version();
     return tuple({&da, &db, &dbias});
 }
 
