@@ -675,7 +675,8 @@ def fp8_cross_entropy_grad(A, B, scale_a, scale_b, scale_mode: int, target, lse,
 def fp8_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, beta1: float = 0.9, beta2: float = 0.999,
               eps: float = 1e-8, weight_decay: float = 1e-2, masters=None, exp_avg_scales=None, exp_avg_sq_scales=None,
               grad_scale=None, stream=None) -> None:
-    """One AdamW step over lists of contiguous tensors, in place.
+    """One AdamW step over lists of contiguous tensors, in place. Gradients, moments and masters have their parameter's
+    shape.
 
     ``params`` (bf16, fp16 or fp32, all of one dtype) are updated, or, with
     ``masters`` (fp32), receive the rounding of the updated masters. The states

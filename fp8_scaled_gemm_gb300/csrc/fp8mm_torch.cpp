@@ -719,13 +719,15 @@ struct Sequence {
     const Tensor &operator[](Py_ssize_t i) const { return *tensor(name, PyTuple_GET_ITEM(seq, i)); }
 };
 
-// Element i of a sequence beside parameter p: contiguous, of p's device and as
-// many values; `type` where one is asked for.
-void *beside_param(const Sequence &s, Py_ssize_t i, const Tensor &p, ScalarType type, int64_t count)
+// Element i of a sequence beside parameter p: contiguous, of p's device, of `type` and
+// of p's shape, or (scales) of `count` values in any.
+void *beside_param(const Sequence &s, Py_ssize_t i, const Tensor &p, ScalarType type, int64_t count, bool any_shape = false)
 {
     const Tensor &t = s[i];
     if (t.scalar_type() != type)
         refuse("%s must all have one dtype, that of a parameter's or of a state", s.name);
+    if (!any_shape && t.sizes() != p.sizes())
+        refuse("%s[%zd] has the shape %s, its parameter %s", s.name, i, shape_of(t).c_str(), shape_of(p).c_str());
     if (t.numel() != count || !t.is_contiguous() || !t.is_cuda() || t.device() != p.device())
         refuse("%s[%zd] must be a contiguous CUDA tensor of %lld values beside its parameter", s.name, i,
                static_cast<long long>(count));
@@ -765,7 +767,7 @@ PyObject *adamw(PyObject *const *a)
         const Tensor &p = params[i];
         fp8mm_adamw_tensor &t = all[static_cast<size_t>(i)];
         t.count = p.numel();
-        t.param = beside_param(params, i, first, type, t.count);
+        t.param = beside_param(params, i, first, type, t.count, true);
         t.grad = beside_param(grads, i, p, grad_type, t.count);
         t.exp_avg = beside_param(ms, i, p, state, t.count);
         t.exp_avg_sq = beside_param(vs, i, p, state, t.count);
@@ -773,8 +775,8 @@ PyObject *adamw(PyObject *const *a)
             t.master = static_cast<float *>(beside_param(masters, i, p, ScalarType::Float, t.count));
         if (eight) {
             const int64_t blocks = (t.count + 255) / 256;
-            t.exp_avg_scale = static_cast<float *>(beside_param(m_scales, i, p, ScalarType::Float, blocks));
-            t.exp_avg_sq_scale = static_cast<float *>(beside_param(v_scales, i, p, ScalarType::Float, blocks));
+            t.exp_avg_scale = static_cast<float *>(beside_param(m_scales, i, p, ScalarType::Float, blocks, true));
+            t.exp_avg_sq_scale = static_cast<float *>(beside_param(v_scales, i, p, ScalarType::Float, blocks, true));
         }
     }
     // autograd is told of the change afterwards, which an inference tensor has no place for
