@@ -23,6 +23,7 @@ import importlib.machinery
 import importlib.util
 import os
 import threading
+import warnings
 from typing import Optional
 
 import torch
@@ -674,7 +675,7 @@ def fp8_cross_entropy_grad(A, B, scale_a, scale_b, scale_mode: int, target, lse,
 
 def fp8_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, beta1: float = 0.9, beta2: float = 0.999,
               eps: float = 1e-8, weight_decay: float = 1e-2, masters=None, exp_avg_scales=None, exp_avg_sq_scales=None,
-              grad_scale=None, stream=None) -> None:
+              grad_scale=None, stream=None, exp_avg_rounding=None) -> None:
     """One AdamW step over lists of contiguous tensors, in place. Gradients, moments and masters have their parameter's
     shape.
 
@@ -685,13 +686,36 @@ def fp8_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, beta1: float 
     1; it (int64) and ``lr`` (fp32) may be CUDA tensors of one value, which a
     captured call reads when it is replayed. ``grad_scale``, a CUDA tensor of
     one fp32 value, multiplies the gradients.
+
+    ``exp_avg_rounding`` is of 8-bit states: train with "stochastic", which
+    rounds the first moment's codes up or down such that their mean is kept.
+    With "nearest" (and None, which warns once) a moment whose step is under
+    half of its codes' distance stays as it is unless its gradient is zero, and
+    where a gradient falls far under the others of its block the weight moves
+    on in the old direction, by up to about ``lr`` a step, without end.
     """
+    if exp_avg_rounding not in (None, "nearest", "stochastic"):
+        raise ValueError('exp_avg_rounding must be "nearest", "stochastic" or None')
     if stream is not None:
         with _on(stream, params[0] if len(params) else None):
             return fp8_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr, beta1, beta2, eps, weight_decay, masters,
-                             exp_avg_scales, exp_avg_sq_scales, grad_scale, None)
+                             exp_avg_scales, exp_avg_sq_scales, grad_scale, None, exp_avg_rounding)
+    if exp_avg_rounding is None and exp_avg_scales is not None:
+        _warn_of_nearest()
     (_native or _load_native()).adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr, beta1, beta2, eps, weight_decay,
-                                      masters, exp_avg_scales, exp_avg_sq_scales, grad_scale)
+                                      masters, exp_avg_scales, exp_avg_sq_scales, grad_scale,
+                                      exp_avg_rounding == "stochastic")
+
+
+_warned_of_nearest = False
+
+
+def _warn_of_nearest() -> None:
+    global _warned_of_nearest
+    if not _warned_of_nearest:
+        _warned_of_nearest = True
+        warnings.warn('fp8_adamw rounds the codes of 8-bit first moments to the nearest, which does not follow gradients '
+                      'that become small: pass exp_avg_rounding="stochastic" (or "nearest" to keep it)', stacklevel=3)
 
 
 def fp8mm_reserve_workspace(nbytes: int) -> None:

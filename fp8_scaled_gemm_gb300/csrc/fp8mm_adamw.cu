@@ -68,7 +68,7 @@ int launch_types(const Params<T> &p, bool masters, int sms, cudaStream_t stream)
 
 // Tensors [from, to) of the call, T at most, which hold anything.
 template <int T>
-int step_some(const fp8mm_adamw_tensor *tensors, int64_t from, int64_t to, const fp8mm_adamw_options &o, const Hyper &h,
+int step_some(const fp8mm_adamw_tensor *tensors, int64_t from, int64_t to, const fp8mm_adamw_options &o, int bits, const Hyper &h,
               int sms, cudaStream_t stream)
 {
     Params<T> p{};
@@ -76,7 +76,7 @@ int step_some(const fp8mm_adamw_tensor *tensors, int64_t from, int64_t to, const
     p.param_type = o.param_type;
     p.grad_type = o.grad_type;
     bool masters = false;              // (all have one, or none)
-    const int code = o.state_bits == 8 ? 8 : 16;      // alignment of 8 elements of a state
+    const int code = bits == 8 ? 8 : 16;              // alignment of 8 elements of a state
     for (int64_t i = from; i < to; ++i) {
         const fp8mm_adamw_tensor &a = tensors[i];
         if (a.count == 0)
@@ -99,8 +99,8 @@ int step_some(const fp8mm_adamw_tensor *tensors, int64_t from, int64_t to, const
     if (p.tensors == 0)
         return FP8MM_OK;
     if (p.grad_type == FP8MM_OUT_F32)
-        return o.state_bits == 8 ? launch_types<8, true>(p, masters, sms, stream) : launch_types<32, true>(p, masters, sms, stream);
-    return o.state_bits == 8 ? launch_types<8, false>(p, masters, sms, stream) : launch_types<32, false>(p, masters, sms, stream);
+        return bits == 8 ? launch_types<8, true>(p, masters, sms, stream) : launch_types<32, true>(p, masters, sms, stream);
+    return bits == 8 ? launch_types<8, false>(p, masters, sms, stream) : launch_types<32, false>(p, masters, sms, stream);
 }
 
 }  // namespace
@@ -110,7 +110,9 @@ extern "C" int fp8_adamw(const fp8mm_adamw_tensor *tensors, int64_t n, const fp8
     if (!options || (n > 0 && !tensors))
         return FP8MM_ERR_NULL;
     const fp8mm_adamw_options &o = *options;
-    if (!row_type_known(o.param_type) || !row_type_known(o.grad_type) || (o.state_bits != 8 && o.state_bits != 32))
+    const bool stochastic = o.state_bits == (8 | FP8MM_STOCHASTIC_EXP_AVG);
+    const int bits = stochastic ? 8 : o.state_bits;
+    if (!row_type_known(o.param_type) || !row_type_known(o.grad_type) || (bits != 8 && bits != 32))
         return FP8MM_ERR_MODE;
     if (n < 0 || n > (int64_t(1) << 32) || (!o.step_device && o.step < 1) || !std::isfinite(o.lr) || !(o.beta1 >= 0.0 && o.beta1 < 1.0) ||
         !(o.beta2 >= 0.0 && o.beta2 < 1.0) || !(o.eps >= 0.0 && std::isfinite(o.eps)) || !std::isfinite(o.weight_decay))
@@ -118,7 +120,7 @@ extern "C" int fp8_adamw(const fp8mm_adamw_tensor *tensors, int64_t n, const fp8
     if (!aligned_to(o.lr_device, 4) || !aligned_to(o.step_device, 8) || !aligned_to(o.grad_scale, 4))
         return FP8MM_ERR_ALIGN;
     const int64_t param_bytes = row_type_bytes(o.param_type), grad_bytes = row_type_bytes(o.grad_type);
-    const int64_t state_bytes = o.state_bits / 8;
+    const int64_t state_bytes = bits / 8;
     std::vector<Stretch> all, other;
     std::vector<size_t> runs;
     try {
@@ -146,11 +148,11 @@ extern "C" int fp8_adamw(const fp8mm_adamw_tensor *tensors, int64_t n, const fp8
         if (t.count == 0)
             continue;
         if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq ||
-            (o.state_bits == 8 && (!t.exp_avg_scale || !t.exp_avg_sq_scale)))
+            (bits == 8 && (!t.exp_avg_scale || !t.exp_avg_sq_scale)))
             return FP8MM_ERR_NULL;
         if (!aligned_to(t.param, param_bytes) || !aligned_to(t.grad, grad_bytes) || !aligned_to(t.master, 4) ||
             !aligned_to(t.exp_avg, state_bytes) || !aligned_to(t.exp_avg_sq, state_bytes) ||
-            (o.state_bits == 8 && (!aligned_to(t.exp_avg_scale, 4) || !aligned_to(t.exp_avg_sq_scale, 4))))
+            (bits == 8 && (!aligned_to(t.exp_avg_scale, 4) || !aligned_to(t.exp_avg_sq_scale, 4))))
             return FP8MM_ERR_ALIGN;
         any = true;
     }
@@ -167,7 +169,7 @@ extern "C" int fp8_adamw(const fp8mm_adamw_tensor *tensors, int64_t n, const fp8
     note_all(&T::master, 4, 1, true);
     note_all(&T::exp_avg, state_bytes, 1, true);
     note_all(&T::exp_avg_sq, state_bytes, 1, true);
-    if (o.state_bits == 8) {
+    if (bits == 8) {
         note_all(&T::exp_avg_scale, 4, kBlock, true);
         note_all(&T::exp_avg_sq_scale, 4, kBlock, true);
     }
@@ -211,14 +213,15 @@ extern "C" int fp8_adamw(const fp8mm_adamw_tensor *tensors, int64_t n, const fp8
     h.lr_device = o.lr_device;
     h.step_device = o.step_device;
     h.step = static_cast<uint32_t>(o.step);
+    h.stochastic = stochastic;
     h.grad_scale = o.grad_scale;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (n <= kFew)
-        return step_some<kFew>(tensors, 0, n, o, h, sms, s);
+        return step_some<kFew>(tensors, 0, n, o, bits, h, sms, s);
     if (n <= kSome)
-        return step_some<kSome>(tensors, 0, n, o, h, sms, s);
+        return step_some<kSome>(tensors, 0, n, o, bits, h, sms, s);
     for (int64_t i = 0; i < n; i += kMany)
-        if ((rc = step_some<kMany>(tensors, i, std::min<int64_t>(n, i + kMany), o, h, sms, s)) != FP8MM_OK)
+        if ((rc = step_some<kMany>(tensors, i, std::min<int64_t>(n, i + kMany), o, bits, h, sms, s)) != FP8MM_OK)
             return rc;
     return FP8MM_OK;
 }

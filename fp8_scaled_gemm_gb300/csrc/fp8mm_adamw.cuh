@@ -10,12 +10,17 @@
 // States in 8 bits: e4m3 codes in blocks of 256 elements with an fp32 scale
 // each (largest magnitude / 448), m as itself and v as its root: the root
 // halves the exponents v spans, and e4m3 with the block's scale then reaches
-// 2^-18 of the block's largest. m is rounded to the nearest code: a step moves it
-// by about a tenth of its distance to g. The root of v moves by less than
-// 0.05 % of itself in a step with b2 = 0.999, codes are 6 to 12 % apart, and the
-// nearest one would be the old one for ever; it is rounded up or down with the
-// probabilities that keep its mean, by a hash of the element's place and of the
-// step. A root that is not zero does not become zero, since it divides.
+// 2^-18 of the block's largest. Codes are 6 to 12 % apart (the smallest ones up to
+// twice), and a step moves the root of v by less than 0.05 % of itself with b2 =
+// 0.999, m by (1 - b1) of its distance to g: where that is under half of the codes'
+// distance, the nearest code is the old one for ever. The root of v is therefore rounded
+// up or down with the probabilities that keep its mean, by a hash of the element's place
+// and of the step; it does not become zero unless it is, since it divides. m likewise with
+// `stochastic`, which is how the states follow the ones in 32 bits over many steps.
+// Without it m goes to the nearest code, but for an element whose gradient is zero. There
+// the nearest code would hold m while v goes to its floor, and the weight would move for
+// ever: with b1, b2 = 0.9, 0.95 by 0.7 lr a step, 2000 steps after its gradient ended;
+// so it still does where a gradient is not zero but falls to a millionth.
 //
 // Bound by memory: with bf16 weights and gradients, fp32 originals and 8-bit
 // states 16 bytes an element. A warp takes a block of 256 elements, 8
@@ -53,6 +58,7 @@ struct Hyper {
     const float *lr_device;
     const int64_t *step_device;
     uint32_t step;                     // low bits, for the rounding
+    int stochastic;                    // m's codes too
     const float *grad_scale;
 };
 
@@ -131,14 +137,17 @@ __device__ __forceinline__ float2 decode2(uint32_t codes)
 
 __device__ __forceinline__ float decode1(uint8_t code) { return decode2(code).x; }
 
-// 20 bits for the rounding of element e at a step.
-__device__ __forceinline__ uint32_t dither(uint32_t e, uint32_t step)
+// 32 bits for the rounding of element e at a step, of which v's root takes the upper 20 and m
+// those of another product.
+__device__ __forceinline__ uint32_t hash(uint32_t e, uint32_t step)
 {
     uint32_t x = e * 0x9E3779B1u + step * 0x85EBCA77u;
     x = (x ^ (x >> 15)) * 0x2C1B3C6Du;
     x = (x ^ (x >> 13)) * 0x297A2D39u;
-    return (x ^ (x >> 16)) >> 12;
+    return x ^ (x >> 16);
 }
+__device__ __forceinline__ uint32_t root_bits(uint32_t hash) { return hash >> 12; }
+__device__ __forceinline__ uint32_t moment_bits(uint32_t hash) { return hash * 0x9E3779B1u >> 12; }
 
 // q >= 0 (or NaN) to a value that e4m3 holds, up or down by u. Codes are 2^-3 of
 // the power of two apart, 20 bits of an fp32 mantissa, and 2^-9 below 2^-6.
@@ -148,6 +157,15 @@ __device__ __forceinline__ float round_by(float q, uint32_t u)
     if (q < 0x1p-6f)
         return q > 0.0f ? fmaxf(floorf(__fadd_rn(q * 512.0f, static_cast<float>(u) * 0x1p-20f)) * 0x1p-9f, 0x1p-9f) : q;
     return q == q ? __uint_as_float((__float_as_uint(q) + u) & ~0xFFFFFu) : q;
+}
+
+// The same for either sign, and to zero as well.
+__device__ __forceinline__ float round_signed(float q, uint32_t u)
+{
+    const float a = fminf(fabsf(q), 448.0f);
+    const float r = a < 0x1p-6f ? floorf(__fadd_rn(a * 512.0f, static_cast<float>(u) * 0x1p-20f)) * 0x1p-9f
+                                : __uint_as_float((__float_as_uint(a) + u) & ~0xFFFFFu);
+    return q == q ? copysignf(r, q) : q;
 }
 
 // ------------------------------------------- roots and quotients of pairs ---
@@ -270,19 +288,21 @@ __device__ __forceinline__ void block_scales(float most_m, float most_v, int lan
 struct Factors {
     float keep, step_size, root, gs, ms, vs;
     uint32_t step;
-    bool scaled_grad;
+    bool scaled_grad, stochastic;
     bool pairs;                        // eps and the root's factor allow roots and quotients of pairs
 };
 
 // ------------------------------------------------------- the step of one lane ---
 // Eight elements: w, m and v (codes' values with BITS = 8) become the new ones, r the root of v; two at a time, in
 // single operations each rounded by itself. Gives the largest |m| and v and the least
-// v, of which the last is 0 where the pairs' range was left.
+// v, of which the last is 0 where the pairs' range was left, and (BITS = 8) the elements
+// whose m is to be rounded up or down, a bit each.
 template <int BITS>
 __device__ __forceinline__ void update(float (&w)[8], const float (&g)[8], float (&m)[8], float (&v)[8], float (&r)[8],
-                                       const Hyper &h, const Factors &f, float &most_m, float &most_v, float &least)
+                                       const Hyper &h, const Factors &f, float &most_m, float &most_v, float &least, uint32_t &by_chance)
 {
     uint64_t m2[4], v2[4];
+    float least_g = INFINITY;
     least = kRootTo;
     most_m = most_v = 0.0f;
 #pragma unroll
@@ -293,6 +313,9 @@ __device__ __forceinline__ void update(float (&w)[8], const float (&g)[8], float
         if (f.scaled_grad)
             gi = ptx::mul_f32x2(gi, both(f.gs));
         if constexpr (BITS == 8) {
+            float g0, g1;
+            ptx::unpack_f32x2(gi, g0, g1);
+            least_g = min3(least_g, fabsf(g0), fabsf(g1));
             m2[i] = ptx::mul_f32x2(m2[i], both(f.ms));
             v2[i] = ptx::mul_f32x2(v2[i], both(f.vs));
             v2[i] = ptx::mul_f32x2(v2[i], v2[i]);
@@ -304,6 +327,12 @@ __device__ __forceinline__ void update(float (&w)[8], const float (&g)[8], float
         least = min3(least, v[2 * i], v[2 * i + 1]);
         most_v = max3_nan(most_v, v[2 * i], v[2 * i + 1]);
         most_m = max3_nan(most_m, fabsf(m[2 * i]), fabsf(m[2 * i + 1]));
+    }
+    by_chance = BITS == 8 && f.stochastic ? 0xFFu : 0u;
+    if (BITS == 8 && least_g == 0.0f && !f.stochastic) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            by_chance |= (f.scaled_grad ? g[i] * f.gs : g[i]) == 0.0f ? 1u << i : 0u;
     }
     // v and |m| at most 2^59: the root, the denominator and m are in the quotient's range
     // when eps and the root's factor are (a NaN is not)
@@ -330,10 +359,10 @@ __device__ __forceinline__ void update(float (&w)[8], const float (&g)[8], float
 }
 
 // Codes of a lane's eight m (in place: their quotients by the new scale, which a
-// conversion rounds) and r (to values that e4m3 holds). `least`: of the r's squares,
-// or 0.
+// conversion rounds, those of `by_chance` to values that e4m3 holds) and r (to values that
+// e4m3 holds). `least`: of the r's squares, or 0.
 __device__ __forceinline__ void encode(float (&m)[8], float (&r)[8], const Scale &ms, const Scale &vs, float least, uint32_t e0,
-                                       int stride, uint32_t step)
+                                       int stride, uint32_t step, uint32_t by_chance)
 {
     if (ms.fast && vs.fast) {
         // (the block's values are finite and at most 448 scales: the reciprocal's way,
@@ -343,11 +372,11 @@ __device__ __forceinline__ void encode(float (&m)[8], float (&r)[8], const Scale
             ptx::unpack_f32x2(divide2(ptx::f32x2(m[i], m[i + 1]), both(-ms.s), both(ms.r)), m[i], m[i + 1]);
             ptx::unpack_f32x2(divide2(ptx::f32x2(r[i], r[i + 1]), both(-vs.s), both(vs.r)), r[i], r[i + 1]);
         }
-        if (least >= 0x1.01p-12f * vs.s * vs.s) {
+        if (least >= 0x1.01p-12f * vs.s * vs.s && by_chance == 0) {
             // none under 2^-6: see round_by
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                r[i] = __uint_as_float((__float_as_uint(r[i]) + dither(e0 + static_cast<uint32_t>(stride * i), step)) & ~0xFFFFFu);
+                r[i] = __uint_as_float((__float_as_uint(r[i]) + root_bits(hash(e0 + static_cast<uint32_t>(stride * i), step))) & ~0xFFFFFu);
             return;
         }
     } else {
@@ -358,8 +387,12 @@ __device__ __forceinline__ void encode(float (&m)[8], float (&r)[8], const Scale
         }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        r[i] = round_by(r[i], dither(e0 + static_cast<uint32_t>(stride * i), step));
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t x = hash(e0 + static_cast<uint32_t>(stride * i), step);
+        r[i] = round_by(r[i], root_bits(x));
+        if (by_chance >> i & 1)
+            m[i] = round_signed(m[i], moment_bits(x));
+    }
 }
 
 // -------------------------------------------------------------- blocks ---
@@ -424,7 +457,8 @@ __device__ __forceinline__ void whole_block(const Tensor &t, long long block, in
         }
     }
     float r[8], most_m, most_v, least;
-    update<BITS>(w, g, m, v, r, h, f, most_m, most_v, least);
+    uint32_t by_chance;
+    update<BITS>(w, g, m, v, r, h, f, most_m, most_v, least, by_chance);
     if constexpr (MASTER)
         store8(t.master, fp8rows::kF32, at, w);
     store8(t.param, W32 && !MASTER ? fp8rows::kF32 : param_type, at, w);
@@ -438,7 +472,7 @@ __device__ __forceinline__ void whole_block(const Tensor &t, long long block, in
             t.m_scale[block] = ms.s;
             t.v_scale[block] = vs.s;
         }
-        encode(m, r, ms, vs, least, static_cast<uint32_t>(at), 1, f.step);
+        encode(m, r, ms, vs, least, static_cast<uint32_t>(at), 1, f.step, by_chance);
         uint32_t cm[4], cv[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -473,7 +507,8 @@ __device__ __noinline__ void any_block(const Tensor &t, long long block, int par
         v[i] = !in ? 0.0f : BITS == 32 ? static_cast<const float *>(t.v)[e] : decode1(static_cast<const uint8_t *>(t.v)[e]);
     }
     float most_m, most_v, least;
-    update<BITS>(w, g, m, v, r, h, f, most_m, most_v, least);
+    uint32_t by_chance;
+    update<BITS>(w, g, m, v, r, h, f, most_m, most_v, least, by_chance);
     if constexpr (BITS == 8) {
         most_m = most_v = 0.0f;
 #pragma unroll
@@ -489,7 +524,7 @@ __device__ __noinline__ void any_block(const Tensor &t, long long block, int par
             t.m_scale[block] = ms.s;
             t.v_scale[block] = vs.s;
         }
-        encode(m, r, ms, vs, least, static_cast<uint32_t>(at), 32, f.step);
+        encode(m, r, ms, vs, least, static_cast<uint32_t>(at), 32, f.step, by_chance);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -543,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) adamw_kernel(const __gri
         step = shared_step;
     }
     Factors f{keep, step_size, root, p.h.grad_scale ? __ldcg(p.h.grad_scale) : 1.0f, 0.0f, 0.0f, step,
-              p.h.grad_scale != nullptr, p.h.eps >= 0x1p-60f && p.h.eps <= 0x1p59f && root <= 0x1p29f};
+              p.h.grad_scale != nullptr, p.h.stochastic != 0, p.h.eps >= 0x1p-60f && p.h.eps <= 0x1p59f && root <= 0x1p29f};
     const int lane = threadIdx.x & 31;
     const long long warps = static_cast<long long>(gridDim.x) * (kThreads / 32);
     // With 8-bit states a block takes arithmetic for as long as its loads' wait, which its being

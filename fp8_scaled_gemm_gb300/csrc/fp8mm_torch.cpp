@@ -735,7 +735,7 @@ void *beside_param(const Sequence &s, Py_ssize_t i, const Tensor &p, ScalarType 
 }
 
 // params, grads, exp_avgs, exp_avg_sqs, step, lr, beta1, beta2, eps,
-// weight_decay, masters, exp_avg_scales, exp_avg_sq_scales, grad_scale
+// weight_decay, masters, exp_avg_scales, exp_avg_sq_scales, grad_scale, stochastic
 PyObject *adamw(PyObject *const *a)
 {
     const Sequence params("params", a[0]), grads("grads", a[1]), ms("exp_avgs", a[2]), vs("exp_avg_sqs", a[3]),
@@ -762,6 +762,11 @@ PyObject *adamw(PyObject *const *a)
     o.param_type = row_code(type);
     o.grad_type = row_code(grad_type);
     o.state_bits = eight ? 8 : 32;
+    if (truth(a[14])) {
+        if (!eight)
+            refuse("exp_avg_rounding is of exp_avgs of torch.float8_e4m3fn");
+        o.state_bits |= FP8MM_STOCHASTIC_EXP_AVG;
+    }
     std::vector<fp8mm_adamw_tensor> all(static_cast<size_t>(params.n));
     for (Py_ssize_t i = 0; i < params.n; ++i) {
         const Tensor &p = params[i];
@@ -890,7 +895,7 @@ PyMethodDef methods[] = {
     method<layer_norm_grad, 8>("layer_norm_grad"),
     method<cross_entropy, 8>("cross_entropy"),
     method<cross_entropy_grad, 16>("cross_entropy_grad"),
-    method<adamw, 14>("adamw"),
+    method<adamw, 15>("adamw"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -599,9 +599,13 @@ typedef struct fp8mm_adamw_tensor {
     int64_t count;
 } fp8mm_adamw_tensor;
 
+/* Beside 8 state_bits: codes of the first moment are rounded up or down as the second
+ * one's are, not to the nearest. */
+#define FP8MM_STOCHASTIC_EXP_AVG 256
+
 typedef struct fp8mm_adamw_options {
     int param_type, grad_type; /* FP8MM_OUT_BF16, _F16 or _F32, of all tensors             */
-    int state_bits;            /* 32 or 8                                                  */
+    int state_bits;            /* 32, 8 or 8 | FP8MM_STOCHASTIC_EXP_AVG                    */
     double lr, beta1, beta2, eps, weight_decay;
     int64_t step;              /* t, from 1                                                */
     const float *lr_device;    /* device memory that holds lr instead, or NULL             */
@@ -621,12 +625,24 @@ typedef struct fp8mm_adamw_options {
  * (param receives its rounding), else param. All tensors have a master or none has.
  *
  * States in 8 bits are e4m3 codes with an fp32 scale per block of 256 elements
- * (max / 448; a zero scale gives zeros; a NaN makes its block NaN): m rounded
- * to the nearest code, sqrt(v) rounded up or down by a hash of the element's
- * place in its tensor and of t, with the probabilities that keep its mean (to
- * the nearest code it would not move), and to no less than 2^-9 of the scale
- * unless it is zero. The update takes the unrounded m and v. Zeros are the
- * states to begin with. Same arguments, same bits.
+ * (max / 448; a zero scale gives zeros; a NaN makes its block NaN). sqrt(v) is
+ * rounded up or down by a hash of the element's place in its tensor and of t, with
+ * the probabilities that keep its mean (to the nearest code it would not move), and
+ * to no less than 2^-9 of the scale unless it is zero. m is rounded to the nearest
+ * code, or up or down by the hash where its gradient is zero and, with
+ * FP8MM_STOCHASTIC_EXP_AVG, everywhere. The update takes the unrounded m and v.
+ * Zeros are the states to begin with. Same arguments, same bits.
+ *
+ * How far states in 8 bits follow AdamW: one step is that of the values that the codes
+ * stand for. Over many, v and a stochastic m keep their means, with noise of about 4 %
+ * of themselves; sqrt(v) stays above 2^-9 of its block's scale, so that a weight whose
+ * gradients are far smaller than its block's others' moves less than it would. An m
+ * that is rounded to the nearest code stays where a step moves it by less than half of
+ * the codes' distance ((1 - beta1) of its distance to the gradient: with beta1 = 0.9 the
+ * smallest codes, with 0.95 most, with 0.98 all). Where a gradient then falls far under
+ * its block's others', m keeps the old one's direction while sqrt(v) falls, and the
+ * weight moves on, without end, by up to about lr a step. Train with
+ * FP8MM_STOCHASTIC_EXP_AVG.
  *
  * lr_device and step_device let a captured step be replayed: the graph reads
  * them when it runs (t as it is then; the call does not count it up).
