@@ -159,13 +159,14 @@ __device__ __forceinline__ float round_by(float q, uint32_t u)
     return q == q ? __uint_as_float((__float_as_uint(q) + u) & ~0xFFFFFu) : q;
 }
 
-// The same for either sign, and to zero as well.
+// The same for a finite q of either sign, and to zero as well: what is under 2^-6 with
+// 2^-6 added, between which and 2^-5 codes are 2^-9 apart too. (Beyond 448 the conversion
+// saturates. With round_by's conversions instead of these sums a step of 470 M elements
+// took 1685 us, so 1459; to the nearest code 1293.)
 __device__ __forceinline__ float round_signed(float q, uint32_t u)
 {
-    const float a = fminf(fabsf(q), 448.0f);
-    const float r = a < 0x1p-6f ? floorf(__fadd_rn(a * 512.0f, static_cast<float>(u) * 0x1p-20f)) * 0x1p-9f
-                                : __uint_as_float((__float_as_uint(a) + u) & ~0xFFFFFu);
-    return q == q ? copysignf(r, q) : q;
+    const float more = fabsf(q) < 0x1p-6f ? copysignf(0x1p-6f, q) : 0.0f;
+    return __fsub_rn(__uint_as_float((__float_as_uint(__fadd_rn(q, more)) + u) & ~0xFFFFFu), more);
 }
 
 // ------------------------------------------- roots and quotients of pairs ---
@@ -372,11 +373,21 @@ __device__ __forceinline__ void encode(float (&m)[8], float (&r)[8], const Scale
             ptx::unpack_f32x2(divide2(ptx::f32x2(m[i], m[i + 1]), both(-ms.s), both(ms.r)), m[i], m[i + 1]);
             ptx::unpack_f32x2(divide2(ptx::f32x2(r[i], r[i + 1]), both(-vs.s), both(vs.r)), r[i], r[i + 1]);
         }
-        if (least >= 0x1.01p-12f * vs.s * vs.s && by_chance == 0) {
-            // none under 2^-6: see round_by
+        if (least >= 0x1.01p-12f * vs.s * vs.s) {
+            // no root under 2^-6: see round_by
+            if (by_chance == 0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                r[i] = __uint_as_float((__float_as_uint(r[i]) + root_bits(hash(e0 + static_cast<uint32_t>(stride * i), step))) & ~0xFFFFFu);
+                for (int i = 0; i < 8; ++i)
+                    r[i] = __uint_as_float((__float_as_uint(r[i]) + root_bits(hash(e0 + static_cast<uint32_t>(stride * i), step))) & ~0xFFFFFu);
+                return;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t x = hash(e0 + static_cast<uint32_t>(stride * i), step);
+                r[i] = __uint_as_float((__float_as_uint(r[i]) + root_bits(x)) & ~0xFFFFFu);
+                if (by_chance >> i & 1)
+                    m[i] = round_signed(m[i], moment_bits(x));
+            }
             return;
         }
     } else {
@@ -390,7 +401,7 @@ __device__ __forceinline__ void encode(float (&m)[8], float (&r)[8], const Scale
     for (int i = 0; i < 8; ++i) {
         const uint32_t x = hash(e0 + static_cast<uint32_t>(stride * i), step);
         r[i] = round_by(r[i], root_bits(x));
-        if (by_chance >> i & 1)
+        if ((by_chance >> i & 1) && fabsf(m[i]) <= 512.0f)      // (neither infinite nor NaN)
             m[i] = round_signed(m[i], moment_bits(x));
     }
 }

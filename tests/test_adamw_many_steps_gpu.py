@@ -102,10 +102,11 @@ def test_rounding_of_the_moment_keeps_its_mean():
 
 def chance(q, u):
     """q to a value that e4m3 holds, up or down by u (20 bits)."""
-    a = q.abs().clamp(max=448.0)
-    up = ((a.view(torch.int32) + u) & -(1 << 20)).view(F32)
-    low = torch.floor(a * 512.0 + u.float() * 2.0 ** -20) * 2.0 ** -9
-    return torch.copysign(torch.where(a < 2.0 ** -6, low, up), q)
+    a = q.abs()
+    # codes are 2^-9 apart up to 2^-5, an eighth of the power of two above
+    more = torch.where(a < 2.0 ** -6, 2.0 ** -6, 0.0)
+    up = (((a + more).view(torch.int32) + u) & -(1 << 20)).view(F32) - more
+    return torch.where(up == 0, 0.0, torch.copysign(up, q)).clamp(-448.0, 448.0)
 
 
 @pytest.mark.parametrize("rounding", [None, "nearest", "stochastic"])
