@@ -527,7 +527,7 @@ int64_t fp8_layer_norm_grad_workspace(int64_t R, int64_t C);
  * A row whose every z is -inf has lse = -inf and a loss of NaN; a NaN or +inf
  * among a row's z makes both NaN. loss, lse and workspace must not overlap one
  * another or an input (FP8MM_ERR_MODE). M == 0 is a no-op. The sums are added in an
- * order that depends on the sizes only, so results repeat.
+ * order that depends on the sizes and the SM count only, so results repeat.
  * Asynchronous on `stream`, two launches; bounded waits and errors as above.
  */
 int fp8_cross_entropy(const void *A, int a_type, const void *B, int b_type,
@@ -645,7 +645,7 @@ typedef struct fp8mm_adamw_options {
  * FP8MM_STOCHASTIC_EXP_AVG.
  *
  * lr_device and step_device let a captured step be replayed: the graph reads
- * them when it runs (t as it is then; the call does not count it up).
+ * them when it runs (t as it is then, at least 1; the call does not count it up).
  *
  * Tensors may have any alignment of their elements; 16-byte aligned ones (8 for
  * codes) run fastest. Memory that is written must not be given twice nor
