@@ -634,8 +634,9 @@ typedef struct fp8mm_adamw_options {
  * Zeros are the states to begin with. Same arguments, same bits.
  *
  * How far states in 8 bits follow AdamW: one step is that of the values that the codes
- * stand for. Over many, v and a stochastic m keep their means, with noise of about 4 %
- * of themselves; sqrt(v) stays above 2^-9 of its block's scale, so that a weight whose
+ * stand for. Over many, sqrt(v) and a stochastic m keep their means (sqrt(v) up to 1 %
+ * above it) with noise: of gradients of unit noise and means, m 8 % (beta1 = 0.9) to
+ * 14 % (0.98) and sqrt(v) 11 % (beta2 = 0.95) to 15 % (0.999); sqrt(v) stays above 2^-9 of its block's scale, so that a weight whose
  * gradients are far smaller than its block's others' moves less than it would. An m
  * that is rounded to the nearest code stays where a step moves it by less than half of
  * the codes' distance ((1 - beta1) of its distance to the gradient: with beta1 = 0.9 the
