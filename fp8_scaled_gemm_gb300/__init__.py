@@ -692,7 +692,7 @@ def fp8_adamw(params, grads, exp_avgs, exp_avg_sqs, step, lr=1e-3, beta1: float 
     With "nearest" (and None, which warns once) a moment whose step is under
     half of its codes' distance stays as it is unless its gradient is zero, and
     where a gradient falls far under the others of its block the weight moves
-    on in the old direction, by up to about ``lr`` a step, without end.
+    on in the old direction, by steps of the order of ``lr``, without end.
     """
     if exp_avg_rounding not in (None, "nearest", "stochastic"):
         raise ValueError('exp_avg_rounding must be "nearest", "stochastic" or None')
