@@ -639,8 +639,9 @@ typedef struct fp8mm_adamw_options {
  * 14 % (0.98) and sqrt(v) 11 % (beta2 = 0.95) to 15 % (0.999). sqrt(v) stays above
  * 2^-9 of its block's scale, so that a weight whose gradients are far smaller than its
  * block's others' moves less than it would. An m that is rounded to the nearest
- * code stays where a step moves it by less than half of the codes' distance ((1 - beta1) of its distance to the gradient: with beta1 = 0.9 the
- * smallest codes, with 0.95 most, with 0.98 all). Where a gradient then falls far under
+ * code stays where a step moves it by less than half of the codes' distance ((1 -
+ * beta1) of its distance to the gradient: with beta1 = 0.9 the smallest codes, with
+ * 0.95 most, with 0.98 all). Where a gradient then falls far under
  * its block's others', m keeps the old one's direction while sqrt(v) falls, and the
  * weight moves on, without end, by steps of the order of lr. Train with
  * FP8MM_STOCHASTIC_EXP_AVG.
